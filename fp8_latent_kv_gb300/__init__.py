@@ -16,7 +16,8 @@ LIB_PATH = os.path.join(PKG, "libkv8mla.so")
 KV8_ROW_BYTES, KV8_KL, KV8_KR = 576, 512, 64
 KV8_MAX_HEADS, KV8_MAX_ROWS, KV8_MAX_SELECT = 128, 1 << 20, 4096
 KV8_OK, KV8_EINVAL, KV8_EWORKSPACE, KV8_ECUDA, KV8_EUNSUPPORTED = 0, -1, -2, -3, -4
-KV8_ERR_INDEX, KV8_ERR_TIMEOUT = 1, 2
+KV8_MAX_SEQS, KV8_MAX_TREE, KV8_MIN_PAGE, KV8_MAX_PAGE = 4096, 256, 16, 65536
+KV8_ERR_INDEX, KV8_ERR_TIMEOUT, KV8_ERR_PAGES = 1, 2, 4
 KV8_F32, KV8_BF16 = 0, 1
 
 # (restype, argtypes) for every exported symbol of include/kv8mla.h
@@ -43,6 +44,12 @@ SIGNATURES = {
     "dsa_index_workspace_bytes": (_I, [_I, _P]),
     "dsa_index_topk8": (_I, [_P, _I, _P, _I, _I, _P, _P, _I64, _I64, _I, _P, _SZ, _P, _P, _P, _P]),
     "mla_out_project8": (_I, [_P, _I, _I, _P, _P, _P, _P, _P]),
+    "kv8_page_plan": (_I, [_I, _P, _P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P]),
+    "kv8_tree_mask": (_I, [_I, _P, _P, _I, _P, _P, _I, _P, _P, _P]),
+    "mla_tree8_workspace_bytes": (_I, [_I, _I, _I, _I, _P]),
+    "mla_absorb_tree8": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P, _I64, _P, _I, _I, _F, _P, _SZ, _P, _P, _I,
+                              _P]),
+    "kv8_tree_commit": (_I, [_I, _P, _P, _P, _P, _I, _I, _P, _P, _I64, _P, _I, _I, _P, _P, _P]),
     "kv8_copy": (_I, [_P, _P, _SZ, _P]),
     "kv8_wait_selftest": (_I, [ctypes.c_uint64, _P, _P, _P]),
     "kv8_strerror": (ctypes.c_char_p, [_I]),
@@ -217,6 +224,107 @@ def mla_out_project8(ctx, w8, w_scale, out, err_word=None, stream=None) -> None:
     S = ctx.numel() // (H * 512)
     _check("mla_out_project8", load().mla_out_project8(_ptr(ctx), S, H, _ptr(w8), _ptr(w_scale), _ptr(out),
                                                        _ptr(err_word), _stream(stream)))
+
+
+def _dtype_code(dtype) -> int:
+    import torch
+    if dtype == torch.bfloat16:
+        return KV8_BF16
+    if dtype == torch.float32:
+        return KV8_F32
+    raise TypeError(f"float32 or bfloat16 expected, got {dtype}")
+
+
+def _args(fn: str, *args) -> None:
+    """Checks of the paged calls' tensors, each (name, tensor, dtype, shape): a wrong one would be read or
+    written out of its bounds by a kernel, so it is refused here.  None passes (an optional argument)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t, dtype, shape in args:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{dev}")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}"
+                             f"{'' if t.is_contiguous() else ' with strides ' + str(t.stride())}")
+
+
+def kv8_page_plan(lens, q_start, page_size: int, n_pages, block_table, free_list, n_free, slots, err_word=None,
+                  stream=None) -> None:
+    """Pages and slots of a step: lens [B], q_start [B+1], n_pages [B], block_table [B][max_pages], free_list [cap],
+    n_free [1] int32 (the last four updated) -> slots [R] int64, the dst_rows of kv8_quant_rows_scatter."""
+    import torch
+    i32 = torch.int32
+    B, R = lens.numel(), slots.numel()
+    _args("kv8_page_plan", ("lens", lens, i32, (B,)), ("q_start", q_start, i32, (B + 1,)), ("n_pages", n_pages, i32, (B,)),
+          ("block_table", block_table, i32, (B, block_table.shape[-1])), ("free_list", free_list, i32, (free_list.numel(),)),
+          ("n_free", n_free, i32, (1,)), ("slots", slots, torch.int64, (R,)), ("err_word", err_word, i32, (1,)))
+    _check("kv8_page_plan", load().kv8_page_plan(
+        B, _ptr(lens), _ptr(q_start), R, page_size, block_table.shape[1], _ptr(n_pages), _ptr(block_table),
+        _ptr(free_list), free_list.numel(), _ptr(n_free), _ptr(slots), _ptr(err_word), _stream(stream)))
+
+
+def kv8_tree_mask(parent, q_start, lens, mask, position=None, err_word=None, stream=None) -> None:
+    """parent [R] int32 (-1: follows the context) -> mask [R][words] int32 bits, position [R] int32 (optional)."""
+    import torch
+    i32 = torch.int32
+    B, R = q_start.numel() - 1, parent.numel()
+    _args("kv8_tree_mask", ("parent", parent, i32, (R,)), ("q_start", q_start, i32, (B + 1,)), ("lens", lens, i32, (B,)),
+          ("mask", mask, i32, (R, mask.shape[-1])), ("position", position, i32, (R,)), ("err_word", err_word, i32, (1,)))
+    _check("kv8_tree_mask", load().kv8_tree_mask(B, _ptr(q_start), _ptr(lens), R, _ptr(parent), _ptr(mask), mask.shape[1],
+                                                 _ptr(position), _ptr(err_word), _stream(stream)))
+
+
+def mla_tree8_workspace_bytes(R: int, H: int, B: int, q_dtype) -> int:
+    """q_dtype: torch.bfloat16 or torch.float32, the queries' type."""
+    out = ctypes.c_size_t(0)
+    _check("mla_tree8_workspace_bytes", load().mla_tree8_workspace_bytes(R, H, B, _dtype_code(q_dtype),
+                                                                         ctypes.addressof(out)))
+    return out.value
+
+
+def mla_absorb_tree8(q_lat, q_rope, q_start, lens, mask, kv8, kv_scale, block_table, page_size: int, sm_scale: float,
+                     workspace, out, err_word=None, stream=None) -> None:
+    """Drafted tokens q_lat [R][H][512], q_rope [R][H][64] (f32 / bf16) of B sequences over the paged cache kv8
+    [rows][576] uint8, kv_scale [rows] f32 -> out [R][H][512] (f32 / bf16).  mask [R][words] int32, or None: a chain."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    R, H = q_lat.shape[0], q_lat.shape[1]
+    B, rows = lens.numel(), kv8.shape[0]
+    _args("mla_absorb_tree8", ("q_lat", q_lat, q_lat.dtype, (R, H, 512)), ("q_rope", q_rope, q_lat.dtype, (R, H, 64)),
+          ("q_start", q_start, i32, (B + 1,)), ("lens", lens, i32, (B,)),
+          ("mask", mask, i32, (R, 0 if mask is None else mask.shape[-1])), ("kv8", kv8, torch.uint8, (rows, 576)),
+          ("kv_scale", kv_scale, f32, (rows,)), ("block_table", block_table, i32, (B, block_table.shape[-1])),
+          ("workspace", workspace, workspace.dtype, workspace.shape), ("out", out, out.dtype, (R, H, 512)),
+          ("err_word", err_word, i32, (1,)))
+    _check("mla_absorb_tree8", load().mla_absorb_tree8(
+        _ptr(q_lat), _ptr(q_rope), _dtype_code(q_lat.dtype), R, H, B, _ptr(q_start), _ptr(lens), _ptr(mask),
+        0 if mask is None else mask.shape[1], _ptr(kv8), _ptr(kv_scale), rows, _ptr(block_table), block_table.shape[1],
+        page_size, sm_scale, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_word), _ptr(out),
+        _dtype_code(out.dtype), _stream(stream)))
+
+
+def kv8_tree_commit(q_start, lens, accept, n_accept, kv8, kv_scale, block_table, page_size: int, new_lens, err_word=None,
+                    stream=None) -> None:
+    """Moves the accepted rows (accept [B][most], n_accept [B] int32) next to the context, in kv8 [rows][576] or
+    [layers][rows][576] uint8 and kv_scale [rows] or [layers][rows]; new_lens [B] int32 = lens + n_accept."""
+    import torch
+    i32 = torch.int32
+    B, rows = lens.numel(), kv8.shape[-2]
+    layers = kv8.shape[0] if kv8.dim() == 3 else 1
+    shape = (layers, rows) if kv8.dim() == 3 else (rows,)
+    _args("kv8_tree_commit", ("q_start", q_start, i32, (B + 1,)), ("lens", lens, i32, (B,)),
+          ("accept", accept, i32, (B, accept.shape[-1])), ("n_accept", n_accept, i32, (B,)),
+          ("kv8", kv8, torch.uint8, (*shape, 576)), ("kv_scale", kv_scale, torch.float32, shape),
+          ("block_table", block_table, i32, (B, block_table.shape[-1])), ("new_lens", new_lens, i32, (B,)),
+          ("err_word", err_word, i32, (1,)))
+    _check("kv8_tree_commit", load().kv8_tree_commit(
+        B, _ptr(q_start), _ptr(lens), _ptr(accept), _ptr(n_accept), accept.shape[1], layers, _ptr(kv8),
+        _ptr(kv_scale), rows, _ptr(block_table), block_table.shape[1], page_size, _ptr(new_lens), _ptr(err_word),
+        _stream(stream)))
 
 
 def kv8_wait_selftest(limit_ns: int, err_word, wait_status, stream=None) -> None:

@@ -68,6 +68,16 @@ cudaError_t launch_attn_mixed(const void *q_nope, const void *q_rope, int q_bf16
                               float *ws, void *scratch, int *err_word, cudaStream_t st);
 // staging for the mixed decode's query prep (query images, score factors, row-scale maxima)
 size_t mixed_scratch_bytes(int H, int P);
+// paged caches and drafted tokens (tree_plan.cu)
+cudaError_t launch_page_plan(int B, const int32_t *lens, const int32_t *q_start, int R, int page_shift, int max_pages,
+                             int32_t *n_pages, int32_t *table, int32_t *free_list, int free_cap, int32_t *n_free,
+                             int64_t *slots, int *err_word, cudaStream_t st);
+cudaError_t launch_tree_mask(int B, const int32_t *q_start, const int32_t *lens, int R, const int32_t *parent,
+                             uint32_t *mask, int W, int32_t *position, int *err_word, cudaStream_t st);
+cudaError_t launch_tree_commit(int B, const int32_t *q_start, const int32_t *lens, const int32_t *accept,
+                               const int32_t *n_accept, int max_accept, int layers, uint8_t *kv8, float *kv_scale,
+                               int64_t cache_rows, const int32_t *table, int max_pages, int page_shift,
+                               int32_t *new_lens, int *err_word, cudaStream_t st);
 cudaError_t launch_copy(void *dst, const void *src, size_t bytes, cudaStream_t st);
 cudaError_t launch_lse_merge(const float *ws, int B, int P, int H, float *out, cudaStream_t st);
 

@@ -3,7 +3,7 @@
 // Every entry point validates its scalars and pointers before enqueuing anything, returns a
 // KV8_E* code instead of falling back, allocates nothing and never synchronises (page "B1 Mixed
 // FP8/BF16 FMHA first pass", "Intentional first-pass limits": unsupported shapes are a hard error).
-#include "internal.h"
+#include "tree.cuh"
 
 #include <math.h>
 
@@ -20,6 +20,18 @@ inline bool valid_q(const void *q_lat, const void *q_rope, int q_dtype) {
 
 inline bool valid_cache(const uint8_t *kv8, const float *kv_scale, int64_t T) {
     return aligned(kv8, 16) && aligned(kv_scale, 4) && T >= 1 && T <= KV8_MAX_ROWS;
+}
+
+// log2 of a page size that the paged calls take, or -1
+inline int page_shift(int page_size) {
+    if (page_size < KV8_MIN_PAGE || page_size > KV8_MAX_PAGE || (page_size & (page_size - 1)) != 0) return -1;
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
+inline bool valid_batch(int B, const int32_t *q_start, const int32_t *lens, int R) {
+    return B >= 1 && B <= KV8_MAX_SEQS && R >= 0 && R <= KV8_MAX_ROWS && aligned(q_start, 4) && aligned(lens, 4);
 }
 
 // The address the current device's kernels use for p: device memory of the current device as is,
@@ -255,6 +267,95 @@ int mla_out_project8(const float *ctx, int S, int H, const uint8_t *w8, const fl
     if (S < 1 || S > KV8_MAX_ROWS || H < 1 || H > KV8_MAX_HEADS) return KV8_EINVAL;
     if (!aligned(ctx, 16) || !aligned(w8, 16) || !aligned(w_scale, 4) || !aligned(out, 16)) return KV8_EINVAL;
     return status(launch_out_project(ctx, S, H, w8, w_scale, out, err_word, (cudaStream_t)stream));
+}
+
+int kv8_page_plan(int B, const int32_t *lens, const int32_t *q_start, int R, int page_size, int max_pages,
+                  int32_t *n_pages, int32_t *block_table, int32_t *free_list, int free_cap, int32_t *n_free,
+                  int64_t *slots, int *err_word, void *stream) {
+    const int shift = page_shift(page_size);
+    if (!valid_batch(B, q_start, lens, R) || shift < 0 || max_pages < 1 || !aligned(n_pages, 4) ||
+        !aligned(block_table, 4) || free_cap < 0 || (free_cap > 0 && !aligned(free_list, 4)) || !aligned(n_free, 4) ||
+        (R > 0 && !aligned(slots, 8)))
+        return KV8_EINVAL;
+    return status(launch_page_plan(B, lens, q_start, R, shift, max_pages, n_pages, block_table, free_list, free_cap,
+                                   n_free, slots, err_word, (cudaStream_t)stream));
+}
+
+int kv8_tree_mask(int B, const int32_t *q_start, const int32_t *lens, int R, const int32_t *parent, uint32_t *mask,
+                  int mask_words, int32_t *position, int *err_word, void *stream) {
+    if (!valid_batch(B, q_start, lens ? lens : q_start, R) || mask_words < 1 || mask_words > KV8_MAX_TREE / 32)
+        return KV8_EINVAL;
+    if (R == 0) return KV8_OK;
+    if (!aligned(parent, 4) || !aligned(mask, 4) || (position && !aligned(position, 4))) return KV8_EINVAL;
+    return status(launch_tree_mask(B, q_start, lens, R, parent, mask, mask_words, position, err_word,
+                                   (cudaStream_t)stream));
+}
+
+int mla_tree8_workspace_bytes(int R, int H, int B, int q_dtype, size_t *bytes) {
+    if (R < 1 || R > KV8_MAX_ROWS || H < 1 || H > KV8_MAX_HEADS || B < 1 || B > KV8_MAX_SEQS || !bytes ||
+        (q_dtype != KV8_F32 && q_dtype != KV8_BF16))
+        return KV8_EINVAL;
+    *bytes = tree_workspace(R, H, B, q_dtype == KV8_BF16).total;
+    return KV8_OK;
+}
+
+int mla_absorb_tree8(const void *q_lat, const void *q_rope, int q_dtype, int R, int H, int B, const int32_t *q_start,
+                     const int32_t *lens, const uint32_t *mask, int mask_words, const uint8_t *kv8,
+                     const float *kv_scale, int64_t cache_rows, const int32_t *block_table, int max_pages, int page_size,
+                     float sm_scale, void *workspace, size_t ws_bytes, int *err_word, void *out, int out_dtype,
+                     void *stream) {
+    size_t need = 0;
+    int rc = mla_tree8_workspace_bytes(R, H, B, q_dtype, &need);
+    if (rc != KV8_OK) return rc;
+    const int shift = page_shift(page_size);
+    if (!valid_q(q_lat, q_rope, q_dtype) || !valid_batch(B, q_start, lens, R) || !aligned(kv8, 16) ||
+        !aligned(kv_scale, 4) || cache_rows < 1 || cache_rows > 0x7fffffffLL || !aligned(block_table, 4) || max_pages < 1 ||
+        shift < 0 || !isfinite(sm_scale) || !aligned(workspace, 16) || !aligned(out, 16) ||
+        (out_dtype != KV8_F32 && out_dtype != KV8_BF16) ||
+        (mask && (!aligned(mask, 4) || mask_words < 1 || mask_words > KV8_MAX_TREE / 32)))
+        return KV8_EINVAL;
+    if (ws_bytes < need) return KV8_EWORKSPACE;
+    TreeArgs a{};
+    a.q_lat = q_lat;
+    a.q_rope = q_rope;
+    a.q_bf16 = q_dtype == KV8_BF16;
+    a.R = R;
+    a.H = H;
+    a.B = B;
+    a.q_start = q_start;
+    a.lens = lens;
+    a.mask = mask;
+    a.mask_words = mask_words;
+    a.kv8 = kv8;
+    a.kv_scale = kv_scale;
+    a.cache_rows = cache_rows;
+    a.table = block_table;
+    a.max_pages = max_pages;
+    a.page_shift = shift;
+    a.sm_scale_log2 = sm_scale * kLog2e;
+    a.out = out;
+    a.out_bf16 = out_dtype == KV8_BF16;
+    a.err_word = err_word;
+    a.ctas = tree_ctas();
+    const TreeWorkspace w = tree_workspace(R, H, B, a.q_bf16);
+    a.sched = static_cast<TreeSched *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.part);
+    return status(launch_tree_simt(a, (cudaStream_t)stream));
+}
+
+int kv8_tree_commit(int B, const int32_t *q_start, const int32_t *lens, const int32_t *accept,
+                    const int32_t *n_accept, int max_accept, int layers, uint8_t *kv8, float *kv_scale,
+                    int64_t cache_rows, const int32_t *block_table, int max_pages, int page_size, int32_t *new_lens,
+                    int *err_word, void *stream) {
+    const int shift = page_shift(page_size);
+    if (!valid_batch(B, q_start, lens, 0) || !aligned(accept, 4) || !aligned(n_accept, 4) || max_accept < 1 ||
+        max_accept > KV8_MAX_TREE || layers < 1 || layers > 65535 || !aligned(kv8, 16) || !aligned(kv_scale, 4) ||
+        cache_rows < 1 || cache_rows > 0x7fffffffLL || !aligned(block_table, 4) || max_pages < 1 || shift < 0 ||
+        !aligned(new_lens, 4) || new_lens == lens)
+        return KV8_EINVAL;
+    return status(launch_tree_commit(B, q_start, lens, accept, n_accept, max_accept, layers, kv8, kv_scale,
+                                     cache_rows, block_table, max_pages, shift, new_lens, err_word,
+                                     (cudaStream_t)stream));
 }
 
 int kv8_copy(void *dst, const void *src, size_t bytes, void *stream) {

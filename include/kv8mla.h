@@ -66,6 +66,10 @@ extern "C" {
 #define KV8_MAX_IDX_HEADS 128  /* DSA indexer: index heads per query (a multiple of 16) */
 #define KV8_MX_NOPE 448        /* mixed cache: no-position values per row (e4m3 + row scale) */
 #define KV8_MX_ROPE 64         /* mixed cache: RoPE values per row (bf16) */
+#define KV8_MAX_SEQS 4096      /* paged calls: sequences per call */
+#define KV8_MAX_TREE 256       /* paged calls: drafted tokens per sequence */
+#define KV8_MIN_PAGE 16        /* paged calls: rows per page, a power of two from here ... */
+#define KV8_MAX_PAGE 65536     /* ... to here */
 
 /* return codes */
 #define KV8_OK 0
@@ -77,6 +81,7 @@ extern "C" {
 /* bits OR-ed into *err_word by the device */
 #define KV8_ERR_INDEX 1u    /* a selected row index was outside [0, T): that entry was skipped */
 #define KV8_ERR_TIMEOUT 2u  /* a bounded wait in a kernel gave up: that output is not valid */
+#define KV8_ERR_PAGES 4u    /* kv8_page_plan: the free pages, or the table, did not suffice for a sequence */
 
 /* query element types */
 #define KV8_F32 0
@@ -309,6 +314,98 @@ KV8_API int dsa_index_workspace_bytes(int B, size_t *bytes);
 KV8_API int dsa_index_topk8(const void *q_idx, int q_dtype, const float *w, int B, int HI, const uint8_t *k8,
                             const float *k_scale, int64_t T, int64_t seq_stride_rows, int NS, void *workspace,
                             size_t ws_bytes, float *scores, int32_t *idx, int *err_word, void *stream);
+
+/* -----------------------------------------------------------------------------------------------
+ * Paged caches and drafted tokens.  The pages have no counterpart to these calls; they exist for users
+ * of this library who serve many sequences from one cache and verify several drafted tokens per step.
+ *
+ * A paged cache is one buffer of rows (kv8 [cache_rows][576], kv_scale [cache_rows], as everywhere) cut
+ * into pages of page_size rows, page g being rows g*page_size .. (g+1)*page_size - 1.  Sequence b's
+ * position t lives in cache row
+ *     block_table[b][t / page_size] * page_size + t % page_size        (block_table: device int32 [B][max_pages])
+ * page_size is a power of two in [KV8_MIN_PAGE, KV8_MAX_PAGE].  Table entries past a sequence's rows are
+ * not read.
+ *
+ * A step adds n_b = q_start[b+1] - q_start[b] rows to sequence b, whose first lens[b] rows are already
+ * there (device int32 lens [B], q_start [B+1], ascending from 0 to R): the step's row q_start[b] + i is
+ * the sequence's drafted token i and lives at position lens[b] + i, whatever branch it stands on.  n_b may
+ * differ between sequences and may be 0; n_b <= KV8_MAX_TREE; B in [1, KV8_MAX_SEQS].
+ * A sequence whose numbers are not possible (lens[b] < 0, n_b < 0 or too large, rows outside [0, R), more
+ * positions than its table holds) is skipped, what it would have written is left as it was, and
+ * KV8_ERR_INDEX is set.
+ *
+ * kv8_page_plan -- block tables and slot maps from the lengths.  Afterwards every sequence holds exactly
+ * the pages of its lens[b] + n_b rows, and slots[q_start[b] + i] is the cache row of its position
+ * lens[b] + i: the dst_rows that kv8_quant_rows_scatter takes.
+ *   n_pages [B] int32 in/out: pages the sequence holds, block_table[b][0 .. n_pages[b]).
+ *   block_table in/out: entries of new pages are written, all others left.
+ *   free_list [free_cap] int32, n_free [1] int32 in/out: a stack of free pages, its top at n_free - 1.
+ *   slots [R] int64 out.  free_cap >= 0, R >= 0 (free_list / slots may be NULL when 0).
+ * First every sequence returns the pages it holds beyond its rows; then missing pages are taken from the
+ * top, sequence by sequence in order.  Pages return in the order that makes the same growth take the same
+ * pages again.  A sequence that wants more pages than are left after the ones before it (their wants
+ * counted whether met or not), or more than max_pages, keeps the pages it has, gets -1 in its slots and
+ * sets KV8_ERR_PAGES.  The result depends on the arguments alone.  n_pages[b] outside [0, max_pages],
+ * n_free outside [0, free_cap], or more returned pages than free_cap holds: KV8_ERR_INDEX, as above (for
+ * n_free: every sequence).
+ * Lengths of 0 return all of a sequence's pages.
+ * --------------------------------------------------------------------------------------------- */
+KV8_API int kv8_page_plan(int B, const int32_t *lens, const int32_t *q_start, int R, int page_size, int max_pages,
+                          int32_t *n_pages, int32_t *block_table, int32_t *free_list, int free_cap, int32_t *n_free,
+                          int64_t *slots, int *err_word, void *stream);
+
+/* kv8_tree_mask -- from each drafted token's parent, the tokens it attends and its position.
+ *   parent [R] int32: the index, within the sequence, of the token before it on its branch, smaller than
+ *   its own; -1 for a token that follows the context directly (a sequence may have several).
+ *   mask [R][mask_words] uint32 out: bit j of row q_start[b] + i (word j/32, bit j%32) is set when j is i
+ *   or one of its ancestors.  mask_words in [1, KV8_MAX_TREE/32]; a sequence with more than 32*mask_words
+ *   tokens is skipped (KV8_ERR_INDEX).
+ *   position [R] int32 out (may be NULL): lens[b] + number of i's ancestors: the angle index of its RoPE.
+ *   A parent outside [-1, i) counts as -1 and sets KV8_ERR_INDEX.  lens may be NULL (positions from 0). */
+KV8_API int kv8_tree_mask(int B, const int32_t *q_start, const int32_t *lens, int R, const int32_t *parent,
+                          uint32_t *mask, int mask_words, int32_t *position, int *err_word, void *stream);
+
+/* -----------------------------------------------------------------------------------------------
+ * mla_absorb_tree8 -- absorbed attention of every drafted token, over the paged cache.  For row
+ * r = q_start[b] + i and head h, over the sequence's rows t with the cache row's bytes and scale s_t:
+ *     score[t] = sm_scale * s_t * ( q_lat[r][h].e4m3(Lc8_t) + q_rope[r][h].e4m3(Rc8_t) )
+ *     out[r][h] = sum_t softmax_t(score) * s_t * e4m3(Lc8_t)
+ * where t runs over the context 0 .. lens[b]-1 and over lens[b] + j for every set bit j < n_b of r's mask
+ * row.  Nothing to attend gives zeros.  mask NULL: token i attends drafted tokens 0 .. i (a chain; one
+ * token per sequence is an ordinary decode step, several are a chunk of a causal prefill).
+ * The drafted rows must be in the cache already (kv8_quant_rows_scatter).
+ *   q_lat [R][H][512], q_rope [R][H][64] of type q_dtype; out [R][H][512] of type out_dtype (KV8_F32 /
+ *   KV8_BF16; bf16 rounds to nearest even).  R in [1, KV8_MAX_ROWS]; H in [1, 128]; rows of out outside
+ *   every sequence are left as they were.  cache_rows in [1, 2^31).
+ *   mask [R][mask_words] uint32 as kv8_tree_mask writes it (any bits: it need not be a tree); bits past
+ *   32*mask_words count as 0.
+ *   A page outside the cache: its rows are left out and KV8_ERR_INDEX is set.  Rows that nobody attends
+ *   may hold anything, NaN codes and scales included.  Scales are not negative.
+ *   workspace: >= mla_tree8_workspace_bytes(R, H, B, q_dtype) bytes; calls that may overlap on the GPU
+ *   (graph replays included) need their own.  err_word: optional.
+ * Runs on the CUDA cores in f32.  The work is cut into equal shares of row tiles for the device's SMs, whatever the
+ * lengths; what a share leaves unfinished is joined by log-sum-exp.
+ * --------------------------------------------------------------------------------------------- */
+KV8_API int mla_tree8_workspace_bytes(int R, int H, int B, int q_dtype, size_t *bytes);
+KV8_API int mla_absorb_tree8(const void *q_lat, const void *q_rope, int q_dtype, int R, int H, int B,
+                             const int32_t *q_start, const int32_t *lens, const uint32_t *mask, int mask_words,
+                             const uint8_t *kv8, const float *kv_scale, int64_t cache_rows, const int32_t *block_table,
+                             int max_pages, int page_size, float sm_scale, void *workspace, size_t ws_bytes,
+                             int *err_word, void *out, int out_dtype, void *stream);
+
+/* kv8_tree_commit -- after the target model has chosen a branch: moves the branch's rows next to the
+ * context, in every layer's cache at once.  For k < n_accept[b], position lens[b] + accept[b][k] is
+ * copied to position lens[b] + k (bytes and scale), and new_lens[b] = lens[b] + n_accept[b].
+ *   accept [B][max_accept] int32, strictly ascending within the first n_accept[b], each in [0, n_b).
+ *   kv8 [layers][cache_rows][576], kv_scale [layers][cache_rows], one block table for all layers.
+ *   new_lens [B] int32 out, must not be lens.  max_accept in [1, KV8_MAX_TREE]; layers in [1, 65535].
+ *   A branch that is not ascending or not in the draft, n_accept[b] outside [0, max_accept], a page
+ *   outside the cache: nothing of the sequence moves, new_lens[b] = lens[b], KV8_ERR_INDEX.
+ *   Sequences must not share the pages of the rows that move. */
+KV8_API int kv8_tree_commit(int B, const int32_t *q_start, const int32_t *lens, const int32_t *accept,
+                            const int32_t *n_accept, int max_accept, int layers, uint8_t *kv8, float *kv_scale,
+                            int64_t cache_rows, const int32_t *block_table, int max_pages, int page_size,
+                            int32_t *new_lens, int *err_word, void *stream);
 
 /* -----------------------------------------------------------------------------------------------
  * kv8_copy -- copy `bytes` bytes from src to dst with a kernel (the SMs' loads and stores, not a
