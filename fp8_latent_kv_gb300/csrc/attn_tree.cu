@@ -1,5 +1,5 @@
-// attn_tree.cu -- attention of drafted tokens over a paged latent cache: the shares' bookkeeping, the CUDA-core
-// kernel, and the merge of the groups that a share boundary cuts.
+// attn_tree.cu -- attention of drafted tokens over a paged latent cache: the CUDA-core kernel for f32
+// queries, and the merge of the groups that a share boundary cuts.
 //
 // For column (token i, head h) of a sequence and row t:  s_t = sm_scale * scale_t * q.e4m3(row_t),
 // out = sum_t 2^((s_t - m) log2 e) scale_t e4m3(Lc_t) / sum_t 2^((s_t - m) log2 e), one pass over the rows with
@@ -33,7 +33,6 @@ __global__ void __launch_bounds__(288) tree_sched_kernel(TreeArgs a) {
     tree_schedule<kCols, kRows>(a, scan);
 }
 
-template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -52,8 +51,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
             if (c < nc) {
                 const int64_t at = k < kKL ? (q_base + c) * kKL + k : (q_base + c) * kKR + (k - kKL);
                 const void *base = k < kKL ? a.q_lat : a.q_rope;
-                v = kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[at])
-                          : static_cast<const float *>(base)[at];
+                v = static_cast<const float *>(base)[at];
             }
             sm.q[c][k] = v;
         }
@@ -197,13 +195,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
             if (tid < nc) {
                 part[kCols * kKL + tid] = sm.m_run[tid];
                 part[kCols * (kKL + 1) + tid] = sm.z_run[tid];
+                part[kCols * (kKL + 2) + tid] = 0.f;
             }
         }
     }
     if (bad_page && a.err_word) atomicOr(a.err_word, (int)KV8_ERR_INDEX);
 }
 
-// Joins the parts of the cut groups: out = sum_p 2^(m_p - M) cl_p / sum_p 2^(m_p - M) z_p with M = max_p m_p.
+// Joins the parts of the cut groups: out = sum_p 2^(m_p - M) cl_p / (sum_p 2^(m_p - M) z_p + 2^-M sum_p n0_p) with
+// M = max_p m_p.
 // An item is one column of one cut group; 128 threads hold four dims each, two halves of the block take
 // alternate parts.
 constexpr int kMergeThreads = 256;
@@ -232,13 +232,15 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, i
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kMergeThreads / 32; ++w) m = fmaxf(m, red[w][0]);
-        float z = 0.f;
+        float z = 0.f, n0 = 0.f;
         for (int p = tid; p < job.count; p += kMergeThreads) {
+            n0 += part(p)[cols * (kKL + 2) + c];
             const float mp = part(p)[cols * kKL + c];
             const float w = mp == -INFINITY ? 0.f : exp2f(mp - m);
             wt[p] = w;
             if (w != 0.f) z = fmaf(w, part(p)[cols * (kKL + 1) + c], z);
         }
+        if (n0 != 0.f && m != -INFINITY) z = fmaf(n0, exp2f(-m), z);
         z = warp_sum(z);
         if (lane == 0) red[warp][1] = z;
         __syncthreads();
@@ -290,8 +292,8 @@ TreeWorkspace tree_workspace(int R, int H, int B, bool q_bf16) {
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     TreeWorkspace w;
     w.part = up(sizeof(TreeSched));
-    w.total = w.part + up((size_t)tree_ctas() * 2 * tree_part_floats(kCols) * sizeof(float));
-    (void)R, (void)H, (void)B, (void)q_bf16;
+    w.images = w.part + up(q_bf16 ? tree_tc_part_bytes(tree_ctas()) : (size_t)tree_ctas() * 2 * tree_part_floats(kCols) * sizeof(float));
+    w.total = w.images + (q_bf16 ? up(tree_tc_images(R, H, B)) : 0);
     return w;
 }
 
@@ -311,12 +313,11 @@ cudaError_t launch_tree_merge(const TreeArgs &a, int cols, cudaStream_t st) {
 }
 
 cudaError_t launch_tree_simt(const TreeArgs &a, cudaStream_t st) {
-    auto kernel = a.q_bf16 ? attn_tree_simt_kernel<true> : attn_tree_simt_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    cudaError_t e = cudaFuncSetAttribute(attn_tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
     if (e != cudaSuccess) return e;
     tree_sched_kernel<<<1, 288, 0, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    kernel<<<(unsigned)a.ctas, kThreads, sizeof(Smem), st>>>(a);
+    attn_tree_simt_kernel<<<(unsigned)a.ctas, kThreads, sizeof(Smem), st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_tree_merge(a, kCols, st);
 }

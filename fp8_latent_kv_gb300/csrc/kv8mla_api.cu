@@ -340,7 +340,9 @@ int mla_absorb_tree8(const void *q_lat, const void *q_rope, int q_dtype, int R, 
     const TreeWorkspace w = tree_workspace(R, H, B, a.q_bf16);
     a.sched = static_cast<TreeSched *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.part);
-    return status(launch_tree_simt(a, (cudaStream_t)stream));
+    // bf16 queries: tensor cores; f32 queries keep full f32 precision on the CUDA cores
+    return status(a.q_bf16 ? launch_tree_tc(a, static_cast<uint8_t *>(workspace) + w.images, (cudaStream_t)stream)
+                           : launch_tree_simt(a, (cudaStream_t)stream));
 }
 
 int kv8_tree_commit(int B, const int32_t *q_start, const int32_t *lens, const int32_t *accept,

@@ -72,10 +72,11 @@ struct TreeArgs {
     int *err_word;
     int ctas;                    // shares asked for
     TreeSched *sched;
-    float *part;                 // partial sets: [ctas][2] x { cl [cols][512], m [cols], z [cols] }
+    float *part;                 // partial sets: [ctas][2] x { cl [cols][512], m [cols], z [cols], n0 [cols] }
 };
 
-__host__ __device__ constexpr size_t tree_part_floats(int cols) { return (size_t)cols * (kKL + 2); }
+// A partial set: cl and z relative to 2^m, and n0, the weight (relative to 2^0) of rows that only count in the sum.
+__host__ __device__ constexpr size_t tree_part_floats(int cols) { return (size_t)cols * (kKL + 3); }
 
 // Cache row of position t of sequence b, or -1 where its page is outside the cache.
 __device__ __forceinline__ int64_t tree_row(const TreeArgs &a, int b, int64_t t) {
@@ -230,12 +231,15 @@ struct TreeWalk {
 };
 
 struct TreeWorkspace {
-    size_t part, total;  // the shares come first
+    size_t part, images, total;  // the shares come first
 };
 TreeWorkspace tree_workspace(int R, int H, int B, bool q_bf16);
 
 cudaError_t launch_tree_merge(const TreeArgs &a, int cols, cudaStream_t st);
 cudaError_t launch_tree_simt(const TreeArgs &a, cudaStream_t st);
+cudaError_t launch_tree_tc(const TreeArgs &a, void *images, cudaStream_t st);
+size_t tree_tc_images(int R, int H, int B);
+size_t tree_tc_part_bytes(int ctas);
 int tree_ctas();
 
 }  // namespace kv8

@@ -383,7 +383,8 @@ KV8_API int kv8_tree_mask(int B, const int32_t *q_start, const int32_t *lens, in
  *   may hold anything, NaN codes and scales included.  Scales are not negative.
  *   workspace: >= mla_tree8_workspace_bytes(R, H, B, q_dtype) bytes; calls that may overlap on the GPU
  *   (graph replays included) need their own.  err_word: optional.
- * Runs on the CUDA cores in f32.  The work is cut into equal shares of row tiles for the device's SMs, whatever the
+ * bf16 queries run on the tensor cores (as mla_absorb_decode8: weights to about 2^-9), f32 queries on the
+ * CUDA cores in f32.  The work is cut into equal shares of row tiles for the device's SMs, whatever the
  * lengths; what a share leaves unfinished is joined by log-sum-exp.
  * --------------------------------------------------------------------------------------------- */
 KV8_API int mla_tree8_workspace_bytes(int R, int H, int B, int q_dtype, size_t *bytes);
