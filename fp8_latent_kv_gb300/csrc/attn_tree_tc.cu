@@ -1,15 +1,16 @@
 // attn_tree_tc.cu -- attention of drafted tokens over a paged latent cache on the tensor cores (tcgen05, sm_103a),
 // for bf16 queries.
 //
-// All (token, head) columns of a sequence read the same rows, so a group of 64 columns against a tile of 128 rows
-// is two contractions:
-//   score    S^T[t][n]  = sum_k K8[t][k] Qs[n][k]      M = 128 rows, N = 128, K = 576 (e4m3 x e4m3)
-//            Qs = [Q_hi; Q_lo]: a bf16 query element, scaled by its column's power of two, is the sum of two e4m3
-//            values, so the two halves of S^T add up to the bf16 dot product.
-//   context  O^T[d][n] += sum_t V8[t][d] W^T[t][n]     M = 128 dims (x4), K = 128 rows; V8 = the same bytes read
-//            MN-major, W the softmax weights as two pieces, hi in e4m3 and lo, what hi leaves, in e5m2: 2^-7 of a
-//            weight at most, and terms down to 2^-22 of the column's largest still count (two e4m3 pieces would
-//            round everything below 2^-16 to nothing, which a long context's many small terms add up to).
+// All (token, head) columns of a sequence read the same rows, so a group of 64 columns against a tile of 64 rows is
+// two contractions:
+//   score    S[x][t]    = sum_k Qs[x][k] K8[t][k]      M = 128, N = 64 rows, K = 576 (e4m3 x e4m3)
+//            Qs: a bf16 query element, scaled by its column's power of two, is the sum of two e4m3 values; each
+//            TMEM lane quadrant holds 16 columns' hi pieces on lanes 0..15 and their lo pieces on lanes 16..31, so
+//            that one shuffle adds the halves of the dot product.
+//   context  O^T[d][n] += sum_t V8[t][d] W[n][t]       M = 128 dims (x4), N = 64 columns, K = 64 rows; V8 = the same
+//            bytes read MN-major, W the softmax weights as two pieces, hi in e4m3 and lo, what hi leaves, in e5m2:
+//            2^-7 of a weight at most, and terms down to 2^-22 of the column's largest still count (two e4m3 pieces
+//            would round everything below 2^-16 to nothing, which a long context's many small terms add up to).
 // Weights: with e_t = score_t log2(e) + log2(scale_t) and a running reference m >= max e - 2 for each column,
 // w_t = 2^(e_t - m + 6) <= 256 holds the row scale already, O = sum w_t v_t and z = sum w_t / scale_t; the factor
 // 2^6 cancels.  A weight's share of e4m3's range then follows its own column's largest term whatever rows, drafted
@@ -17,11 +18,13 @@
 // nothing to O: such rows are only counted, and the count enters z as n0 2^-m at the end.
 //
 // Work: equal shares of (group, tile) units (tree.cuh), one CTA per SM.
-// Warps: 0 = loads, 1 = MMA issue and TMEM, 2..17 = softmax and output in four sets of four warps (a warp per TMEM
-// lane quadrant), 16 columns each; a thread holds one row of the tile.
-// Shared memory: query image 72 KB, eight 16 KB latent blocks (two tiles; a block is refilled as soon as the context
-// product has read it, and the score starts on a block when it lands), one 8 KB RoPE block (free again after the
-// score), weights hi and lo 8 KB each.  TMEM: two score buffers of 128 columns, context accumulators 4 x 64.
+// Warps: 0 = row loads, 1 = MMA issue and TMEM, 2 = the rows' scales, 3..18 = softmax and output; warp % 4 is a
+// warp's TMEM lane quadrant, its set (0..3) picks 16 of the tile's rows, and a thread holds 8 rows of one column.
+// The query pieces are the score's A operand in TMEM, so shared memory holds rows: five stages of 64 rows (36 KB),
+// two 8 KB weight buffers, the queries' RoPE part (8 KB).  Small tiles and many stages because a stage is held from
+// its load through score, softmax and context product, and that chain, not any one unit, set the pace with two
+// stages of 128 rows beside a 72 KB query image (7,500 cycles per 128 rows; see the figures at the kernel).
+// TMEM: query 128 columns, two score buffers of 64, context accumulators 4 x 64.
 // Every wait is bounded in time; one that gives up sets KV8_ERR_TIMEOUT and the CTA winds down.
 #include "sm100.cuh"
 #include "tree.cuh"
@@ -35,44 +38,72 @@ namespace {
 using namespace sm100;
 
 constexpr int kCols = 64;
-constexpr int kRows = 128;
-constexpr int kHG = 16;                    // columns per softmax set
-constexpr int kNG = kCols / kHG;
-constexpr int kSoftmaxThreads = 128 * kNG;
-constexpr int kThreads = 64 + kSoftmaxThreads;
-constexpr uint32_t kBlk = 16384;           // 128 rows x 128 latent bytes (SW128)
-constexpr uint32_t kRope = 8192;           // 128 rows x 64 RoPE bytes (SW64)
-constexpr uint32_t kImg = 4 * kBlk + kRope;
-constexpr uint32_t OFF_Q = 0, OFF_RING = kImg, OFF_ROPE = OFF_RING + 8 * kBlk, OFF_WHI = OFF_ROPE + kRope,
-                   OFF_WLO = OFF_WHI + 8192, OFF_MISC = OFF_WLO + 8192;
+constexpr int kRows = 64;
+constexpr int kStages = 5;
+constexpr int kSoftmaxThreads = 512;
+constexpr int kThreads = 96 + kSoftmaxThreads;
+constexpr uint32_t kBlk = 8192;            // 64 rows x 128 latent bytes (SW128)
+constexpr uint32_t kRope = 4096;           // 64 rows x 64 RoPE bytes (SW64)
+constexpr uint32_t kStage = 4 * kBlk + kRope;
+constexpr uint32_t kQLat = 128 * 512;      // a group's query image: 128 lanes x 512 latent bytes, row-major,
+constexpr uint32_t kQRope = 128 * 64;      // then 128 x 64 RoPE bytes (SW64)
+constexpr uint32_t kImg = kQLat + kQRope;
+constexpr uint32_t kW = 8192;              // hi [64 columns][64 rows] (SW64), then lo
+constexpr uint32_t OFF_ST = 0, OFF_W = kStages * kStage, OFF_Q = OFF_W + 2 * kW, OFF_MISC = OFF_Q + kQRope;
 constexpr float kTau = 2.0f;               // the reference moves when a term exceeds it by more than 2^kTau
 constexpr float kUp = 6.0f;                // weights are held times 2^kUp: at most 2^8 < 448
 constexpr float kTiny = 7.888609e-31f;     // 2^-100
-constexpr uint32_t TM_S = 0, TM_O = 256;  // two score buffers of 128 columns, four accumulators of 64
+constexpr uint32_t TM_Q = 0, TM_S = 128, TM_O = 256;
 
+struct RowInfo {
+    alignas(16) float scale[kRows];        // 0 for rows that are not there
+    alignas(16) float lg[kRows];           // log2(scale) + kUp
+    alignas(16) float inv[kRows];          // 1 / scale
+    uint64_t in, zero;                     // rows that are there / whose scale is below 2^-100
+};
 struct Misc {
-    alignas(16) float m_run[2][kCols];     // reference per column (log2 units), -inf before any attended row
-    alignas(16) float red[4][kCols];       // per-quadrant maxima / row sums
-    alignas(16) float c_head[kCols];       // sm_scale * log2(e) * 2^-e of the column's query
-    alignas(16) float alpha[kNG][kHG];     // rescale factors, and the reference shifts; at the end 1 / z
-    alignas(16) float delta[kNG][kHG];
-    uint64_t blk_full[8], blk_free[8], rope_full, rope_free, q_full, q_free, s_full[2], s_free[2], w_full, lo_free, done[2],
+    RowInfo rows[kStages];
+    alignas(16) float red[4][kCols];       // per-set maxima / sums
+    alignas(16) float alpha[kCols];        // rescale factors; at the end 1 / z
+    uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_full[2], s_free[2], w_full[2], pv_done[2], q_ready,
         final_bar;
     uint32_t tmem_base;
     int abort_flag;
 };
 constexpr uint32_t kSmemBytes = OFF_MISC + sizeof(Misc);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(offsetof(Misc, blk_full) % 8 == 0 && OFF_MISC % 1024 == 0, "alignment");
+static_assert(offsetof(Misc, kv_full) % 8 == 0 && OFF_MISC % 1024 == 0 && OFF_W % 1024 == 0 && kStage % 1024 == 0, "alignment");
 
 struct TcArgs {
     TreeArgs t;
     const uint8_t *img;    // query images, one kImg for each group
-    const float *c_head;   // [images][64]
+    const float *c_head;   // [images][64]: sm_scale * log2(e) * 2^-e of the column's query
 };
 
 // A sequence's groups' images begin at slot q0 * H / 64 + b: never past the next sequence's first.
 __host__ __device__ __forceinline__ int64_t tree_slot(int64_t q0, int H, int b) { return q0 * H / kCols + b; }
+
+// Lane of column n's piece (0 = hi, 1 = lo).
+__device__ __forceinline__ int query_lane(int n, int piece) { return (n >> 4) * 32 + piece * 16 + (n & 15); }
+
+// Score MMA with A in tensor memory.
+__device__ __forceinline__ void mma_f8f6f4_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
 
 __device__ __forceinline__ uint32_t enc_pair(float a, float b) {
     uint16_t v;
@@ -113,6 +144,11 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
 // Query images, column factors, and (block 0) the work shares.  A block splits eight consecutive (row, head)
 // columns, 36 threads each.
 // ------------------------------------------------------------------------------------------------------------
+// Byte offset of 16-byte chunk ch (32 latent, 4 RoPE) of a lane's query pieces.
+__device__ __forceinline__ uint32_t image_offset(int lane, int ch) {
+    return ch < 32 ? (uint32_t)lane * 512u + ch * 16u : kQLat + sw64_offset(lane, (ch - 32) * 16);
+}
+
 constexpr int kPrepCols = 8, kPrepThreads = kPrepCols * 36;
 
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uint8_t *img, float *c_head) {
@@ -184,14 +220,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
         const int col = (row - q.q0) * a.H + head, n = col % kCols;
         const int64_t slot = tree_slot(q.q0, a.H, b) + col / kCols;
         uint8_t *dst = img + slot * kImg;
-        uint32_t off_hi, off_lo;
-        if (ch < 32) {
-            off_hi = (ch >> 3) * kBlk + sw128_offset(n, (ch & 7) * 16);
-            off_lo = (ch >> 3) * kBlk + sw128_offset(n + 64, (ch & 7) * 16);
-        } else {
-            off_hi = 4 * kBlk + sw64_offset(n, (ch - 32) * 16);
-            off_lo = 4 * kBlk + sw64_offset(n + 64, (ch - 32) * 16);
-        }
+        const uint32_t off_hi = image_offset(query_lane(n, 0), ch), off_lo = image_offset(query_lane(n, 1), ch);
         *reinterpret_cast<uint4 *>(dst + off_hi) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(dst + off_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (ch == 0) {
@@ -208,9 +237,8 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
         if (cols <= 0) continue;
         uint8_t *dst = img + pad_slot[c] * kImg;
         for (int i = tid; i < cols * 72; i += kPrepThreads) {
-            const int n = from + i / 72, p = i % 72, lo = p / 36 * 64, k = p % 36;
-            const uint32_t off = k < 32 ? (k >> 3) * kBlk + sw128_offset(n + lo, (k & 7) * 16)
-                                        : 4 * kBlk + sw64_offset(n + lo, (k - 32) * 16);
+            const int n = from + i / 72, p = i % 72;
+            const uint32_t off = image_offset(query_lane(n, p / 36), p % 36);
             *reinterpret_cast<uint4 *>(dst + off) = make_uint4(0u, 0u, 0u, 0u);
         }
         for (int n = from + tid; n < kCols; n += kPrepThreads) c_head[pad_slot[c] * kCols + n] = 0.f;
@@ -218,7 +246,6 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
 }
 
 // ------------------------------------------------------------------------------------------------------------
-// 18 warps: a sub-partition holding 5 warps caps a thread at 96 registers.
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tree_tc_kernel(const __grid_constant__ CUtensorMap map_lc, const __grid_constant__ CUtensorMap map_rc, TcArgs x) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -230,22 +257,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (tid == 0) {
-        for (int s = 0; s < 8; ++s) {
-            mbar_init(&ms.blk_full[s], 1);
-            mbar_init(&ms.blk_free[s], 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ms.kv_full[s], 1);
+            mbar_init(&ms.kv_free[s], 1);
+            mbar_init(&ms.row_full[s], 32);
         }
-        mbar_init(&ms.rope_full, 1);
-        mbar_init(&ms.rope_free, 1);
-        mbar_init(&ms.q_full, 1);
-        mbar_init(&ms.q_free, 1);
         for (int k = 0; k < 2; ++k) {
             mbar_init(&ms.s_full[k], 1);
             mbar_init(&ms.s_free[k], kSoftmaxThreads);
+            mbar_init(&ms.w_full[k], kSoftmaxThreads);
+            mbar_init(&ms.pv_done[k], 1);
         }
-        mbar_init(&ms.w_full, kSoftmaxThreads);
-        mbar_init(&ms.lo_free, 1);
-        mbar_init(&ms.done[0], 1);
-        mbar_init(&ms.done[1], 1);
+        mbar_init(&ms.q_ready, kSoftmaxThreads);
         mbar_init(&ms.final_bar, 1);
         ms.abort_flag = 0;
         fence_barrier_init();
@@ -268,518 +291,489 @@ __global__ void __launch_bounds__(kThreads, 1)
     TreeSegment seg;
 
     if (warp == 0) {
-        // ================================ loads ================================
-        // A block's barrier is armed after its release, which implies that its previous phase is complete.
+        // ================================ row loads ================================
+        // Lane l fetches the tile's l-th piece (a page, or the tile where pages are larger); pieces past the
+        // sequence's rows or outside the cache are not loaded.  A stage's barrier is armed after its release, which
+        // implies that its previous phase is complete.
         const int sub_rows = min(kRows, 1 << a.page_shift), subs = kRows / sub_rows;
-        int it = 0, sg = 0;
-        uint32_t armed = 0;  // per slot: loads in flight since its last arming (bits), 8 = RoPE, 9 = image
+        int it = 0, s = 0;
+        uint32_t ph = 1;  // parity of the release that stage s waits for
         bool ok = true;
         while (ok && walk.next<kCols, kRows>(a, seg)) {
             const int64_t end = seg.q.len + seg.q.n;
-            for (int t = seg.t0; ok && t < seg.t1; ++t, ++it) {
-                // lane l < subs holds the cache row where the tile's l-th piece begins, or -1
+            auto piece = [&](int t) -> int64_t {
                 const int64_t pos = (int64_t)t * kRows + (int64_t)lane * sub_rows;
-                int64_t row = -1;
-                if (lane < subs && pos < end) row = tree_row(a, seg.b, pos);
+                return lane < subs && pos < end ? tree_row(a, seg.b, pos) : -1;
+            };
+            int64_t next = piece(seg.t0);
+            for (int t = seg.t0; t < seg.t1; ++t, ++it) {
+                const int64_t row = next;
+                next = t + 1 < seg.t1 ? piece(t + 1) : -1;  // a page entry's latency ahead
                 const int pieces = __popc(__ballot_sync(0xffffffffu, row >= 0));
-                const uint32_t ph = ((it >> 1) - 1) & 1;
-#pragma unroll 1
-                for (int kb = 0; kb < 4 && ok; ++kb) {
-                    const int s = (it & 1) * 4 + kb;
-                    if (it >= 2) ok = mbar_wait(&ms.blk_free[s], ph, &ms.abort_flag, a.err_word);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(&ms.blk_full[s], (uint32_t)pieces * sub_rows * 128u);
-                    armed |= 1u << s;
-                    __syncwarp();
-                    if (row >= 0)
-                        tma_load_2d(smem + OFF_RING + s * kBlk + lane * sub_rows * 128, &map_lc, kb * 128, (int)row,
-                                    &ms.blk_full[s]);
-                }
-                if (ok && it >= 1) ok = mbar_wait(&ms.rope_free, (it - 1) & 1, &ms.abort_flag, a.err_word);
-                ok = __all_sync(0xffffffffu, ok);
+                if (it >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], ph, &ms.abort_flag, a.err_word));
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&ms.rope_full, (uint32_t)pieces * sub_rows * 64u);
-                armed |= 1u << 8;
+                uint8_t *st = smem + OFF_ST + s * kStage;
+                if (lane == 0) mbar_arrive_expect_tx(&ms.kv_full[s], (uint32_t)pieces * sub_rows * (uint32_t)kRow);
                 __syncwarp();
-                if (row >= 0) tma_load_2d(smem + OFF_ROPE + lane * sub_rows * 64, &map_rc, 512, (int)row, &ms.rope_full);
-                if (t == seg.t0) {
-                    // the segment's query image, once the last score of the segment before it has read the old one
-                    if (sg >= 1) ok = mbar_wait(&ms.q_free, (sg - 1) & 1, &ms.abort_flag, a.err_word);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&ms.q_full, kImg);
-                        const uint8_t *src = x.img + (tree_slot(seg.q.q0, a.H, seg.b) + seg.g) * kImg;
-                        for (int kb = 0; kb < 4; ++kb) bulk_load(smem + OFF_Q + kb * kBlk, src + kb * kBlk, kBlk, &ms.q_full);
-                        bulk_load(smem + OFF_Q + 4 * kBlk, src + 4 * kBlk, kRope, &ms.q_full);
-                    }
-                    armed |= 1u << 9;
-                    ++sg;
+                if (row >= 0) {
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+                        tma_load_2d(st + kb * kBlk + lane * sub_rows * 128, &map_lc, kb * 128, (int)row, &ms.kv_full[s]);
+                    tma_load_2d(st + 4 * kBlk + lane * sub_rows * 64, &map_rc, 512, (int)row, &ms.kv_full[s]);
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
         }
-        // every load in flight lands before the CTA ends: the last phase of each armed barrier
-        if (lane == 0) {
-            const int last = ok ? it - 1 : it;  // after a timeout tile `it` is partly armed: waiting for it too
-            for (int kb = 0; kb < 8; ++kb)
-                if (armed >> kb & 1) {
-                    // the newest tile of this parity whose block was armed
-                    int i = last - ((last ^ (kb >> 2)) & 1);
-                    if (i >= 0) mbar_wait(&ms.blk_full[kb], (i >> 1) & 1, nullptr, a.err_word, ok ? 200000000ull : 20000000ull);
-                }
-            if (armed >> 8 & 1) mbar_wait(&ms.rope_full, last & 1, nullptr, a.err_word, ok ? 200000000ull : 20000000ull);
-            if (armed >> 9 & 1) mbar_wait(&ms.q_full, (sg - 1) & 1, nullptr, a.err_word, 200000000ull);
-        }
+        // every load in flight lands before the CTA ends
+        if (lane == 0)
+            for (int i = max(0, it - kStages); i < it; ++i)
+                mbar_wait(&ms.kv_full[i % kStages], (i / kStages) & 1, nullptr, a.err_word, 200000000ull);
         __syncwarp();
     } else if (warp == 1) {
         // ================================ MMA issue ================================
-        if (lane == 0) {
-            const uint32_t id_s = idesc_e4m3_f32(128, 128, false, false);
-            const uint32_t id_hi = idesc_e4m3_f32(128, 64, true, true), id_lo = id_hi | (1u << 10);  // B in e5m2
-            const uint32_t qb = sbase + OFF_Q, rope = sbase + OFF_ROPE, phi = sbase + OFF_WHI, plo = sbase + OFF_WLO;
-            const int64_t n_tiles = walk.end - walk.unit;
-            auto issue_pv = [&](int j, bool first) {
-                const int s = (j & 1) * 4;
-                const uint32_t st = sbase + OFF_RING + s * kBlk;
-                const uint32_t keep = first ? 0u : 1u;
-                // the lo pieces first: the next tile's may then be written while the hi pieces run
+        // The whole warp runs the loop, its conditions voted on, and one elected lane issues: operands stay in uniform
+        // registers.  (Issued from `if (lane == 0)` the same score MMAs took 46 cycles each instead of 32 alone, and
+        // 85 beside the softmax warps.)
+        const uint32_t id_s = idesc_e4m3_f32(128, kRows, false, false);
+        const uint32_t id_hi = idesc_e4m3_f32(128, kCols, true, false), id_lo = id_hi | (1u << 10);  // B in e5m2
+        // descriptors of stage 0, weight buffer 0 and the query's RoPE part: an offset adds to the address field
+        const uint64_t k_desc = smem_desc(sbase + OFF_ST, 0, 1024, kSw128);
+        const uint64_t kr_desc = smem_desc(sbase + OFF_ST + 4 * kBlk, 0, 512, kSw64);
+        const uint64_t qr_desc = smem_desc(sbase + OFF_Q, 0, 512, kSw64);
+        const uint64_t w_desc = smem_desc(sbase + OFF_W, 0, 512, kSw64);
+        const int n_tiles = (int)(walk.end - walk.unit);
+        int ns = 0, np = 0, sg = 0, ss = 0, ps = 0;  // tiles, segments and stages of the score / the product
+        uint32_t s_ph = 0;                           // parity of stage ss's load
+        int seg_first = 0, seg_end = 0;              // the score side's segment
+        uint32_t firsts = 0;                         // bit i % 32: tile i begins a segment
+        uint64_t t_last = globaltimer_ns();
+        uint32_t spins = 0;
+        auto ready = [&](uint64_t *bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+        };
+        while (np < n_tiles) {
+            bool did = false;
+            if (np < ns && ready(&ms.w_full[np & 1], (np >> 1) & 1)) {
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t v = k_desc + (uint64_t)(ps * (kStage >> 4));  // (the same bytes, MN-major)
+                    const uint64_t w = w_desc + (uint64_t)((np & 1) * (kW >> 4));
+                    const uint32_t keep = firsts >> (np & 31) & 1 ? 0u : 1u;
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
+                    for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f8f6f4(tmem + TM_O + 64u * ch, smem_desc(st + ch * kBlk + kk * 4096, 0, 1024, kSw128),
-                                   smem_desc(plo + kk * 2048, 0, 512, kSw64), id_lo, kk ? 1u : keep);
-                mma_commit(&ms.lo_free);
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f8f6f4(tmem + TM_O + 64u * ch, smem_desc(st + ch * kBlk + kk * 4096, 0, 1024, kSw128),
-                                   smem_desc(phi + kk * 2048, 0, 512, kSw64), id_hi, 1u);
-                    mma_commit(&ms.blk_free[s + ch]);
-                }
-                mma_commit(&ms.done[j & 1]);
-            };
-            // whichever is ready: the next context product (its weights written), else the next part of the next
-            // score (part kb needs latent block kb, part 4 the RoPE block)
-            int ns = 0, part = 0, np = 0, sg = 0;
-            int seg_end = 0;          // first tile after the score side's segment
-            uint32_t firsts = 0;      // bit i % 32: tile i begins a segment
-            uint64_t t_last = globaltimer_ns();
-            uint32_t spins = 0;
-            while (np < n_tiles) {
-                bool did = false;
-                if (np < ns && mbar_test_wait(&ms.w_full, np & 1)) {
-                    tc_fence_after_sync();
-                    issue_pv(np, firsts >> (np & 31) & 1);
-                    ++np;
-                    did = true;
-                } else if (ns < n_tiles) {
-                    bool ready = true;
-                    if (part == 0) {
-                        if (ns == seg_end) {  // a new segment
-                            walk.next<kCols, kRows>(a, seg);
-                            seg_end = ns + (seg.t1 - seg.t0);
-                            ++sg;
-                            firsts |= 1u << (ns & 31);
-                        } else if (ns != seg_end - (seg.t1 - seg.t0)) {
-                            firsts &= ~(1u << (ns & 31));
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const uint64_t av = v + (uint64_t)((ch * kBlk + kk * 4096) >> 4);
+                            mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kk * 32) >> 4), id_hi, kk ? 1u : keep);
+                            mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kW / 2 + kk * 32) >> 4), id_lo, 1u);
                         }
-                        ready = mbar_test_wait(&ms.q_full, (sg - 1) & 1) && (ns < 2 || mbar_test_wait(&ms.s_free[ns & 1], ((ns >> 1) - 1) & 1));
-                    }
-                    const int s = (ns & 1) * 4;
-                    if (ready) ready = part < 4 ? mbar_test_wait(&ms.blk_full[s + part], (ns >> 1) & 1)
-                                                : mbar_test_wait(&ms.rope_full, ns & 1);
-                    if (ready) {
-                        tc_fence_after_sync();
-                        if (part < 4) {
-                            const uint32_t kblk = sbase + OFF_RING + (s + part) * kBlk, qblk = qb + part * kBlk;
+                    mma_commit(&ms.kv_free[ps]);
+                    mma_commit(&ms.pv_done[np & 1]);
+                }
+                __syncwarp();
+                if (++ps == kStages) ps = 0;
+                ++np;
+                did = true;
+            } else if (ns < n_tiles) {
+                if (ns == seg_end) {  // a new segment
+                    walk.next<kCols, kRows>(a, seg);
+                    seg_first = ns;
+                    seg_end = ns + (seg.t1 - seg.t0);
+                    ++sg;
+                }
+                if (ready(&ms.kv_full[ss], s_ph) && (ns < 2 || ready(&ms.s_free[ns & 1], ((ns >> 1) - 1) & 1)) &&
+                    (ns > seg_first || ready(&ms.q_ready, (sg - 1) & 1))) {
+                    tc_fence_after_sync();
+                    firsts = ns == seg_first ? firsts | 1u << (ns & 31) : firsts & ~(1u << (ns & 31));
+                    if (elect_one()) {
+                        const uint32_t d = tmem + TM_S + 64u * (ns & 1);
+                        const uint64_t k = k_desc + (uint64_t)(ss * (kStage >> 4)), kr = kr_desc + (uint64_t)(ss * (kStage >> 4));
+#pragma unroll
+                        for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_f8f6f4(tmem + TM_S + 128u * (ns & 1), smem_desc(kblk + kk * 32, 0, 1024, kSw128),
-                                           smem_desc(qblk + kk * 32, 0, 1024, kSw128), id_s, (part | kk) != 0);
-                            ++part;
-                        } else {
+                                mma_f8f6f4_ts(d, tmem + TM_Q + kb * 32 + kk * 8, k + (uint64_t)((kb * kBlk + kk * 32) >> 4), id_s,
+                                              (kb | kk) != 0);
 #pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)
-                                mma_f8f6f4(tmem + TM_S + 128u * (ns & 1), smem_desc(rope + kk * 32, 0, 512, kSw64),
-                                           smem_desc(qb + 4 * kBlk + kk * 32, 0, 512, kSw64), id_s, 1u);
-                            mma_commit(&ms.s_full[ns & 1]);
-                            mma_commit(&ms.rope_free);
-                            if (ns + 1 == seg_end) mma_commit(&ms.q_free);
-                            ++ns;
-                            part = 0;
-                        }
-                        did = true;
+                        for (int kk = 0; kk < 2; ++kk)
+                            mma_f8f6f4(d, qr_desc + (uint64_t)(kk * 2), kr + (uint64_t)(kk * 2), id_s, 1u);
+                        mma_commit(&ms.s_full[ns & 1]);
                     }
-                }
-                if (did) {
-                    spins = 0;
-                } else if ((++spins & 255u) == 0) {
-                    const uint64_t now = globaltimer_ns();
-                    if (*(volatile int *)&ms.abort_flag) break;
-                    if (spins > 256u && now - t_last > 2000000000ull) {  // no progress for 2 s
-                        ms.abort_flag = 1;
-                        if (a.err_word) atomicOr(a.err_word, (int)KV8_ERR_TIMEOUT);
-                        break;
+                    __syncwarp();
+                    ++ns;
+                    if (++ss == kStages) {
+                        ss = 0;
+                        s_ph ^= 1;
                     }
-                } else if (spins == 1) {
-                    t_last = globaltimer_ns();
+                    did = true;
                 }
             }
-            mma_commit(&ms.final_bar);  // all issued MMAs complete before the CTA tears down
-            mbar_wait(&ms.final_bar, 0, nullptr, a.err_word, 200000000ull);
+            if (did) {
+                spins = 0;
+            } else if ((++spins & 255u) == 0) {
+                const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+                if (__any_sync(0xffffffffu, *(volatile int *)&ms.abort_flag)) break;
+                if (spins > 256u && now - t_last > 2000000000ull) {  // no progress for 2 s
+                    if (lane == 0) {
+                        ms.abort_flag = 1;
+                        if (a.err_word) atomicOr(a.err_word, (int)KV8_ERR_TIMEOUT);
+                    }
+                    break;
+                }
+            } else if (spins == 1) {
+                t_last = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+            }
         }
+        if (elect_one()) mma_commit(&ms.final_bar);  // all issued MMAs complete before the CTA tears down
         __syncwarp();
+        mbar_wait(&ms.final_bar, 0, nullptr, a.err_word, 200000000ull);
+        __syncwarp();
+    } else if (warp == 2) {
+        // ================================ the rows' scales ================================
+        // Four tiles at a time, eight rows per lane: their page entries, then their scales, one latency each; the
+        // stages' five sets of row figures keep this ahead of the softmax.
+        constexpr int kBatch = 4;
+        int it = 0;
+        bool ok = true, bad_page = false;
+        while (ok && walk.next<kCols, kRows>(a, seg)) {
+            const int64_t end = seg.q.len + seg.q.n;
+            for (int t = seg.t0; ok && t < seg.t1; t += kBatch) {
+                int64_t row[2 * kBatch];
+                float sc[2 * kBatch];
+#pragma unroll
+                for (int u = 0; u < 2 * kBatch; ++u) {
+                    const int64_t pos = (int64_t)t * kRows + 32 * u + lane;
+                    row[u] = -1;
+                    if (t + u / 2 < seg.t1 && pos < end) {
+                        row[u] = tree_row(a, seg.b, pos);
+                        bad_page |= row[u] < 0;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2 * kBatch; ++u) sc[u] = row[u] >= 0 ? __ldg(a.kv_scale + row[u]) : 0.f;
+#pragma unroll
+                for (int v = 0; v < kBatch; ++v) {
+                    if (t + v >= seg.t1) break;
+                    const int s = it % kStages;
+                    if (it >= kStages)
+                        ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], (it / kStages - 1) & 1, &ms.abort_flag, a.err_word));
+                    if (!ok) break;
+                    RowInfo &ri = ms.rows[s];
+                    uint32_t in[2], zero[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float c = sc[2 * v + h];
+                        const bool there = row[2 * v + h] >= 0;
+                        in[h] = __ballot_sync(0xffffffffu, there);
+                        zero[h] = __ballot_sync(0xffffffffu, there && c < kTiny);
+                        ri.scale[32 * h + lane] = c;
+                        ri.lg[32 * h + lane] = lg2_approx(c) + kUp;
+                        // 0 for a zero row (its weight is 0) and for a scale that is not finite (its weight is NaN
+                        // where it is attended)
+                        ri.inv[32 * h + lane] = c >= kTiny && c <= 3.402823466e38f ? __fdividef(1.f, c) : 0.f;
+                    }
+                    if (lane == 0) {
+                        ri.in = in[0] | (uint64_t)in[1] << 32;
+                        ri.zero = zero[0] | (uint64_t)zero[1] << 32;
+                    }
+                    mbar_arrive(&ms.row_full[s]);
+                    ++it;
+                }
+            }
+        }
+        if (bad_page && a.err_word) atomicOr(a.err_word, (int)KV8_ERR_INDEX);
     } else {
         // ============================ softmax and output ============================
-        // A wait that gives up clears `ok`; the thread then skips its remaining waits but still reaches every named
-        // barrier, so that no other warp waits for it.
-        constexpr int kV4 = kHG / 4, kP = kHG / 2;
-        const int q = warp & 3, grp = (warp - 2) >> 2, h0 = kHG * grp, r = q * 32 + lane;
+        // A wait that gives up clears `ok` (the same in a warp's lanes: TMEM accesses need all of them); the warp
+        // then skips its remaining waits but still reaches every named barrier, so that no other warp waits for it.
+        const int st = tid - 96;                        // 0..511
+        const int q = warp & 3, set = (warp - 3) >> 2;  // TMEM lane quadrant; rows 16 set .. 16 set + 15
+        const int half = lane >> 4;                     // this thread's 8 of them
+        const int n = 16 * q + (lane & 15);             // its column
+        const int r0 = 16 * set + 8 * half;             // its first row
         const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
-        const int bar_id = 2 + grp;
-        const int pshift = a.page_shift;
-        const int64_t pmask = ((int64_t)1 << pshift) - 1;
-        bool ok = true, bad_page = false;  // ok is the same in a warp's lanes: TMEM loads need all of them
+        const int h0 = 16 * set;                        // rescale and output: columns h0..h0+15, dims 128 c + 32 q + lane
+        bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &ms.abort_flag, a.err_word));
         };
         grid_launch_dependents();
-        int it = 0;
+        int it = 0, s = 0;
+        uint32_t s_ph = 0;
         while (walk.next<kCols, kRows>(a, seg)) {
-            const int64_t end = seg.q.len + seg.q.n;
-            const int32_t *table = a.table + (int64_t)seg.b * a.max_pages;
             const int64_t slot = tree_slot(seg.q.q0, a.H, seg.b) + seg.g;
-            named_sync(bar_id, 128);  // the set's arrays: every warp is done with the segment before
-            if (q == 0 && lane < kHG) {
-                ms.c_head[h0 + lane] = x.c_head[slot * kCols + h0 + lane];
-                ms.m_run[0][h0 + lane] = -INFINITY;
-            }
-            named_sync(bar_id, 128);
-            uint64_t z2[kP];
+            // ---- the group's queries: 128 latent bytes of this thread's lane to TMEM, one RoPE chunk to shared memory.
+            // (The scores of the segment before are complete: their last one has been read here.)
+            {
+                const uint8_t *img = x.img + slot * kImg;
+                const uint4 *src = reinterpret_cast<const uint4 *>(img + (32 * q + lane) * 512 + set * 128);
+                uint4 v[8];
 #pragma unroll
-            for (int j = 0; j < kP; ++j) z2[j] = f2_pack(0.f, 0.f);
-            // the row of position pos: page entries are fetched two tiles ahead, scales one
-            auto page_of = [&](int64_t pos) -> int64_t { return pos < end ? (int64_t)__ldg(table + (pos >> pshift)) : -1; };
-            auto scale_of = [&](int64_t pos, int64_t page, bool &in) -> float {
-                const int64_t row = (page << pshift) + (pos & pmask);
-                in = page >= 0 && row < a.cache_rows;
-                bad_page |= pos < end && !in;
-                return in ? __ldg(a.kv_scale + row) : 1.f;
-            };
-            bool in_next;
-            const int64_t p_first = (int64_t)seg.t0 * kRows + r;
-            int64_t page2 = page_of(p_first);
-            float sc_next = scale_of(p_first, page2, in_next);
-            page2 = seg.t0 + 1 < seg.t1 ? page_of(p_first + kRows) : -1;
-            int n0 = 0;             // zero rows of the context that this thread has met
-            uint32_t n0_draft = 0;  // and of the draft, column j's count in bits j and 16 + j
-            bool seen = false;  // every column of the set has a finite reference
-            int cur = 0;        // which copy of ms.m_run is current
-            for (int t = seg.t0; t < seg.t1; ++t, ++it) {
-                const int64_t pos = (int64_t)t * kRows + r;
-                const float sc = sc_next;
-                const bool in = in_next;
-                if (t + 1 < seg.t1) {
-                    sc_next = scale_of(pos + kRows, page2, in_next);
-                    if (t + 2 < seg.t1) page2 = page_of(pos + 2 * kRows);
-                }
-                // which of the 16 columns attend the row: all of them in the context, by their bits in the draft
-                uint32_t sees = in ? 0xFFFFu : 0u;
-                const int64_t draft = pos - seg.q.len;
-                const bool drafted = in && draft >= 0;
-                if (drafted) {
-                    sees = 0;
-                    const int c0 = seg.g * kCols + h0, top = seg.q.n * a.H;
-                    int node = c0 / a.H, left = a.H - (c0 - node * a.H);
-#pragma unroll 1
-                    for (int j = 0; j < kHG; ++j) {
-                        if (c0 + j < top && tree_sees(a, seg.q.q0, node, (int)draft)) sees |= 1u << j;
-                        if (--left == 0) {
-                            ++node;
-                            left = a.H;
-                        }
-                    }
-                }
-                if (sc < kTiny) {  // a zero row: counted, and left out of everything else
-                    if (!drafted) n0 += sees ? 1 : 0;
-                    else {  // two bits for each column: a thread has at most three of the draft's rows
-                        const uint32_t both = n0_draft & 0xFFFFu & sees;
-                        n0_draft = (n0_draft ^ sees) ^ (both << 16);
-                    }
-                    sees = 0;
-                }
-                const float lg = lg2_approx(sc) + kUp;
-                // 0 for a zero row (its w is 0) and for a scale that is not finite (its w is NaN where it is attended)
-                const float inv = sc >= kTiny && sc <= 3.402823466e38f ? __fdividef(1.f, sc) : 0.f;
-
-                wait(&ms.s_full[it & 1], (it >> 1) & 1);
-                tc_fence_after_sync();
-                uint64_t s2[kP];  // hi + lo halves of the score, column pairs packed
-                {
-                    uint32_t shi[16], slo[16];
-                    const uint32_t ta = tmem + lane_addr + TM_S + 128u * (it & 1) + (uint32_t)h0;
-                    tmem_ld_32x32b_x16(ta, shi);
-                    tmem_ld_32x32b_x16(ta + 64u, slo);
-                    tmem_wait_ld();
+                for (int k = 0; k < 8; ++k) v[k] = __ldg(src + k);
+                const uint4 rp = __ldg(reinterpret_cast<const uint4 *>(img + kQLat) + st);
 #pragma unroll
-                    for (int j = 0; j < kP; ++j)
-                        s2[j] = f2_add(f2_pack(__uint_as_float(shi[2 * j]), __uint_as_float(shi[2 * j + 1])),
-                                       f2_pack(__uint_as_float(slo[2 * j]), __uint_as_float(slo[2 * j + 1])));
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t w[16] = {v[4 * k].x,     v[4 * k].y,     v[4 * k].z,     v[4 * k].w,
+                                            v[4 * k + 1].x, v[4 * k + 1].y, v[4 * k + 1].z, v[4 * k + 1].w,
+                                            v[4 * k + 2].x, v[4 * k + 2].y, v[4 * k + 2].z, v[4 * k + 2].w,
+                                            v[4 * k + 3].x, v[4 * k + 3].y, v[4 * k + 3].z, v[4 * k + 3].w};
+                    tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + set * 32 + 16 * k, w);
                 }
+                *reinterpret_cast<uint4 *>(smem + OFF_Q + st * 16) = rp;
+                tmem_wait_st();
+                fence_proxy_async_smem();
                 tc_fence_before_sync();
-                mbar_arrive(&ms.s_free[it & 1]);
-                // d = e + 6 - m (m counts as 0 while it is -inf)
-                uint64_t d2[kP];
+                mbar_arrive(&ms.q_ready);
+            }
+            const float c_q = __ldg(x.c_head + slot * kCols + n);
+            const int col = seg.g * kCols + n, top = seg.q.n * a.H;
+            const int node = col < top ? col / a.H : 0;
+            float m = -INFINITY, z = 0.f;
+            int n0 = 0;  // zero rows that the column attends among this thread's rows
+            for (int t = seg.t0; t < seg.t1; ++t, ++it) {
+                const int64_t p0 = (int64_t)t * kRows;
+                const int buf = it & 1;
+                // ---- the rows' figures, and which of the thread's 8 rows the column attends
+                wait(&ms.row_full[s], s_ph);
+                const RowInfo &ri = ms.rows[s];
+                const uint64_t in = ri.in;
+                uint32_t on = (uint32_t)(in >> r0) & 0xFFu;
+                const int64_t draft = p0 + r0 - seg.q.len;  // the first row's index in the draft
+                const bool drafted = p0 + kRows > seg.q.len;
+                if (drafted) {
+                    // bits draft .. draft + 7 of the token's mask row; a row of the context counts as set
+                    uint32_t bits = 0;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (draft + u < 0 || ((on >> u & 1) && tree_sees(a, seg.q.q0, node, (int)(draft + u)))) bits |= 1u << u;
+                    on &= bits;
+                }
+                const uint32_t zr = (uint32_t)(ri.zero >> r0) & on;
+                n0 += __popc(zr);
+                on ^= zr;
+                float4 f4[2];
+                uint64_t cs[4], lg[4], inv[4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    f4[0] = *reinterpret_cast<const float4 *>(&ri.scale[r0 + 4 * k]);
+                    const uint64_t c2 = f2_pack(c_q, c_q);
+                    cs[2 * k] = f2_mul(f2_pack(f4[0].x, f4[0].y), c2);
+                    cs[2 * k + 1] = f2_mul(f2_pack(f4[0].z, f4[0].w), c2);
+                    f4[0] = *reinterpret_cast<const float4 *>(&ri.lg[r0 + 4 * k]);
+                    lg[2 * k] = f2_pack(f4[0].x, f4[0].y);
+                    lg[2 * k + 1] = f2_pack(f4[0].z, f4[0].w);
+                    f4[0] = *reinterpret_cast<const float4 *>(&ri.inv[r0 + 4 * k]);
+                    inv[2 * k] = f2_pack(f4[0].x, f4[0].y);
+                    inv[2 * k + 1] = f2_pack(f4[0].z, f4[0].w);
+                }
+                // ---- scores: 16 rows of this thread's piece; a shuffle adds the other piece's half of 8 of them
+                wait(&ms.s_full[buf], (it >> 1) & 1);
+                tc_fence_after_sync();
+                uint64_t d2[4];
+                {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 64u * buf + (uint32_t)h0, v);
+                    tmem_wait_ld();
+                    tc_fence_before_sync();
+                    mbar_arrive(&ms.s_free[buf]);
+                    float sv[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float send = __uint_as_float(half ? v[j] : v[8 + j]), keep = __uint_as_float(half ? v[8 + j] : v[j]);
+                        sv[j] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d2[j] = f2_pack(sv[2 * j], sv[2 * j + 1]);
+                }
+                // ---- d = e + 6 - m (m counts as 0 while it is -inf)
+                const float ref_o = m == -INFINITY ? 0.f : m;
                 float dmax = -INFINITY;
                 {
-                    const uint64_t st2 = f2_pack(sc, sc), lg2 = f2_pack(lg, lg);
+                    const uint64_t mr = f2_pack(-ref_o, -ref_o);
+                    float d[8];
 #pragma unroll
-                    for (int j4 = 0; j4 < kV4; ++j4) {
-                        const float4 c4 = *reinterpret_cast<const float4 *>(&ms.c_head[h0 + 4 * j4]);
-                        float4 r4 = *reinterpret_cast<const float4 *>(&ms.m_run[cur][h0 + 4 * j4]);
-                        if (!seen) {
-                            r4.x = r4.x == -INFINITY ? 0.f : r4.x;
-                            r4.y = r4.y == -INFINITY ? 0.f : r4.y;
-                            r4.z = r4.z == -INFINITY ? 0.f : r4.z;
-                            r4.w = r4.w == -INFINITY ? 0.f : r4.w;
-                        }
-                        d2[2 * j4] = f2_fma(s2[2 * j4], f2_mul(f2_pack(c4.x, c4.y), st2), f2_add(lg2, f2_pack(-r4.x, -r4.y)));
-                        d2[2 * j4 + 1] =
-                            f2_fma(s2[2 * j4 + 1], f2_mul(f2_pack(c4.z, c4.w), st2), f2_add(lg2, f2_pack(-r4.z, -r4.w)));
+                    for (int j = 0; j < 4; ++j) {
+                        d2[j] = f2_fma(d2[j], cs[j], f2_add(lg[j], mr));
+                        f2_unpack(d2[j], d[2 * j], d[2 * j + 1]);
                     }
-                    if (sees != 0xFFFFu) {
+                    if (on != 0xFFu) {
 #pragma unroll
-                        for (int j = 0; j < kP; ++j) {
-                            float u, v;
-                            f2_unpack(d2[j], u, v);
-                            d2[j] = f2_pack(sees >> (2 * j) & 1 ? u : -INFINITY, sees >> (2 * j + 1) & 1 ? v : -INFINITY);
-                        }
+                        for (int j = 0; j < 8; ++j) d[j] = on >> j & 1 ? d[j] : -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) d2[j] = f2_pack(d[2 * j], d[2 * j + 1]);
                     }
 #pragma unroll
-                    for (int j = 0; j < kP; ++j) {
-                        float u, v;
-                        f2_unpack(d2[j], u, v);
-                        dmax = fmaxf(dmax, fmaxf(u, v));
-                    }
+                    for (int j = 0; j < 8; ++j) dmax = fmaxf(dmax, d[j]);
                 }
-                // the set moves its references together when a term exceeds one by more than kTau, or while a column
-                // has none
-                const bool slow = bar_red_or(bar_id, 128, dmax > kTau + kUp || !seen);
-                bool any_alpha = false;
+                // all columns move their references together: when a term exceeds one by more than kTau, or a column
+                // that has none meets its first row
+                const bool slow = bar_red_or(1, kSoftmaxThreads, dmax > kTau + kUp || (m == -INFINITY && dmax > -INFINITY));
                 if (slow) {
-                    float hm[kHG];
+                    const float hm = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 16));
+                    if (half == 0) ms.red[set][n] = hm;
+                    named_sync(1, kSoftmaxThreads);
+                    const float tmax = fmaxf(fmaxf(ms.red[0][n], ms.red[1][n]), fmaxf(ms.red[2][n], ms.red[3][n])) + (ref_o - kUp);
+                    const float mn = m == -INFINITY ? tmax : (tmax > m + kTau ? tmax : m);
+                    const float al = (m == -INFINITY || mn == m) ? 1.f : ex2_approx(m - mn);
+                    if (set == 0 && half == 0) ms.alpha[n] = al;
+                    const float dl = mn == -INFINITY ? 0.f : ref_o - mn;
+                    m = mn;
+                    z *= al;
+                    const uint64_t dl2 = f2_pack(dl, dl);
 #pragma unroll
-                    for (int j = 0; j < kP; ++j) {
-                        float u, v;
-                        f2_unpack(d2[j], u, v);
-                        hm[2 * j] = warp_redux_max(u);
-                        hm[2 * j + 1] = warp_redux_max(v);
-                    }
-                    if (lane == 0) {
+                    for (int j = 0; j < 4; ++j) d2[j] = f2_add(d2[j], dl2);
+                    if (bar_red_or(1, kSoftmaxThreads, al != 1.f) && t > seg.t0) {
+                        // rescale this warp's part of the accumulators once the context product before is complete
+                        wait(&ms.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+                        tc_fence_after_sync();
+                        float f[16];
 #pragma unroll
-                        for (int j4 = 0; j4 < kV4; ++j4)
-                            *reinterpret_cast<float4 *>(&ms.red[q][h0 + 4 * j4]) =
-                                make_float4(hm[4 * j4], hm[4 * j4 + 1], hm[4 * j4 + 2], hm[4 * j4 + 3]);
-                    }
-                    const int hl = lane & (kHG - 1), hj = h0 + hl;
-                    named_sync(bar_id, 128);
-                    const float mo = ms.m_run[cur][hj], ref_o = mo == -INFINITY ? 0.f : mo;
-                    const float tmax = fmaxf(fmaxf(ms.red[0][hj], ms.red[1][hj]), fmaxf(ms.red[2][hj], ms.red[3][hj])) + (ref_o - kUp);
-                    const float mn = mo == -INFINITY ? tmax : (tmax > mo + kTau ? tmax : mo);
-                    const float al = (mo == -INFINITY || mn == mo) ? 1.f : ex2_approx(mo - mn);
-                    const float ref_n = mn == -INFINITY ? 0.f : mn;
-                    if (lane < kHG) {  // the four quadrant warps write the same values
-                        ms.m_run[cur ^ 1][hj] = mn;
-                        ms.alpha[grp][hl] = al;
-                        ms.delta[grp][hl] = ref_o - ref_n;
-                    }
-                    seen = __all_sync(0xffffffffu, mn != -INFINITY);
-                    any_alpha = __any_sync(0xffffffffu, al != 1.f);
-                    __syncwarp();
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 a4 = *reinterpret_cast<const float4 *>(&ms.alpha[h0 + 4 * k]);
+                            f[4 * k] = a4.x;
+                            f[4 * k + 1] = a4.y;
+                            f[4 * k + 2] = a4.z;
+                            f[4 * k + 3] = a4.w;
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o);
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int j4 = 0; j4 < kV4; ++j4) {
-                        const float4 a4 = *reinterpret_cast<const float4 *>(&ms.alpha[grp][4 * j4]);
-                        const float4 e4 = *reinterpret_cast<const float4 *>(&ms.delta[grp][4 * j4]);
-                        d2[2 * j4] = f2_add(d2[2 * j4], f2_pack(e4.x, e4.y));
-                        d2[2 * j4 + 1] = f2_add(d2[2 * j4 + 1], f2_pack(e4.z, e4.w));
-                        z2[2 * j4] = f2_mul(z2[2 * j4], f2_pack(a4.x, a4.y));
-                        z2[2 * j4 + 1] = f2_mul(z2[2 * j4 + 1], f2_pack(a4.z, a4.w));
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[j]);
+                            tmem_st_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o);
+                        }
+                        tmem_wait_st();
                     }
-                    cur ^= 1;
                 }
-                const uint64_t inv2 = f2_pack(inv, inv);
-                uint32_t whi[kV4], wlo[kV4];
+                // ---- weights
+                uint32_t whi[2], wlo[2];
 #pragma unroll
-                for (int j4 = 0; j4 < kV4; ++j4) {
-                    float d0, d1, e0, e1;
-                    f2_unpack(d2[2 * j4], d0, d1);
-                    f2_unpack(d2[2 * j4 + 1], e0, e1);
-                    const float w0 = ex2_approx(d0), w1 = ex2_approx(d1), w3 = ex2_approx(e0), w4 = ex2_approx(e1);
-                    z2[2 * j4] = f2_fma(f2_pack(w0, w1), inv2, z2[2 * j4]);
-                    z2[2 * j4 + 1] = f2_fma(f2_pack(w3, w4), inv2, z2[2 * j4 + 1]);
+                for (int k = 0; k < 2; ++k) {
+                    float d0, d1, d3, d4;
+                    f2_unpack(d2[2 * k], d0, d1);
+                    f2_unpack(d2[2 * k + 1], d3, d4);
+                    const float w0 = ex2_approx(d0), w1 = ex2_approx(d1), w3 = ex2_approx(d3), w4 = ex2_approx(d4);
+                    float u0, u1, u3, u4;
+                    f2_unpack(f2_mul(f2_pack(w0, w1), inv[2 * k]), u0, u1);
+                    f2_unpack(f2_mul(f2_pack(w3, w4), inv[2 * k + 1]), u3, u4);
+                    z += (u0 + u1) + (u3 + u4);
                     uint32_t h01, l01, h23, l23;
                     split_weights(w0, w1, h01, l01);
                     split_weights(w3, w4, h23, l23);
-                    whi[j4] = h01 | (h23 << 16);
-                    wlo[j4] = l01 | (l23 << 16);
+                    whi[k] = h01 | (h23 << 16);
+                    wlo[k] = l01 | (l23 << 16);
                 }
-                // rows that were not loaded, and NaN codes of drafted rows (attended columns have NaN weights
-                // already): a weight of 0 must not meet them.  Thread (row, set) owns the row's bytes in block `grp`.
-                if (!in || drafted) {
-                    // (complete since before the score: this makes the copy's bytes visible here too)
-                    (void)mbar_wait(&ms.blk_full[(it & 1) * 4 + grp], (it >> 1) & 1, &ms.abort_flag, a.err_word);
-                    uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_RING + ((it & 1) * 4 + grp) * kBlk + r * 128);
+                // ---- rows that were not loaded, and NaN codes of drafted rows (attended columns have NaN weights
+                // already): a weight of 0 must not meet them.  Two threads own a row's 128 bytes of a latent block.
+                if (drafted || in != ~(uint64_t)0) {
+                    const int r = (st >> 1) & 63;
+                    const bool there = in >> r & 1;
+                    if (!there || p0 + r >= seg.q.len) {
+                        // (complete since before the score: this makes the copy's bytes visible here too)
+                        (void)mbar_wait(&ms.kv_full[s], s_ph, &ms.abort_flag, a.err_word);
+                        uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s * kStage + (st >> 7) * kBlk + r * 128 + (st & 1) * 64);
 #pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (in) {
-                            v = p[k];
-                            v.x = without_nan(v.x);
-                            v.y = without_nan(v.y);
-                            v.z = without_nan(v.z);
-                            v.w = without_nan(v.w);
-                        }
-                        p[k] = v;
-                    }
-                }
-                if (it >= 1) {
-                    // the context product before has read its lo weights
-                    wait(&ms.lo_free, (it - 1) & 1);
-                }
-                *reinterpret_cast<uint4 *>(smem + OFF_WLO + sw64_offset(r, h0)) = make_uint4(wlo[0], wlo[1], wlo[2], wlo[3]);
-                auto rescale_trip = [&](int c0) {
-                    uint32_t o[2][kHG];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x16(tmem + lane_addr + TM_O + 64u * (c0 + c) + (uint32_t)h0, o[c]);
-                    tmem_wait_ld();
-                    const float *al = ms.alpha[grp];
-#pragma unroll
-                    for (int j4 = 0; j4 < kV4; ++j4) {
-                        const float4 a4 = *reinterpret_cast<const float4 *>(al + 4 * j4);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t *oc = &o[c][4 * j4];
-                            oc[0] = __float_as_uint(__uint_as_float(oc[0]) * a4.x);
-                            oc[1] = __float_as_uint(__uint_as_float(oc[1]) * a4.y);
-                            oc[2] = __float_as_uint(__uint_as_float(oc[2]) * a4.z);
-                            oc[3] = __float_as_uint(__uint_as_float(oc[3]) * a4.w);
+                        for (int k = 0; k < 4; ++k) {
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (there) {
+                                v = p[k];
+                                v.x = without_nan(v.x);
+                                v.y = without_nan(v.y);
+                                v.z = without_nan(v.z);
+                                v.w = without_nan(v.w);
+                            }
+                            p[k] = v;
                         }
                     }
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) tmem_st_32x32b_x16(tmem + lane_addr + TM_O + 64u * (c0 + c) + (uint32_t)h0, o[c]);
-                };
-                const bool rescale = any_alpha && t > seg.t0;
-                if (it >= 1) wait(&ms.done[(it - 1) & 1], ((it - 1) >> 1) & 1);
-                *reinterpret_cast<uint4 *>(smem + OFF_WHI + sw64_offset(r, h0)) = make_uint4(whi[0], whi[1], whi[2], whi[3]);
-                if (rescale) {
-                    tc_fence_after_sync();
-                    rescale_trip(0);
-                    rescale_trip(2);
-                    tmem_wait_st();
                 }
+                // the context product two tiles back has read this weight buffer
+                if (it >= 2) wait(&ms.pv_done[buf], ((it >> 1) - 1) & 1);
+                uint8_t *wb = smem + OFF_W + buf * kW + sw64_offset(n, r0);
+                *reinterpret_cast<uint2 *>(wb) = make_uint2(whi[0], whi[1]);
+                *reinterpret_cast<uint2 *>(wb + kW / 2) = make_uint2(wlo[0], wlo[1]);
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
-                mbar_arrive(&ms.w_full);
+                mbar_arrive(&ms.w_full[buf]);
+                if (++s == kStages) {
+                    s = 0;
+                    s_ph ^= 1;
+                }
             }
 
-            // ---- output: sums over the warp's rows (lane l ends up with column l % 16), then over the quadrants
-            auto over_rows = [&](float (&v)[kHG]) -> float {
-#pragma unroll
-                for (int k = kHG / 2; k >= 1; k >>= 1) {
-                    const bool upper = (lane & k) != 0;
-#pragma unroll
-                    for (int j = 0; j < k; ++j) {
-                        const float send = upper ? v[j] : v[j + k], keep = upper ? v[j + k] : v[j];
-                        v[j] = keep + __shfl_xor_sync(0xffffffffu, send, k);
-                    }
-                }
-                return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
-            };
-            const int hcol = h0 + (lane & (kHG - 1));
-            auto over_quadrants = [&]() -> float { return ms.red[0][hcol] + ms.red[1][hcol] + ms.red[2][hcol] + ms.red[3][hcol]; };
-            float nn = 0.f;
-            float z[kHG];
-            // (the barrier also says that a last slow path's readers of red are done)
-            if (bar_red_or(bar_id, 128, n0 != 0 || n0_draft != 0)) {
-#pragma unroll
-                for (int j = 0; j < kHG; ++j) z[j] = (float)(n0 + (n0_draft >> j & 1) + 2 * (n0_draft >> (16 + j) & 1));
-                const float nw = over_rows(z);
-                if (lane < kHG) ms.red[q][hcol] = nw;
-                named_sync(bar_id, 128);
-                nn = over_quadrants() * exp2f(kUp);
-                named_sync(bar_id, 128);
-            }
-#pragma unroll
-            for (int j = 0; j < kP; ++j) f2_unpack(z2[j], z[2 * j], z[2 * j + 1]);
-            const float zw = over_rows(z);
-            if (lane < kHG) ms.red[q][hcol] = zw;
-            wait(&ms.done[(it - 1) & 1], ((it - 1) >> 1) & 1);
-            tc_fence_after_sync();
-            named_sync(bar_id, 128);
+            // ---- output: sums over a column's 8 threads
+            const int c0 = seg.g * kCols, nc = min(kCols, top - c0);
             const bool whole = seg.first && seg.last;
-            const float zz = over_quadrants();
-            const int c0 = seg.g * kCols, nc = min(kCols, seg.q.n * a.H - c0);
             float *part = a.part + ((int64_t)blockIdx.x * 2 + (seg.first ? 1 : 0)) * tree_part_floats(kCols);
-            const float mm = ms.m_run[cur][hcol];
-            if (lane < kHG) {  // the same from all four warps
+            auto over_sets = [&](float v) -> float {
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                named_sync(1, kSoftmaxThreads);  // red's readers before this are done
+                if (half == 0) ms.red[set][n] = v;
+                named_sync(1, kSoftmaxThreads);
+                return ms.red[0][n] + ms.red[1][n] + ms.red[2][n] + ms.red[3][n];
+            };
+            const float nn = over_sets((float)n0) * exp2f(kUp);
+            const float zz = over_sets(z);
+            if (set == 0 && half == 0) {
                 // nothing but zero rows: the accumulators are 0 and stay so
-                const float all = nn == 0.f ? zz : zz + nn * exp2f(mm == -INFINITY ? 0.f : -mm);
-                ms.alpha[grp][lane] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
+                const float all = nn == 0.f ? zz : zz + nn * exp2f(m == -INFINITY ? 0.f : -m);
+                ms.alpha[n] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
+                if (!whole) {
+                    part[kCols * kKL + n] = m;
+                    part[kCols * (kKL + 1) + n] = zz;
+                    part[kCols * (kKL + 2) + n] = nn;
+                }
             }
-            if (!whole && q == 0 && lane < kHG) {
-                part[kCols * kKL + hcol] = mm;
-                part[kCols * (kKL + 1) + hcol] = zz;
-                part[kCols * (kKL + 2) + hcol] = nn;
-            }
-            __syncwarp();
+            wait(&ms.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+            tc_fence_after_sync();
+            named_sync(1, kSoftmaxThreads);
             if (ok) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    // thread: dim 128 c + r of 16 columns
-                    uint32_t o[kHG];
+                    // thread: dim 128 c + 32 q + lane of columns h0 .. h0 + 15
+                    uint32_t o[16];
                     tmem_ld_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o);
                     tmem_wait_ld();
-                    float v[kHG];
+                    const int d = 128 * c + 32 * q + lane;
+                    float v[16];
 #pragma unroll
-                    for (int j4 = 0; j4 < kV4; ++j4) {
-                        const float4 a4 = *reinterpret_cast<const float4 *>(&ms.alpha[grp][4 * j4]);
-                        v[4 * j4] = __uint_as_float(o[4 * j4]) * a4.x;
-                        v[4 * j4 + 1] = __uint_as_float(o[4 * j4 + 1]) * a4.y;
-                        v[4 * j4 + 2] = __uint_as_float(o[4 * j4 + 2]) * a4.z;
-                        v[4 * j4 + 3] = __uint_as_float(o[4 * j4 + 3]) * a4.w;
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 a4 = *reinterpret_cast<const float4 *>(&ms.alpha[h0 + 4 * k]);
+                        v[4 * k] = __uint_as_float(o[4 * k]) * a4.x;
+                        v[4 * k + 1] = __uint_as_float(o[4 * k + 1]) * a4.y;
+                        v[4 * k + 2] = __uint_as_float(o[4 * k + 2]) * a4.z;
+                        v[4 * k + 3] = __uint_as_float(o[4 * k + 3]) * a4.w;
                     }
                     if (!whole) {
 #pragma unroll
-                        for (int j = 0; j < kHG; ++j)
-                            if (h0 + j < nc) part[(h0 + j) * kKL + 128 * c + r] = v[j];
+                        for (int j = 0; j < 16; ++j)
+                            if (h0 + j < nc) part[(h0 + j) * kKL + d] = v[j];
                     } else if (a.out_bf16) {
                         // even lanes store column j, odd lanes column j + 1: two dims each
                         const bool odd = lane & 1;
 #pragma unroll
-                        for (int j = 0; j < kHG; j += 2) {
+                        for (int j = 0; j < 16; j += 2) {
                             const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
                             const __nv_bfloat162 pk = odd ? __floats2bfloat162_rn(other, v[j + 1]) : __floats2bfloat162_rn(v[j], other);
-                            const int col = h0 + j + (odd ? 1 : 0);
-                            if (col < nc)
+                            const int cj = h0 + j + (odd ? 1 : 0);
+                            if (cj < nc)
                                 *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                                    ((int64_t)seg.q.q0 * a.H + c0 + col) * kKL + 128 * c + (r & ~1)) = pk;
+                                                                    ((int64_t)seg.q.q0 * a.H + c0 + cj) * kKL + (d & ~1)) = pk;
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < kHG; ++j)
+                        for (int j = 0; j < 16; ++j)
                             if (h0 + j < nc)
-                                static_cast<float *>(a.out)[((int64_t)seg.q.q0 * a.H + c0 + h0 + j) * kKL + 128 * c + r] = v[j];
+                                static_cast<float *>(a.out)[((int64_t)seg.q.q0 * a.H + c0 + h0 + j) * kKL + d] = v[j];
                     }
                 }
             }
             tc_fence_before_sync();  // the accumulators' reads come before the next segment's first weights
         }
-        if (bad_page && a.err_word) atomicOr(a.err_word, (int)KV8_ERR_INDEX);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -797,7 +791,7 @@ cudaError_t launch_tree_tc(const TreeArgs &a, void *images, cudaStream_t st) {
     CUtensorMap m_lc, m_rc;
     const cuuint64_t dims[2] = {(cuuint64_t)kRow, (cuuint64_t)a.cache_rows};
     const cuuint64_t strides[1] = {(cuuint64_t)kRow};
-    const cuuint32_t rows = (cuuint32_t)(a.page_shift < 7 ? 1 << a.page_shift : kRows);
+    const cuuint32_t rows = (cuuint32_t)(a.page_shift < 6 ? 1 << a.page_shift : kRows);
     const cuuint32_t box_lc[2] = {128, rows}, box_rc[2] = {64, rows}, es[2] = {1, 1};
     void *base = const_cast<uint8_t *>(a.kv8);
     if (encode(&m_lc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box_lc, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
