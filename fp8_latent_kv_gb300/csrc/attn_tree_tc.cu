@@ -1,13 +1,13 @@
 // attn_tree_tc.cu -- attention of drafted tokens over a paged latent cache on the tensor cores (tcgen05, sm_103a),
 // for bf16 queries.
 //
-// All (token, head) columns of a sequence read the same rows, so a group of 64 columns against a tile of 64 rows is
+// All (token, head) columns of a sequence read the same rows, so a group of 64 columns against a tile of 128 rows is
 // two contractions:
-//   score    S[x][t]    = sum_k Qs[x][k] K8[t][k]      M = 128, N = 64 rows, K = 576 (e4m3 x e4m3)
+//   score    S[x][t]    = sum_k Qs[x][k] K8[t][k]      M = 128, N = 2 x 64 rows, K = 576 (e4m3 x e4m3)
 //            Qs: a bf16 query element, scaled by its column's power of two, is the sum of two e4m3 values; each
 //            TMEM lane quadrant holds 16 columns' hi pieces on lanes 0..15 and their lo pieces on lanes 16..31, so
 //            that one shuffle adds the halves of the dot product.
-//   context  O^T[d][n] += sum_t V8[t][d] W[n][t]       M = 128 dims (x4), N = 64 columns, K = 64 rows; V8 = the same
+//   context  O^T[d][n] += sum_t V8[t][d] W[n][t]       M = 128 dims (x4), N = 64 columns, K = 128 rows; V8 = the same
 //            bytes read MN-major, W the softmax weights as two pieces, hi in e4m3 and lo, what hi leaves, in e5m2:
 //            2^-7 of a weight at most, and terms down to 2^-22 of the column's largest still count (two e4m3 pieces
 //            would round everything below 2^-16 to nothing, which a long context's many small terms add up to).
@@ -19,12 +19,11 @@
 //
 // Work: equal shares of (group, tile) units (tree.cuh), one CTA per SM.
 // Warps: 0 = row loads, 1 = MMA issue and TMEM, 2 = the rows' scales, 3..18 = softmax and output; warp % 4 is a
-// warp's TMEM lane quadrant, its set (0..3) picks 16 of the tile's rows, and a thread holds 8 rows of one column.
+// warp's TMEM lane quadrant, its set (0..3) picks 32 of the tile's rows, and a thread holds 16 rows of one column.
 // The query pieces are the score's A operand in TMEM, so shared memory holds rows: five stages of 64 rows (36 KB),
-// two 8 KB weight buffers, the queries' RoPE part (8 KB).  Small tiles and many stages because a stage is held from
-// its load through score, softmax and context product, and that chain, not any one unit, set the pace with two
-// stages of 128 rows beside a 72 KB query image (7,500 cycles per 128 rows; see the figures at the kernel).
-// TMEM: query 128 columns, two score buffers of 64, context accumulators 4 x 64.
+// two 16 KB weight buffers, the queries' RoPE part (8 KB).  A stage is held from its load through score, softmax and
+// context product; with two stages of 128 rows beside a 72 KB query image that chain set the pace.
+// TMEM: query 128 columns, score 128, context accumulators 4 x 64.
 // Every wait is bounded in time; one that gives up sets KV8_ERR_TIMEOUT and the CTA winds down.
 #include "sm100.cuh"
 #include "tree.cuh"
@@ -38,7 +37,8 @@ namespace {
 using namespace sm100;
 
 constexpr int kCols = 64;
-constexpr int kRows = 64;
+constexpr int kRows = 128;                 // per tile: two stages
+constexpr int kHalf = 64;
 constexpr int kStages = 5;
 constexpr int kSoftmaxThreads = 512;
 constexpr int kThreads = 96 + kSoftmaxThreads;
@@ -48,7 +48,7 @@ constexpr uint32_t kStage = 4 * kBlk + kRope;
 constexpr uint32_t kQLat = 128 * 512;      // a group's query image: 128 lanes x 512 latent bytes, row-major,
 constexpr uint32_t kQRope = 128 * 64;      // then 128 x 64 RoPE bytes (SW64)
 constexpr uint32_t kImg = kQLat + kQRope;
-constexpr uint32_t kW = 8192;              // hi [64 columns][64 rows] (SW64), then lo
+constexpr uint32_t kW = 16384;             // hi [64 columns][128 rows] (SW128), then lo
 constexpr uint32_t OFF_ST = 0, OFF_W = kStages * kStage, OFF_Q = OFF_W + 2 * kW, OFF_MISC = OFF_Q + kQRope;
 constexpr float kTau = 2.0f;               // the reference moves when a term exceeds it by more than 2^kTau
 constexpr float kUp = 6.0f;                // weights are held times 2^kUp: at most 2^8 < 448
@@ -56,16 +56,16 @@ constexpr float kTiny = 7.888609e-31f;     // 2^-100
 constexpr uint32_t TM_Q = 0, TM_S = 128, TM_O = 256;
 
 struct RowInfo {
-    alignas(16) float scale[kRows];        // 0 for rows that are not there
-    alignas(16) float lg[kRows];           // log2(scale) + kUp
-    alignas(16) float inv[kRows];          // 1 / scale
+    alignas(16) float scale[kHalf];        // 0 for rows that are not there
+    alignas(16) float lg[kHalf];           // log2(scale) + kUp
+    alignas(16) float inv[kHalf];          // 1 / scale
     uint64_t in, zero;                     // rows that are there / whose scale is below 2^-100
 };
 struct Misc {
     RowInfo rows[kStages];
     alignas(16) float red[4][kCols];       // per-set maxima / sums
     alignas(16) float alpha[kCols];        // rescale factors; at the end 1 / z
-    uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_full[2], s_free[2], w_full[2], pv_done[2], q_ready,
+    uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_full, s_free, w_full[2], pv_done[2], q_ready,
         final_bar;
     uint32_t tmem_base;
     int abort_flag;
@@ -262,9 +262,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms.kv_free[s], 1);
             mbar_init(&ms.row_full[s], 32);
         }
+        mbar_init(&ms.s_full, 1);
+        mbar_init(&ms.s_free, kSoftmaxThreads);
         for (int k = 0; k < 2; ++k) {
-            mbar_init(&ms.s_full[k], 1);
-            mbar_init(&ms.s_free[k], kSoftmaxThreads);
             mbar_init(&ms.w_full[k], kSoftmaxThreads);
             mbar_init(&ms.pv_done[k], 1);
         }
@@ -295,22 +295,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Lane l fetches the tile's l-th piece (a page, or the tile where pages are larger); pieces past the
         // sequence's rows or outside the cache are not loaded.  A stage's barrier is armed after its release, which
         // implies that its previous phase is complete.
-        const int sub_rows = min(kRows, 1 << a.page_shift), subs = kRows / sub_rows;
-        int it = 0, s = 0;
-        uint32_t ph = 1;  // parity of the release that stage s waits for
+        const int sub_rows = min(kHalf, 1 << a.page_shift), subs = kHalf / sub_rows;
+        int is = 0, s = 0;  // stages filled, and the next one
+        uint32_t ph = 1;    // parity of the release that stage s waits for
         bool ok = true;
         while (ok && walk.next<kCols, kRows>(a, seg)) {
             const int64_t end = seg.q.len + seg.q.n;
-            auto piece = [&](int t) -> int64_t {
-                const int64_t pos = (int64_t)t * kRows + (int64_t)lane * sub_rows;
+            auto piece = [&](int h) -> int64_t {
+                const int64_t pos = (int64_t)h * kHalf + (int64_t)lane * sub_rows;
                 return lane < subs && pos < end ? tree_row(a, seg.b, pos) : -1;
             };
-            int64_t next = piece(seg.t0);
-            for (int t = seg.t0; t < seg.t1; ++t, ++it) {
+            int64_t next = piece(2 * seg.t0);
+            for (int h = 2 * seg.t0; h < 2 * seg.t1; ++h, ++is) {
                 const int64_t row = next;
-                next = t + 1 < seg.t1 ? piece(t + 1) : -1;  // a page entry's latency ahead
+                next = h + 1 < 2 * seg.t1 ? piece(h + 1) : -1;  // a page entry's latency ahead
                 const int pieces = __popc(__ballot_sync(0xffffffffu, row >= 0));
-                if (it >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], ph, &ms.abort_flag, a.err_word));
+                if (is >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], ph, &ms.abort_flag, a.err_word));
                 if (!ok) break;
                 uint8_t *st = smem + OFF_ST + s * kStage;
                 if (lane == 0) mbar_arrive_expect_tx(&ms.kv_full[s], (uint32_t)pieces * sub_rows * (uint32_t)kRow);
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every load in flight lands before the CTA ends
         if (lane == 0)
-            for (int i = max(0, it - kStages); i < it; ++i)
+            for (int i = max(0, is - kStages); i < is; ++i)
                 mbar_wait(&ms.kv_full[i % kStages], (i / kStages) & 1, nullptr, a.err_word, 200000000ull);
         __syncwarp();
     } else if (warp == 1) {
@@ -337,15 +337,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The whole warp runs the loop, its conditions voted on, and one elected lane issues: operands stay in uniform
         // registers.  (Issued from `if (lane == 0)` the same score MMAs took 46 cycles each instead of 32 alone, and
         // 85 beside the softmax warps.)
-        const uint32_t id_s = idesc_e4m3_f32(128, kRows, false, false);
+        const uint32_t id_s = idesc_e4m3_f32(128, kHalf, false, false);
         const uint32_t id_hi = idesc_e4m3_f32(128, kCols, true, false), id_lo = id_hi | (1u << 10);  // B in e5m2
         // descriptors of stage 0, weight buffer 0 and the query's RoPE part: an offset adds to the address field
         const uint64_t k_desc = smem_desc(sbase + OFF_ST, 0, 1024, kSw128);
         const uint64_t kr_desc = smem_desc(sbase + OFF_ST + 4 * kBlk, 0, 512, kSw64);
         const uint64_t qr_desc = smem_desc(sbase + OFF_Q, 0, 512, kSw64);
-        const uint64_t w_desc = smem_desc(sbase + OFF_W, 0, 512, kSw64);
+        const uint64_t w_desc = smem_desc(sbase + OFF_W, 0, 1024, kSw128);
         const int n_tiles = (int)(walk.end - walk.unit);
         int ns = 0, np = 0, sg = 0, ss = 0, ps = 0;  // tiles, segments and stages of the score / the product
+        int part = 0;                                // half of tile ns that is scored next
         uint32_t s_ph = 0;                           // parity of stage ss's load
         int seg_first = 0, seg_end = 0;              // the score side's segment
         uint32_t firsts = 0;                         // bit i % 32: tile i begins a segment
@@ -358,23 +359,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool did = false;
             if (np < ns && ready(&ms.w_full[np & 1], (np >> 1) & 1)) {
                 tc_fence_after_sync();
-                if (elect_one()) {
-                    const uint64_t v = k_desc + (uint64_t)(ps * (kStage >> 4));  // (the same bytes, MN-major)
-                    const uint64_t w = w_desc + (uint64_t)((np & 1) * (kW >> 4));
-                    const uint32_t keep = firsts >> (np & 31) & 1 ? 0u : 1u;
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch)
+                for (int h = 0; h < 2; ++h) {
+                    if (elect_one()) {
+                        const uint64_t v = k_desc + (uint64_t)(ps * (kStage >> 4));  // (the same bytes, MN-major)
+                        const uint64_t w = w_desc + (uint64_t)((np & 1) * (kW >> 4) + 4 * h);
+                        const uint32_t keep = h || !(firsts >> (np & 31) & 1) ? 1u : 0u;
 #pragma unroll
-                        for (int kk = 0; kk < 2; ++kk) {
-                            const uint64_t av = v + (uint64_t)((ch * kBlk + kk * 4096) >> 4);
-                            mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kk * 32) >> 4), id_hi, kk ? 1u : keep);
-                            mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kW / 2 + kk * 32) >> 4), id_lo, 1u);
-                        }
-                    mma_commit(&ms.kv_free[ps]);
-                    mma_commit(&ms.pv_done[np & 1]);
+                        for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk) {
+                                const uint64_t av = v + (uint64_t)((ch * kBlk + kk * 4096) >> 4);
+                                mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kk * 32) >> 4), id_hi, kk ? 1u : keep);
+                                mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kW / 2 + kk * 32) >> 4), id_lo, 1u);
+                            }
+                        mma_commit(&ms.kv_free[ps]);
+                        if (h) mma_commit(&ms.pv_done[np & 1]);
+                    }
+                    __syncwarp();
+                    if (++ps == kStages) ps = 0;
                 }
-                __syncwarp();
-                if (++ps == kStages) ps = 0;
                 ++np;
                 did = true;
             } else if (ns < n_tiles) {
@@ -384,12 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     seg_end = ns + (seg.t1 - seg.t0);
                     ++sg;
                 }
-                if (ready(&ms.kv_full[ss], s_ph) && (ns < 2 || ready(&ms.s_free[ns & 1], ((ns >> 1) - 1) & 1)) &&
+                if (ready(&ms.kv_full[ss], s_ph) && (part || ns == 0 || ready(&ms.s_free, (ns - 1) & 1)) &&
                     (ns > seg_first || ready(&ms.q_ready, (sg - 1) & 1))) {
                     tc_fence_after_sync();
                     firsts = ns == seg_first ? firsts | 1u << (ns & 31) : firsts & ~(1u << (ns & 31));
                     if (elect_one()) {
-                        const uint32_t d = tmem + TM_S + 64u * (ns & 1);
+                        const uint32_t d = tmem + TM_S + 64u * part;
                         const uint64_t k = k_desc + (uint64_t)(ss * (kStage >> 4)), kr = kr_desc + (uint64_t)(ss * (kStage >> 4));
 #pragma unroll
                         for (int kb = 0; kb < 4; ++kb)
@@ -400,10 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < 2; ++kk)
                             mma_f8f6f4(d, qr_desc + (uint64_t)(kk * 2), kr + (uint64_t)(kk * 2), id_s, 1u);
-                        mma_commit(&ms.s_full[ns & 1]);
+                        if (part) mma_commit(&ms.s_full);
                     }
                     __syncwarp();
-                    ++ns;
+                    ns += part;
+                    part ^= 1;
                     if (++ss == kStages) {
                         ss = 0;
                         s_ph ^= 1;
@@ -433,21 +438,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 2) {
         // ================================ the rows' scales ================================
-        // Four tiles at a time, eight rows per lane: their page entries, then their scales, one latency each; the
+        // Four stages at a time, eight rows per lane: their page entries, then their scales, one latency each; the
         // stages' five sets of row figures keep this ahead of the softmax.
         constexpr int kBatch = 4;
-        int it = 0;
+        int is = 0;
         bool ok = true, bad_page = false;
         while (ok && walk.next<kCols, kRows>(a, seg)) {
             const int64_t end = seg.q.len + seg.q.n;
-            for (int t = seg.t0; ok && t < seg.t1; t += kBatch) {
+            for (int h = 2 * seg.t0; ok && h < 2 * seg.t1; h += kBatch) {
                 int64_t row[2 * kBatch];
                 float sc[2 * kBatch];
 #pragma unroll
                 for (int u = 0; u < 2 * kBatch; ++u) {
-                    const int64_t pos = (int64_t)t * kRows + 32 * u + lane;
+                    const int64_t pos = (int64_t)h * kHalf + 32 * u + lane;
                     row[u] = -1;
-                    if (t + u / 2 < seg.t1 && pos < end) {
+                    if (h + u / 2 < 2 * seg.t1 && pos < end) {
                         row[u] = tree_row(a, seg.b, pos);
                         bad_page |= row[u] < 0;
                     }
@@ -456,31 +461,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < 2 * kBatch; ++u) sc[u] = row[u] >= 0 ? __ldg(a.kv_scale + row[u]) : 0.f;
 #pragma unroll
                 for (int v = 0; v < kBatch; ++v) {
-                    if (t + v >= seg.t1) break;
-                    const int s = it % kStages;
-                    if (it >= kStages)
-                        ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], (it / kStages - 1) & 1, &ms.abort_flag, a.err_word));
+                    if (h + v >= 2 * seg.t1) break;
+                    const int s = is % kStages;
+                    if (is >= kStages)
+                        ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], (is / kStages - 1) & 1, &ms.abort_flag, a.err_word));
                     if (!ok) break;
                     RowInfo &ri = ms.rows[s];
                     uint32_t in[2], zero[2];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float c = sc[2 * v + h];
-                        const bool there = row[2 * v + h] >= 0;
-                        in[h] = __ballot_sync(0xffffffffu, there);
-                        zero[h] = __ballot_sync(0xffffffffu, there && c < kTiny);
-                        ri.scale[32 * h + lane] = c;
-                        ri.lg[32 * h + lane] = lg2_approx(c) + kUp;
+                    for (int k = 0; k < 2; ++k) {
+                        const float c = sc[2 * v + k];
+                        const bool there = row[2 * v + k] >= 0;
+                        in[k] = __ballot_sync(0xffffffffu, there);
+                        zero[k] = __ballot_sync(0xffffffffu, there && c < kTiny);
+                        ri.scale[32 * k + lane] = c;
+                        ri.lg[32 * k + lane] = lg2_approx(c) + kUp;
                         // 0 for a zero row (its weight is 0) and for a scale that is not finite (its weight is NaN
                         // where it is attended)
-                        ri.inv[32 * h + lane] = c >= kTiny && c <= 3.402823466e38f ? __fdividef(1.f, c) : 0.f;
+                        ri.inv[32 * k + lane] = c >= kTiny && c <= 3.402823466e38f ? __fdividef(1.f, c) : 0.f;
                     }
                     if (lane == 0) {
                         ri.in = in[0] | (uint64_t)in[1] << 32;
                         ri.zero = zero[0] | (uint64_t)zero[1] << 32;
                     }
                     mbar_arrive(&ms.row_full[s]);
-                    ++it;
+                    ++is;
                 }
             }
         }
@@ -490,10 +495,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A wait that gives up clears `ok` (the same in a warp's lanes: TMEM accesses need all of them); the warp
         // then skips its remaining waits but still reaches every named barrier, so that no other warp waits for it.
         const int st = tid - 96;                        // 0..511
-        const int q = warp & 3, set = (warp - 3) >> 2;  // TMEM lane quadrant; rows 16 set .. 16 set + 15
-        const int half = lane >> 4;                     // this thread's 8 of them
+        const int q = warp & 3, set = (warp - 3) >> 2;  // TMEM lane quadrant; rows 32 set .. 32 set + 31 of the tile
+        const int half = lane >> 4;                     // this thread's 16 of them
         const int n = 16 * q + (lane & 15);             // its column
-        const int r0 = 16 * set + 8 * half;             // its first row
+        const int stage_of = set >> 1;                  // the stage of the tile that they are in,
+        const int r0 = 32 * (set & 1) + 16 * half;      // and its first row there
         const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
         const int h0 = 16 * set;                        // rescale and output: columns h0..h0+15, dims 128 c + 32 q + lane
         bool ok = true;
@@ -501,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &ms.abort_flag, a.err_word));
         };
         grid_launch_dependents();
-        int it = 0, s = 0;
+        int it = 0, s = stage_of;  // tiles, and the stage of this thread's rows
         uint32_t s_ph = 0;
         while (walk.next<kCols, kRows>(a, seg)) {
             const int64_t slot = tree_slot(seg.q.q0, a.H, seg.b) + seg.g;
@@ -534,83 +540,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, z = 0.f;
             int n0 = 0;  // zero rows that the column attends among this thread's rows
             for (int t = seg.t0; t < seg.t1; ++t, ++it) {
-                const int64_t p0 = (int64_t)t * kRows;
+                const int64_t p0 = (int64_t)t * kRows + stage_of * kHalf;  // position of the stage's first row
                 const int buf = it & 1;
-                // ---- the rows' figures, and which of the thread's 8 rows the column attends
+                // ---- scores: 32 rows of this thread's piece; a shuffle adds the other piece's half of 16 of them
+                wait(&ms.s_full, it & 1);
+                tc_fence_after_sync();
+                uint32_t v[32];
+                tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 32u * set, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+                tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 32u * set + 16u, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+                // meanwhile the rows' figures, and which of the thread's rows the column attends
                 wait(&ms.row_full[s], s_ph);
                 const RowInfo &ri = ms.rows[s];
                 const uint64_t in = ri.in;
-                uint32_t on = (uint32_t)(in >> r0) & 0xFFu;
+                uint32_t on = (uint32_t)(in >> r0) & 0xFFFFu;
                 const int64_t draft = p0 + r0 - seg.q.len;  // the first row's index in the draft
-                const bool drafted = p0 + kRows > seg.q.len;
+                const bool drafted = p0 + kHalf > seg.q.len;
                 if (drafted) {
-                    // bits draft .. draft + 7 of the token's mask row; a row of the context counts as set
+                    // bits draft .. draft + 15 of the token's mask row; a row of the context counts as set
                     uint32_t bits = 0;
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
+#pragma unroll 1
+                    for (int u = 0; u < 16; ++u)
                         if (draft + u < 0 || ((on >> u & 1) && tree_sees(a, seg.q.q0, node, (int)(draft + u)))) bits |= 1u << u;
                     on &= bits;
                 }
                 const uint32_t zr = (uint32_t)(ri.zero >> r0) & on;
                 n0 += __popc(zr);
                 on ^= zr;
-                float4 f4[2];
-                uint64_t cs[4], lg[4], inv[4];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    f4[0] = *reinterpret_cast<const float4 *>(&ri.scale[r0 + 4 * k]);
-                    const uint64_t c2 = f2_pack(c_q, c_q);
-                    cs[2 * k] = f2_mul(f2_pack(f4[0].x, f4[0].y), c2);
-                    cs[2 * k + 1] = f2_mul(f2_pack(f4[0].z, f4[0].w), c2);
-                    f4[0] = *reinterpret_cast<const float4 *>(&ri.lg[r0 + 4 * k]);
-                    lg[2 * k] = f2_pack(f4[0].x, f4[0].y);
-                    lg[2 * k + 1] = f2_pack(f4[0].z, f4[0].w);
-                    f4[0] = *reinterpret_cast<const float4 *>(&ri.inv[r0 + 4 * k]);
-                    inv[2 * k] = f2_pack(f4[0].x, f4[0].y);
-                    inv[2 * k + 1] = f2_pack(f4[0].z, f4[0].w);
-                }
-                // ---- scores: 16 rows of this thread's piece; a shuffle adds the other piece's half of 8 of them
-                wait(&ms.s_full[buf], (it >> 1) & 1);
-                tc_fence_after_sync();
-                uint64_t d2[4];
+                const float ref_o = m == -INFINITY ? 0.f : m;  // m counts as 0 while it is -inf
+                tmem_wait_ld();
+                tc_fence_before_sync();
+                mbar_arrive(&ms.s_free);
+                // ---- d = e + 6 - m
+                float d[16], dmax = -INFINITY;
                 {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 64u * buf + (uint32_t)h0, v);
-                    tmem_wait_ld();
-                    tc_fence_before_sync();
-                    mbar_arrive(&ms.s_free[buf]);
-                    float sv[8];
+                    const uint64_t c2 = f2_pack(c_q, c_q), mr = f2_pack(-ref_o, -ref_o);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float send = __uint_as_float(half ? v[j] : v[8 + j]), keep = __uint_as_float(half ? v[8 + j] : v[j]);
-                        sv[j] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+                    for (int j = 0; j < 16; ++j) {
+                        const float send = __uint_as_float(half ? v[j] : v[16 + j]), keep = __uint_as_float(half ? v[16 + j] : v[j]);
+                        d[j] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) d2[j] = f2_pack(sv[2 * j], sv[2 * j + 1]);
-                }
-                // ---- d = e + 6 - m (m counts as 0 while it is -inf)
-                const float ref_o = m == -INFINITY ? 0.f : m;
-                float dmax = -INFINITY;
-                {
-                    const uint64_t mr = f2_pack(-ref_o, -ref_o);
-                    float d[8];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        d2[j] = f2_fma(d2[j], cs[j], f2_add(lg[j], mr));
-                        f2_unpack(d2[j], d[2 * j], d[2 * j + 1]);
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 sc = *reinterpret_cast<const float4 *>(&ri.scale[r0 + 4 * k]);
+                        const float4 lg = *reinterpret_cast<const float4 *>(&ri.lg[r0 + 4 * k]);
+                        f2_unpack(f2_fma(f2_pack(d[4 * k], d[4 * k + 1]), f2_mul(f2_pack(sc.x, sc.y), c2), f2_add(f2_pack(lg.x, lg.y), mr)),
+                                  d[4 * k], d[4 * k + 1]);
+                        f2_unpack(f2_fma(f2_pack(d[4 * k + 2], d[4 * k + 3]), f2_mul(f2_pack(sc.z, sc.w), c2),
+                                         f2_add(f2_pack(lg.z, lg.w), mr)),
+                                  d[4 * k + 2], d[4 * k + 3]);
                     }
-                    if (on != 0xFFu) {
+                    if (on != 0xFFFFu) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) d[j] = on >> j & 1 ? d[j] : -INFINITY;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) d2[j] = f2_pack(d[2 * j], d[2 * j + 1]);
+                        for (int j = 0; j < 16; ++j) d[j] = on >> j & 1 ? d[j] : -INFINITY;
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) dmax = fmaxf(dmax, d[j]);
+                    for (int j = 0; j < 16; ++j) dmax = fmaxf(dmax, d[j]);
                 }
                 // all columns move their references together: when a term exceeds one by more than kTau, or a column
                 // that has none meets its first row
                 const bool slow = bar_red_or(1, kSoftmaxThreads, dmax > kTau + kUp || (m == -INFINITY && dmax > -INFINITY));
+                bool rescale = false;
                 if (slow) {
                     const float hm = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 16));
                     if (half == 0) ms.red[set][n] = hm;
@@ -622,85 +611,86 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float dl = mn == -INFINITY ? 0.f : ref_o - mn;
                     m = mn;
                     z *= al;
-                    const uint64_t dl2 = f2_pack(dl, dl);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) d2[j] = f2_add(d2[j], dl2);
-                    if (bar_red_or(1, kSoftmaxThreads, al != 1.f) && t > seg.t0) {
-                        // rescale this warp's part of the accumulators once the context product before is complete
-                        wait(&ms.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
-                        tc_fence_after_sync();
-                        float f[16];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float4 a4 = *reinterpret_cast<const float4 *>(&ms.alpha[h0 + 4 * k]);
-                            f[4 * k] = a4.x;
-                            f[4 * k + 1] = a4.y;
-                            f[4 * k + 2] = a4.z;
-                            f[4 * k + 3] = a4.w;
-                        }
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t o[16];
-                            tmem_ld_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f[j]);
-                            tmem_st_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o);
-                        }
-                        tmem_wait_st();
-                    }
+                    for (int j = 0; j < 16; ++j) d[j] += dl;
+                    rescale = bar_red_or(1, kSoftmaxThreads, al != 1.f) && t > seg.t0;
                 }
                 // ---- weights
-                uint32_t whi[2], wlo[2];
+                uint32_t whi[4], wlo[4];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float d0, d1, d3, d4;
-                    f2_unpack(d2[2 * k], d0, d1);
-                    f2_unpack(d2[2 * k + 1], d3, d4);
-                    const float w0 = ex2_approx(d0), w1 = ex2_approx(d1), w3 = ex2_approx(d3), w4 = ex2_approx(d4);
-                    float u0, u1, u3, u4;
-                    f2_unpack(f2_mul(f2_pack(w0, w1), inv[2 * k]), u0, u1);
-                    f2_unpack(f2_mul(f2_pack(w3, w4), inv[2 * k + 1]), u3, u4);
-                    z += (u0 + u1) + (u3 + u4);
+                for (int k = 0; k < 4; ++k) {
+                    const float4 inv = *reinterpret_cast<const float4 *>(&ri.inv[r0 + 4 * k]);
+                    const float w0 = ex2_approx(d[4 * k]), w1 = ex2_approx(d[4 * k + 1]), w2 = ex2_approx(d[4 * k + 2]),
+                                w3 = ex2_approx(d[4 * k + 3]);
+                    z = fmaf(w0, inv.x, z);
+                    z = fmaf(w1, inv.y, z);
+                    z = fmaf(w2, inv.z, z);
+                    z = fmaf(w3, inv.w, z);
                     uint32_t h01, l01, h23, l23;
                     split_weights(w0, w1, h01, l01);
-                    split_weights(w3, w4, h23, l23);
+                    split_weights(w2, w3, h23, l23);
                     whi[k] = h01 | (h23 << 16);
                     wlo[k] = l01 | (l23 << 16);
                 }
                 // ---- rows that were not loaded, and NaN codes of drafted rows (attended columns have NaN weights
-                // already): a weight of 0 must not meet them.  Two threads own a row's 128 bytes of a latent block.
+                // already): a weight of 0 must not meet them.  A thread owns a row's 128 bytes of a latent block.
                 if (drafted || in != ~(uint64_t)0) {
-                    const int r = (st >> 1) & 63;
+                    const int r = st & 63;
                     const bool there = in >> r & 1;
                     if (!there || p0 + r >= seg.q.len) {
                         // (complete since before the score: this makes the copy's bytes visible here too)
                         (void)mbar_wait(&ms.kv_full[s], s_ph, &ms.abort_flag, a.err_word);
-                        uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s * kStage + (st >> 7) * kBlk + r * 128 + (st & 1) * 64);
+                        uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s * kStage + ((st >> 6) & 3) * kBlk + r * 128);
 #pragma unroll 1
-                        for (int k = 0; k < 4; ++k) {
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        for (int k = 0; k < 8; ++k) {
+                            uint4 u = make_uint4(0u, 0u, 0u, 0u);
                             if (there) {
-                                v = p[k];
-                                v.x = without_nan(v.x);
-                                v.y = without_nan(v.y);
-                                v.z = without_nan(v.z);
-                                v.w = without_nan(v.w);
+                                u = p[k];
+                                u.x = without_nan(u.x);
+                                u.y = without_nan(u.y);
+                                u.z = without_nan(u.z);
+                                u.w = without_nan(u.w);
                             }
-                            p[k] = v;
+                            p[k] = u;
                         }
                     }
                 }
                 // the context product two tiles back has read this weight buffer
                 if (it >= 2) wait(&ms.pv_done[buf], ((it >> 1) - 1) & 1);
-                uint8_t *wb = smem + OFF_W + buf * kW + sw64_offset(n, r0);
-                *reinterpret_cast<uint2 *>(wb) = make_uint2(whi[0], whi[1]);
-                *reinterpret_cast<uint2 *>(wb + kW / 2) = make_uint2(wlo[0], wlo[1]);
+                uint8_t *wb = smem + OFF_W + buf * kW + sw128_offset(n, 32 * set + 16 * half);
+                *reinterpret_cast<uint4 *>(wb) = make_uint4(whi[0], whi[1], whi[2], whi[3]);
+                *reinterpret_cast<uint4 *>(wb + kW / 2) = make_uint4(wlo[0], wlo[1], wlo[2], wlo[3]);
+                if (rescale) {
+                    // this warp's part of the accumulators, once the context product before is complete, where one of
+                    // its columns moved
+                    wait(&ms.pv_done[buf ^ 1], ((it - 1) >> 1) & 1);
+                    tc_fence_after_sync();
+                    const float mine = ms.alpha[h0 + (lane & 15)];
+                    if (__any_sync(0xffffffffu, mine != 1.f)) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; c += 2) {
+                            uint32_t o[2][16];
+                            tmem_ld_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o[0]);
+                            tmem_ld_32x32b_x16(tmem + lane_addr + TM_O + 64u * (c + 1) + (uint32_t)h0, o[1]);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float f = __shfl_sync(0xffffffffu, mine, j);
+                                o[0][j] = __float_as_uint(__uint_as_float(o[0][j]) * f);
+                                o[1][j] = __float_as_uint(__uint_as_float(o[1][j]) * f);
+                            }
+                            tmem_st_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o[0]);
+                            tmem_st_32x32b_x16(tmem + lane_addr + TM_O + 64u * (c + 1) + (uint32_t)h0, o[1]);
+                        }
+                        tmem_wait_st();
+                    }
+                }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 mbar_arrive(&ms.w_full[buf]);
-                if (++s == kStages) {
-                    s = 0;
+                s += 2;
+                if (s >= kStages) {
+                    s -= kStages;
                     s_ph ^= 1;
                 }
             }
@@ -791,7 +781,7 @@ cudaError_t launch_tree_tc(const TreeArgs &a, void *images, cudaStream_t st) {
     CUtensorMap m_lc, m_rc;
     const cuuint64_t dims[2] = {(cuuint64_t)kRow, (cuuint64_t)a.cache_rows};
     const cuuint64_t strides[1] = {(cuuint64_t)kRow};
-    const cuuint32_t rows = (cuuint32_t)(a.page_shift < 6 ? 1 << a.page_shift : kRows);
+    const cuuint32_t rows = (cuuint32_t)(a.page_shift < 6 ? 1 << a.page_shift : kHalf);
     const cuuint32_t box_lc[2] = {128, rows}, box_rc[2] = {64, rows}, es[2] = {1, 1};
     void *base = const_cast<uint8_t *>(a.kv8);
     if (encode(&m_lc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box_lc, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
