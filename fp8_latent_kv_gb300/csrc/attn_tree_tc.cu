@@ -37,18 +37,17 @@ namespace {
 using namespace sm100;
 
 constexpr int kCols = 64;
-constexpr int kRows = 128;                 // per tile: two stages
-constexpr int kHalf = 64;
+constexpr int kRows = 64;
 constexpr int kStages = 5;
-constexpr int kSoftmaxThreads = 512;
-constexpr int kThreads = 96 + kSoftmaxThreads;
+constexpr int kTeam = 256;                 // threads of a softmax team
+constexpr int kThreads = 96 + 2 * kTeam;
 constexpr uint32_t kBlk = 8192;            // 64 rows x 128 latent bytes (SW128)
 constexpr uint32_t kRope = 4096;           // 64 rows x 64 RoPE bytes (SW64)
 constexpr uint32_t kStage = 4 * kBlk + kRope;
 constexpr uint32_t kQLat = 128 * 512;      // a group's query image: 128 lanes x 512 latent bytes, row-major,
 constexpr uint32_t kQRope = 128 * 64;      // then 128 x 64 RoPE bytes (SW64)
 constexpr uint32_t kImg = kQLat + kQRope;
-constexpr uint32_t kW = 16384;             // hi [64 columns][128 rows] (SW128), then lo
+constexpr uint32_t kW = 8192;              // hi [64 columns][64 rows] (SW64), then lo
 constexpr uint32_t OFF_ST = 0, OFF_W = kStages * kStage, OFF_Q = OFF_W + 2 * kW, OFF_MISC = OFF_Q + kQRope;
 constexpr float kTau = 2.0f;               // the reference moves when a term exceeds it by more than 2^kTau
 constexpr float kUp = 6.0f;                // weights are held times 2^kUp: at most 2^8 < 448
@@ -56,16 +55,17 @@ constexpr float kTiny = 7.888609e-31f;     // 2^-100
 constexpr uint32_t TM_Q = 0, TM_S = 128, TM_O = 256;
 
 struct RowInfo {
-    alignas(16) float scale[kHalf];        // 0 for rows that are not there
-    alignas(16) float lg[kHalf];           // log2(scale) + kUp
-    alignas(16) float inv[kHalf];          // 1 / scale
+    alignas(16) float scale[kRows];        // 0 for rows that are not there
+    alignas(16) float lg[kRows];           // log2(scale) + kUp
+    alignas(16) float inv[kRows];          // 1 / scale
     uint64_t in, zero;                     // rows that are there / whose scale is below 2^-100
 };
 struct Misc {
     RowInfo rows[kStages];
-    alignas(16) float red[4][kCols];       // per-set maxima / sums
-    alignas(16) float alpha[kCols];        // rescale factors; at the end 1 / z
-    uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_full, s_free, w_full[2], pv_done[2], q_ready,
+    alignas(16) float m[kCols];            // running references (log2 units), -inf before any attended row
+    alignas(16) float red[4][kCols];       // maxima of a team's two sets of rows, team by team; at the end sums
+    alignas(16) float alpha[2][kCols];     // each team's rescale factors; at the end alpha[0] = 1 / z
+    uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_full[2], s_free[2], w_full[2], pv_done[2], q_ready,
         final_bar;
     uint32_t tmem_base;
     int abort_flag;
@@ -85,6 +85,12 @@ __host__ __device__ __forceinline__ int64_t tree_slot(int64_t q0, int H, int b) 
 
 // Lane of column n's piece (0 = hi, 1 = lo).
 __device__ __forceinline__ int query_lane(int n, int piece) { return (n >> 4) * 32 + piece * 16 + (n & 15); }
+
+// Arrive at a named barrier that other threads wait at; what this thread wrote before is theirs to read after it.
+__device__ __forceinline__ void named_arrive(int id, int count) {
+    __threadfence_block();
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
 
 // Score MMA with A in tensor memory.
 __device__ __forceinline__ void mma_f8f6f4_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -262,13 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms.kv_free[s], 1);
             mbar_init(&ms.row_full[s], 32);
         }
-        mbar_init(&ms.s_full, 1);
-        mbar_init(&ms.s_free, kSoftmaxThreads);
         for (int k = 0; k < 2; ++k) {
-            mbar_init(&ms.w_full[k], kSoftmaxThreads);
+            mbar_init(&ms.s_full[k], 1);
+            mbar_init(&ms.s_free[k], kTeam);
+            mbar_init(&ms.w_full[k], kTeam);
             mbar_init(&ms.pv_done[k], 1);
         }
-        mbar_init(&ms.q_ready, kSoftmaxThreads);
+        mbar_init(&ms.q_ready, 2 * kTeam);
         mbar_init(&ms.final_bar, 1);
         ms.abort_flag = 0;
         fence_barrier_init();
@@ -295,30 +301,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Lane l fetches the tile's l-th piece (a page, or the tile where pages are larger); pieces past the
         // sequence's rows or outside the cache are not loaded.  A stage's barrier is armed after its release, which
         // implies that its previous phase is complete.
-        const int sub_rows = min(kHalf, 1 << a.page_shift), subs = kHalf / sub_rows;
-        int is = 0, s = 0;  // stages filled, and the next one
-        uint32_t ph = 1;    // parity of the release that stage s waits for
+        const int sub_rows = min(kRows, 1 << a.page_shift), subs = kRows / sub_rows;
+        int it = 0, s = 0;
+        uint32_t ph = 1;  // parity of the release that stage s waits for
         bool ok = true;
         while (ok && walk.next<kCols, kRows>(a, seg)) {
             const int64_t end = seg.q.len + seg.q.n;
-            auto piece = [&](int h) -> int64_t {
-                const int64_t pos = (int64_t)h * kHalf + (int64_t)lane * sub_rows;
+            auto piece = [&](int t) -> int64_t {
+                const int64_t pos = (int64_t)t * kRows + (int64_t)lane * sub_rows;
                 return lane < subs && pos < end ? tree_row(a, seg.b, pos) : -1;
             };
-            int64_t next = piece(2 * seg.t0);
-            for (int h = 2 * seg.t0; h < 2 * seg.t1; ++h, ++is) {
+            int64_t next = piece(seg.t0);
+            for (int t = seg.t0; t < seg.t1; ++t, ++it) {
                 const int64_t row = next;
-                next = h + 1 < 2 * seg.t1 ? piece(h + 1) : -1;  // a page entry's latency ahead
+                next = t + 1 < seg.t1 ? piece(t + 1) : -1;  // a page entry's latency ahead
                 const int pieces = __popc(__ballot_sync(0xffffffffu, row >= 0));
-                if (is >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], ph, &ms.abort_flag, a.err_word));
+                if (it >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], ph, &ms.abort_flag, a.err_word));
                 if (!ok) break;
                 uint8_t *st = smem + OFF_ST + s * kStage;
                 if (lane == 0) mbar_arrive_expect_tx(&ms.kv_full[s], (uint32_t)pieces * sub_rows * (uint32_t)kRow);
                 __syncwarp();
                 if (row >= 0) {
+                    if (subs == 1) {  // one copy for the four latent blocks
+                        tma_load_3d(st, &map_lc, 0, (int)row, 0, &ms.kv_full[s]);
+                    } else {
 #pragma unroll
-                    for (int kb = 0; kb < 4; ++kb)
-                        tma_load_2d(st + kb * kBlk + lane * sub_rows * 128, &map_lc, kb * 128, (int)row, &ms.kv_full[s]);
+                        for (int kb = 0; kb < 4; ++kb)
+                            tma_load_3d(st + kb * kBlk + lane * sub_rows * 128, &map_lc, 0, (int)row, kb, &ms.kv_full[s]);
+                    }
                     tma_load_2d(st + 4 * kBlk + lane * sub_rows * 64, &map_rc, 512, (int)row, &ms.kv_full[s]);
                 }
                 if (++s == kStages) {
@@ -329,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every load in flight lands before the CTA ends
         if (lane == 0)
-            for (int i = max(0, is - kStages); i < is; ++i)
+            for (int i = max(0, it - kStages); i < it; ++i)
                 mbar_wait(&ms.kv_full[i % kStages], (i / kStages) & 1, nullptr, a.err_word, 200000000ull);
         __syncwarp();
     } else if (warp == 1) {
@@ -337,16 +347,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The whole warp runs the loop, its conditions voted on, and one elected lane issues: operands stay in uniform
         // registers.  (Issued from `if (lane == 0)` the same score MMAs took 46 cycles each instead of 32 alone, and
         // 85 beside the softmax warps.)
-        const uint32_t id_s = idesc_e4m3_f32(128, kHalf, false, false);
+        const uint32_t id_s = idesc_e4m3_f32(128, kRows, false, false);
         const uint32_t id_hi = idesc_e4m3_f32(128, kCols, true, false), id_lo = id_hi | (1u << 10);  // B in e5m2
         // descriptors of stage 0, weight buffer 0 and the query's RoPE part: an offset adds to the address field
         const uint64_t k_desc = smem_desc(sbase + OFF_ST, 0, 1024, kSw128);
         const uint64_t kr_desc = smem_desc(sbase + OFF_ST + 4 * kBlk, 0, 512, kSw64);
         const uint64_t qr_desc = smem_desc(sbase + OFF_Q, 0, 512, kSw64);
-        const uint64_t w_desc = smem_desc(sbase + OFF_W, 0, 1024, kSw128);
+        const uint64_t w_desc = smem_desc(sbase + OFF_W, 0, 512, kSw64);
         const int n_tiles = (int)(walk.end - walk.unit);
         int ns = 0, np = 0, sg = 0, ss = 0, ps = 0;  // tiles, segments and stages of the score / the product
-        int part = 0;                                // half of tile ns that is scored next
         uint32_t s_ph = 0;                           // parity of stage ss's load
         int seg_first = 0, seg_end = 0;              // the score side's segment
         uint32_t firsts = 0;                         // bit i % 32: tile i begins a segment
@@ -359,26 +368,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool did = false;
             if (np < ns && ready(&ms.w_full[np & 1], (np >> 1) & 1)) {
                 tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t v = k_desc + (uint64_t)(ps * (kStage >> 4));  // (the same bytes, MN-major)
+                    const uint64_t w = w_desc + (uint64_t)((np & 1) * (kW >> 4));
+                    const uint32_t keep = firsts >> (np & 31) & 1 ? 0u : 1u;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (elect_one()) {
-                        const uint64_t v = k_desc + (uint64_t)(ps * (kStage >> 4));  // (the same bytes, MN-major)
-                        const uint64_t w = w_desc + (uint64_t)((np & 1) * (kW >> 4) + 4 * h);
-                        const uint32_t keep = h || !(firsts >> (np & 31) & 1) ? 1u : 0u;
+                    for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                            for (int kk = 0; kk < 2; ++kk) {
-                                const uint64_t av = v + (uint64_t)((ch * kBlk + kk * 4096) >> 4);
-                                mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kk * 32) >> 4), id_hi, kk ? 1u : keep);
-                                mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kW / 2 + kk * 32) >> 4), id_lo, 1u);
-                            }
-                        mma_commit(&ms.kv_free[ps]);
-                        if (h) mma_commit(&ms.pv_done[np & 1]);
-                    }
-                    __syncwarp();
-                    if (++ps == kStages) ps = 0;
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const uint64_t av = v + (uint64_t)((ch * kBlk + kk * 4096) >> 4);
+                            mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kk * 32) >> 4), id_hi, kk ? 1u : keep);
+                            mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kW / 2 + kk * 32) >> 4), id_lo, 1u);
+                        }
+                    mma_commit(&ms.kv_free[ps]);
+                    mma_commit(&ms.pv_done[np & 1]);
                 }
+                __syncwarp();
+                if (++ps == kStages) ps = 0;
                 ++np;
                 did = true;
             } else if (ns < n_tiles) {
@@ -388,12 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     seg_end = ns + (seg.t1 - seg.t0);
                     ++sg;
                 }
-                if (ready(&ms.kv_full[ss], s_ph) && (part || ns == 0 || ready(&ms.s_free, (ns - 1) & 1)) &&
+                if (ready(&ms.kv_full[ss], s_ph) && (ns < 2 || ready(&ms.s_free[ns & 1], ((ns >> 1) - 1) & 1)) &&
                     (ns > seg_first || ready(&ms.q_ready, (sg - 1) & 1))) {
                     tc_fence_after_sync();
                     firsts = ns == seg_first ? firsts | 1u << (ns & 31) : firsts & ~(1u << (ns & 31));
                     if (elect_one()) {
-                        const uint32_t d = tmem + TM_S + 64u * part;
+                        const uint32_t d = tmem + TM_S + 64u * (ns & 1);
                         const uint64_t k = k_desc + (uint64_t)(ss * (kStage >> 4)), kr = kr_desc + (uint64_t)(ss * (kStage >> 4));
 #pragma unroll
                         for (int kb = 0; kb < 4; ++kb)
@@ -404,11 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < 2; ++kk)
                             mma_f8f6f4(d, qr_desc + (uint64_t)(kk * 2), kr + (uint64_t)(kk * 2), id_s, 1u);
-                        if (part) mma_commit(&ms.s_full);
+                        mma_commit(&ms.s_full[ns & 1]);
                     }
                     __syncwarp();
-                    ns += part;
-                    part ^= 1;
+                    ++ns;
                     if (++ss == kStages) {
                         ss = 0;
                         s_ph ^= 1;
@@ -445,14 +450,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true, bad_page = false;
         while (ok && walk.next<kCols, kRows>(a, seg)) {
             const int64_t end = seg.q.len + seg.q.n;
-            for (int h = 2 * seg.t0; ok && h < 2 * seg.t1; h += kBatch) {
+            for (int t = seg.t0; ok && t < seg.t1; t += kBatch) {
                 int64_t row[2 * kBatch];
                 float sc[2 * kBatch];
 #pragma unroll
                 for (int u = 0; u < 2 * kBatch; ++u) {
-                    const int64_t pos = (int64_t)h * kHalf + 32 * u + lane;
+                    const int64_t pos = (int64_t)t * kRows + 32 * u + lane;
                     row[u] = -1;
-                    if (h + u / 2 < 2 * seg.t1 && pos < end) {
+                    if (t + u / 2 < seg.t1 && pos < end) {
                         row[u] = tree_row(a, seg.b, pos);
                         bad_page |= row[u] < 0;
                     }
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < 2 * kBatch; ++u) sc[u] = row[u] >= 0 ? __ldg(a.kv_scale + row[u]) : 0.f;
 #pragma unroll
                 for (int v = 0; v < kBatch; ++v) {
-                    if (h + v >= 2 * seg.t1) break;
+                    if (t + v >= seg.t1) break;
                     const int s = is % kStages;
                     if (is >= kStages)
                         ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], (is / kStages - 1) & 1, &ms.abort_flag, a.err_word));
@@ -494,28 +499,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ============================ softmax and output ============================
         // A wait that gives up clears `ok` (the same in a warp's lanes: TMEM accesses need all of them); the warp
         // then skips its remaining waits but still reaches every named barrier, so that no other warp waits for it.
-        const int st = tid - 96;                        // 0..511
-        const int q = warp & 3, set = (warp - 3) >> 2;  // TMEM lane quadrant; rows 32 set .. 32 set + 31 of the tile
-        const int half = lane >> 4;                     // this thread's 16 of them
-        const int n = 16 * q + (lane & 15);             // its column
-        const int stage_of = set >> 1;                  // the stage of the tile that they are in,
-        const int r0 = 32 * (set & 1) + 16 * half;      // and its first row there
+        const int st = tid - 96;                      // 0..511
+        const int q = warp & 3, w16 = (warp - 3) >> 2;
+        const int team = w16 >> 1, set = w16 & 1;     // tiles of the team's parity; rows 32 set .. 32 set + 31 of them
+        const int half = lane >> 4;                   // this thread's 16 of them
+        const int n = 16 * q + (lane & 15);           // its column
+        const int r0 = 32 * set + 16 * half;          // its first row
         const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
-        const int h0 = 16 * set;                        // rescale and output: columns h0..h0+15, dims 128 c + 32 q + lane
+        const int team_bar = 2 + team;                // the team's own barrier
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &ms.abort_flag, a.err_word));
         };
         grid_launch_dependents();
-        int it = 0, s = stage_of;  // tiles, and the stage of this thread's rows
+        int it = 0, s = 0;  // tiles and stages, the other team's included
         uint32_t s_ph = 0;
         while (walk.next<kCols, kRows>(a, seg)) {
             const int64_t slot = tree_slot(seg.q.q0, a.H, seg.b) + seg.g;
             // ---- the group's queries: 128 latent bytes of this thread's lane to TMEM, one RoPE chunk to shared memory.
-            // (The scores of the segment before are complete: their last one has been read here.)
+            // (The scores of the segment before are complete: its last one was read before the output's barriers.)
             {
                 const uint8_t *img = x.img + slot * kImg;
-                const uint4 *src = reinterpret_cast<const uint4 *>(img + (32 * q + lane) * 512 + set * 128);
+                const uint4 *src = reinterpret_cast<const uint4 *>(img + (32 * q + lane) * 512 + w16 * 128);
                 uint4 v[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = __ldg(src + k);
@@ -526,35 +531,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             v[4 * k + 1].x, v[4 * k + 1].y, v[4 * k + 1].z, v[4 * k + 1].w,
                                             v[4 * k + 2].x, v[4 * k + 2].y, v[4 * k + 2].z, v[4 * k + 2].w,
                                             v[4 * k + 3].x, v[4 * k + 3].y, v[4 * k + 3].z, v[4 * k + 3].w};
-                    tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + set * 32 + 16 * k, w);
+                    tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + w16 * 32 + 16 * k, w);
                 }
                 *reinterpret_cast<uint4 *>(smem + OFF_Q + st * 16) = rp;
+                if (w16 == 0 && half == 0) ms.m[n] = -INFINITY;
                 tmem_wait_st();
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 mbar_arrive(&ms.q_ready);
             }
+            named_sync(1, 2 * kTeam);
             const float c_q = __ldg(x.c_head + slot * kCols + n);
             const int col = seg.g * kCols + n, top = seg.q.n * a.H;
             const int node = col < top ? col / a.H : 0;
-            float m = -INFINITY, z = 0.f;
+            float m = -INFINITY, z = 0.f;  // the reference that z is relative to: the team's last
             int n0 = 0;  // zero rows that the column attends among this thread's rows
             for (int t = seg.t0; t < seg.t1; ++t, ++it) {
-                const int64_t p0 = (int64_t)t * kRows + stage_of * kHalf;  // position of the stage's first row
-                const int buf = it & 1;
+                const bool mine = (it & 1) == team;
+                const int s_now = s;
+                const uint32_t ph_now = s_ph;
+                if (++s == kStages) {
+                    s = 0;
+                    s_ph ^= 1;
+                }
+                if (!mine) continue;
+                const int64_t p0 = (int64_t)t * kRows;
                 // ---- scores: 32 rows of this thread's piece; a shuffle adds the other piece's half of 16 of them
-                wait(&ms.s_full, it & 1);
+                wait(&ms.s_full[team], (it >> 1) & 1);
                 tc_fence_after_sync();
                 uint32_t v[32];
-                tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 32u * set, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
-                tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 32u * set + 16u, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+                tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 64u * team + 32u * set, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+                tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 64u * team + 32u * set + 16u,
+                                   *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
                 // meanwhile the rows' figures, and which of the thread's rows the column attends
-                wait(&ms.row_full[s], s_ph);
-                const RowInfo &ri = ms.rows[s];
+                wait(&ms.row_full[s_now], ph_now);
+                const RowInfo &ri = ms.rows[s_now];
                 const uint64_t in = ri.in;
                 uint32_t on = (uint32_t)(in >> r0) & 0xFFFFu;
                 const int64_t draft = p0 + r0 - seg.q.len;  // the first row's index in the draft
-                const bool drafted = p0 + kHalf > seg.q.len;
+                const bool drafted = p0 + kRows > seg.q.len;
                 if (drafted) {
                     // bits draft .. draft + 15 of the token's mask row; a row of the context counts as set
                     uint32_t bits = 0;
@@ -566,14 +581,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t zr = (uint32_t)(ri.zero >> r0) & on;
                 n0 += __popc(zr);
                 on ^= zr;
-                const float ref_o = m == -INFINITY ? 0.f : m;  // m counts as 0 while it is -inf
                 tmem_wait_ld();
                 tc_fence_before_sync();
-                mbar_arrive(&ms.s_free);
-                // ---- d = e + 6 - m
+                mbar_arrive(&ms.s_free[team]);
+                // ---- d = e + 6
                 float d[16], dmax = -INFINITY;
                 {
-                    const uint64_t c2 = f2_pack(c_q, c_q), mr = f2_pack(-ref_o, -ref_o);
+                    const uint64_t c2 = f2_pack(c_q, c_q);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float send = __uint_as_float(half ? v[j] : v[16 + j]), keep = __uint_as_float(half ? v[16 + j] : v[j]);
@@ -583,10 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; ++k) {
                         const float4 sc = *reinterpret_cast<const float4 *>(&ri.scale[r0 + 4 * k]);
                         const float4 lg = *reinterpret_cast<const float4 *>(&ri.lg[r0 + 4 * k]);
-                        f2_unpack(f2_fma(f2_pack(d[4 * k], d[4 * k + 1]), f2_mul(f2_pack(sc.x, sc.y), c2), f2_add(f2_pack(lg.x, lg.y), mr)),
+                        f2_unpack(f2_fma(f2_pack(d[4 * k], d[4 * k + 1]), f2_mul(f2_pack(sc.x, sc.y), c2), f2_pack(lg.x, lg.y)),
                                   d[4 * k], d[4 * k + 1]);
-                        f2_unpack(f2_fma(f2_pack(d[4 * k + 2], d[4 * k + 3]), f2_mul(f2_pack(sc.z, sc.w), c2),
-                                         f2_add(f2_pack(lg.z, lg.w), mr)),
+                        f2_unpack(f2_fma(f2_pack(d[4 * k + 2], d[4 * k + 3]), f2_mul(f2_pack(sc.z, sc.w), c2), f2_pack(lg.z, lg.w)),
                                   d[4 * k + 2], d[4 * k + 3]);
                     }
                     if (on != 0xFFFFu) {
@@ -596,32 +609,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) dmax = fmaxf(dmax, d[j]);
                 }
-                // all columns move their references together: when a term exceeds one by more than kTau, or a column
-                // that has none meets its first row
-                const bool slow = bar_red_or(1, kSoftmaxThreads, dmax > kTau + kUp || (m == -INFINITY && dmax > -INFINITY));
+                // ---- the references, tile after tile: the other team has decided on the tile before.  They move
+                // together when a term exceeds one by more than kTau, or a column that has none meets its first row.
+                if (t > seg.t0) named_sync(4 + (team ^ 1), 2 * kTeam);
+                const float m_o = ms.m[n];
+                float m_n = m_o;
+                const bool slow = bar_red_or(team_bar, kTeam, dmax > m_o + (kTau + kUp));
                 bool rescale = false;
                 if (slow) {
                     const float hm = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 16));
-                    if (half == 0) ms.red[set][n] = hm;
-                    named_sync(1, kSoftmaxThreads);
-                    const float tmax = fmaxf(fmaxf(ms.red[0][n], ms.red[1][n]), fmaxf(ms.red[2][n], ms.red[3][n])) + (ref_o - kUp);
-                    const float mn = m == -INFINITY ? tmax : (tmax > m + kTau ? tmax : m);
-                    const float al = (m == -INFINITY || mn == m) ? 1.f : ex2_approx(m - mn);
-                    if (set == 0 && half == 0) ms.alpha[n] = al;
-                    const float dl = mn == -INFINITY ? 0.f : ref_o - mn;
-                    m = mn;
-                    z *= al;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) d[j] += dl;
-                    rescale = bar_red_or(1, kSoftmaxThreads, al != 1.f) && t > seg.t0;
+                    if (half == 0) ms.red[w16][n] = hm;
+                    named_sync(team_bar, kTeam);
+                    const float tmax = fmaxf(ms.red[2 * team][n], ms.red[2 * team + 1][n]) - kUp;
+                    m_n = tmax > m_o + kTau ? tmax : m_o;
+                    const float al = (m_o == -INFINITY || m_n == m_o) ? 1.f : ex2_approx(m_o - m_n);
+                    if (set == 0 && half == 0) {
+                        ms.alpha[team][n] = al;
+                        ms.m[n] = m_n;
+                    }
+                    rescale = bar_red_or(team_bar, kTeam, al != 1.f) && t > seg.t0;
                 }
-                // ---- weights
+                if (t + 1 < seg.t1) named_arrive(4 + team, 2 * kTeam);
+                if (m != m_n) {  // z, relative to the team's last reference, to this one
+                    if (m != -INFINITY) z *= ex2_approx(m - m_n);
+                    m = m_n;
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                // ---- weights 2^(e + 6 - m)
                 uint32_t whi[4], wlo[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float4 inv = *reinterpret_cast<const float4 *>(&ri.inv[r0 + 4 * k]);
-                    const float w0 = ex2_approx(d[4 * k]), w1 = ex2_approx(d[4 * k + 1]), w2 = ex2_approx(d[4 * k + 2]),
-                                w3 = ex2_approx(d[4 * k + 3]);
+                    const float w0 = ex2_approx(d[4 * k] - ref), w1 = ex2_approx(d[4 * k + 1] - ref),
+                                w2 = ex2_approx(d[4 * k + 2] - ref), w3 = ex2_approx(d[4 * k + 3] - ref);
                     z = fmaf(w0, inv.x, z);
                     z = fmaf(w1, inv.y, z);
                     z = fmaf(w2, inv.z, z);
@@ -639,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool there = in >> r & 1;
                     if (!there || p0 + r >= seg.q.len) {
                         // (complete since before the score: this makes the copy's bytes visible here too)
-                        (void)mbar_wait(&ms.kv_full[s], s_ph, &ms.abort_flag, a.err_word);
-                        uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s * kStage + ((st >> 6) & 3) * kBlk + r * 128);
+                        (void)mbar_wait(&ms.kv_full[s_now], ph_now, &ms.abort_flag, a.err_word);
+                        uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s_now * kStage + ((st >> 6) & 3) * kBlk + r * 128);
 #pragma unroll 1
                         for (int k = 0; k < 8; ++k) {
                             uint4 u = make_uint4(0u, 0u, 0u, 0u);
@@ -655,44 +675,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                // the context product two tiles back has read this weight buffer
-                if (it >= 2) wait(&ms.pv_done[buf], ((it >> 1) - 1) & 1);
-                uint8_t *wb = smem + OFF_W + buf * kW + sw128_offset(n, 32 * set + 16 * half);
+                // the context product of the team's tile before has read this weight buffer
+                if (it >= 2) wait(&ms.pv_done[team], ((it >> 1) - 1) & 1);
+                uint8_t *wb = smem + OFF_W + team * kW + sw64_offset(n, r0);
                 *reinterpret_cast<uint4 *>(wb) = make_uint4(whi[0], whi[1], whi[2], whi[3]);
                 *reinterpret_cast<uint4 *>(wb + kW / 2) = make_uint4(wlo[0], wlo[1], wlo[2], wlo[3]);
                 if (rescale) {
-                    // this warp's part of the accumulators, once the context product before is complete, where one of
-                    // its columns moved
-                    wait(&ms.pv_done[buf ^ 1], ((it - 1) >> 1) & 1);
+                    // this warp's part of the accumulators, 32 columns by 32 dims of each block, where a column moved,
+                    // once the context product before is complete.  (The one before that is: the wait above.)
+                    wait(&ms.pv_done[team ^ 1], ((it - 1) >> 1) & 1);
                     tc_fence_after_sync();
-                    const float mine = ms.alpha[h0 + (lane & 15)];
-                    if (__any_sync(0xffffffffu, mine != 1.f)) {
+                    const float f32 = ms.alpha[team][32 * set + lane];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!__any_sync(0xffffffffu, half == h && f32 != 1.f)) continue;
 #pragma unroll 1
                         for (int c = 0; c < 4; c += 2) {
                             uint32_t o[2][16];
-                            tmem_ld_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o[0]);
-                            tmem_ld_32x32b_x16(tmem + lane_addr + TM_O + 64u * (c + 1) + (uint32_t)h0, o[1]);
+                            const uint32_t at = tmem + lane_addr + TM_O + 64u * c + 32u * set + 16u * h;
+                            tmem_ld_32x32b_x16(at, o[0]);
+                            tmem_ld_32x32b_x16(at + 64u, o[1]);
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
-                                const float f = __shfl_sync(0xffffffffu, mine, j);
+                                const float f = __shfl_sync(0xffffffffu, f32, 16 * h + j);
                                 o[0][j] = __float_as_uint(__uint_as_float(o[0][j]) * f);
                                 o[1][j] = __float_as_uint(__uint_as_float(o[1][j]) * f);
                             }
-                            tmem_st_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o[0]);
-                            tmem_st_32x32b_x16(tmem + lane_addr + TM_O + 64u * (c + 1) + (uint32_t)h0, o[1]);
+                            tmem_st_32x32b_x16(at, o[0]);
+                            tmem_st_32x32b_x16(at + 64u, o[1]);
                         }
-                        tmem_wait_st();
                     }
+                    tmem_wait_st();
                 }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
-                mbar_arrive(&ms.w_full[buf]);
-                s += 2;
-                if (s >= kStages) {
-                    s -= kStages;
-                    s_ph ^= 1;
-                }
+                mbar_arrive(&ms.w_full[team]);
             }
 
             // ---- output: sums over a column's 8 threads
@@ -701,26 +719,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *part = a.part + ((int64_t)blockIdx.x * 2 + (seg.first ? 1 : 0)) * tree_part_floats(kCols);
             auto over_sets = [&](float v) -> float {
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
-                named_sync(1, kSoftmaxThreads);  // red's readers before this are done
-                if (half == 0) ms.red[set][n] = v;
-                named_sync(1, kSoftmaxThreads);
+                named_sync(1, 2 * kTeam);  // red's readers before this are done
+                if (half == 0) ms.red[w16][n] = v;
+                named_sync(1, 2 * kTeam);
                 return ms.red[0][n] + ms.red[1][n] + ms.red[2][n] + ms.red[3][n];
             };
             const float nn = over_sets((float)n0) * exp2f(kUp);
-            const float zz = over_sets(z);
-            if (set == 0 && half == 0) {
+            const float m_end = ms.m[n];  // (the barriers above: both teams' last)
+            const float zz = over_sets(m == -INFINITY ? z : z * ex2_approx(m - m_end));
+            if (w16 == 0 && half == 0) {
                 // nothing but zero rows: the accumulators are 0 and stay so
-                const float all = nn == 0.f ? zz : zz + nn * exp2f(m == -INFINITY ? 0.f : -m);
-                ms.alpha[n] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
+                const float all = nn == 0.f ? zz : zz + nn * exp2f(m_end == -INFINITY ? 0.f : -m_end);
+                ms.alpha[0][n] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
                 if (!whole) {
-                    part[kCols * kKL + n] = m;
+                    part[kCols * kKL + n] = m_end;
                     part[kCols * (kKL + 1) + n] = zz;
                     part[kCols * (kKL + 2) + n] = nn;
                 }
             }
             wait(&ms.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
             tc_fence_after_sync();
-            named_sync(1, kSoftmaxThreads);
+            named_sync(1, 2 * kTeam);
+            const int h0 = 16 * w16;  // columns h0 .. h0 + 15
             if (ok) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -732,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float v[16];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float4 a4 = *reinterpret_cast<const float4 *>(&ms.alpha[h0 + 4 * k]);
+                        const float4 a4 = *reinterpret_cast<const float4 *>(&ms.alpha[0][h0 + 4 * k]);
                         v[4 * k] = __uint_as_float(o[4 * k]) * a4.x;
                         v[4 * k + 1] = __uint_as_float(o[4 * k + 1]) * a4.y;
                         v[4 * k + 2] = __uint_as_float(o[4 * k + 2]) * a4.z;
@@ -779,15 +799,17 @@ cudaError_t launch_tree_tc(const TreeArgs &a, void *images, cudaStream_t st) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
     CUtensorMap m_lc, m_rc;
-    const cuuint64_t dims[2] = {(cuuint64_t)kRow, (cuuint64_t)a.cache_rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)kRow};
-    const cuuint32_t rows = (cuuint32_t)(a.page_shift < 6 ? 1 << a.page_shift : kHalf);
-    const cuuint32_t box_lc[2] = {128, rows}, box_rc[2] = {64, rows}, es[2] = {1, 1};
+    // latent bytes as [4 blocks][rows][128 bytes], so that one copy lays four swizzled blocks down; RoPE bytes by row
+    const bool whole = a.page_shift >= 6;  // a tile lies within a page
+    const cuuint64_t dims_lc[3] = {128, (cuuint64_t)a.cache_rows, 4}, strides_lc[2] = {(cuuint64_t)kRow, 128};
+    const cuuint64_t dims_rc[2] = {(cuuint64_t)kRow, (cuuint64_t)a.cache_rows}, strides_rc[1] = {(cuuint64_t)kRow};
+    const cuuint32_t rows = (cuuint32_t)(whole ? kRows : 1 << a.page_shift);
+    const cuuint32_t box_lc[3] = {128, rows, whole ? 4u : 1u}, box_rc[2] = {64, rows}, es[3] = {1, 1, 1};
     void *base = const_cast<uint8_t *>(a.kv8);
-    if (encode(&m_lc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box_lc, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    if (encode(&m_lc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims_lc, strides_lc, box_lc, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
             CUDA_SUCCESS ||
-        encode(&m_rc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box_rc, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        encode(&m_rc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims_rc, strides_rc, box_rc, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
             CUDA_SUCCESS)
         return cudaErrorInvalidValue;
