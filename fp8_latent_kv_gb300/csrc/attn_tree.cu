@@ -29,8 +29,8 @@ struct Smem {
 };
 
 __global__ void __launch_bounds__(288) tree_sched_kernel(TreeArgs a) {
-    __shared__ int64_t scan[33];
-    tree_schedule<kCols, kRows>(a, scan);
+    __shared__ int64_t scan[66];
+    tree_schedule<kCols, kRows, 1>(a, scan);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a) {

@@ -9,11 +9,11 @@
 //            that one shuffle adds the halves of the dot product.
 //   context  O^T[d][n] += sum_t V8[t][d] W[n][t]       M = 128 dims (x4), N = 64 columns, K = 128 rows; V8 = the same
 //            bytes read MN-major, W the softmax weights as two pieces, hi in e4m3 and lo, what hi leaves, in e5m2:
-//            2^-7 of a weight at most, and terms down to 2^-22 of the column's largest still count (two e4m3 pieces
+//            2^-7 of a weight at most, and terms down to 2^-21 of the column's largest still count (two e4m3 pieces
 //            would round everything below 2^-16 to nothing, which a long context's many small terms add up to).
-// Weights: with e_t = score_t log2(e) + log2(scale_t) and a running reference m >= max e - 2 for each column,
-// w_t = 2^(e_t - m + 6) <= 256 holds the row scale already, O = sum w_t v_t and z = sum w_t / scale_t; the factor
-// 2^6 cancels.  A weight's share of e4m3's range then follows its own column's largest term whatever rows, drafted
+// Weights: with e_t = score_t log2(e) + log2(scale_t) and a running reference m >= max e - 3.75 for each column,
+// w_t = 2^(e_t - m + 5) <= 2^8.75 holds the row scale already, O = sum w_t v_t and z = sum w_t / scale_t; the factor
+// 2^5 cancels.  A weight's share of e4m3's range then follows its own column's largest term whatever rows, drafted
 // or not, other columns attend.  A row whose scale is below 2^-100 (zeros, subnormal maxima) has score 0 and adds
 // nothing to O: such rows are only counted, and the count enters z as n0 2^-m at the end.
 //
@@ -39,6 +39,7 @@ using namespace sm100;
 constexpr int kCols = 64;
 constexpr int kRows = 64;
 constexpr int kStages = 5;
+constexpr int kSegment = 8;                // a segment's start and end cost about as much as this many tiles
 constexpr int kTeam = 256;                 // threads of a softmax team
 constexpr int kThreads = 96 + 2 * kTeam;
 constexpr uint32_t kBlk = 8192;            // 64 rows x 128 latent bytes (SW128)
@@ -49,8 +50,8 @@ constexpr uint32_t kQRope = 128 * 64;      // then 128 x 64 RoPE bytes (SW64)
 constexpr uint32_t kImg = kQLat + kQRope;
 constexpr uint32_t kW = 8192;              // hi [64 columns][64 rows] (SW64), then lo
 constexpr uint32_t OFF_ST = 0, OFF_W = kStages * kStage, OFF_Q = OFF_W + 2 * kW, OFF_MISC = OFF_Q + kQRope;
-constexpr float kTau = 2.0f;               // the reference moves when a term exceeds it by more than 2^kTau
-constexpr float kUp = 6.0f;                // weights are held times 2^kUp: at most 2^8 < 448
+constexpr float kTau = 3.75f;              // the reference moves when a term exceeds it by more than 2^kTau
+constexpr float kUp = 5.0f;                // weights are held times 2^kUp: at most 2^8.75 < 448
 constexpr float kTiny = 7.888609e-31f;     // 2^-100
 constexpr uint32_t TM_Q = 0, TM_S = 128, TM_O = 256;
 
@@ -64,7 +65,7 @@ struct Misc {
     RowInfo rows[kStages];
     alignas(16) float m[kCols];            // running references (log2 units), -inf before any attended row
     alignas(16) float red[4][kCols];       // maxima of a team's two sets of rows, team by team; at the end sums
-    alignas(16) float alpha[2][kCols];     // each team's rescale factors; at the end alpha[0] = 1 / z
+    alignas(16) float zinv[kCols];         // at the end: 1 / z
     uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_full[2], s_free[2], w_full[2], pv_done[2], q_ready,
         final_bar;
     uint32_t tmem_base;
@@ -90,6 +91,17 @@ __device__ __forceinline__ int query_lane(int n, int piece) { return (n >> 4) * 
 __device__ __forceinline__ void named_arrive(int id, int count) {
     __threadfence_block();
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// 16 lanes x 32 consecutive 32-bit columns: register 4 i + k of lane l holds lane l / 4 + 8 (k / 2), column
+// 8 i + 2 (l % 4) + k % 2.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 
 // Score MMA with A in tensor memory.
@@ -122,18 +134,15 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint3
     e4m3x2_to_f32((uint16_t)hi, x, y);
     lo = enc_pair(a - x, b - y);
 }
-// Two softmax weights (at most 2^8) -> e4m3 pieces and e5m2 pieces of what those leave.  By way of f16, whose 11
+// Two softmax weights (at most 2^8.75) -> e4m3 pieces and e5m2 pieces of what those leave.  By way of f16, whose 11
 // bits are finer than the 7 that the pieces keep; the residual is exact there.
-__device__ __forceinline__ void split_weights(float a, float b, uint32_t &hi, uint32_t &lo) {
+__device__ __forceinline__ void split_weights(float a, float b, uint16_t &hi, uint16_t &lo) {
     uint32_t w16, h16, r16;
-    uint16_t h8, l8;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w16) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h8) : "r"(w16));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(w16));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(hi));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r16) : "r"(w16), "r"(h16));
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(l8) : "r"(r16));
-    hi = h8;
-    lo = l8;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r16));
 }
 __device__ __forceinline__ float lg2_approx(float x) {
     float y;
@@ -160,13 +169,13 @@ constexpr int kPrepCols = 8, kPrepThreads = kPrepCols * 36;
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uint8_t *img, float *c_head) {
     grid_dependency_wait();
     grid_launch_dependents();
-    __shared__ int64_t scan[33];
+    __shared__ int64_t scan[66];
     __shared__ int qmax_bits[kPrepCols];
     __shared__ int64_t pad_slot[kPrepCols];
     __shared__ int pad_from[kPrepCols];
     const int tid = threadIdx.x;
     if (blockIdx.x == 0) {
-        tree_schedule<kCols, kRows>(a, scan);
+        tree_schedule<kCols, kRows, kSegment>(a, scan);
         return;
     }
     const int64_t col0 = (int64_t)(blockIdx.x - 1) * kPrepCols;
@@ -266,15 +275,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&ms.kv_full[s], 1);
             mbar_init(&ms.kv_free[s], 1);
-            mbar_init(&ms.row_full[s], 32);
+            mbar_init(&ms.row_full[s], 1);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&ms.s_full[k], 1);
-            mbar_init(&ms.s_free[k], kTeam);
-            mbar_init(&ms.w_full[k], kTeam);
+            mbar_init(&ms.s_free[k], kTeam / 32);  // one arrival for each warp
+            mbar_init(&ms.w_full[k], kTeam / 32);
             mbar_init(&ms.pv_done[k], 1);
         }
-        mbar_init(&ms.q_ready, 2 * kTeam);
+        mbar_init(&ms.q_ready, 2 * kTeam / 32);
         mbar_init(&ms.final_bar, 1);
         ms.abort_flag = 0;
         fence_barrier_init();
@@ -489,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ri.in = in[0] | (uint64_t)in[1] << 32;
                         ri.zero = zero[0] | (uint64_t)zero[1] << 32;
                     }
-                    mbar_arrive(&ms.row_full[s]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.row_full[s]);
                     ++is;
                 }
             }
@@ -502,9 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = tid - 96;                      // 0..511
         const int q = warp & 3, w16 = (warp - 3) >> 2;
         const int team = w16 >> 1, set = w16 & 1;     // tiles of the team's parity; rows 32 set .. 32 set + 31 of them
-        const int half = lane >> 4;                   // this thread's 16 of them
-        const int n = 16 * q + (lane & 15);           // its column
-        const int r0 = 32 * set + 16 * half;          // its first row
+        // A 16-lane TMEM load of 8 columns hands lane l rows 2 (l % 4) and 2 (l % 4) + 1 of columns l / 4 and l / 4 + 8: the
+        // hi and lo pieces' loads match register by register.  So a thread holds, for two columns, rows 8 i + 2 (l % 4)
+        // and the next, i < 4, of its set's 32.
+        const int n_a = 16 * q + (lane >> 2), n_b = n_a + 8;
+        const int r0 = 32 * set + 2 * (lane & 3);     // its first row
         const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
         const int team_bar = 2 + team;                // the team's own barrier
         bool ok = true;
@@ -534,18 +546,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + w16 * 32 + 16 * k, w);
                 }
                 *reinterpret_cast<uint4 *>(smem + OFF_Q + st * 16) = rp;
-                if (w16 == 0 && half == 0) ms.m[n] = -INFINITY;
+                if (st < kCols) ms.m[st] = -INFINITY;
                 tmem_wait_st();
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
-                mbar_arrive(&ms.q_ready);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.q_ready);
             }
             named_sync(1, 2 * kTeam);
-            const float c_q = __ldg(x.c_head + slot * kCols + n);
-            const int col = seg.g * kCols + n, top = seg.q.n * a.H;
-            const int node = col < top ? col / a.H : 0;
-            float m = -INFINITY, z = 0.f;  // the reference that z is relative to: the team's last
-            int n0 = 0;  // zero rows that the column attends among this thread's rows
+            const float c_a = __ldg(x.c_head + slot * kCols + n_a), c_b = __ldg(x.c_head + slot * kCols + n_b);
+            const int top = seg.q.n * a.H;
+            float m_a = -INFINITY, m_b = -INFINITY;             // the references that z is relative to: the team's last
+            uint64_t z_a = f2_pack(0.f, 0.f), z_b = f2_pack(0.f, 0.f);
+            int zero_a = 0, zero_b = 0;                         // zero rows that the columns attend among this thread's
             for (int t = seg.t0; t < seg.t1; ++t, ++it) {
                 const bool mine = (it & 1) == team;
                 const int s_now = s;
@@ -556,101 +569,144 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!mine) continue;
                 const int64_t p0 = (int64_t)t * kRows;
-                // ---- scores: 32 rows of this thread's piece; a shuffle adds the other piece's half of 16 of them
+                // ---- scores
                 wait(&ms.s_full[team], (it >> 1) & 1);
                 tc_fence_after_sync();
-                uint32_t v[32];
-                tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 64u * team + 32u * set, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
-                tmem_ld_32x32b_x16(tmem + lane_addr + TM_S + 64u * team + 32u * set + 16u,
-                                   *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
-                // meanwhile the rows' figures, and which of the thread's rows the column attends
+                uint32_t hi[16], lo[16];
+                tmem_ld_16x256b_x4(tmem + lane_addr + TM_S + 64u * team + 32u * set, hi);
+                tmem_ld_16x256b_x4(tmem + lane_addr + (16u << 16) + TM_S + 64u * team + 32u * set, lo);
+                // meanwhile the rows' figures, and which rows the columns attend (bit 2 i + k: row r0 + 8 i + k)
                 wait(&ms.row_full[s_now], ph_now);
                 const RowInfo &ri = ms.rows[s_now];
                 const uint64_t in = ri.in;
-                uint32_t on = (uint32_t)(in >> r0) & 0xFFFFu;
-                const int64_t draft = p0 + r0 - seg.q.len;  // the first row's index in the draft
                 const bool drafted = p0 + kRows > seg.q.len;
-                if (drafted) {
-                    // bits draft .. draft + 15 of the token's mask row; a row of the context counts as set
-                    uint32_t bits = 0;
+                const bool plain = !drafted && in == ~(uint64_t)0 && ri.zero == 0;  // every column attends every row
+                uint32_t on_a = 0xFFu, on_b = 0xFFu;
+                if (!plain) {
+                    on_a = on_b = 0;
+                    const int c0 = seg.g * kCols, node_a = min(c0 + n_a, top - 1) / a.H, node_b = min(c0 + n_b, top - 1) / a.H;
 #pragma unroll 1
-                    for (int u = 0; u < 16; ++u)
-                        if (draft + u < 0 || ((on >> u & 1) && tree_sees(a, seg.q.q0, node, (int)(draft + u)))) bits |= 1u << u;
-                    on &= bits;
+                    for (int u = 0; u < 8; ++u) {
+                        const int r = r0 + 8 * (u >> 1) + (u & 1);
+                        if (!(in >> r & 1)) continue;
+                        const int64_t draft = p0 + r - seg.q.len;  // the row's index in the draft
+                        const bool sa = draft < 0 || tree_sees(a, seg.q.q0, node_a, (int)draft);
+                        const bool sb = draft < 0 || tree_sees(a, seg.q.q0, node_b, (int)draft);
+                        if (ri.zero >> r & 1) {
+                            zero_a += sa;
+                            zero_b += sb;
+                        } else {
+                            on_a |= (uint32_t)sa << u;
+                            on_b |= (uint32_t)sb << u;
+                        }
+                    }
                 }
-                const uint32_t zr = (uint32_t)(ri.zero >> r0) & on;
-                n0 += __popc(zr);
-                on ^= zr;
                 tmem_wait_ld();
                 tc_fence_before_sync();
-                mbar_arrive(&ms.s_free[team]);
-                // ---- d = e + 6
-                float d[16], dmax = -INFINITY;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.s_free[team]);
+                // ---- e + 5, row pairs packed: 0..3 of column a, 4..7 of column b
+                uint64_t d2[8];
+                float max_a = -INFINITY, max_b = -INFINITY;
                 {
-                    const uint64_t c2 = f2_pack(c_q, c_q);
+                    const uint64_t ca = f2_pack(c_a, c_a), cb = f2_pack(c_b, c_b);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float send = __uint_as_float(half ? v[j] : v[16 + j]), keep = __uint_as_float(half ? v[16 + j] : v[j]);
-                        d[j] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 sc = *reinterpret_cast<const float2 *>(&ri.scale[r0 + 8 * i]);
+                        const float2 lg = *reinterpret_cast<const float2 *>(&ri.lg[r0 + 8 * i]);
+                        const uint64_t sc2 = f2_pack(sc.x, sc.y), lg2 = f2_pack(lg.x, lg.y);
+                        const uint64_t sa = f2_add(f2_pack(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
+                                                   f2_pack(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])));
+                        const uint64_t sb = f2_add(f2_pack(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])),
+                                                   f2_pack(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])));
+                        d2[i] = f2_fma(sa, f2_mul(sc2, ca), lg2);
+                        d2[4 + i] = f2_fma(sb, f2_mul(sc2, cb), lg2);
+                    }
+                    if (!plain) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float u, v;
+                            f2_unpack(d2[i], u, v);
+                            d2[i] = f2_pack(on_a >> (2 * i) & 1 ? u : -INFINITY, on_a >> (2 * i + 1) & 1 ? v : -INFINITY);
+                            f2_unpack(d2[4 + i], u, v);
+                            d2[4 + i] = f2_pack(on_b >> (2 * i) & 1 ? u : -INFINITY, on_b >> (2 * i + 1) & 1 ? v : -INFINITY);
+                        }
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 sc = *reinterpret_cast<const float4 *>(&ri.scale[r0 + 4 * k]);
-                        const float4 lg = *reinterpret_cast<const float4 *>(&ri.lg[r0 + 4 * k]);
-                        f2_unpack(f2_fma(f2_pack(d[4 * k], d[4 * k + 1]), f2_mul(f2_pack(sc.x, sc.y), c2), f2_pack(lg.x, lg.y)),
-                                  d[4 * k], d[4 * k + 1]);
-                        f2_unpack(f2_fma(f2_pack(d[4 * k + 2], d[4 * k + 3]), f2_mul(f2_pack(sc.z, sc.w), c2), f2_pack(lg.z, lg.w)),
-                                  d[4 * k + 2], d[4 * k + 3]);
+                    for (int i = 0; i < 4; ++i) {
+                        float u, v;
+                        f2_unpack(d2[i], u, v);
+                        max_a = fmaxf(max_a, fmaxf(u, v));
+                        f2_unpack(d2[4 + i], u, v);
+                        max_b = fmaxf(max_b, fmaxf(u, v));
                     }
-                    if (on != 0xFFFFu) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) d[j] = on >> j & 1 ? d[j] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) dmax = fmaxf(dmax, d[j]);
                 }
                 // ---- the references, tile after tile: the other team has decided on the tile before.  They move
                 // together when a term exceeds one by more than kTau, or a column that has none meets its first row.
                 if (t > seg.t0) named_sync(4 + (team ^ 1), 2 * kTeam);
-                const float m_o = ms.m[n];
-                float m_n = m_o;
-                const bool slow = bar_red_or(team_bar, kTeam, dmax > m_o + (kTau + kUp));
-                bool rescale = false;
+                float na = ms.m[n_a], nb = ms.m[n_b];
+                const float m_c = ms.m[32 * set + lane];  // of the accumulator columns that this warp rescales
+                const bool slow = bar_red_or(team_bar, kTeam, max_a > na + (kTau + kUp) || max_b > nb + (kTau + kUp));
+                float move = 1.f;                         // that column's factor
                 if (slow) {
-                    const float hm = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 16));
-                    if (half == 0) ms.red[w16][n] = hm;
-                    named_sync(team_bar, kTeam);
-                    const float tmax = fmaxf(ms.red[2 * team][n], ms.red[2 * team + 1][n]) - kUp;
-                    m_n = tmax > m_o + kTau ? tmax : m_o;
-                    const float al = (m_o == -INFINITY || m_n == m_o) ? 1.f : ex2_approx(m_o - m_n);
-                    if (set == 0 && half == 0) {
-                        ms.alpha[team][n] = al;
-                        ms.m[n] = m_n;
+                    max_a = fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 1));
+                    max_b = fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 1));
+                    max_a = fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 2));
+                    max_b = fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 2));
+                    if ((lane & 3) == 0) {
+                        ms.red[w16][n_a] = max_a;
+                        ms.red[w16][n_b] = max_b;
                     }
-                    rescale = bar_red_or(team_bar, kTeam, al != 1.f) && t > seg.t0;
+                    named_sync(team_bar, kTeam);
+                    auto moved = [&](int n, float m) -> float {
+                        const float top_e = fmaxf(ms.red[2 * team][n], ms.red[2 * team + 1][n]) - kUp;
+                        return top_e > m + kTau ? top_e : m;
+                    };
+                    na = moved(n_a, na);
+                    nb = moved(n_b, nb);
+                    const float nc = moved(32 * set + lane, m_c);
+                    if (q == 0) ms.m[32 * set + lane] = nc;  // (all have read the old ones)
+                    move = m_c == -INFINITY || nc == m_c ? 1.f : ex2_approx(m_c - nc);
                 }
                 if (t + 1 < seg.t1) named_arrive(4 + team, 2 * kTeam);
-                if (m != m_n) {  // z, relative to the team's last reference, to this one
-                    if (m != -INFINITY) z *= ex2_approx(m - m_n);
-                    m = m_n;
+                if (m_a != na || m_b != nb) {  // z, relative to the team's last references, to these
+                    const float fa = m_a == -INFINITY || m_a == na ? 1.f : ex2_approx(m_a - na);
+                    const float fb = m_b == -INFINITY || m_b == nb ? 1.f : ex2_approx(m_b - nb);
+                    z_a = f2_mul(z_a, f2_pack(fa, fa));
+                    z_b = f2_mul(z_b, f2_pack(fb, fb));
+                    m_a = na;
+                    m_b = nb;
                 }
-                const float ref = m == -INFINITY ? 0.f : m;
-                // ---- weights 2^(e + 6 - m)
-                uint32_t whi[4], wlo[4];
+                // the context product of the team's tile before has read this weight buffer
+                if (it >= 2) wait(&ms.pv_done[team], ((it >> 1) - 1) & 1);
+                // ---- weights 2^(e + 5 - m)
+                {
+                    const float ref_a = m_a == -INFINITY ? 0.f : -m_a, ref_b = m_b == -INFINITY ? 0.f : -m_b;
+                    const uint64_t ra = f2_pack(ref_a, ref_a), rb = f2_pack(ref_b, ref_b);
+                    uint8_t *const wb = smem + OFF_W + team * kW;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 inv = *reinterpret_cast<const float4 *>(&ri.inv[r0 + 4 * k]);
-                    const float w0 = ex2_approx(d[4 * k] - ref), w1 = ex2_approx(d[4 * k + 1] - ref),
-                                w2 = ex2_approx(d[4 * k + 2] - ref), w3 = ex2_approx(d[4 * k + 3] - ref);
-                    z = fmaf(w0, inv.x, z);
-                    z = fmaf(w1, inv.y, z);
-                    z = fmaf(w2, inv.z, z);
-                    z = fmaf(w3, inv.w, z);
-                    uint32_t h01, l01, h23, l23;
-                    split_weights(w0, w1, h01, l01);
-                    split_weights(w2, w3, h23, l23);
-                    whi[k] = h01 | (h23 << 16);
-                    wlo[k] = l01 | (l23 << 16);
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 inv = *reinterpret_cast<const float2 *>(&ri.inv[r0 + 8 * i]);
+                        const uint64_t inv2 = f2_pack(inv.x, inv.y);
+                        float u, v, x0, x1, y0, y1;
+                        f2_unpack(f2_add(d2[i], ra), u, v);
+                        x0 = ex2_approx(u);
+                        x1 = ex2_approx(v);
+                        f2_unpack(f2_add(d2[4 + i], rb), u, v);
+                        y0 = ex2_approx(u);
+                        y1 = ex2_approx(v);
+                        z_a = f2_fma(f2_pack(x0, x1), inv2, z_a);
+                        z_b = f2_fma(f2_pack(y0, y1), inv2, z_b);
+                        uint16_t wh, wl;
+                        split_weights(x0, x1, wh, wl);
+                        uint8_t *p = wb + sw64_offset(n_a, r0 + 8 * i);
+                        *reinterpret_cast<uint16_t *>(p) = wh;
+                        *reinterpret_cast<uint16_t *>(p + kW / 2) = wl;
+                        split_weights(y0, y1, wh, wl);
+                        p = wb + sw64_offset(n_b, r0 + 8 * i);
+                        *reinterpret_cast<uint16_t *>(p) = wh;
+                        *reinterpret_cast<uint16_t *>(p + kW / 2) = wl;
+                    }
                 }
                 // ---- rows that were not loaded, and NaN codes of drafted rows (attended columns have NaN weights
                 // already): a weight of 0 must not meet them.  A thread owns a row's 128 bytes of a latent block.
@@ -675,66 +731,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                // the context product of the team's tile before has read this weight buffer
-                if (it >= 2) wait(&ms.pv_done[team], ((it >> 1) - 1) & 1);
-                uint8_t *wb = smem + OFF_W + team * kW + sw64_offset(n, r0);
-                *reinterpret_cast<uint4 *>(wb) = make_uint4(whi[0], whi[1], whi[2], whi[3]);
-                *reinterpret_cast<uint4 *>(wb + kW / 2) = make_uint4(wlo[0], wlo[1], wlo[2], wlo[3]);
-                if (rescale) {
+                if (slow && t > seg.t0 && __any_sync(0xffffffffu, move != 1.f)) {
                     // this warp's part of the accumulators, 32 columns by 32 dims of each block, where a column moved,
                     // once the context product before is complete.  (The one before that is: the wait above.)
                     wait(&ms.pv_done[team ^ 1], ((it - 1) >> 1) & 1);
                     tc_fence_after_sync();
-                    const float f32 = ms.alpha[team][32 * set + lane];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (!__any_sync(0xffffffffu, half == h && f32 != 1.f)) continue;
+                        if (!__any_sync(0xffffffffu, (lane >> 4) == h && move != 1.f)) continue;
+                        const uint32_t at = tmem + lane_addr + TM_O + 32u * set + 16u * h;
 #pragma unroll 1
                         for (int c = 0; c < 4; c += 2) {
                             uint32_t o[2][16];
-                            const uint32_t at = tmem + lane_addr + TM_O + 64u * c + 32u * set + 16u * h;
-                            tmem_ld_32x32b_x16(at, o[0]);
-                            tmem_ld_32x32b_x16(at + 64u, o[1]);
+                            tmem_ld_32x32b_x16(at + 64u * c, o[0]);
+                            tmem_ld_32x32b_x16(at + 64u * (c + 1), o[1]);
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
-                                const float f = __shfl_sync(0xffffffffu, f32, 16 * h + j);
+                                const float f = __shfl_sync(0xffffffffu, move, 16 * h + j);
                                 o[0][j] = __float_as_uint(__uint_as_float(o[0][j]) * f);
                                 o[1][j] = __float_as_uint(__uint_as_float(o[1][j]) * f);
                             }
-                            tmem_st_32x32b_x16(at, o[0]);
-                            tmem_st_32x32b_x16(at + 64u, o[1]);
+                            tmem_st_32x32b_x16(at + 64u * c, o[0]);
+                            tmem_st_32x32b_x16(at + 64u * (c + 1), o[1]);
                         }
                     }
                     tmem_wait_st();
                 }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
-                mbar_arrive(&ms.w_full[team]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.w_full[team]);
             }
 
-            // ---- output: sums over a column's 8 threads
+            // ---- output: sums over a column's threads, four lanes of each set
             const int c0 = seg.g * kCols, nc = min(kCols, top - c0);
             const bool whole = seg.first && seg.last;
             float *part = a.part + ((int64_t)blockIdx.x * 2 + (seg.first ? 1 : 0)) * tree_part_floats(kCols);
-            auto over_sets = [&](float v) -> float {
-                v += __shfl_xor_sync(0xffffffffu, v, 16);
+            // returns the sum for column st (threads st < 64)
+            auto over_sets = [&](float u, float v) -> float {
+                u += __shfl_xor_sync(0xffffffffu, u, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                u += __shfl_xor_sync(0xffffffffu, u, 2);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
                 named_sync(1, 2 * kTeam);  // red's readers before this are done
-                if (half == 0) ms.red[w16][n] = v;
+                if ((lane & 3) == 0) {
+                    ms.red[w16][n_a] = u;
+                    ms.red[w16][n_b] = v;
+                }
                 named_sync(1, 2 * kTeam);
+                const int n = st & (kCols - 1);
                 return ms.red[0][n] + ms.red[1][n] + ms.red[2][n] + ms.red[3][n];
             };
-            const float nn = over_sets((float)n0) * exp2f(kUp);
-            const float m_end = ms.m[n];  // (the barriers above: both teams' last)
-            const float zz = over_sets(m == -INFINITY ? z : z * ex2_approx(m - m_end));
-            if (w16 == 0 && half == 0) {
+            const float nn = over_sets((float)zero_a, (float)zero_b) * exp2f(kUp);
+            float zz;
+            {
+                const float ea = ms.m[n_a], eb = ms.m[n_b];  // (the barriers above: both teams' last)
+                float u, v, fa = m_a == -INFINITY ? 1.f : ex2_approx(m_a - ea), fb = m_b == -INFINITY ? 1.f : ex2_approx(m_b - eb);
+                f2_unpack(z_a, u, v);
+                fa *= u + v;
+                f2_unpack(z_b, u, v);
+                fb *= u + v;
+                zz = over_sets(fa, fb);
+            }
+            if (st < kCols) {
+                const float m_end = ms.m[st];
                 // nothing but zero rows: the accumulators are 0 and stay so
                 const float all = nn == 0.f ? zz : zz + nn * exp2f(m_end == -INFINITY ? 0.f : -m_end);
-                ms.alpha[0][n] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
+                ms.zinv[st] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
                 if (!whole) {
-                    part[kCols * kKL + n] = m_end;
-                    part[kCols * (kKL + 1) + n] = zz;
-                    part[kCols * (kKL + 2) + n] = nn;
+                    part[kCols * kKL + st] = m_end;
+                    part[kCols * (kKL + 1) + st] = zz;
+                    part[kCols * (kKL + 2) + st] = nn;
                 }
             }
             wait(&ms.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
@@ -752,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float v[16];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float4 a4 = *reinterpret_cast<const float4 *>(&ms.alpha[0][h0 + 4 * k]);
+                        const float4 a4 = *reinterpret_cast<const float4 *>(&ms.zinv[h0 + 4 * k]);
                         v[4 * k] = __uint_as_float(o[4 * k]) * a4.x;
                         v[4 * k + 1] = __uint_as_float(o[4 * k + 1]) * a4.y;
                         v[4 * k + 2] = __uint_as_float(o[4 * k + 2]) * a4.z;

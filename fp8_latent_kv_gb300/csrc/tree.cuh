@@ -30,14 +30,14 @@ __host__ __device__ __forceinline__ int64_t tree_positions(int max_pages, int pa
 }
 
 // Work shares.  A group is kCols consecutive (token, head) columns of one sequence (column = token * H +
-// head); its work is the ceil(rows / kRows) row tiles of the sequence.  All groups' tiles in order (sequence,
-// group, tile) are one line of W units, cut into `shares` equal pieces, one for each CTA: whatever the
-// lengths, no CTA has more than one tile more than another.  A group that one CTA walks from its first tile
-// to its last is finished there; one that a cut falls into leaves one partial set for each CTA that walks a
-// part of it, and the merge joins them.
+// head); its work is the ceil(rows / kRows) row tiles of the sequence, and kSegment tiles' worth for its start
+// and end.  All groups' work in order (sequence, group, tile) is one line, cut into `shares` equal pieces, one
+// for each CTA, whatever the lengths.  A group that one CTA walks from its first tile to its last is finished
+// there; one that a cut falls into leaves one partial set for each CTA that walks a part of it, and the merge
+// joins them.
 struct TreeShare {
-    int64_t unit;  // first unit of the share
-    int b, g, t;   // where that is
+    int64_t unit;  // tiles on the line before the share
+    int b, g, t;   // where it begins
     int pad;
 };
 struct TreeJob {  // a group that was cut
@@ -46,12 +46,13 @@ struct TreeJob {  // a group that was cut
 };
 constexpr int kMaxShares = 512;
 struct TreeSched {
-    int shares;  // CTAs that have work
+    int shares;  // CTAs that may have work
     int jobs;
     int pad[2];
     TreeShare share[kMaxShares + 1];  // [shares] ends the last one
     TreeJob job[kMaxShares];
-    int64_t unit0[KV8_MAX_SEQS + 1];  // units before sequence b
+    int64_t unit0[KV8_MAX_SEQS + 1];  // tiles before sequence b
+    int64_t work0[KV8_MAX_SEQS + 1];  // work before sequence b
 };
 
 struct TreeArgs {
@@ -92,93 +93,107 @@ __device__ __forceinline__ bool tree_sees(const TreeArgs &a, int q0, int i, int 
     return (__ldg(a.mask + (int64_t)(q0 + i) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u;
 }
 
-// One block: the shares and the cut groups.  `scan`: 33 * 8 bytes of shared memory.
-template <int kCols, int kRows>
+// One block: the shares and the cut groups.  `scan`: 66 * 8 bytes of shared memory.
+template <int kCols, int kRows, int kSegment>
 __device__ void tree_schedule(const TreeArgs &a, int64_t *scan) {
     TreeSched &s = *a.sched;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = (blockDim.x + 31) >> 5;
     const int64_t positions = tree_positions(a.max_pages, a.page_shift);
     const int per = (a.B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    auto units = [&](int b, bool &bad) -> int64_t {
+    auto size_of = [&](int b, bool &bad, int64_t &groups, int64_t &tiles) {
         const TreeSeq q = tree_seq(a.q_start, a.lens, b, a.R, positions);
         bad |= q.n < 0;
-        if (q.n <= 0) return 0;
-        return (int64_t)((q.n * a.H + kCols - 1) / kCols) * ((q.len + q.n + kRows - 1) / kRows);
+        groups = q.n > 0 ? (q.n * a.H + kCols - 1) / kCols : 0;
+        tiles = (q.len + q.n + kRows - 1) / kRows;
     };
     bool bad = false;
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units(b, bad);
+    int64_t groups, tiles, units = 0, work = 0;
+    for (int b = b0; b < b1; ++b) {
+        size_of(b, bad, groups, tiles);
+        units += groups * tiles;
+        work += groups * (tiles + kSegment);
+    }
     if (bad && a.err_word) atomicOr(a.err_word, (int)KV8_ERR_INDEX);
-    int64_t inc = mine;
+    int64_t ui = units, wi = work;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+        const int64_t u = __shfl_up_sync(0xffffffffu, ui, o), w = __shfl_up_sync(0xffffffffu, wi, o);
+        if (lane >= o) {
+            ui += u;
+            wi += w;
+        }
     }
-    if (lane == 31) scan[warp] = inc;
+    if (lane == 31) {
+        scan[warp] = ui;
+        scan[33 + warp] = wi;
+    }
     __syncthreads();
     if (warp == 0) {
-        int64_t v = lane < n_warps ? scan[lane] : 0;
+        int64_t u = lane < n_warps ? scan[lane] : 0, w = lane < n_warps ? scan[33 + lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
-        }
-        scan[lane] = v;
-    }
-    __syncthreads();
-    int64_t at = inc - mine + (warp > 0 ? scan[warp - 1] : 0);
-    for (int b = b0; b < b1; ++b) {
-        s.unit0[b] = at;
-        bool ignored = false;
-        at += units(b, ignored);
-    }
-    const int64_t W = scan[n_warps - 1];
-    if (tid == 0) {
-        s.unit0[a.B] = W;
-        s.jobs = 0;
-        s.shares = (int)min((int64_t)a.ctas, W);
-    }
-    __syncthreads();
-    const int C = (int)min((int64_t)a.ctas, W);
-    // the last sequence whose first unit is <= u (it has work: the next one's first unit is larger)
-    auto locate = [&](int64_t u, TreeShare &sh) {
-        int lo = 0, hi = a.B;  // unit0[lo] <= u < unit0[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s.unit0[mid] <= u) lo = mid;
-            else hi = mid;
-        }
-        const TreeSeq q = tree_seq(a.q_start, a.lens, lo, a.R, positions);
-        const int64_t tiles = (q.len + q.n + kRows - 1) / kRows, r = u - s.unit0[lo];
-        sh.unit = u;
-        sh.b = lo;
-        sh.g = (int)(r / tiles);
-        sh.t = (int)(r - sh.g * tiles);
-        return tiles;
-    };
-    for (int c = tid; c <= C; c += blockDim.x) {
-        TreeShare sh{};
-        const int64_t u = C ? W / C * c + W % C * c / C : 0;  // floor(W * c / C) without the product
-        if (c == C) {
-            sh.unit = W;
-            sh.b = a.B;
-        } else {
-            const int64_t tiles = locate(u, sh);
-            // a share that begins inside a group whose first tile the share before it walks: that group is cut
-            if (sh.t > 0) {
-                const int64_t g0 = u - sh.t, g1 = g0 + tiles;
-                const int64_t before = W / C * (c - 1) + W % C * (c - 1) / C;
-                if (g0 >= before) {
-                    int last = c;  // the share that holds the group's last unit
-                    while (last + 1 < C && W / C * (last + 1) + W % C * (last + 1) / C < g1) ++last;
-                    const int j = atomicAdd(&s.jobs, 1);
-                    s.job[j] = TreeJob{sh.b, sh.g, c - 1, last - c + 2};
-                }
+            const int64_t x = __shfl_up_sync(0xffffffffu, u, o), y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) {
+                u += x;
+                w += y;
             }
         }
+        scan[lane] = u;
+        scan[33 + lane] = w;
+    }
+    __syncthreads();
+    int64_t u_at = ui - units + (warp > 0 ? scan[warp - 1] : 0), w_at = wi - work + (warp > 0 ? scan[33 + warp - 1] : 0);
+    for (int b = b0; b < b1; ++b) {
+        bool ignored = false;
+        s.unit0[b] = u_at;
+        s.work0[b] = w_at;
+        size_of(b, ignored, groups, tiles);
+        u_at += groups * tiles;
+        w_at += groups * (tiles + kSegment);
+    }
+    const int64_t U = scan[n_warps - 1], W = scan[33 + n_warps - 1];
+    const int C = (int)min((int64_t)a.ctas, U);
+    if (tid == 0) {
+        s.unit0[a.B] = U;
+        s.work0[a.B] = W;
+        s.jobs = 0;
+        s.shares = C;
+    }
+    __syncthreads();
+    for (int c = tid; c <= C; c += blockDim.x) {
+        TreeShare sh{};
+        sh.unit = U;
+        sh.b = a.B;
+        if (c < C) {
+            const int64_t w = W / C * c + W % C * c / C;  // floor(W c / C) without the product
+            int lo = 0, hi = a.B;  // work0[lo] <= w < work0[hi]: the last such sequence, so it has work
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s.work0[mid] <= w) lo = mid;
+                else hi = mid;
+            }
+            bool ignored = false;
+            size_of(lo, ignored, groups, tiles);
+            const int64_t r = w - s.work0[lo], g = r / (tiles + kSegment), t = r - g * (tiles + kSegment) - kSegment;
+            // (a cut in a group's start and end cost is one before its first tile)
+            sh.b = lo;
+            sh.g = (int)g;
+            sh.t = (int)max(t, (int64_t)0);
+            sh.unit = s.unit0[lo] + g * tiles + sh.t;
+        }
         s.share[c] = sh;
+    }
+    __syncthreads();
+    // a share that begins inside a group whose first tile the share before it walks: that group is cut
+    for (int c = 1 + tid; c < C; c += blockDim.x) {
+        const TreeShare sh = s.share[c];
+        if (sh.t == 0 || sh.unit - sh.t < s.share[c - 1].unit) continue;
+        bool ignored = false;
+        size_of(sh.b, ignored, groups, tiles);
+        int last = c;  // the share that holds the group's last tile
+        while (last + 1 < C && s.share[last + 1].unit < sh.unit - sh.t + tiles) ++last;
+        s.job[atomicAdd(&s.jobs, 1)] = TreeJob{sh.b, sh.g, c - 1, last - c + 2};
     }
 }
 

@@ -39,7 +39,7 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
                that a query element is rounded to (bf16: 2^-17, f32: none), v the 32-bit sum's (2^-24 a step of
                at most 576, taken as 576 2^-24).  Each weight is then off by exp(+-2 d) relative.
       weights  f32: 2 steps of exp2 and a product.  bf16: held as w = p_t s_t in units that put the column's largest
-               at 2^6 or more; rounded to 11 bits (2^-12 w at most, 2^-25 where f16 is subnormal); an e4m3 piece
+               at 2^5 or more; rounded to 11 bits (2^-12 w at most, 2^-25 where f16 is subnormal); an e4m3 piece
                leaves at most 2^-4 w, and at most 2^-10 where it is subnormal (w < 2^-6; all of w below 2^-10); an
                e5m2 piece of that is off by 2^-3 of it at most, or 2^-17 where that is subnormal.  Together at most
                2^-7 w + min(2^-13, 2^-3 w) + 2^-17 + 2^-11 w, each times the row's |e4m3 value|.
@@ -72,7 +72,7 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
         tol[i] += A * (2.0 ** -21 + (2 * T + 64) * 2.0 ** -24)
         if not f32:
             ps = p * scale[rows[on]].astype(np.float64)
-            unit = ps.max(1, keepdims=True) / 64
+            unit = ps.max(1, keepdims=True) / 32
             w = ps / np.where(unit > 0, unit, 1)
             off = 2.0 ** -7 * w + np.minimum(2.0 ** -13, w / 8) + 2.0 ** -17 + 2.0 ** -11 * w
             tol[i] += (off * unit) @ np.abs(TABLE[kv8[rows[on]]][:, :512])
