@@ -18,7 +18,7 @@
 // nothing to O: such rows are only counted, and the count enters z as n0 2^-m at the end.
 //
 // Work: equal shares of (group, tile) units (tree.cuh), one CTA per SM.
-// Warps: 0 = row loads, 1 = MMA issue and TMEM, 2 = the rows' scales, 3..18 = softmax and output; warp % 4 is a
+// Warps: 0 = row loads, 1 = scores and TMEM, 2 = the rows' scales, 3 = context products, 4..19 = softmax and output; warp % 4 is a
 // warp's TMEM lane quadrant, its set (0..3) picks 32 of the tile's rows, and a thread holds 16 rows of one column.
 // The query pieces are the score's A operand in TMEM, so shared memory holds rows: five stages of 64 rows (36 KB),
 // two 16 KB weight buffers, the queries' RoPE part (8 KB).  A stage is held from its load through score, softmax and
@@ -41,7 +41,7 @@ constexpr int kRows = 64;
 constexpr int kStages = 5;
 constexpr int kSegment = 8;                // a segment's start and end cost about as much as this many tiles
 constexpr int kTeam = 256;                 // threads of a softmax team
-constexpr int kThreads = 96 + 2 * kTeam;
+constexpr int kThreads = 128 + 2 * kTeam;
 constexpr uint32_t kBlk = 8192;            // 64 rows x 128 latent bytes (SW128)
 constexpr uint32_t kRope = 4096;           // 64 rows x 64 RoPE bytes (SW64)
 constexpr uint32_t kStage = 4 * kBlk + kRope;
@@ -67,7 +67,7 @@ struct Misc {
     alignas(16) float red[4][kCols];       // maxima of a team's two sets of rows, team by team; at the end sums
     alignas(16) float zinv[kCols];         // at the end: 1 / z
     uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_full[2], s_free[2], w_full[2], pv_done[2], q_ready,
-        final_bar;
+        final_bar[2];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -112,6 +112,27 @@ __device__ __forceinline__ void mma_f8f6f4_ts(uint32_t d_tmem, uint32_t a_tmem, 
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// Bounded wait on the SM's own clock: reading the global timer takes about a microsecond, which a wait that is not
+// ready at once would pay every time.  2^32 cycles are two seconds; drains give a shorter limit.
+constexpr long long kLimit = 1ll << 32;
+
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err,
+                                         long long limit = kLimit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 31u) == 0) {
+            if (abort_flag && *abort_flag) return false;
+            if (clock64() - t0 > limit) {
+                if (abort_flag) *abort_flag = 1;
+                if (err) atomicOr(err, (int)KV8_ERR_TIMEOUT);
+                return false;
+            }
+        }
+    }
 }
 
 // True in one lane of a converged warp, the same one every time.
@@ -284,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms.pv_done[k], 1);
         }
         mbar_init(&ms.q_ready, 2 * kTeam / 32);
-        mbar_init(&ms.final_bar, 1);
+        mbar_init(&ms.final_bar[0], 1);
+        mbar_init(&ms.final_bar[1], 1);
         ms.abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&map_lc);
@@ -325,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t row = next;
                 next = t + 1 < seg.t1 ? piece(t + 1) : -1;  // a page entry's latency ahead
                 const int pieces = __popc(__ballot_sync(0xffffffffu, row >= 0));
-                if (it >= kStages) ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], ph, &ms.abort_flag, a.err_word));
+                if (it >= kStages) ok = __all_sync(0xffffffffu, bar_wait(&ms.kv_free[s], ph, &ms.abort_flag, a.err_word));
                 if (!ok) break;
                 uint8_t *st = smem + OFF_ST + s * kStage;
                 if (lane == 0) mbar_arrive_expect_tx(&ms.kv_full[s], (uint32_t)pieces * sub_rows * (uint32_t)kRow);
@@ -349,38 +371,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every load in flight lands before the CTA ends
         if (lane == 0)
             for (int i = max(0, it - kStages); i < it; ++i)
-                mbar_wait(&ms.kv_full[i % kStages], (i / kStages) & 1, nullptr, a.err_word, 200000000ull);
+                bar_wait(&ms.kv_full[i % kStages], (i / kStages) & 1, nullptr, a.err_word, kLimit / 8);
         __syncwarp();
     } else if (warp == 1) {
-        // ================================ MMA issue ================================
-        // The whole warp runs the loop, its conditions voted on, and one elected lane issues: operands stay in uniform
-        // registers.  (Issued from `if (lane == 0)` the same score MMAs took 46 cycles each instead of 32 alone, and
-        // 85 beside the softmax warps.)
+        // ================================ scores ================================
+        // The whole warp runs the loop and one elected lane issues: operands stay in uniform registers.  (Issued from
+        // `if (lane == 0)` the same MMAs took 46 cycles each instead of 32 alone, and 85 beside the softmax warps.)
+        // Scores and context products have a warp each: the tensor core's queue takes a few MMAs only, so the hundreds
+        // of cycles that an issuer spends on its waits are the core's idle time unless another one issues meanwhile.
         const uint32_t id_s = idesc_e4m3_f32(128, kRows, false, false);
-        const uint32_t id_hi = idesc_e4m3_f32(128, kCols, true, false), id_lo = id_hi | (1u << 10);  // B in e5m2
-        // descriptors of stage 0, weight buffer 0 and the query's RoPE part: an offset adds to the address field
+        // descriptors of stage 0 and of the query's RoPE part: an offset adds to the address field
         const uint64_t k_desc = smem_desc(sbase + OFF_ST, 0, 1024, kSw128);
         const uint64_t kr_desc = smem_desc(sbase + OFF_ST + 4 * kBlk, 0, 512, kSw64);
         const uint64_t qr_desc = smem_desc(sbase + OFF_Q, 0, 512, kSw64);
-        const uint64_t w_desc = smem_desc(sbase + OFF_W, 0, 512, kSw64);
-        const int n_tiles = (int)(walk.end - walk.unit);
-        int ns = 0, np = 0, sg = 0, ss = 0, ps = 0;  // tiles, segments and stages of the score / the product
-        uint32_t s_ph = 0;                           // parity of stage ss's load
-        int seg_first = 0, seg_end = 0;              // the score side's segment
-        uint32_t firsts = 0;                         // bit i % 32: tile i begins a segment
-        uint64_t t_last = globaltimer_ns();
-        uint32_t spins = 0;
-        auto ready = [&](uint64_t *bar, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok) ok = bar_wait(bar, parity, &ms.abort_flag, a.err_word);
+            ok = __all_sync(0xffffffffu, ok);
         };
-        while (np < n_tiles) {
-            bool did = false;
-            if (np < ns && ready(&ms.w_full[np & 1], (np >> 1) & 1)) {
+        int j = 0, sg = 0, s = 0;  // tiles, segments, the stage
+        uint32_t s_ph = 0;
+        while (ok && walk.next<kCols, kRows>(a, seg)) {
+            wait(&ms.q_ready, sg & 1);
+            ++sg;
+            for (int t = seg.t0; ok && t < seg.t1; ++t, ++j) {
+                wait(&ms.kv_full[s], s_ph);
+                if (j >= 2) wait(&ms.s_free[j & 1], ((j >> 1) - 1) & 1);
                 tc_fence_after_sync();
-                if (elect_one()) {
-                    const uint64_t v = k_desc + (uint64_t)(ps * (kStage >> 4));  // (the same bytes, MN-major)
-                    const uint64_t w = w_desc + (uint64_t)((np & 1) * (kW >> 4));
-                    const uint32_t keep = firsts >> (np & 31) & 1 ? 0u : 1u;
+                if (ok && elect_one()) {
+                    const uint32_t d = tmem + TM_S + 64u * (j & 1);
+                    const uint64_t k = k_desc + (uint64_t)(s * (kStage >> 4)), kr = kr_desc + (uint64_t)(s * (kStage >> 4));
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f8f6f4_ts(d, tmem + TM_Q + kb * 32 + kk * 8, k + (uint64_t)((kb * kBlk + kk * 32) >> 4), id_s, (kb | kk) != 0);
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) mma_f8f6f4(d, qr_desc + (uint64_t)(kk * 2), kr + (uint64_t)(kk * 2), id_s, 1u);
+                    mma_commit(&ms.s_full[j & 1]);
+                }
+                __syncwarp();
+                if (++s == kStages) {
+                    s = 0;
+                    s_ph ^= 1;
+                }
+            }
+        }
+        if (elect_one()) mma_commit(&ms.final_bar[0]);  // all issued MMAs complete before the CTA tears down
+        __syncwarp();
+        bar_wait(&ms.final_bar[0], 0, nullptr, a.err_word, kLimit / 8);
+        __syncwarp();
+    } else if (warp == 3) {
+        // ================================ context products ================================
+        const uint32_t id_hi = idesc_e4m3_f32(128, kCols, true, false), id_lo = id_hi | (1u << 10);  // B in e5m2
+        const uint64_t v_desc = smem_desc(sbase + OFF_ST, 0, 1024, kSw128);  // (the score's bytes, MN-major)
+        const uint64_t w_desc = smem_desc(sbase + OFF_W, 0, 512, kSw64);
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok) ok = bar_wait(bar, parity, &ms.abort_flag, a.err_word);
+            ok = __all_sync(0xffffffffu, ok);
+        };
+        int i = 0, s = 0;
+        uint32_t s_ph = 0;
+        while (ok && walk.next<kCols, kRows>(a, seg)) {
+            for (int t = seg.t0; ok && t < seg.t1; ++t, ++i) {
+                wait(&ms.kv_full[s], s_ph);  // (complete since before the score)
+                wait(&ms.w_full[i & 1], (i >> 1) & 1);
+                tc_fence_after_sync();
+                if (ok && elect_one()) {
+                    const uint64_t v = v_desc + (uint64_t)(s * (kStage >> 4));
+                    const uint64_t w = w_desc + (uint64_t)((i & 1) * (kW >> 4));
+                    const uint32_t keep = t > seg.t0;
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
@@ -389,66 +450,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kk * 32) >> 4), id_hi, kk ? 1u : keep);
                             mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kW / 2 + kk * 32) >> 4), id_lo, 1u);
                         }
-                    mma_commit(&ms.kv_free[ps]);
-                    mma_commit(&ms.pv_done[np & 1]);
+                    mma_commit(&ms.kv_free[s]);
+                    mma_commit(&ms.pv_done[i & 1]);
                 }
                 __syncwarp();
-                if (++ps == kStages) ps = 0;
-                ++np;
-                did = true;
-            } else if (ns < n_tiles) {
-                if (ns == seg_end) {  // a new segment
-                    walk.next<kCols, kRows>(a, seg);
-                    seg_first = ns;
-                    seg_end = ns + (seg.t1 - seg.t0);
-                    ++sg;
+                if (++s == kStages) {
+                    s = 0;
+                    s_ph ^= 1;
                 }
-                if (ready(&ms.kv_full[ss], s_ph) && (ns < 2 || ready(&ms.s_free[ns & 1], ((ns >> 1) - 1) & 1)) &&
-                    (ns > seg_first || ready(&ms.q_ready, (sg - 1) & 1))) {
-                    tc_fence_after_sync();
-                    firsts = ns == seg_first ? firsts | 1u << (ns & 31) : firsts & ~(1u << (ns & 31));
-                    if (elect_one()) {
-                        const uint32_t d = tmem + TM_S + 64u * (ns & 1);
-                        const uint64_t k = k_desc + (uint64_t)(ss * (kStage >> 4)), kr = kr_desc + (uint64_t)(ss * (kStage >> 4));
-#pragma unroll
-                        for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_f8f6f4_ts(d, tmem + TM_Q + kb * 32 + kk * 8, k + (uint64_t)((kb * kBlk + kk * 32) >> 4), id_s,
-                                              (kb | kk) != 0);
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)
-                            mma_f8f6f4(d, qr_desc + (uint64_t)(kk * 2), kr + (uint64_t)(kk * 2), id_s, 1u);
-                        mma_commit(&ms.s_full[ns & 1]);
-                    }
-                    __syncwarp();
-                    ++ns;
-                    if (++ss == kStages) {
-                        ss = 0;
-                        s_ph ^= 1;
-                    }
-                    did = true;
-                }
-            }
-            if (did) {
-                spins = 0;
-            } else if ((++spins & 255u) == 0) {
-                const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
-                if (__any_sync(0xffffffffu, *(volatile int *)&ms.abort_flag)) break;
-                if (spins > 256u && now - t_last > 2000000000ull) {  // no progress for 2 s
-                    if (lane == 0) {
-                        ms.abort_flag = 1;
-                        if (a.err_word) atomicOr(a.err_word, (int)KV8_ERR_TIMEOUT);
-                    }
-                    break;
-                }
-            } else if (spins == 1) {
-                t_last = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
             }
         }
-        if (elect_one()) mma_commit(&ms.final_bar);  // all issued MMAs complete before the CTA tears down
+        if (elect_one()) mma_commit(&ms.final_bar[1]);
         __syncwarp();
-        mbar_wait(&ms.final_bar, 0, nullptr, a.err_word, 200000000ull);
+        bar_wait(&ms.final_bar[1], 0, nullptr, a.err_word, kLimit / 8);
         __syncwarp();
     } else if (warp == 2) {
         // ================================ the rows' scales ================================
@@ -478,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t + v >= seg.t1) break;
                     const int s = is % kStages;
                     if (is >= kStages)
-                        ok = __all_sync(0xffffffffu, mbar_wait(&ms.kv_free[s], (is / kStages - 1) & 1, &ms.abort_flag, a.err_word));
+                        ok = __all_sync(0xffffffffu, bar_wait(&ms.kv_free[s], (is / kStages - 1) & 1, &ms.abort_flag, a.err_word));
                     if (!ok) break;
                     RowInfo &ri = ms.rows[s];
                     uint32_t in[2], zero[2];
@@ -509,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ============================ softmax and output ============================
         // A wait that gives up clears `ok` (the same in a warp's lanes: TMEM accesses need all of them); the warp
         // then skips its remaining waits but still reaches every named barrier, so that no other warp waits for it.
-        const int st = tid - 96;                      // 0..511
-        const int q = warp & 3, w16 = (warp - 3) >> 2;
+        const int st = tid - 128;                     // 0..511
+        const int q = warp & 3, w16 = (warp - 4) >> 2;
         const int team = w16 >> 1, set = w16 & 1;     // tiles of the team's parity; rows 32 set .. 32 set + 31 of them
         // A 16-lane TMEM load of 8 columns hands lane l rows 2 (l % 4) and 2 (l % 4) + 1 of columns l / 4 and l / 4 + 8: the
         // hi and lo pieces' loads match register by register.  So a thread holds, for two columns, rows 8 i + 2 (l % 4)
@@ -521,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int team_bar = 2 + team;                // the team's own barrier
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &ms.abort_flag, a.err_word));
+            if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, &ms.abort_flag, a.err_word));
         };
         grid_launch_dependents();
         int it = 0, s = 0;  // tiles and stages, the other team's included
@@ -715,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool there = in >> r & 1;
                     if (!there || p0 + r >= seg.q.len) {
                         // (complete since before the score: this makes the copy's bytes visible here too)
-                        (void)mbar_wait(&ms.kv_full[s_now], ph_now, &ms.abort_flag, a.err_word);
+                        (void)bar_wait(&ms.kv_full[s_now], ph_now, &ms.abort_flag, a.err_word);
                         uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s_now * kStage + ((st >> 6) & 3) * kBlk + r * 128);
 #pragma unroll 1
                         for (int k = 0; k < 8; ++k) {
