@@ -7,23 +7,25 @@
 //            Qs: a bf16 query element, scaled by its column's power of two, is the sum of two e4m3 values; each
 //            TMEM lane quadrant holds 16 columns' hi pieces on lanes 0..15 and their lo pieces on lanes 16..31, so
 //            that one shuffle adds the halves of the dot product.
-//   context  O^T[d][n] += sum_t V8[t][d] W[n][t]       M = 128 dims (x4), N = 64 columns, K = 128 rows; V8 = the same
-//            bytes read MN-major, W the softmax weights as two pieces, hi in e4m3 and lo, what hi leaves, in e5m2:
-//            2^-7 of a weight at most, and terms down to 2^-21 of the column's largest still count (two e4m3 pieces
-//            would round everything below 2^-16 to nothing, which a long context's many small terms add up to).
-// Weights: with e_t = score_t log2(e) + log2(scale_t) and a running reference m >= max e - 3.75 for each column,
-// w_t = 2^(e_t - m + 5) <= 2^8.75 holds the row scale already, O = sum w_t v_t and z = sum w_t / scale_t; the factor
-// 2^5 cancels.  A weight's share of e4m3's range then follows its own column's largest term whatever rows, drafted
-// or not, other columns attend.  A row whose scale is below 2^-100 (zeros, subnormal maxima) has score 0 and adds
-// nothing to O: such rows are only counted, and the count enters z as n0 2^-m at the end.
+//   context  O^T[d][n] += sum_t V8[t][d] W[n][t]       M = 128 dims (x4), N = 64 columns, K = 64 rows; V8 = the same
+//            bytes read MN-major, W the softmax weights as the sum of two e4m3 values with a power of two for each
+//            column and 32 rows (the block-scaled form of the MMA).
+// Weights: with e_t = score_t log2(e) + log2(scale_t), X = floor(max e) over a block of 32 rows and R the column's
+// reference, a weight is held as 2^(e_t - X + 7) < 256 and the block's power is 2^(X - R - 67).  So O and z are relative
+// to 2^(R + 60) in 32-bit floats, each block's weights use all of e4m3's range whatever the others hold, and R, the
+// exponent of the column's first tile, has to move (and O to be rescaled) only when a term exceeds it by 2^100, not
+// whenever a larger one turns up: with one power for all rows, 64 columns' new maxima had every second tile of the
+// first fifty wait for the context product before it and rescale.
+// w_t holds the row scale already: O = sum w_t v_t, z = sum w_t / scale_t.  A row whose scale is below 2^-60 (zeros,
+// subnormal maxima) has score 0 and adds nothing to O: such rows are only counted, and the count enters z at the end.
 //
 // Work: equal shares of (group, tile) units (tree.cuh), one CTA per SM.
-// Warps: 0 = row loads, 1 = scores and TMEM, 2 = the rows' scales, 3 = context products, 4..19 = softmax and output; warp % 4 is a
-// warp's TMEM lane quadrant, its set (0..3) picks 32 of the tile's rows, and a thread holds 16 rows of one column.
-// The query pieces are the score's A operand in TMEM, so shared memory holds rows: five stages of 64 rows (36 KB),
-// two 16 KB weight buffers, the queries' RoPE part (8 KB).  A stage is held from its load through score, softmax and
-// context product; with two stages of 128 rows beside a 72 KB query image that chain set the pace.
-// TMEM: query 128 columns, score 128, context accumulators 4 x 64.
+// Warps: 0 = row loads, 1 = scores and TMEM, 2 = the rows' scales, 3 = context products, 4..19 = softmax and output in
+// two teams that take alternate tiles.  warp % 4 is a warp's TMEM lane quadrant, its set (0, 1) the block of 32 rows,
+// and a thread holds 8 rows of two columns.
+// The query pieces are the score's A operand in TMEM (448 latent bytes) and shared memory (the rest).  Shared memory:
+// five stages of 64 rows (36 KB each), two weight buffers of 8 KB, the query's part 16 KB.
+// TMEM: query 112 columns, scale factors 12, two score buffers of 64, context accumulators 4 x 64.
 // Every wait is bounded in time; one that gives up sets KV8_ERR_TIMEOUT and the CTA winds down.
 #include "sm100.cuh"
 #include "tree.cuh"
@@ -45,26 +47,27 @@ constexpr int kThreads = 128 + 2 * kTeam;
 constexpr uint32_t kBlk = 8192;            // 64 rows x 128 latent bytes (SW128)
 constexpr uint32_t kRope = 4096;           // 64 rows x 64 RoPE bytes (SW64)
 constexpr uint32_t kStage = 4 * kBlk + kRope;
-constexpr uint32_t kQLat = 128 * 512;      // a group's query image: 128 lanes x 512 latent bytes, row-major,
-constexpr uint32_t kQRope = 128 * 64;      // then 128 x 64 RoPE bytes (SW64)
-constexpr uint32_t kImg = kQLat + kQRope;
+constexpr uint32_t kQLat = 128 * 448;      // a group's query image: 128 lanes x 448 latent bytes, row-major,
+constexpr uint32_t kQTail = 128 * 128;     // then 128 x (64 latent + 64 RoPE bytes) (SW128)
+constexpr uint32_t kImg = kQLat + kQTail;
 constexpr uint32_t kW = 8192;              // hi [64 columns][64 rows] (SW64), then lo
-constexpr uint32_t OFF_ST = 0, OFF_W = kStages * kStage, OFF_Q = OFF_W + 2 * kW, OFF_MISC = OFF_Q + kQRope;
-constexpr float kTau = 3.75f;              // the reference moves when a term exceeds it by more than 2^kTau
-constexpr float kUp = 5.0f;                // weights are held times 2^kUp: at most 2^8.75 < 448
-constexpr float kTiny = 7.888609e-31f;     // 2^-100
-constexpr uint32_t TM_Q = 0, TM_S = 128, TM_O = 256;
+constexpr uint32_t OFF_ST = 0, OFF_W = kStages * kStage, OFF_Q = OFF_W + 2 * kW, OFF_MISC = OFF_Q + kQTail;
+constexpr float kRoom = 100.0f;            // the reference moves when a block's exponent exceeds it by more
+constexpr int kBase = 60;                  // O and z are relative to 2^(reference + kBase)
+constexpr float kTiny = 8.6736174e-19f;    // 2^-60
+constexpr uint32_t TM_Q = 0, TM_SFA = 112, TM_SFB = 116, TM_S = 128, TM_O = 256;
 
 struct RowInfo {
-    alignas(16) float scale[kRows];        // 0 for rows that are not there
-    alignas(16) float lg[kRows];           // log2(scale) + kUp
+    alignas(16) float sl[kRows / 2][4];    // for each pair of rows: scales (0 for rows that are not there), log2
     alignas(16) float inv[kRows];          // 1 / scale
-    uint64_t in, zero;                     // rows that are there / whose scale is below 2^-100
+    uint64_t in, zero;                     // rows that are there / whose scale is below 2^-60
+    uint32_t full;                         // all there, none of them zero
 };
 struct Misc {
     RowInfo rows[kStages];
-    alignas(16) float m[kCols];            // running references (log2 units), -inf before any attended row
-    alignas(16) float red[4][kCols];       // maxima of a team's two sets of rows, team by team; at the end sums
+    alignas(16) float ref[kCols];          // the columns' references R (whole numbers), -inf before any attended row
+    alignas(16) float top[2][2][2][kCols]; // X of each block: [team][tile pair][set][column]
+    alignas(16) float red[4][kCols];       // at the end: sums
     alignas(16) float zinv[kCols];         // at the end: 1 / z
     uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_full[2], s_free[2], w_full[2], pv_done[2], q_ready,
         final_bar[2];
@@ -104,6 +107,25 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         : "r"(taddr));
 }
 
+// Block-scaled MMA (e4m3 x e4m3, 32 elements of K): each row of A and of B times a power of two, an exponent byte per
+// row that the instruction descriptor's ids pick from the 32-bit words at `sfa` / `sfb` in TMEM (row r: lane r % 32 of
+// every quadrant, column r / 32).
+__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// Its instruction descriptor: e4m3 A (MN-major) and B (K-major), scale bytes are exponents.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int sfb_id) {
+    return ((uint32_t)sfb_id << 4) | (1u << 15) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void tmem_st_32x32b_x2(uint32_t taddr, uint32_t a, uint32_t b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(a), "r"(b) : "memory");
+}
+
 // Score MMA with A in tensor memory.
 __device__ __forceinline__ void mma_f8f6f4_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate) {
@@ -118,21 +140,29 @@ __device__ __forceinline__ void mma_f8f6f4_ts(uint32_t d_tmem, uint32_t a_tmem, 
 // ready at once would pay every time.  2^32 cycles are two seconds; drains give a shorter limit.
 constexpr long long kLimit = 1ll << 32;
 
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err,
-                                         long long limit = kLimit) {
-    if (mbar_try_wait(bar, parity)) return true;
+// (Out of line: a wait that is not ready at once has time, and the code beside the ready ones stays small.)
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, int *abort_flag, int *err, long long limit) {
     const long long t0 = clock64();
     for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
         if ((i & 31u) == 0) {
-            if (abort_flag && *abort_flag) return false;
+            if (abort_flag && *(volatile int *)abort_flag) return false;
             if (clock64() - t0 > limit) {
-                if (abort_flag) *abort_flag = 1;
+                if (abort_flag) *(volatile int *)abort_flag = 1;
                 if (err) atomicOr(err, (int)KV8_ERR_TIMEOUT);
                 return false;
             }
         }
     }
+}
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, int *abort_flag, int *err, long long limit = kLimit) {
+    return mbar_try_wait(bar, parity) || bar_wait_slow(smem_u32(bar), parity, abort_flag, err, limit);
 }
 
 // True in one lane of a converged warp, the same one every time.
@@ -155,15 +185,18 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint3
     e4m3x2_to_f32((uint16_t)hi, x, y);
     lo = enc_pair(a - x, b - y);
 }
-// Two softmax weights (at most 2^8.75) -> e4m3 pieces and e5m2 pieces of what those leave.  By way of f16, whose 11
-// bits are finer than the 7 that the pieces keep; the residual is exact there.
+// Two softmax weights (at most 2^8) -> e4m3 pieces and e4m3 pieces of what those leave.  By way of f16, whose 11 bits
+// are finer than the 8 that the pieces keep; the residual is exact there.
 __device__ __forceinline__ void split_weights(float a, float b, uint16_t &hi, uint16_t &lo) {
     uint32_t w16, h16, r16;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w16) : "f"(b), "f"(a));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(w16));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(hi));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r16) : "r"(w16), "r"(h16));
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r16));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r16));
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 __device__ __forceinline__ float lg2_approx(float x) {
     float y;
@@ -182,7 +215,7 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
 // ------------------------------------------------------------------------------------------------------------
 // Byte offset of 16-byte chunk ch (32 latent, 4 RoPE) of a lane's query pieces.
 __device__ __forceinline__ uint32_t image_offset(int lane, int ch) {
-    return ch < 32 ? (uint32_t)lane * 512u + ch * 16u : kQLat + sw64_offset(lane, (ch - 32) * 16);
+    return ch < 28 ? (uint32_t)lane * 448u + ch * 16u : kQLat + sw128_offset(lane, (ch - 28) * 16);
 }
 
 constexpr int kPrepCols = 8, kPrepThreads = kPrepCols * 36;
@@ -380,10 +413,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Scores and context products have a warp each: the tensor core's queue takes a few MMAs only, so the hundreds
         // of cycles that an issuer spends on its waits are the core's idle time unless another one issues meanwhile.
         const uint32_t id_s = idesc_e4m3_f32(128, kRows, false, false);
-        // descriptors of stage 0 and of the query's RoPE part: an offset adds to the address field
+        // descriptors of stage 0 and of the query's part in shared memory: an offset adds to the address field
         const uint64_t k_desc = smem_desc(sbase + OFF_ST, 0, 1024, kSw128);
         const uint64_t kr_desc = smem_desc(sbase + OFF_ST + 4 * kBlk, 0, 512, kSw64);
-        const uint64_t qr_desc = smem_desc(sbase + OFF_Q, 0, 512, kSw64);
+        const uint64_t q_desc = smem_desc(sbase + OFF_Q, 0, 1024, kSw128);
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok) ok = bar_wait(bar, parity, &ms.abort_flag, a.err_word);
@@ -402,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t d = tmem + TM_S + 64u * (j & 1);
                     const uint64_t k = k_desc + (uint64_t)(s * (kStage >> 4)), kr = kr_desc + (uint64_t)(s * (kStage >> 4));
 #pragma unroll
-                    for (int kb = 0; kb < 4; ++kb)
+                    for (int kk = 0; kk < 14; ++kk)
+                        mma_f8f6f4_ts(d, tmem + TM_Q + kk * 8, k + (uint64_t)(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4), id_s, kk != 0);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f8f6f4_ts(d, tmem + TM_Q + kb * 32 + kk * 8, k + (uint64_t)((kb * kBlk + kk * 32) >> 4), id_s, (kb | kk) != 0);
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) mma_f8f6f4(d, qr_desc + (uint64_t)(kk * 2), kr + (uint64_t)(kk * 2), id_s, 1u);
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8f6f4(d, q_desc + (uint64_t)(kk * 2), kk < 2 ? k + (uint64_t)((3 * kBlk + 64 + kk * 32) >> 4) : kr + (uint64_t)((kk - 2) * 2),
+                                   id_s, 1u);
                     mma_commit(&ms.s_full[j & 1]);
                 }
                 __syncwarp();
@@ -423,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 3) {
         // ================================ context products ================================
-        const uint32_t id_hi = idesc_e4m3_f32(128, kCols, true, false), id_lo = id_hi | (1u << 10);  // B in e5m2
         const uint64_t v_desc = smem_desc(sbase + OFF_ST, 0, 1024, kSw128);  // (the score's bytes, MN-major)
         const uint64_t w_desc = smem_desc(sbase + OFF_W, 0, 512, kSw64);
         bool ok = true;
@@ -447,8 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < 2; ++kk) {
                             const uint64_t av = v + (uint64_t)((ch * kBlk + kk * 4096) >> 4);
-                            mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kk * 32) >> 4), id_hi, kk ? 1u : keep);
-                            mma_f8f6f4(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kW / 2 + kk * 32) >> 4), id_lo, 1u);
+                            const uint32_t sfb = tmem + TM_SFB + 4u * (i & 1);
+                            mma_mxf8(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kk * 32) >> 4), idesc_mxf8(128, kCols, kk), tmem + TM_SFA,
+                                     sfb, kk ? 1u : keep);
+                            mma_mxf8(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kW / 2 + kk * 32) >> 4), idesc_mxf8(128, kCols, kk),
+                                     tmem + TM_SFA, sfb, 1u);
                         }
                     mma_commit(&ms.kv_free[s]);
                     mma_commit(&ms.pv_done[i & 1]);
@@ -502,8 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool there = row[2 * v + k] >= 0;
                         in[k] = __ballot_sync(0xffffffffu, there);
                         zero[k] = __ballot_sync(0xffffffffu, there && c < kTiny);
-                        ri.scale[32 * k + lane] = c;
-                        ri.lg[32 * k + lane] = lg2_approx(c) + kUp;
+                        float *sl = &ri.sl[16 * k + (lane >> 1)][lane & 1];
+                        sl[0] = c;
+                        sl[2] = lg2_approx(c);
                         // 0 for a zero row (its weight is 0) and for a scale that is not finite (its weight is NaN
                         // where it is attended)
                         ri.inv[32 * k + lane] = c >= kTiny && c <= 3.402823466e38f ? __fdividef(1.f, c) : 0.f;
@@ -511,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         ri.in = in[0] | (uint64_t)in[1] << 32;
                         ri.zero = zero[0] | (uint64_t)zero[1] << 32;
+                        ri.full = (in[0] & in[1]) == 0xffffffffu && (zero[0] | zero[1]) == 0;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.row_full[s]);
@@ -521,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad_page && a.err_word) atomicOr(a.err_word, (int)KV8_ERR_INDEX);
     } else {
         // ============================ softmax and output ============================
-        // A wait that gives up clears `ok` (the same in a warp's lanes: TMEM accesses need all of them); the warp
-        // then skips its remaining waits but still reaches every named barrier, so that no other warp waits for it.
+        // After a wait that gave up (`ok` false) a thread skips its remaining waits but still reaches every named
+        // barrier, so that no other warp waits for it.
         const int st = tid - 128;                     // 0..511
         const int q = warp & 3, w16 = (warp - 4) >> 2;
         const int team = w16 >> 1, set = w16 & 1;     // tiles of the team's parity; rows 32 set .. 32 set + 31 of them
@@ -532,228 +569,242 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_a = 16 * q + (lane >> 2), n_b = n_a + 8;
         const int r0 = 32 * set + 2 * (lane & 3);     // its first row
         const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+        const uint32_t s_addr = tmem + lane_addr + TM_S + 64u * team + 32u * set;
+        const uint32_t o_addr = tmem + lane_addr + TM_O;
         const int team_bar = 2 + team;                // the team's own barrier
+        // where its weights go: rows r0 + 8 i of column a are at w_addr[i / 2] + 8 (i % 2), column b's 512 bytes on
+        const uint32_t w_base = sbase + OFF_W + team * kW;
+        const uint32_t w_addr[2] = {w_base + sw64_offset(n_a, r0), w_base + sw64_offset(n_a, r0 + 16)};
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, &ms.abort_flag, a.err_word));
+            if (ok) ok = bar_wait(bar, parity, &ms.abort_flag, a.err_word);
         };
         grid_launch_dependents();
-        int it = 0, s = 0;  // tiles and stages, the other team's included
-        uint32_t s_ph = 0;
-        while (walk.next<kCols, kRows>(a, seg)) {
-            const int64_t slot = tree_slot(seg.q.q0, a.H, seg.b) + seg.g;
-            // ---- the group's queries: 128 latent bytes of this thread's lane to TMEM, one RoPE chunk to shared memory.
-            // (The scores of the segment before are complete: its last one was read before the output's barriers.)
-            {
-                const uint8_t *img = x.img + slot * kImg;
-                const uint4 *src = reinterpret_cast<const uint4 *>(img + (32 * q + lane) * 512 + w16 * 128);
-                uint4 v[8];
+        // a group's queries: 128 (the last set's: 64) latent bytes of this thread's lane, two chunks of the part in shared
+        // memory, two columns' factors
+        uint4 qv[8], qt[2];
+        float c_a = 0.f, c_b = 0.f;
+        auto fetch_queries = [&](const TreeSegment &g) {
+            const int64_t slot = tree_slot(g.q.q0, a.H, g.b) + g.g;
+            const uint8_t *img = x.img + slot * kImg;
+            const uint4 *src = reinterpret_cast<const uint4 *>(img + (32 * q + lane) * 448 + w16 * 128);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = __ldg(src + k);
-                const uint4 rp = __ldg(reinterpret_cast<const uint4 *>(img + kQLat) + st);
+            for (int k = 0; k < 8; ++k)
+                if (k < 4 || w16 < 3) qv[k] = __ldg(src + k);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t w[16] = {v[4 * k].x,     v[4 * k].y,     v[4 * k].z,     v[4 * k].w,
-                                            v[4 * k + 1].x, v[4 * k + 1].y, v[4 * k + 1].z, v[4 * k + 1].w,
-                                            v[4 * k + 2].x, v[4 * k + 2].y, v[4 * k + 2].z, v[4 * k + 2].w,
-                                            v[4 * k + 3].x, v[4 * k + 3].y, v[4 * k + 3].z, v[4 * k + 3].w};
-                    tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + w16 * 32 + 16 * k, w);
-                }
-                *reinterpret_cast<uint4 *>(smem + OFF_Q + st * 16) = rp;
-                if (st < kCols) ms.m[st] = -INFINITY;
-                tmem_wait_st();
-                fence_proxy_async_smem();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.q_ready);
+            for (int k = 0; k < 2; ++k) qt[k] = __ldg(reinterpret_cast<const uint4 *>(img + kQLat) + 512 * k + st);
+            c_a = __ldg(x.c_head + slot * kCols + n_a);
+            c_b = __ldg(x.c_head + slot * kCols + n_b);
+        };
+        auto store_queries = [&]() {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t w[16] = {qv[4 * k].x,     qv[4 * k].y,     qv[4 * k].z,     qv[4 * k].w,
+                                        qv[4 * k + 1].x, qv[4 * k + 1].y, qv[4 * k + 1].z, qv[4 * k + 1].w,
+                                        qv[4 * k + 2].x, qv[4 * k + 2].y, qv[4 * k + 2].z, qv[4 * k + 2].w,
+                                        qv[4 * k + 3].x, qv[4 * k + 3].y, qv[4 * k + 3].z, qv[4 * k + 3].w};
+                if (k == 0 || w16 < 3) tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + w16 * 32 + 16 * k, w);
             }
-            named_sync(1, 2 * kTeam);
-            const float c_a = __ldg(x.c_head + slot * kCols + n_a), c_b = __ldg(x.c_head + slot * kCols + n_b);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4 *>(smem + OFF_Q + (512 * k + st) * 16) = qt[k];
+            tmem_wait_st();
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.q_ready);
+        };
+        // the value rows' factors are all 1
+        if (w16 == 0) {
+            tmem_st_32x32b_x2(tmem + lane_addr + TM_SFA, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            tmem_st_32x32b_x2(tmem + lane_addr + TM_SFA + 2, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            tmem_wait_st();
+        }
+        bool more = walk.next<kCols, kRows>(a, seg);
+        if (more) {
+            fetch_queries(seg);
+            store_queries();
+        }
+        if (st < kCols) ms.ref[st] = -INFINITY;
+        named_sync(1, 2 * kTeam);
+        int it0 = 0;  // tiles before the segment
+        while (more) {
             const int top = seg.q.n * a.H;
-            float m_a = -INFINITY, m_b = -INFINITY;             // the references that z is relative to: the team's last
+            const int tiles = seg.t1 - seg.t0;
+            float ref_a = -INFINITY, ref_b = -INFINITY;         // the references that z is relative to: the team's last
             uint64_t z_a = f2_pack(0.f, 0.f), z_b = f2_pack(0.f, 0.f);
             int zero_a = 0, zero_b = 0;                         // zero rows that the columns attend among this thread's
-            for (int t = seg.t0; t < seg.t1; ++t, ++it) {
-                const bool mine = (it & 1) == team;
-                const int s_now = s;
-                const uint32_t ph_now = s_ph;
-                if (++s == kStages) {
-                    s = 0;
-                    s_ph ^= 1;
-                }
-                if (!mine) continue;
-                const int64_t p0 = (int64_t)t * kRows;
+            const uint64_t ca = f2_pack(c_a, c_a), cb = f2_pack(c_b, c_b);
+            const int ctx_tiles = (int)(seg.q.len / kRows);     // tiles of context only
+            for (int u = (it0 ^ team) & 1; u < tiles; u += 2) {
+                const int it = it0 + u, t = seg.t0 + u;
+                const uint32_t s_now = (uint32_t)it % kStages, ph_now = ((uint32_t)it / kStages) & 1u, half_ph = ((uint32_t)it >> 1) & 1u;
                 // ---- scores
-                wait(&ms.s_full[team], (it >> 1) & 1);
+                wait(&ms.s_full[team], half_ph);
                 tc_fence_after_sync();
                 uint32_t hi[16], lo[16];
-                tmem_ld_16x256b_x4(tmem + lane_addr + TM_S + 64u * team + 32u * set, hi);
-                tmem_ld_16x256b_x4(tmem + lane_addr + (16u << 16) + TM_S + 64u * team + 32u * set, lo);
-                // meanwhile the rows' figures, and which rows the columns attend (bit 2 i + k: row r0 + 8 i + k)
+                tmem_ld_16x256b_x4(s_addr, hi);
+                tmem_ld_16x256b_x4(s_addr + (16u << 16), lo);
                 wait(&ms.row_full[s_now], ph_now);
                 const RowInfo &ri = ms.rows[s_now];
-                const uint64_t in = ri.in;
-                const bool drafted = p0 + kRows > seg.q.len;
-                const bool plain = !drafted && in == ~(uint64_t)0 && ri.zero == 0;  // every column attends every row
-                uint32_t on_a = 0xFFu, on_b = 0xFFu;
-                if (!plain) {
-                    on_a = on_b = 0;
-                    const int c0 = seg.g * kCols, node_a = min(c0 + n_a, top - 1) / a.H, node_b = min(c0 + n_b, top - 1) / a.H;
-#pragma unroll 1
-                    for (int u = 0; u < 8; ++u) {
-                        const int r = r0 + 8 * (u >> 1) + (u & 1);
-                        if (!(in >> r & 1)) continue;
-                        const int64_t draft = p0 + r - seg.q.len;  // the row's index in the draft
-                        const bool sa = draft < 0 || tree_sees(a, seg.q.q0, node_a, (int)draft);
-                        const bool sb = draft < 0 || tree_sees(a, seg.q.q0, node_b, (int)draft);
-                        if (ri.zero >> r & 1) {
-                            zero_a += sa;
-                            zero_b += sb;
-                        } else {
-                            on_a |= (uint32_t)sa << u;
-                            on_b |= (uint32_t)sb << u;
-                        }
-                    }
-                }
+                float4 sl[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sl[i] = *reinterpret_cast<const float4 *>(&ri.sl[(r0 >> 1) + 4 * i][0]);
+                const bool plain = t < ctx_tiles && ri.full;  // every column attends every row
                 tmem_wait_ld();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.s_free[team]);
-                // ---- e + 5, row pairs packed: 0..3 of column a, 4..7 of column b
+                // ---- e, row pairs packed: 0..3 of column a, 4..7 of column b
                 uint64_t d2[8];
-                float max_a = -INFINITY, max_b = -INFINITY;
-                {
-                    const uint64_t ca = f2_pack(c_a, c_a), cb = f2_pack(c_b, c_b);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 sc = *reinterpret_cast<const float2 *>(&ri.scale[r0 + 8 * i]);
-                        const float2 lg = *reinterpret_cast<const float2 *>(&ri.lg[r0 + 8 * i]);
-                        const uint64_t sc2 = f2_pack(sc.x, sc.y), lg2 = f2_pack(lg.x, lg.y);
-                        const uint64_t sa = f2_add(f2_pack(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
-                                                   f2_pack(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])));
-                        const uint64_t sb = f2_add(f2_pack(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])),
-                                                   f2_pack(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])));
-                        d2[i] = f2_fma(sa, f2_mul(sc2, ca), lg2);
-                        d2[4 + i] = f2_fma(sb, f2_mul(sc2, cb), lg2);
-                    }
-                    if (!plain) {
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t sc2 = f2_pack(sl[i].x, sl[i].y), lg2 = f2_pack(sl[i].z, sl[i].w);
+                    const uint64_t sa = f2_add(f2_pack(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
+                                               f2_pack(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])));
+                    const uint64_t sb = f2_add(f2_pack(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])),
+                                               f2_pack(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])));
+                    d2[i] = f2_fma(sa, f2_mul(sc2, ca), lg2);
+                    d2[4 + i] = f2_fma(sb, f2_mul(sc2, cb), lg2);
+                }
+                if (!plain) {
+                    // the rows that the columns attend: those that are there, of the draft those of their masks
+                    const uint64_t in = ri.in, zr = ri.zero;
+                    const int64_t j0 = (int64_t)t * kRows - seg.q.len;  // the tile's first row's index in the draft
+                    const int c0 = seg.g * kCols;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t att = in & tree_attended(a, seg.q.q0, min(c0 + (h ? n_b : n_a), top - 1) / a.H, j0);
+                        (h ? zero_b : zero_a) += __popcll(att & zr & (0x03030303ull << r0));
+                        const uint32_t on = (uint32_t)((att & ~zr) >> r0);  // bits 8 i and 8 i + 1
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float u, v;
-                            f2_unpack(d2[i], u, v);
-                            d2[i] = f2_pack(on_a >> (2 * i) & 1 ? u : -INFINITY, on_a >> (2 * i + 1) & 1 ? v : -INFINITY);
-                            f2_unpack(d2[4 + i], u, v);
-                            d2[4 + i] = f2_pack(on_b >> (2 * i) & 1 ? u : -INFINITY, on_b >> (2 * i + 1) & 1 ? v : -INFINITY);
+                            float e0, e1;
+                            f2_unpack(d2[4 * h + i], e0, e1);
+                            d2[4 * h + i] = f2_pack(on >> (8 * i) & 1 ? e0 : -INFINITY, on >> (8 * i + 1) & 1 ? e1 : -INFINITY);
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float u, v;
-                        f2_unpack(d2[i], u, v);
-                        max_a = fmaxf(max_a, fmaxf(u, v));
-                        f2_unpack(d2[4 + i], u, v);
-                        max_b = fmaxf(max_b, fmaxf(u, v));
-                    }
                 }
-                // ---- the references, tile after tile: the other team has decided on the tile before.  They move
-                // together when a term exceeds one by more than kTau, or a column that has none meets its first row.
-                if (t > seg.t0) named_sync(4 + (team ^ 1), 2 * kTeam);
-                float na = ms.m[n_a], nb = ms.m[n_b];
-                const float m_c = ms.m[32 * set + lane];  // of the accumulator columns that this warp rescales
-                const bool slow = bar_red_or(team_bar, kTeam, max_a > na + (kTau + kUp) || max_b > nb + (kTau + kUp));
-                float move = 1.f;                         // that column's factor
+                float max_a = -INFINITY, max_b = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float e0, e1;
+                    f2_unpack(d2[i], e0, e1);
+                    max_a = fmaxf(max_a, fmaxf(e0, e1));
+                    f2_unpack(d2[4 + i], e0, e1);
+                    max_b = fmaxf(max_b, fmaxf(e0, e1));
+                }
+                // ---- X = floor(max e) of the block: over the column's four lanes
+                max_a = fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 1));
+                max_b = fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 1));
+                max_a = floorf(fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 2)));
+                max_b = floorf(fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 2)));
+                float(*const tops)[kCols] = ms.top[team][half_ph];
+                if ((lane & 3) == 0) {
+                    tops[set][n_a] = max_a;
+                    tops[set][n_b] = max_b;
+                }
+                // ---- the references, tile after tile: the other team has decided on the tile before.  (The barrier also
+                // hands the blocks' exponents to the warps that write the scale factors.)
+                if (u > 0) named_sync(4 + (team ^ 1), 2 * kTeam);
+                float na = ms.ref[n_a], nb = ms.ref[n_b];
+                const bool slow = bar_red_or(team_bar, kTeam, max_a > na + kRoom || max_b > nb + kRoom);
+                auto moved = [&](int n, float r) -> float {  // a column's reference r from this tile on
+                    const float x = fmaxf(tops[0][n], tops[1][n]);
+                    return slow && x > r + kRoom ? x : r;
+                };
+                float rl = 0.f, rh = 0.f;  // of the columns whose factors this lane writes
+                if (set == 0) {
+                    rl = moved(lane, ms.ref[lane]);
+                    rh = moved(32 + lane, ms.ref[32 + lane]);
+                }
+                float move = 1.f;          // the factor of the accumulator column 32 set + lane
                 if (slow) {
-                    max_a = fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 1));
-                    max_b = fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 1));
-                    max_a = fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 2));
-                    max_b = fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 2));
-                    if ((lane & 3) == 0) {
-                        ms.red[w16][n_a] = max_a;
-                        ms.red[w16][n_b] = max_b;
-                    }
-                    named_sync(team_bar, kTeam);
-                    auto moved = [&](int n, float m) -> float {
-                        const float top_e = fmaxf(ms.red[2 * team][n], ms.red[2 * team + 1][n]) - kUp;
-                        return top_e > m + kTau ? top_e : m;
-                    };
                     na = moved(n_a, na);
                     nb = moved(n_b, nb);
-                    const float nc = moved(32 * set + lane, m_c);
-                    if (q == 0) ms.m[32 * set + lane] = nc;  // (all have read the old ones)
-                    move = m_c == -INFINITY || nc == m_c ? 1.f : ex2_approx(m_c - nc);
+                    const float r = ms.ref[32 * set + lane], rn = moved(32 * set + lane, r);
+                    move = r == -INFINITY || rn == r ? 1.f : ex2_approx(r - rn);
+                    named_sync(team_bar, kTeam);
+                    if (q == 0) ms.ref[32 * set + lane] = rn;  // (all have read the old ones)
                 }
-                if (t + 1 < seg.t1) named_arrive(4 + team, 2 * kTeam);
-                if (m_a != na || m_b != nb) {  // z, relative to the team's last references, to these
-                    const float fa = m_a == -INFINITY || m_a == na ? 1.f : ex2_approx(m_a - na);
-                    const float fb = m_b == -INFINITY || m_b == nb ? 1.f : ex2_approx(m_b - nb);
+                if (u + 1 < tiles) named_arrive(4 + team, 2 * kTeam);
+                if (ref_a != na || ref_b != nb) {  // z, relative to the team's last references, to these
+                    const float fa = ref_a == -INFINITY || ref_a == na ? 1.f : ex2_approx(ref_a - na);
+                    const float fb = ref_b == -INFINITY || ref_b == nb ? 1.f : ex2_approx(ref_b - nb);
                     z_a = f2_mul(z_a, f2_pack(fa, fa));
                     z_b = f2_mul(z_b, f2_pack(fb, fb));
-                    m_a = na;
-                    m_b = nb;
+                    ref_a = na;
+                    ref_b = nb;
                 }
-                // the context product of the team's tile before has read this weight buffer
-                if (it >= 2) wait(&ms.pv_done[team], ((it >> 1) - 1) & 1);
-                // ---- weights 2^(e + 5 - m)
+                // a block's factor 2^(byte - 127), byte = X - R + 60, at least 1: weights of a block that lies 2^59 below
+                // the reference are that much smaller instead
+                auto factor = [](float x, float r) -> uint32_t { return (uint32_t)fminf(fmaxf(x - r + (float)kBase, 1.f), 254.f); };
+                const uint32_t byte_a = factor(max_a, na), byte_b = factor(max_b, nb);
+                // the context product of the team's tile before has read this weight buffer and its factors
+                if (it >= 2) wait(&ms.pv_done[team], half_ph ^ 1u);
+                if (set == 0) {
+                    tc_fence_after_sync();
+                    tmem_st_32x32b_x2(tmem + lane_addr + TM_SFB + 4u * team, factor(tops[0][lane], rl) | factor(tops[1][lane], rl) << 8,
+                                      factor(tops[0][32 + lane], rh) | factor(tops[1][32 + lane], rh) << 8);
+                }
+                // ---- weights 2^(e - X + 7)
                 {
-                    const float ref_a = m_a == -INFINITY ? 0.f : -m_a, ref_b = m_b == -INFINITY ? 0.f : -m_b;
-                    const uint64_t ra = f2_pack(ref_a, ref_a), rb = f2_pack(ref_b, ref_b);
-                    uint8_t *const wb = smem + OFF_W + team * kW;
+                    // (nothing attended so far: e is -inf throughout, whatever is subtracted)
+                    const float xa = na == -INFINITY ? 7.f : (float)(kBase + 7) - na - (float)byte_a;
+                    const float xb = nb == -INFINITY ? 7.f : (float)(kBase + 7) - nb - (float)byte_b;
+                    const uint64_t ra = f2_pack(xa, xa), rb = f2_pack(xb, xb);
+                    uint64_t za = f2_pack(0.f, 0.f), zb = za;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 inv = *reinterpret_cast<const float2 *>(&ri.inv[r0 + 8 * i]);
                         const uint64_t inv2 = f2_pack(inv.x, inv.y);
-                        float u, v, x0, x1, y0, y1;
-                        f2_unpack(f2_add(d2[i], ra), u, v);
-                        x0 = ex2_approx(u);
-                        x1 = ex2_approx(v);
-                        f2_unpack(f2_add(d2[4 + i], rb), u, v);
-                        y0 = ex2_approx(u);
-                        y1 = ex2_approx(v);
-                        z_a = f2_fma(f2_pack(x0, x1), inv2, z_a);
-                        z_b = f2_fma(f2_pack(y0, y1), inv2, z_b);
+                        float e0, e1, x0, x1, y0, y1;
+                        f2_unpack(f2_add(d2[i], ra), e0, e1);
+                        x0 = ex2_approx(e0);
+                        x1 = ex2_approx(e1);
+                        f2_unpack(f2_add(d2[4 + i], rb), e0, e1);
+                        y0 = ex2_approx(e0);
+                        y1 = ex2_approx(e1);
+                        za = f2_fma(f2_pack(x0, x1), inv2, za);
+                        zb = f2_fma(f2_pack(y0, y1), inv2, zb);
                         uint16_t wh, wl;
+                        const uint32_t p = w_addr[i >> 1] + 8 * (i & 1);
                         split_weights(x0, x1, wh, wl);
-                        uint8_t *p = wb + sw64_offset(n_a, r0 + 8 * i);
-                        *reinterpret_cast<uint16_t *>(p) = wh;
-                        *reinterpret_cast<uint16_t *>(p + kW / 2) = wl;
+                        st_shared_u16(p, wh);
+                        st_shared_u16(p + kW / 2, wl);
                         split_weights(y0, y1, wh, wl);
-                        p = wb + sw64_offset(n_b, r0 + 8 * i);
-                        *reinterpret_cast<uint16_t *>(p) = wh;
-                        *reinterpret_cast<uint16_t *>(p + kW / 2) = wl;
+                        st_shared_u16(p + 512, wh);
+                        st_shared_u16(p + 512 + kW / 2, wl);
                     }
+                    const float fa = __uint_as_float(byte_a << 23), fb = __uint_as_float(byte_b << 23);
+                    z_a = f2_fma(za, f2_pack(fa, fa), z_a);
+                    z_b = f2_fma(zb, f2_pack(fb, fb), z_b);
                 }
                 // ---- rows that were not loaded, and NaN codes of drafted rows (attended columns have NaN weights
                 // already): a weight of 0 must not meet them.  A thread owns a row's 128 bytes of a latent block.
-                if (drafted || in != ~(uint64_t)0) {
+                if (!plain) {
                     const int r = st & 63;
-                    const bool there = in >> r & 1;
-                    if (!there || p0 + r >= seg.q.len) {
+                    const bool there = ri.in >> r & 1;
+                    if (!there || (int64_t)t * kRows + r >= seg.q.len) {
                         // (complete since before the score: this makes the copy's bytes visible here too)
                         (void)bar_wait(&ms.kv_full[s_now], ph_now, &ms.abort_flag, a.err_word);
                         uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s_now * kStage + ((st >> 6) & 3) * kBlk + r * 128);
-#pragma unroll 1
-                        for (int k = 0; k < 8; ++k) {
-                            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                            if (there) {
-                                u = p[k];
-                                u.x = without_nan(u.x);
-                                u.y = without_nan(u.y);
-                                u.z = without_nan(u.z);
-                                u.w = without_nan(u.w);
-                            }
-                            p[k] = u;
-                        }
+                        uint4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = there ? p[k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            p[k] = make_uint4(without_nan(v[k].x), without_nan(v[k].y), without_nan(v[k].z), without_nan(v[k].w));
                     }
                 }
-                if (slow && t > seg.t0 && __any_sync(0xffffffffu, move != 1.f)) {
+                if (slow && u > 0 && __any_sync(0xffffffffu, move != 1.f)) {
                     // this warp's part of the accumulators, 32 columns by 32 dims of each block, where a column moved,
                     // once the context product before is complete.  (The one before that is: the wait above.)
-                    wait(&ms.pv_done[team ^ 1], ((it - 1) >> 1) & 1);
+                    wait(&ms.pv_done[team ^ 1], ((uint32_t)(it - 1) >> 1) & 1u);
                     tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         if (!__any_sync(0xffffffffu, (lane >> 4) == h && move != 1.f)) continue;
-                        const uint32_t at = tmem + lane_addr + TM_O + 32u * set + 16u * h;
+                        const uint32_t at = o_addr + 32u * set + 16u * h;
 #pragma unroll 1
                         for (int c = 0; c < 4; c += 2) {
                             uint32_t o[2][16];
@@ -772,44 +823,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_wait_st();
                 }
+                if (set == 0) tmem_wait_st();
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.w_full[team]);
             }
+            it0 += tiles;
 
-            // ---- output: sums over a column's threads, four lanes of each set
-            const int c0 = seg.g * kCols, nc = min(kCols, top - c0);
-            const bool whole = seg.first && seg.last;
-            float *part = a.part + ((int64_t)blockIdx.x * 2 + (seg.first ? 1 : 0)) * tree_part_floats(kCols);
-            // returns the sum for column st (threads st < 64)
-            auto over_sets = [&](float u, float v) -> float {
+            // ---- output, and the next segment's queries: after the first barrier every score of this one is read
+            const TreeSegment done = seg;
+            more = walk.next<kCols, kRows>(a, seg);
+            if (more) fetch_queries(seg);
+            const int c0 = done.g * kCols, nc = min(kCols, top - c0);
+            const bool whole = done.first && done.last;
+            float *part = a.part + ((int64_t)blockIdx.x * 2 + (done.first ? 1 : 0)) * tree_part_floats(kCols);
+            // sums over a column's threads, four lanes of each set
+            auto to_sets = [&](float u, float v) {
                 u += __shfl_xor_sync(0xffffffffu, u, 1);
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
                 u += __shfl_xor_sync(0xffffffffu, u, 2);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
-                named_sync(1, 2 * kTeam);  // red's readers before this are done
                 if ((lane & 3) == 0) {
                     ms.red[w16][n_a] = u;
                     ms.red[w16][n_b] = v;
                 }
-                named_sync(1, 2 * kTeam);
-                const int n = st & (kCols - 1);
-                return ms.red[0][n] + ms.red[1][n] + ms.red[2][n] + ms.red[3][n];
             };
-            const float nn = over_sets((float)zero_a, (float)zero_b) * exp2f(kUp);
-            float zz;
+            auto over_sets = [&](int n) -> float { return ms.red[0][n] + ms.red[1][n] + ms.red[2][n] + ms.red[3][n]; };
+            float nn = 0.f;
+            if (bar_red_or(1, 2 * kTeam, (zero_a | zero_b) != 0)) {
+                to_sets((float)zero_a, (float)zero_b);
+                named_sync(1, 2 * kTeam);
+                nn = over_sets(st & (kCols - 1)) * exp2f(-(float)kBase);
+                named_sync(1, 2 * kTeam);
+            }
             {
-                const float ea = ms.m[n_a], eb = ms.m[n_b];  // (the barriers above: both teams' last)
-                float u, v, fa = m_a == -INFINITY ? 1.f : ex2_approx(m_a - ea), fb = m_b == -INFINITY ? 1.f : ex2_approx(m_b - eb);
+                const float ea = ms.ref[n_a], eb = ms.ref[n_b];  // both teams' last
+                float u, v, fa = ref_a == -INFINITY ? 1.f : ex2_approx(ref_a - ea), fb = ref_b == -INFINITY ? 1.f : ex2_approx(ref_b - eb);
                 f2_unpack(z_a, u, v);
                 fa *= u + v;
                 f2_unpack(z_b, u, v);
                 fb *= u + v;
-                zz = over_sets(fa, fb);
+                to_sets(fa, fb);
             }
+            if (more) store_queries();
+            named_sync(1, 2 * kTeam);
             if (st < kCols) {
-                const float m_end = ms.m[st];
+                const float m_end = ms.ref[st], zz = over_sets(st);
+                ms.ref[st] = -INFINITY;
                 // nothing but zero rows: the accumulators are 0 and stay so
                 const float all = nn == 0.f ? zz : zz + nn * exp2f(m_end == -INFINITY ? 0.f : -m_end);
                 ms.zinv[st] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
@@ -819,16 +880,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     part[kCols * (kKL + 2) + st] = nn;
                 }
             }
-            wait(&ms.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+            wait(&ms.pv_done[(it0 - 1) & 1], ((uint32_t)(it0 - 1) >> 1) & 1u);
             tc_fence_after_sync();
             named_sync(1, 2 * kTeam);
             const int h0 = 16 * w16;  // columns h0 .. h0 + 15
-            if (ok) {
+            const bool odd = lane & 1;
+            if (__all_sync(0xffffffffu, ok)) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     // thread: dim 128 c + 32 q + lane of columns h0 .. h0 + 15
                     uint32_t o[16];
-                    tmem_ld_32x32b_x16(tmem + lane_addr + TM_O + 64u * c + (uint32_t)h0, o);
+                    tmem_ld_32x32b_x16(o_addr + 64u * c + (uint32_t)h0, o);
                     tmem_wait_ld();
                     const int d = 128 * c + 32 * q + lane;
                     float v[16];
@@ -840,31 +902,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         v[4 * k + 2] = __uint_as_float(o[4 * k + 2]) * a4.z;
                         v[4 * k + 3] = __uint_as_float(o[4 * k + 3]) * a4.w;
                     }
-                    if (!whole) {
+                    if (!whole || !a.out_bf16) {
+                        float *dst = (whole ? static_cast<float *>(a.out) + ((int64_t)done.q.q0 * a.H + c0) * kKL : part) + h0 * kKL + d;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (h0 + j < nc) part[(h0 + j) * kKL + d] = v[j];
-                    } else if (a.out_bf16) {
+                            if (h0 + j < nc) dst[j * kKL] = v[j];
+                    } else {
                         // even lanes store column j, odd lanes column j + 1: two dims each
-                        const bool odd = lane & 1;
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)done.q.q0 * a.H + c0 + h0 + odd) * kKL + (d & ~1);
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-                            const __nv_bfloat162 pk = odd ? __floats2bfloat162_rn(other, v[j + 1]) : __floats2bfloat162_rn(v[j], other);
-                            const int cj = h0 + j + (odd ? 1 : 0);
-                            if (cj < nc)
-                                *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                                    ((int64_t)seg.q.q0 * a.H + c0 + cj) * kKL + (d & ~1)) = pk;
+                            if (h0 + j + odd < nc)
+                                *reinterpret_cast<__nv_bfloat162 *>(dst + j * kKL) =
+                                    odd ? __floats2bfloat162_rn(other, v[j + 1]) : __floats2bfloat162_rn(v[j], other);
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (h0 + j < nc)
-                                static_cast<float *>(a.out)[((int64_t)seg.q.q0 * a.H + c0 + h0 + j) * kKL + d] = v[j];
                     }
                 }
             }
-            tc_fence_before_sync();  // the accumulators' reads come before the next segment's first weights
+            tc_fence_before_sync();  // the accumulators are read before the next segment's first product
+            named_sync(1, 2 * kTeam);
         }
     }
     tc_fence_before_sync();

@@ -93,6 +93,26 @@ __device__ __forceinline__ bool tree_sees(const TreeArgs &a, int q0, int i, int 
     return (__ldg(a.mask + (int64_t)(q0 + i) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u;
 }
 
+// The rows of a 64-row tile that drafted token i attends (bit r: row r), where the tile's first row is the draft's
+// row j0 (negative: a row of the context; all of those count).
+__device__ __forceinline__ uint64_t tree_attended(const TreeArgs &a, int q0, int i, int64_t j0) {
+    if (j0 <= -64) return ~(uint64_t)0;
+    if (j0 >= KV8_MAX_TREE) return 0;
+    const int skip = j0 < 0 ? (int)-j0 : 0, j = j0 < 0 ? 0 : (int)j0;  // rows of context, then draft from j on
+    uint64_t bits;
+    if (!a.mask) {
+        const int n = i - j + 1;
+        bits = n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1;
+    } else {
+        const uint32_t *m = a.mask + (int64_t)(q0 + i) * a.mask_words;
+        uint32_t w[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) w[k] = (j >> 5) + k < a.mask_words ? __ldg(m + (j >> 5) + k) : 0u;
+        bits = __funnelshift_r(w[0], w[1], j & 31) | (uint64_t)__funnelshift_r(w[1], w[2], j & 31) << 32;
+    }
+    return skip ? bits << skip | (((uint64_t)1 << skip) - 1) : bits;
+}
+
 // One block: the shares and the cut groups.  `scan`: 66 * 8 bytes of shared memory.
 template <int kCols, int kRows, int kSegment>
 __device__ void tree_schedule(const TreeArgs &a, int64_t *scan) {

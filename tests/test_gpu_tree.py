@@ -250,7 +250,7 @@ def test_one_token_each_agrees_with_the_batched_decode(lib, oracle):
                                  i32([x + 1 for x in lens]), SM, ws, out)
     other = out.double().cpu().numpy()
     assert err == 0
-    # each is within 2^-7 of the same value, in the mean over weights far less: their difference within that
+    # each is within 2^-8 or so of the same value: their difference within twice that
     assert np.linalg.norm(got - other) <= 2.0 ** -7 * np.linalg.norm(other)
 
 
@@ -331,9 +331,30 @@ def test_many_small_terms_beside_a_large_one(lib, q_dtype):
     p = np.exp(SM * q[0, 0, 1])
     got, err = run_tree(lib, q, q_dtype, F32, [1], [T], None, kv8, scale, np.arange(T // page + 1)[None], page)
     assert err == 0
-    # a weight of 2^(6 - 17): hi takes a whole number of 2^-9, lo the rest to 2^-3; the large one to 2^-7
-    assert np.abs(got[0, :, 0] - 1).max() <= 0.5 * 2.0 ** -3 + 0.5 * 2.0 ** -7 + 1e-3
-    assert np.abs(got[0, :, 1] - p / (p + T)).max() <= 2.0 ** -7 + 1e-3
+    # every block of 32 rows has its own power of two, so each weight is within 2^-8 (the 31 beside the large one are lost)
+    assert np.abs(got[0, :, 0] - 1).max() <= 2.0 ** -8 + 31 / (p + T) + 1e-3
+    assert np.abs(got[0, :, 1] - p / (p + T)).max() <= 2.0 ** -8 + 1e-3
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+@pytest.mark.parametrize("up", [True, False])
+def test_scores_hundreds_of_binary_orders_apart(lib, q_dtype, up):
+    """Scores that climb (or fall) by about 150 binary orders every 100 rows: what came before is rescaled to nothing,
+    and the largest term alone is left."""
+    T, H, page = 700, 16, 64
+    rng = np.random.default_rng(12)
+    kv8 = rng.integers(0x30, 0x40, ((T + page) // page * page, 576)).astype(np.uint8)
+    kv8[:, 512:] = 0
+    step = (np.arange(len(kv8)) // 100) * (1 if up else -1) + (0 if up else 7)
+    kv8[:, 512] = torch.tensor(step, dtype=F32).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    scale = np.ones(len(kv8), np.float32)
+    q = np.zeros((2, H, 576), np.float32)
+    q[:, :, 512] = 1440 + 64 * (np.arange(H) % 4)     # SM * 1440 log2 e: about 150
+    q[1] *= -1
+    table = np.arange(len(kv8) // page)[None]
+    got, err = run_tree(lib, q, q_dtype, F32, [2], [T - 2], None, kv8, scale, table, page)
+    assert err == 0
+    check(got, q, [2], [T - 2], [np.tril(np.ones((2, 2), bool))], kv8, scale, [np.arange(T)], F32, q_dtype == F32)
 
 
 # ------------------------------------------------------------------------------------------------------------

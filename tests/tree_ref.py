@@ -38,11 +38,11 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
       scores   |d score| <= sm s_t (u q_max sum|k| + v sum|q||k|): u the part of a head's largest query element
                that a query element is rounded to (bf16: 2^-17, f32: none), v the 32-bit sum's (2^-24 a step of
                at most 576, taken as 576 2^-24).  Each weight is then off by exp(+-2 d) relative.
-      weights  f32: 2 steps of exp2 and a product.  bf16: held as w = p_t s_t in units that put the column's largest
-               at 2^5 or more; rounded to 11 bits (2^-12 w at most, 2^-25 where f16 is subnormal); an e4m3 piece
-               leaves at most 2^-4 w, and at most 2^-10 where it is subnormal (w < 2^-6; all of w below 2^-10); an
-               e5m2 piece of that is off by 2^-3 of it at most, or 2^-17 where that is subnormal.  Together at most
-               2^-7 w + min(2^-13, 2^-3 w) + 2^-17 + 2^-11 w, each times the row's |e4m3 value|.
+      weights  f32: 2 steps of exp2 and a product.  bf16: the weights w = p_t s_t of 32 rows (positions 32 i to 32 i +
+               31) are held in units that put the largest of them at 2^7 or more; rounded to 11 bits (2^-12 w at most),
+               then to an e4m3 value, which leaves at most 2^-4 w (2^-10 where it is subnormal, or all of w below that),
+               and that to another (2^-4 of it, or 2^-10 where that is subnormal): at most 2^-8 w + 2^-10, each times the
+               row's |e4m3 value|.
       sum      32 bits, one step for each row and one for each part
       output   out_eps relative (half a step of its type)
     """
@@ -66,6 +66,17 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
         p /= p.sum(1, keepdims=True)
         out[i] = p @ kk[:, :512]
         A = p @ np.abs(kk[:, :512])
+        # exp(2 d) - 1 for every row, weighted as the terms are, twice: numerator and denominator
+        e = np.expm1(2 * d)
+        tol[i] = (p * e) @ np.abs(kk[:, :512]) + (p * e).sum(1)[:, None] * A
+        tol[i] += A * (2.0 ** -21 + (2 * T + 64) * 2.0 ** -24)
+        if not f32:
+            ps = p * scale[rows[on]].astype(np.float64)
+            block = np.nonzero(on)[0] // 32
+            unit = np.zeros((H, T // 32 + 1))
+            np.maximum.at(unit.T, block, ps.T)
+            off = (2.0 ** -8 + 2.0 ** -12) * ps + 2.0 ** -10 * unit[:, block] / 128
+            tol[i] += off @ np.abs(TABLE[kv8[rows[on]]][:, :512])
         # exp(2 d) - 1 for every row, weighted as the terms are, twice: numerator and denominator
         e = np.expm1(2 * d)
         tol[i] = (p * e) @ np.abs(kk[:, :512]) + (p * e).sum(1)[:, None] * A
