@@ -42,8 +42,10 @@ constexpr int kCols = 64;
 constexpr int kRows = 64;
 constexpr int kStages = 5;
 constexpr int kSegment = 8;                // a segment's start and end cost about as much as this many tiles
-constexpr int kTeam = 256;                 // threads of a softmax team
-constexpr int kThreads = 128 + 2 * kTeam;
+constexpr int kTeams = 2;                  // softmax teams of 256 threads
+constexpr int kTeam = 256;
+constexpr int kSoftmax = kTeams * kTeam;
+constexpr int kThreads = 128 + kSoftmax;
 constexpr uint32_t kBlk = 8192;            // 64 rows x 128 latent bytes (SW128)
 constexpr uint32_t kRope = 4096;           // 64 rows x 64 RoPE bytes (SW64)
 constexpr uint32_t kStage = 4 * kBlk + kRope;
@@ -51,26 +53,30 @@ constexpr uint32_t kQLat = 128 * 448;      // a group's query image: 128 lanes x
 constexpr uint32_t kQTail = 128 * 128;     // then 128 x (64 latent + 64 RoPE bytes) (SW128)
 constexpr uint32_t kImg = kQLat + kQTail;
 constexpr uint32_t kW = 8192;              // hi [64 columns][64 rows] (SW64), then lo
-constexpr uint32_t OFF_ST = 0, OFF_W = kStages * kStage, OFF_Q = OFF_W + 2 * kW, OFF_MISC = OFF_Q + kQTail;
+constexpr uint32_t OFF_ST = 0, OFF_W = kStages * kStage, OFF_Q = OFF_W + kTeams * kW, OFF_MISC = OFF_Q + kQTail;
 constexpr float kRoom = 100.0f;            // the reference moves when a block's exponent exceeds it by more
 constexpr int kBase = 60;                  // O and z are relative to 2^(reference + kBase)
 constexpr float kTiny = 8.6736174e-19f;    // 2^-60
 constexpr uint32_t TM_Q = 0, TM_SFA = 112, TM_SFB = 116, TM_S = 128, TM_O = 256;
 
 struct RowInfo {
-    alignas(16) float sl[kRows / 2][4];    // for each pair of rows: scales (0 for rows that are not there), log2
-    alignas(16) float inv[kRows];          // 1 / scale
+    alignas(16) float scale[kRows];        // 0 for rows that are not there
     uint64_t in, zero;                     // rows that are there / whose scale is below 2^-60
-    uint32_t full;                         // all there, none of them zero
+    float norm[2];                         // 2^-K of each block of 32 rows, K = ceil(log2 of its largest scale) ...
+    uint32_t even;                         // ... where all are there and within 2^8 of one another; else 0
 };
 struct Misc {
     RowInfo rows[kStages];
     alignas(16) float ref[kCols];          // the columns' references R (whole numbers), -inf before any attended row
-    alignas(16) float top[2][2][2][kCols]; // X of each block: [team][tile pair][set][column]
-    alignas(16) float red[4][kCols];       // at the end: sums
     alignas(16) float zinv[kCols];         // at the end: 1 / z
-    uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_full[2], s_free[2], w_full[2], pv_done[2], q_ready,
-        final_bar[2];
+    union {
+        float top[kTeams][2][kCols];       // X of a team's two blocks
+        float red[2 * kTeams][kCols];      // at the end: sums
+    };
+    TreeSegment seg[2];                    // this segment and the next
+    int more[2];
+    uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_free[2], s_full[kTeams], w_full[kTeams], pv_done[kTeams],
+        q_ready, final_bar[2];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -90,9 +96,8 @@ __host__ __device__ __forceinline__ int64_t tree_slot(int64_t q0, int H, int b) 
 // Lane of column n's piece (0 = hi, 1 = lo).
 __device__ __forceinline__ int query_lane(int n, int piece) { return (n >> 4) * 32 + piece * 16 + (n & 15); }
 
-// Arrive at a named barrier that other threads wait at; what this thread wrote before is theirs to read after it.
+// Arrive at a named barrier that other threads wait at.
 __device__ __forceinline__ void named_arrive(int id, int count) {
-    __threadfence_block();
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
@@ -187,17 +192,23 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint3
 }
 // Two softmax weights (at most 2^8) -> e4m3 pieces and e4m3 pieces of what those leave.  By way of f16, whose 11 bits
 // are finer than the 8 that the pieces keep; the residual is exact there.
-__device__ __forceinline__ void split_weights(float a, float b, uint16_t &hi, uint16_t &lo) {
+__device__ __forceinline__ uint32_t split_weights(uint64_t w) {  // hi pieces in the low half, lo pieces in the high half
     uint32_t w16, h16, r16;
+    uint16_t hi, lo;
+    float a, b;
+    f2_unpack(w, a, b);
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w16) : "f"(b), "f"(a));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(w16));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(hi));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r16) : "r"(w16), "r"(h16));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r16));
+    return (uint32_t)hi | (uint32_t)lo << 16;
 }
-__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// log2 of a power of two
+__device__ __forceinline__ float log2_whole(float p) { return (float)((int)(__float_as_uint(p) >> 23) - 127); }
 __device__ __forceinline__ float lg2_approx(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -331,13 +342,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms.kv_free[s], 1);
             mbar_init(&ms.row_full[s], 1);
         }
-        for (int k = 0; k < 2; ++k) {
-            mbar_init(&ms.s_full[k], 1);
-            mbar_init(&ms.s_free[k], kTeam / 32);  // one arrival for each warp
+        mbar_init(&ms.s_free[0], kTeam / 32);  // one arrival for each warp
+        mbar_init(&ms.s_free[1], kTeam / 32);
+        for (int k = 0; k < kTeams; ++k) {
+            mbar_init(&ms.s_full[k], 1);  // (a team's own: a waiter that skipped phases could take one for another)
             mbar_init(&ms.w_full[k], kTeam / 32);
             mbar_init(&ms.pv_done[k], 1);
         }
-        mbar_init(&ms.q_ready, 2 * kTeam / 32);
+        mbar_init(&ms.q_ready, kSoftmax / 32);
         mbar_init(&ms.final_bar[0], 1);
         mbar_init(&ms.final_bar[1], 1);
         ms.abort_flag = 0;
@@ -422,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ok = bar_wait(bar, parity, &ms.abort_flag, a.err_word);
             ok = __all_sync(0xffffffffu, ok);
         };
-        int j = 0, sg = 0, s = 0;  // tiles, segments, the stage
+        int j = 0, sg = 0, s = 0, w3 = 0;  // tiles, segments, the stage, the team
         uint32_t s_ph = 0;
         while (ok && walk.next<kCols, kRows>(a, seg)) {
             wait(&ms.q_ready, sg & 1);
@@ -441,9 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 4; ++kk)
                         mma_f8f6f4(d, q_desc + (uint64_t)(kk * 2), kk < 2 ? k + (uint64_t)((3 * kBlk + 64 + kk * 32) >> 4) : kr + (uint64_t)((kk - 2) * 2),
                                    id_s, 1u);
-                    mma_commit(&ms.s_full[j & 1]);
+                    mma_commit(&ms.s_full[w3]);
                 }
                 __syncwarp();
+                w3 = w3 + 1 == kTeams ? 0 : w3 + 1;
                 if (++s == kStages) {
                     s = 0;
                     s_ph ^= 1;
@@ -463,32 +476,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ok = bar_wait(bar, parity, &ms.abort_flag, a.err_word);
             ok = __all_sync(0xffffffffu, ok);
         };
-        int i = 0, s = 0;
-        uint32_t s_ph = 0;
+        int i = 0, s = 0, w3 = 0;  // tiles, the stage, the team
+        uint32_t s_ph = 0, w_ph = 0;
         while (ok && walk.next<kCols, kRows>(a, seg)) {
             for (int t = seg.t0; ok && t < seg.t1; ++t, ++i) {
                 wait(&ms.kv_full[s], s_ph);  // (complete since before the score)
-                wait(&ms.w_full[i & 1], (i >> 1) & 1);
+                wait(&ms.w_full[w3], w_ph);
                 tc_fence_after_sync();
                 if (ok && elect_one()) {
                     const uint64_t v = v_desc + (uint64_t)(s * (kStage >> 4));
-                    const uint64_t w = w_desc + (uint64_t)((i & 1) * (kW >> 4));
+                    const uint64_t w = w_desc + (uint64_t)(w3 * (kW >> 4));
                     const uint32_t keep = t > seg.t0;
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
                         for (int kk = 0; kk < 2; ++kk) {
                             const uint64_t av = v + (uint64_t)((ch * kBlk + kk * 4096) >> 4);
-                            const uint32_t sfb = tmem + TM_SFB + 4u * (i & 1);
+                            const uint32_t sfb = tmem + TM_SFB + 4u * w3;
                             mma_mxf8(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kk * 32) >> 4), idesc_mxf8(128, kCols, kk), tmem + TM_SFA,
                                      sfb, kk ? 1u : keep);
                             mma_mxf8(tmem + TM_O + 64u * ch, av, w + (uint64_t)((kW / 2 + kk * 32) >> 4), idesc_mxf8(128, kCols, kk),
                                      tmem + TM_SFA, sfb, 1u);
                         }
                     mma_commit(&ms.kv_free[s]);
-                    mma_commit(&ms.pv_done[i & 1]);
+                    mma_commit(&ms.pv_done[w3]);
                 }
                 __syncwarp();
+                if (++w3 == kTeams) {
+                    w3 = 0;
+                    w_ph ^= 1;
+                }
                 if (++s == kStages) {
                     s = 0;
                     s_ph ^= 1;
@@ -531,23 +548,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     RowInfo &ri = ms.rows[s];
                     uint32_t in[2], zero[2];
+                    float norm[2];
+                    bool even = true;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const float c = sc[2 * v + k];
                         const bool there = row[2 * v + k] >= 0;
                         in[k] = __ballot_sync(0xffffffffu, there);
                         zero[k] = __ballot_sync(0xffffffffu, there && c < kTiny);
-                        float *sl = &ri.sl[16 * k + (lane >> 1)][lane & 1];
-                        sl[0] = c;
-                        sl[2] = lg2_approx(c);
-                        // 0 for a zero row (its weight is 0) and for a scale that is not finite (its weight is NaN
-                        // where it is attended)
-                        ri.inv[32 * k + lane] = c >= kTiny && c <= 3.402823466e38f ? __fdividef(1.f, c) : 0.f;
+                        ri.scale[32 * k + lane] = c;
+                        const float lo = -warp_redux_max(-c), hi = warp_redux_max(c);
+                        even = even && lo >= kTiny && hi <= 1.f / kTiny && hi <= 256.f * lo && in[k] == 0xffffffffu;
+                        // (scales are compared, so a NaN is not even)
+                        if (!__all_sync(0xffffffffu, c == c)) even = false;
+                        int K;
+                        frexpf(hi, &K);  // hi <= 2^K
+                        norm[k] = even ? ldexpf(1.f, -K) : 0.f;
                     }
                     if (lane == 0) {
                         ri.in = in[0] | (uint64_t)in[1] << 32;
                         ri.zero = zero[0] | (uint64_t)zero[1] << 32;
-                        ri.full = (in[0] & in[1]) == 0xffffffffu && (zero[0] | zero[1]) == 0;
+                        ri.norm[0] = norm[0];
+                        ri.norm[1] = norm[1];
+                        ri.even = even;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.row_full[s]);
@@ -562,52 +585,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         // barrier, so that no other warp waits for it.
         const int st = tid - 128;                     // 0..511
         const int q = warp & 3, w16 = (warp - 4) >> 2;
-        const int team = w16 >> 1, set = w16 & 1;     // tiles of the team's parity; rows 32 set .. 32 set + 31 of them
+        const int team = w16 >> 1, set = w16 & 1;     // alternate tiles; rows 32 set .. 32 set + 31 of them
         // A 16-lane TMEM load of 8 columns hands lane l rows 2 (l % 4) and 2 (l % 4) + 1 of columns l / 4 and l / 4 + 8: the
         // hi and lo pieces' loads match register by register.  So a thread holds, for two columns, rows 8 i + 2 (l % 4)
         // and the next, i < 4, of its set's 32.
         const int n_a = 16 * q + (lane >> 2), n_b = n_a + 8;
         const int r0 = 32 * set + 2 * (lane & 3);     // its first row
         const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
-        const uint32_t s_addr = tmem + lane_addr + TM_S + 64u * team + 32u * set;
+        const uint32_t s_addr = tmem + lane_addr + TM_S + 32u * set;
         const uint32_t o_addr = tmem + lane_addr + TM_O;
-        const int team_bar = 2 + team;                // the team's own barrier
-        // where its weights go: rows r0 + 8 i of column a are at w_addr[i / 2] + 8 (i % 2), column b's 512 bytes on
+        // named barriers: 1 = all teams, 2 + team its own, 5 + team: it has decided, the next team waits
+        const int team_bar = 2 + team, before = team == 0 ? kTeams - 1 : team - 1;
+        // where its weights go: lane pairs exchange, so that an even lane stores rows 8 i + 4 (l % 4 / 2) .. + 3 of its set's
+        // even i, an odd lane of its odd i; column b's are 512 bytes on
+        const uint32_t w_row = 32 * set + 8 * (lane & 1) + 4 * ((lane & 3) >> 1);
         const uint32_t w_base = sbase + OFF_W + team * kW;
-        const uint32_t w_addr[2] = {w_base + sw64_offset(n_a, r0), w_base + sw64_offset(n_a, r0 + 16)};
+        const uint32_t w_addr[2] = {w_base + sw64_offset(n_a, w_row), w_base + sw64_offset(n_a, w_row + 16)};
+        const uint32_t lo_first = lane & 1 ? 0x1054u : 0x5410u, hi_first = lane & 1 ? 0x3276u : 0x7632u;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok) ok = bar_wait(bar, parity, &ms.abort_flag, a.err_word);
         };
         grid_launch_dependents();
-        // a group's queries: 128 (the last set's: 64) latent bytes of this thread's lane, two chunks of the part in shared
-        // memory, two columns' factors
-        uint4 qv[8], qt[2];
-        float c_a = 0.f, c_b = 0.f;
-        auto fetch_queries = [&](const TreeSegment &g) {
-            const int64_t slot = tree_slot(g.q.q0, a.H, g.b) + g.g;
-            const uint8_t *img = x.img + slot * kImg;
-            const uint4 *src = reinterpret_cast<const uint4 *>(img + (32 * q + lane) * 448 + w16 * 128);
+        // a group's queries: the lane's 448 latent bytes to TMEM by the first four warps of each quadrant (the fourth: 64
+        // bytes), the part in shared memory by all
+        auto load_queries = [&](const TreeSegment &g) {
+            const uint8_t *img = x.img + (tree_slot(g.q.q0, a.H, g.b) + g.g) * kImg;
+            if (w16 < 4) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(img + (32 * q + lane) * 448 + w16 * 128);
+                uint4 v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < 4 || w16 < 3) qv[k] = __ldg(src + k);
+                for (int k = 0; k < 8; ++k)
+                    if (k < 4 || w16 < 3) v[k] = __ldg(src + k);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) qt[k] = __ldg(reinterpret_cast<const uint4 *>(img + kQLat) + 512 * k + st);
-            c_a = __ldg(x.c_head + slot * kCols + n_a);
-            c_b = __ldg(x.c_head + slot * kCols + n_b);
-        };
-        auto store_queries = [&]() {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t w[16] = {qv[4 * k].x,     qv[4 * k].y,     qv[4 * k].z,     qv[4 * k].w,
-                                        qv[4 * k + 1].x, qv[4 * k + 1].y, qv[4 * k + 1].z, qv[4 * k + 1].w,
-                                        qv[4 * k + 2].x, qv[4 * k + 2].y, qv[4 * k + 2].z, qv[4 * k + 2].w,
-                                        qv[4 * k + 3].x, qv[4 * k + 3].y, qv[4 * k + 3].z, qv[4 * k + 3].w};
-                if (k == 0 || w16 < 3) tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + w16 * 32 + 16 * k, w);
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t w[16] = {v[4 * k].x,     v[4 * k].y,     v[4 * k].z,     v[4 * k].w,
+                                            v[4 * k + 1].x, v[4 * k + 1].y, v[4 * k + 1].z, v[4 * k + 1].w,
+                                            v[4 * k + 2].x, v[4 * k + 2].y, v[4 * k + 2].z, v[4 * k + 2].w,
+                                            v[4 * k + 3].x, v[4 * k + 3].y, v[4 * k + 3].z, v[4 * k + 3].w};
+                    if (k == 0 || w16 < 3) tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + w16 * 32 + 16 * k, w);
+                }
+                tmem_wait_st();
             }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4 *>(smem + OFF_Q + (512 * k + st) * 16) = qt[k];
-            tmem_wait_st();
+            for (int k = st; k < (int)kQTail / 16; k += kSoftmax)
+                *reinterpret_cast<uint4 *>(smem + OFF_Q + k * 16) = __ldg(reinterpret_cast<const uint4 *>(img + kQLat) + k);
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
@@ -619,68 +640,78 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_32x32b_x2(tmem + lane_addr + TM_SFA + 2, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
             tmem_wait_st();
         }
-        bool more = walk.next<kCols, kRows>(a, seg);
-        if (more) {
-            fetch_queries(seg);
-            store_queries();
-        }
+        // One thread walks the share, a segment ahead of the others.
+        if (st == 0) ms.more[0] = walk.next<kCols, kRows>(a, ms.seg[0]);
         if (st < kCols) ms.ref[st] = -INFINITY;
-        named_sync(1, 2 * kTeam);
-        int it0 = 0;  // tiles before the segment
-        while (more) {
-            const int top = seg.q.n * a.H;
-            const int tiles = seg.t1 - seg.t0;
+        named_sync(1, kSoftmax);
+        if (ms.more[0]) load_queries(ms.seg[0]);
+        int first_tile = 0;                    // tiles before the segment, modulo kTeams
+        uint32_t own = 0;                      // the team's tiles so far
+        int it = team, s_now = team;           // the team's next tile, and its stage
+        uint32_t s_ph = 0;
+        int end_tile = 0;                      // tiles up to the segment's end
+        for (int k = 0; ms.more[k & 1]; ++k) {
+            const TreeSegment &sg = ms.seg[k & 1];
+            if (st == 0) ms.more[(k + 1) & 1] = walk.next<kCols, kRows>(a, ms.seg[(k + 1) & 1]);
+            first_tile = end_tile;
+            end_tile += sg.t1 - sg.t0;
+            const int plain_end = first_tile + (int)min(sg.q.len / kRows - sg.t0, (int64_t)(end_tile - first_tile));  // tiles of context only
+            float c_a, c_b;
+            {
+                const float *c = x.c_head + (tree_slot(sg.q.q0, a.H, sg.b) + sg.g) * kCols;
+                c_a = __ldg(c + n_a);
+                c_b = __ldg(c + n_b);
+            }
             float ref_a = -INFINITY, ref_b = -INFINITY;         // the references that z is relative to: the team's last
             uint64_t z_a = f2_pack(0.f, 0.f), z_b = f2_pack(0.f, 0.f);
             int zero_a = 0, zero_b = 0;                         // zero rows that the columns attend among this thread's
-            const uint64_t ca = f2_pack(c_a, c_a), cb = f2_pack(c_b, c_b);
-            const int ctx_tiles = (int)(seg.q.len / kRows);     // tiles of context only
-            for (int u = (it0 ^ team) & 1; u < tiles; u += 2) {
-                const int it = it0 + u, t = seg.t0 + u;
-                const uint32_t s_now = (uint32_t)it % kStages, ph_now = ((uint32_t)it / kStages) & 1u, half_ph = ((uint32_t)it >> 1) & 1u;
+            for (; it < end_tile; it += kTeams, ++own) {
+                const uint32_t own_ph = own & 1u;
                 // ---- scores
-                wait(&ms.s_full[team], half_ph);
+                wait(&ms.s_full[team], own_ph);
                 tc_fence_after_sync();
                 uint32_t hi[16], lo[16];
-                tmem_ld_16x256b_x4(s_addr, hi);
-                tmem_ld_16x256b_x4(s_addr + (16u << 16), lo);
-                wait(&ms.row_full[s_now], ph_now);
+                tmem_ld_16x256b_x4(s_addr + 64u * (it & 1), hi);
+                tmem_ld_16x256b_x4(s_addr + 64u * (it & 1) + (16u << 16), lo);
+                wait(&ms.row_full[s_now], s_ph);
                 const RowInfo &ri = ms.rows[s_now];
-                float4 sl[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sl[i] = *reinterpret_cast<const float4 *>(&ri.sl[(r0 >> 1) + 4 * i][0]);
-                const bool plain = t < ctx_tiles && ri.full;  // every column attends every row
+                // every column attends every row, and the rows' scales are near one another
+                const bool plain = it < plain_end && ri.even;
+                const float norm = ri.norm[set];
                 tmem_wait_ld();
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.s_free[team]);
-                // ---- e, row pairs packed: 0..3 of column a, 4..7 of column b
-                uint64_t d2[8];
+                if (lane == 0) mbar_arrive(&ms.s_free[it & 1]);
+                // ---- scores (log2 units), row pairs packed: 0..3 of column a, 4..7 of column b
+                uint64_t d2[8], sc2[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint64_t sc2 = f2_pack(sl[i].x, sl[i].y), lg2 = f2_pack(sl[i].z, sl[i].w);
+                    const float2 sc = *reinterpret_cast<const float2 *>(&ri.scale[r0 + 8 * i]);
+                    sc2[i] = f2_pack(sc.x, sc.y);
                     const uint64_t sa = f2_add(f2_pack(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
                                                f2_pack(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])));
                     const uint64_t sb = f2_add(f2_pack(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])),
                                                f2_pack(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])));
-                    d2[i] = f2_fma(sa, f2_mul(sc2, ca), lg2);
-                    d2[4 + i] = f2_fma(sb, f2_mul(sc2, cb), lg2);
+                    d2[i] = f2_mul(sa, f2_mul(sc2[i], f2_pack(c_a, c_a)));
+                    d2[4 + i] = f2_mul(sb, f2_mul(sc2[i], f2_pack(c_b, c_b)));
                 }
                 if (!plain) {
                     // the rows that the columns attend: those that are there, of the draft those of their masks
                     const uint64_t in = ri.in, zr = ri.zero;
-                    const int64_t j0 = (int64_t)t * kRows - seg.q.len;  // the tile's first row's index in the draft
-                    const int c0 = seg.g * kCols;
+                    const int64_t j0 = (int64_t)(sg.t0 + it - first_tile) * kRows - sg.q.len;  // the tile's first row's index in the draft
+                    const int c0 = sg.g * kCols, top = sg.q.n * a.H;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint64_t att = in & tree_attended(a, seg.q.q0, min(c0 + (h ? n_b : n_a), top - 1) / a.H, j0);
+                        const uint64_t att = in & tree_attended(a, sg.q.q0, min(c0 + (h ? n_b : n_a), top - 1) / a.H, j0);
                         (h ? zero_b : zero_a) += __popcll(att & zr & (0x03030303ull << r0));
                         const uint32_t on = (uint32_t)((att & ~zr) >> r0);  // bits 8 i and 8 i + 1
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float e0, e1;
+                            float e0, e1, s0, s1;
                             f2_unpack(d2[4 * h + i], e0, e1);
-                            d2[4 * h + i] = f2_pack(on >> (8 * i) & 1 ? e0 : -INFINITY, on >> (8 * i + 1) & 1 ? e1 : -INFINITY);
+                            f2_unpack(sc2[i], s0, s1);
+                            d2[4 * h + i] = f2_pack(on >> (8 * i) & 1 ? e0 + lg2_approx(s0) : -INFINITY,
+                                                    on >> (8 * i + 1) & 1 ? e1 + lg2_approx(s1) : -INFINITY);
                         }
                     }
                 }
@@ -693,40 +724,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     f2_unpack(d2[4 + i], e0, e1);
                     max_b = fmaxf(max_b, fmaxf(e0, e1));
                 }
-                // ---- X = floor(max e) of the block: over the column's four lanes
+                // ---- X of the block, over the column's four lanes: floor(max e), or in a plain tile floor(max score) + K
+                const float K = plain ? -log2_whole(norm) : 0.f;
                 max_a = fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 1));
                 max_b = fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 1));
-                max_a = floorf(fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 2)));
-                max_b = floorf(fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 2)));
-                float(*const tops)[kCols] = ms.top[team][half_ph];
+                max_a = floorf(fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 2))) + K;
+                max_b = floorf(fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 2))) + K;
+                // the context product of the team's tile before has read its weight buffer and factors (and the exponents
+                // that they were made from)
+                if (own > 0) wait(&ms.pv_done[team], own_ph ^ 1u);
+                float(*const tops)[kCols] = ms.top[team];
                 if ((lane & 3) == 0) {
                     tops[set][n_a] = max_a;
                     tops[set][n_b] = max_b;
                 }
                 // ---- the references, tile after tile: the other team has decided on the tile before.  (The barrier also
                 // hands the blocks' exponents to the warps that write the scale factors.)
-                if (u > 0) named_sync(4 + (team ^ 1), 2 * kTeam);
+                if (it > first_tile) named_sync(5 + before, 2 * kTeam);
                 float na = ms.ref[n_a], nb = ms.ref[n_b];
                 const bool slow = bar_red_or(team_bar, kTeam, max_a > na + kRoom || max_b > nb + kRoom);
                 auto moved = [&](int n, float r) -> float {  // a column's reference r from this tile on
                     const float x = fmaxf(tops[0][n], tops[1][n]);
                     return slow && x > r + kRoom ? x : r;
                 };
-                float rl = 0.f, rh = 0.f;  // of the columns whose factors this lane writes
-                if (set == 0) {
-                    rl = moved(lane, ms.ref[lane]);
-                    rh = moved(32 + lane, ms.ref[32 + lane]);
-                }
                 float move = 1.f;          // the factor of the accumulator column 32 set + lane
+                float rl = ms.ref[lane], rh = ms.ref[32 + lane];  // of the columns whose factors this lane may write
                 if (slow) {
+                    rl = moved(lane, rl);
+                    rh = moved(32 + lane, rh);
                     na = moved(n_a, na);
                     nb = moved(n_b, nb);
                     const float r = ms.ref[32 * set + lane], rn = moved(32 * set + lane, r);
                     move = r == -INFINITY || rn == r ? 1.f : ex2_approx(r - rn);
                     named_sync(team_bar, kTeam);
                     if (q == 0) ms.ref[32 * set + lane] = rn;  // (all have read the old ones)
+                    __threadfence_block();                     // before the other team, which arrives below, reads them
                 }
-                if (u + 1 < tiles) named_arrive(4 + team, 2 * kTeam);
+                if (it + 1 < end_tile) named_arrive(5 + team, 2 * kTeam);
                 if (ref_a != na || ref_b != nb) {  // z, relative to the team's last references, to these
                     const float fa = ref_a == -INFINITY || ref_a == na ? 1.f : ex2_approx(ref_a - na);
                     const float fb = ref_b == -INFINITY || ref_b == nb ? 1.f : ex2_approx(ref_b - nb);
@@ -739,24 +773,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the reference are that much smaller instead
                 auto factor = [](float x, float r) -> uint32_t { return (uint32_t)fminf(fmaxf(x - r + (float)kBase, 1.f), 254.f); };
                 const uint32_t byte_a = factor(max_a, na), byte_b = factor(max_b, nb);
-                // the context product of the team's tile before has read this weight buffer and its factors
-                if (it >= 2) wait(&ms.pv_done[team], half_ph ^ 1u);
                 if (set == 0) {
                     tc_fence_after_sync();
                     tmem_st_32x32b_x2(tmem + lane_addr + TM_SFB + 4u * team, factor(tops[0][lane], rl) | factor(tops[1][lane], rl) << 8,
                                       factor(tops[0][32 + lane], rh) | factor(tops[1][32 + lane], rh) << 8);
                 }
-                // ---- weights 2^(e - X + 7)
+                // ---- weights 2^(e - X + 7): in a plain tile p = 2^(score - X + K + 7) times scale 2^-K, and z the sum of p 2^-K
                 {
                     // (nothing attended so far: e is -inf throughout, whatever is subtracted)
-                    const float xa = na == -INFINITY ? 7.f : (float)(kBase + 7) - na - (float)byte_a;
-                    const float xb = nb == -INFINITY ? 7.f : (float)(kBase + 7) - nb - (float)byte_b;
-                    const uint64_t ra = f2_pack(xa, xa), rb = f2_pack(xb, xb);
+                    const float xa = na == -INFINITY ? 7.f : (float)(kBase + 7) - na - (float)byte_a + K;
+                    const float xb = nb == -INFINITY ? 7.f : (float)(kBase + 7) - nb - (float)byte_b + K;
+                    const uint64_t ra = f2_pack(xa, xa), rb = f2_pack(xb, xb), nm2 = f2_pack(norm, norm);
                     uint64_t za = f2_pack(0.f, 0.f), zb = za;
+                    uint32_t keep_a = 0, keep_b = 0;  // the odd (even lanes) or even (odd lanes) pair of rows that the neighbour gets
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 inv = *reinterpret_cast<const float2 *>(&ri.inv[r0 + 8 * i]);
-                        const uint64_t inv2 = f2_pack(inv.x, inv.y);
                         float e0, e1, x0, x1, y0, y1;
                         f2_unpack(f2_add(d2[i], ra), e0, e1);
                         x0 = ex2_approx(e0);
@@ -764,18 +795,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                         f2_unpack(f2_add(d2[4 + i], rb), e0, e1);
                         y0 = ex2_approx(e0);
                         y1 = ex2_approx(e1);
-                        za = f2_fma(f2_pack(x0, x1), inv2, za);
-                        zb = f2_fma(f2_pack(y0, y1), inv2, zb);
-                        uint16_t wh, wl;
-                        const uint32_t p = w_addr[i >> 1] + 8 * (i & 1);
-                        split_weights(x0, x1, wh, wl);
-                        st_shared_u16(p, wh);
-                        st_shared_u16(p + kW / 2, wl);
-                        split_weights(y0, y1, wh, wl);
-                        st_shared_u16(p + 512, wh);
-                        st_shared_u16(p + 512 + kW / 2, wl);
+                        uint64_t wa = f2_pack(x0, x1), wb = f2_pack(y0, y1);
+                        if (plain) {
+                            const uint64_t f = f2_mul(sc2[i], nm2);
+                            za = f2_add(za, wa);
+                            zb = f2_add(zb, wb);
+                            wa = f2_mul(wa, f);
+                            wb = f2_mul(wb, f);
+                        } else {
+                            float s0, s1;
+                            f2_unpack(sc2[i], s0, s1);
+                            // 0 for a zero row (its weight is 0) and for a scale that is not finite (its weight is NaN
+                            // where it is attended)
+                            const uint64_t inv2 = f2_pack(s0 >= kTiny && s0 <= 3.402823466e38f ? __fdividef(1.f, s0) : 0.f,
+                                                          s1 >= kTiny && s1 <= 3.402823466e38f ? __fdividef(1.f, s1) : 0.f);
+                            za = f2_fma(wa, inv2, za);
+                            zb = f2_fma(wb, inv2, zb);
+                        }
+                        // pieces: hi in the low half, lo in the high half
+                        const uint32_t pa = split_weights(wa), pb = split_weights(wb);
+                        // neighbouring lanes hold neighbouring pairs of rows: each stores four rows of every other i
+                        const bool mine = (i & 1) == (lane & 1);
+                        if ((i & 1) == 0) {
+                            keep_a = pa;
+                            keep_b = pb;
+                        } else {
+                            const uint32_t ga = __shfl_xor_sync(0xffffffffu, mine ? keep_a : pa, 1), gb = __shfl_xor_sync(0xffffffffu, mine ? keep_b : pb, 1);
+                            const uint32_t oa = mine ? pa : keep_a, ob = mine ? pb : keep_b;
+                            // even lanes: rows of i - 1, own pair first; odd lanes: rows of i, the neighbour's first
+                            const uint32_t p = w_addr[i >> 1];
+                            st_shared_u32(p, __byte_perm(oa, ga, lo_first));
+                            st_shared_u32(p + kW / 2, __byte_perm(oa, ga, hi_first));
+                            st_shared_u32(p + 512, __byte_perm(ob, gb, lo_first));
+                            st_shared_u32(p + 512 + kW / 2, __byte_perm(ob, gb, hi_first));
+                        }
                     }
-                    const float fa = __uint_as_float(byte_a << 23), fb = __uint_as_float(byte_b << 23);
+                    const float f = plain ? norm : 1.f;
+                    const float fa = __uint_as_float(byte_a << 23) * f, fb = __uint_as_float(byte_b << 23) * f;
                     z_a = f2_fma(za, f2_pack(fa, fa), z_a);
                     z_b = f2_fma(zb, f2_pack(fb, fb), z_b);
                 }
@@ -784,9 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!plain) {
                     const int r = st & 63;
                     const bool there = ri.in >> r & 1;
-                    if (!there || (int64_t)t * kRows + r >= seg.q.len) {
+                    if (!there || (int64_t)(sg.t0 + it - first_tile) * kRows + r >= sg.q.len) {
                         // (complete since before the score: this makes the copy's bytes visible here too)
-                        (void)bar_wait(&ms.kv_full[s_now], ph_now, &ms.abort_flag, a.err_word);
+                        (void)bar_wait(&ms.kv_full[s_now], s_ph, &ms.abort_flag, a.err_word);
                         uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s_now * kStage + ((st >> 6) & 3) * kBlk + r * 128);
                         uint4 v[8];
 #pragma unroll
@@ -796,10 +852,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p[k] = make_uint4(without_nan(v[k].x), without_nan(v[k].y), without_nan(v[k].z), without_nan(v[k].w));
                     }
                 }
-                if (slow && u > 0 && __any_sync(0xffffffffu, move != 1.f)) {
+                if (slow && it > first_tile && __any_sync(0xffffffffu, move != 1.f)) {
                     // this warp's part of the accumulators, 32 columns by 32 dims of each block, where a column moved,
                     // once the context product before is complete.  (The one before that is: the wait above.)
-                    wait(&ms.pv_done[team ^ 1], ((uint32_t)(it - 1) >> 1) & 1u);
+                    wait(&ms.pv_done[before], ((uint32_t)(it - 1) / kTeams) & 1u);
                     tc_fence_after_sync();
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
@@ -828,16 +884,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.w_full[team]);
+                s_now += kTeams;
+                if (s_now >= kStages) {
+                    s_now -= kStages;
+                    s_ph ^= 1u;
+                }
             }
-            it0 += tiles;
 
             // ---- output, and the next segment's queries: after the first barrier every score of this one is read
-            const TreeSegment done = seg;
-            more = walk.next<kCols, kRows>(a, seg);
-            if (more) fetch_queries(seg);
-            const int c0 = done.g * kCols, nc = min(kCols, top - c0);
-            const bool whole = done.first && done.last;
-            float *part = a.part + ((int64_t)blockIdx.x * 2 + (done.first ? 1 : 0)) * tree_part_floats(kCols);
+            const int c0 = sg.g * kCols, nc = min(kCols, sg.q.n * a.H - c0);
+            const bool whole = sg.first && sg.last;
+            float *part = a.part + ((int64_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * tree_part_floats(kCols);
             // sums over a column's threads, four lanes of each set
             auto to_sets = [&](float u, float v) {
                 u += __shfl_xor_sync(0xffffffffu, u, 1);
@@ -849,13 +906,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ms.red[w16][n_b] = v;
                 }
             };
-            auto over_sets = [&](int n) -> float { return ms.red[0][n] + ms.red[1][n] + ms.red[2][n] + ms.red[3][n]; };
+            auto over_sets = [&](int n) -> float {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < 2 * kTeams; ++w) v += ms.red[w][n];
+                return v;
+            };
             float nn = 0.f;
-            if (bar_red_or(1, 2 * kTeam, (zero_a | zero_b) != 0)) {
+            if (bar_red_or(1, kSoftmax, (zero_a | zero_b) != 0)) {
                 to_sets((float)zero_a, (float)zero_b);
-                named_sync(1, 2 * kTeam);
+                named_sync(1, kSoftmax);
                 nn = over_sets(st & (kCols - 1)) * exp2f(-(float)kBase);
-                named_sync(1, 2 * kTeam);
+                named_sync(1, kSoftmax);
             }
             {
                 const float ea = ms.ref[n_a], eb = ms.ref[n_b];  // both teams' last
@@ -866,8 +928,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fb *= u + v;
                 to_sets(fa, fb);
             }
-            if (more) store_queries();
-            named_sync(1, 2 * kTeam);
+            if (ms.more[(k + 1) & 1]) load_queries(ms.seg[(k + 1) & 1]);
+            named_sync(1, kSoftmax);
             if (st < kCols) {
                 const float m_end = ms.ref[st], zz = over_sets(st);
                 ms.ref[st] = -INFINITY;
@@ -880,48 +942,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                     part[kCols * (kKL + 2) + st] = nn;
                 }
             }
-            wait(&ms.pv_done[(it0 - 1) & 1], ((uint32_t)(it0 - 1) >> 1) & 1u);
+            wait(&ms.pv_done[(uint32_t)(end_tile - 1) % kTeams], ((uint32_t)(end_tile - 1) / kTeams) & 1u);
             tc_fence_after_sync();
-            named_sync(1, 2 * kTeam);
-            const int h0 = 16 * w16;  // columns h0 .. h0 + 15
+            named_sync(1, kSoftmax);
             const bool odd = lane & 1;
             if (__all_sync(0xffffffffu, ok)) {
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    // thread: dim 128 c + 32 q + lane of columns h0 .. h0 + 15
+                for (int u = w16; u < 16; u += 2 * kTeams) {
+                    // thread: dim 32 (u & 12) + 32 q + lane of columns h0 .. h0 + 15
+                    const int h0 = 16 * (u & 3);
                     uint32_t o[16];
-                    tmem_ld_32x32b_x16(o_addr + 64u * c + (uint32_t)h0, o);
+                    tmem_ld_32x32b_x16(o_addr + 64u * (u >> 2) + (uint32_t)h0, o);
                     tmem_wait_ld();
-                    const int d = 128 * c + 32 * q + lane;
-                    float v[16];
+                    const int d = 128 * (u >> 2) + 32 * q + lane;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 a4 = *reinterpret_cast<const float4 *>(&ms.zinv[h0 + 4 * k]);
-                        v[4 * k] = __uint_as_float(o[4 * k]) * a4.x;
-                        v[4 * k + 1] = __uint_as_float(o[4 * k + 1]) * a4.y;
-                        v[4 * k + 2] = __uint_as_float(o[4 * k + 2]) * a4.z;
-                        v[4 * k + 3] = __uint_as_float(o[4 * k + 3]) * a4.w;
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const float4 a4 = *reinterpret_cast<const float4 *>(&ms.zinv[h0 + 4 * k4]);
+                        o[4 * k4] = __float_as_uint(__uint_as_float(o[4 * k4]) * a4.x);
+                        o[4 * k4 + 1] = __float_as_uint(__uint_as_float(o[4 * k4 + 1]) * a4.y);
+                        o[4 * k4 + 2] = __float_as_uint(__uint_as_float(o[4 * k4 + 2]) * a4.z);
+                        o[4 * k4 + 3] = __float_as_uint(__uint_as_float(o[4 * k4 + 3]) * a4.w);
                     }
                     if (!whole || !a.out_bf16) {
-                        float *dst = (whole ? static_cast<float *>(a.out) + ((int64_t)done.q.q0 * a.H + c0) * kKL : part) + h0 * kKL + d;
+                        float *dst = (whole ? static_cast<float *>(a.out) + ((int64_t)sg.q.q0 * a.H + c0) * kKL : part) + h0 * kKL + d;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (h0 + j < nc) dst[j * kKL] = v[j];
+                            if (h0 + j < nc) dst[j * kKL] = __uint_as_float(o[j]);
                     } else {
                         // even lanes store column j, odd lanes column j + 1: two dims each
-                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)done.q.q0 * a.H + c0 + h0 + odd) * kKL + (d & ~1);
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)sg.q.q0 * a.H + c0 + h0 + odd) * kKL + (d & ~1);
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                            const float mine = __uint_as_float(odd ? o[j + 1] : o[j]);
+                            const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? o[j] : o[j + 1], 1));
                             if (h0 + j + odd < nc)
                                 *reinterpret_cast<__nv_bfloat162 *>(dst + j * kKL) =
-                                    odd ? __floats2bfloat162_rn(other, v[j + 1]) : __floats2bfloat162_rn(v[j], other);
+                                    odd ? __floats2bfloat162_rn(other, mine) : __floats2bfloat162_rn(mine, other);
                         }
                     }
                 }
             }
             tc_fence_before_sync();  // the accumulators are read before the next segment's first product
-            named_sync(1, 2 * kTeam);
+            named_sync(1, kSoftmax);
         }
     }
     tc_fence_before_sync();

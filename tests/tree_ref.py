@@ -39,7 +39,8 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
                that a query element is rounded to (bf16: 2^-17, f32: none), v the 32-bit sum's (2^-24 a step of
                at most 576, taken as 576 2^-24).  Each weight is then off by exp(+-2 d) relative.
       weights  f32: 2 steps of exp2 and a product.  bf16: the weights w = p_t s_t of 32 rows (positions 32 i to 32 i +
-               31) are held in units that put the largest of them at 2^7 or more; rounded to 11 bits (2^-12 w at most),
+               31) are held in units that put the largest of them at 2^7 or more, or, in a tile of 64 context rows with
+               scales within 2^8 of one another, the largest p_t times the power of two above the largest s_t; rounded to 11 bits (2^-12 w at most),
                then to an e4m3 value, which leaves at most 2^-4 w (2^-10 where it is subnormal, or all of w below that),
                and that to another (2^-4 of it, or 2^-10 where that is subnormal): at most 2^-8 w + 2^-10, each times the
                row's |e4m3 value|.
@@ -73,8 +74,14 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
         if not f32:
             ps = p * scale[rows[on]].astype(np.float64)
             block = np.nonzero(on)[0] // 32
-            unit = np.zeros((H, T // 32 + 1))
+            st = scale[rows[on]].astype(np.float64)
+            unit, pm, sm_, sl = (np.zeros((H, T // 32 + 2)) for _ in range(4))
             np.maximum.at(unit.T, block, ps.T)
+            np.maximum.at(pm.T, block, p.T)
+            np.maximum.at(sm_.T, block, np.broadcast_to(st[:, None], ps.T.shape))
+            sl[:] = np.inf
+            np.minimum.at(sl.T, block, np.broadcast_to(st[:, None], ps.T.shape))
+            unit = np.where(sm_ <= 256 * sl, np.maximum(unit, 2 * pm * sm_), unit)
             off = (2.0 ** -8 + 2.0 ** -12) * ps + 2.0 ** -10 * unit[:, block] / 128
             tol[i] += off @ np.abs(TABLE[kv8[rows[on]]][:, :512])
         # exp(2 d) - 1 for every row, weighted as the terms are, twice: numerator and denominator
