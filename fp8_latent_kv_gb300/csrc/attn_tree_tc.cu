@@ -677,7 +677,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const RowInfo &ri = ms.rows[s_now];
                 // every column attends every row, and the rows' scales are near one another
                 const bool plain = it < plain_end && ri.even;
-                const float norm = ri.norm[set];
                 tmem_wait_ld();
                 tc_fence_before_sync();
                 __syncwarp();
@@ -695,37 +694,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                     d2[i] = f2_mul(sa, f2_mul(sc2[i], f2_pack(c_a, c_a)));
                     d2[4 + i] = f2_mul(sb, f2_mul(sc2[i], f2_pack(c_b, c_b)));
                 }
-                if (!plain) {
+                // ---- X of the block, over the column's four lanes: in a plain tile floor(max score) + K, else floor(max e)
+                float max_a = -INFINITY, max_b = -INFINITY, K, nm;
+                if (plain) {
+                    nm = ri.norm[set];
+                    K = -log2_whole(nm);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float e0, e1;
+                        f2_unpack(d2[i], e0, e1);
+                        max_a = fmaxf(max_a, fmaxf(e0, e1));
+                        f2_unpack(d2[4 + i], e0, e1);
+                        max_b = fmaxf(max_b, fmaxf(e0, e1));
+                    }
+                } else {
                     // the rows that the columns attend: those that are there, of the draft those of their masks
+                    nm = 1.f;
+                    K = 0.f;
                     const uint64_t in = ri.in, zr = ri.zero;
                     const int64_t j0 = (int64_t)(sg.t0 + it - first_tile) * kRows - sg.q.len;  // the tile's first row's index in the draft
                     const int c0 = sg.g * kCols, top = sg.q.n * a.H;
+                    uint32_t on[2];  // bits 8 i and 8 i + 1 of each column
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint64_t att = in & tree_attended(a, sg.q.q0, min(c0 + (h ? n_b : n_a), top - 1) / a.H, j0);
                         (h ? zero_b : zero_a) += __popcll(att & zr & (0x03030303ull << r0));
-                        const uint32_t on = (uint32_t)((att & ~zr) >> r0);  // bits 8 i and 8 i + 1
+                        on[h] = (uint32_t)((att & ~zr) >> r0);
+                    }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float e0, e1, s0, s1;
-                            f2_unpack(d2[4 * h + i], e0, e1);
-                            f2_unpack(sc2[i], s0, s1);
-                            d2[4 * h + i] = f2_pack(on >> (8 * i) & 1 ? e0 + lg2_approx(s0) : -INFINITY,
-                                                    on >> (8 * i + 1) & 1 ? e1 + lg2_approx(s1) : -INFINITY);
+                    for (int i = 0; i < 4; ++i) {
+                        float s[2], e[2][2];
+                        f2_unpack(sc2[i], s[0], s[1]);
+                        f2_unpack(d2[i], e[0][0], e[0][1]);
+                        f2_unpack(d2[4 + i], e[1][0], e[1][1]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            // a scale that is not a number must not meet the weight 0 of a column that leaves the row out,
+                            // and makes that of a column that does not NaN
+                            const bool fine = s[k] <= 3.402823466e38f;
+                            const float lg = lg2_approx(s[k]);
+                            s[k] = fine ? s[k] : 1.f;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const bool sees = on[h] >> (8 * i + k) & 1;
+                                e[h][k] = !sees ? -INFINITY : fine ? e[h][k] : NAN;
+                                (h ? max_b : max_a) = fmaxf(h ? max_b : max_a, sees ? e[h][k] + lg : -INFINITY);
+                            }
                         }
+                        sc2[i] = f2_pack(s[0], s[1]);
+                        d2[i] = f2_pack(e[0][0], e[0][1]);
+                        d2[4 + i] = f2_pack(e[1][0], e[1][1]);
                     }
                 }
-                float max_a = -INFINITY, max_b = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float e0, e1;
-                    f2_unpack(d2[i], e0, e1);
-                    max_a = fmaxf(max_a, fmaxf(e0, e1));
-                    f2_unpack(d2[4 + i], e0, e1);
-                    max_b = fmaxf(max_b, fmaxf(e0, e1));
-                }
-                // ---- X of the block, over the column's four lanes: floor(max e), or in a plain tile floor(max score) + K
-                const float K = plain ? -log2_whole(norm) : 0.f;
                 max_a = fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 1));
                 max_b = fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 1));
                 max_a = floorf(fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 2))) + K;
@@ -770,68 +790,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ref_b = nb;
                 }
                 // a block's factor 2^(byte - 127), byte = X - R + 60, at least 1: weights of a block that lies 2^59 below
-                // the reference are that much smaller instead
-                auto factor = [](float x, float r) -> uint32_t { return (uint32_t)fminf(fmaxf(x - r + (float)kBase, 1.f), 254.f); };
-                const uint32_t byte_a = factor(max_a, na), byte_b = factor(max_b, nb);
+                // the reference are that much smaller instead.  (As a float, whole: adding 2^23 leaves it in the low bits.)
+                auto factor = [](float t, float r) -> float { return fminf(fmaxf(t - r + (float)kBase, 1.f), 254.f); };
+                auto whole_bits = [](float f) -> uint32_t { return __float_as_uint(f + 8388608.f); };
                 if (set == 0) {
                     tc_fence_after_sync();
-                    tmem_st_32x32b_x2(tmem + lane_addr + TM_SFB + 4u * team, factor(tops[0][lane], rl) | factor(tops[1][lane], rl) << 8,
-                                      factor(tops[0][32 + lane], rh) | factor(tops[1][32 + lane], rh) << 8);
+                    tmem_st_32x32b_x2(tmem + lane_addr + TM_SFB + 4u * team,
+                                      __byte_perm(whole_bits(factor(tops[0][lane], rl)), whole_bits(factor(tops[1][lane], rl)), 0x4040),
+                                      __byte_perm(whole_bits(factor(tops[0][32 + lane], rh)), whole_bits(factor(tops[1][32 + lane], rh)), 0x4040));
                 }
-                // ---- weights 2^(e - X + 7): in a plain tile p = 2^(score - X + K + 7) times scale 2^-K, and z the sum of p 2^-K
+                // ---- weights: p = 2^(score - X + K + 7) times scale 2^-K, at most 2^8; z is the sum of p 2^-K
                 {
-                    // (nothing attended so far: e is -inf throughout, whatever is subtracted)
-                    const float xa = na == -INFINITY ? 7.f : (float)(kBase + 7) - na - (float)byte_a + K;
-                    const float xb = nb == -INFINITY ? 7.f : (float)(kBase + 7) - nb - (float)byte_b + K;
-                    const uint64_t ra = f2_pack(xa, xa), rb = f2_pack(xb, xb), nm2 = f2_pack(norm, norm);
+                    const float f_a = factor(max_a, na), f_b = factor(max_b, nb);
+                    // (nothing attended so far: the scores are -inf throughout, whatever is subtracted)
+                    const float xa = na == -INFINITY ? 7.f : (float)(kBase + 7) - na - f_a + K;
+                    const float xb = nb == -INFINITY ? 7.f : (float)(kBase + 7) - nb - f_b + K;
+                    const uint64_t ra = f2_pack(xa, xa), rb = f2_pack(xb, xb), nm2 = f2_pack(nm, nm);
                     uint64_t za = f2_pack(0.f, 0.f), zb = za;
-                    uint32_t keep_a = 0, keep_b = 0;  // the odd (even lanes) or even (odd lanes) pair of rows that the neighbour gets
+                    uint32_t pa[4], pb[4];  // pieces: hi in the low half, lo in the high half
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float e0, e1, x0, x1, y0, y1;
+                        float e0, e1;
                         f2_unpack(f2_add(d2[i], ra), e0, e1);
-                        x0 = ex2_approx(e0);
-                        x1 = ex2_approx(e1);
+                        const uint64_t wa = f2_pack(ex2_approx(e0), ex2_approx(e1));
                         f2_unpack(f2_add(d2[4 + i], rb), e0, e1);
-                        y0 = ex2_approx(e0);
-                        y1 = ex2_approx(e1);
-                        uint64_t wa = f2_pack(x0, x1), wb = f2_pack(y0, y1);
-                        if (plain) {
-                            const uint64_t f = f2_mul(sc2[i], nm2);
-                            za = f2_add(za, wa);
-                            zb = f2_add(zb, wb);
-                            wa = f2_mul(wa, f);
-                            wb = f2_mul(wb, f);
-                        } else {
-                            float s0, s1;
-                            f2_unpack(sc2[i], s0, s1);
-                            // 0 for a zero row (its weight is 0) and for a scale that is not finite (its weight is NaN
-                            // where it is attended)
-                            const uint64_t inv2 = f2_pack(s0 >= kTiny && s0 <= 3.402823466e38f ? __fdividef(1.f, s0) : 0.f,
-                                                          s1 >= kTiny && s1 <= 3.402823466e38f ? __fdividef(1.f, s1) : 0.f);
-                            za = f2_fma(wa, inv2, za);
-                            zb = f2_fma(wb, inv2, zb);
-                        }
-                        // pieces: hi in the low half, lo in the high half
-                        const uint32_t pa = split_weights(wa), pb = split_weights(wb);
-                        // neighbouring lanes hold neighbouring pairs of rows: each stores four rows of every other i
-                        const bool mine = (i & 1) == (lane & 1);
-                        if ((i & 1) == 0) {
-                            keep_a = pa;
-                            keep_b = pb;
-                        } else {
-                            const uint32_t ga = __shfl_xor_sync(0xffffffffu, mine ? keep_a : pa, 1), gb = __shfl_xor_sync(0xffffffffu, mine ? keep_b : pb, 1);
-                            const uint32_t oa = mine ? pa : keep_a, ob = mine ? pb : keep_b;
-                            // even lanes: rows of i - 1, own pair first; odd lanes: rows of i, the neighbour's first
-                            const uint32_t p = w_addr[i >> 1];
-                            st_shared_u32(p, __byte_perm(oa, ga, lo_first));
-                            st_shared_u32(p + kW / 2, __byte_perm(oa, ga, hi_first));
-                            st_shared_u32(p + 512, __byte_perm(ob, gb, lo_first));
-                            st_shared_u32(p + 512 + kW / 2, __byte_perm(ob, gb, hi_first));
-                        }
+                        const uint64_t wb = f2_pack(ex2_approx(e0), ex2_approx(e1));
+                        const uint64_t f = f2_mul(sc2[i], nm2);
+                        za = f2_add(za, wa);
+                        zb = f2_add(zb, wb);
+                        pa[i] = split_weights(f2_mul(wa, f));
+                        pb[i] = split_weights(f2_mul(wb, f));
                     }
-                    const float f = plain ? norm : 1.f;
-                    const float fa = __uint_as_float(byte_a << 23) * f, fb = __uint_as_float(byte_b << 23) * f;
+                    // neighbouring lanes hold neighbouring pairs of rows: each stores four rows of every other i
+                    const bool odd = lane & 1;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t oa = odd ? pa[2 * k + 1] : pa[2 * k], ob = odd ? pb[2 * k + 1] : pb[2 * k];
+                        const uint32_t ga = __shfl_xor_sync(0xffffffffu, odd ? pa[2 * k] : pa[2 * k + 1], 1);
+                        const uint32_t gb = __shfl_xor_sync(0xffffffffu, odd ? pb[2 * k] : pb[2 * k + 1], 1);
+                        // even lanes: rows of i = 2 k, own pair first; odd lanes: of i = 2 k + 1, the neighbour's first
+                        st_shared_u32(w_addr[k], __byte_perm(oa, ga, lo_first));
+                        st_shared_u32(w_addr[k] + kW / 2, __byte_perm(oa, ga, hi_first));
+                        st_shared_u32(w_addr[k] + 512, __byte_perm(ob, gb, lo_first));
+                        st_shared_u32(w_addr[k] + 512 + kW / 2, __byte_perm(ob, gb, hi_first));
+                    }
+                    const float fa = __uint_as_float(whole_bits(f_a) << 23) * nm, fb = __uint_as_float(whole_bits(f_b) << 23) * nm;
                     z_a = f2_fma(za, f2_pack(fa, fa), z_a);
                     z_b = f2_fma(zb, f2_pack(fb, fb), z_b);
                 }
