@@ -204,72 +204,91 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
 
 // Joins the parts of the cut groups: out = sum_p 2^(m_p - M) cl_p / (sum_p 2^(m_p - M) z_p + 2^-M sum_p n0_p) with
 // M = max_p m_p.
-// An item is one column of one cut group; 128 threads hold four dims each, two halves of the block take
-// alternate parts.
-constexpr int kMergeThreads = 256;
+// A warp takes 128 dims of one column of one cut group, four dims a lane, and reads its parts in order.  Where the warps
+// outnumber these (few columns, so many parts each), up to eight warps of a block share the parts.
+constexpr int kMergeWarps = 8;
 
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, int cols) {
-    __shared__ float wt[kMaxShares];
-    __shared__ float red[kMergeThreads / 32][2];
-    __shared__ float4 other[128];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a, int cols) {
+    __shared__ float4 other[kMergeWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int items = a.sched->jobs * cols;
-    const int64_t stride = (int64_t)tree_part_floats(cols);
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const TreeJob job = a.sched->job[it / cols];
-        const int c = it % cols;
-        const TreeSeq q = tree_seq(a.q_start, a.lens, job.b, a.R, tree_positions(a.max_pages, a.page_shift));
-        const int col = job.g * cols + c;
-        if (col >= q.n * a.H) continue;
-        // part p: the first CTA's second set, every other CTA's first
-        const float *base = a.part + (int64_t)job.first * 2 * stride;
-        auto part = [&](int p) { return base + (2 * p + (p == 0 ? 1 : 0)) * stride; };
-        float m = -INFINITY;
-        for (int p = tid; p < job.count; p += kMergeThreads) m = fmaxf(m, part(p)[cols * kKL + c]);
-        m = warp_max(m);
-        if (lane == 0) red[warp][0] = m;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kMergeThreads / 32; ++w) m = fmaxf(m, red[w][0]);
-        float z = 0.f, n0 = 0.f;
-        for (int p = tid; p < job.count; p += kMergeThreads) {
-            n0 += part(p)[cols * (kKL + 2) + c];
-            const float mp = part(p)[cols * kKL + c];
-            const float w = mp == -INFINITY ? 0.f : exp2f(mp - m);
-            wt[p] = w;
-            if (w != 0.f) z = fmaf(w, part(p)[cols * (kKL + 1) + c], z);
-        }
-        if (n0 != 0.f && m != -INFINITY) z = fmaf(n0, exp2f(-m), z);
-        z = warp_sum(z);
-        if (lane == 0) red[warp][1] = z;
-        __syncthreads();
-        z = 0.f;
-#pragma unroll
-        for (int w = 0; w < kMergeThreads / 32; ++w) z += red[w][1];
-        const int d4 = tid & 127, half = tid >> 7;
+    const int64_t tasks = (int64_t)a.sched->jobs * cols * 4, warps = (int64_t)gridDim.x * kMergeWarps;
+    int slices = kMergeWarps;
+    while (slices > 1 && tasks * slices > warps) slices >>= 1;
+    const int slice = warp & (slices - 1);
+    const int64_t stride = (int64_t)tree_part_floats(cols), positions = tree_positions(a.max_pages, a.page_shift);
+    for (int64_t first = (int64_t)blockIdx.x * (kMergeWarps / slices); first < tasks; first += warps / slices) {
+        const int64_t task = first + warp / slices;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int p = half; p < job.count; p += 2) {
-            const float w = wt[p];
-            if (w != 0.f) {  // a part that attended nothing may hold anything
-                const float4 v = *reinterpret_cast<const float4 *>(part(p) + c * kKL + 4 * d4);
-                acc.x = fmaf(w, v.x, acc.x);
-                acc.y = fmaf(w, v.y, acc.y);
-                acc.z = fmaf(w, v.z, acc.z);
-                acc.w = fmaf(w, v.w, acc.w);
+        float inv = 0.f;
+        int64_t at = -1;
+        if (task < tasks) {
+            const TreeJob job = a.sched->job[task / (4 * cols)];
+            const int c = (int)(task >> 2) % cols, d = ((int)task & 3) * 128 + lane * 4;
+            const TreeSeq q = tree_seq(a.q_start, a.lens, job.b, a.R, positions);
+            const int64_t col = (int64_t)job.g * cols + c;
+            if (col < (int64_t)q.n * a.H) {
+                at = ((int64_t)q.q0 * a.H + col) * kKL + d;
+                // part p: the first CTA's second set, every other CTA's first
+                const float *base = a.part + (int64_t)job.first * 2 * stride;
+                auto part = [&](int p) { return base + (2 * p + (p == 0 ? 1 : 0)) * stride; };
+                float m = -INFINITY;
+                for (int p = lane; p < job.count; p += 32) m = fmaxf(m, part(p)[cols * kKL + c]);
+                m = warp_max(m);
+                float z = 0.f, n0 = 0.f;
+                for (int p0 = 0; p0 < job.count; p0 += 32) {
+                    float w = 0.f;
+                    if (p0 + lane < job.count) {
+                        const float *mine = part(p0 + lane);
+                        n0 += mine[cols * (kKL + 2) + c];
+                        const float mp = mine[cols * kKL + c];
+                        if (mp != -INFINITY) w = exp2f(mp - m);
+                        if (w != 0.f) z = fmaf(w, mine[cols * (kKL + 1) + c], z);
+                    }
+                    const int n = min(32, job.count - p0);
+                    for (int i = slice; i < n; i += 4 * slices) {
+                        float4 v[4];
+                        float wi[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int j = i + k * slices;
+                            wi[k] = __shfl_sync(0xffffffffu, w, j & 31);
+                            if (j >= n) wi[k] = 0.f;
+                            // (a part that attended nothing may hold anything)
+                            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (wi[k] != 0.f) v[k] = *reinterpret_cast<const float4 *>(part(p0 + j) + c * kKL + d);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            acc.x = fmaf(wi[k], v[k].x, acc.x);
+                            acc.y = fmaf(wi[k], v[k].y, acc.y);
+                            acc.z = fmaf(wi[k], v[k].z, acc.z);
+                            acc.w = fmaf(wi[k], v[k].w, acc.w);
+                        }
+                    }
+                }
+                z = warp_sum(z);
+                n0 = warp_sum(n0);
+                if (n0 != 0.f && m != -INFINITY) z = fmaf(n0, exp2f(-m), z);
+                inv = z == 0.f ? 0.f : 1.f / z;
             }
         }
-        if (half) other[d4] = acc;
-        __syncthreads();
-        if (!half) {
-            const float4 o = other[d4];
-            const float inv = z == 0.f ? 0.f : 1.f / z;
-            acc.x = (acc.x + o.x) * inv;
-            acc.y = (acc.y + o.y) * inv;
-            acc.z = (acc.z + o.z) * inv;
-            acc.w = (acc.w + o.w) * inv;
-            const int64_t at = ((int64_t)q.q0 * a.H + col) * kKL + 4 * d4;
+        if (slices > 1) {  // (then every task has its warps: the loop runs once)
+            other[warp][lane] = acc;
+            __syncthreads();
+            for (int k = 1; k < slices; ++k) {
+                const float4 o = other[(warp & ~(slices - 1)) + k][lane];
+                acc.x += o.x;
+                acc.y += o.y;
+                acc.z += o.z;
+                acc.w += o.w;
+            }
+        }
+        if (slice == 0 && at >= 0) {
+            acc.x *= inv;
+            acc.y *= inv;
+            acc.z *= inv;
+            acc.w *= inv;
             if (a.out_bf16) {
                 __nv_bfloat162 v[2] = {__floats2bfloat162_rn(acc.x, acc.y), __floats2bfloat162_rn(acc.z, acc.w)};
                 *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = *reinterpret_cast<uint2 *>(v);
@@ -277,7 +296,6 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, i
                 *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = acc;
             }
         }
-        __syncthreads();
     }
 }
 
@@ -300,7 +318,7 @@ TreeWorkspace tree_workspace(int R, int H, int B, bool q_bf16) {
 cudaError_t launch_tree_merge(const TreeArgs &a, int cols, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.ctas * 4u);
-    cfg.blockDim = dim3(kMergeThreads);
+    cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

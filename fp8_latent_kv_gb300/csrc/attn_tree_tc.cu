@@ -41,7 +41,7 @@ using namespace sm100;
 constexpr int kCols = 64;
 constexpr int kRows = 64;
 constexpr int kStages = 5;
-constexpr int kSegment = 8;                // a segment's start and end cost about as much as this many tiles
+constexpr int kSegment = 16;               // a segment's start and end cost about as much as this many tiles
 constexpr int kTeams = 2;                  // softmax teams of 256 threads
 constexpr int kTeam = 256;
 constexpr int kSoftmax = kTeams * kTeam;
