@@ -29,7 +29,7 @@ struct Smem {
 };
 
 __global__ void __launch_bounds__(288) tree_sched_kernel(TreeArgs a) {
-    __shared__ int64_t scan[66];
+    __shared__ TreeScan scan;
     tree_schedule<kCols, kRows, 1>(a, scan);
 }
 

@@ -49,7 +49,7 @@ constexpr int kThreads = 128 + kSoftmax;
 constexpr uint32_t kBlk = 8192;            // 64 rows x 128 latent bytes (SW128)
 constexpr uint32_t kRope = 4096;           // 64 rows x 64 RoPE bytes (SW64)
 constexpr uint32_t kStage = 4 * kBlk + kRope;
-constexpr uint32_t kQLat = 128 * 448;      // a group's query image: 128 lanes x 448 latent bytes, row-major,
+constexpr uint32_t kQLat = 28 * 128 * 16;  // a group's query image: 28 chunks of 16 latent bytes of 128 lanes,
 constexpr uint32_t kQTail = 128 * 128;     // then 128 x (64 latent + 64 RoPE bytes) (SW128)
 constexpr uint32_t kImg = kQLat + kQTail;
 constexpr uint32_t kW = 8192;              // hi [64 columns][64 rows] (SW64), then lo
@@ -73,8 +73,8 @@ struct Misc {
         float top[kTeams][2][kCols];       // X of a team's two blocks
         float red[2 * kTeams][kCols];      // at the end: sums
     };
-    TreeSegment seg[2];                    // this segment and the next
-    int more[2];
+    TreeSegment seg[3];                    // this segment and the next two
+    int more[3];
     uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_free[2], s_full[kTeams], w_full[kTeams], pv_done[kTeams],
         q_ready, final_bar[2];
     uint32_t tmem_base;
@@ -226,7 +226,7 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
 // ------------------------------------------------------------------------------------------------------------
 // Byte offset of 16-byte chunk ch (32 latent, 4 RoPE) of a lane's query pieces.
 __device__ __forceinline__ uint32_t image_offset(int lane, int ch) {
-    return ch < 28 ? (uint32_t)lane * 448u + ch * 16u : kQLat + sw128_offset(lane, (ch - 28) * 16);
+    return ch < 28 ? (uint32_t)(ch * 128 + lane) * 16u : kQLat + sw128_offset(lane, (ch - 28) * 16);
 }
 
 constexpr int kPrepCols = 8, kPrepThreads = kPrepCols * 36;
@@ -234,7 +234,7 @@ constexpr int kPrepCols = 8, kPrepThreads = kPrepCols * 36;
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uint8_t *img, float *c_head) {
     grid_dependency_wait();
     grid_launch_dependents();
-    __shared__ int64_t scan[66];
+    __shared__ TreeScan scan;
     __shared__ int qmax_bits[kPrepCols];
     __shared__ int64_t pad_slot[kPrepCols];
     __shared__ int pad_from[kPrepCols];
@@ -607,32 +607,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ok = bar_wait(bar, parity, &ms.abort_flag, a.err_word);
         };
         grid_launch_dependents();
-        // a group's queries: the lane's 448 latent bytes to TMEM by the first four warps of each quadrant (the fourth: 64
-        // bytes), the part in shared memory by all
-        auto load_queries = [&](const TreeSegment &g) {
-            const uint8_t *img = x.img + (tree_slot(g.q.q0, a.H, g.b) + g.g) * kImg;
-            if (w16 < 4) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(img + (32 * q + lane) * 448 + w16 * 128);
-                uint4 v[8];
+        // a group's queries: the lane's 448 latent bytes to TMEM by way of the first four warps of each quadrant (the
+        // fourth: 64 bytes), the part in shared memory by a copy
+        auto image = [&](const TreeSegment &g) { return x.img + (tree_slot(g.q.q0, a.H, g.b) + g.g) * kImg; };
+        auto load_queries = [&](const TreeSegment &g, auto free) {
+            uint4 query[8];
+            const uint4 *src = reinterpret_cast<const uint4 *>(image(g)) + w16 * 8 * 128 + 32 * q + lane;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < 4 || w16 < 3) v[k] = __ldg(src + k);
+            for (int k = 0; k < 8; ++k)
+                if (k < 4 || w16 < 3) query[k] = __ldg(src + k * 128);
+            free();
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t w[16] = {v[4 * k].x,     v[4 * k].y,     v[4 * k].z,     v[4 * k].w,
-                                            v[4 * k + 1].x, v[4 * k + 1].y, v[4 * k + 1].z, v[4 * k + 1].w,
-                                            v[4 * k + 2].x, v[4 * k + 2].y, v[4 * k + 2].z, v[4 * k + 2].w,
-                                            v[4 * k + 3].x, v[4 * k + 3].y, v[4 * k + 3].z, v[4 * k + 3].w};
-                    if (k == 0 || w16 < 3) tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + w16 * 32 + 16 * k, w);
-                }
-                tmem_wait_st();
+            for (int k = 0; k < 2; ++k) {
+                const uint4 *v = query + 4 * k;
+                const uint32_t w[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
+                                        v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+                if (k == 0 || w16 < 3) tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + w16 * 32 + 16 * k, w);
             }
-            for (int k = st; k < (int)kQTail / 16; k += kSoftmax)
-                *reinterpret_cast<uint4 *>(smem + OFF_Q + k * 16) = __ldg(reinterpret_cast<const uint4 *>(img + kQLat) + k);
-            fence_proxy_async_smem();
+            tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.q_ready);
+            if (st == 0) {
+                mbar_arrive_expect_tx(&ms.q_ready, kQTail);
+                bulk_load(smem + OFF_Q, image(g) + kQLat, kQTail, &ms.q_ready);
+            } else if (lane == 0) {
+                mbar_arrive(&ms.q_ready);
+            }
         };
         // the value rows' factors are all 1
         if (w16 == 0) {
@@ -640,19 +640,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_32x32b_x2(tmem + lane_addr + TM_SFA + 2, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
             tmem_wait_st();
         }
-        // One thread walks the share, a segment ahead of the others.
-        if (st == 0) ms.more[0] = walk.next<kCols, kRows>(a, ms.seg[0]);
+        // One thread walks the share, two segments ahead of the others.
+        if (st == 0) {
+            ms.more[0] = walk.next<kCols, kRows>(a, ms.seg[0]);
+            ms.more[1] = walk.next<kCols, kRows>(a, ms.seg[1]);
+        }
         if (st < kCols) ms.ref[st] = -INFINITY;
         named_sync(1, kSoftmax);
-        if (ms.more[0]) load_queries(ms.seg[0]);
+        if (ms.more[0]) load_queries(ms.seg[0], [] {});
         int first_tile = 0;                    // tiles before the segment, modulo kTeams
         uint32_t own = 0;                      // the team's tiles so far
         int it = team, s_now = team;           // the team's next tile, and its stage
         uint32_t s_ph = 0;
         int end_tile = 0;                      // tiles up to the segment's end
-        for (int k = 0; ms.more[k & 1]; ++k) {
-            const TreeSegment &sg = ms.seg[k & 1];
-            if (st == 0) ms.more[(k + 1) & 1] = walk.next<kCols, kRows>(a, ms.seg[(k + 1) & 1]);
+        int segments = 0;
+        for (int now = 0; ms.more[now]; ++segments) {
+            const TreeSegment &sg = ms.seg[now];
+            const int next = now == 2 ? 0 : now + 1, third = 3 - now - next;
+            if (st == 0) ms.more[third] = walk.next<kCols, kRows>(a, ms.seg[third]);
             first_tile = end_tile;
             end_tile += sg.t1 - sg.t0;
             const int plain_end = first_tile + (int)min(sg.q.len / kRows - sg.t0, (int64_t)(end_tile - first_tile));  // tiles of context only
@@ -839,20 +844,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     z_b = f2_fma(zb, f2_pack(fb, fb), z_b);
                 }
                 // ---- rows that were not loaded, and NaN codes of drafted rows (attended columns have NaN weights
-                // already): a weight of 0 must not meet them.  A thread owns a row's 128 bytes of a latent block.
+                // already): a weight of 0 must not meet them.  (A swizzle keeps a row's 128 bytes together.)
                 if (!plain) {
-                    const int r = st & 63;
-                    const bool there = ri.in >> r & 1;
-                    if (!there || (int64_t)(sg.t0 + it - first_tile) * kRows + r >= sg.q.len) {
-                        // (complete since before the score: this makes the copy's bytes visible here too)
-                        (void)bar_wait(&ms.kv_full[s_now], s_ph, &ms.abort_flag, a.err_word);
-                        uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s_now * kStage + ((st >> 6) & 3) * kBlk + r * 128);
-                        uint4 v[8];
+                    // (complete since before the score: this makes the copy's bytes visible here too)
+                    (void)bar_wait(&ms.kv_full[s_now], s_ph, &ms.abort_flag, a.err_word);
+                    uint4 *p = reinterpret_cast<uint4 *>(smem + OFF_ST + s_now * kStage) + (st & (kTeam - 1));
+                    const int64_t left = sg.q.len - (int64_t)(sg.t0 + it - first_tile) * kRows;  // the tile's rows of context
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = there ? p[k] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            p[k] = make_uint4(without_nan(v[k].x), without_nan(v[k].y), without_nan(v[k].z), without_nan(v[k].w));
+                    for (int k = 0; k < (int)(4 * kBlk / 16 / kTeam); ++k) {
+                        const int r = ((st & (kTeam - 1)) + k * kTeam) >> 3 & (kRows - 1);
+                        const bool there = ri.in >> r & 1;
+                        if (there && r < left) continue;
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (there) v = p[k * kTeam];
+                        p[k * kTeam] = make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
                     }
                 }
                 if (slow && it > first_tile && __any_sync(0xffffffffu, move != 1.f)) {
@@ -895,6 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 
             // ---- output, and the next segment's queries: after the first barrier every score of this one is read
+            const bool more = ms.more[next];
             const int c0 = sg.g * kCols, nc = min(kCols, sg.q.n * a.H - c0);
             const bool whole = sg.first && sg.last;
             float *part = a.part + ((int64_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * tree_part_floats(kCols);
@@ -916,7 +922,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return v;
             };
             float nn = 0.f;
-            if (bar_red_or(1, kSoftmax, (zero_a | zero_b) != 0)) {
+            bool zeros = false;
+            auto all_read = [&] { zeros = bar_red_or(1, kSoftmax, (zero_a | zero_b) != 0); };
+            if (more) load_queries(ms.seg[next], all_read);
+            else all_read();
+            if (zeros) {
                 to_sets((float)zero_a, (float)zero_b);
                 named_sync(1, kSoftmax);
                 nn = over_sets(st & (kCols - 1)) * exp2f(-(float)kBase);
@@ -931,7 +941,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fb *= u + v;
                 to_sets(fa, fb);
             }
-            if (ms.more[(k + 1) & 1]) load_queries(ms.seg[(k + 1) & 1]);
             named_sync(1, kSoftmax);
             if (st < kCols) {
                 const float m_end = ms.ref[st], zz = over_sets(st);
@@ -987,7 +996,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before_sync();  // the accumulators are read before the next segment's first product
             named_sync(1, kSoftmax);
+            now = next;
         }
+        // the last copy of queries lands before the CTA ends
+        if (st == 0 && segments) bar_wait(&ms.q_ready, (segments - 1) & 1, nullptr, a.err_word, kLimit / 8);
     }
     tc_fence_before_sync();
     __syncthreads();

@@ -113,10 +113,15 @@ __device__ __forceinline__ uint64_t tree_attended(const TreeArgs &a, int q0, int
     return skip ? bits << skip | (((uint64_t)1 << skip) - 1) : bits;
 }
 
-// One block: the shares and the cut groups.  `scan`: 66 * 8 bytes of shared memory.
+// One block: the shares and the cut groups.
+struct TreeScan {  // in shared memory
+    int64_t v[66];
+    int64_t unit[kMaxShares + 1];  // the shares' `unit`
+};
 template <int kCols, int kRows, int kSegment>
-__device__ void tree_schedule(const TreeArgs &a, int64_t *scan) {
+__device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
     TreeSched &s = *a.sched;
+    int64_t *const scan = sm.v;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = (blockDim.x + 31) >> 5;
     const int64_t positions = tree_positions(a.max_pages, a.page_shift);
     const int per = (a.B + blockDim.x - 1) / blockDim.x;
@@ -203,17 +208,23 @@ __device__ void tree_schedule(const TreeArgs &a, int64_t *scan) {
             sh.unit = s.unit0[lo] + g * tiles + sh.t;
         }
         s.share[c] = sh;
+        sm.unit[c] = sh.unit;
     }
     __syncthreads();
     // a share that begins inside a group whose first tile the share before it walks: that group is cut
     for (int c = 1 + tid; c < C; c += blockDim.x) {
-        const TreeShare sh = s.share[c];
-        if (sh.t == 0 || sh.unit - sh.t < s.share[c - 1].unit) continue;
+        const TreeShare sh = s.share[c];  // (this thread's own)
+        if (sh.t == 0 || sh.unit - sh.t < sm.unit[c - 1]) continue;
         bool ignored = false;
         size_of(sh.b, ignored, groups, tiles);
-        int last = c;  // the share that holds the group's last tile
-        while (last + 1 < C && s.share[last + 1].unit < sh.unit - sh.t + tiles) ++last;
-        s.job[atomicAdd(&s.jobs, 1)] = TreeJob{sh.b, sh.g, c - 1, last - c + 2};
+        const int64_t end = sh.unit - sh.t + tiles;
+        int lo = c, hi = C;  // the share that holds the group's last tile: unit[lo] < end <= unit[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sm.unit[mid] < end) lo = mid;
+            else hi = mid;
+        }
+        s.job[atomicAdd(&s.jobs, 1)] = TreeJob{sh.b, sh.g, c - 1, lo - c + 2};
     }
 }
 
