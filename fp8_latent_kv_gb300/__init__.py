@@ -93,7 +93,7 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # (3 us less than by a Stream object)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

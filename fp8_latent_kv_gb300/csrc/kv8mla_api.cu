@@ -353,8 +353,9 @@ int kv8_tree_commit(int B, const int32_t *q_start, const int32_t *lens, const in
     if (!valid_batch(B, q_start, lens, 0) || !aligned(accept, 4) || !aligned(n_accept, 4) || max_accept < 1 ||
         max_accept > KV8_MAX_TREE || layers < 1 || layers > 65535 || !aligned(kv8, 16) || !aligned(kv_scale, 4) ||
         cache_rows < 1 || cache_rows > 0x7fffffffLL || !aligned(block_table, 4) || max_pages < 1 || shift < 0 ||
-        !aligned(new_lens, 4) || new_lens == lens)
+        !aligned(new_lens, 4))
         return KV8_EINVAL;
+    if (new_lens < lens + B && lens < new_lens + B) return KV8_EINVAL;  // other blocks still read them
     return status(launch_tree_commit(B, q_start, lens, accept, n_accept, max_accept, layers, kv8, kv_scale,
                                      cache_rows, block_table, max_pages, shift, new_lens, err_word,
                                      (cudaStream_t)stream));

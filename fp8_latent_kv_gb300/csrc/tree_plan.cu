@@ -11,8 +11,7 @@ namespace {
 // need_b = max(0, want_b - have_b) are taken; the places are exclusive prefix sums over the sequences, so the
 // result does not depend on the order in which warps run.
 // One thread-block cluster: every CTA computes all prefix sums for itself (a few words per sequence), returned
-// pages are written, the cluster meets, pages are taken from the list and the slots written, one warp per
-// sequence.  A second launch in place of the cluster's barrier would cost more than all of it.
+// pages are written, the cluster meets, pages are taken from the list and the slots written.  A second launch in place of the cluster's barrier would cost more than all of it.
 // ------------------------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = KV8_MAX_SEQS / kPlanThreads;  // sequences per thread in the scans
@@ -111,13 +110,17 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
     }
     if (broken) err |= KV8_ERR_INDEX;
     __syncthreads();
-    const int n_ctas = gridDim.x, w0 = blockIdx.x * 32 + warp, w_all = n_ctas * 32;
+    // a warp for each sequence where there are warps enough, else eight lanes: what a sequence needs is a chain of loads,
+    // so that four at once take the time of one
+    const int wide = a.B <= (int)gridDim.x * 32 ? 32 : 8, sub = lane & (wide - 1);
+    const uint32_t group = wide == 32 ? 0xffffffffu : 0xffu << (lane & ~7);
+    const int w0 = (blockIdx.x * 32 + warp) * (32 / wide) + lane / wide, w_all = gridDim.x * 32 * (32 / wide);
     // ---- returned pages: the k-th of sequence b stands spre + k places below the new top
     if (!broken)
         for (int b = w0; b < a.B; b += w_all) {
             const int w = want[b];
             const int surplus = w < 0 ? 0 : have[b] - w;
-            for (int k = lane; k < surplus; k += 32)
+            for (int k = sub; k < surplus; k += wide)
                 a.free_list[top - 1 - ((int64_t)spre[b] + k)] = a.table[(int64_t)b * a.max_pages + w + k];
         }
     cluster_sync_all();  // every count has been read and every returned page written
@@ -131,16 +134,16 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
             const bool ok = w >= 0 && (need == 0 || (int64_t)npre[b] + need <= top);
             int32_t *row = a.table + (int64_t)b * a.max_pages;
             if (ok) {
-                for (int k = lane; k < need; k += 32)
+                for (int k = sub; k < need; k += wide)
                     row[h + k] = *(volatile int32_t *)(a.free_list + (top - 1 - ((int64_t)npre[b] + k)));
-                if (lane == 0) a.n_pages[b] = w;
-            } else if (lane == 0 && w >= 0) {
+                if (sub == 0) a.n_pages[b] = w;
+            } else if (sub == 0 && w >= 0) {
                 err |= KV8_ERR_PAGES;
             }
-            __syncwarp();
+            __syncwarp(group);
             const int q0 = a.q_start[b], n = a.q_start[b + 1] - q0;
             const int64_t len = a.lens[b];
-            for (int i = lane; i < n; i += 32) {
+            for (int i = sub; i < n; i += wide) {
                 int64_t slot = -1;
                 if (ok) {
                     const int64_t pos = len + i;
@@ -228,9 +231,10 @@ __global__ void __launch_bounds__(32 * W) tree_mask_kernel(const int32_t *q_star
 // ------------------------------------------------------------------------------------------------------------
 constexpr int kCommitThreads = 288;  // 36 16-byte pieces of a row, eight rows at once
 constexpr int kCommitRows = 8;
+constexpr int kCommitLayers = 4;  // that a block moves at once
 
 struct CommitArgs {
-    int B, max_accept, layers, max_pages, page_shift;
+    int B, max_accept, layers, per_block, max_pages, page_shift;
     const int32_t *q_start, *lens, *accept, *n_accept, *table;
     uint8_t *kv8;
     float *kv_scale;
@@ -241,7 +245,7 @@ struct CommitArgs {
 
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(CommitArgs a) {
     __shared__ int64_t src[KV8_MAX_TREE], dst[KV8_MAX_TREE];
-    const int b = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
+    const int b = blockIdx.x, first = blockIdx.y * a.per_block, tid = threadIdx.x;
     const TreeSeq q = tree_seq(a.q_start, a.lens, b, 0x7fffffff, tree_positions(a.max_pages, a.page_shift));
     const int m = __ldg(a.n_accept + b);
     bool ok = q.n >= 0 && m >= 0 && m <= a.max_accept && m <= q.n;
@@ -261,27 +265,35 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(CommitArgs 
         }
     }
     ok = __syncthreads_and(ok);
-    if (layer == 0 && tid == 0) {
+    if (first == 0 && tid == 0) {
         a.new_lens[b] = __ldg(a.lens + b) + (ok ? m : 0);
         if (!ok && a.err_word) atomicOr(a.err_word, (int)KV8_ERR_INDEX);
     }
     if (!ok) return;
-    uint8_t *kv = a.kv8 + (int64_t)layer * a.cache_rows * kRow;
-    float *sc = a.kv_scale + (int64_t)layer * a.cache_rows;
-    const int piece = tid % 36, sub = tid / 36;
+    const int piece = tid % 36, sub = tid / 36, end = min(first + a.per_block, a.layers);
     for (int k0 = 0; k0 < m; k0 += kCommitRows) {
         const int k = k0 + sub;
         const bool moves = k < m && src[k] != dst[k];
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        float s = 0.f;
-        if (moves) {
-            v = *(reinterpret_cast<const uint4 *>(kv + src[k] * kRow) + piece);
-            if (piece == 0) s = sc[src[k]];
-        }
-        __syncthreads();
-        if (moves) {
-            *(reinterpret_cast<uint4 *>(kv + dst[k] * kRow) + piece) = v;
-            if (piece == 0) sc[dst[k]] = s;
+        for (int l0 = first; l0 < end; l0 += kCommitLayers) {
+            uint4 v[kCommitLayers];
+            float s[kCommitLayers];
+#pragma unroll
+            for (int l = 0; l < kCommitLayers; ++l) {
+                v[l] = make_uint4(0u, 0u, 0u, 0u);
+                s[l] = 0.f;
+                if (!moves || l0 + l >= end) continue;
+                const int64_t at = (int64_t)(l0 + l) * a.cache_rows + src[k];
+                v[l] = *(reinterpret_cast<const uint4 *>(a.kv8 + at * kRow) + piece);
+                if (piece == 0) s[l] = a.kv_scale[at];
+            }
+            __syncthreads();  // a row may be another's place
+#pragma unroll
+            for (int l = 0; l < kCommitLayers; ++l) {
+                if (!moves || l0 + l >= end) continue;
+                const int64_t at = (int64_t)(l0 + l) * a.cache_rows + dst[k];
+                *(reinterpret_cast<uint4 *>(a.kv8 + at * kRow) + piece) = v[l];
+                if (piece == 0) a.kv_scale[at] = s[l];
+            }
         }
         __syncthreads();
     }
@@ -337,9 +349,12 @@ cudaError_t launch_tree_commit(int B, const int32_t *q_start, const int32_t *len
                                const int32_t *n_accept, int max_accept, int layers, uint8_t *kv8, float *kv_scale,
                                int64_t cache_rows, const int32_t *table, int max_pages, int page_shift,
                                int32_t *new_lens, int *err_word, cudaStream_t st) {
-    CommitArgs a{B,     max_accept, layers,   max_pages,  page_shift, q_start, lens, accept, n_accept, table,
+    // one wave of blocks, each with the same number of layers
+    const int64_t wave = (int64_t)device_sm_count() * (2048 / kCommitThreads);
+    const int per = (int)(((int64_t)B * layers + wave - 1) / wave), blocks = (layers + per - 1) / per;
+    CommitArgs a{B,     max_accept, layers,   per,        max_pages, page_shift, q_start, lens, accept, n_accept, table,
                  kv8, kv_scale,   cache_rows, new_lens, err_word};
-    tree_commit_kernel<<<dim3((unsigned)B, (unsigned)layers), kCommitThreads, 0, st>>>(a);
+    tree_commit_kernel<<<dim3((unsigned)B, (unsigned)blocks), kCommitThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

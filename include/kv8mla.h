@@ -399,7 +399,7 @@ KV8_API int mla_absorb_tree8(const void *q_lat, const void *q_rope, int q_dtype,
  * copied to position lens[b] + k (bytes and scale), and new_lens[b] = lens[b] + n_accept[b].
  *   accept [B][max_accept] int32, strictly ascending within the first n_accept[b], each in [0, n_b).
  *   kv8 [layers][cache_rows][576], kv_scale [layers][cache_rows], one block table for all layers.
- *   new_lens [B] int32 out, must not be lens.  max_accept in [1, KV8_MAX_TREE]; layers in [1, 65535].
+ *   new_lens [B] int32 out, must not overlap lens.  max_accept in [1, KV8_MAX_TREE]; layers in [1, 65535].
  *   A branch that is not ascending or not in the draft, n_accept[b] outside [0, max_accept], a page
  *   outside the cache: nothing of the sequence moves, new_lens[b] = lens[b], KV8_ERR_INDEX.
  *   Sequences must not share the pages of the rows that move. */

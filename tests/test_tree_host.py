@@ -89,3 +89,13 @@ def test_binding_refuses_wrong_tensors(monkeypatch):
         kv._args("f", ("t", t, i32, (4, 6)))
     with pytest.raises(TypeError, match="bfloat16"):
         kv.mla_tree8_workspace_bytes(1, 1, 1, torch.float16)
+
+
+def test_commit_refuses_lengths_that_overlap(so):
+    """Blocks of other layers still read lens while new_lens is written."""
+    order = "B q_start lens accept n_accept most layers kv8 sc rows table pages page new st".split()
+    order.insert(order.index("st"), "err")
+    good = dict(B=4, q_start=FAKE, lens=FAKE, accept=FAKE, n_accept=FAKE, most=4, layers=1, kv8=FAKE, sc=FAKE, rows=1000,
+                table=FAKE, pages=5, page=64, new=FAKE, err=None, st=None)
+    for new in (FAKE, FAKE + 4, FAKE + 12, FAKE - 12):
+        assert call(so.kv8_tree_commit, good, order, new=new) == kv.KV8_EINVAL, new
