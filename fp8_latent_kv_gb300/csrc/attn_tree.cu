@@ -284,31 +284,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
 
 // Joins the parts of the cut groups: out = sum_p 2^(m_p - M) cl_p / (sum_p 2^(m_p - M) z_p + 2^-M sum_p n0_p) with
 // M = max_p m_p.
-// A warp takes 128 dims of one column of one cut group, four dims a lane, and reads its parts in order.  Where the warps
-// outnumber these (few columns, so many parts each), up to eight warps of a block share the parts.
+// A warp takes one column of one cut group and reads its parts in order: four dims a lane, 128 or all of them.  Where the
+// warps outnumber the columns (few columns, so many parts each), up to eight warps of a block share a quarter's parts.
 constexpr int kMergeWarps = 8;
 
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a, int cols) {
-    __shared__ float4 other[kMergeWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    grid_dependency_wait();
-    const int64_t tasks = (int64_t)a.sched->jobs * cols * 4, warps = (int64_t)gridDim.x * kMergeWarps;
-    int slices = kMergeWarps;
-    while (slices > 1 && tasks * slices > warps) slices >>= 1;
-    const int slice = warp & (slices - 1);
-    const int64_t stride = (int64_t)tree_part_floats(cols), positions = tree_positions(a.max_pages, a.page_shift);
+template <int kQuarters>
+__device__ __forceinline__ void merge_columns(const TreeArgs &a, int cols, int slices, float4 (*other)[32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slice = warp & (slices - 1);
+    constexpr int kPer = 4 / kQuarters;  // tasks a column
+    const int64_t tasks = (int64_t)a.sched->jobs * cols * kPer, warps = (int64_t)gridDim.x * kMergeWarps;
+    const int64_t stride = (int64_t)tree_part_floats(cols);
     for (int64_t first = (int64_t)blockIdx.x * (kMergeWarps / slices); first < tasks; first += warps / slices) {
         const int64_t task = first + warp / slices;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc[kQuarters];
+#pragma unroll
+        for (int t = 0; t < kQuarters; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
         float inv = 0.f;
         int64_t at = -1;
         if (task < tasks) {
-            const TreeJob job = a.sched->job[task / (4 * cols)];
-            const int c = (int)(task >> 2) % cols, d = ((int)task & 3) * 128 + lane * 4;
-            const TreeSeq q = tree_seq(a.q_start, a.lens, job.b, a.R, positions);
-            const int64_t col = (int64_t)job.g * cols + c;
-            if (col < (int64_t)q.n * a.H) {
-                at = ((int64_t)q.q0 * a.H + col) * kKL + d;
+            const TreeJob job = a.sched->job[task / (kPer * cols)];
+            const int c = (int)(task / kPer) % cols, d = (int)(task % kPer) * 128 + lane * 4;
+            if (c < job.cols) {
+                at = (job.col0 + c) * kKL + d;
                 // part p: the first CTA's second set, every other CTA's first
                 const float *base = a.part + (int64_t)job.first * 2 * stride;
                 auto part = [&](int p) { return base + (2 * p + (p == 0 ? 1 : 0)) * stride; };
@@ -320,31 +317,35 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a
                     float w = 0.f;
                     if (p0 + lane < job.count) {
                         const float *mine = part(p0 + lane);
+                        const float mp = mine[cols * kKL + c], zp = mine[cols * (kKL + 1) + c];
                         n0 += mine[cols * (kKL + 2) + c];
-                        const float mp = mine[cols * kKL + c];
                         if (mp != -INFINITY) w = exp2f(mp - m);
-                        if (w != 0.f) z = fmaf(w, mine[cols * (kKL + 1) + c], z);
+                        if (w != 0.f) z = fmaf(w, zp, z);
                     }
                     const int n = min(32, job.count - p0);
-                    for (int i = slice; i < n; i += 4 * slices) {
-                        float4 v[4];
-                        float wi[4];
+                    constexpr int kAhead = kQuarters == 1 ? 4 : 2;
+                    for (int i = slice; i < n; i += kAhead * slices) {
+                        float4 v[kAhead][kQuarters];
+                        float wi[kAhead];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < kAhead; ++k) {
                             const int j = i + k * slices;
                             wi[k] = __shfl_sync(0xffffffffu, w, j & 31);
                             if (j >= n) wi[k] = 0.f;
-                            // (a part that attended nothing may hold anything)
-                            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (wi[k] != 0.f) v[k] = *reinterpret_cast<const float4 *>(part(p0 + j) + c * kKL + d);
+                            const float4 *src = reinterpret_cast<const float4 *>(part(p0 + j) + c * kKL + d);
+#pragma unroll
+                            for (int t = 0; t < kQuarters; ++t)  // (a part that attended nothing may hold anything)
+                                v[k][t] = wi[k] != 0.f ? src[32 * t] : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            acc.x = fmaf(wi[k], v[k].x, acc.x);
-                            acc.y = fmaf(wi[k], v[k].y, acc.y);
-                            acc.z = fmaf(wi[k], v[k].z, acc.z);
-                            acc.w = fmaf(wi[k], v[k].w, acc.w);
-                        }
+                        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                            for (int t = 0; t < kQuarters; ++t) {
+                                acc[t].x = fmaf(wi[k], v[k][t].x, acc[t].x);
+                                acc[t].y = fmaf(wi[k], v[k][t].y, acc[t].y);
+                                acc[t].z = fmaf(wi[k], v[k][t].z, acc[t].z);
+                                acc[t].w = fmaf(wi[k], v[k][t].w, acc[t].w);
+                            }
                     }
                 }
                 z = warp_sum(z);
@@ -353,30 +354,39 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a
                 inv = z == 0.f ? 0.f : 1.f / z;
             }
         }
-        if (slices > 1) {  // (then every task has its warps: the loop runs once)
-            other[warp][lane] = acc;
+        if (slices > 1) {  // (one quarter, and every task has its warps: the loop runs once)
+            other[warp][lane] = acc[0];
             __syncthreads();
             for (int k = 1; k < slices; ++k) {
                 const float4 o = other[(warp & ~(slices - 1)) + k][lane];
-                acc.x += o.x;
-                acc.y += o.y;
-                acc.z += o.z;
-                acc.w += o.w;
+                acc[0].x += o.x;
+                acc[0].y += o.y;
+                acc[0].z += o.z;
+                acc[0].w += o.w;
             }
         }
-        if (slice == 0 && at >= 0) {
-            acc.x *= inv;
-            acc.y *= inv;
-            acc.z *= inv;
-            acc.w *= inv;
+        if (slice != 0 || at < 0) continue;
+#pragma unroll
+        for (int t = 0; t < kQuarters; ++t) {
+            const float4 o = make_float4(acc[t].x * inv, acc[t].y * inv, acc[t].z * inv, acc[t].w * inv);
             if (a.out_bf16) {
-                __nv_bfloat162 v[2] = {__floats2bfloat162_rn(acc.x, acc.y), __floats2bfloat162_rn(acc.z, acc.w)};
-                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = *reinterpret_cast<uint2 *>(v);
+                __nv_bfloat162 v[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at + 128 * t) = *reinterpret_cast<uint2 *>(v);
             } else {
-                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = acc;
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + 128 * t) = o;
             }
         }
     }
+}
+
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(TreeArgs a, int cols) {
+    __shared__ float4 other[kMergeWarps][32];
+    grid_dependency_wait();
+    const int64_t columns = (int64_t)a.sched->jobs * cols, warps = (int64_t)gridDim.x * kMergeWarps;
+    int slices = kMergeWarps;
+    while (slices > 1 && 4 * columns * slices > warps) slices >>= 1;
+    if (4 * columns > warps) merge_columns<4>(a, cols, 1, other);
+    else merge_columns<1>(a, cols, slices, other);
 }
 
 }  // namespace

@@ -41,8 +41,10 @@ struct TreeShare {
     int pad;
 };
 struct TreeJob {  // a group that was cut
-    int b, g;
+    int64_t col0;      // its first column's place among the step's rows times heads
+    int cols;
     int first, count;  // the CTAs first .. first + count - 1 hold its parts
+    int pad;
 };
 constexpr int kMaxShares = 512;
 struct TreeSched {
@@ -52,7 +54,6 @@ struct TreeSched {
     TreeShare share[kMaxShares + 1];  // [shares] ends the last one
     TreeJob job[kMaxShares];
     int64_t unit0[KV8_MAX_SEQS + 1];  // tiles before sequence b
-    int64_t work0[KV8_MAX_SEQS + 1];  // work before sequence b
 };
 
 struct TreeArgs {
@@ -116,7 +117,8 @@ __device__ __forceinline__ uint64_t tree_attended(const TreeArgs &a, int q0, int
 // One block: the shares and the cut groups.
 struct TreeScan {  // in shared memory
     int64_t v[66];
-    int64_t unit[kMaxShares + 1];  // the shares' `unit`
+    int64_t unit[kMaxShares + 1];      // the shares' `unit`
+    int64_t work0[KV8_MAX_SEQS + 1];   // work before sequence b
 };
 template <int kCols, int kRows, int kSegment>
 __device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
@@ -172,7 +174,7 @@ __device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
     for (int b = b0; b < b1; ++b) {
         bool ignored = false;
         s.unit0[b] = u_at;
-        s.work0[b] = w_at;
+        sm.work0[b] = w_at;
         size_of(b, ignored, groups, tiles);
         u_at += groups * tiles;
         w_at += groups * (tiles + kSegment);
@@ -181,7 +183,7 @@ __device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
     const int C = (int)min((int64_t)a.ctas, U);
     if (tid == 0) {
         s.unit0[a.B] = U;
-        s.work0[a.B] = W;
+        sm.work0[a.B] = W;
         s.jobs = 0;
         s.shares = C;
     }
@@ -195,12 +197,12 @@ __device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
             int lo = 0, hi = a.B;  // work0[lo] <= w < work0[hi]: the last such sequence, so it has work
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (s.work0[mid] <= w) lo = mid;
+                if (sm.work0[mid] <= w) lo = mid;
                 else hi = mid;
             }
             bool ignored = false;
             size_of(lo, ignored, groups, tiles);
-            const int64_t r = w - s.work0[lo], g = r / (tiles + kSegment), t = r - g * (tiles + kSegment) - kSegment;
+            const int64_t r = w - sm.work0[lo], g = r / (tiles + kSegment), t = r - g * (tiles + kSegment) - kSegment;
             // (a cut in a group's start and end cost is one before its first tile)
             sh.b = lo;
             sh.g = (int)g;
@@ -224,7 +226,10 @@ __device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
             if (sm.unit[mid] < end) lo = mid;
             else hi = mid;
         }
-        s.job[atomicAdd(&s.jobs, 1)] = TreeJob{sh.b, sh.g, c - 1, lo - c + 2};
+        const TreeSeq q = tree_seq(a.q_start, a.lens, sh.b, a.R, positions);
+        const int64_t at = (int64_t)sh.g * kCols;
+        s.job[atomicAdd(&s.jobs, 1)] =
+            TreeJob{(int64_t)q.q0 * a.H + at, (int)min((int64_t)kCols, (int64_t)q.n * a.H - at), c - 1, lo - c + 2, 0};
     }
 }
 
