@@ -171,10 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
             if (c < nc)
                 v = k4 < kKL / 4 ? __ldg(static_cast<const float4 *>(a.q_lat) + (q_base + c) * (kKL / 4) + k4)
                                  : __ldg(static_cast<const float4 *>(a.q_rope) + (q_base + c) * (kKR / 4) + (k4 - kKL / 4));
-            sm.q[4 * k4][c] = v.x;
-            sm.q[4 * k4 + 1][c] = v.y;
-            sm.q[4 * k4 + 2][c] = v.z;
-            sm.q[4 * k4 + 3][c] = v.w;
+            sm.q[4 * k4][c] = tree_query(v.x);
+            sm.q[4 * k4 + 1][c] = tree_query(v.y);
+            sm.q[4 * k4 + 2][c] = tree_query(v.z);
+            sm.q[4 * k4 + 3][c] = tree_query(v.w);
         }
         uint64_t acc[8][4];
 #pragma unroll
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
         const bool whole = seg.first && seg.last;
         float *part = a.part + ((int64_t)blockIdx.x * 2 + (seg.first ? 1 : 0)) * tree_part_floats(kCols);
         if (!whole && warp == 0 && lane < nc) {
-            part[kCols * kKL + lane] = m_run;
+            part[kCols * kKL + lane] = tree_part_exponent(m_run, z);
             part[kCols * (kKL + 1) + lane] = z;
             part[kCols * (kKL + 2) + lane] = 0.f;
         }

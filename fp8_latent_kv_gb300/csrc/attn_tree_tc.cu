@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
     }
     __syncthreads();
     if (mine) {
-        const float mx = __int_as_float(qmax_bits[cl]);
+        const float mx = fminf(__int_as_float(qmax_bits[cl]), 3.402823466e38f);
         int E = 0;
         if (mx > 0.f) frexpf(mx, &E);
         const int sh = mx > 0.f ? 8 - E : 0;  // max |q| 2^sh in [128, 256); values are scaled: 2^sh may overflow
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
         for (int e = 0; e < 8; ++e) {
             const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
             uint32_t ph, pl;
-            split_pair(ldexpf(f.x, sh), ldexpf(f.y, sh), ph, pl);
+            split_pair(ldexpf(tree_query(f.x), sh), ldexpf(tree_query(f.y), sh), ph, pl);
             hi[e >> 1] |= ph << ((e & 1) * 16);
             lo[e >> 1] |= pl << ((e & 1) * 16);
         }
@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float all = nn == 0.f ? zz : zz + nn * exp2f(m_end == -INFINITY ? 0.f : -m_end);
                 ms.zinv[st] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
                 if (!whole) {
-                    part[kCols * kKL + st] = m_end;
+                    part[kCols * kKL + st] = tree_part_exponent(m_end, zz);
                     part[kCols * (kKL + 1) + st] = zz;
                     part[kCols * (kKL + 2) + st] = nn;
                 }

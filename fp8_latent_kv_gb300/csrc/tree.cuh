@@ -80,12 +80,18 @@ struct TreeArgs {
 // A partial set: cl and z relative to 2^m, and n0, the weight (relative to 2^0) of rows that only count in the sum.
 __host__ __device__ constexpr size_t tree_part_floats(int cols) { return (size_t)cols * (kKL + 3); }
 
+// The exponent that a partial set is stored with: a set of NaN sums may have none (-inf), which would count as nothing.
+__device__ __forceinline__ float tree_part_exponent(float m, float z) { return z == z ? m : fmaxf(m, 0.f); }
+
 // Cache row of position t of sequence b, or -1 where its page is outside the cache.
 __device__ __forceinline__ int64_t tree_row(const TreeArgs &a, int b, int64_t t) {
     const int64_t page = __ldg(a.table + (int64_t)b * a.max_pages + (t >> a.page_shift));
     const int64_t row = (page << a.page_shift) + (t & (((int64_t)1 << a.page_shift) - 1));
     return page >= 0 && row < a.cache_rows ? row : -1;
 }
+
+// A query's element: infinities count as NaN (an infinite score has no softmax).
+__device__ __forceinline__ float tree_query(float v) { return fabsf(v) <= 3.402823466e38f ? v : __int_as_float(0x7fffffff); }
 
 // Whether drafted token i of a sequence whose rows begin at q0 attends drafted token j.
 __device__ __forceinline__ bool tree_sees(const TreeArgs &a, int q0, int i, int j) {

@@ -170,6 +170,31 @@ def test_any_bits_empty_rows_and_garbage_where_nobody_attends(lib, oracle, q_dty
 
 
 @pytest.mark.parametrize("q_dtype", [BF, F32])
+def test_queries_that_are_not_finite(lib, oracle, q_dtype):
+    """A NaN or an infinity of either sign in a (token, head)'s query, latent or RoPE, makes that output NaN and leaves
+    every other as it was; a token that attends nothing gives zeros all the same."""
+    rng = np.random.default_rng(31)
+    H, lens, n, page = 24, [130, 0], [5, 3], 64
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    sees = [np.tril(np.ones((m, m), bool)) for m in n]
+    sees[1][1] = False
+    mask = np.concatenate([pack(s, 1) for s in sees])
+    q = queries(rng, sum(n), H, q_dtype == F32)
+    q[6, 0, 7] = 0.0
+    ref, _ = run_tree(lib, q, q_dtype, F32, n, lens, mask, kv8, scale, table, page)
+    bad = [(0, 0, 3, np.nan), (1, 5, 511, np.inf), (2, 23, 512, -np.inf), (4, 9, 575, np.nan), (5, 2, 100, -np.inf)]
+    hit = np.zeros((sum(n), H), bool)
+    for r, h, k, v in bad:
+        q[r, h, k] = v
+        hit[r, h] = True
+    q[6, 0, 7] = np.inf           # attends nothing
+    got, err = run_tree(lib, q, q_dtype, F32, n, lens, mask, kv8, scale, table, page)
+    assert err == 0
+    assert np.isnan(got[hit]).all()
+    assert np.array_equal(got[~hit], ref[~hit]) and not got[6].any()
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
 def test_zero_and_tiny_rows_count_in_the_softmax(lib, oracle, q_dtype):
     """Rows of zeros (scale 0), of a subnormal maximum, and of magnitudes eleven binary orders apart."""
     rng = np.random.default_rng(6)

@@ -84,16 +84,6 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
             unit = np.where(sm_ <= 256 * sl, np.maximum(unit, 2 * pm * sm_), unit)
             off = (2.0 ** -8 + 2.0 ** -12) * ps + 2.0 ** -10 * unit[:, block] / 128
             tol[i] += off @ np.abs(TABLE[kv8[rows[on]]][:, :512])
-        # exp(2 d) - 1 for every row, weighted as the terms are, twice: numerator and denominator
-        e = np.expm1(2 * d)
-        tol[i] = (p * e) @ np.abs(kk[:, :512]) + (p * e).sum(1)[:, None] * A
-        tol[i] += A * (2.0 ** -21 + (2 * T + 64) * 2.0 ** -24)
-        if not f32:
-            ps = p * scale[rows[on]].astype(np.float64)
-            unit = ps.max(1, keepdims=True) / 32
-            w = ps / np.where(unit > 0, unit, 1)
-            off = 2.0 ** -7 * w + np.minimum(2.0 ** -13, w / 8) + 2.0 ** -17 + 2.0 ** -11 * w
-            tol[i] += (off * unit) @ np.abs(TABLE[kv8[rows[on]]][:, :512])
         tol[i] += out_eps * (np.abs(out[i]) + tol[i]) + 1e-30
     return out, tol
 
