@@ -530,6 +530,32 @@ def test_commit(lib, layers, page, n):
     assert np.array_equal(k.cpu().numpy().reshape(want.shape), want) and np.array_equal(s.cpu().numpy().reshape(want_s.shape), want_s)
 
 
+@pytest.mark.parametrize("B,layers", [(135, 40), (40, 61), (1100, 3)])
+def test_commit_of_several_layers_by_a_block(lib, B, layers):
+    """More (sequence, layer) pairs than blocks that fit the device at once."""
+    g = torch.Generator(device=DEV).manual_seed(B)
+    page, n, most = 16, 9, 9
+    lens = torch.arange(B, device=DEV) * 5 % 23
+    table = torch.randperm(2 * B, generator=g, device=DEV).view(B, 2)
+    kv8 = torch.randint(0, 256, (layers, 2 * B * page, 576), generator=g, dtype=torch.uint8, device=DEV)
+    scale = torch.rand((layers, 2 * B * page), generator=g, device=DEV)
+    count = torch.arange(B, device=DEV) % (n + 1)
+    accept = torch.rand((B, n), generator=g, device=DEV).argsort(1)
+    k = torch.arange(n, device=DEV)
+    accept = torch.where(k < count[:, None], accept, n).sort(1).values
+    on = k < count[:, None]
+    row = lambda t: table.gather(1, t // page) * page + t % page  # noqa: E731
+    src, dst = row(torch.where(on, lens[:, None] + accept, 0))[on], row(torch.where(on, lens[:, None] + k, 0))[on]
+    want, want_s = kv8.clone(), scale.clone()
+    want[:, dst], want_s[:, dst] = kv8[:, src], scale[:, src]
+    new, err = torch.empty(B, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    to = torch.int32
+    lib.kv8_tree_commit((torch.arange(B + 1, device=DEV) * n).to(to), lens.to(to), accept.to(to), count.to(to), kv8, scale,
+                        table.to(to), page, new, err_word=err)
+    assert err.item() == 0 and torch.equal(new.long(), lens + count)
+    assert torch.equal(kv8, want) and torch.equal(scale, want_s)
+
+
 @pytest.mark.parametrize("accept,count,table", [([2, 2, 4], 3, [0, 1]), ([3, 1, 4], 3, [0, 1]), ([0, 1, 6], 3, [0, 1]),
                                                 ([-1, 1, 2], 3, [0, 1]), ([0, 1, 2], 4, [0, 1]), ([0, 1, 2], -1, [0, 1]),
                                                 ([1, 2, 3], 3, [0, 9]), ([1, 2, 3], 3, [0, -1])])
