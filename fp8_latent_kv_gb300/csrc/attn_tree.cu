@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(288) tree_sched_kernel(TreeArgs a) {
     __shared__ TreeScan scan;
     grid_dependency_wait();
     grid_launch_dependents();
-    tree_schedule<kCols, kUnit, 1>(a, scan);
+    tree_schedule<kCols, kUnit, 1, 1>(a, scan);  // (two units a share instead of one: 46 -> 54 us for 4 x 5 tokens of 16 heads)
 }
 
 // 16 bytes global -> shared, zeros where `there` is false (the address must be valid all the same).

@@ -41,6 +41,9 @@ using namespace sm100;
 constexpr int kCols = 64;
 constexpr int kRows = 64;
 constexpr int kStages = 5;
+// A share is at least two tiles where there is less work than shares: the teams take one each at the same time, and
+// half as many partial sets are written and joined (one token over 4096 rows: 22.0 us with one tile, 19.6 with two, 20.1 with four).
+constexpr int kLeast = 2;
 constexpr int kSegment = 16;               // a segment's start and end cost about as much as this many tiles
 constexpr int kTeams = 2;                  // softmax teams of 256 threads
 constexpr int kTeam = 256;
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
     __shared__ int pad_from[kPrepCols];
     const int tid = threadIdx.x;
     if (blockIdx.x == 0) {
-        tree_schedule<kCols, kRows, kSegment>(a, scan);
+        tree_schedule<kCols, kRows, kSegment, kLeast>(a, scan);
         return;
     }
     const int64_t col0 = (int64_t)(blockIdx.x - 1) * kPrepCols;
@@ -716,15 +719,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the rows that the columns attend: those that are there, of the draft those of their masks
                     nm = 1.f;
                     K = 0.f;
-                    const uint64_t in = ri.in, zr = ri.zero;
+                    const uint32_t in = (uint32_t)(ri.in >> r0), zr = (uint32_t)(ri.zero >> r0);
                     const int64_t j0 = (int64_t)(sg.t0 + it - first_tile) * kRows - sg.q.len;  // the tile's first row's index in the draft
                     const int c0 = sg.g * kCols, top = sg.q.n * a.H;
                     uint32_t on[2];  // bits 8 i and 8 i + 1 of each column
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint64_t att = in & tree_attended(a, sg.q.q0, min(c0 + (h ? n_b : n_a), top - 1) / a.H, j0);
-                        (h ? zero_b : zero_a) += __popcll(att & zr & (0x03030303ull << r0));
-                        on[h] = (uint32_t)((att & ~zr) >> r0);
+                        on[h] = in & (uint32_t)(tree_attended(a, sg.q.q0, min(c0 + (h ? n_b : n_a), top - 1) / a.H, j0) >> r0);
+                        (h ? zero_b : zero_a) += __popc(on[h] & zr & 0x03030303u);
+                        on[h] &= ~zr;
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

@@ -126,7 +126,7 @@ struct TreeScan {  // in shared memory
     int64_t unit[kMaxShares + 1];      // the shares' `unit`
     int64_t work0[KV8_MAX_SEQS + 1];   // work before sequence b
 };
-template <int kCols, int kRows, int kSegment>
+template <int kCols, int kRows, int kSegment, int kLeast>
 __device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
     TreeSched &s = *a.sched;
     int64_t *const scan = sm.v;
@@ -186,7 +186,7 @@ __device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
         w_at += groups * (tiles + kSegment);
     }
     const int64_t U = scan[n_warps - 1], W = scan[33 + n_warps - 1];
-    const int C = (int)min((int64_t)a.ctas, U);
+    const int C = (int)min((int64_t)a.ctas, (U + kLeast - 1) / kLeast);
     if (tid == 0) {
         s.unit0[a.B] = U;
         sm.work0[a.B] = W;
