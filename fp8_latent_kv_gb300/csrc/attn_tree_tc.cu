@@ -90,7 +90,7 @@ static_assert(offsetof(Misc, kv_full) % 8 == 0 && OFF_MISC % 1024 == 0 && OFF_W 
 struct TcArgs {
     TreeArgs t;
     const uint8_t *img;    // query images, one kImg for each group
-    const float *c_head;   // [images][64]: sm_scale * log2(e) * 2^-e of the column's query
+    const float *c_head;   // [images][64]: |sm_scale| * log2(e) * 2^-e of the column's query
 };
 
 // A sequence's groups' images begin at slot q0 * H / 64 + b: never past the next sequence's first.
@@ -291,12 +291,13 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
         int E = 0;
         if (mx > 0.f) frexpf(mx, &E);
         const int sh = mx > 0.f ? 8 - E : 0;  // max |q| 2^sh in [128, 256); values are scaled: 2^sh may overflow
+        const float sign = a.sm_scale_log2 < 0.f ? -1.f : 1.f;  // the column's factor is not negative
         uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
             uint32_t ph, pl;
-            split_pair(ldexpf(tree_query(f.x), sh), ldexpf(tree_query(f.y), sh), ph, pl);
+            split_pair(ldexpf(sign * tree_query(f.x), sh), ldexpf(sign * tree_query(f.y), sh), ph, pl);
             hi[e >> 1] |= ph << ((e & 1) * 16);
             lo[e >> 1] |= pl << ((e & 1) * 16);
         }
@@ -307,7 +308,8 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
         *reinterpret_cast<uint4 *>(dst + off_hi) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(dst + off_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (ch == 0) {
-            c_head[slot * kCols + n] = mx > 0.f ? ldexpf(a.sm_scale_log2, E - 8) : a.sm_scale_log2;
+            const float c = fabsf(a.sm_scale_log2);
+            c_head[slot * kCols + n] = mx > 0.f ? ldexpf(c, E - 8) : c;
             if (col == q.n * a.H - 1) {  // the sequence's last column: the rest of its group is zeros
                 pad_slot[cl] = slot;
                 pad_from[cl] = n + 1;
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lo_first = lane & 1 ? 0x1054u : 0x5410u, hi_first = lane & 1 ? 0x3276u : 0x7632u;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (ok) ok = bar_wait(bar, parity, &ms.abort_flag, a.err_word);
+            ok &= bar_wait(bar, parity, &ms.abort_flag, a.err_word);
         };
         grid_launch_dependents();
         // a group's queries: the lane's 448 latent bytes to TMEM by way of the first four warps of each quadrant (the
@@ -689,27 +691,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.s_free[it & 1]);
-                // ---- scores (log2 units), row pairs packed: 0..3 of column a, 4..7 of column b
+                // ---- dot products, row pairs packed: 0..3 of column a, 4..7 of column b
                 uint64_t d2[8], sc2[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 sc = *reinterpret_cast<const float2 *>(&ri.scale[r0 + 8 * i]);
                     sc2[i] = f2_pack(sc.x, sc.y);
-                    const uint64_t sa = f2_add(f2_pack(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
-                                               f2_pack(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])));
-                    const uint64_t sb = f2_add(f2_pack(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])),
-                                               f2_pack(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])));
-                    d2[i] = f2_mul(sa, f2_mul(sc2[i], f2_pack(c_a, c_a)));
-                    d2[4 + i] = f2_mul(sb, f2_mul(sc2[i], f2_pack(c_b, c_b)));
+                    d2[i] = f2_add(f2_pack(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
+                                   f2_pack(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])));
+                    d2[4 + i] = f2_add(f2_pack(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])),
+                                       f2_pack(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])));
                 }
                 // ---- X of the block, over the column's four lanes: in a plain tile floor(max score) + K, else floor(max e)
-                float max_a = -INFINITY, max_b = -INFINITY, K, nm;
+                // (c is not negative, so that the largest d2 makes the largest score)
+                float max_a = -INFINITY, max_b = -INFINITY, K, nm, ca = 1.f, cb = 1.f;  // scores: ca d2, cb d2 (log2 units)
                 if (plain) {
                     nm = ri.norm[set];
                     K = -log2_whole(nm);
+                    ca = c_a;
+                    cb = c_b;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float e0, e1;
+                        d2[i] = f2_mul(d2[i], sc2[i]);
+                        d2[4 + i] = f2_mul(d2[4 + i], sc2[i]);
                         f2_unpack(d2[i], e0, e1);
                         max_a = fmaxf(max_a, fmaxf(e0, e1));
                         f2_unpack(d2[4 + i], e0, e1);
@@ -733,8 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) {
                         float s[2], e[2][2];
                         f2_unpack(sc2[i], s[0], s[1]);
-                        f2_unpack(d2[i], e[0][0], e[0][1]);
-                        f2_unpack(d2[4 + i], e[1][0], e[1][1]);
+                        f2_unpack(f2_mul(d2[i], f2_mul(sc2[i], f2_pack(c_a, c_a))), e[0][0], e[0][1]);
+                        f2_unpack(f2_mul(d2[4 + i], f2_mul(sc2[i], f2_pack(c_b, c_b))), e[1][0], e[1][1]);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             // a scale that is not a number must not meet the weight 0 of a column that leaves the row out,
@@ -756,8 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 max_a = fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 1));
                 max_b = fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 1));
-                max_a = floorf(fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 2))) + K;
-                max_b = floorf(fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 2))) + K;
+                max_a = floorf(ca * fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, 2))) + K;
+                max_b = floorf(cb * fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 2))) + K;
                 // the context product of the team's tile before has read its weight buffer and factors (and the exponents
                 // that they were made from)
                 if (own > 0) wait(&ms.pv_done[team], own_ph ^ 1u);
@@ -813,15 +818,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (nothing attended so far: the scores are -inf throughout, whatever is subtracted)
                     const float xa = na == -INFINITY ? 7.f : (float)(kBase + 7) - na - f_a + K;
                     const float xb = nb == -INFINITY ? 7.f : (float)(kBase + 7) - nb - f_b + K;
-                    const uint64_t ra = f2_pack(xa, xa), rb = f2_pack(xb, xb), nm2 = f2_pack(nm, nm);
+                    const uint64_t ra = f2_pack(xa, xa), rb = f2_pack(xb, xb), ca2 = f2_pack(ca, ca), cb2 = f2_pack(cb, cb), nm2 = f2_pack(nm, nm);
                     uint64_t za = f2_pack(0.f, 0.f), zb = za;
                     uint32_t pa[4], pb[4];  // pieces: hi in the low half, lo in the high half
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float e0, e1;
-                        f2_unpack(f2_add(d2[i], ra), e0, e1);
+                        f2_unpack(f2_fma(d2[i], ca2, ra), e0, e1);
                         const uint64_t wa = f2_pack(ex2_approx(e0), ex2_approx(e1));
-                        f2_unpack(f2_add(d2[4 + i], rb), e0, e1);
+                        f2_unpack(f2_fma(d2[4 + i], cb2, rb), e0, e1);
                         const uint64_t wb = f2_pack(ex2_approx(e0), ex2_approx(e1));
                         const uint64_t f = f2_mul(sc2[i], nm2);
                         za = f2_add(za, wa);
