@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 max_b = floorf(cb * fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, 2))) + K;
                 // the context product of the team's tile before has read its weight buffer and factors (and the exponents
                 // that they were made from)
-                if (own > 0) wait(&ms.pv_done[team], own_ph ^ 1u);
+                wait(&ms.pv_done[team], own_ph ^ 1u);  // (passes at once before the first)
                 float(*const tops)[kCols] = ms.top[team];
                 if ((lane & 3) == 0) {
                     tops[set][n_a] = max_a;
@@ -829,8 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         f2_unpack(f2_fma(d2[4 + i], cb2, rb), e0, e1);
                         const uint64_t wb = f2_pack(ex2_approx(e0), ex2_approx(e1));
                         const uint64_t f = f2_mul(sc2[i], nm2);
-                        za = f2_add(za, wa);
-                        zb = f2_add(zb, wb);
+                        za = i == 0 ? wa : f2_add(za, wa);
+                        zb = i == 0 ? wb : f2_add(zb, wb);
                         pa[i] = split_weights(f2_mul(wa, f));
                         pb[i] = split_weights(f2_mul(wb, f));
                     }
