@@ -61,7 +61,7 @@ __device__ __forceinline__ void partial_scores(Smem &sm, const uint8_t (*tile)[k
     for (int j = 0; j < kGroups; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[j][c] = 0;
-#pragma unroll 2
+#pragma unroll 6
     for (int k = 0; k < kSlice; ++k) {
         const int w = warp * kSlice + k;
         ulonglong2 q[4][2];
@@ -96,7 +96,7 @@ __device__ __forceinline__ void partial_scores(Smem &sm, const uint8_t (*tile)[k
 // a warp.  kDraft: a drafted row may hold NaN codes where a column does not attend it (weight 0).
 template <bool kDraft>
 __device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kTileStride], int rows, int c0, int d0, uint64_t (*acc)[4]) {
-#pragma unroll 2
+#pragma unroll 4
     for (int r = 0; r < rows; ++r) {
         const uint2 b = *reinterpret_cast<const uint2 *>(&tile[r][d0]);
         float f[8];
