@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms.w_full[k], kTeam / 32);
             mbar_init(&ms.pv_done[k], 1);
         }
-        mbar_init(&ms.q_ready, kSoftmax / 32);
+        mbar_init(&ms.q_ready, kTeam / 32);
         mbar_init(&ms.final_bar[0], 1);
         mbar_init(&ms.final_bar[1], 1);
         ms.abort_flag = 0;
@@ -612,27 +612,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok &= bar_wait(bar, parity, &ms.abort_flag, a.err_word);
         };
         grid_launch_dependents();
-        // a group's queries: the lane's 448 latent bytes to TMEM by way of the first four warps of each quadrant (the
-        // fourth: 64 bytes), the part in shared memory by a copy
+        // a group's queries: a quarter of the lane's 448 latent bytes to TMEM (the last: 64 bytes)
         auto image = [&](const TreeSegment &g) { return x.img + (tree_slot(g.q.q0, a.H, g.b) + g.g) * kImg; };
-        auto load_queries = [&](const TreeSegment &g, auto free) {
+        auto load_queries = [&](const TreeSegment &g, int quarter) {
             uint4 query[8];
-            const uint4 *src = reinterpret_cast<const uint4 *>(image(g)) + w16 * 8 * 128 + 32 * q + lane;
+            const uint4 *src = reinterpret_cast<const uint4 *>(image(g)) + quarter * 8 * 128 + 32 * q + lane;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (k < 4 || w16 < 3) query[k] = __ldg(src + k * 128);
-            free();
+                if (k < 4 || quarter < 3) query[k] = __ldg(src + k * 128);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const uint4 *v = query + 4 * k;
                 const uint32_t w[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
                                         v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
-                if (k == 0 || w16 < 3) tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + w16 * 32 + 16 * k, w);
+                if (k == 0 || quarter < 3) tmem_st_32x32b_x16(tmem + lane_addr + TM_Q + quarter * 32 + 16 * k, w);
             }
+        };
+        // and by each warp of one team, after the barriers that order the quarters: the part in shared memory, by a copy
+        auto queries_ready = [&](const TreeSegment &g) {
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (st == 0) {
+            if ((st & (kTeam - 1)) == 0) {
                 mbar_arrive_expect_tx(&ms.q_ready, kQTail);
                 bulk_load(smem + OFF_Q, image(g) + kQLat, kQTail, &ms.q_ready);
             } else if (lane == 0) {
@@ -652,7 +653,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (st < kCols) ms.ref[st] = -INFINITY;
         named_sync(1, kSoftmax);
-        if (ms.more[0]) load_queries(ms.seg[0], [] {});
+        if (ms.more[0]) {
+            load_queries(ms.seg[0], w16);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            named_sync(1, kSoftmax);
+            if (team == 0) queries_ready(ms.seg[0]);
+        }
         int first_tile = 0;                    // tiles before the segment, modulo kTeams
         uint32_t own = 0;                      // the team's tiles so far
         int it = team, s_now = team;           // the team's next tile, and its stage
@@ -907,8 +914,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
 
-            // ---- output, and the next segment's queries: after the first barrier every score of this one is read
-            const bool more = ms.more[next];
+            // ---- the next segment's queries, by the team that the last tile is not: the last score has read this one's
+            if (ms.more[next] && ((uint32_t)(end_tile - 1) % kTeams) != (uint32_t)team) {
+                wait(&ms.s_full[team ^ 1], ((uint32_t)(end_tile - 1) / kTeams) & 1u);
+                tc_fence_after_sync();
+                load_queries(ms.seg[next], 2 * set);
+                load_queries(ms.seg[next], 2 * set + 1);
+                queries_ready(ms.seg[next]);
+            }
+            // ---- output
             const int c0 = sg.g * kCols, nc = min(kCols, sg.q.n * a.H - c0);
             const bool whole = sg.first && sg.last;
             float *part = a.part + ((int64_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * tree_part_floats(kCols);
@@ -930,11 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return v;
             };
             float nn = 0.f;
-            bool zeros = false;
-            auto all_read = [&] { zeros = bar_red_or(1, kSoftmax, (zero_a | zero_b) != 0); };
-            if (more) load_queries(ms.seg[next], all_read);
-            else all_read();
-            if (zeros) {
+            if (bar_red_or(1, kSoftmax, (zero_a | zero_b) != 0)) {
                 to_sets((float)zero_a, (float)zero_b);
                 named_sync(1, kSoftmax);
                 nn = over_sets(st & (kCols - 1)) * exp2f(-(float)kBase);
