@@ -96,9 +96,6 @@ struct TcArgs {
 // A sequence's groups' images begin at slot q0 * H / 64 + b: never past the next sequence's first.
 __host__ __device__ __forceinline__ int64_t tree_slot(int64_t q0, int H, int b) { return q0 * H / kCols + b; }
 
-// Lane of column n's piece (0 = hi, 1 = lo).
-__device__ __forceinline__ int query_lane(int n, int piece) { return (n >> 4) * 32 + piece * 16 + (n & 15); }
-
 // Arrive at a named barrier that other threads wait at.
 __device__ __forceinline__ void named_arrive(int id, int count) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
@@ -224,110 +221,119 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
 }
 
 // ------------------------------------------------------------------------------------------------------------
-// Query images, column factors, and (block 0) the work shares.  A block splits eight consecutive (row, head)
-// columns, 36 threads each.
+// Query images, column factors, and (block 0) the work shares.  A block splits 16 columns of a group, two by each warp:
+// their pieces are 32 consecutive lanes of the image, so that by way of shared memory whole lines are written.
 // ------------------------------------------------------------------------------------------------------------
-// Byte offset of 16-byte chunk ch (32 latent, 4 RoPE) of a lane's query pieces.
-__device__ __forceinline__ uint32_t image_offset(int lane, int ch) {
-    return ch < 28 ? (uint32_t)(ch * 128 + lane) * 16u : kQLat + sw128_offset(lane, (ch - 28) * 16);
-}
+constexpr int kPrepCols = 16, kPrepWarps = 8, kPrepThreads = 32 * kPrepWarps;
+constexpr int kPieceStride = 33;  // 16-byte units of a chunk's 32 lanes, and one against bank conflicts
 
-constexpr int kPrepCols = 8, kPrepThreads = kPrepCols * 36;
+// 16 bf16 elements times 2^sh -> 16 bytes of hi pieces and of lo pieces
+__device__ __forceinline__ void split_chunk(const uint4 (&u)[2], float f0, float f1, uint4 &hi, uint4 &lo) {
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+    uint32_t h[4] = {0u, 0u, 0u, 0u}, l[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float x = __uint_as_float(w[e] << 16) * f0 * f1, y = __uint_as_float(w[e] & 0xFFFF0000u) * f0 * f1;
+        uint32_t ph, pl;
+        split_pair(x, y, ph, pl);
+        h[e >> 1] |= ph << ((e & 1) * 16);
+        l[e >> 1] |= pl << ((e & 1) * 16);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// The largest magnitude of 16 bf16 elements, as its bits (NaN above infinity above numbers).
+__device__ __forceinline__ uint32_t chunk_max(const uint4 (&u)[2]) {
+    uint32_t m = 0;
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = __vmaxu2(m, w[e] & 0x7FFF7FFFu);
+    return max(m >> 16, m & 0xFFFFu);
+}
 
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uint8_t *img, float *c_head) {
     grid_dependency_wait();
     grid_launch_dependents();
-    __shared__ TreeScan scan;
-    __shared__ int qmax_bits[kPrepCols];
-    __shared__ int64_t pad_slot[kPrepCols];
-    __shared__ int pad_from[kPrepCols];
-    const int tid = threadIdx.x;
+    __shared__ union {
+        TreeScan scan;
+        struct {
+            uint4 piece[28 * kPieceStride];  // 28 latent chunks of 32 lanes
+            uint4 tail[32 * 8];              // the lanes' 128 bytes, swizzled
+        };
+    } sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (blockIdx.x == 0) {
-        tree_schedule<kCols, kRows, kSegment, kLeast>(a, scan);
+        tree_schedule<kCols, kRows, kSegment, kLeast>(a, sm.scan);
         return;
     }
-    const int64_t col0 = (int64_t)(blockIdx.x - 1) * kPrepCols;
-    const int cl = tid / 36, ch = tid - cl * 36;
-    const int64_t gc = col0 + cl;
-    const int row = (int)(gc / a.H), head = (int)(gc - (int64_t)row * a.H);
-    if (tid < kPrepCols) {
-        qmax_bits[tid] = 0;
-        pad_from[tid] = kCols;
+    const int64_t slot = (blockIdx.x - 1) / (kCols / kPrepCols);
+    const int quarter = (blockIdx.x - 1) % (kCols / kPrepCols);
+    // the slot's sequence: the last one whose images begin at or before it
+    int b = -1;
+    for (int k0 = 0; k0 < a.B; k0 += kPrepThreads) {
+        const int k = k0 + tid;
+        b += __syncthreads_count(k < a.B && tree_slot(__ldg(a.q_start + k), a.H, k) <= slot);
     }
-    // the sequence of the block's first column: how many sequences end at or before its row
-    int b = 0;
+    if (b < 0) return;
+    const TreeSeq q = tree_seq(a.q_start, a.lens, b, a.R, tree_positions(a.max_pages, a.page_shift));
+    const int64_t col0 = (slot - tree_slot(q.q0, a.H, b)) * kCols + quarter * kPrepCols, cols = (int64_t)q.n * a.H;
+    // (a group's columns that the sequence does not have are zeros)
+    if (q.n <= 0 || col0 < 0 || col0 - quarter * kPrepCols >= cols) return;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    // a warp's two columns: 32 chunks of latent elements by lane, four of RoPE elements by lanes 0..3 and 4..7
+    uint4 u[3][2];
+    const int64_t at = (int64_t)q.q0 * a.H + col0 + 2 * warp;
+    const bool mine[2] = {col0 + 2 * warp < cols, col0 + 2 * warp + 1 < cols};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint4 *src = static_cast<const uint4 *>(a.q_lat) + (at + k) * (kKL / 8) + 2 * lane;
+        u[k][0] = mine[k] ? __ldg(src) : zero;
+        u[k][1] = mine[k] ? __ldg(src + 1) : zero;
+    }
+    const int rope = lane >> 2;
+    const bool has = rope < 2 && mine[rope & 1];
     {
-        const int row0 = (int)(col0 / a.H);
-        for (int k0 = 0; k0 < a.B; k0 += kPrepThreads) {
-            const int k = k0 + tid;
-            b += __syncthreads_count(k < a.B && __ldg(a.q_start + k + 1) <= row0);
-        }
+        const uint4 *src = static_cast<const uint4 *>(a.q_rope) + (at + (rope & 1)) * (kKR / 8) + 2 * (lane & 3);
+        u[2][0] = has ? __ldg(src) : zero;
+        u[2][1] = has ? __ldg(src + 1) : zero;
     }
-    while (b < a.B && __ldg(a.q_start + b + 1) <= row) ++b;
-    bool mine = row < a.R && b < a.B;
-    TreeSeq q{};
-    if (mine) {
-        q = tree_seq(a.q_start, a.lens, b, a.R, tree_positions(a.max_pages, a.page_shift));
-        mine = q.n > 0 && row >= q.q0 && row < q.q0 + q.n;
-    }
-    uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    if (mine) {
-        const __nv_bfloat16 *src = ch < 32 ? static_cast<const __nv_bfloat16 *>(a.q_lat) + gc * kKL + ch * 16
-                                           : static_cast<const __nv_bfloat16 *>(a.q_rope) + gc * kKR + (ch - 32) * 16;
-        const uint4 u0 = __ldg(reinterpret_cast<const uint4 *>(src)), u1 = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
-        w[0] = u0.x; w[1] = u0.y; w[2] = u0.z; w[3] = u0.w;
-        w[4] = u1.x; w[5] = u1.y; w[6] = u1.z; w[7] = u1.w;
-        float mx = 0.f;
+    const uint32_t m_rope = chunk_max(u[2]);
+    float f0[2], f1[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
-            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-        atomicMax(&qmax_bits[cl], __float_as_int(mx));  // non-negative floats order like ints
-    }
-    __syncthreads();
-    if (mine) {
-        const float mx = fminf(__int_as_float(qmax_bits[cl]), 3.402823466e38f);
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, max(chunk_max(u[k]), rope == k ? m_rope : 0u));
+        const float mx = __uint_as_float(bits << 16);
         int E = 0;
-        if (mx > 0.f) frexpf(mx, &E);
-        const int sh = mx > 0.f ? 8 - E : 0;  // max |q| 2^sh in [128, 256); values are scaled: 2^sh may overflow
-        const float sign = a.sm_scale_log2 < 0.f ? -1.f : 1.f;  // the column's factor is not negative
-        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+        if (bits != 0u && bits < 0x7F80u) frexpf(mx, &E);
+        const int sh = bits != 0u && bits < 0x7F80u ? 8 - E : 0;  // max |q| 2^sh in [128, 256)
+        const int half = min(sh, 127);                            // (sh from -120 to 140)
+        const float sign = a.sm_scale_log2 < 0.f ? -1.f : 1.f;    // the column's factor is not negative
+        // a query with a NaN or an infinity: every piece is NaN
+        f0[k] = bits < 0x7F80u ? sign * __int_as_float((127 + half) << 23) : NAN;
+        f1[k] = __int_as_float((127 + sh - half) << 23);
+        const int n = quarter * kPrepCols + 2 * warp + k;
+        if (lane == 0) c_head[slot * kCols + n] = mine[k] ? ldexpf(fabsf(a.sm_scale_log2), -sh) : 0.f;
+    }
+    const int l0 = 2 * warp;  // the columns' hi lanes are l0 and l0 + 1, their lo lanes 16 on
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
-            uint32_t ph, pl;
-            split_pair(ldexpf(sign * tree_query(f.x), sh), ldexpf(sign * tree_query(f.y), sh), ph, pl);
-            hi[e >> 1] |= ph << ((e & 1) * 16);
-            lo[e >> 1] |= pl << ((e & 1) * 16);
-        }
-        const int col = (row - q.q0) * a.H + head, n = col % kCols;
-        const int64_t slot = tree_slot(q.q0, a.H, b) + col / kCols;
-        uint8_t *dst = img + slot * kImg;
-        const uint32_t off_hi = image_offset(query_lane(n, 0), ch), off_lo = image_offset(query_lane(n, 1), ch);
-        *reinterpret_cast<uint4 *>(dst + off_hi) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(dst + off_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if (ch == 0) {
-            const float c = fabsf(a.sm_scale_log2);
-            c_head[slot * kCols + n] = mx > 0.f ? ldexpf(c, E - 8) : c;
-            if (col == q.n * a.H - 1) {  // the sequence's last column: the rest of its group is zeros
-                pad_slot[cl] = slot;
-                pad_from[cl] = n + 1;
-            }
+    for (int k = 0; k < 3; ++k) {
+        uint4 hi, lo;
+        const bool second = k == 1 || (k == 2 && rope == 1);
+        split_chunk(u[k], second ? f0[1] : f0[0], second ? f1[1] : f1[0], hi, lo);
+        const int l = l0 + (second ? 1 : 0), ch = k < 2 ? lane : 32 + (lane & 3);
+        if (ch < 28) {
+            sm.piece[ch * kPieceStride + l] = hi;
+            sm.piece[ch * kPieceStride + l + 16] = lo;
+        } else if (k < 2 || rope < 2) {
+            sm.tail[sw128_offset(l, (ch - 28) * 16) / 16] = hi;
+            sm.tail[sw128_offset(l + 16, (ch - 28) * 16) / 16] = lo;
         }
     }
     __syncthreads();
-    for (int c = 0; c < kPrepCols; ++c) {
-        const int from = pad_from[c], cols = kCols - from;
-        if (cols <= 0) continue;
-        uint8_t *dst = img + pad_slot[c] * kImg;
-        for (int i = tid; i < cols * 72; i += kPrepThreads) {
-            const int n = from + i / 72, p = i % 72;
-            const uint32_t off = image_offset(query_lane(n, p / 36), p % 36);
-            *reinterpret_cast<uint4 *>(dst + off) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        for (int n = from + tid; n < kCols; n += kPrepThreads) c_head[pad_slot[c] * kCols + n] = 0.f;
-    }
+    uint8_t *dst = img + slot * kImg;
+    for (int i = tid; i < 28 * 32; i += kPrepThreads)
+        *reinterpret_cast<uint4 *>(dst + ((i >> 5) * 128 + quarter * 32 + (i & 31)) * 16) = sm.piece[(i >> 5) * kPieceStride + (i & 31)];
+    *reinterpret_cast<uint4 *>(dst + kQLat + quarter * 32 * 128 + tid * 16) = sm.tail[tid];
 }
 
 // ------------------------------------------------------------------------------------------------------------
@@ -1058,7 +1064,7 @@ cudaError_t launch_tree_tc(const TreeArgs &a, void *images, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(1 + ((int64_t)a.R * a.H + kPrepCols - 1) / kPrepCols));
+    cfg.gridDim = dim3((unsigned)(1 + slots * (kCols / kPrepCols)));
     cfg.blockDim = dim3(kPrepThreads);
     cfg.stream = st;
     cfg.attrs = attr;
