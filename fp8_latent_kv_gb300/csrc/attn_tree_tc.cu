@@ -41,10 +41,14 @@ using namespace sm100;
 constexpr int kCols = 64;
 constexpr int kRows = 64;
 constexpr int kStages = 5;
+// A segment's start and end cost as much as eight tiles, its draft's tile included.  Ragged sequences are where it shows: 16
+// sequences of 64 tokens took 1799 us with 4, 1646 with 6, 1573 with 8, 1582 with 12, 1597 with 16; 32 of 13 tokens and 16
+// heads 80.5, 78.8, 79.6, 82.1, 84.4.
+constexpr int kSegment = 8;
 // A share is at least two tiles where there is less work than shares: the teams take one each at the same time, and
-// half as many partial sets are written and joined (one token over 4096 rows: 22.0 us with one tile, 19.6 with two, 20.1 with four).
+// half as many partial sets are written and joined (one token over 4096 rows: 22.0 us with one tile, 19.6 with two, 20.1
+// with four).
 constexpr int kLeast = 2;
-constexpr int kSegment = 16;               // a segment's start and end cost about as much as this many tiles
 constexpr int kTeams = 2;                  // softmax teams of 256 threads
 constexpr int kTeam = 256;
 constexpr int kSoftmax = kTeams * kTeam;
