@@ -1,9 +1,14 @@
-// attn_tree.cu -- attention of drafted tokens over a paged latent cache: the CUDA-core kernel for f32
-// queries, and the merge of the groups that a share boundary cuts.
+// attn_tree.cu -- attention of drafted tokens over a paged latent cache: the kernel for f32 queries, and the merge of the
+// groups that a share boundary cuts.
 //
 // For column (token i, head h) of a sequence and row t:  s_t = sm_scale * scale_t * q.e4m3(row_t),
 // out = sum_t 2^((s_t - m) log2 e) scale_t e4m3(Lc_t) / sum_t 2^((s_t - m) log2 e), one pass over the rows with
 // the running maximum m.  All columns of a sequence read the same rows.
+//
+// The products run on the tensor cores with f16 operands, which hold every e4m3 value: a query element, scaled by its
+// column's power of two, is the sum of two f16 values to 2^-22 of itself (or 2^-39 of the column's largest), and so is a
+// weight p * scale, scaled by a power of two for its column and step.  The sums are kept in f32: the context's over 64 rows
+// at most in the tensor core, whose additions are not rounded to nearest, then by f32 additions.
 #include "sm100.cuh"
 #include "tree.cuh"
 
@@ -19,23 +24,26 @@ constexpr int kUnit = 32;      // rows that the shares count
 constexpr int kRows = 64;      // rows per step: two units where there are two
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTileStride = 592;           // bytes: 16-byte copies, and 148 words put eight consecutive rows into eight banks
-constexpr int kQStride = kCols + 4;        // words: 16-byte loads, four-way instead of 32-way conflicts where it is filled
-constexpr int kSlice = kRow / 4 / kWarps;  // words of a row that a warp's part of the scores covers
-static_assert(kSlice * 4 * kWarps == kRow, "a row's words by warp");
+// Strides in bytes.  A tile's: 16-byte copies, and 148 words put eight rows' four words into 32 banks.  A query column's and a
+// weight column's: four columns' four 8-byte pieces in 128 bytes of banks (the weights': nearly, for the stores' sake).
+constexpr int kTileStride = 592, kQStride = 2 * kRow + 32, kWStride = 2 * kRows + 40;
+constexpr int kSStride = kCols + 8;        // words
+constexpr int kSteps = kRow / 16 / 4;      // 16-byte steps of a row that a warp's part of the scores covers
+static_assert(kSteps * 64 == kRow, "a row's quarters");
 
 struct Smem {
-    float q[kRow][kQStride];               // the columns' queries, transposed
-    uint8_t tile[2][kRows][kTileStride];   // this step's cache rows and the next's; rows that are left out are zero
+    alignas(16) uint8_t q[2][kCols][kQStride];  // the columns' queries: f16 pieces
+    alignas(16) uint8_t tile[2][kRows][kTileStride];  // this step's cache rows and the next's; rows left out are zero
     union {
-        float s[kWarps][kRows][kCols];     // the warps' parts of the dot products
-        float2 p[kRows][kCols];            // weights p * scale, twice each
+        float s[4][kRows][kSStride];       // the dot products, by quarter of the row
+        alignas(16) uint8_t w[2][kCols][kWStride];  // weights: f16 pieces, a 16-row step's rows as 0 1 8 9 2 3 10 11 ...
     };
     int64_t row[kRows];                    // of the next step: cache row, or -1
-    float scale[2][kRows];
+    float scale[2][kRows], log_scale[2][kRows];
     uint8_t there[2][kRows];
-    float m_part[kWarps][kCols];
-    float corr[kCols];
+    float m_part[kWarps][kCols], e_part[kWarps][kCols];
+    float corr[kCols], unit[kCols];        // the accumulators' factor, the step's weights'
+    float factor[kCols];                   // scores: sm_scale log2(e) / the column's power of two
 };
 
 __global__ void __launch_bounds__(288) tree_sched_kernel(TreeArgs a) {
@@ -51,79 +59,124 @@ __device__ __forceinline__ void copy_16(void *dst, const void *src, bool there) 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// Dot products: warp w takes words 18 w .. 18 w + 17 of every row, so that a thread's 8 rows (rg + 8 j) by 8 columns
-// (8 cg + ..) use a loaded value eight times; the parts are summed through shared memory.  kGroups groups of 8 rows.
-template <int kGroups>
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
+    return r;
+}
+// d += a b: a [16][16], b [16][8] f16, d [16][8] f32.  Lane 4 g + c holds of a rows g and g + 8, columns 2 c, 2 c + 1 (a0, a1)
+// and 8 on (a2, a3); of b column g, the same rows (b0, b1); of d rows g (d0, d1) and g + 8, columns 2 c, 2 c + 1.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two values -> f16 pieces: the nearest, and the nearest to what is left.
+__device__ __forceinline__ void split_f16(float x, float y, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// Dot products: a warp takes 32 rows and a quarter of their bytes against all columns, a thread's four bytes of a 16-byte
+// step standing for rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of the contraction on both sides.
 __device__ __forceinline__ void partial_scores(Smem &sm, const uint8_t (*tile)[kTileStride], int warp, int lane) {
-    const int rg = lane & 7, cg = lane >> 3;
-    uint64_t acc[kGroups][4];
+    const int g = lane >> 2, c = lane & 3, r0 = 32 * (warp & 1) + g, part = warp >> 1;
+    float acc[2][4][4];
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[j][c] = 0;
-#pragma unroll 6
-    for (int k = 0; k < kSlice; ++k) {
-        const int w = warp * kSlice + k;
-        ulonglong2 q[4][2];
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            q[e][0] = *reinterpret_cast<const ulonglong2 *>(&sm.q[4 * w + e][8 * cg]);
-            q[e][1] = *reinterpret_cast<const ulonglong2 *>(&sm.q[4 * w + e][8 * cg + 4]);
-        }
+            for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+#pragma unroll 3
+    for (int k = 0; k < kSteps; ++k) {
+        const int at = 16 * (part * kSteps + k) + 4 * c;
+        uint32_t a[2][4];
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-            float v[4];
-            e4m3x4_to_f32(*reinterpret_cast<const uint32_t *>(&tile[rg + 8 * j][4 * w]), v[0], v[1], v[2], v[3]);
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint64_t vv = f2_pack(v[e], v[e]);
-                acc[j][0] = f2_fma(q[e][0].x, vv, acc[j][0]);
-                acc[j][1] = f2_fma(q[e][0].y, vv, acc[j][1]);
-                acc[j][2] = f2_fma(q[e][1].x, vv, acc[j][2]);
-                acc[j][3] = f2_fma(q[e][1].y, vv, acc[j][3]);
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t v = *reinterpret_cast<const uint32_t *>(&tile[r0 + 16 * m + 8 * i][at]);
+                a[m][i] = e4m3x2_to_f16x2(v);
+                a[m][2 + i] = e4m3x2_to_f16x2(v >> 16);
             }
-        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int piece = 1; piece >= 0; --piece) {
+                const uint2 b = *reinterpret_cast<const uint2 *>(&sm.q[piece][8 * n + g][2 * at]);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) mma_f16(acc[m][n], a[m], b.x, b.y);
+            }
     }
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-        ulonglong2 *dst = reinterpret_cast<ulonglong2 *>(&sm.s[warp][rg + 8 * j][8 * cg]);
-        dst[0] = make_ulonglong2(acc[j][0], acc[j][1]);
-        dst[1] = make_ulonglong2(acc[j][2], acc[j][3]);
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<float2 *>(&sm.s[part][r0 + 16 * m + 8 * i][8 * n + 2 * c]) = make_float2(acc[m][n][2 * i], acc[m][n][2 * i + 1]);
+}
+
+// acc = acc * corr + weights x rows * unit: a warp has all columns by 64 latent dims.  Of its 32 dims h a thread's bytes
+// 4 g .. 4 g + 3 of two rows make the operand's pairs for four products of 8 dims (4 g + n, g < 8); so it ends with columns
+// g + 8 i + 16 m, dims 8 c + n and 8 c + 4 + n.
+__device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kTileStride], int steps, int warp, int lane, float (&acc)[2][2][4][4]) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float t[2][4][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[m][n][i] = 0.f;
+#pragma unroll 2
+        for (int k = 0; k < steps; ++k) {
+            uint32_t b[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t *src = &tile[16 * k + 8 * i + 2 * c][64 * warp + 32 * h + 4 * g];
+                const uint32_t x = *reinterpret_cast<const uint32_t *>(src), y = *reinterpret_cast<const uint32_t *>(src + kTileStride);
+                const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
+                b[i][0] = e4m3x2_to_f16x2(lo);
+                b[i][1] = e4m3x2_to_f16x2(lo >> 16);
+                b[i][2] = e4m3x2_to_f16x2(hi);
+                b[i][3] = e4m3x2_to_f16x2(hi >> 16);
+            }
+#pragma unroll
+            for (int piece = 1; piece >= 0; --piece)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(&sm.w[piece][16 * m + g][32 * k + 8 * c]);
+                    const uint2 v = *reinterpret_cast<const uint2 *>(&sm.w[piece][16 * m + 8 + g][32 * k + 8 * c]);
+                    const uint32_t a[4] = {u.x, v.x, u.y, v.y};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) mma_f16(t[m][n], a, b[0][n], b[1][n]);
+                }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float f = sm.corr[16 * m + 8 * i + g], u = sm.unit[16 * m + 8 * i + g];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    acc[h][m][n][2 * i] = fmaf(acc[h][m][n][2 * i], f, t[m][n][2 * i] * u);
+                    acc[h][m][n][2 * i + 1] = fmaf(acc[h][m][n][2 * i + 1], f, t[m][n][2 * i + 1] * u);
+                }
+            }
     }
 }
 
-// acc += weights x rows: a thread holds 8 columns (8 (warp % 4) + ..) by 8 latent dims, a row's weights are the same for
-// a warp.  kDraft: a drafted row may hold NaN codes where a column does not attend it (weight 0).
-template <bool kDraft>
-__device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kTileStride], int rows, int c0, int d0, uint64_t (*acc)[4]) {
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-        const uint2 b = *reinterpret_cast<const uint2 *>(&tile[r][d0]);
-        float f[8];
-        e4m3x4_to_f32(b.x, f[0], f[1], f[2], f[3]);
-        e4m3x4_to_f32(b.y, f[4], f[5], f[6], f[7]);
-        uint64_t v[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) v[d] = f2_pack(f[2 * d], f[2 * d + 1]);
-#pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-            const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&sm.p[r][c0 + c]);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint64_t wt = u ? w.y : w.x;
-                if (kDraft && (uint32_t)wt << 1 == 0u) continue;  // (uniform: all lanes hold the same weight)
-#pragma unroll
-                for (int d = 0; d < 4; ++d) acc[c + u][d] = f2_fma(wt, v[d], acc[c + u][d]);
-            }
-        }
-    }
-}
-
-__global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int c0 = 8 * (warp & 3), d0 = 256 * (warp >> 2) + 8 * lane;  // this thread's part of the context
     bool bad_page = false;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -149,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
             if (tid < kRows) {
                 sm.row[tid] = row;
                 sm.scale[buf][tid] = scale;
+                sm.log_scale[buf][tid] = log2f(scale);
                 sm.there[buf][tid] = row >= 0;
             }
         };
@@ -164,23 +218,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
         store_row(0);
         __syncthreads();
         copy_rows(0);
-        for (int i = tid; i < kCols * (kRow / 4); i += kThreads) {
-            // eight threads read 128 bytes of a column
-            const int k4 = (i & 7) + 8 * (i / (8 * kCols)), c = (i >> 3) % kCols;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c < nc)
-                v = k4 < kKL / 4 ? __ldg(static_cast<const float4 *>(a.q_lat) + (q_base + c) * (kKL / 4) + k4)
-                                 : __ldg(static_cast<const float4 *>(a.q_rope) + (q_base + c) * (kKR / 4) + (k4 - kKL / 4));
-            sm.q[4 * k4][c] = tree_query(v.x);
-            sm.q[4 * k4 + 1][c] = tree_query(v.y);
-            sm.q[4 * k4 + 2][c] = tree_query(v.z);
-            sm.q[4 * k4 + 3][c] = tree_query(v.w);
+        {
+            // eight threads split a column
+            const int c = tid >> 3;
+            float4 v[kRow / 32];
+            float mx = 0.f;
+            bool fine = true;
+#pragma unroll
+            for (int j = 0; j < kRow / 32; ++j) {
+                const int k4 = (tid & 7) + 8 * j;
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c < nc)
+                    v[j] = k4 < kKL / 4 ? __ldg(static_cast<const float4 *>(a.q_lat) + (q_base + c) * (kKL / 4) + k4)
+                                        : __ldg(static_cast<const float4 *>(a.q_rope) + (q_base + c) * (kKR / 4) + (k4 - kKL / 4));
+            }
+#pragma unroll
+            for (int j = 0; j < kRow / 32; ++j) {
+                const float most = fmaxf(fmaxf(fabsf(v[j].x), fabsf(v[j].y)), fmaxf(fabsf(v[j].z), fabsf(v[j].w)));
+                mx = fmaxf(mx, most);
+                fine = fine && v[j].x == v[j].x && v[j].y == v[j].y && v[j].z == v[j].z && v[j].w == v[j].w;
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // a NaN or an infinity makes all of the column's pieces NaN
+            const uint32_t odd = __ballot_sync(0xffffffffu, !fine || mx > 3.402823466e38f);
+            fine = (odd >> (lane & 24) & 0xFFu) == 0u;
+            int E = 0;
+            if (fine && mx > 0.f) frexpf(mx, &E);
+            const int up = fine && mx > 0.f ? min(15 - E, 100) : 0;  // max |q| 2^up in [2^14, 2^15), or less below 2^-86
+            const float f = fine ? ldexpf(1.f, up) : NAN;
+            if ((tid & 7) == 0) sm.factor[c] = ldexpf(a.sm_scale_log2, -up);
+#pragma unroll
+            for (int j = 0; j < kRow / 32; ++j) {
+                uint2 hi, lo;
+                split_f16(v[j].x * f, v[j].y * f, hi.x, lo.x);
+                split_f16(v[j].z * f, v[j].w * f, hi.y, lo.y);
+                *reinterpret_cast<uint2 *>(&sm.q[0][c][8 * ((tid & 7) + 8 * j)]) = hi;
+                *reinterpret_cast<uint2 *>(&sm.q[1][c][8 * ((tid & 7) + 8 * j)]) = lo;
+            }
         }
-        uint64_t acc[8][4];
+        float acc[2][2][4][4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) acc[c][d] = 0;
+        for (int i = 0; i < 64; ++i) acc[i >> 5][i >> 4 & 1][i >> 2 & 3][i & 3] = 0.f;
         const int node = (g0 + lane) / a.H;      // of column `lane`
         float m_run = -INFINITY, z_run = 0.f;    // of column `lane`: the maximum so far, and the sum over this warp's rows
 
@@ -191,56 +270,72 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncthreads();  // the rows are there; the step before is done with its weights and its rows
             if (more) fetch_row(p0 + kRows);
-            if (nr > kUnit) partial_scores<kRows / 8>(sm, sm.tile[buf], warp, lane);
-            else partial_scores<kUnit / 8>(sm, sm.tile[buf], warp, lane);
+            if (nr > 32 * (warp & 1)) partial_scores(sm, sm.tile[buf], warp, lane);
             if (more) store_row(buf ^ 1);
             __syncthreads();
             if (more) copy_rows(buf ^ 1);
-            // ---- softmax: warp w has rows w + 8 j, lane = column
-            float s[kRows / kWarps];
-            float m_new = -INFINITY;
+            // ---- softmax: warp w has rows 8 w .. 8 w + 7, lane = column
+            float s[8];
+            float m_new = -INFINITY, e_max = -INFINITY;  // of the scores, and of the weights' logarithms
+            const float factor = sm.factor[lane];
 #pragma unroll
-            for (int j = 0; j < kRows / kWarps; ++j) {
-                const int r = warp + kWarps * j;
+            for (int j = 0; j < 8; ++j) {
+                const int r = 8 * warp + j;
                 s[j] = -INFINITY;
                 if (r >= nr || !sm.there[buf][r] || lane >= nc) continue;
                 const int64_t draft = p0 + r - seg.q.len;  // the row's index in the draft
                 if (draft >= 0 && !tree_sees(a, seg.q.q0, node, (int)draft)) continue;
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) v += sm.s[w][r][lane];
-                s[j] = v * (sm.scale[buf][r] * a.sm_scale_log2);
+                const float v = (sm.s[0][r][lane] + sm.s[1][r][lane]) + (sm.s[2][r][lane] + sm.s[3][r][lane]);
+                s[j] = v * (sm.scale[buf][r] * factor);
                 m_new = fmaxf(m_new, s[j]);
+                e_max = fmaxf(e_max, s[j] + sm.log_scale[buf][r]);
             }
             sm.m_part[warp][lane] = m_new;
-            __syncthreads();  // (and the parts are read: the weights take their place)
+            sm.e_part[warp][lane] = e_max;
+            // codes that a weight of 0 must not meet: NaN in drafted rows (a column that attends them has NaN weights)
+            if (p0 + nr > seg.q.len)
+                for (int i = tid; i < nr * (kKL / 16); i += kThreads) {
+                    const int r = i / (kKL / 16);
+                    if (p0 + r < seg.q.len) continue;
+                    uint4 *p = reinterpret_cast<uint4 *>(&sm.tile[buf][r][16 * (i % (kKL / 16))]);
+                    *p = make_uint4(without_nan(p->x), without_nan(p->y), without_nan(p->z), without_nan(p->w));
+                }
+            __syncthreads();  // (and the dot products are read: the weights take their place)
             m_new = m_run;
+            e_max = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, sm.m_part[w][lane]);
+            for (int w = 0; w < kWarps; ++w) {
+                m_new = fmaxf(m_new, sm.m_part[w][lane]);
+                e_max = fmaxf(e_max, sm.e_part[w][lane]);
+            }
             const float ref = m_new == -INFINITY ? 0.f : m_new;
             const float corr = exp2f(m_run - ref);  // 0 before any row
             m_run = m_new;
-            if (warp == 0) sm.corr[lane] = corr;
+            // the step's largest weight, of a column, times 2^(14 - top) in (2^13, 2^14]
+            const float top = fminf(fmaxf(ceilf(e_max - ref), -110.f), 127.f), up = exp2f(14.f - top);
+            if (warp == 0) {
+                sm.corr[lane] = corr;
+                sm.unit[lane] = exp2f(top - 14.f);
+            }
             z_run *= corr;
 #pragma unroll
-            for (int j = 0; j < kRows / kWarps; ++j) {
-                const int r = warp + kWarps * j;
-                // a row that the column does not attend weighs 0 whatever its scale holds
-                const float pr = s[j] == -INFINITY ? 0.f : exp2f(s[j] - ref);
-                z_run += pr;
-                const float w = s[j] == -INFINITY ? 0.f : pr * sm.scale[buf][r];
-                sm.p[r][lane] = make_float2(w, w);
+            for (int j = 0; j < 8; j += 2) {
+                float w[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    // a row that the column does not attend weighs 0 whatever its scale holds
+                    const float pr = s[j + k] == -INFINITY ? 0.f : exp2f(s[j + k] - ref);
+                    z_run += pr;
+                    w[k] = s[j + k] == -INFINITY ? 0.f : pr * up * sm.scale[buf][8 * warp + j + k];
+                }
+                uint32_t hi, lo;
+                split_f16(w[0], w[1], hi, lo);
+                const int at = 32 * (warp >> 1) + 4 * j + 4 * (warp & 1);  // rows 8 w + j of 16 (w / 2) + ..: a place of four bytes
+                *reinterpret_cast<uint32_t *>(&sm.w[0][lane][at]) = hi;
+                *reinterpret_cast<uint32_t *>(&sm.w[1][lane][at]) = lo;
             }
             __syncthreads();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float f = sm.corr[c0 + c];
-                const uint64_t ff = f2_pack(f, f);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) acc[c][d] = f2_mul(acc[c][d], ff);
-            }
-            if (p0 + nr > seg.q.len) context<true>(sm, sm.tile[buf], nr, c0, d0, acc);
-            else context<false>(sm, sm.tile[buf], nr, c0, d0, acc);
+            context(sm, sm.tile[buf], (nr + 15) / 16, warp, lane, acc);
         }
         __syncthreads();
         sm.m_part[warp][lane] = z_run;
@@ -256,28 +351,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_simt_kernel(TreeArgs a)
             part[kCols * (kKL + 2) + lane] = 0.f;
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float zc = __shfl_sync(0xffffffffu, z, c0 + c);
-            if (c0 + c >= nc) continue;
-            const float inv = !whole ? 1.f : zc == 0.f ? 0.f : 1.f / zc;
-            float o[8];
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                f2_unpack(acc[c][d], o[2 * d], o[2 * d + 1]);
-                o[2 * d] *= inv;
-                o[2 * d + 1] *= inv;
-            }
-            if (whole && a.out_bf16) {
-                __nv_bfloat162 h[4];
+            for (int i = 0; i < 2; ++i) {
+                const int c = 16 * m + 8 * i + (lane >> 2);
+                const float zc = __shfl_sync(0xffffffffu, z, c);
+                if (c >= nc) continue;
+                const float inv = !whole ? 1.f : zc == 0.f ? 0.f : 1.f / zc;
 #pragma unroll
-                for (int d = 0; d < 4; ++d) h[d] = __floats2bfloat162_rn(o[2 * d], o[2 * d + 1]);
-                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (q_base + c0 + c) * kKL + d0) = *reinterpret_cast<uint4 *>(h);
-            } else {
-                float4 *dst = reinterpret_cast<float4 *>((whole ? static_cast<float *>(a.out) + (q_base + c0 + c) * kKL : part + (c0 + c) * kKL) + d0);
-                dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-                dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+                for (int h = 0; h < 2; ++h) {
+                    const int d = 64 * warp + 32 * h + 8 * (lane & 3);
+                    float o[8];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        o[n] = acc[h][m][n][2 * i] * inv;
+                        o[4 + n] = acc[h][m][n][2 * i + 1] * inv;
+                    }
+                    if (whole && a.out_bf16) {
+                        __nv_bfloat162 b[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) b[n] = __floats2bfloat162_rn(o[2 * n], o[2 * n + 1]);
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (q_base + c) * kKL + d) = *reinterpret_cast<uint4 *>(b);
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>((whole ? static_cast<float *>(a.out) + (q_base + c) * kKL : part + c * kKL) + d);
+                        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+                        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+                    }
+                }
             }
-        }
     }
     if (bad_page && a.err_word) atomicOr(a.err_word, (int)KV8_ERR_INDEX);
 }
@@ -426,11 +527,11 @@ cudaError_t launch_tree_merge(const TreeArgs &a, int cols, cudaStream_t st) {
     return launch_behind(tree_merge_kernel, (unsigned)a.ctas * 4u, kMergeWarps * 32u, 0, st, a, cols);
 }
 
-cudaError_t launch_tree_simt(const TreeArgs &a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(attn_tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+cudaError_t launch_tree_f32(const TreeArgs &a, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(attn_tree_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
     if (e != cudaSuccess) return e;
     if ((e = launch_behind(tree_sched_kernel, 1, 288, 0, st, a)) != cudaSuccess) return e;
-    if ((e = launch_behind(attn_tree_simt_kernel, (unsigned)a.ctas, kThreads, sizeof(Smem), st, a)) != cudaSuccess) return e;
+    if ((e = launch_behind(attn_tree_f32_kernel, (unsigned)a.ctas, kThreads, sizeof(Smem), st, a)) != cudaSuccess) return e;
     return launch_tree_merge(a, kCols, st);
 }
 

@@ -218,12 +218,6 @@ __device__ __forceinline__ float lg2_approx(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// e4m3 NaN codes (0x7F, 0xFF) of four bytes -> 0
-__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
-    const uint32_t hit = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    return w & ~hit;
-}
-
 // ------------------------------------------------------------------------------------------------------------
 // Query images, column factors, and (block 0) the work shares.  A block splits 16 columns of a group, two by each warp:
 // their pieces are 32 consecutive lanes of the image, so that by way of shared memory whole lines are written.

@@ -342,7 +342,7 @@ int mla_absorb_tree8(const void *q_lat, const void *q_rope, int q_dtype, int R, 
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.part);
     // bf16 queries: tensor cores; f32 queries keep full f32 precision on the CUDA cores
     return status(a.q_bf16 ? launch_tree_tc(a, static_cast<uint8_t *>(workspace) + w.images, (cudaStream_t)stream)
-                           : launch_tree_simt(a, (cudaStream_t)stream));
+                           : launch_tree_f32(a, (cudaStream_t)stream));
 }
 
 int kv8_tree_commit(int B, const int32_t *q_start, const int32_t *lens, const int32_t *accept,

@@ -90,14 +90,17 @@ __device__ __forceinline__ int64_t tree_row(const TreeArgs &a, int b, int64_t t)
     return page >= 0 && row < a.cache_rows ? row : -1;
 }
 
-// A query's element: infinities count as NaN (an infinite score has no softmax).
-__device__ __forceinline__ float tree_query(float v) { return fabsf(v) <= 3.402823466e38f ? v : __int_as_float(0x7fffffff); }
-
 // Whether drafted token i of a sequence whose rows begin at q0 attends drafted token j.
 __device__ __forceinline__ bool tree_sees(const TreeArgs &a, int q0, int i, int j) {
     if (!a.mask) return j <= i;
     if ((j >> 5) >= a.mask_words) return false;
     return (__ldg(a.mask + (int64_t)(q0 + i) * a.mask_words + (j >> 5)) >> (j & 31)) & 1u;
+}
+
+// e4m3 NaN codes (0x7F, 0xFF) of four bytes -> 0
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+    const uint32_t hit = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    return w & ~hit;
 }
 
 // The rows of a 64-row tile that drafted token i attends (bit r: row r), where the tile's first row is the draft's
@@ -293,7 +296,7 @@ struct TreeWorkspace {
 TreeWorkspace tree_workspace(int R, int H, int B, bool q_bf16);
 
 cudaError_t launch_tree_merge(const TreeArgs &a, int cols, cudaStream_t st);
-cudaError_t launch_tree_simt(const TreeArgs &a, cudaStream_t st);
+cudaError_t launch_tree_f32(const TreeArgs &a, cudaStream_t st);
 cudaError_t launch_tree_tc(const TreeArgs &a, void *images, cudaStream_t st);
 size_t tree_tc_images(int R, int H, int B);
 size_t tree_tc_part_bytes(int ctas);

@@ -36,15 +36,18 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
     q [n][H][576] f64, sees [n][n] bool, rows: cache rows of positions 0 .. ctx+n-1, valid: those that count.
     The bound, term by term (A = sum_t p_t s_t |v_t|, the size of the sum's terms):
       scores   |d score| <= sm s_t (u q_max sum|k| + v sum|q||k|): u the part of a head's largest query element
-               that a query element is rounded to (bf16: 2^-17, f32: none), v the 32-bit sum's (2^-24 a step of
-               at most 576, taken as 576 2^-24).  Each weight is then off by exp(+-2 d) relative.
-      weights  f32: 2 steps of exp2 and a product.  bf16: the weights w = p_t s_t of 32 rows (positions 32 i to 32 i +
+               that a query element is rounded to (bf16: 2^-17, f32: 2^-39), v the sum's, 576 2^-24: for bf16 2^-24 a
+               step of at most 576; for f32 18 products of 16 elements each a quarter, whose 17 terms may each be cut at
+               2^-24 of the largest, and 2^-22 of an element that its two pieces leave: 306 + 3 + 4 steps of 2^-24.
+               Each weight is then off by exp(+-2 d) relative.
+      weights  2 steps of exp2 and a product.  f32: two f16 pieces of w = p_t s_t, which leave 2^-22 of it, or 2^-25 where
+               the step's largest is 2^13 or more.  bf16: the weights w = p_t s_t of 32 rows (positions 32 i to 32 i +
                31) are held in units that put the largest of them at 2^7 or more, or, in a tile of 64 context rows with
                scales within 2^8 of one another, the largest p_t times the power of two above the largest s_t; rounded to 11 bits (2^-12 w at most),
                then to an e4m3 value, which leaves at most 2^-4 w (2^-10 where it is subnormal, or all of w below that),
                and that to another (2^-4 of it, or 2^-10 where that is subnormal): at most 2^-8 w + 2^-10, each times the
                row's |e4m3 value|.
-      sum      32 bits, one step for each row and one for each part
+      sum      32 bits, one step for each row and one for each part; f32: in 64 rows 8 products of 17 terms, as above
       output   out_eps relative (half a step of its type)
     """
     n, H, _ = q.shape
@@ -61,8 +64,7 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
         s = SM * q[i] @ kk.T
         qk = SM * np.abs(q[i]) @ np.abs(kk).T
         d = 576 * 2.0 ** -24 * qk
-        if not f32:
-            d = d + 2.0 ** -17 * SM * np.abs(q[i]).max(1)[:, None] * np.abs(kk).sum(1)[None]
+        d = d + (2.0 ** -39 if f32 else 2.0 ** -17) * SM * np.abs(q[i]).max(1)[:, None] * np.abs(kk).sum(1)[None]
         p = np.exp(s - s.max(1, keepdims=True))
         p /= p.sum(1, keepdims=True)
         out[i] = p @ kk[:, :512]
@@ -71,8 +73,11 @@ def attend(q, sees, ctx, rows, valid, kv8, scale, out_eps, f32):
         e = np.expm1(2 * d)
         tol[i] = (p * e) @ np.abs(kk[:, :512]) + (p * e).sum(1)[:, None] * A
         tol[i] += A * (2.0 ** -21 + (2 * T + 64) * 2.0 ** -24)
-        if not f32:
-            ps = p * scale[rows[on]].astype(np.float64)
+        ps = p * scale[rows[on]].astype(np.float64)
+        if f32:
+            tol[i] += A * (2.0 ** -22 + 136 * 2.0 ** -24)
+            tol[i] += 2.0 ** -38 * ps.max(1, keepdims=True) * np.abs(TABLE[kv8[rows[on]]][:, :512]).sum(0)
+        else:
             block = np.nonzero(on)[0] // 32
             st = scale[rows[on]].astype(np.float64)
             unit, pm, sm_, sl = (np.zeros((H, T // 32 + 2)) for _ in range(4))
