@@ -22,7 +22,7 @@ using namespace sm100;
 constexpr int kCols = 32;      // (token, head) columns per block
 constexpr int kUnit = 32;      // rows that the shares count
 constexpr int kRows = 64;      // rows per step: two units where there are two
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 // Strides in bytes.  A tile's: 16-byte copies, and 148 words put eight rows' four words into 32 banks.  A query column's and a
 // weight column's: four columns' four 8-byte pieces in 128 bytes of banks (the weights': nearly, for the stores' sake).
@@ -80,15 +80,15 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t &hi, uint32
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// Dot products: a warp takes 32 rows and a quarter of their bytes against all columns, a thread's four bytes of a 16-byte
+// Dot products: a warp takes 32 rows and a quarter of their bytes against 16 columns, a thread's four bytes of a 16-byte
 // step standing for rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of the contraction on both sides.
 __device__ __forceinline__ void partial_scores(Smem &sm, const uint8_t (*tile)[kTileStride], int warp, int lane) {
-    const int g = lane >> 2, c = lane & 3, r0 = 32 * (warp & 1) + g, part = warp >> 1;
-    float acc[2][4][4];
+    const int g = lane >> 2, c = lane & 3, r0 = 32 * (warp & 1) + g, part = warp >> 1 & 3, n0 = 16 * (warp >> 3);
+    float acc[2][2][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
 #pragma unroll 3
@@ -104,10 +104,10 @@ __device__ __forceinline__ void partial_scores(Smem &sm, const uint8_t (*tile)[k
                 a[m][2 + i] = e4m3x2_to_f16x2(v >> 16);
             }
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int piece = 1; piece >= 0; --piece) {
-                const uint2 b = *reinterpret_cast<const uint2 *>(&sm.q[piece][8 * n + g][2 * at]);
+                const uint2 b = *reinterpret_cast<const uint2 *>(&sm.q[piece][n0 + 8 * n + g][2 * at]);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) mma_f16(acc[m][n], a[m], b.x, b.y);
             }
@@ -115,19 +115,18 @@ __device__ __forceinline__ void partial_scores(Smem &sm, const uint8_t (*tile)[k
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<float2 *>(&sm.s[part][r0 + 16 * m + 8 * i][8 * n + 2 * c]) = make_float2(acc[m][n][2 * i], acc[m][n][2 * i + 1]);
+                *reinterpret_cast<float2 *>(&sm.s[part][r0 + 16 * m + 8 * i][n0 + 8 * n + 2 * c]) = make_float2(acc[m][n][2 * i], acc[m][n][2 * i + 1]);
 }
 
-// acc = acc * corr + weights x rows * unit: a warp has all columns by 64 latent dims.  Of its 32 dims h a thread's bytes
+// acc = acc * corr + weights x rows * unit: a warp has all columns by 32 latent dims.  A thread's bytes
 // 4 g .. 4 g + 3 of two rows make the operand's pairs for four products of 8 dims (4 g + n, g < 8); so it ends with columns
 // g + 8 i + 16 m, dims 8 c + n and 8 c + 4 + n.
-__device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kTileStride], int steps, int warp, int lane, float (&acc)[2][2][4][4]) {
+__device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kTileStride], int steps, int warp, int lane, float (&acc)[2][4][4]) {
     const int g = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    {
         float t[2][4][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -140,7 +139,7 @@ __device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kT
             uint32_t b[2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint8_t *src = &tile[16 * k + 8 * i + 2 * c][64 * warp + 32 * h + 4 * g];
+                const uint8_t *src = &tile[16 * k + 8 * i + 2 * c][32 * warp + 4 * g];
                 const uint32_t x = *reinterpret_cast<const uint32_t *>(src), y = *reinterpret_cast<const uint32_t *>(src + kTileStride);
                 const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
                 b[i][0] = e4m3x2_to_f16x2(lo);
@@ -166,8 +165,8 @@ __device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kT
                 const float f = sm.corr[16 * m + 8 * i + g], u = sm.unit[16 * m + 8 * i + g];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    acc[h][m][n][2 * i] = fmaf(acc[h][m][n][2 * i], f, t[m][n][2 * i] * u);
-                    acc[h][m][n][2 * i + 1] = fmaf(acc[h][m][n][2 * i + 1], f, t[m][n][2 * i + 1] * u);
+                    acc[m][n][2 * i] = fmaf(acc[m][n][2 * i], f, t[m][n][2 * i] * u);
+                    acc[m][n][2 * i + 1] = fmaf(acc[m][n][2 * i + 1], f, t[m][n][2 * i + 1] * u);
                 }
             }
     }
@@ -219,47 +218,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
         __syncthreads();
         copy_rows(0);
         {
-            // eight threads split a column
-            const int c = tid >> 3;
-            float4 v[kRow / 32];
+            // sixteen threads split a column
+            const int c = tid >> 4;
+            float4 v[kRow / 64];
             float mx = 0.f;
             bool fine = true;
 #pragma unroll
-            for (int j = 0; j < kRow / 32; ++j) {
-                const int k4 = (tid & 7) + 8 * j;
+            for (int j = 0; j < kRow / 64; ++j) {
+                const int k4 = (tid & 15) + 16 * j;
                 v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (c < nc)
                     v[j] = k4 < kKL / 4 ? __ldg(static_cast<const float4 *>(a.q_lat) + (q_base + c) * (kKL / 4) + k4)
                                         : __ldg(static_cast<const float4 *>(a.q_rope) + (q_base + c) * (kKR / 4) + (k4 - kKL / 4));
             }
 #pragma unroll
-            for (int j = 0; j < kRow / 32; ++j) {
+            for (int j = 0; j < kRow / 64; ++j) {
                 const float most = fmaxf(fmaxf(fabsf(v[j].x), fabsf(v[j].y)), fmaxf(fabsf(v[j].z), fabsf(v[j].w)));
                 mx = fmaxf(mx, most);
                 fine = fine && v[j].x == v[j].x && v[j].y == v[j].y && v[j].z == v[j].z && v[j].w == v[j].w;
             }
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             // a NaN or an infinity makes all of the column's pieces NaN
             const uint32_t odd = __ballot_sync(0xffffffffu, !fine || mx > 3.402823466e38f);
-            fine = (odd >> (lane & 24) & 0xFFu) == 0u;
+            fine = (odd >> (lane & 16) & 0xFFFFu) == 0u;
             int E = 0;
             if (fine && mx > 0.f) frexpf(mx, &E);
             const int up = fine && mx > 0.f ? min(15 - E, 100) : 0;  // max |q| 2^up in [2^14, 2^15), or less below 2^-86
             const float f = fine ? ldexpf(1.f, up) : NAN;
-            if ((tid & 7) == 0) sm.factor[c] = ldexpf(a.sm_scale_log2, -up);
+            if ((tid & 15) == 0) sm.factor[c] = ldexpf(a.sm_scale_log2, -up);
 #pragma unroll
-            for (int j = 0; j < kRow / 32; ++j) {
+            for (int j = 0; j < kRow / 64; ++j) {
                 uint2 hi, lo;
                 split_f16(v[j].x * f, v[j].y * f, hi.x, lo.x);
                 split_f16(v[j].z * f, v[j].w * f, hi.y, lo.y);
-                *reinterpret_cast<uint2 *>(&sm.q[0][c][8 * ((tid & 7) + 8 * j)]) = hi;
-                *reinterpret_cast<uint2 *>(&sm.q[1][c][8 * ((tid & 7) + 8 * j)]) = lo;
+                *reinterpret_cast<uint2 *>(&sm.q[0][c][8 * ((tid & 15) + 16 * j)]) = hi;
+                *reinterpret_cast<uint2 *>(&sm.q[1][c][8 * ((tid & 15) + 16 * j)]) = lo;
             }
         }
-        float acc[2][2][4][4];
+        float acc[2][4][4];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i >> 5][i >> 4 & 1][i >> 2 & 3][i & 3] = 0.f;
+        for (int i = 0; i < 32; ++i) acc[i >> 4][i >> 2 & 3][i & 3] = 0.f;
         const int node = (g0 + lane) / a.H;      // of column `lane`
         float m_run = -INFINITY, z_run = 0.f;    // of column `lane`: the maximum so far, and the sum over this warp's rows
 
@@ -274,13 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
             if (more) store_row(buf ^ 1);
             __syncthreads();
             if (more) copy_rows(buf ^ 1);
-            // ---- softmax: warp w has rows 8 w .. 8 w + 7, lane = column
-            float s[8];
+            // ---- softmax: warp w has rows 4 w .. 4 w + 3, lane = column
+            float s[4];
             float m_new = -INFINITY, e_max = -INFINITY;  // of the scores, and of the weights' logarithms
             const float factor = sm.factor[lane];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = 8 * warp + j;
+            for (int j = 0; j < 4; ++j) {
+                const int r = 4 * warp + j;
                 s[j] = -INFINITY;
                 if (r >= nr || !sm.there[buf][r] || lane >= nc) continue;
                 const int64_t draft = p0 + r - seg.q.len;  // the row's index in the draft
@@ -319,18 +318,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
             }
             z_run *= corr;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
+            for (int j = 0; j < 4; j += 2) {
                 float w[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     // a row that the column does not attend weighs 0 whatever its scale holds
                     const float pr = s[j + k] == -INFINITY ? 0.f : exp2f(s[j + k] - ref);
                     z_run += pr;
-                    w[k] = s[j + k] == -INFINITY ? 0.f : pr * up * sm.scale[buf][8 * warp + j + k];
+                    w[k] = s[j + k] == -INFINITY ? 0.f : pr * up * sm.scale[buf][4 * warp + j + k];
                 }
                 uint32_t hi, lo;
                 split_f16(w[0], w[1], hi, lo);
-                const int at = 32 * (warp >> 1) + 4 * j + 4 * (warp & 1);  // rows 8 w + j of 16 (w / 2) + ..: a place of four bytes
+                const int r = 4 * (warp & 3) + j, at = 32 * (warp >> 2) + 4 * (r & 7) + 4 * (r >> 3);  // rows r and r + 1 of 16
                 *reinterpret_cast<uint32_t *>(&sm.w[0][lane][at]) = hi;
                 *reinterpret_cast<uint32_t *>(&sm.w[1][lane][at]) = lo;
             }
@@ -358,14 +357,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
                 const float zc = __shfl_sync(0xffffffffu, z, c);
                 if (c >= nc) continue;
                 const float inv = !whole ? 1.f : zc == 0.f ? 0.f : 1.f / zc;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int d = 64 * warp + 32 * h + 8 * (lane & 3);
+                {
+                    const int d = 32 * warp + 8 * (lane & 3);
                     float o[8];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
-                        o[n] = acc[h][m][n][2 * i] * inv;
-                        o[4 + n] = acc[h][m][n][2 * i + 1] * inv;
+                        o[n] = acc[m][n][2 * i] * inv;
+                        o[4 + n] = acc[m][n][2 * i + 1] * inv;
                     }
                     if (whole && a.out_bf16) {
                         __nv_bfloat162 b[4];
