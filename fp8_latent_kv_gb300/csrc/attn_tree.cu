@@ -24,9 +24,9 @@ constexpr int kUnit = 32;      // rows that the shares count
 constexpr int kRows = 64;      // rows per step: two units where there are two
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-// Strides in bytes.  A tile's: 16-byte copies, and 148 words put eight rows' four words into 32 banks.  A query column's and a
-// weight column's: four columns' four 8-byte pieces in 128 bytes of banks (the weights': nearly, for the stores' sake).
-constexpr int kTileStride = 592, kQStride = 2 * kRow + 32, kWStride = 2 * kRows + 40;
+// Strides in bytes.  A tile's: 16-byte copies, and 148 words put eight rows' four words into 32 banks.  A query column's: four
+// columns' four 8-byte pieces in 32 banks.
+constexpr int kTileStride = 592, kQStride = 2 * kRow + 32;
 constexpr int kSStride = kCols + 8;        // words
 constexpr int kSteps = kRow / 16 / 4;      // 16-byte steps of a row that a warp's part of the scores covers
 static_assert(kSteps * 64 == kRow, "a row's quarters");
@@ -36,12 +36,14 @@ struct Smem {
     alignas(16) uint8_t tile[2][kRows][kTileStride];  // this step's cache rows and the next's; rows left out are zero
     union {
         float s[4][kRows][kSStride];       // the dot products, by quarter of the row
-        alignas(16) uint8_t w[2][kCols][kWStride];  // weights: f16 pieces, a 16-row step's rows as 0 1 8 9 2 3 10 11 ...
+        alignas(16) uint8_t w[2][kCols][2 * kRows];  // weights: f16 pieces, a 16-row step's rows as 0 1 8 9 2 3 10 11 ...
     };
-    int64_t row[kRows];                    // of the next step: cache row, or -1
+    uint64_t full[2];                      // a step's rows have landed
     float scale[2][kRows], log_scale[2][kRows];
-    uint8_t there[2][kRows];
-    float m_part[kWarps][kCols], e_part[kWarps][kCols];
+    alignas(4) uint8_t there[2][kRows];
+    int m_max[2][kCols], e_max[2][kCols];  // of a step's scores and of the weights' logarithms, in the order of whole numbers
+    float z_part[kWarps][kCols];
+    int abort_flag;
     float corr[kCols], unit[kCols];        // the accumulators' factor, the step's weights'
     float factor[kCols];                   // scores: sm_scale log2(e) / the column's power of two
 };
@@ -53,11 +55,15 @@ __global__ void __launch_bounds__(288) tree_sched_kernel(TreeArgs a) {
     tree_schedule<kCols, kUnit, 1, 1>(a, scan);  // (two units a share instead of one: 46 -> 54 us for 4 x 5 tokens of 16 heads)
 }
 
-// 16 bytes global -> shared, zeros where `there` is false (the address must be valid all the same).
-__device__ __forceinline__ void copy_16(void *dst, const void *src, bool there) {
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(there ? 16 : 0) : "memory");
+// Floats as whole numbers of the same order, and back.
+__device__ __forceinline__ int float_order(float v) {
+    const int i = __float_as_int(v);
+    return i >= 0 ? i : i ^ 0x7fffffff;
 }
+__device__ __forceinline__ float order_float(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
+// A column's 8-byte piece u of 16 (four rows of a 16-row step): where a load of four columns by four pieces, and a store of
+// one piece of 16 columns, meet 32 banks.
+__device__ __forceinline__ int weight_offset(int col, int u) { return 8 * (u ^ (4 * (col & 3)) ^ (col >> 2 & 3)); }
 
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
     uint32_t r;
@@ -151,8 +157,8 @@ __device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kT
             for (int piece = 1; piece >= 0; --piece)
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(&sm.w[piece][16 * m + g][32 * k + 8 * c]);
-                    const uint2 v = *reinterpret_cast<const uint2 *>(&sm.w[piece][16 * m + 8 + g][32 * k + 8 * c]);
+                    const uint2 u = *reinterpret_cast<const uint2 *>(&sm.w[piece][16 * m + g][weight_offset(g, 4 * k + c)]);
+                    const uint2 v = *reinterpret_cast<const uint2 *>(&sm.w[piece][16 * m + 8 + g][weight_offset(8 + g, 4 * k + c)]);
                     const uint32_t a[4] = {u.x, v.x, u.y, v.y};
 #pragma unroll
                     for (int n = 0; n < 4; ++n) mma_f16(t[m][n], a, b[0][n], b[1][n]);
@@ -176,47 +182,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    bool bad_page = false;
+    bool bad_page = false, ok = true;
+    if (tid == 0) {
+        mbar_init(&sm.full[0], kRows);
+        mbar_init(&sm.full[1], kRows);
+        sm.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (tid < 2 * kCols) (&sm.m_max[0][0])[tid] = (&sm.e_max[0][0])[tid] = float_order(-INFINITY);
+    __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
     TreeWalk walk;
     walk.begin(a, blockIdx.x);
     TreeSegment seg;
-    while (walk.next<kCols, kUnit>(a, seg)) {
+    uint32_t step = 0;  // of all segments
+    while (ok && walk.next<kCols, kUnit>(a, seg)) {
         const int g0 = seg.g * kCols, nc = min(kCols, seg.q.n * a.H - g0);
         const int64_t q_base = (int64_t)seg.q.q0 * a.H + g0, rows_end = seg.q.len + seg.q.n;
         const int64_t p_begin = (int64_t)seg.t0 * kUnit, p_end = min((int64_t)seg.t1 * kUnit, rows_end);
-        // the step's cache rows from position p0 on, of which the first 64 threads hold one each
+        // the step's cache rows from position p0 on, of which a warp's first lanes hold one each
+        const int r_own = 4 * warp + lane;
         int64_t row = -1;
         float scale = 0.f;
         auto fetch_row = [&](int64_t p0) {
             row = -1;
-            if (tid < kRows && p0 + tid < p_end) {
-                row = tree_row(a, seg.b, p0 + tid);
+            if (lane < 4 && p0 + r_own < p_end) {
+                row = tree_row(a, seg.b, p0 + r_own);
                 bad_page |= row < 0;
             }
             scale = row >= 0 ? __ldg(a.kv_scale + row) : 0.f;
         };
-        auto store_row = [&](int buf) {
-            if (tid < kRows) {
-                sm.row[tid] = row;
-                sm.scale[buf][tid] = scale;
-                sm.log_scale[buf][tid] = log2f(scale);
-                sm.there[buf][tid] = row >= 0;
+        // and brings into a buffer that all threads are done with
+        auto copy_row = [&](int buf) {
+            if (lane >= 4) return;
+            const bool there = row >= 0;
+            sm.scale[buf][r_own] = scale;
+            sm.log_scale[buf][r_own] = log2f(scale);
+            sm.there[buf][r_own] = there;
+            if (there) {
+                fence_proxy_async_smem();  // (the threads have read the buffer; the copy writes it)
+                mbar_arrive_expect_tx(&sm.full[buf], kRow);
+                bulk_load(sm.tile[buf][r_own], a.kv8 + row * kRow, kRow, &sm.full[buf]);
+            } else {
+                for (int i = 0; i < kRow; i += 16) *reinterpret_cast<uint4 *>(&sm.tile[buf][r_own][i]) = make_uint4(0u, 0u, 0u, 0u);
+                mbar_arrive(&sm.full[buf]);
             }
         };
-        auto copy_rows = [&](int buf) {
-            for (int i = tid; i < kRows * (kRow / 16); i += kThreads) {
-                const int r = i / (kRow / 16), ch = i - r * (kRow / 16);
-                const int64_t at = sm.row[r];
-                copy_16(&sm.tile[buf][r][ch * 16], a.kv8 + (at >= 0 ? at : 0) * kRow + ch * 16, at >= 0);
-            }
-        };
-        __syncthreads();  // the segment before is done with all of this
         fetch_row(p_begin);
-        store_row(0);
-        __syncthreads();
-        copy_rows(0);
+        __syncthreads();  // the segment before is done with all of this
+        copy_row(step & 1);
         {
             // sixteen threads split a column
             const int c = tid >> 4;
@@ -262,35 +277,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
         const int node = (g0 + lane) / a.H;      // of column `lane`
         float m_run = -INFINITY, z_run = 0.f;    // of column `lane`: the maximum so far, and the sum over this warp's rows
 
-        int buf = 0;
-        for (int64_t p0 = p_begin; p0 < p_end; p0 += kRows, buf ^= 1) {
-            const int nr = (int)min((int64_t)kRows, p_end - p0);
+        for (int64_t p0 = p_begin; p0 < p_end; p0 += kRows, ++step) {
+            const int nr = (int)min((int64_t)kRows, p_end - p0), buf = step & 1;
             const bool more = p0 + kRows < p_end;
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncthreads();  // the rows are there; the step before is done with its weights and its rows
+            ok = mbar_wait(&sm.full[buf], step >> 1 & 1, &sm.abort_flag, a.err_word);
+            // the rows are there; the step before is done with its weights and its rows
+            ok = __syncthreads_and(ok);
+            if (!ok) break;
             if (more) fetch_row(p0 + kRows);
             if (nr > 32 * (warp & 1)) partial_scores(sm, sm.tile[buf], warp, lane);
-            if (more) store_row(buf ^ 1);
             __syncthreads();
-            if (more) copy_rows(buf ^ 1);
+            if (more) copy_row(buf ^ 1);
             // ---- softmax: warp w has rows 4 w .. 4 w + 3, lane = column
             float s[4];
             float m_new = -INFINITY, e_max = -INFINITY;  // of the scores, and of the weights' logarithms
             const float factor = sm.factor[lane];
+            auto dot = [&](int r) -> float { return (sm.s[0][r][lane] + sm.s[1][r][lane]) + (sm.s[2][r][lane] + sm.s[3][r][lane]); };
+            if (p0 + kRows <= seg.q.len && nc == kCols && *reinterpret_cast<const uint32_t *>(&sm.there[buf][4 * warp]) == 0x01010101u) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = 4 * warp + j;
-                s[j] = -INFINITY;
-                if (r >= nr || !sm.there[buf][r] || lane >= nc) continue;
-                const int64_t draft = p0 + r - seg.q.len;  // the row's index in the draft
-                if (draft >= 0 && !tree_sees(a, seg.q.q0, node, (int)draft)) continue;
-                const float v = (sm.s[0][r][lane] + sm.s[1][r][lane]) + (sm.s[2][r][lane] + sm.s[3][r][lane]);
-                s[j] = v * (sm.scale[buf][r] * factor);
-                m_new = fmaxf(m_new, s[j]);
-                e_max = fmaxf(e_max, s[j] + sm.log_scale[buf][r]);
+                for (int j = 0; j < 4; ++j) {  // every column attends every row
+                    const int r = 4 * warp + j;
+                    s[j] = dot(r) * (sm.scale[buf][r] * factor);
+                    m_new = fmaxf(m_new, s[j]);
+                    e_max = fmaxf(e_max, s[j] + sm.log_scale[buf][r]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 4 * warp + j;
+                    s[j] = -INFINITY;
+                    if (r >= nr || !sm.there[buf][r] || lane >= nc) continue;
+                    const int64_t draft = p0 + r - seg.q.len;  // the row's index in the draft
+                    if (draft >= 0 && !tree_sees(a, seg.q.q0, node, (int)draft)) continue;
+                    s[j] = dot(r) * (sm.scale[buf][r] * factor);
+                    m_new = fmaxf(m_new, s[j]);
+                    e_max = fmaxf(e_max, s[j] + sm.log_scale[buf][r]);
+                }
             }
-            sm.m_part[warp][lane] = m_new;
-            sm.e_part[warp][lane] = e_max;
+            atomicMax(&sm.m_max[buf][lane], float_order(m_new));
+            atomicMax(&sm.e_max[buf][lane], float_order(e_max));
             // codes that a weight of 0 must not meet: NaN in drafted rows (a column that attends them has NaN weights)
             if (p0 + nr > seg.q.len)
                 for (int i = tid; i < nr * (kKL / 16); i += kThreads) {
@@ -300,13 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
                     *p = make_uint4(without_nan(p->x), without_nan(p->y), without_nan(p->z), without_nan(p->w));
                 }
             __syncthreads();  // (and the dot products are read: the weights take their place)
-            m_new = m_run;
-            e_max = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                m_new = fmaxf(m_new, sm.m_part[w][lane]);
-                e_max = fmaxf(e_max, sm.e_part[w][lane]);
-            }
+            m_new = fmaxf(m_run, order_float(sm.m_max[buf][lane]));
+            e_max = order_float(sm.e_max[buf][lane]);
+            if (warp == 1) sm.m_max[buf ^ 1][lane] = sm.e_max[buf ^ 1][lane] = float_order(-INFINITY);  // (read in the step before)
             const float ref = m_new == -INFINITY ? 0.f : m_new;
             const float corr = exp2f(m_run - ref);  // 0 before any row
             m_run = m_new;
@@ -329,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
                 }
                 uint32_t hi, lo;
                 split_f16(w[0], w[1], hi, lo);
-                const int r = 4 * (warp & 3) + j, at = 32 * (warp >> 2) + 4 * (r & 7) + 4 * (r >> 3);  // rows r and r + 1 of 16
+                const int r = 4 * (warp & 3) + j;  // rows r and r + 1 of 16: half of piece r / 2 % 4
+                const int at = weight_offset(lane, 4 * (warp >> 2) + (r >> 1 & 3)) + 4 * (r >> 3);
                 *reinterpret_cast<uint32_t *>(&sm.w[0][lane][at]) = hi;
                 *reinterpret_cast<uint32_t *>(&sm.w[1][lane][at]) = lo;
             }
@@ -337,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
             context(sm, sm.tile[buf], (nr + 15) / 16, warp, lane, acc);
         }
         __syncthreads();
-        sm.m_part[warp][lane] = z_run;
+        sm.z_part[warp][lane] = z_run;
         __syncthreads();
         float z = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) z += sm.m_part[w][lane];
+        for (int w = 0; w < kWarps; ++w) z += sm.z_part[w][lane];
         const bool whole = seg.first && seg.last;
         float *part = a.part + ((int64_t)blockIdx.x * 2 + (seg.first ? 1 : 0)) * tree_part_floats(kCols);
         if (!whole && warp == 0 && lane < nc) {
