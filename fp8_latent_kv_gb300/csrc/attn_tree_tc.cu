@@ -1,12 +1,12 @@
 // attn_tree_tc.cu -- attention of drafted tokens over a paged latent cache on the tensor cores (tcgen05, sm_103a),
 // for bf16 queries.
 //
-// All (token, head) columns of a sequence read the same rows, so a group of 64 columns against a tile of 128 rows is
+// All (token, head) columns of a sequence read the same rows, so a group of 64 columns against a tile of 64 rows is
 // two contractions:
-//   score    S[x][t]    = sum_k Qs[x][k] K8[t][k]      M = 128, N = 2 x 64 rows, K = 576 (e4m3 x e4m3)
+//   score    S[x][t]    = sum_k Qs[x][k] K8[t][k]      M = 128, N = 64 rows, K = 576 (e4m3 x e4m3)
 //            Qs: a bf16 query element, scaled by its column's power of two, is the sum of two e4m3 values; each
 //            TMEM lane quadrant holds 16 columns' hi pieces on lanes 0..15 and their lo pieces on lanes 16..31, so
-//            that one shuffle adds the halves of the dot product.
+//            that two 16-lane loads hand a thread both halves of its dot products.
 //   context  O^T[d][n] += sum_t V8[t][d] W[n][t]       M = 128 dims (x4), N = 64 columns, K = 64 rows; V8 = the same
 //            bytes read MN-major, W the softmax weights as the sum of two e4m3 values with a power of two for each
 //            column and 32 rows (the block-scaled form of the MMA).
@@ -16,10 +16,18 @@
 // exponent of the column's first tile, has to move (and O to be rescaled) only when a term exceeds it by 2^100, not
 // whenever a larger one turns up: with one power for all rows, 64 columns' new maxima had every second tile of the
 // first fifty wait for the context product before it and rescale.
+// A tile of context rows alone, all there, with scales within 2^8 of one another, needs no masks and no logarithms: its
+// blocks' powers are the largest scores' times the power of two above the scales, which costs a weight up to 8 of the
+// binary orders below the block's largest (plain in the code; the others took 6.5 thousand cycles against 3.2).
 // w_t holds the row scale already: O = sum w_t v_t, z = sum w_t / scale_t.  A row whose scale is below 2^-60 (zeros,
 // subnormal maxima) has score 0 and adds nothing to O: such rows are only counted, and the count enters z at the end.
 //
 // Work: equal shares of (group, tile) units (tree.cuh), one CTA per SM.
+// What bounds it: a tile's products take 1408 cycles of the tensor pipe (18 score MMAs of 32 to 48 cycles, 16 context MMAs of
+// 48), a tile 1580 in all where a share has hundreds of them, the pipe busy 69 %: two teams' 3.9 thousand warp instructions
+// a tile, more than half of them conversions, maxima and exchanges of the softmax, take most of the issue slots.  64 tokens of
+// 128 heads over 32768 rows: 411 us, 1422 TFLOP/s.  Three teams did not pay: of eight warps each they spilled (658 us against 522
+// then), of four they missed the instruction cache (557 against 497).
 // Warps: 0 = row loads, 1 = scores and TMEM, 2 = the rows' scales, 3 = context products, 4..19 = softmax and output in
 // two teams that take alternate tiles.  warp % 4 is a warp's TMEM lane quadrant, its set (0, 1) the block of 32 rows,
 // and a thread holds 8 rows of two columns.

