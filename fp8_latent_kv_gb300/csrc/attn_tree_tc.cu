@@ -274,12 +274,17 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
     }
     const int64_t slot = (blockIdx.x - 1) / (kCols / kPrepCols);
     const int quarter = (blockIdx.x - 1) % (kCols / kPrepCols);
-    // the slot's sequence: the last one whose images begin at or before it
+    // the slot's sequence: the last one whose images begin at or before it (whatever an impossible one before it says)
+    __shared__ int last;
+    if (tid == 0) last = -1;
+    __syncthreads();
     int b = -1;
-    for (int k0 = 0; k0 < a.B; k0 += kPrepThreads) {
-        const int k = k0 + tid;
-        b += __syncthreads_count(k < a.B && tree_slot(__ldg(a.q_start + k), a.H, k) <= slot);
-    }
+    for (int k = tid; k < a.B; k += kPrepThreads)
+        if (tree_slot(__ldg(a.q_start + k), a.H, k) <= slot) b = k;
+    b = __reduce_max_sync(0xffffffffu, b);
+    if (lane == 0 && b >= 0) atomicMax(&last, b);
+    __syncthreads();
+    b = last;
     if (b < 0) return;
     const TreeSeq q = tree_seq(a.q_start, a.lens, b, a.R, tree_positions(a.max_pages, a.page_shift));
     const int64_t col0 = (slot - tree_slot(q.q0, a.H, b)) * kCols + quarter * kPrepCols, cols = (int64_t)q.n * a.H;

@@ -40,7 +40,7 @@ def build(oracle, rng, lens, n, page, spare=3, lo=0.5, hi=2.0):
     return kv8, scale, table, rows
 
 
-def run_tree(lib, q, q_dtype, out_dtype, n, lens, mask, kv8, scale, table, page, fill=7.0, rows=None):
+def run_tree(lib, q, q_dtype, out_dtype, n, lens, mask, kv8, scale, table, page, fill=7.0, rows=None, sm=SM, start=None):
     """The call, on tensors; rows: how many q rows the batch really has (more than the sequences' sum allowed)."""
     R, H = q.shape[0], q.shape[1]
     ql = torch.from_numpy(np.ascontiguousarray(q[..., :512])).to(DEV).to(q_dtype)
@@ -48,9 +48,9 @@ def run_tree(lib, q, q_dtype, out_dtype, n, lens, mask, kv8, scale, table, page,
     out = torch.full((R, H, 512), fill, dtype=out_dtype, device=DEV)
     err = torch.zeros(1, dtype=torch.int32, device=DEV)
     ws = torch.full((lib.mla_tree8_workspace_bytes(R, H, len(lens), q_dtype),), 0xFF, dtype=torch.uint8, device=DEV)
-    start = i32(np.concatenate([[0], np.cumsum(n)]))
+    start = i32(np.concatenate([[0], np.cumsum(n)]) if start is None else start)
     lib.mla_absorb_tree8(ql, qr, start, i32(lens), None if mask is None else torch.from_numpy(mask).to(DEV),
-                         torch.from_numpy(kv8).to(DEV), torch.from_numpy(scale).to(DEV), i32(table), page, SM, ws, out,
+                         torch.from_numpy(kv8).to(DEV), torch.from_numpy(scale).to(DEV), i32(table), page, sm, ws, out,
                          err_word=err)
     torch.cuda.synchronize()
     return out.double().cpu().numpy(), err.item()
@@ -192,6 +192,34 @@ def test_queries_that_are_not_finite(lib, oracle, q_dtype):
     assert err == 0
     assert np.isnan(got[hit]).all()
     assert np.array_equal(got[~hit], ref[~hit]) and not got[6].any()
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+def test_softmax_scales_of_either_sign_and_zero(lib, oracle, q_dtype):
+    """A negative sm_scale is the positive one with the queries' signs turned (the products' signs alone differ, so to the
+    bit); with 0 every row counts the same, to the bounds of a query of zeros."""
+    rng = np.random.default_rng(33)
+    H, lens, n, page = 20, [200, 0], [7, 4], 64
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    sees = [np.tril(np.ones((m, m), bool)) for m in n]
+    q = queries(rng, sum(n), H, q_dtype == F32)
+    pos, _ = run_tree(lib, -q, q_dtype, F32, n, lens, None, kv8, scale, table, page)
+    neg, err = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8, scale, table, page, sm=-SM)
+    assert err == 0 and np.array_equal(neg, pos)
+    flat, _ = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8, scale, table, page, sm=0.0)
+    check(flat, 0 * q, n, lens, sees, kv8, scale, rows, F32, q_dtype == F32)
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+def test_starts_that_go_back_spare_the_sequences_after_them(lib, oracle, q_dtype):
+    """q_start 9, 0, 4, 9: the first sequence is impossible, the others are as they would be alone."""
+    rng = np.random.default_rng(35)
+    H, lens, n, page = 128, [40, 130, 7], [1, 4, 5], 16
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    q = queries(rng, 9, H, q_dtype == F32)
+    got, err = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8, scale, table, page, start=[9, 0, 4, 9])
+    assert err == BAD_INDEX
+    check(got, q, n[1:], lens[1:], [np.tril(np.ones((m, m), bool)) for m in n[1:]], kv8, scale, rows[1:], F32, q_dtype == F32)
 
 
 @pytest.mark.parametrize("q_dtype", [BF, F32])
