@@ -195,6 +195,52 @@ def test_queries_that_are_not_finite(lib, oracle, q_dtype):
 
 
 @pytest.mark.parametrize("q_dtype", [BF, F32])
+def test_pages_that_sequences_share(lib, oracle, q_dtype):
+    """Three sequences whose contexts begin with the same two pages, each with its own pages behind them."""
+    rng = np.random.default_rng(37)
+    H, page, lens, n = 16, 64, [130, 128, 190], [9, 3, 1]
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    for b in (1, 2):
+        table[b, :2] = table[0, :2]
+        rows[b] = np.concatenate([rows[0][:128], rows[b][128:]])
+    sees = [np.tril(np.ones((m, m), bool)) for m in n]
+    q = queries(rng, sum(n), H, q_dtype == F32)
+    got, err = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8, scale, table, page)
+    assert err == 0
+    check(got, q, n, lens, sees, kv8, scale, rows, F32, q_dtype == F32)
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+def test_the_most_sequences(lib, oracle, q_dtype):
+    """4096 sequences of 0 to 2 tokens over contexts of 0 to 70 rows; every 37th is checked."""
+    rng = np.random.default_rng(39)
+    B, H, page = 4096, 8, 16
+    n = [int(x) for x in rng.integers(0, 3, B)]
+    lens = [int(x) for x in rng.integers(0, 71, B)]
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    q = queries(rng, sum(n), H, q_dtype == F32)
+    got, err = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8, scale, table, page)
+    assert err == 0 and np.isfinite(got).all()
+    at = np.concatenate([[0], np.cumsum(n)])
+    pick = [b for b in range(0, B, 37) if n[b]]
+    own = np.concatenate([np.arange(at[b], at[b + 1]) for b in pick])
+    check(got[own], q[own], [n[b] for b in pick], [lens[b] for b in pick], [np.tril(np.ones((n[b], n[b]), bool)) for b in pick],
+          kv8, scale, [rows[b] for b in pick], F32, q_dtype == F32)
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+def test_a_long_context(lib, oracle, q_dtype):
+    """50000 rows: many steps of one column's sums, and every share a part of two groups."""
+    rng = np.random.default_rng(41)
+    H, page, lens, n = 3, 128, [50000], [2]
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    q = queries(rng, sum(n), H, q_dtype == F32)
+    got, err = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8, scale, table, page)
+    assert err == 0
+    check(got, q, n, lens, [np.tril(np.ones((2, 2), bool))], kv8, scale, rows, F32, q_dtype == F32)
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
 def test_softmax_scales_of_either_sign_and_zero(lib, oracle, q_dtype):
     """A negative sm_scale is the positive one with the queries' signs turned (the products' signs alone differ, so to the
     bit); with 0 every row counts the same, to the bounds of a query of zeros."""
