@@ -88,6 +88,7 @@ struct Misc {
         float top[kTeams][2][kCols];       // X of a team's two blocks
         float red[2 * kTeams][kCols];      // at the end: sums
     };
+    TreeWalk walk;                         // the softmax's: one thread's, kept out of the others' registers
     TreeSegment seg[3];                    // this segment and the next two
     int more[3];
     uint64_t kv_full[kStages], kv_free[kStages], row_full[kStages], s_free[2], s_full[kTeams], w_full[kTeams], pv_done[kTeams],
@@ -665,8 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // One thread walks the share, two segments ahead of the others.
         if (st == 0) {
-            ms.more[0] = walk.next<kCols, kRows>(a, ms.seg[0]);
-            ms.more[1] = walk.next<kCols, kRows>(a, ms.seg[1]);
+            ms.walk = walk;
+            ms.more[0] = ms.walk.next<kCols, kRows>(a, ms.seg[0]);
+            ms.more[1] = ms.walk.next<kCols, kRows>(a, ms.seg[1]);
         }
         if (st < kCols) ms.ref[st] = -INFINITY;
         named_sync(1, kSoftmax);
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int now = 0; ms.more[now]; ++segments) {
             const TreeSegment &sg = ms.seg[now];
             const int next = now == 2 ? 0 : now + 1, third = 3 - now - next;
-            if (st == 0) ms.more[third] = walk.next<kCols, kRows>(a, ms.seg[third]);
+            if (st == 0) ms.more[third] = ms.walk.next<kCols, kRows>(a, ms.seg[third]);
             first_tile = end_tile;
             end_tile += sg.t1 - sg.t0;
             const int plain_end = first_tile + (int)min(sg.q.len / kRows - sg.t0, (int64_t)(end_tile - first_tile));  // tiles of context only
