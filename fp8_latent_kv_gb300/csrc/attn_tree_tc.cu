@@ -277,17 +277,25 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
     const int quarter = (blockIdx.x - 1) % (kCols / kPrepCols);
     // the slot's sequence: the last one whose images begin at or before it (whatever an impossible one before it says)
     __shared__ int last;
+    __shared__ TreeSeq found;
     if (tid == 0) last = -1;
     __syncthreads();
-    int b = -1;
-    for (int k = tid; k < a.B; k += kPrepThreads)
-        if (tree_slot(__ldg(a.q_start + k), a.H, k) <= slot) b = k;
-    b = __reduce_max_sync(0xffffffffu, b);
+    int mine_b = -1;
+    TreeSeq q{};
+    for (int k = tid; k < a.B; k += kPrepThreads) {
+        const TreeSeq t = tree_seq(a.q_start, a.lens, k, a.R, tree_positions(a.max_pages, a.page_shift));
+        if (tree_slot(t.q0, a.H, k) > slot) continue;
+        mine_b = k;
+        q = t;
+    }
+    int b = __reduce_max_sync(0xffffffffu, mine_b);
     if (lane == 0 && b >= 0) atomicMax(&last, b);
     __syncthreads();
     b = last;
     if (b < 0) return;
-    const TreeSeq q = tree_seq(a.q_start, a.lens, b, a.R, tree_positions(a.max_pages, a.page_shift));
+    if (mine_b == b) found = q;
+    __syncthreads();
+    q = found;
     const int64_t col0 = (slot - tree_slot(q.q0, a.H, b)) * kCols + quarter * kPrepCols, cols = (int64_t)q.n * a.H;
     // (a group's columns that the sequence does not have are zeros)
     if (q.n <= 0 || col0 < 0 || col0 - quarter * kPrepCols >= cols) return;
@@ -314,9 +322,8 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(TreeArgs a, uin
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const uint32_t bits = __reduce_max_sync(0xffffffffu, max(chunk_max(u[k]), rope == k ? m_rope : 0u));
-        const float mx = __uint_as_float(bits << 16);
-        int E = 0;
-        if (bits != 0u && bits < 0x7F80u) frexpf(mx, &E);
+        // max |q| = f 2^E, f in [1/2, 1), of a bf16's bits
+        const int E = bits >= 0x80u ? (int)(bits >> 7) - 126 : 32 - __clz(bits) - 133;
         const int sh = bits != 0u && bits < 0x7F80u ? 8 - E : 0;  // max |q| 2^sh in [128, 256)
         const int half = min(sh, 127);                            // (sh from -120 to 140)
         const float sign = a.sm_scale_log2 < 0.f ? -1.f : 1.f;    // the column's factor is not negative

@@ -53,7 +53,8 @@ struct TreeSched {
     int pad[2];
     TreeShare share[kMaxShares + 1];  // [shares] ends the last one
     TreeJob job[kMaxShares];
-    int64_t unit0[KV8_MAX_SEQS + 1];  // tiles before sequence b
+    int64_t unit0[KV8_MAX_SEQS + 1];  // tiles and groups before sequence b, where they are more than shared memory takes
+    int group0[KV8_MAX_SEQS + 1];
 };
 
 struct TreeArgs {
@@ -123,123 +124,130 @@ __device__ __forceinline__ uint64_t tree_attended(const TreeArgs &a, int q0, int
     return skip ? bits << skip | (((uint64_t)1 << skip) - 1) : bits;
 }
 
-// One block: the shares and the cut groups.
+// One block of 256 threads or more: the shares and the cut groups.
+constexpr int kScanSeqs = 1024;
 struct TreeScan {  // in shared memory
-    int64_t v[66];
-    int64_t unit[kMaxShares + 1];      // the shares' `unit`
-    int64_t work0[KV8_MAX_SEQS + 1];   // work before sequence b
+    int64_t unit0[kScanSeqs + 1];  // as in TreeSched
+    int64_t unit[kMaxShares + 1];  // the shares' `unit`
+    int64_t units[32];             // by warp
+    int groups[32];
+    int group0[kScanSeqs + 1];
+    int jobs;
 };
 template <int kCols, int kRows, int kSegment, int kLeast>
 __device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
     TreeSched &s = *a.sched;
-    int64_t *const scan = sm.v;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = (blockDim.x + 31) >> 5;
     const int64_t positions = tree_positions(a.max_pages, a.page_shift);
+    int64_t *const unit0 = a.B <= kScanSeqs ? sm.unit0 : s.unit0;
+    int *const group0 = a.B <= kScanSeqs ? sm.group0 : s.group0;
     const int per = (a.B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    auto size_of = [&](int b, bool &bad, int64_t &groups, int64_t &tiles) {
+    auto size_of = [&](int b, int &groups, int &tiles) -> TreeSeq {
         const TreeSeq q = tree_seq(a.q_start, a.lens, b, a.R, positions);
-        bad |= q.n < 0;
         groups = q.n > 0 ? (q.n * a.H + kCols - 1) / kCols : 0;
-        tiles = (q.len + q.n + kRows - 1) / kRows;
+        tiles = q.n > 0 ? (int)((q.len + q.n + kRows - 1) / kRows) : 0;
+        return q;
     };
     bool bad = false;
-    int64_t groups, tiles, units = 0, work = 0;
+    int groups = 0, tiles = 0, gs = 0;
+    int64_t us = 0;
     for (int b = b0; b < b1; ++b) {
-        size_of(b, bad, groups, tiles);
-        units += groups * tiles;
-        work += groups * (tiles + kSegment);
+        bad |= size_of(b, groups, tiles).n < 0;
+        us += (int64_t)groups * tiles;
+        gs += groups;
     }
     if (bad && a.err_word) atomicOr(a.err_word, (int)KV8_ERR_INDEX);
-    int64_t ui = units, wi = work;
+    int64_t ui = us;
+    int gi = gs;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, ui, o), w = __shfl_up_sync(0xffffffffu, wi, o);
+        const int64_t u = __shfl_up_sync(0xffffffffu, ui, o);
+        const int g = __shfl_up_sync(0xffffffffu, gi, o);
         if (lane >= o) {
             ui += u;
-            wi += w;
+            gi += g;
         }
     }
     if (lane == 31) {
-        scan[warp] = ui;
-        scan[33 + warp] = wi;
+        sm.units[warp] = ui;
+        sm.groups[warp] = gi;
     }
     __syncthreads();
-    if (warp == 0) {
-        int64_t u = lane < n_warps ? scan[lane] : 0, w = lane < n_warps ? scan[33 + lane] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, u, o), y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) {
-                u += x;
-                w += y;
-            }
+    int64_t U = 0, u_at = ui - us;
+    int G = 0, g_at = gi - gs;
+    for (int w = 0; w < n_warps; ++w) {
+        if (w == warp) {
+            u_at += U;
+            g_at += G;
         }
-        scan[lane] = u;
-        scan[33 + lane] = w;
+        U += sm.units[w];
+        G += sm.groups[w];
     }
-    __syncthreads();
-    int64_t u_at = ui - units + (warp > 0 ? scan[warp - 1] : 0), w_at = wi - work + (warp > 0 ? scan[33 + warp - 1] : 0);
     for (int b = b0; b < b1; ++b) {
-        bool ignored = false;
-        s.unit0[b] = u_at;
-        sm.work0[b] = w_at;
-        size_of(b, ignored, groups, tiles);
-        u_at += groups * tiles;
-        w_at += groups * (tiles + kSegment);
+        unit0[b] = u_at;
+        group0[b] = g_at;
+        if (per > 1) size_of(b, groups, tiles);
+        u_at += (int64_t)groups * tiles;
+        g_at += groups;
     }
-    const int64_t U = scan[n_warps - 1], W = scan[33 + n_warps - 1];
+    const int64_t W = U + (int64_t)kSegment * G;
     const int C = (int)min((int64_t)a.ctas, (U + kLeast - 1) / kLeast);
     if (tid == 0) {
-        s.unit0[a.B] = U;
-        sm.work0[a.B] = W;
-        s.jobs = 0;
+        sm.jobs = 0;
         s.shares = C;
     }
     __syncthreads();
-    for (int c = tid; c <= C; c += blockDim.x) {
-        TreeShare sh{};
-        sh.unit = U;
-        sh.b = a.B;
+    // (most numbers have 32 bits, whose divisions are a fraction of the longer ones' time)
+    constexpr int kPer = kMaxShares / 256 + 1;
+    TreeShare sh[kPer];
+    TreeSeq q[kPer];
+    int its[kPer];  // tiles of the share's first group
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int c = tid + i * (int)blockDim.x;
+        if (c > C) break;
+        sh[i] = TreeShare{U, a.B, 0, 0, 0};
         if (c < C) {
-            const int64_t w = W / C * c + W % C * c / C;  // floor(W c / C) without the product
-            int lo = 0, hi = a.B;  // work0[lo] <= w < work0[hi]: the last such sequence, so it has work
+            const bool narrow = W <= 0x7fffffff;
+            const int64_t w = narrow ? (int64_t)((uint32_t)W / C * c + (uint32_t)W % C * c / C) : W / C * c + W % C * c / C;  // floor(W c / C)
+            int lo = 0, hi = a.B;  // work before lo <= w < work before hi: the last such sequence, so it has work
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (sm.work0[mid] <= w) lo = mid;
+                if (unit0[mid] + (int64_t)kSegment * group0[mid] <= w) lo = mid;
                 else hi = mid;
             }
-            bool ignored = false;
-            size_of(lo, ignored, groups, tiles);
-            const int64_t r = w - sm.work0[lo], g = r / (tiles + kSegment), t = r - g * (tiles + kSegment) - kSegment;
+            q[i] = size_of(lo, groups, its[i]);
+            const int64_t r = w - unit0[lo] - (int64_t)kSegment * group0[lo];
+            const int each = its[i] + kSegment;
+            const int g = narrow ? (int)((uint32_t)r / (uint32_t)each) : (int)(r / each);
             // (a cut in a group's start and end cost is one before its first tile)
-            sh.b = lo;
-            sh.g = (int)g;
-            sh.t = (int)max(t, (int64_t)0);
-            sh.unit = s.unit0[lo] + g * tiles + sh.t;
+            const int t = max((int)(r - (int64_t)g * each) - kSegment, 0);
+            sh[i] = TreeShare{unit0[lo] + (int64_t)g * its[i] + t, lo, g, t, 0};
         }
-        s.share[c] = sh;
-        sm.unit[c] = sh.unit;
+        s.share[c] = sh[i];
+        sm.unit[c] = sh[i].unit;
     }
     __syncthreads();
     // a share that begins inside a group whose first tile the share before it walks: that group is cut
-    for (int c = 1 + tid; c < C; c += blockDim.x) {
-        const TreeShare sh = s.share[c];  // (this thread's own)
-        if (sh.t == 0 || sh.unit - sh.t < sm.unit[c - 1]) continue;
-        bool ignored = false;
-        size_of(sh.b, ignored, groups, tiles);
-        const int64_t end = sh.unit - sh.t + tiles;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int c = tid + i * (int)blockDim.x;
+        if (c >= C) break;
+        const int64_t begin = sh[i].unit - sh[i].t, end = begin + its[i];
+        if (c == 0 || sh[i].t == 0 || begin < sm.unit[c - 1]) continue;
         int lo = c, hi = C;  // the share that holds the group's last tile: unit[lo] < end <= unit[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (sm.unit[mid] < end) lo = mid;
             else hi = mid;
         }
-        const TreeSeq q = tree_seq(a.q_start, a.lens, sh.b, a.R, positions);
-        const int64_t at = (int64_t)sh.g * kCols;
-        s.job[atomicAdd(&s.jobs, 1)] =
-            TreeJob{(int64_t)q.q0 * a.H + at, (int)min((int64_t)kCols, (int64_t)q.n * a.H - at), c - 1, lo - c + 2, 0};
+        const int64_t at = (int64_t)sh[i].g * kCols;
+        s.job[atomicAdd(&sm.jobs, 1)] = TreeJob{(int64_t)q[i].q0 * a.H + at, (int)min((int64_t)kCols, (int64_t)q[i].n * a.H - at),
+                                                c - 1, lo - c + 2, 0};
     }
+    __syncthreads();
+    if (tid == 0) s.jobs = sm.jobs;
 }
 
 // The next segment of a CTA's share: tiles [t0, t1) of group g of sequence b.
