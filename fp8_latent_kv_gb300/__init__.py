@@ -90,10 +90,11 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev=None) -> int:
     if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # (3 us less than by a Stream object)
+        # (3 us less than by a Stream object)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -235,9 +236,9 @@ def _dtype_code(dtype) -> int:
     raise TypeError(f"float32 or bfloat16 expected, got {dtype}")
 
 
-def _args(fn: str, *args) -> None:
+def _args(fn: str, *args) -> int:
     """Checks of the paged calls' tensors, each (name, tensor, dtype, shape): a wrong one would be read or
-    written out of its bounds by a kernel, so it is refused here.  None passes (an optional argument)."""
+    written out of its bounds by a kernel, so it is refused here.  None passes (an optional argument).  Returns the device."""
     import torch
     dev = torch.cuda.current_device()
     for name, t, dtype, shape in args:
@@ -250,6 +251,8 @@ def _args(fn: str, *args) -> None:
         if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}"
                              f"{'' if t.is_contiguous() else ' with strides ' + str(t.stride())}")
+    return dev
+
 
 
 def kv8_page_plan(lens, q_start, page_size: int, n_pages, block_table, free_list, n_free, slots, err_word=None,
@@ -259,12 +262,12 @@ def kv8_page_plan(lens, q_start, page_size: int, n_pages, block_table, free_list
     import torch
     i32 = torch.int32
     B, R = lens.numel(), slots.numel()
-    _args("kv8_page_plan", ("lens", lens, i32, (B,)), ("q_start", q_start, i32, (B + 1,)), ("n_pages", n_pages, i32, (B,)),
+    dev = _args("kv8_page_plan", ("lens", lens, i32, (B,)), ("q_start", q_start, i32, (B + 1,)), ("n_pages", n_pages, i32, (B,)),
           ("block_table", block_table, i32, (B, block_table.shape[-1])), ("free_list", free_list, i32, (free_list.numel(),)),
           ("n_free", n_free, i32, (1,)), ("slots", slots, torch.int64, (R,)), ("err_word", err_word, i32, (1,)))
     _check("kv8_page_plan", load().kv8_page_plan(
-        B, _ptr(lens), _ptr(q_start), R, page_size, block_table.shape[1], _ptr(n_pages), _ptr(block_table),
-        _ptr(free_list), free_list.numel(), _ptr(n_free), _ptr(slots), _ptr(err_word), _stream(stream)))
+        B, lens.data_ptr(), q_start.data_ptr(), R, page_size, block_table.shape[1], n_pages.data_ptr(), block_table.data_ptr(),
+        free_list.data_ptr(), free_list.numel(), n_free.data_ptr(), slots.data_ptr(), _ptr(err_word), _stream(stream, dev)))
 
 
 def kv8_tree_mask(parent, q_start, lens, mask, position=None, err_word=None, stream=None) -> None:
@@ -272,10 +275,11 @@ def kv8_tree_mask(parent, q_start, lens, mask, position=None, err_word=None, str
     import torch
     i32 = torch.int32
     B, R = q_start.numel() - 1, parent.numel()
-    _args("kv8_tree_mask", ("parent", parent, i32, (R,)), ("q_start", q_start, i32, (B + 1,)), ("lens", lens, i32, (B,)),
+    dev = _args("kv8_tree_mask", ("parent", parent, i32, (R,)), ("q_start", q_start, i32, (B + 1,)), ("lens", lens, i32, (B,)),
           ("mask", mask, i32, (R, mask.shape[-1])), ("position", position, i32, (R,)), ("err_word", err_word, i32, (1,)))
-    _check("kv8_tree_mask", load().kv8_tree_mask(B, _ptr(q_start), _ptr(lens), R, _ptr(parent), _ptr(mask), mask.shape[1],
-                                                 _ptr(position), _ptr(err_word), _stream(stream)))
+    _check("kv8_tree_mask", load().kv8_tree_mask(
+        B, q_start.data_ptr(), _ptr(lens), R, parent.data_ptr(), mask.data_ptr(), mask.shape[1], _ptr(position),
+        _ptr(err_word), _stream(stream, dev)))
 
 
 def mla_tree8_workspace_bytes(R: int, H: int, B: int, q_dtype) -> int:
@@ -294,17 +298,17 @@ def mla_absorb_tree8(q_lat, q_rope, q_start, lens, mask, kv8, kv_scale, block_ta
     i32, f32 = torch.int32, torch.float32
     R, H = q_lat.shape[0], q_lat.shape[1]
     B, rows = lens.numel(), kv8.shape[0]
-    _args("mla_absorb_tree8", ("q_lat", q_lat, q_lat.dtype, (R, H, 512)), ("q_rope", q_rope, q_lat.dtype, (R, H, 64)),
+    dev = _args("mla_absorb_tree8", ("q_lat", q_lat, q_lat.dtype, (R, H, 512)), ("q_rope", q_rope, q_lat.dtype, (R, H, 64)),
           ("q_start", q_start, i32, (B + 1,)), ("lens", lens, i32, (B,)),
           ("mask", mask, i32, (R, 0 if mask is None else mask.shape[-1])), ("kv8", kv8, torch.uint8, (rows, 576)),
           ("kv_scale", kv_scale, f32, (rows,)), ("block_table", block_table, i32, (B, block_table.shape[-1])),
           ("workspace", workspace, workspace.dtype, workspace.shape), ("out", out, out.dtype, (R, H, 512)),
           ("err_word", err_word, i32, (1,)))
     _check("mla_absorb_tree8", load().mla_absorb_tree8(
-        _ptr(q_lat), _ptr(q_rope), _dtype_code(q_lat.dtype), R, H, B, _ptr(q_start), _ptr(lens), _ptr(mask),
-        0 if mask is None else mask.shape[1], _ptr(kv8), _ptr(kv_scale), rows, _ptr(block_table), block_table.shape[1],
-        page_size, sm_scale, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_word), _ptr(out),
-        _dtype_code(out.dtype), _stream(stream)))
+        q_lat.data_ptr(), q_rope.data_ptr(), _dtype_code(q_lat.dtype), R, H, B, q_start.data_ptr(), lens.data_ptr(), _ptr(mask),
+        0 if mask is None else mask.shape[1], kv8.data_ptr(), kv_scale.data_ptr(), rows, block_table.data_ptr(),
+        block_table.shape[1], page_size, sm_scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(err_word), out.data_ptr(),
+        _dtype_code(out.dtype), _stream(stream, dev)))
 
 
 def kv8_tree_commit(q_start, lens, accept, n_accept, kv8, kv_scale, block_table, page_size: int, new_lens, err_word=None,
@@ -316,15 +320,15 @@ def kv8_tree_commit(q_start, lens, accept, n_accept, kv8, kv_scale, block_table,
     B, rows = lens.numel(), kv8.shape[-2]
     layers = kv8.shape[0] if kv8.dim() == 3 else 1
     shape = (layers, rows) if kv8.dim() == 3 else (rows,)
-    _args("kv8_tree_commit", ("q_start", q_start, i32, (B + 1,)), ("lens", lens, i32, (B,)),
+    dev = _args("kv8_tree_commit", ("q_start", q_start, i32, (B + 1,)), ("lens", lens, i32, (B,)),
           ("accept", accept, i32, (B, accept.shape[-1])), ("n_accept", n_accept, i32, (B,)),
           ("kv8", kv8, torch.uint8, (*shape, 576)), ("kv_scale", kv_scale, torch.float32, shape),
           ("block_table", block_table, i32, (B, block_table.shape[-1])), ("new_lens", new_lens, i32, (B,)),
           ("err_word", err_word, i32, (1,)))
     _check("kv8_tree_commit", load().kv8_tree_commit(
-        B, _ptr(q_start), _ptr(lens), _ptr(accept), _ptr(n_accept), accept.shape[1], layers, _ptr(kv8),
-        _ptr(kv_scale), rows, _ptr(block_table), block_table.shape[1], page_size, _ptr(new_lens), _ptr(err_word),
-        _stream(stream)))
+        B, q_start.data_ptr(), lens.data_ptr(), accept.data_ptr(), n_accept.data_ptr(), accept.shape[1], layers, kv8.data_ptr(),
+        kv_scale.data_ptr(), rows, block_table.data_ptr(), block_table.shape[1], page_size, new_lens.data_ptr(), _ptr(err_word),
+        _stream(stream, dev)))
 
 
 def kv8_wait_selftest(limit_ns: int, err_word, wait_status, stream=None) -> None:

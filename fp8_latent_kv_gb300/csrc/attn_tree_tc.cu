@@ -26,7 +26,7 @@
 // What bounds it: a tile's products take 1408 cycles of the tensor pipe (18 score MMAs of 32 to 48 cycles, 16 context MMAs of
 // 48), a tile 1570 in all where a share has hundreds of them, the pipe busy 69 %: two teams' 3.9 thousand warp instructions
 // a tile, more than half of them conversions, maxima and exchanges of the softmax, take most of the issue slots.  64 tokens of
-// 128 heads over 32768 rows: 403 us, 1451 TFLOP/s.  Three teams did not pay: of eight warps each they spilled (658 us against 522
+// 128 heads over 32768 rows: 396 us, 1476 TFLOP/s.  Three teams did not pay: of eight warps each they spilled (658 us against 522
 // then), of four they missed the instruction cache (557 against 497).
 // Warps: 0 = row loads, 1 = scores and TMEM, 2 = the rows' scales, 3 = context products, 4..19 = softmax and output in
 // two teams that take alternate tiles.  warp % 4 is a warp's TMEM lane quadrant, its set (0, 1) the block of 32 rows,

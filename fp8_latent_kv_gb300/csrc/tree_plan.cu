@@ -308,9 +308,10 @@ cudaError_t launch_page_plan(int B, const int32_t *lens, const int32_t *q_start,
                              int64_t *slots, int *err_word, cudaStream_t st) {
     PlanArgs a{B, R, page_shift, max_pages, free_cap, lens, q_start, n_pages, table, free_list, n_free, slots, err_word};
     const size_t smem = (size_t)B * 4 * sizeof(int32_t);
-    cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(KV8_MAX_SEQS * 4 * sizeof(int32_t)));
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    if (smem > 48 * 1024 && (e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                      (int)(KV8_MAX_SEQS * 4 * sizeof(int32_t)))) != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kPlanCtas);
     cfg.blockDim = dim3(kPlanThreads);
