@@ -29,6 +29,10 @@ using namespace sm100;
 constexpr int kCols = 32;      // (token, head) columns per block
 constexpr int kUnit = 32;      // rows that the shares count
 constexpr int kRows = 64;      // rows per step: two units where there are two
+// A segment's start and end cost as much as this many units: 16 sequences of up to 4 tokens of 32 heads over up to 700 rows
+// took 42.2 us with 0, 34.2 with 1, 30.7 with 2, 28.6 with 4, 32.3 with 8; 30 of up to 3 tokens of 20 heads over up to 3000
+// rows 78.1, 77.2, 72.0, 72.6, 77.1.
+constexpr int kSegment = 4;
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 // Strides in bytes.  A tile's: 16-byte copies, and 148 words put eight rows' four words into 32 banks.  A query column's: four
@@ -59,7 +63,7 @@ __global__ void __launch_bounds__(288) tree_sched_kernel(TreeArgs a) {
     __shared__ TreeScan scan;
     grid_dependency_wait();
     grid_launch_dependents();
-    tree_schedule<kCols, kUnit, 1, 1>(a, scan);  // (two units a share instead of one: 46 -> 54 us for 4 x 5 tokens of 16 heads)
+    tree_schedule<kCols, kUnit, kSegment, 1>(a, scan);
 }
 
 // Floats as whole numbers of the same order, and back.
