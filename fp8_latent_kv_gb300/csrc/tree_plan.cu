@@ -16,6 +16,11 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCtas = 8;  // (one CTA: 4.0 us as well for 4 sequences, 6.2 against 4.8 for 256, 40 against 10 for 4096)
 constexpr int kPlanPer = KV8_MAX_SEQS / kPlanThreads;  // sequences per thread in the scans
+// All of the kernel's shared memory is the launch's, so that its size alone says which launches need the larger limit: the
+// warps' sums, then four words a sequence.
+constexpr size_t kPlanSums = 32 * 2 * sizeof(int64_t);
+constexpr size_t plan_smem_bytes(int B) { return kPlanSums + (size_t)B * 4 * sizeof(int32_t); }
+constexpr size_t kDefaultSmem = 48 * 1024;  // what a launch may have without asking
 
 struct PlanArgs {
     int B, R, page_shift, max_pages, free_cap;
@@ -30,9 +35,9 @@ __device__ __forceinline__ void cluster_sync_all() {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
-    extern __shared__ __align__(16) int32_t psm[];
-    int32_t *have = psm, *want = psm + a.B, *spre = psm + 2 * a.B, *npre = psm + 3 * a.B;
-    __shared__ int64_t wsum[32][2];
+    extern __shared__ __align__(16) unsigned char plan_smem[];
+    int64_t(*const wsum)[2] = reinterpret_cast<int64_t(*)[2]>(plan_smem);
+    int32_t *have = reinterpret_cast<int32_t *>(plan_smem + kPlanSums), *want = have + a.B, *spre = want + a.B, *npre = spre + a.B;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t positions = 0x7fffffff;  // a table that is too narrow is a page error, not a bad number
     int err = 0;
@@ -307,10 +312,10 @@ cudaError_t launch_page_plan(int B, const int32_t *lens, const int32_t *q_start,
                              int32_t *n_pages, int32_t *table, int32_t *free_list, int free_cap, int32_t *n_free,
                              int64_t *slots, int *err_word, cudaStream_t st) {
     PlanArgs a{B, R, page_shift, max_pages, free_cap, lens, q_start, n_pages, table, free_list, n_free, slots, err_word};
-    const size_t smem = (size_t)B * 4 * sizeof(int32_t);
+    const size_t smem = plan_smem_bytes(B);
     cudaError_t e;
-    if (smem > 48 * 1024 && (e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      (int)(KV8_MAX_SEQS * 4 * sizeof(int32_t)))) != cudaSuccess)
+    if (smem > kDefaultSmem && (e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                         (int)plan_smem_bytes(KV8_MAX_SEQS))) != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kPlanCtas);
