@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) tree_prep_kernel(TreeArgs a, 
     }
     const int64_t slot = (blockIdx.x - 1) / (kCols / kPrepCols);
     const int quarter = (blockIdx.x - 1) % (kCols / kPrepCols);
-    // the slot's sequence: the last one whose images begin at or before it (whatever an impossible one before it says)
+    // the slot's sequence: the last one with rows whose images begin at or before it (an impossible one's start says nothing)
     __shared__ int last;
     __shared__ TreeSeq found;
     if (tid == 0) last = -1;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) tree_prep_kernel(TreeArgs a, 
     TreeSeq q{};
     for (int k = tid; k < a.B; k += kPrepThreads) {
         const TreeSeq t = tree_seq(a.q_start, a.lens, k, a.R, tree_positions(a.max_pages, a.page_shift));
-        if (tree_slot(t.q0, a.H, k) > slot) continue;
+        if (t.n <= 0 || tree_slot(t.q0, a.H, k) > slot) continue;
         mine_b = k;
         q = t;
     }
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) tree_prep_kernel(TreeArgs a, 
     q = found;
     const int64_t col0 = (slot - tree_slot(q.q0, a.H, b)) * kCols + quarter * kPrepCols, cols = (int64_t)q.n * a.H;
     // (a group's columns that the sequence does not have are zeros)
-    if (q.n <= 0 || col0 < 0 || col0 - quarter * kPrepCols >= cols) return;
+    if (col0 - quarter * kPrepCols >= cols) return;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     // a warp's two columns: 32 chunks of latent elements by lane, four of RoPE elements by lanes 0..3 and 4..7
     uint4 u[3][2];
