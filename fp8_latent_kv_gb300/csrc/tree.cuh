@@ -23,6 +23,37 @@ __device__ __forceinline__ TreeSeq tree_seq(const int32_t *q_start, const int32_
     return s;
 }
 
+// Whether the sequences' rows go back: a possible sequence with rows begins before the end of an earlier one (which takes an
+// impossible one between them: each start is the end before it, so a batch without any need not be asked).  Calls that
+// place things by rows then leave the batch.  One block; a thread's sequences are [b0, b1), in order; `ends` has a word a warp.
+static __device__ __noinline__ bool tree_goes_back(const int32_t *q_start, const int32_t *lens, int b0, int b1, int R, int64_t positions,
+                                                   int *ends) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int most = 0;  // the largest end so far
+    bool back = false;
+    for (int b = b0; b < b1; ++b) {
+        const TreeSeq q = tree_seq(q_start, lens, b, R, positions);
+        if (q.n <= 0) continue;
+        back |= q.q0 < most;
+        most = max(most, q.q0 + q.n);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int m = __shfl_up_sync(0xffffffffu, most, o);
+        if (lane >= o) most = max(most, m);
+    }
+    if (lane == 31) ends[warp] = most;
+    most = __shfl_up_sync(0xffffffffu, most, 1);  // of the threads before
+    if (lane == 0) most = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) most = max(most, ends[w]);
+    for (int b = b0; b < b1; ++b) {
+        const TreeSeq q = tree_seq(q_start, lens, b, R, positions);
+        back |= q.n > 0 && q.q0 < most;
+    }
+    return __syncthreads_or(back);
+}
+
 // Positions that a table row of max_pages pages holds, as far as 32-bit lengths reach.
 __host__ __device__ __forceinline__ int64_t tree_positions(int max_pages, int page_shift) {
     const int64_t p = (int64_t)max_pages << page_shift;
@@ -130,7 +161,7 @@ struct TreeScan {  // in shared memory
     int64_t unit0[kScanSeqs + 1];  // as in TreeSched
     int64_t unit[kMaxShares + 1];  // the shares' `unit`
     int64_t units[32];             // by warp
-    int groups[32];
+    int groups[32], ends[32];
     int group0[kScanSeqs + 1];
     int jobs;
 };
@@ -173,7 +204,10 @@ __device__ void tree_schedule(const TreeArgs &a, TreeScan &sm) {
         sm.units[warp] = ui;
         sm.groups[warp] = gi;
     }
-    __syncthreads();
+    if (__syncthreads_or(bad) && tree_goes_back(a.q_start, a.lens, b0, b1, a.R, positions, sm.ends)) {
+        if (tid == 0) s.shares = s.jobs = 0;
+        return;
+    }
     int64_t U = 0, u_at = ui - us;
     int G = 0, g_at = gi - gs;
     for (int w = 0; w < n_warps; ++w) {

@@ -332,7 +332,9 @@ KV8_API int dsa_index_topk8(const void *q_idx, int q_dtype, const float *w, int 
  * differ between sequences and may be 0; n_b <= KV8_MAX_TREE; B in [1, KV8_MAX_SEQS].
  * A sequence whose numbers are not possible (lens[b] < 0, n_b < 0 or too large, rows outside [0, R), more
  * positions than its table holds) is skipped, what it would have written is left as it was, and
- * KV8_ERR_INDEX is set.
+ * KV8_ERR_INDEX is set.  Where a possible sequence's rows begin before the end of an earlier possible one's
+ * (which takes a q_start that falls between them), kv8_page_plan and mla_absorb_tree8 skip every sequence,
+ * with KV8_ERR_INDEX; kv8_tree_mask leaves words of either in rows that two sequences claim.
  *
  * kv8_page_plan -- block tables and slot maps from the lengths.  Afterwards every sequence holds exactly
  * the pages of its lens[b] + n_b rows, and slots[q_start[b] + i] is the cache row of its position

@@ -48,3 +48,45 @@ def test_impossible_starts_spare_the_sequences_before_them(lib, oracle, q_dtype,
         check(got[at], q[at], n[b:b + 1], lens[b:b + 1], chains(n[b:b + 1]), kv8, scale, rows[b:b + 1], F32, q_dtype == F32)
         left[at] = False
     assert (got[left] == 7.0).all()
+
+
+BACK = [([8, 12, 0, 4], 12, "a sequence before an earlier one"), ([0, 8, 4, 12], 12, "rows of two sequences"),
+        ([0, 8, 4, 12, 2, 9], 12, "rows of three"), ([0] + [5, 0] * 500 + [5, 9], 9, "the same rows, many times")]
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+@pytest.mark.parametrize("start,R,what", BACK, ids=[x[2] for x in BACK])
+def test_rows_that_go_back_are_left(lib, oracle, q_dtype, start, R, what):
+    """Possible sequences whose rows are not in order: nothing is written, and the error word says so."""
+    rng = np.random.default_rng(R)
+    H, page, B = 16, 16, len(start) - 1
+    lens = [int(x) for x in rng.integers(0, 60, B)]
+    kv8, scale, table, rows = build(oracle, rng, lens, [12] * B, page)
+    q = queries(rng, R, H, q_dtype == F32)
+    got, err = run_tree(lib, q, q_dtype, F32, None, lens, None, kv8, scale, table, page, start=start)
+    assert err == BAD_INDEX and (got == 7.0).all()
+
+
+@pytest.mark.parametrize("start,R,what", BACK, ids=[x[2] for x in BACK])
+def test_plan_of_rows_that_go_back_changes_nothing(lib, start, R, what):
+    B = len(start) - 1
+    state = dict(n_pages=[1] * B, block_table=np.arange(4 * B).reshape(B, 4), free_list=4 * B + np.arange(3 * B), n_free=[3 * B])
+    state = {k: i32(v) for k, v in state.items()}
+    before = {k: v.clone() for k, v in state.items()}
+    slots, err = torch.full((R,), -9, dtype=torch.int64, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    lib.kv8_page_plan(i32([20] * B), i32(start), 16, slots=slots, err_word=err, **state)
+    assert err.item() == BAD_INDEX and (slots == -9).all()
+    assert all(torch.equal(state[k], before[k]) for k in state)
+
+
+def test_plan_spares_possible_sequences_in_order(lib):
+    """An impossible start between sequences whose rows are in order, empty sequences with any start among them."""
+    start, lens = [9, 9, 0, 3, 3, -1, 3, 9], [1, 2, 17, 4, 5, 6, 15]
+    state = dict(n_pages=[0] * 7, block_table=np.full((7, 4), -7), free_list=np.arange(20), n_free=[20])
+    state = {k: i32(v) for k, v in state.items()}
+    slots, err = torch.full((9,), -9, dtype=torch.int64, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    lib.kv8_page_plan(i32(lens), i32(start), 16, slots=slots, err_word=err, **state)
+    assert err.item() == BAD_INDEX
+    # sequences 0 (2 positions' page, no rows), 2 (two pages), 3 (one) and 6 (two) from the top of the list
+    assert state["n_pages"].tolist() == [1, 0, 2, 1, 0, 0, 2] and state["n_free"].item() == 14
+    assert slots.tolist() == [17 * 16 + 1, 17 * 16 + 2, 17 * 16 + 3, 15 * 16 + 15] + [14 * 16 + i for i in range(5)]
