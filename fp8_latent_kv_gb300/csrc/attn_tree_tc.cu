@@ -21,6 +21,8 @@
 // binary orders below the block's largest (plain in the code; the others took 6.5 thousand cycles against 3.2).
 // w_t holds the row scale already: O = sum w_t v_t, z = sum w_t / scale_t.  A row whose scale is below 2^-60 (zeros,
 // subnormal maxima) has score 0 and adds nothing to O: such rows are only counted, and the count enters z at the end.
+// A row whose scale is above 2^60 would have its term of z, 2^-60 / scale relative to its weight, fall out of 32 bits: its
+// weight is NaN instead.
 //
 // Work: equal shares of (group, tile) units (tree.cuh), one CTA per SM.
 // What bounds it: a tile's products take 1408 cycles of the tensor pipe (18 score MMAs of 32 to 48 cycles, 16 context MMAs of
@@ -777,9 +779,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         f2_unpack(f2_mul(d2[4 + i], f2_mul(sc2[i], f2_pack(c_b, c_b))), e[1][0], e[1][1]);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            // a scale that is not a number must not meet the weight 0 of a column that leaves the row out,
-                            // and makes that of a column that does not NaN
-                            const bool fine = s[k] <= 3.402823466e38f;
+                            // a scale that is not a number, or so large that its term would be lost from z, must not meet the
+                            // weight 0 of a column that leaves the row out, and makes that of a column that does not NaN
+                            const bool fine = s[k] <= 1.f / kTiny;
                             const float lg = lg2_approx(s[k]);
                             s[k] = fine ? s[k] : 1.f;
 #pragma unroll

@@ -90,3 +90,53 @@ def test_plan_spares_possible_sequences_in_order(lib):
     # sequences 0 (2 positions' page, no rows), 2 (two pages), 3 (one) and 6 (two) from the top of the list
     assert state["n_pages"].tolist() == [1, 0, 2, 1, 0, 0, 2] and state["n_free"].item() == 14
     assert slots.tolist() == [17 * 16 + 1, 17 * 16 + 2, 17 * 16 + 3, 15 * 16 + 15] + [14 * 16 + i for i in range(5)]
+
+
+def with_scales(oracle, rng, lens, n, page, scales):
+    """build()'s cache with other row scales."""
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    for r in rows:
+        scale[r] = scales(len(r)).astype(np.float32)
+    return kv8, scale, table, rows
+
+
+@pytest.mark.parametrize("q_dtype,top", [(BF, 60), (F32, 60), (F32, 80)])
+@pytest.mark.parametrize("kind", ["small", "large", "both"])
+def test_row_scales_at_the_ends_of_their_range(lib, oracle, q_dtype, top, kind):
+    """Whole caches with scales next to 2^-60 (f32 queries: 2^-80 too) or 2^60, and both in one sequence, under queries that
+    bring the scores back to ordinary sizes."""
+    rng = np.random.default_rng(71)
+    H, page, lens, n = 24, 64, [700, 0, 63], [3, 9, 1]
+    low, high = 2.0 ** -top, 2.0 ** top
+
+    def scales(m):
+        s = rng.uniform(1, 4, m) * low
+        h = rng.uniform(0.25, 1, m) * high
+        return {"small": s, "large": h, "both": np.where(rng.random(m) < 0.5, s, h)}[kind]
+
+    kv8, scale, table, rows = with_scales(oracle, rng, lens, n, page, scales)
+    for r in rows:  # the ends themselves
+        if len(r) > 2 and kind != "large":
+            scale[r[1]] = low
+        if len(r) > 2 and kind != "small":
+            scale[r[2]] = high
+    q = queries(rng, sum(n), H, q_dtype == F32) * np.float32(2.0 ** -8 * (high if kind == "small" else low))
+    got, err = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8, scale, table, page)
+    assert err == 0
+    check(got, q, n, lens, chains(n), kv8, scale, rows, F32, q_dtype == F32)
+
+
+@pytest.mark.parametrize("at", [5, 320, 701])
+@pytest.mark.parametrize("big", [float(np.nextafter(np.float32(2.0 ** 60), np.float32(np.inf))), 2.0 ** 90, 2.0 ** 127])
+def test_larger_scales_than_bf16_queries_take_say_so(lib, oracle, big, at):
+    """One attended row beyond the range: NaN for every token that attends it, the others as they were."""
+    rng = np.random.default_rng(73)
+    H, page, lens, n = 16, 64, [700], [4]
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    q = queries(rng, 4, H, False)
+    ref, _ = run_tree(lib, q, BF, F32, n, lens, None, kv8, scale, table, page)
+    scale[rows[0][at]] = big
+    got, err = run_tree(lib, q, BF, F32, n, lens, None, kv8, scale, table, page)
+    first = max(0, at - 700)
+    assert err == 0 and np.isnan(got[first:]).all()
+    assert np.array_equal(got[:first], ref[:first])
