@@ -140,3 +140,20 @@ def test_larger_scales_than_bf16_queries_take_say_so(lib, oracle, big, at):
     first = max(0, at - 700)
     assert err == 0 and np.isnan(got[first:]).all()
     assert np.array_equal(got[:first], ref[:first])
+
+
+def test_smaller_scales_than_bf16_queries_take_count_as_zero_rows(lib, oracle):
+    """Below 2^-60 a row's score counts as 0 and its value as zeros; at 2^-60 and above it is itself.  The queries are such
+    that the scores of those rows would show."""
+    rng = np.random.default_rng(79)
+    H, page, lens, n = 16, 64, [300, 10], [3, 20]
+    edge = np.float32(2.0 ** -60)
+    below = np.nextafter(edge, np.float32(0))
+    kv8, scale, table, rows = with_scales(oracle, rng, lens, n, page, lambda m: np.where(rng.random(m) < 0.5, edge, below))
+    q = queries(rng, sum(n), H, False) * np.float32(2.0 ** 52)
+    as_zero = np.where(scale < edge, np.float32(0), scale)
+    sees = [rng.random((m, m)) < 0.6 for m in n]
+    mask = np.concatenate([pack(x, 1) for x in sees])
+    got, err = run_tree(lib, q, BF, F32, n, lens, mask, kv8, scale, table, page)
+    assert err == 0
+    check(got, q, n, lens, sees, kv8, as_zero, rows, F32, False)
