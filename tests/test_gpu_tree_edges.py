@@ -157,3 +157,50 @@ def test_smaller_scales_than_bf16_queries_take_count_as_zero_rows(lib, oracle):
     got, err = run_tree(lib, q, BF, F32, n, lens, mask, kv8, scale, table, page)
     assert err == 0
     check(got, q, n, lens, sees, kv8, as_zero, rows, F32, False)
+
+
+def test_f32_sums_of_many_small_terms(lib):
+    """2^17 rows that together weigh as much as one: sums of f32 queries are held to f32, not to the bf16 form's weights.
+
+    The bound, in steps of 2^-24 of the sums (all terms are positive): a weight's two f16 pieces leave 2^-22 (4); 64 rows are 8
+    products whose 17 terms may each be cut (136); a share is at most 2^17 / 32 / 100 + 1 units of 32 rows (100 shares or
+    more), so 21 such steps, each an addition to the context (21) and four to each of sixteen warps' sums (84 + 16); the merge adds
+    at most 2 x 152 parts (304, context and sums: at most as many again); the large row's score, 17 ln 2, has a product,
+    a factor and a constant (3 x 17 log2 e ln 2 = 51), exp2 and the merge's own (2 + 2).  In all 4 + 136 + 21 + 100 + 608 + 55 =
+    924: less than 2^-14."""
+    T, H, page = 1 << 17, 16, 1024
+    kv8 = np.zeros((T + page, 576), np.uint8)
+    kv8[:, 0] = 0x38                            # 1.0 in every row
+    kv8[T // 2, 1] = 0x38                       # the row that the query asks for
+    scale = np.ones(T + page, np.float32)
+    q = np.zeros((1, H, 576), np.float32)
+    q[:, :, 1] = round(17 * np.log(2) / SM)
+    p = np.exp(SM * float(q[0, 0, 1]))
+    got, err = run_tree(lib, q, F32, F32, [1], [T], None, kv8, scale, np.arange(T // page + 1)[None], page)
+    assert err == 0
+    assert np.abs(got[0, :, 0] - 1).max() <= 2.0 ** -14
+    assert np.abs(got[0, :, 1] - p / (p + T)).max() <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_a_cache_that_ends_inside_a_page(lib, oracle, q_dtype, page):
+    """cache_rows no multiple of the page: the last page's rows past the end are left out, with the error bit."""
+    rng = np.random.default_rng(83)
+    H, lens, n = 16, [3 * page + 5, 20], [7, 2]
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    end = max(int(r.max()) for r in rows) - 4        # inside the page that holds the highest row
+    valid = [r < end for r in rows]
+    q = queries(rng, sum(n), H, q_dtype == F32)
+    got, err = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8[:end].copy(), scale[:end].copy(), table, page)
+    assert err == BAD_INDEX
+    check(got, q, n, lens, chains(n), kv8, scale, [np.where(v, r, 0) for v, r in zip(valid, rows)], F32, q_dtype == F32, valid=valid)
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+def test_a_step_without_drafted_tokens(lib, oracle, q_dtype):
+    rng = np.random.default_rng(89)
+    kv8, scale, table, rows = build(oracle, rng, [30, 0], [0, 0], 16)
+    q = queries(rng, 3, 16, q_dtype == F32)
+    got, err = run_tree(lib, q, q_dtype, F32, [0, 0], [30, 0], None, kv8, scale, table, 16)
+    assert err == 0 and (got == 7.0).all()
