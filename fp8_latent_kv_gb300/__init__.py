@@ -332,8 +332,8 @@ def kv8_tree_commit(q_start, lens, accept, n_accept, kv8, kv_scale, block_table,
 
 
 def kv8_wait_selftest(limit_ns: int, err_word, wait_status, stream=None) -> None:
-    """Diagnostic: a bounded wait that nothing completes; sets KV8_ERR_TIMEOUT in err_word and 2 in wait_status
-    (both int32 device tensors) after limit_ns."""
+    """Diagnostic: both bounded waits on what nothing completes, limit_ns each; sets KV8_ERR_TIMEOUT in err_word and 2 in
+    wait_status (both int32 device tensors)."""
     _check("kv8_wait_selftest", load().kv8_wait_selftest(limit_ns, _ptr(err_word), _ptr(wait_status), _stream(stream)))
 
 

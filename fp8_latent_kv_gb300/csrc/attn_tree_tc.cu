@@ -156,35 +156,6 @@ __device__ __forceinline__ void mma_f8f6f4_ts(uint32_t d_tmem, uint32_t a_tmem, 
         : "memory");
 }
 
-// Bounded wait on the SM's own clock: reading the global timer takes about a microsecond, which a wait that is not
-// ready at once would pay every time.  2^32 cycles are two seconds; drains give a shorter limit.
-constexpr long long kLimit = 1ll << 32;
-
-// (Out of line: a wait that is not ready at once has time, and the code beside the ready ones stays small.)
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, int *abort_flag, int *err, long long limit) {
-    const long long t0 = clock64();
-    for (uint32_t i = 1;; ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (done) return true;
-        if ((i & 31u) == 0) {
-            if (abort_flag && *(volatile int *)abort_flag) return false;
-            if (clock64() - t0 > limit) {
-                if (abort_flag) *(volatile int *)abort_flag = 1;
-                if (err) atomicOr(err, (int)KV8_ERR_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, int *abort_flag, int *err, long long limit = kLimit) {
-    return mbar_try_wait(bar, parity) || bar_wait_slow(smem_u32(bar), parity, abort_flag, err, limit);
-}
-
 // True in one lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -450,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every load in flight lands before the CTA ends
         if (lane == 0)
             for (int i = max(0, it - kStages); i < it; ++i)
-                bar_wait(&ms.kv_full[i % kStages], (i / kStages) & 1, nullptr, a.err_word, kLimit / 8);
+                bar_wait(&ms.kv_full[i % kStages], (i / kStages) & 1, nullptr, a.err_word, kWaitCycles / 8);
         __syncwarp();
     } else if (warp == 1) {
         // ================================ scores ================================
@@ -499,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) mma_commit(&ms.final_bar[0]);  // all issued MMAs complete before the CTA tears down
         __syncwarp();
-        bar_wait(&ms.final_bar[0], 0, nullptr, a.err_word, kLimit / 8);
+        bar_wait(&ms.final_bar[0], 0, nullptr, a.err_word, kWaitCycles / 8);
         __syncwarp();
     } else if (warp == 3) {
         // ================================ context products ================================
@@ -548,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) mma_commit(&ms.final_bar[1]);
         __syncwarp();
-        bar_wait(&ms.final_bar[1], 0, nullptr, a.err_word, kLimit / 8);
+        bar_wait(&ms.final_bar[1], 0, nullptr, a.err_word, kWaitCycles / 8);
         __syncwarp();
     } else if (warp == 2) {
         // ================================ the rows' scales ================================
@@ -1047,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             now = next;
         }
         // the last copy of queries lands before the CTA ends
-        if (st == 0 && segments) bar_wait(&ms.q_ready, (segments - 1) & 1, nullptr, a.err_word, kLimit / 8);
+        if (st == 0 && segments) bar_wait(&ms.q_ready, (segments - 1) & 1, nullptr, a.err_word, kWaitCycles / 8);
     }
     tc_fence_before_sync();
     __syncthreads();

@@ -57,8 +57,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Wait for the phase with the given parity to complete, giving up after `limit_ns`.  On a timeout it
-// sets KV8_ERR_TIMEOUT in *err (if given) and *abort_flag (shared), and returns false.
 // Non-blocking test of the phase with the given parity (for a thread that polls several barriers).
 __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
@@ -72,6 +70,8 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Wait for the phase with the given parity to complete, giving up after `limit_ns`.  On a timeout it
+// sets KV8_ERR_TIMEOUT in *err (if given) and *abort_flag (shared), and returns false.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err,
                                           uint64_t limit_ns = 2000000000ull) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -87,6 +87,35 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
             }
         }
     }
+}
+
+// The same with a limit on the SM's own clock: reading the global timer takes about a microsecond, which a wait that is
+// not ready at once would pay every time.  2^32 cycles are two seconds; drains give a shorter limit.
+constexpr long long kWaitCycles = 1ll << 32;
+
+// (Out of line: a wait that is not ready at once has time, and the code beside the ready ones stays small.)
+static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, int *abort_flag, int *err, long long limit) {
+    const long long t0 = clock64();
+    for (uint32_t i = 1;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 31u) == 0) {
+            if (abort_flag && *(volatile int *)abort_flag) return false;
+            if (clock64() - t0 > limit) {
+                if (abort_flag) *(volatile int *)abort_flag = 1;
+                if (err) atomicOr(err, (int)KV8_ERR_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, int *abort_flag, int *err, long long limit = kWaitCycles) {
+    return mbar_try_wait(bar, parity) || bar_wait_slow(smem_u32(bar), parity, abort_flag, err, limit);
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -433,9 +433,10 @@ KV8_API int kv8_copy(void *dst, const void *src, size_t bytes, void *stream);
 
 /* -----------------------------------------------------------------------------------------------
  * kv8_wait_selftest -- diagnostic of the timeout path.  One CTA waits on an mbarrier that nothing
- * completes, through the same bounded wait the library's tensor-core kernels use for their TMA, MMA and
- * softmax hand-offs.  After limit_ns (in [1000, 1e9] ns) the wait gives up: KV8_ERR_TIMEOUT is OR-ed into
- * *err_word, *wait_status is set to 2 (1 would mean the wait completed) and the kernel returns normally,
+ * completes, through the bounded waits the library's tensor-core kernels use for their TMA, MMA and
+ * softmax hand-offs, one after the other: one with its limit in nanoseconds, one in cycles of the SM's clock
+ * (2 a nanosecond).  After limit_ns (in [1000, 1e9] ns) each gives up: KV8_ERR_TIMEOUT is OR-ed into
+ * *err_word, *wait_status is set to 2 (1 would mean a wait completed) and the kernel returns normally,
  * leaving the context usable.  err_word and wait_status: device ints (required).
  * --------------------------------------------------------------------------------------------- */
 KV8_API int kv8_wait_selftest(uint64_t limit_ns, int *err_word, int *wait_status, void *stream);

@@ -54,3 +54,18 @@ def test_context_usable_after_a_timeout(lib, oracle):
     torch.cuda.synchronize()
     assert int(err.item()) == 0
     parity(out.cpu().numpy(), oracle.attn_decode(ql, qr, q_o, s_o, synth.SM_SCALE), "decode after a timeout")
+
+
+def test_both_bounded_waits_run_to_their_limits(lib):
+    """50 ms by the global timer, then 10^8 cycles of the SM's clock (48 ms at its highest, 2.07 GHz); the wait that finds the
+    abort flag set adds nothing like its own 4 x 10^8."""
+    err, st = (torch.zeros(1, dtype=torch.int32, device=DEV) for _ in range(2))
+    lib.kv8_wait_selftest(1000, err, st)  # (the first launch loads the kernel)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    err.zero_(), st.zero_()
+    begin.record()
+    lib.kv8_wait_selftest(50_000_000, err, st)
+    end.record()
+    torch.cuda.synchronize()
+    assert err.item() == lib.KV8_ERR_TIMEOUT and st.item() == 2
+    assert 95 < begin.elapsed_time(end) < 240
