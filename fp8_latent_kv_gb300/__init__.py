@@ -93,8 +93,9 @@ def _ptr(t) -> int | None:
 def _stream(stream, dev=None) -> int:
     if stream is None:
         import torch
-        # (3 us less than by a Stream object)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
+        dev = torch.cuda.current_device() if dev is None else dev
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (3 us less than by a Stream object, but no public name)
+        return torch.cuda.current_stream(dev).cuda_stream if raw is None else raw(dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

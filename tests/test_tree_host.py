@@ -99,3 +99,18 @@ def test_commit_refuses_lengths_that_overlap(so):
                 table=FAKE, pages=5, page=64, new=FAKE, err=None, st=None)
     for new in (FAKE, FAKE + 4, FAKE + 12, FAKE - 12):
         assert call(so.kv8_tree_commit, good, order, new=new) == kv.KV8_EINVAL, new
+
+
+def test_the_current_stream_is_found_by_its_public_name_too(monkeypatch):
+    """torch's raw lookup is no public name: without it the same stream comes from torch.cuda.current_stream."""
+    class Fake:
+        cuda_stream = 77
+
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: asked.append(dev) or Fake)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 100 + dev, raising=False)
+    assert kv._stream(None) == 103 and kv._stream(None, 1) == 101 and asked == []
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert kv._stream(None) == 77 and kv._stream(None, 1) == 77 and asked == [3, 1]
+    assert kv._stream(5) == 5 and kv._stream(Fake) == 77
