@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
 }
 
 // Joins the parts of the cut groups: out = sum_p 2^(m_p - M) cl_p / (sum_p 2^(m_p - M) z_p + 2^-M sum_p n0_p) with
-// M = max_p m_p.
+// M = max_p m_p.  (A set of NaN sums has m_p = +inf: its factor is NaN, the others' are 0.)
 // A warp takes one column of one cut group and reads its parts in order: four dims a lane, of 128 or (kQuarters 4) all of
 // them.  With a quarter each, and where the warps outnumber these (few columns, so many parts each), up to eight warps of a
 // block share the parts.

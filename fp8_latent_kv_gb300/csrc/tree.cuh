@@ -112,8 +112,8 @@ struct TreeArgs {
 // A partial set: cl and z relative to 2^m, and n0, the weight (relative to 2^0) of rows that only count in the sum.
 __host__ __device__ constexpr size_t tree_part_floats(int cols) { return (size_t)cols * (kKL + 3); }
 
-// The exponent that a partial set is stored with: a set of NaN sums may have none (-inf), which would count as nothing.
-__device__ __forceinline__ float tree_part_exponent(float m, float z) { return z == z ? m : fmaxf(m, 0.f); }
+// The exponent that a partial set is stored with: a set of NaN sums has the largest, so that no other's makes it count as nothing.
+__device__ __forceinline__ float tree_part_exponent(float m, float z) { return z == z ? m : INFINITY; }
 
 // Cache row of position t of sequence b, or -1 where its page is outside the cache.
 __device__ __forceinline__ int64_t tree_row(const TreeArgs &a, int b, int64_t t) {

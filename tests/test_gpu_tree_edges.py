@@ -204,3 +204,29 @@ def test_a_step_without_drafted_tokens(lib, oracle, q_dtype):
     q = queries(rng, 3, 16, q_dtype == F32)
     got, err = run_tree(lib, q, q_dtype, F32, [0, 0], [30, 0], None, kv8, scale, table, 16)
     assert err == 0 and (got == 7.0).all()
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+@pytest.mark.parametrize("bad", ["scale", "codes"])
+@pytest.mark.parametrize("at", [3, 9000, 20001])
+def test_a_row_that_is_not_a_number_shows_whatever_the_others_weigh(lib, q_dtype, bad, at):
+    """One attended row of NaN among shares whose largest scores lie hundreds of binary orders above and below its share's."""
+    page, T, H = 128, 20002, 16
+    kv8 = np.full((T + page, 576), 0x38, np.uint8)       # 1.0
+    kv8[:, 512:] = 0
+    kv8[:, 512] = torch.tensor(np.arange(T + page) // 2000 % 8 * 2.0, dtype=F32).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    scale = np.ones(T + page, np.float32)
+    q = np.zeros((2, H, 576), np.float32)
+    q[:, :, 512] = 2000 * np.where(np.arange(H) % 2, 1, -1)   # about 200 binary orders a level
+    table = np.arange(T // page + 1)[None]
+    ref, _ = run_tree(lib, q, q_dtype, F32, [2], [T - 2], None, kv8, scale, table, page)
+    assert np.isfinite(ref).all()
+    if bad == "scale":
+        scale[at] = np.nan
+    else:
+        kv8[at, :512:3] = 0x7F
+    got, err = run_tree(lib, q, q_dtype, F32, [2], [T - 2], None, kv8, scale, table, page)
+    sees = [at < T - 1, True]
+    assert err == 0
+    for i in range(2):
+        assert np.isnan(got[i, :, 0]).all() if sees[i] else np.array_equal(got[i], ref[i])
