@@ -72,6 +72,9 @@ constexpr uint32_t kImg = kQLat + kQTail;
 constexpr uint32_t kW = 8192;              // hi [64 columns][64 rows] (SW64), then lo
 constexpr uint32_t OFF_ST = 0, OFF_W = kStages * kStage, OFF_Q = OFF_W + kTeams * kW, OFF_MISC = OFF_Q + kQTail;
 constexpr float kRoom = 100.0f;            // the reference moves when a block's exponent exceeds it by more
+// A reference is the sum of a score, a scale's logarithm and small whole numbers: from 2^24 on it would round those away, and the
+// weights would no longer fit their pieces.  A column whose reference goes beyond 2^23 is NaN.
+constexpr float kFar = 8388608.f;
 constexpr int kBase = 60;                  // O and z are relative to 2^(reference + kBase)
 constexpr float kTiny = 8.6736174e-19f;    // 2^-60
 constexpr uint32_t TM_Q = 0, TM_SFA = 112, TM_SFB = 116, TM_S = 128, TM_O = 256;
@@ -786,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool slow = bar_red_or(team_bar, kTeam, max_a > na + kRoom || max_b > nb + kRoom);
                 auto moved = [&](int n, float r) -> float {  // a column's reference r from this tile on
                     const float x = fmaxf(tops[0][n], tops[1][n]);
-                    return slow && x > r + kRoom ? x : r;
+                    return slow && x > r + kRoom ? (fabsf(x) <= kFar ? x : NAN) : r;
                 };
                 float move = 1.f;          // the factor of the accumulator column 32 set + lane
                 float rl = ms.ref[lane], rh = ms.ref[32 + lane];  // of the columns whose factors this lane may write

@@ -382,11 +382,13 @@ KV8_API int kv8_tree_mask(int B, const int32_t *q_start, const int32_t *lens, in
  *   mask [R][mask_words] uint32 as kv8_tree_mask writes it (any bits: it need not be a tree); bits past
  *   32*mask_words count as 0.
  *   A page outside the cache: its rows are left out and KV8_ERR_INDEX is set.  Rows that nobody attends
- *   may hold anything, NaN codes and scales included.  Scales are not negative.  bf16 queries take scales
- *   from 2^-60 to 2^60, and 0: an attended row with a larger one makes the output NaN, and one with a
- *   smaller one (its values are below 3.9e-16) counts as a row of zeros: score 0, nothing added to the
- *   output.  A NaN or an infinity in a query makes that (row, head)'s output NaN where it attends anything
- *   (bf16 queries: anything but rows that count as zeros), and no other.
+ *   may hold anything, NaN codes and scales included.  Scales are not negative.
+ *   A NaN or an infinity in a query makes that (row, head)'s output NaN where it attends anything, and no
+ *   other.
+ *   bf16 queries: scales are 0 or from 2^-60 to 2^60.  An attended row with a larger one makes the output
+ *   NaN; one with a smaller one (its values are below 3.9e-16) counts as a row of zeros: score 0, nothing
+ *   added to the output, not even a query's NaN.  Scores lie within 5.8e6 (2^23 log 2) of 0: a (row, head)
+ *   whose largest ones do not is NaN.
  *   workspace: >= mla_tree8_workspace_bytes(R, H, B, q_dtype) bytes; calls that may overlap on the GPU
  *   (graph replays included) need their own.  err_word: optional.
  * bf16 queries run on the tensor cores: a query element to 2^-17 of its head's largest, the weights

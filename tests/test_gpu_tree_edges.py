@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from test_gpu_tree import BF, DEV, F32, build, check, i32, queries, run_tree
-from tree_ref import BAD_INDEX, SM, pack
+from tree_ref import BAD_INDEX, SM, TABLE, pack
 
 pytestmark = pytest.mark.gpu
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -230,3 +230,47 @@ def test_a_row_that_is_not_a_number_shows_whatever_the_others_weigh(lib, q_dtype
     assert err == 0
     for i in range(2):
         assert np.isnan(got[i, :, 0]).all() if sees[i] else np.array_equal(got[i], ref[i])
+
+
+@pytest.mark.parametrize("q_dtype", [BF])
+@pytest.mark.parametrize("base", [0.0156, 0.058, 9.8])
+@pytest.mark.parametrize("uneven", [False, True])
+@pytest.mark.parametrize("side", [1, -1])
+def test_scores_far_from_zero(lib, q_dtype, side, uneven, base):
+    """Scores of all sizes, every column's of one sign.  From about 2^12 on the largest row is all that is left, and the output is its
+    values, to the weights' rounding (bf16: 2^-8 and 2^-12; f32: 2^-22) and a few steps of 2^-24.  For bf16 queries scores of
+    2^23 log 2 and more are beyond what the reference exponents hold, and the output is NaN, nothing else."""
+    rng = np.random.default_rng(97)
+    page, T, powers = 64, 300, np.arange(4, 112)
+    H = len(powers)
+    kv8 = rng.integers(0x30, 0x40, (512, 576)).astype(np.uint8)
+    kv8[:, 512:] = 0
+    level = rng.permutation(np.arange(T) % 11)           # whole numbers that e4m3 has
+    level = level if side > 0 else -2 - level
+    top = 108
+    level[top] = 13 if side > 0 else -1
+    table = rng.permutation(8)[None]
+    row = table[0, np.arange(T) // page] * page + np.arange(T) % page
+    kv8[row, 520] = torch.tensor(level, dtype=F32).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    scale = np.ones(512, np.float32)
+    scale[row] = base * rng.uniform(0.9, 1, T)
+    if uneven:  # (rows of score 0, or far below all others)
+        some = np.nonzero(level == 0 if side > 0 else level < -10)[0]
+        scale[row[some]] = base * rng.choice(np.float32([2.0 ** (-7 * side), 2.0 ** 6, 1.5]), len(some))
+    q = np.zeros((2, H, 576), np.float32)
+    q[:, :, 520] = np.ldexp(1.0 + rng.integers(0, 128, H) / 128, powers)  # exact in bf16
+    got, err = run_tree(lib, q, q_dtype, F32, [2], [T - 2], None, kv8, scale, table, page)
+    assert err == 0
+    score = SM / np.log(2) * q[0, :, 520:521].astype(np.float64) * (level * scale[row].astype(np.float64))  # [H][T]
+    want = TABLE[kv8[row[top], :512]] * float(scale[row[top]])
+    gap = score[:, top] - np.delete(score, top, 1).max(1)
+    fine, beyond = gap > 40, np.zeros(H, bool)
+    if q_dtype == BF:
+        fine &= np.abs(score).max(1) < 2.0 ** 23
+        beyond = np.abs(score[:, top]) > 1.01 * 2.0 ** 23
+        assert beyond.sum() >= 60
+    assert fine.sum() >= 5
+    eps = 2.0 ** -8 + 2.0 ** -11 if q_dtype == BF else 2.0 ** -21
+    off = np.abs(got / want - 1).max((0, 2))
+    assert (off[fine] <= eps).all(), off
+    assert np.isnan(got[:, beyond]).all(), off
