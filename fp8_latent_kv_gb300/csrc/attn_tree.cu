@@ -189,6 +189,16 @@ __device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kT
     }
 }
 
+// ceil(log2) of the largest scale among the step's rows that a token attends: where its scores are so far from 0 that the logarithm
+// of a scale is lost beside them, what its weights are measured by.
+constexpr float kFar = 4194304.f;
+__device__ __noinline__ float largest_scale(const TreeArgs &a, const Smem &sm, int buf, int nr, int64_t draft, int q0, int node, bool column) {
+    float most = -INFINITY;
+    for (int r = 0; column && r < nr; ++r)
+        if (sm.there[buf][r] && (draft + r < 0 || tree_sees(a, q0, node, (int)(draft + r)))) most = fmaxf(most, sm.log_scale[buf][r]);
+    return ceilf(most);
+}
+
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
@@ -343,7 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
             const float corr = exp2f(m_run - ref);  // 0 before any row
             m_run = m_new;
             // the step's largest weight, of a column, times 2^(14 - top) in (2^13, 2^14]
-            const float top = fminf(fmaxf(ceilf(e_max - ref), -110.f), 127.f), up = exp2f(14.f - top);
+            float top = ceilf(e_max - ref);
+            if (fabsf(ref) >= kFar) top = largest_scale(a, sm, buf, nr, p0 - seg.q.len, seg.q.q0, node, lane < nc);
+            top = fminf(fmaxf(top, -110.f), 127.f);
+            const float up = exp2f(14.f - top);
             if (warp == 0) {
                 sm.corr[lane] = corr;
                 sm.unit[lane] = exp2f(top - 14.f);

@@ -232,7 +232,7 @@ def test_a_row_that_is_not_a_number_shows_whatever_the_others_weigh(lib, q_dtype
         assert np.isnan(got[i, :, 0]).all() if sees[i] else np.array_equal(got[i], ref[i])
 
 
-@pytest.mark.parametrize("q_dtype", [BF])
+@pytest.mark.parametrize("q_dtype", [BF, F32])
 @pytest.mark.parametrize("base", [0.0156, 0.058, 9.8])
 @pytest.mark.parametrize("uneven", [False, True])
 @pytest.mark.parametrize("side", [1, -1])
