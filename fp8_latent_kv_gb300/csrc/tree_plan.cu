@@ -17,8 +17,8 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanCtas = 8;  // (one CTA: 4.0 us as well for 4 sequences, 6.2 against 4.8 for 256, 40 against 10 for 4096)
 constexpr int kPlanPer = KV8_MAX_SEQS / kPlanThreads;  // sequences per thread in the scans
 // All of the kernel's shared memory is the launch's, so that its size alone says which launches need the larger limit: the
-// warps' sums and ends, then four words a sequence.
-constexpr size_t kPlanSums = 32 * (2 * sizeof(int64_t) + sizeof(int));
+// warps' sums, then four words a sequence.
+constexpr size_t kPlanSums = 32 * 2 * sizeof(int64_t);
 constexpr size_t plan_smem_bytes(int B) { return kPlanSums + (size_t)B * 4 * sizeof(int32_t); }
 constexpr size_t kDefaultSmem = 48 * 1024;  // what a launch may have without asking
 
@@ -37,7 +37,6 @@ __device__ __forceinline__ void cluster_sync_all() {
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
     extern __shared__ __align__(16) unsigned char plan_smem[];
     int64_t(*const wsum)[2] = reinterpret_cast<int64_t(*)[2]>(plan_smem);
-    int *const ends = reinterpret_cast<int *>(plan_smem + 32 * sizeof(*wsum));
     int32_t *have = reinterpret_cast<int32_t *>(plan_smem + kPlanSums), *want = have + a.B, *spre = want + a.B, *npre = spre + a.B;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t positions = 0x7fffffff;  // a table that is too narrow is a page error, not a bad number
@@ -100,7 +99,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
         wsum[lane][1] = y;
     }
     const bool back = __syncthreads_or(err & KV8_ERR_INDEX) &&
-                      tree_goes_back(a.q_start, a.lens, min(b0, a.B), min(b0 + per, a.B), a.R, positions, ends);
+                      tree_goes_back(a.q_start, a.lens, min(b0, a.B), min(b0 + per, a.B), a.R, positions);
     const int64_t S = wsum[31][0];
     const int F0 = *a.n_free;
     // the list itself is not possible, or rows would have two slots
