@@ -39,6 +39,10 @@ constexpr int kThreads = 32 * kWarps;
 // columns' four 8-byte pieces in 32 banks.
 constexpr int kTileStride = 592, kQStride = 2 * kRow + 32;
 constexpr int kSStride = kCols + 8;        // words
+// A step's weights are measured by its largest score plus a scale's logarithm, a sum that from here on may be binary orders off: weights
+// would leave their f16 pieces.  Such a column is NaN.  (Measuring them again, with the maximum taken off first: 555 us against 550
+// for the largest case, which does not do it.)
+constexpr float kFar = 33554432.f;
 constexpr int kSteps = kRow / 16 / 4;      // 16-byte steps of a row that a warp's part of the scores covers
 static_assert(kSteps * 64 == kRow, "a row's quarters");
 
@@ -187,16 +191,6 @@ __device__ __forceinline__ void context(const Smem &sm, const uint8_t (*tile)[kT
                 }
             }
     }
-}
-
-// ceil(log2) of the largest scale among the step's rows that a token attends: where its scores are so far from 0 that the logarithm
-// of a scale is lost beside them, what its weights are measured by.
-constexpr float kFar = 4194304.f;
-__device__ __noinline__ float largest_scale(const TreeArgs &a, const Smem &sm, int buf, int nr, int64_t draft, int q0, int node, bool column) {
-    float most = -INFINITY;
-    for (int r = 0; column && r < nr; ++r)
-        if (sm.there[buf][r] && (draft + r < 0 || tree_sees(a, q0, node, (int)(draft + r)))) most = fmaxf(most, sm.log_scale[buf][r]);
-    return ceilf(most);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) {
@@ -349,14 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
             m_new = fmaxf(m_run, order_float(sm.m_max[buf][lane]));
             e_max = order_float(sm.e_max[buf][lane]);
             if (warp == 1) sm.m_max[buf ^ 1][lane] = sm.e_max[buf ^ 1][lane] = float_order(-INFINITY);  // (read in the step before)
-            const float ref = m_new == -INFINITY ? 0.f : m_new;
+            const float ref = fabsf(m_new) <= kFar ? m_new : m_new == -INFINITY ? 0.f : NAN;
             const float corr = exp2f(m_run - ref);  // 0 before any row
             m_run = m_new;
             // the step's largest weight, of a column, times 2^(14 - top) in (2^13, 2^14]
-            float top = ceilf(e_max - ref);
-            if (fabsf(ref) >= kFar) top = largest_scale(a, sm, buf, nr, p0 - seg.q.len, seg.q.q0, node, lane < nc);
-            top = fminf(fmaxf(top, -110.f), 127.f);
-            const float up = exp2f(14.f - top);
+            const float top = fminf(fmaxf(ceilf(e_max - ref), -110.f), 127.f), up = exp2f(14.f - top);
             if (warp == 0) {
                 sm.corr[lane] = corr;
                 sm.unit[lane] = exp2f(top - 14.f);

@@ -387,8 +387,9 @@ KV8_API int kv8_tree_mask(int B, const int32_t *q_start, const int32_t *lens, in
  *   other.
  *   bf16 queries: scales are 0 or from 2^-60 to 2^60.  An attended row with a larger one makes the output
  *   NaN; one with a smaller one (its values are below 3.9e-16) counts as a row of zeros: score 0, nothing
- *   added to the output, not even a query's NaN.  Scores lie within 5.8e6 (2^23 log 2) of 0: a (row, head)
- *   whose largest ones do not is NaN.
+ *   added to the output, not even a query's NaN.
+ *   Scores lie within 5.8e6 (2^23 log 2) of 0 for bf16 queries, 2.3e7 (2^25 log 2) for f32 queries: a
+ *   (row, head) whose largest ones do not is NaN.
  *   workspace: >= mla_tree8_workspace_bytes(R, H, B, q_dtype) bytes; calls that may overlap on the GPU
  *   (graph replays included) need their own.  err_word: optional.
  * bf16 queries run on the tensor cores: a query element to 2^-17 of its head's largest, the weights

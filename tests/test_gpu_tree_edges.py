@@ -238,8 +238,8 @@ def test_a_row_that_is_not_a_number_shows_whatever_the_others_weigh(lib, q_dtype
 @pytest.mark.parametrize("side", [1, -1])
 def test_scores_far_from_zero(lib, q_dtype, side, uneven, base):
     """Scores of all sizes, every column's of one sign.  From about 2^12 on the largest row is all that is left, and the output is its
-    values, to the weights' rounding (bf16: 2^-8 and 2^-12; f32: 2^-22) and a few steps of 2^-24.  For bf16 queries scores of
-    2^23 log 2 and more are beyond what the reference exponents hold, and the output is NaN, nothing else."""
+    values, to the weights' rounding (bf16: 2^-8 and 2^-12; f32: 2^-22) and a few steps of 2^-24.  Scores
+    from 2^23 log 2 (bf16 queries) or 2^25 log 2 on are beyond what the exponents hold, and the output is NaN, nothing else."""
     rng = np.random.default_rng(97)
     page, T, powers = 64, 300, np.arange(4, 112)
     H = len(powers)
@@ -264,12 +264,9 @@ def test_scores_far_from_zero(lib, q_dtype, side, uneven, base):
     score = SM / np.log(2) * q[0, :, 520:521].astype(np.float64) * (level * scale[row].astype(np.float64))  # [H][T]
     want = TABLE[kv8[row[top], :512]] * float(scale[row[top]])
     gap = score[:, top] - np.delete(score, top, 1).max(1)
-    fine, beyond = gap > 40, np.zeros(H, bool)
-    if q_dtype == BF:
-        fine &= np.abs(score).max(1) < 2.0 ** 23
-        beyond = np.abs(score[:, top]) > 1.01 * 2.0 ** 23
-        assert beyond.sum() >= 60
-    assert fine.sum() >= 5
+    far = 2.0 ** (23 if q_dtype == BF else 25)
+    fine, beyond = (gap > 40) & (np.abs(score).max(1) < far), np.abs(score[:, top]) > 1.01 * far
+    assert fine.sum() >= 5 and beyond.sum() >= 60
     eps = 2.0 ** -8 + 2.0 ** -11 if q_dtype == BF else 2.0 ** -21
     off = np.abs(got / want - 1).max((0, 2))
     assert (off[fine] <= eps).all(), off
