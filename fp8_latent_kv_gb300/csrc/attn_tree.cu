@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tree_f32_kernel(TreeArgs a) 
         auto copy_row = [&](int buf) {
             if (lane >= 4) return;
             const bool there = row >= 0;
+            if (scale > 3.402823466e38f) scale = NAN;  // (a score of -inf would say that nobody attends the row)
             sm.scale[buf][r_own] = scale;
             sm.log_scale[buf][r_own] = log2f(scale);
             sm.there[buf][r_own] = there;

@@ -271,3 +271,20 @@ def test_scores_far_from_zero(lib, q_dtype, side, uneven, base):
     off = np.abs(got / want - 1).max((0, 2))
     assert (off[fine] <= eps).all(), off
     assert np.isnan(got[:, beyond]).all(), off
+
+
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+@pytest.mark.parametrize("at", [5, 400, 701])
+def test_an_infinite_scale_shows_whatever_its_scores_sign(lib, oracle, q_dtype, at):
+    """An attended row of infinite scale: NaN, where its score would be minus infinity too."""
+    rng = np.random.default_rng(101)
+    H, page, lens, n = 16, 64, [700], [4]
+    kv8, scale, table, rows = build(oracle, rng, lens, n, page)
+    q = queries(rng, 4, H, q_dtype == F32)
+    sign = TABLE[kv8[rows[0][at]]] @ q.reshape(-1, 576).T.astype(np.float64) > 0
+    assert 8 < sign.sum() < 56
+    ref, _ = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8, scale, table, page)
+    scale[rows[0][at]] = np.inf
+    got, err = run_tree(lib, q, q_dtype, F32, n, lens, None, kv8, scale, table, page)
+    first = max(0, at - 700)
+    assert err == 0 and np.isnan(got[first:]).all() and np.array_equal(got[:first], ref[:first])
