@@ -11,7 +11,7 @@
 // at most in the tensor core, whose additions are not rounded to nearest, then by f32 additions.
 // These are register-operand MMAs (3 cycles of an SM for 16 x 8 x 16, measured here), which take the rows' e4m3 pairs
 // converted in registers; tcgen05 would want the rows as f16 in shared memory, 74 KB of 64 rows written by the threads beside 76 KB of
-// queries.  8 x 8 tokens of 128 heads over 4096 rows: 546 us, 134 TFLOP/s (38.6 on the CUDA cores); a step of 64 rows
+// queries.  8 x 8 tokens of 128 heads over 4096 rows: 550 us, 133 TFLOP/s (38.6 on the CUDA cores); a step of 64 rows
 // takes 9.3 thousand cycles, 3.4 in the scores and 3.5 in the context, which the MMAs' rate bounds, the rest between the
 // barriers of the softmax.
 #include "sm100.cuh"

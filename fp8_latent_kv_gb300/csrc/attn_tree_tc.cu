@@ -25,11 +25,12 @@
 // weight is NaN instead.
 //
 // Work: equal shares of (group, tile) units (tree.cuh), one CTA per SM.
-// What bounds it: a tile's products take 1408 cycles of the tensor pipe (18 score MMAs of 32 to 48 cycles, 16 context MMAs of
-// 48), a tile 1570 in all where a share has hundreds of them, the pipe busy 69 %: two teams' 3.9 thousand warp instructions
-// a tile, more than half of them conversions, maxima and exchanges of the softmax, take most of the issue slots.  64 tokens of
-// 128 heads over 32768 rows: 396 us, 1476 TFLOP/s.  Three teams did not pay: of eight warps each they spilled (658 us against 522
-// then), of four they missed the instruction cache (557 against 497).
+// What bounds it: a tile's products take 1408 cycles (14 score MMAs with A in TMEM at 32, 4 from shared memory and 16 context MMAs at
+// 48) of the 1570 that a tile takes where a share has hundreds of them.  An MMA with both operands in shared memory has 6 KB to read,
+// 128 + 64 rows of 32 bytes, at 128 bytes a cycle; its 32 cycles of arithmetic are what the pipe's counter shows (69 %).
+// The two teams' 3.9 thousand warp instructions a tile run beside that.  64 tokens of 128 heads over 32768 rows: 396 us, 1476
+// TFLOP/s.  Three teams did not pay: of eight warps each they spilled (658 us against 522 then), of four they missed the
+// instruction cache (557 against 497).
 // Warps: 0 = row loads, 1 = scores and TMEM, 2 = the rows' scales, 3 = context products, 4..19 = softmax and output in
 // two teams that take alternate tiles.  warp % 4 is a warp's TMEM lane quadrant, its set (0, 1) the block of 32 rows,
 // and a thread holds 8 rows of two columns.
@@ -234,8 +235,8 @@ __device__ __forceinline__ uint32_t chunk_max(const uint4 (&u)[2]) {
     return max(m >> 16, m & 0xFFFFu);
 }
 
-// (Six blocks an SM: 48 warps' loads in flight.  Four, as many as the shares' block would leave: 546 us against 537 for 16 x 64
-// tokens over 2048 rows.)
+// (Six blocks an SM: 48 warps' loads in flight, for which the compiler has 40 registers and spills 28 bytes of the shares' code.
+// Four, as many as the shares' block would leave: 546 us against 537 for 16 x 64 tokens over 2048 rows.)
 __global__ void __launch_bounds__(kPrepThreads, 6) tree_prep_kernel(TreeArgs a, uint8_t *img, float *c_head) {
     grid_dependency_wait();
     grid_launch_dependents();

@@ -340,7 +340,7 @@ int mla_absorb_tree8(const void *q_lat, const void *q_rope, int q_dtype, int R, 
     const TreeWorkspace w = tree_workspace(R, H, B, a.q_bf16);
     a.sched = static_cast<TreeSched *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.part);
-    // bf16 queries: tensor cores; f32 queries keep full f32 precision on the CUDA cores
+    // bf16 queries: tcgen05 on e4m3 pieces; f32 queries: f16 MMAs, two pieces of each query element and weight (2^-22), f32 sums
     return status(a.q_bf16 ? launch_tree_tc(a, static_cast<uint8_t *>(workspace) + w.images, (cudaStream_t)stream)
                            : launch_tree_f32(a, (cudaStream_t)stream));
 }
@@ -436,7 +436,7 @@ int mla_decode8_partial(const void *q_lat, const void *q_rope, int q_dtype, int 
     a.out = nullptr;
     a.err_word = err_word;
     a.tc_scratch = static_cast<uint8_t *>(workspace) + decode_partial_bytes(a.P, H);
-    // bf16 queries: tensor cores; f32 queries keep full f32 precision on the CUDA cores
+    // bf16 queries: tcgen05 on e4m3 pieces; f32 queries: f16 MMAs, two pieces of each query element and weight (2^-22), f32 sums
     return status(a.q_bf16 ? launch_attn_tc(a, (cudaStream_t)stream) : launch_attn_simt(a, (cudaStream_t)stream));
 }
 

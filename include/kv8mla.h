@@ -346,11 +346,15 @@ KV8_API int dsa_index_topk8(const void *q_idx, int q_dtype, const float *w, int 
  * First every sequence returns the pages it holds beyond its rows; then missing pages are taken from the
  * top, sequence by sequence in order.  Pages return in the order that makes the same growth take the same
  * pages again.  A sequence that wants more pages than are left after the ones before it (their wants
- * counted whether met or not), or more than max_pages, keeps the pages it has, gets -1 in its slots and
- * sets KV8_ERR_PAGES.  The result depends on the arguments alone.  n_pages[b] outside [0, max_pages],
- * n_free outside [0, free_cap], or more returned pages than free_cap holds: KV8_ERR_INDEX, as above (for
- * n_free: every sequence).
- * Lengths of 0 return all of a sequence's pages.
+ * counted whether met or not), or more than max_pages (which counts as no want), keeps the pages it has,
+ * gets -1 in its slots and sets KV8_ERR_PAGES.  The result depends on the arguments alone.  n_pages[b]
+ * outside [0, max_pages], n_free outside [0, free_cap], or more returned pages than free_cap holds:
+ * KV8_ERR_INDEX, as above (for n_free: every sequence).
+ * Lengths of 0 return all of a sequence's pages.  A prompt of more than KV8_MAX_TREE rows is planned in
+ * several calls of up to that many.
+ * A page has one holder: it stands in one sequence's row of the table or on the free list.  Nothing here
+ * counts the holders of a page that sequences share (a common prefix): each of them would return it, and
+ * two would be given it.  Sequences may share pages as long as none shrinks below them.
  * --------------------------------------------------------------------------------------------- */
 KV8_API int kv8_page_plan(int B, const int32_t *lens, const int32_t *q_start, int R, int page_size, int max_pages,
                           int32_t *n_pages, int32_t *block_table, int32_t *free_list, int free_cap, int32_t *n_free,
