@@ -13,15 +13,18 @@ import os
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libkv8mla.so")
 
-KV8_ROW_BYTES, KV8_KL, KV8_KR = 576, 512, 64
+KV8_ROW_BYTES, KV8_KL, KV8_KR, KV8_KVB_BLOCK = 576, 512, 64, 128
 KV8_MAX_HEADS, KV8_MAX_ROWS, KV8_MAX_SELECT = 128, 1 << 20, 4096
 KV8_OK, KV8_EINVAL, KV8_EWORKSPACE, KV8_ECUDA, KV8_EUNSUPPORTED = 0, -1, -2, -3, -4
 KV8_MAX_SEQS, KV8_MAX_TREE, KV8_MIN_PAGE, KV8_MAX_PAGE = 4096, 256, 16, 65536
 KV8_ERR_INDEX, KV8_ERR_TIMEOUT, KV8_ERR_PAGES = 1, 2, 4
 KV8_F32, KV8_BF16 = 0, 1
+KV8_ROPE_INTERLEAVED, KV8_ROPE_HALF = 0, 1
+KV8_MAX_WIDTH, KV8_MAX_NORM_WIDTH, KV8_MAX_ROPE = 65536, 16384, 256
 
 # (restype, argtypes) for every exported symbol of include/kv8mla.h
 _P, _I, _I64, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_D = ctypes.c_double
 SIGNATURES = {
     "kv8_encode_e4m3": (_I, [_P, _I64, _P, _P]),
     "kv8_quant_rows": (_I, [_P, _I64, _P, _P, _P]),
@@ -50,6 +53,11 @@ SIGNATURES = {
     "mla_absorb_tree8": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P, _I64, _P, _I, _I, _F, _P, _SZ, _P, _P, _I,
                               _P]),
     "kv8_tree_commit": (_I, [_I, _P, _P, _P, _P, _I, _I, _P, _P, _I64, _P, _I, _I, _P, _P, _P]),
+    "kv8_rope_freqs": (_I, [_I, _D, _D, _D, _D, _D, _P, _P]),
+    "kv8_rope": (_I, [_P, _I, _I64, _I, _I, _I, _I, _I64, _I64, _P, _P, _F, _I, _P, _I64, _I64, _P, _I64, _I64, _I, _P]),
+    "kv8_norm_rope_rows": (_I, [_P, _I, _I64, _I64, _P, _F, _P, _P, _F, _I, _P, _P, _P, _I64, _P, _P]),
+    "kv8_quant_blocks": (_I, [_P, _I, _I64, _I, _I64, _P, _F, _P, _P, _I64, _P]),
+    "kv8_matmul8": (_I, [_P, _I64, _P, _I64, _I, _I, _I, _P, _P, _P, _I, _I64, _P, _P]),
     "kv8_copy": (_I, [_P, _P, _SZ, _P]),
     "kv8_wait_selftest": (_I, [ctypes.c_uint64, _P, _P, _P]),
     "kv8_strerror": (ctypes.c_char_p, [_I]),
@@ -329,6 +337,97 @@ def kv8_tree_commit(q_start, lens, accept, n_accept, kv8, kv_scale, block_table,
     _check("kv8_tree_commit", load().kv8_tree_commit(
         B, q_start.data_ptr(), lens.data_ptr(), accept.data_ptr(), n_accept.data_ptr(), accept.shape[1], layers, kv8.data_ptr(),
         kv_scale.data_ptr(), rows, block_table.data_ptr(), block_table.shape[1], page_size, new_lens.data_ptr(), _ptr(err_word),
+        _stream(stream, dev)))
+
+
+def _rows(fn: str, name: str, t, dtypes, shape, dev: int) -> None:
+    """As _args, for a tensor whose last dimension is contiguous and whose other strides are the call's to take."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{fn}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{dev}")
+    if t.shape != shape or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)} and a contiguous last dimension, got {tuple(t.shape)} with "
+                         f"strides {t.stride()}")
+
+
+def kv8_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0, context: float = 4096, beta_fast: float = 32.0,
+                   beta_slow: float = 1.0):
+    """(inv_freq [rope_dim / 2] f32 CPU tensor, rope_scale): plain frequencies, or interpolated by parts for a context `factor`
+    times as long."""
+    import torch
+    table, scale = (ctypes.c_float * max(1, rope_dim // 2))(), ctypes.c_float()
+    _check("kv8_rope_freqs", load().kv8_rope_freqs(rope_dim, theta, factor, context, beta_fast, beta_slow, ctypes.addressof(table),
+                                                   ctypes.addressof(scale)))
+    return torch.tensor(list(table), dtype=torch.float32), scale.value
+
+
+def kv8_rope(x, position, inv_freq, rope_at: int, rot, rest=None, rope_scale: float = 1.0, layout: int = KV8_ROPE_INTERLEAVED,
+             stream=None) -> None:
+    """x [n][heads][width] (f32 / bf16, strided) -> rot [n][heads][rope_dim], its elements rope_at.. rotated, and (optional) rest
+    [n][heads][width - rope_dim] (both f32 / bf16, strided).  position [n] int32, inv_freq [rope_dim / 2] f32.  In place:
+    rot = x[..., rope_at:rope_at + rope_dim]."""
+    import torch
+    fn, f = "kv8_rope", (torch.float32, torch.bfloat16)
+    (n, heads, width), dim = x.shape, rot.shape[-1]
+    dev = _args(fn, ("position", position, torch.int32, (n,)), ("inv_freq", inv_freq, torch.float32, (dim // 2,)))
+    _rows(fn, "x", x, f, (n, heads, width), dev)
+    _rows(fn, "rot", rot, f, (n, heads, dim), dev)
+    if rest is not None:
+        _rows(fn, "rest", rest, (rot.dtype,), (n, heads, width - dim), dev)
+    _check(fn, load().kv8_rope(
+        x.data_ptr(), _dtype_code(x.dtype), n, heads, width, rope_at, dim, x.stride(0), x.stride(1), position.data_ptr(),
+        inv_freq.data_ptr(), rope_scale, layout, rot.data_ptr(), rot.stride(0), rot.stride(1), _ptr(rest),
+        0 if rest is None else rest.stride(0), 0 if rest is None else rest.stride(1), _dtype_code(rot.dtype), _stream(stream, dev)))
+
+
+def kv8_norm_rope_rows(x, norm_w, eps: float, position, inv_freq, dst_rows, kv8, kv_scale, rope_scale: float = 1.0,
+                       layout: int = KV8_ROPE_INTERLEAVED, err_word=None, stream=None) -> None:
+    """x [n][576] (f32 / bf16, rows strided): norm of 0..511 with norm_w [512] f32, rotation of 512..575 by position [n] int32 and
+    inv_freq [32] f32, quantized into cache rows dst_rows [n] int64 of kv8 [rows][576] uint8, kv_scale [rows] f32."""
+    import torch
+    fn, f32 = "kv8_norm_rope_rows", torch.float32
+    n, rows = x.shape[0], kv8.shape[0]
+    dev = _args(fn, ("norm_w", norm_w, f32, (KV8_KL,)), ("position", position, torch.int32, (n,)), ("inv_freq", inv_freq, f32, (KV8_KR // 2,)),
+                ("dst_rows", dst_rows, torch.int64, (n,)), ("kv8", kv8, torch.uint8, (rows, KV8_ROW_BYTES)), ("kv_scale", kv_scale, f32, (rows,)),
+                ("err_word", err_word, torch.int32, (1,)))
+    _rows(fn, "x", x, (f32, torch.bfloat16), (n, KV8_ROW_BYTES), dev)
+    _check(fn, load().kv8_norm_rope_rows(
+        x.data_ptr(), _dtype_code(x.dtype), n, x.stride(0) if n > 1 else KV8_ROW_BYTES, norm_w.data_ptr(), eps, position.data_ptr(),
+        inv_freq.data_ptr(), rope_scale, layout, dst_rows.data_ptr(), kv8.data_ptr(), kv_scale.data_ptr(), rows, _ptr(err_word),
+        _stream(stream, dev)))
+
+
+def kv8_quant_blocks(x, q, scale, norm_w=None, eps: float = 1e-6, stream=None) -> None:
+    """x [n][width] (f32 / bf16, rows strided), normed with norm_w [width] f32 where given -> q [n][width] uint8 e4m3, scale
+    [ceil(width / 128)][n] f32 (rows strided)."""
+    import torch
+    fn, f32 = "kv8_quant_blocks", torch.float32
+    n, width = x.shape
+    blocks = -(-width // KV8_KVB_BLOCK)
+    dev = _args(fn, ("q", q, torch.uint8, (n, width)), ("norm_w", norm_w, f32, (width,)))
+    _rows(fn, "x", x, (f32, torch.bfloat16), (n, width), dev)
+    _rows(fn, "scale", scale, (f32,), (blocks, n), dev)
+    _check(fn, load().kv8_quant_blocks(
+        x.data_ptr(), _dtype_code(x.dtype), n, width, x.stride(0) if n > 1 else -(-width // 16) * 16, _ptr(norm_w), eps, q.data_ptr(),
+        scale.data_ptr(), scale.stride(0) if blocks > 1 else n, _stream(stream, dev)))
+
+
+def kv8_matmul8(a8, a_scale, w8, w_scale, out, err_word=None, stream=None) -> None:
+    """out [M][N] (f32 / bf16, rows strided) = a8 [M][K] uint8 e4m3 (rows strided), with a_scale [ceil(K / 128)][M] f32 (rows
+    strided) or [M] f32, times the fmt=8 weight w8 [N][K] uint8, w_scale [ceil(N / 128)][ceil(K / 128)] f32."""
+    import torch
+    fn, f32, u8 = "kv8_matmul8", torch.float32, torch.uint8
+    (M, K), N = a8.shape, w8.shape[0]
+    kb = -(-K // KV8_KVB_BLOCK)
+    dev = _args(fn, ("w8", w8, u8, (N, K)), ("w_scale", w_scale, f32, (-(-N // KV8_KVB_BLOCK), kb)), ("err_word", err_word, torch.int32, (1,)))
+    _rows(fn, "a8", a8, (u8,), (M, K), dev)
+    per_row = a_scale.dim() == 1
+    _rows(fn, "a_scale", a_scale, (f32,), (M,) if per_row else (kb, M), dev)
+    _rows(fn, "out", out, (f32, torch.bfloat16), (M, N), dev)
+    _check(fn, load().kv8_matmul8(
+        a8.data_ptr(), a8.stride(0) if M > 1 else -(-K // 16) * 16, a_scale.data_ptr(), 0 if per_row else (a_scale.stride(0) if kb > 1 else M),
+        M, N, K, w8.data_ptr(), w_scale.data_ptr(), out.data_ptr(), _dtype_code(out.dtype), out.stride(0) if M > 1 else N, _ptr(err_word),
         _stream(stream, dev)))
 
 

@@ -78,6 +78,20 @@ cudaError_t launch_tree_commit(int B, const int32_t *q_start, const int32_t *len
                                const int32_t *n_accept, int max_accept, int layers, uint8_t *kv8, float *kv_scale,
                                int64_t cache_rows, const int32_t *table, int max_pages, int page_shift,
                                int32_t *new_lens, int *err_word, cudaStream_t st);
+// what stands around the attention in a layer (rope_rows.cu, quant_blocks.cu, matmul8.cu)
+cudaError_t launch_rope(const void *x, int x_bf16, int64_t n, int heads, int width, int rope_at, int rope_dim,
+                        int64_t x_row, int64_t x_head, const int32_t *position, const float *inv_freq, float scale,
+                        int half_layout, void *rot, int64_t rot_row, int64_t rot_head, void *rest, int64_t rest_row,
+                        int64_t rest_head, int out_bf16, cudaStream_t st);
+cudaError_t launch_norm_rope_rows(const void *x, int x_bf16, int64_t n, int64_t x_stride, const float *norm_w, float eps,
+                                  const int32_t *position, const float *inv_freq, float rope_scale, int half_layout,
+                                  const int64_t *dst, uint8_t *kv8, float *kv_scale, int64_t cache_rows, int *err_word,
+                                  cudaStream_t st);
+cudaError_t launch_quant_blocks(const void *x, int x_bf16, int64_t n, int width, int64_t x_stride, const float *norm_w,
+                                float eps, uint8_t *q, float *scale, int64_t scale_stride, cudaStream_t st);
+cudaError_t launch_matmul8(const uint8_t *a8, int64_t a_stride, const float *a_scale, int64_t a_scale_stride, int M, int N,
+                           int K, const uint8_t *w8, const float *w_scale, void *out, int out_bf16, int64_t out_stride,
+                           int *err_word, cudaStream_t st);
 cudaError_t launch_copy(void *dst, const void *src, size_t bytes, cudaStream_t st);
 cudaError_t launch_lse_merge(const float *ws, int B, int P, int H, float *out, cudaStream_t st);
 

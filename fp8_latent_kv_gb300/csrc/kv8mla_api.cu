@@ -30,6 +30,20 @@ inline int page_shift(int page_size) {
     return s;
 }
 
+inline bool valid_dtype(int t) { return t == KV8_F32 || t == KV8_BF16; }
+
+inline int elem_bytes(int dtype) { return dtype == KV8_BF16 ? 2 : 4; }
+
+inline bool valid_layout(int layout) { return layout == KV8_ROPE_INTERLEAVED || layout == KV8_ROPE_HALF; }
+
+// n rows of `heads` runs of `width` elements, none of which touches another
+inline bool apart(int64_t n, int64_t row, int heads, int64_t head, int64_t width) {
+    if (n == 1 && heads == 1) return true;
+    if (heads == 1) return row >= width;
+    if (n == 1) return head >= width;
+    return (head >= width && row >= (heads - 1) * head + width) || (row >= width && head >= (n - 1) * row + width);
+}
+
 inline bool valid_batch(int B, const int32_t *q_start, const int32_t *lens, int R) {
     return B >= 1 && B <= KV8_MAX_SEQS && R >= 0 && R <= KV8_MAX_ROWS && aligned(q_start, 4) && aligned(lens, 4);
 }
@@ -359,6 +373,95 @@ int kv8_tree_commit(int B, const int32_t *q_start, const int32_t *lens, const in
     return status(launch_tree_commit(B, q_start, lens, accept, n_accept, max_accept, layers, kv8, kv_scale,
                                      cache_rows, block_table, max_pages, shift, new_lens, err_word,
                                      (cudaStream_t)stream));
+}
+
+int kv8_rope_freqs(int rope_dim, double theta, double factor, double context, double beta_fast, double beta_slow,
+                   float *inv_freq, float *rope_scale) {
+    if (rope_dim < 2 || rope_dim > KV8_MAX_ROPE || rope_dim % 2 != 0 || !(theta > 1.0 && theta <= 1e30) ||
+        !(factor >= 1.0 && factor <= 1e6) || !(context >= 1.0 && context <= 1e15) ||
+        !(beta_slow > 0.0 && beta_slow <= beta_fast && beta_fast <= 1e6) || !inv_freq || !rope_scale)
+        return KV8_EINVAL;
+    // the pair that makes `beta` turns within the context
+    auto pair_of = [&](double beta) {
+        return rope_dim * log(context / (beta * 6.283185307179586)) / (2.0 * log(theta));
+    };
+    const double low = fmax(floor(pair_of(beta_fast)), 0.0), high = fmin(ceil(pair_of(beta_slow)), rope_dim - 1.0);
+    for (int i = 0; i < rope_dim / 2; ++i) {
+        const double f = pow(theta, -2.0 * i / rope_dim);
+        const double far = i <= low ? 0.0 : i >= high ? 1.0 : (i - low) / (high - low);
+        inv_freq[i] = (float)(f * (1.0 - far) + f / factor * far);
+    }
+    *rope_scale = (float)(1.0 + 0.1 * log(factor));
+    return KV8_OK;
+}
+
+int kv8_rope(const void *x, int x_dtype, int64_t n, int heads, int width, int rope_at, int rope_dim, int64_t x_row_stride,
+             int64_t x_head_stride, const int32_t *position, const float *inv_freq, float rope_scale, int layout, void *rot,
+             int64_t rot_row_stride, int64_t rot_head_stride, void *rest, int64_t rest_row_stride, int64_t rest_head_stride,
+             int out_dtype, void *stream) {
+    if (n < 0 || n > KV8_MAX_ROWS || heads < 1 || heads > KV8_MAX_HEADS || rope_dim < 2 || rope_dim > KV8_MAX_ROPE ||
+        rope_dim % 2 != 0 || width > KV8_MAX_WIDTH || rope_at < 0 || rope_at > width - rope_dim || !valid_dtype(x_dtype) ||
+        !valid_dtype(out_dtype) || !valid_layout(layout) || !isfinite(rope_scale))
+        return KV8_EINVAL;
+    if (n == 0) return KV8_OK;
+    if (width == rope_dim) rest = nullptr;
+    constexpr int64_t kMost = 1ll << 40;
+    if (x_row_stride < 0 || x_head_stride < 0 || x_row_stride > kMost || x_head_stride > kMost || rot_row_stride > kMost ||
+        rot_head_stride > kMost || (rest && (rest_row_stride > kMost || rest_head_stride > kMost)) ||
+        !apart(n, rot_row_stride, heads, rot_head_stride, rope_dim) ||
+        (rest && !apart(n, rest_row_stride, heads, rest_head_stride, width - rope_dim)))
+        return KV8_EINVAL;
+    if (!aligned(x, elem_bytes(x_dtype)) || !aligned(rot, elem_bytes(out_dtype)) || (rest && !aligned(rest, elem_bytes(out_dtype))) ||
+        !aligned(position, 4) || !aligned(inv_freq, 4))
+        return KV8_EINVAL;
+    return status(launch_rope(x, x_dtype == KV8_BF16, n, heads, width, rope_at, rope_dim, x_row_stride, x_head_stride, position,
+                              inv_freq, rope_scale, layout == KV8_ROPE_HALF, rot, rot_row_stride, rot_head_stride, rest,
+                              rest_row_stride, rest_head_stride, out_dtype == KV8_BF16, (cudaStream_t)stream));
+}
+
+int kv8_norm_rope_rows(const void *x, int x_dtype, int64_t n, int64_t x_stride, const float *norm_w, float eps,
+                       const int32_t *position, const float *inv_freq, float rope_scale, int layout, const int64_t *dst_rows,
+                       uint8_t *kv8, float *kv_scale, int64_t cache_rows, int *err_word, void *stream) {
+    if (n < 0 || cache_rows < 0 || !valid_dtype(x_dtype) || !valid_layout(layout) || !isfinite(rope_scale) ||
+        !(eps >= 0.f && isfinite(eps)))
+        return KV8_EINVAL;
+    if (n == 0) return KV8_OK;
+    if (x_stride < KV8_ROW_BYTES || x_stride > (1ll << 40) || x_stride * elem_bytes(x_dtype) % 16 != 0 || !aligned(x, 16) ||
+        !aligned(norm_w, 16) || !aligned(position, 4) || !aligned(inv_freq, 4) || !aligned(dst_rows, 8) || !aligned(kv8, 16) ||
+        !aligned(kv_scale, 4))
+        return KV8_EINVAL;
+    return status(launch_norm_rope_rows(x, x_dtype == KV8_BF16, n, x_stride, norm_w, eps, position, inv_freq, rope_scale,
+                                        layout == KV8_ROPE_HALF, dst_rows, kv8, kv_scale, cache_rows, err_word,
+                                        (cudaStream_t)stream));
+}
+
+int kv8_quant_blocks(const void *x, int x_dtype, int64_t n, int width, int64_t x_stride, const float *norm_w, float eps,
+                     uint8_t *q, float *scale, int64_t scale_stride, void *stream) {
+    if (n < 0 || n > KV8_MAX_ROWS || width < 16 || width % 16 != 0 || width > (norm_w ? KV8_MAX_NORM_WIDTH : KV8_MAX_WIDTH) ||
+        !valid_dtype(x_dtype) || (norm_w && !(eps >= 0.f && isfinite(eps))))
+        return KV8_EINVAL;
+    if (n == 0) return KV8_OK;
+    if (x_stride < width || x_stride > (1ll << 40) || x_stride * elem_bytes(x_dtype) % 16 != 0 || scale_stride < n ||
+        scale_stride > (1ll << 40) || !aligned(x, 16) || (norm_w && !aligned(norm_w, 16)) || !aligned(q, 16) || !aligned(scale, 4))
+        return KV8_EINVAL;
+    return status(launch_quant_blocks(x, x_dtype == KV8_BF16, n, width, x_stride, norm_w, eps, q, scale, scale_stride,
+                                      (cudaStream_t)stream));
+}
+
+int kv8_matmul8(const uint8_t *a8, int64_t a_stride, const float *a_scale, int64_t a_scale_stride, int M, int N, int K,
+                const uint8_t *w8, const float *w_scale, void *out, int out_dtype, int64_t out_stride, int *err_word,
+                void *stream) {
+    if (M < 0 || M > KV8_MAX_ROWS || N < 1 || N > KV8_MAX_ROWS || K < 16 || K % 16 != 0 || K > KV8_MAX_WIDTH ||
+        !valid_dtype(out_dtype))
+        return KV8_EINVAL;
+    if (M == 0) return KV8_OK;
+    if (a_stride < K || a_stride % 16 != 0 || a_stride > (1ll << 39) || (a_scale_stride != 0 && a_scale_stride < M) ||
+        a_scale_stride > (1ll << 40) || out_stride < N || out_stride > (1ll << 36))
+        return KV8_EINVAL;
+    if (!aligned(a8, 16) || !aligned(a_scale, 4) || !aligned(w8, 16) || !aligned(w_scale, 4) || !aligned(out, elem_bytes(out_dtype)))
+        return KV8_EINVAL;
+    return status(launch_matmul8(a8, a_stride, a_scale, a_scale_stride, M, N, K, w8, w_scale, out, out_dtype == KV8_BF16, out_stride,
+                                 err_word, (cudaStream_t)stream));
 }
 
 int kv8_copy(void *dst, const void *src, size_t bytes, void *stream) {

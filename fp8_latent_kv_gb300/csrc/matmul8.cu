@@ -1,0 +1,465 @@
+// matmul8.cu -- product of e4m3 rows with an fmt=8 weight on the tensor cores (tcgen05, sm_103a).
+//
+//     out[m][n] = sum_kb  sa[kb][m] sw[n / 128][kb]  sum_{k in block kb} e4m3(a8[m][k]) e4m3(w8[n][k])
+//
+// The inner sums (128 exact products) run in kind::f8f6f4 MMAs with f32 accumulators; the scales change from one block of
+// 128 to the next, so each block's sums leave TMEM, are multiplied by sa sw and added in f32 registers while the tensor
+// cores work on the next block in other columns.
+//
+// Two layouts of one kernel:
+//   many rows (kSwap = false): MMA rows are 128 rows of a8, columns kNT rows of w8.  sa is one number a thread, sw one
+//     a warp.  Persistent blocks, one an SM.
+//   few rows (kSwap = true): MMA rows are 128 rows of w8, columns up to kNT = 16 / 32 / 64 rows of a8: the weight is read
+//     once, whatever the number of rows, and no MMA row is idle.  The columns' factors sa sw stand in shared memory.
+// Where the tiles are fewer than the SMs, a cluster of 2, 4 or 8 blocks shares a tile along K; each block adds the others'
+// sums for its part of the tile through distributed shared memory, in the order of their ranks (the result does not depend
+// on timing, and no workspace is needed).
+#include "elem.cuh"
+#include "internal.h"
+#include "sm100_more.cuh"
+
+namespace kv8 {
+namespace {
+
+using namespace sm100;
+
+constexpr int kMmBlk = KV8_KVB_BLOCK;  // K per scale block: 128 e4m3 bytes, one 128-byte swizzled row
+constexpr int kMmRows = 128;           // MMA M
+constexpr int kFacBlocks = 32;         // K blocks whose column factors stand in shared memory at a time (kSwap)
+constexpr int kGroupTiles = 16;        // row tiles that are walked together, for the L2's sake
+
+struct MmArgs {
+    const float *a_scale;
+    int64_t a_scale_stride;  // between K blocks; 0: one scale a row
+    const float *w_scale;
+    void *out;
+    int64_t out_stride;
+    int M, N, kb;            // kb: blocks of 128 along K
+    int p_tiles, q_tiles;    // tiles along the MMA rows' and columns' operand
+    int split;               // blocks of a cluster, along K
+    int tma_out;             // out can be written by tensor stores
+    int *err_word;
+};
+
+template <bool kSwap, int kNT, int kStages>
+struct MmShape {
+    static constexpr int kEpi = kSwap ? 4 : 8;                 // warps that scale and add
+    static constexpr int kThreads = 64 + 32 * kEpi;
+    static constexpr int kCols = kSwap ? kNT : kNT / 2;        // accumulator columns of a thread
+    static constexpr int kAcc = kNT >= 256 ? 2 : 4;            // TMEM accumulators in turn
+    static constexpr uint32_t kTmem = kNT * kAcc < 32 ? 32 : kNT * kAcc;
+    static constexpr uint32_t kStage = (kMmRows + kNT) * 128;
+    static constexpr uint32_t kStaging = kSwap ? 0 : kEpi * 4096;
+    static constexpr uint32_t kFac = kSwap ? kFacBlocks * kNT * 4 : 0;
+    static constexpr uint32_t kBytes = 1024 + kStages * kStage + kStaging + kFac + 256;
+    static_assert(kBytes <= 227 * 1024, "shared memory of a block");
+    static_assert(kNT * kMmRows * 4 <= kStages * kStage || kNT == 256, "a tile's sums fit the stages");
+};
+
+template <bool kSwap, int kNT, int kStages, int kBlocks, bool kBf16, bool kSplit>
+__global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlocks)
+    matmul8_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ CUtensorMap map_out, const MmArgs a) {
+    using S = MmShape<kSwap, kNT, kStages>;
+    using Out = typename Elem<kBf16>::T;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *staging = smem + kStages * S::kStage;
+    float *fac = reinterpret_cast<float *>(staging + S::kStaging);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + S::kStaging + S::kFac);
+    uint64_t *full = bars, *empty = bars + kStages, *t_full = bars + 2 * kStages, *t_empty = t_full + S::kAcc, *drain = t_empty + S::kAcc;
+    static_assert((2 * kStages + 2 * S::kAcc + 1) * 8 + 8 <= 256, "barriers");
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int split = kSplit ? a.split : 1;
+    const int rank = kSplit ? (int)cluster_rank() : 0;
+    const int first = kSplit ? (int)blockIdx.x / split : (int)blockIdx.x, step = kSplit ? (int)gridDim.x / split : (int)gridDim.x;
+    const int tiles = a.p_tiles * a.q_tiles;
+    const int kb0 = (int)((int64_t)a.kb * rank / split), kb1 = (int)((int64_t)a.kb * (rank + 1) / split);
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < S::kAcc; ++i) {
+            mbar_init(t_full + i, 1);
+            mbar_init(t_empty + i, S::kEpi);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, S::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    // tile -> (tile of the MMA rows' operand, tile of the columns'): kGroupTiles row tiles at a time, the columns' outside
+    auto place = [&](int tile, int &tp, int &tq) {
+        const int per = kGroupTiles * a.q_tiles, g = tile / per, r = tile - g * per;
+        const int rows = min(kGroupTiles, a.p_tiles - g * kGroupTiles);
+        tq = r / rows;
+        tp = g * kGroupTiles + r - tq * rows;
+    };
+
+    if (warp == 0) {
+        // ---- loads
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                int tp, tq;
+                place(tile, tp, tq);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !bar_wait(empty + s, (it / kStages - 1) & 1, abort_flag, a.err_word)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *p = smem + s * S::kStage;
+                    mbar_arrive_expect_tx(full + s, S::kStage);
+                    tma_load_2d(p, &map_p, kb * kMmBlk, tp * kMmRows, full + s);
+                    tma_load_2d(p + kMmRows * 128, &map_q, kb * kMmBlk, tq * kNT, full + s);
+                }
+            }
+            if (!ok)  // the copies in flight end before the block does
+                for (int i = it < kStages ? 0 : it - kStages; i < it; ++i)
+                    (void)bar_wait(full + i % kStages, (i / kStages) & 1, nullptr, nullptr, 1ll << 28);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- products
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(kMmRows, kNT, false, false);
+            int it = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % kStages, c = it % S::kAcc;
+                    if (it >= S::kAcc && !bar_wait(t_empty + c, (it / S::kAcc - 1) & 1, abort_flag, a.err_word)) ok = false;
+                    if (ok && !bar_wait(full + s, (it / kStages) & 1, abort_flag, a.err_word)) ok = false;
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t p = smem_u32(smem + s * S::kStage), d = tmem + (uint32_t)(c * kNT);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8f6f4(d, smem_desc(p + kk * 32, 0, 1024, kSw128), smem_desc(p + kMmRows * 128 + kk * 32, 0, 1024, kSw128),
+                                   idesc, kk > 0);
+                    mma_commit(empty + s);
+                    mma_commit(t_full + c);
+                }
+            }
+            if (!ok) {
+                mma_commit(drain);
+                (void)bar_wait(drain, 0, nullptr, nullptr, 1ll << 28);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- scales and sums
+        const int quad = warp & 3, half = (warp - 2) >> 2, epi_tid = tid - 64;  // (a warp reads TMEM lanes 32 (warp % 4) ..)
+        const int row = quad * 32 + lane, col0 = half * S::kCols;
+        const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+        Out *out = static_cast<Out *>(a.out);
+        int it = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles; tile += step) {
+            int tp, tq;
+            place(tile, tp, tq);
+            uint64_t acc[S::kCols / 2];
+#pragma unroll
+            for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0;
+            // adds one K block: acc += D * factor, the loads one ahead of the sums
+            auto add_block = [&](auto factor) {
+                const int c = it % S::kAcc;
+                if (ok) ok = bar_wait(t_full + c, (it / S::kAcc) & 1, abort_flag, a.err_word);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                tc_fence_after_sync();
+                const uint32_t d = tmem + lane_addr + (uint32_t)(c * kNT + col0);
+                uint32_t v[2][16];
+                tmem_ld_32x32b_x16(d, v[0]);
+#pragma unroll
+                for (int j = 0; j < S::kCols / 16; ++j) {
+                    tmem_wait_ld(v[j & 1]);
+                    if (j + 1 < S::kCols / 16) {
+                        tmem_ld_32x32b_x16(d + 16 * (j + 1), v[(j + 1) & 1]);
+                    } else {
+                        tc_fence_before_sync();
+                        if (lane == 0) mbar_arrive(t_empty + c);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        acc[8 * j + i] = f2_fma(f2_pack(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])),
+                                                factor(8 * j + i), acc[8 * j + i]);
+                }
+                ++it;
+            };
+            if constexpr (kSwap) {
+                for (int k0 = kb0; k0 < kb1; k0 += kFacBlocks) {
+                    const int nk = min(kFacBlocks, kb1 - k0);
+                    named_sync(1, 32 * S::kEpi);
+                    for (int i = epi_tid; i < nk * kNT; i += 32 * S::kEpi) {
+                        const int k = i / kNT, m = tq * kNT + i - k * kNT;
+                        fac[i] = m < a.M ? __ldg(a.a_scale + (k0 + k) * a.a_scale_stride + m) * __ldg(a.w_scale + (int64_t)tp * a.kb + k0 + k) : 0.f;
+                    }
+                    named_sync(1, 32 * S::kEpi);
+                    for (int k = 0; k < nk; ++k) {
+                        const uint64_t *f = reinterpret_cast<const uint64_t *>(fac + k * kNT);
+                        add_block([&](int i) { return f[i]; });
+                    }
+                }
+            } else {
+                const int m = tp * kMmRows + row, nb = (tq * kNT + col0) / kMmBlk;
+                const float *sa = a.a_scale + m, *sw = a.w_scale + (int64_t)nb * a.kb;
+                const bool have = m < a.M && nb * kMmBlk < a.N;
+                float fa[4], fw[4];  // the factors of the next four blocks, on their way
+                auto fetch = [&](int u, int kb) {
+                    const bool h = have && kb < kb1;
+                    fa[u] = h ? __ldg(sa + kb * a.a_scale_stride) : 0.f;
+                    fw[u] = h ? __ldg(sw + kb) : 0.f;
+                };
+#pragma unroll
+                for (int u = 0; u < 4; ++u) fetch(u, kb0 + u);
+                for (int k = kb0; k < kb1; k += 4) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        if (k + u < kb1) {
+                            const float f = fa[u] * fw[u];
+                            const uint64_t ff = f2_pack(f, f);
+                            fetch(u, k + u + 4);
+                            add_block([&](int) { return ff; });
+                        }
+                    }
+                }
+            }
+            if constexpr (kSplit) {
+                // the block's sums, [column][row], over the stages (which no copy or product uses any more)
+                float *red = reinterpret_cast<float *>(smem);
+#pragma unroll
+                for (int i = 0; i < S::kCols / 2; ++i) {
+                    float lo, hi;
+                    f2_unpack(acc[i], lo, hi);
+                    red[(col0 + 2 * i) * kMmRows + row] = lo;
+                    red[(col0 + 2 * i + 1) * kMmRows + row] = hi;
+                }
+            } else if (!ok) {
+            } else if constexpr (kSwap) {
+                const int n = tp * kMmRows + row;
+#pragma unroll
+                for (int i = 0; i < S::kCols; ++i) {
+                    float v[2];
+                    f2_unpack(acc[i / 2], v[0], v[1]);
+                    const int m = tq * kNT + i;
+                    const float r[1] = {v[i & 1]};
+                    if (m < a.M && n < a.N) store<1>(out + m * a.out_stride + n, r);
+                }
+            } else {
+                // 32 rows x 128 bytes at a time through a swizzled staging tile of the warp's own
+                constexpr int kPart = kBf16 ? 64 : 32;
+                uint8_t *st = staging + (warp - 2) * 4096;
+                const int m0 = tp * kMmRows + quad * 32;
+#pragma unroll
+                for (int c = 0; c < S::kCols; c += kPart) {
+                    const int n0 = tq * kNT + col0 + c;
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint4 w;
+                        if constexpr (kBf16) {
+                            float v[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) f2_unpack(acc[c / 2 + 4 * j + i], v[2 * i], v[2 * i + 1]);
+                            w = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+                        } else {
+                            float v[4];
+                            f2_unpack(acc[c / 2 + 2 * j], v[0], v[1]);
+                            f2_unpack(acc[c / 2 + 2 * j + 1], v[2], v[3]);
+                            w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+                        }
+                        *reinterpret_cast<uint4 *>(st + sw128_offset(lane, 16 * j)) = w;
+                    }
+                    if (a.tma_out) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && m0 < a.M && n0 < a.N) {
+                            tma_store_2d(&map_out, st, n0, m0);
+                            bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        for (int r = 0; r < 32 && m0 + r < a.M; ++r)
+                            for (int e = lane; e < kPart && n0 + e < a.N; e += 32)
+                                out[(int64_t)(m0 + r) * a.out_stride + n0 + e] =
+                                    *reinterpret_cast<const Out *>(st + sw128_offset(r, e * (int)sizeof(Out)));
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        if constexpr (!kSplit && !kSwap) {
+            if (lane == 0) bulk_wait();
+            __syncwarp();
+        }
+    }
+    if constexpr (kSplit) {
+        __syncthreads();
+        cluster_sync();
+        if (warp >= 2 && *(volatile int *)abort_flag == 0) {
+            int tp, tq;
+            place(first, tp, tq);
+            const uint32_t red = smem_u32(smem);
+            Out *out = static_cast<Out *>(a.out);
+            const int per = kNT / split, c0 = rank * per;  // this block's columns of the tile
+            if constexpr (kSwap) {
+                for (int i = tid - 64; i < per * kMmRows; i += 32 * S::kEpi) {
+                    const int c = c0 + i / kMmRows, r = i % kMmRows;
+                    float v[1] = {0.f};
+                    for (int b = 0; b < split; ++b) v[0] += cluster_load(red + (c * kMmRows + r) * 4, b);
+                    const int m = tq * kNT + c, n = tp * kMmRows + r;
+                    if (m < a.M && n < a.N) store<1>(out + m * a.out_stride + n, v);
+                }
+            } else {
+                for (int i = tid - 64; i < per / 8 * kMmRows; i += 32 * S::kEpi) {
+                    const int c = c0 + i / kMmRows * 8, r = i % kMmRows;
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+                    for (int b = 0; b < split; ++b)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] += cluster_load(red + ((c + j) * kMmRows + r) * 4, b);
+                    const int m = tp * kMmRows + r, n = tq * kNT + c;
+                    if (m >= a.M) continue;
+                    Out *o = out + m * a.out_stride + n;
+                    if (a.tma_out && n + 8 <= a.N) {
+                        store<8>(o, v);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float one[1] = {v[j]};
+                            if (n + j < a.N) store<1>(o + j, one);
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // nobody leaves while another block reads its sums
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, S::kTmem);
+}
+
+bool map_bytes(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const uint8_t *p, int K, int64_t rows, int64_t stride, int box) {
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
+    const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, es[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(p), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct MmCall {
+    const uint8_t *a8, *w8;
+    int64_t a_stride;
+    int K;
+    bool bf16;
+    MmArgs a;
+    cudaStream_t st;
+};
+
+template <bool kSwap, int kNT, int kStages, int kBlocks, bool kBf16, bool kSplit>
+cudaError_t mm_launch(MmCall c, int blocks) {
+    using S = MmShape<kSwap, kNT, kStages>;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    alignas(64) CUtensorMap map_a, map_w, map_out;
+    const int w = kBf16 ? 2 : 4;
+    if (!map_bytes(encode, &map_a, c.a8, c.K, c.a.M, c.a_stride, kSwap ? kNT : kMmRows) ||
+        !map_bytes(encode, &map_w, c.w8, c.K, c.a.N, c.K, kSwap ? kMmRows : kNT))
+        return cudaErrorInvalidValue;
+    map_out = map_a;  // (not read where out is not written by tensor stores)
+    c.a.tma_out = reinterpret_cast<uintptr_t>(c.a.out) % 16 == 0 && c.a.out_stride * w % 16 == 0;
+    if (!kSwap && !kSplit && c.a.tma_out) {
+        const cuuint64_t dims[2] = {(cuuint64_t)c.a.N, (cuuint64_t)c.a.M}, strides[1] = {(cuuint64_t)c.a.out_stride * w};
+        const cuuint32_t box[2] = {128u / w, 32}, es[2] = {1, 1};
+        if (encode(&map_out, kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, c.a.out, dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    auto kernel = matmul8_kernel<kSwap, kNT, kStages, kBlocks, kBf16, kSplit>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kBytes;
+    cfg.stream = c.st;
+    cudaLaunchAttribute attr[1];
+    if (kSplit) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)c.a.split;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    e = kSwap ? cudaLaunchKernelEx(&cfg, kernel, map_w, map_a, map_out, c.a) : cudaLaunchKernelEx(&cfg, kernel, map_a, map_w, map_out, c.a);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+template <bool kSwap, int kNT, int kStages, int kBlocks, bool kSplit>
+cudaError_t mm_typed(const MmCall &c, int blocks) {
+    return c.bf16 ? mm_launch<kSwap, kNT, kStages, kBlocks, true, kSplit>(c, blocks)
+                  : mm_launch<kSwap, kNT, kStages, kBlocks, false, kSplit>(c, blocks);
+}
+
+int tiles_of(int n, int t) { return (n + t - 1) / t; }
+
+}  // namespace
+
+cudaError_t launch_matmul8(const uint8_t *a8, int64_t a_stride, const float *a_scale, int64_t a_scale_stride, int M, int N,
+                           int K, const uint8_t *w8, const float *w_scale, void *out, int out_bf16, int64_t out_stride,
+                           int *err_word, cudaStream_t st) {
+    MmCall c{};
+    c.a8 = a8, c.w8 = w8, c.a_stride = a_stride, c.K = K, c.bf16 = out_bf16 != 0, c.st = st;
+    c.a.a_scale = a_scale, c.a.a_scale_stride = a_scale_stride, c.a.w_scale = w_scale;
+    c.a.out = out, c.a.out_stride = out_stride, c.a.M = M, c.a.N = N, c.a.kb = tiles_of(K, kMmBlk), c.a.err_word = err_word;
+    const int sms = device_sm_count();
+    if (M <= 64) {
+        const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64, slots = 2 * sms;
+        c.a.p_tiles = tiles_of(N, kMmRows), c.a.q_tiles = 1;
+        c.a.split = 1;
+        while (c.a.split < 8 && c.a.p_tiles * c.a.split * 2 <= slots && c.a.kb >= c.a.split * 4) c.a.split *= 2;
+        const int blocks = c.a.p_tiles * c.a.split;
+        if (nt == 16) return mm_typed<true, 16, 5, 2, true>(c, blocks);
+        if (nt == 32) return mm_typed<true, 32, 5, 2, true>(c, blocks);
+        return mm_typed<true, 64, 4, 2, true>(c, blocks);
+    }
+    c.a.p_tiles = tiles_of(M, kMmRows);
+    const int wide = c.a.p_tiles * tiles_of(N, 256), narrow = c.a.p_tiles * tiles_of(N, 128);
+    if (narrow * 2 <= sms && c.a.kb >= 4) {
+        c.a.q_tiles = tiles_of(N, 128);
+        c.a.split = 1;
+        while (c.a.split < 8 && narrow * c.a.split * 2 <= sms && c.a.kb >= c.a.split * 4) c.a.split *= 2;
+        return mm_typed<false, 128, 5, 1, true>(c, narrow * c.a.split);
+    }
+    c.a.split = 1;
+    // in units of a 128 x 128 tile's time: rounds of the persistent blocks
+    if (2 * tiles_of(wide, sms) <= tiles_of(narrow, sms)) {
+        c.a.q_tiles = tiles_of(N, 256);
+        return mm_typed<false, 256, 4, 1, false>(c, wide < sms ? wide : sms);
+    }
+    c.a.q_tiles = tiles_of(N, 128);
+    return mm_typed<false, 128, 5, 1, false>(c, narrow < sms ? narrow : sms);
+}
+
+}  // namespace kv8

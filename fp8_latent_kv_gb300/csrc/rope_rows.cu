@@ -1,0 +1,287 @@
+// rope_rows.cu -- rotary positions of a part of each head, and a projection's fresh rows made into cache rows.
+//
+// The rotation of dims [at, at + dim) of a head at position p, for i < dim / 2 with the pair (u, v) = elements
+// (2 i, 2 i + 1) (interleaved layout) or (i, i + dim / 2) (half layout):
+//     a = p inv_freq[i];   u' = scale (u cos a - v sin a);   v' = scale (u sin a + v cos a)
+// All arithmetic is f32; an output in bf16 is rounded once.
+//
+// Both kernels read every value once and write every value once, so DRAM bounds them.
+#include "elem.cuh"
+#include "internal.h"
+#include "norm.cuh"
+#include "quant_row.cuh"
+#include "rope.cuh"
+#include "sm100.cuh"
+
+namespace kv8 {
+namespace {
+
+// ---------------------------------------------------------------------------------------------------------
+// kv8_rope
+// ---------------------------------------------------------------------------------------------------------
+constexpr int kRopeThreads = 256, kRopeUnroll = 4, kRopeTable = 1024;  // cos / sin pairs of a block's tokens
+
+struct RopeArgs {
+    const void *x;
+    int64_t x_row, x_head;  // strides in elements
+    void *rot, *rest;
+    int64_t rot_row, rot_head, rest_row, rest_head;
+    const int32_t *position;
+    const float *inv_freq;
+    float scale;
+    int64_t n;
+    int heads, at, dim, n_rest;      // n_rest: elements of a head that are not turned, 0 where `rest` is not asked for
+    int tokens, head_part, n_parts;  // a block: `tokens` tokens of `head_part` heads, n_parts blocks for all heads
+};
+
+// A block takes some tokens and heads; a thread's item is V values of the rest, V / 2 interleaved pairs, or V pairs
+// of the half layout.  The loads of a thread's items go out together.  An item reads all it needs before it writes,
+// so the rotated part may be written over x.
+template <bool kInBf16, bool kOutBf16, bool kHalf, int V>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+    using In = typename Elem<kInBf16>::T;
+    using Out = typename Elem<kOutBf16>::T;
+    constexpr int P = kHalf ? V : (V == 1 ? 1 : V / 2);  // pairs of a rotated item
+    constexpr int W = kHalf ? V : 2 * P;                 // its values in one place
+    __shared__ float2 table[kRopeTable];
+    const int half_dim = a.dim / 2;
+    const int64_t block = blockIdx.x / a.n_parts;
+    const int part = (int)(blockIdx.x - block * a.n_parts);
+    const int64_t n0 = block * a.tokens;
+    const int tokens = (int)(a.n - n0 < a.tokens ? a.n - n0 : a.tokens);
+    const int h0 = part * a.head_part, heads = min(a.head_part, a.heads - h0);
+    for (int i = threadIdx.x; i < tokens * half_dim; i += kRopeThreads) {
+        const int t = i / half_dim, k = i - t * half_dim;
+        table[i] = turn_cos_sin(__ldg(a.position + n0 + t), turn_of(__ldg(a.inv_freq + k)), a.scale);
+    }
+    const int rest_items = a.n_rest / V, per_head = rest_items + half_dim / P, items = tokens * heads * per_head;
+    __syncthreads();
+    for (int base = threadIdx.x; base < items; base += kRopeThreads * kRopeUnroll) {
+        float u[kRopeUnroll][W], v[kRopeUnroll][kHalf ? W : 1];
+#pragma unroll
+        for (int j = 0; j < kRopeUnroll; ++j) {
+            const int it = base + j * kRopeThreads;
+            if (it >= items) break;
+            const int th = it / per_head, k = it - th * per_head, t = th / heads, h = h0 + th - t * heads;
+            const In *x = static_cast<const In *>(a.x) + (n0 + t) * a.x_row + h * a.x_head;
+            if (k < rest_items) {
+                float r[V];
+                const int e = k * V;
+                load<V>(x + (e < a.at ? e : e + a.dim), r);
+#pragma unroll
+                for (int q = 0; q < V; ++q) u[j][q] = r[q];
+            } else if constexpr (kHalf) {
+                const int i = (k - rest_items) * P;
+                load<W>(x + a.at + i, u[j]);
+                load<W>(x + a.at + half_dim + i, v[j]);
+            } else if constexpr (V == 1) {  // (the two values may not be aligned as a pair)
+                const In *p = x + a.at + 2 * (k - rest_items);
+                float r[1];
+                load<1>(p, r);
+                u[j][0] = r[0];
+                load<1>(p + 1, r);
+                u[j][1] = r[0];
+            } else {
+                load<W>(x + a.at + (k - rest_items) * W, u[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kRopeUnroll; ++j) {
+            const int it = base + j * kRopeThreads;
+            if (it >= items) break;
+            const int th = it / per_head, k = it - th * per_head, t = th / heads, h = h0 + th - t * heads;
+            if (k < rest_items) {
+                float r[V];
+#pragma unroll
+                for (int q = 0; q < V; ++q) r[q] = u[j][q];
+                store<V>(static_cast<Out *>(a.rest) + (n0 + t) * a.rest_row + h * a.rest_head + k * V, r);
+                continue;
+            }
+            const int i = (k - rest_items) * P;
+            Out *o = static_cast<Out *>(a.rot) + (n0 + t) * a.rot_row + h * a.rot_head;
+            const float2 *cs = table + t * half_dim + i;
+            if constexpr (kHalf) {
+                float p[W], q[W];
+#pragma unroll
+                for (int m = 0; m < P; ++m) {
+                    p[m] = u[j][m] * cs[m].x - v[j][m] * cs[m].y;
+                    q[m] = u[j][m] * cs[m].y + v[j][m] * cs[m].x;
+                }
+                store<W>(o + i, p);
+                store<W>(o + half_dim + i, q);
+            } else {
+                float p[W];
+#pragma unroll
+                for (int m = 0; m < P; ++m) {
+                    p[2 * m] = u[j][2 * m] * cs[m].x - u[j][2 * m + 1] * cs[m].y;
+                    p[2 * m + 1] = u[j][2 * m] * cs[m].y + u[j][2 * m + 1] * cs[m].x;
+                }
+                if constexpr (V == 1) {
+                    const float p0[1] = {p[0]}, p1[1] = {p[1]};
+                    store<1>(o + 2 * i, p0);
+                    store<1>(o + 2 * i + 1, p1);
+                } else {
+                    store<W>(o + 2 * i, p);
+                }
+            }
+        }
+    }
+}
+
+template <bool kInBf16, bool kOutBf16, bool kHalf>
+cudaError_t rope_go(const RopeArgs &a, bool wide, int64_t blocks, cudaStream_t st) {
+    if (wide)
+        rope_kernel<kInBf16, kOutBf16, kHalf, 8><<<(unsigned)blocks, kRopeThreads, 0, st>>>(a);
+    else
+        rope_kernel<kInBf16, kOutBf16, kHalf, 1><<<(unsigned)blocks, kRopeThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// kv8_norm_rope_rows
+// ---------------------------------------------------------------------------------------------------------
+constexpr int kRowsThreads = 256;
+
+// One warp a row, grid-stride: lane l holds latent elements 8 l .. and 256 + 8 l .., and rotary elements 2 l, 2 l + 1
+// (a pair of the interleaved layout; of the half layout the partners sit in lane l xor 16).
+template <bool kBf16, bool kHalf>
+__global__ void __launch_bounds__(kRowsThreads) norm_rope_rows_kernel(
+    const void *__restrict__ xv, int64_t n, int64_t x_stride, const float *__restrict__ norm_w, float eps,
+    const int32_t *__restrict__ position, const float *__restrict__ inv_freq, float rope_scale,
+    const int64_t *__restrict__ dst, uint8_t *__restrict__ kv8, float *__restrict__ kv_scale, int64_t cache_rows,
+    int *err_word) {
+    using T = typename Elem<kBf16>::T;
+    const T *x = static_cast<const T *>(xv);
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (kRowsThreads / 32);
+    uint64_t turn[kHalf ? 2 : 1];
+    if constexpr (kHalf) {
+        turn[0] = turn_of(__ldg(inv_freq + 2 * (lane & 15)));
+        turn[1] = turn_of(__ldg(inv_freq + 2 * (lane & 15) + 1));
+    } else {
+        turn[0] = turn_of(__ldg(inv_freq + lane));
+    }
+    for (int64_t r = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5); r < n; r += warps) {
+        const int64_t row = __ldg(dst + r);
+        if (row < 0 || row >= cache_rows) {
+            if (lane == 0 && err_word) atomicOr(err_word, (int)KV8_ERR_INDEX);
+            continue;
+        }
+        const T *xr = x + r * x_stride;
+        float y[2][8], k[2];
+        load<8>(xr + 8 * lane, y[0]);
+        load<8>(xr + 256 + 8 * lane, y[1]);
+        load<2>(xr + kKL + 2 * lane, k);
+        const int32_t pos = __ldg(position + r);
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) ss = fmaf(y[j >> 3][j & 7], y[j >> 3][j & 7], ss);
+        ss = warp_sum(ss);
+        const float ms = ss * (1.f / kKL) + eps;
+        float pre = 1.f, inv = __frsqrt_rn(ms);
+        if (!(ms >= 1e-32f && ss <= 1e30f)) {  // squares that leave the f32 range, infinities, NaN
+            double sd = 0.0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sd += (double)y[j >> 3][j & 7] * (double)y[j >> 3][j & 7];
+            norm_factor_f64(warp_sum_f64(sd) / kKL + (double)eps, pre, inv);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(norm_w + 256 * j + 8 * lane));
+            const float4 b = __ldg(reinterpret_cast<const float4 *>(norm_w + 256 * j + 8 * lane) + 1);
+            const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[j][q] = y[j][q] * pre * inv * w[q];
+        }
+        const float2 c0 = turn_cos_sin(pos, turn[0], rope_scale);
+        if constexpr (kHalf) {
+            const float2 c1 = turn_cos_sin(pos, turn[1], rope_scale);
+            const float sign = lane < 16 ? -1.f : 1.f;
+            const float o0 = __shfl_xor_sync(0xffffffffu, k[0], 16), o1 = __shfl_xor_sync(0xffffffffu, k[1], 16);
+            k[0] = k[0] * c0.x + sign * o0 * c0.y;
+            k[1] = k[1] * c1.x + sign * o1 * c1.y;
+        } else {
+            const float u = k[0], v = k[1];
+            k[0] = u * c0.x - v * c0.y;
+            k[1] = u * c0.y + v * c0.x;
+        }
+        float amax = finite_abs_max(finite_abs_max(0.f, k[0]), k[1]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) amax = finite_abs_max(amax, y[j >> 3][j & 7]);
+        amax = warp_max(amax);
+        float qpre, mul, sc;
+        row_quant_factors(amax, qpre, mul, sc);
+        if (lane == 0) kv_scale[row] = sc;
+        uint8_t *q = kv8 + row * kRow;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<uint2 *>(q + 256 * j + 8 * lane) =
+                make_uint2(enc4(scale4(make_float4(y[j][0], y[j][1], y[j][2], y[j][3]), qpre, mul)),
+                           enc4(scale4(make_float4(y[j][4], y[j][5], y[j][6], y[j][7]), qpre, mul)));
+        *reinterpret_cast<uint16_t *>(q + kKL + 2 * lane) =
+            (uint16_t)enc2(__fmul_rn(__fmul_rn(k[0], qpre), mul), __fmul_rn(__fmul_rn(k[1], qpre), mul));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const void *x, int x_bf16, int64_t n, int heads, int width, int rope_at, int rope_dim,
+                        int64_t x_row, int64_t x_head, const int32_t *position, const float *inv_freq, float scale,
+                        int half_layout, void *rot, int64_t rot_row, int64_t rot_head, void *rest, int64_t rest_row,
+                        int64_t rest_head, int out_bf16, cudaStream_t st) {
+    RopeArgs a{};
+    a.x = x, a.x_row = x_row, a.x_head = x_head;
+    a.rot = rot, a.rot_row = rot_row, a.rot_head = rot_head;
+    a.rest = rest, a.rest_row = rest_row, a.rest_head = rest_head;
+    a.position = position, a.inv_freq = inv_freq, a.scale = scale;
+    a.n = n, a.heads = heads, a.at = rope_at, a.dim = rope_dim;
+    a.n_rest = rest ? width - rope_dim : 0;
+    // eight values at a time where every run of eight lies on 16 bytes
+    const int64_t odd = x_row | x_head | rot_row | rot_head | (rest ? rest_row | rest_head : 0) | rope_at | (width - rope_dim) |
+                        (half_layout ? rope_dim / 2 : rope_dim);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(rot) | reinterpret_cast<uintptr_t>(rest);
+    const bool wide = odd % 8 == 0 && at % 16 == 0;
+    const int V = wide ? 8 : 1;
+    const int per_head = a.n_rest / V + (half_layout ? rope_dim / 2 / V : rope_dim / (wide ? 8 : 2));
+    // a block's items: four a thread, or one where that many blocks would leave SMs without work
+    const int64_t all = n * heads * (int64_t)per_head;
+    const int target = all >= (int64_t)device_sm_count() * kRopeThreads * kRopeUnroll ? kRopeThreads * kRopeUnroll : kRopeThreads;
+    int hp = target / per_head;
+    a.head_part = hp < 1 ? 1 : hp < heads ? hp : heads;
+    a.n_parts = (heads + a.head_part - 1) / a.head_part;
+    a.head_part = (heads + a.n_parts - 1) / a.n_parts;  // even parts
+    int tokens = a.n_parts > 1 ? 1 : target / (heads * per_head);
+    const int most = kRopeTable / (rope_dim / 2);
+    a.tokens = tokens < 1 ? 1 : tokens < most ? tokens : most;
+    const int64_t blocks = (n + a.tokens - 1) / a.tokens * a.n_parts;
+    switch ((x_bf16 ? 4 : 0) | (out_bf16 ? 2 : 0) | (half_layout ? 1 : 0)) {
+        case 0: return rope_go<false, false, false>(a, wide, blocks, st);
+        case 1: return rope_go<false, false, true>(a, wide, blocks, st);
+        case 2: return rope_go<false, true, false>(a, wide, blocks, st);
+        case 3: return rope_go<false, true, true>(a, wide, blocks, st);
+        case 4: return rope_go<true, false, false>(a, wide, blocks, st);
+        case 5: return rope_go<true, false, true>(a, wide, blocks, st);
+        case 6: return rope_go<true, true, false>(a, wide, blocks, st);
+        default: return rope_go<true, true, true>(a, wide, blocks, st);
+    }
+}
+
+cudaError_t launch_norm_rope_rows(const void *x, int x_bf16, int64_t n, int64_t x_stride, const float *norm_w, float eps,
+                                  const int32_t *position, const float *inv_freq, float rope_scale, int half_layout,
+                                  const int64_t *dst, uint8_t *kv8, float *kv_scale, int64_t cache_rows, int *err_word,
+                                  cudaStream_t st) {
+    int64_t blocks = (n + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
+    const int64_t cap = (int64_t)device_sm_count() * 8;
+    if (blocks > cap) blocks = cap;
+    auto go = [&](auto kernel) {
+        kernel<<<(unsigned)blocks, kRowsThreads, 0, st>>>(x, n, x_stride, norm_w, eps, position, inv_freq, rope_scale, dst,
+                                                          kv8, kv_scale, cache_rows, err_word);
+    };
+    if (x_bf16)
+        half_layout ? go(norm_rope_rows_kernel<true, true>) : go(norm_rope_rows_kernel<true, false>);
+    else
+        half_layout ? go(norm_rope_rows_kernel<false, true>) : go(norm_rope_rows_kernel<false, false>);
+    return cudaGetLastError();
+}
+
+}  // namespace kv8

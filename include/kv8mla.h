@@ -66,6 +66,9 @@ extern "C" {
 #define KV8_MAX_IDX_HEADS 128  /* DSA indexer: index heads per query (a multiple of 16) */
 #define KV8_MX_NOPE 448        /* mixed cache: no-position values per row (e4m3 + row scale) */
 #define KV8_MX_ROPE 64         /* mixed cache: RoPE values per row (bf16) */
+#define KV8_MAX_WIDTH 65536    /* kv8_quant_blocks, kv8_matmul8: columns (K); kv8_rope: elements of a head */
+#define KV8_MAX_NORM_WIDTH 16384 /* kv8_quant_blocks with a norm: columns */
+#define KV8_MAX_ROPE 256       /* kv8_rope: rotated elements of a head */
 #define KV8_MAX_SEQS 4096      /* paged calls: sequences per call */
 #define KV8_MAX_TREE 256       /* paged calls: drafted tokens per sequence */
 #define KV8_MIN_PAGE 16        /* paged calls: rows per page, a power of two from here ... */
@@ -86,6 +89,10 @@ extern "C" {
 /* query element types */
 #define KV8_F32 0
 #define KV8_BF16 1
+
+/* rotary layouts: which elements of the rotated part form pair i */
+#define KV8_ROPE_INTERLEAVED 0 /* 2i and 2i + 1 */
+#define KV8_ROPE_HALF 1        /* i and i + rope_dim / 2 */
 
 /* -----------------------------------------------------------------------------------------------
  * kv8_encode_e4m3 -- the element encoder of the row quantizer, without scaling.
@@ -422,6 +429,88 @@ KV8_API int kv8_tree_commit(int B, const int32_t *q_start, const int32_t *lens, 
                             const int32_t *n_accept, int max_accept, int layers, uint8_t *kv8, float *kv_scale,
                             int64_t cache_rows, const int32_t *block_table, int max_pages, int page_size,
                             int32_t *new_lens, int *err_word, void *stream);
+
+/* -----------------------------------------------------------------------------------------------
+ * What stands around the attention in a layer: the projections, the rotation of the query heads, and the
+ * producer that [KV8]'s first commit speaks of, which quantizes the fresh normed / roped row.  In a layer's order:
+ * kv8_quant_blocks (hidden states) -> kv8_matmul8 (query and latent projections) -> kv8_norm_rope_rows (rows into
+ * the cache) and kv8_rope (query heads) -> mla_q_absorb8 -> an attention call -> mla_out_project8 ->
+ * kv8_quant_blocks -> kv8_matmul8 (output projection).
+ *
+ * Rotary positions.  Pair i of a rotated part (u, v: KV8_ROPE_INTERLEAVED or KV8_ROPE_HALF) at position p becomes
+ *     u' = rope_scale (u cos a - v sin a),   v' = rope_scale (u sin a + v cos a),   a = p inv_freq[i]
+ * with inv_freq [rope_dim / 2] f32 (device, finite), position [n] int32 (any value; a negative one turns back, so
+ * -p undoes p where rope_scale is 1).  The angle is reduced exactly: positions of a million lose nothing.
+ * Every scaling for long contexts is a choice of inv_freq and rope_scale.
+ *
+ * kv8_rope_freqs -- such a choice, on the host: inv_freq [rope_dim / 2] and *rope_scale are HOST memory.
+ *   f_i = theta^(-2i / rope_dim); with factor = 1 the table is f and the scale 1.  With factor > 1 the frequencies are
+ *   interpolated by parts ("YaRN: Efficient Context Window Extension of Large Language Models", NTK-by-parts): a pair that
+ *   makes more than beta_fast turns in `context` positions keeps f_i, one that makes fewer than beta_slow gets
+ *   f_i / factor, and between the two pairs (their numbers rounded outward, limited to [0, rope_dim - 1]) the share of
+ *   f_i / factor grows linearly with i; the scale is 0.1 ln(factor) + 1.
+ *   rope_dim even in [2, KV8_MAX_ROPE]; theta > 1; factor >= 1; context >= 1; 0 < beta_slow <= beta_fast.
+ * --------------------------------------------------------------------------------------------- */
+KV8_API int kv8_rope_freqs(int rope_dim, double theta, double factor, double context, double beta_fast, double beta_slow,
+                           float *inv_freq, float *rope_scale);
+
+/* kv8_rope -- rotates elements [rope_at, rope_at + rope_dim) of each head and hands the two parts out apart, as
+ * mla_q_absorb8 (the rest) and the attention calls (the rotated part) take them.
+ *   x [n][heads][width] of type x_dtype, element (r, h, e) at x[r * x_row_stride + h * x_head_stride + e]; strides in
+ *   elements, >= 0 (0 repeats).
+ *   rot [n][heads][rope_dim], rest [n][heads][width - rope_dim] (the elements before the rotated part, then those after
+ *   it) of type out_dtype, with strides of their own that keep them apart; rest may be NULL: it is not written.
+ *   In place: rot = x + rope_at with x's strides and type, rest NULL.  No other overlap.
+ *   n in [0, KV8_MAX_ROWS]; heads in [1, KV8_MAX_HEADS]; rope_dim even in [2, KV8_MAX_ROPE]; width up to KV8_MAX_WIDTH.
+ *   Pointers are aligned to their elements; where pointers, strides, rope_at and both parts' widths are multiples of 8
+ *   elements (and pointers of 16 bytes) the call is several times faster.
+ *   f32 arithmetic, one rounding to out_dtype; the rest is copied.  NaN and infinities stay in their pair. */
+KV8_API int kv8_rope(const void *x, int x_dtype, int64_t n, int heads, int width, int rope_at, int rope_dim,
+                     int64_t x_row_stride, int64_t x_head_stride, const int32_t *position, const float *inv_freq,
+                     float rope_scale, int layout, void *rot, int64_t rot_row_stride, int64_t rot_head_stride, void *rest,
+                     int64_t rest_row_stride, int64_t rest_head_stride, int out_dtype, void *stream);
+
+/* kv8_norm_rope_rows -- a projection's rows made into cache rows: of each row x [576], elements 0..511 are normed,
+ *     y_i = x_i norm_w[i] / sqrt(mean over 512 of x^2 + eps),
+ * elements 512..575 rotated, and the 576 results quantized as kv8_quant_rows does and written to cache row dst_rows[r].
+ *   x [n][576] of type x_dtype, rows x_stride elements apart (>= 576; x and the rows 16-byte aligned): the rows may be
+ *   part of a wider projection's output.  norm_w [512] f32; eps >= 0.
+ *   dst_rows [n] int64, as kv8_page_plan's slots: rows that differ from one another; one outside [0, cache_rows) is
+ *   skipped and sets KV8_ERR_INDEX (slots of -1 among them).
+ *   Between x and the quantizer all arithmetic is f32 and nothing is rounded to fewer bits.  Rows of any finite magnitude
+ *   are normed (squares that leave the f32 range are summed in f64).  A NaN or an infinity among the 512 makes their
+ *   bytes 0, one among the 64 those of its pair (0, or the largest code), as kv8_quant_rows does with them. */
+KV8_API int kv8_norm_rope_rows(const void *x, int x_dtype, int64_t n, int64_t x_stride, const float *norm_w, float eps,
+                               const int32_t *position, const float *inv_freq, float rope_scale, int layout,
+                               const int64_t *dst_rows, uint8_t *kv8, float *kv_scale, int64_t cache_rows, int *err_word,
+                               void *stream);
+
+/* kv8_quant_blocks -- rows to e4m3 with one f32 scale for each block of 128 columns: the left operand of kv8_matmul8.
+ * Every block is quantized as kv8_quant_rows quantizes a row (amax / 448 over its finite values, the same bytes).
+ *   x [n][width] of type x_dtype, rows x_stride elements apart (>= width; x and the rows 16-byte aligned).
+ *   norm_w [width] f32 (16-byte aligned) or NULL: with it, x_i is first replaced by x_i norm_w[i] / sqrt(mean(x^2) + eps),
+ *   in f32, not rounded in between; a row with a NaN or an infinity becomes zeros.
+ *   q [n][width] u8; scale: block k of row r at scale[k * scale_stride + r] (f32, scale_stride >= n), so one block's
+ *   scales of all rows lie together.  The last block is shorter where width is no multiple of 128.
+ *   width a multiple of 16 in [16, KV8_MAX_WIDTH], with a norm up to KV8_MAX_NORM_WIDTH; n in [0, KV8_MAX_ROWS]. */
+KV8_API int kv8_quant_blocks(const void *x, int x_dtype, int64_t n, int width, int64_t x_stride, const float *norm_w, float eps,
+                             uint8_t *q, float *scale, int64_t scale_stride, void *stream);
+
+/* kv8_matmul8 -- product of e4m3 rows with an fmt=8 weight ([FMT8]: one f32 scale per 128 x 128 block):
+ *     out[m][n] = sum_kb sa[kb][m] w_scale[n / 128][kb] sum_{k in block kb} e4m3(a8[m][k]) e4m3(w8[n][k])
+ *   a8 [M][K] u8, rows a_stride bytes apart (>= K, a multiple of 16); sa[kb][m] = a_scale[kb * a_scale_stride + m] as
+ *   kv8_quant_blocks writes it, or a_scale_stride = 0: one scale a row.  The latter takes the rows of a latent cache as
+ *   they lie (K = 512, a_stride = 576, a_scale = kv_scale): an expansion of cached rows through kv_b.
+ *   w8 [N][K] u8, w_scale [ceil(N/128)][ceil(K/128)] f32.  out [M][N] of type out_dtype, rows out_stride elements apart.
+ *   M in [0, KV8_MAX_ROWS]; N in [1, KV8_MAX_ROWS]; K a multiple of 16 in [16, KV8_MAX_WIDTH].  a8 and w8 16-byte
+ *   aligned; out aligned to its elements, and faster where it and its rows lie on 16 bytes.
+ *   err_word: optional (KV8_ERR_TIMEOUT).
+ * The products are exact, a block's sum is taken by the tensor cores in f32, the scaled sums are added in f32; bf16 output
+ * rounds once.  A NaN code makes the outputs of its row (of a8) or column (of w8) NaN.  A pair of scales whose product is
+ * below 2^-126 or beyond f32 counts as that product is rounded in f32. */
+KV8_API int kv8_matmul8(const uint8_t *a8, int64_t a_stride, const float *a_scale, int64_t a_scale_stride, int M, int N, int K,
+                        const uint8_t *w8, const float *w_scale, void *out, int out_dtype, int64_t out_stride, int *err_word,
+                        void *stream);
 
 /* -----------------------------------------------------------------------------------------------
  * kv8_copy -- copy `bytes` bytes from src to dst with a kernel (the SMs' loads and stores, not a
