@@ -1,4 +1,4 @@
-// elem.cuh -- f32 / bf16 values in memory, eight (16 or 32 bytes), two or one at a time, as f32 in registers.
+// elem.cuh -- f32 / bf16 values in memory, sixteen bytes or one value at a time, as f32 in registers.
 #pragma once
 
 #include "common.cuh"
@@ -25,44 +25,71 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <int V>
-__device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&v)[V]) {
-    if constexpr (V == 8) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        unpack2(w.x, v[0], v[1]);
-        unpack2(w.y, v[2], v[3]);
-        unpack2(w.z, v[4], v[5]);
-        unpack2(w.w, v[6], v[7]);
-    } else if constexpr (V == 2) {
-        unpack2(*reinterpret_cast<const uint32_t *>(p), v[0], v[1]);
-    } else {
-        v[0] = __bfloat162float(*p);
+// A run of V values as it lies in memory, so that a load in flight takes no more registers than its bytes: V values are 16
+// or 32 bytes, or one value.
+template <bool kBf16, int V>
+struct Raw {
+    static constexpr int kWords = V == 1 ? 1 : V * (kBf16 ? 2 : 4) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const typename Elem<kBf16>::T *p) {
+        if constexpr (V == 1) {
+            if constexpr (kBf16)
+                w[0] = __bfloat16_as_ushort(*p);
+            else
+                w[0] = __float_as_uint(*p);
+        } else if constexpr (kWords < 4) {
+#pragma unroll
+            for (int i = 0; i < kWords / 2; ++i) {
+                const uint2 a = reinterpret_cast<const uint2 *>(p)[i];
+                w[2 * i] = a.x, w[2 * i + 1] = a.y;
+            }
+            if constexpr (kWords % 2) w[kWords - 1] = reinterpret_cast<const uint32_t *>(p)[kWords - 1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 a = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+            }
+        }
     }
-}
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void get(float (&v)[V]) const {
+        if constexpr (V == 1) {
+            v[0] = kBf16 ? __uint_as_float(w[0] << 16) : __uint_as_float(w[0]);
+        } else if constexpr (kBf16) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) unpack2(w[i], v[2 * i], v[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i]);
+        }
+    }
+};
+
 template <int V>
 __device__ __forceinline__ void load(const float *p, float (&v)[V]) {
-    if constexpr (V == 8) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else if constexpr (V == 2) {
-        const float2 a = *reinterpret_cast<const float2 *>(p);
-        v[0] = a.x, v[1] = a.y;
-    } else {
-        v[0] = *p;
-    }
+    Raw<false, V> r;
+    r.load(p);
+    r.get(v);
 }
+
 template <int V>
 __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[V]) {
     if constexpr (V == 8)
         *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+    else if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
     else
         *p = __float2bfloat16_rn(v[0]);
 }
 template <int V>
 __device__ __forceinline__ void store(float *p, const float (&v)[V]) {
-    if constexpr (V == 8) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    if constexpr (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) reinterpret_cast<float4 *>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     } else {
         *p = v[0];
     }

@@ -54,22 +54,22 @@ __global__ void __launch_bounds__(kQThreads) quant_blocks_kernel(const void *__r
     const int kb0 = (int)(blockIdx.x - tile * col_parts) * kQCols;
     const int64_t row = tile * kQRows + warp;
     const T *x = static_cast<const T *>(xv) + row * x_stride;
-    float y[kQCols / 2][8];
+    Raw<kBf16, 8> raw[kQCols / 2];
 #pragma unroll
     for (int j = 0; j < kQCols / 2; ++j) {
         const int col = (kb0 + 2 * j) * kQBlk + 8 * lane;
-        if (row < n && col < width) {
-            load<8>(x + col, y[j]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[j][i] = 0.f;
-        }
+        if (row < n && col < width)
+            raw[j].load(x + col);
+        else
+            raw[j].zero();
     }
 #pragma unroll
     for (int j = 0; j < kQCols / 2; ++j) {
         const int col = (kb0 + 2 * j) * kQBlk + 8 * lane;
+        float y[8];
+        raw[j].get(y);
         uint2 b;
-        const float s = quant8(y[j], b);
+        const float s = quant8(y, b);
         if (row < n && col < width) *reinterpret_cast<uint2 *>(q + row * width + col) = b;
         if ((lane & 15) == 0) sc[2 * j + (lane >> 4)][warp] = s;
     }
@@ -93,17 +93,18 @@ __global__ void __launch_bounds__(kQThreads) norm_quant_blocks_kernel(const void
     const int64_t row = (int64_t)blockIdx.x * (kQThreads / kT) + (kT == 32 ? warp : 0);
     if (row >= n) return;  // (whole warps; with kT == kQThreads no block)
     const T *x = static_cast<const T *>(xv) + row * x_stride;
-    float y[kJ][8], ss = 0.f;
+    Raw<kBf16, 8> raw[kJ];
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
         const int col = 8 * (t + kT * j);
-        if (col < width) {
-            load<8>(x + col, y[j]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[j][i] = 0.f;
-        }
+        if (col < width)
+            raw[j].load(x + col);
+        else
+            raw[j].zero();
     }
+    float y[kJ][8], ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) raw[j].get(y[j]);
 #pragma unroll
     for (int j = 0; j < kJ; ++j)
 #pragma unroll

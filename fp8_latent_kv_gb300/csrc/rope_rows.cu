@@ -35,14 +35,15 @@ struct RopeArgs {
 };
 
 // A block takes some tokens and heads; a thread's item is V values of the rest, V / 2 interleaved pairs, or V pairs
-// of the half layout.  The loads of a thread's items go out together.  An item reads all it needs before it writes,
-// so the rotated part may be written over x.
+// of the half layout (V: 16 bytes of x, or one value).  The loads of a thread's items go out together, the first ones
+// before the block's cosines and sines are computed.  An item reads all it needs before it writes, so the rotated part
+// may be written over x.
 template <bool kInBf16, bool kOutBf16, bool kHalf, int V>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     using In = typename Elem<kInBf16>::T;
     using Out = typename Elem<kOutBf16>::T;
     constexpr int P = kHalf ? V : (V == 1 ? 1 : V / 2);  // pairs of a rotated item
-    constexpr int W = kHalf ? V : 2 * P;                 // its values in one place
+    constexpr bool kTwo = kHalf || V == 1;               // which lies in two places
     __shared__ float2 table[kRopeTable];
     const int half_dim = a.dim / 2;
     const int64_t block = blockIdx.x / a.n_parts;
@@ -50,79 +51,70 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     const int64_t n0 = block * a.tokens;
     const int tokens = (int)(a.n - n0 < a.tokens ? a.n - n0 : a.tokens);
     const int h0 = part * a.head_part, heads = min(a.head_part, a.heads - h0);
+    const int rest_items = a.n_rest / V, per_head = rest_items + half_dim / P, items = tokens * heads * per_head;
+    Raw<kInBf16, V> u[kRopeUnroll], v[kTwo ? kRopeUnroll : 1];
+    auto where = [&](int it, int &t, int &h, int &k) {
+        const int th = it / per_head;
+        k = it - th * per_head;
+        t = th / heads;
+        h = h0 + th - t * heads;
+    };
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int j = 0; j < kRopeUnroll; ++j) {
+            const int it = base + j * kRopeThreads;
+            if (it >= items) break;
+            int t, h, k;
+            where(it, t, h, k);
+            const In *x = static_cast<const In *>(a.x) + (n0 + t) * a.x_row + h * a.x_head;
+            const int i = (k - rest_items) * P;
+            const int e = k < rest_items ? (k * V < a.at ? k * V : k * V + a.dim) : a.at + (kHalf ? i : 2 * i);
+            u[j].load(x + e);
+            if constexpr (kTwo)
+                if (k >= rest_items) v[j].load(x + e + (kHalf ? half_dim : 1));
+        }
+    };
+    fetch(threadIdx.x);
     for (int i = threadIdx.x; i < tokens * half_dim; i += kRopeThreads) {
         const int t = i / half_dim, k = i - t * half_dim;
         table[i] = turn_cos_sin(__ldg(a.position + n0 + t), turn_of(__ldg(a.inv_freq + k)), a.scale);
     }
-    const int rest_items = a.n_rest / V, per_head = rest_items + half_dim / P, items = tokens * heads * per_head;
     __syncthreads();
     for (int base = threadIdx.x; base < items; base += kRopeThreads * kRopeUnroll) {
-        float u[kRopeUnroll][W], v[kRopeUnroll][kHalf ? W : 1];
+        if (base != threadIdx.x) fetch(base);
 #pragma unroll
         for (int j = 0; j < kRopeUnroll; ++j) {
             const int it = base + j * kRopeThreads;
             if (it >= items) break;
-            const int th = it / per_head, k = it - th * per_head, t = th / heads, h = h0 + th - t * heads;
-            const In *x = static_cast<const In *>(a.x) + (n0 + t) * a.x_row + h * a.x_head;
+            int t, h, k;
+            where(it, t, h, k);
+            float x[V], y[V];
+            u[j].get(x);
             if (k < rest_items) {
-                float r[V];
-                const int e = k * V;
-                load<V>(x + (e < a.at ? e : e + a.dim), r);
-#pragma unroll
-                for (int q = 0; q < V; ++q) u[j][q] = r[q];
-            } else if constexpr (kHalf) {
-                const int i = (k - rest_items) * P;
-                load<W>(x + a.at + i, u[j]);
-                load<W>(x + a.at + half_dim + i, v[j]);
-            } else if constexpr (V == 1) {  // (the two values may not be aligned as a pair)
-                const In *p = x + a.at + 2 * (k - rest_items);
-                float r[1];
-                load<1>(p, r);
-                u[j][0] = r[0];
-                load<1>(p + 1, r);
-                u[j][1] = r[0];
-            } else {
-                load<W>(x + a.at + (k - rest_items) * W, u[j]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kRopeUnroll; ++j) {
-            const int it = base + j * kRopeThreads;
-            if (it >= items) break;
-            const int th = it / per_head, k = it - th * per_head, t = th / heads, h = h0 + th - t * heads;
-            if (k < rest_items) {
-                float r[V];
-#pragma unroll
-                for (int q = 0; q < V; ++q) r[q] = u[j][q];
-                store<V>(static_cast<Out *>(a.rest) + (n0 + t) * a.rest_row + h * a.rest_head + k * V, r);
+                store<V>(static_cast<Out *>(a.rest) + (n0 + t) * a.rest_row + h * a.rest_head + k * V, x);
                 continue;
             }
             const int i = (k - rest_items) * P;
-            Out *o = static_cast<Out *>(a.rot) + (n0 + t) * a.rot_row + h * a.rot_head;
+            Out *o = static_cast<Out *>(a.rot) + (n0 + t) * a.rot_row + h * a.rot_head + (kHalf ? i : 2 * i);
             const float2 *cs = table + t * half_dim + i;
-            if constexpr (kHalf) {
-                float p[W], q[W];
+            if constexpr (kTwo) {
+                v[j].get(y);
 #pragma unroll
-                for (int m = 0; m < P; ++m) {
-                    p[m] = u[j][m] * cs[m].x - v[j][m] * cs[m].y;
-                    q[m] = u[j][m] * cs[m].y + v[j][m] * cs[m].x;
+                for (int m = 0; m < V; ++m) {
+                    const float p = x[m], q = y[m];
+                    x[m] = p * cs[m].x - q * cs[m].y;
+                    y[m] = p * cs[m].y + q * cs[m].x;
                 }
-                store<W>(o + i, p);
-                store<W>(o + half_dim + i, q);
+                store<V>(o, x);
+                store<V>(o + (kHalf ? half_dim : 1), y);
             } else {
-                float p[W];
 #pragma unroll
                 for (int m = 0; m < P; ++m) {
-                    p[2 * m] = u[j][2 * m] * cs[m].x - u[j][2 * m + 1] * cs[m].y;
-                    p[2 * m + 1] = u[j][2 * m] * cs[m].y + u[j][2 * m + 1] * cs[m].x;
+                    const float p = x[2 * m], q = x[2 * m + 1];
+                    x[2 * m] = p * cs[m].x - q * cs[m].y;
+                    x[2 * m + 1] = p * cs[m].y + q * cs[m].x;
                 }
-                if constexpr (V == 1) {
-                    const float p0[1] = {p[0]}, p1[1] = {p[1]};
-                    store<1>(o + 2 * i, p0);
-                    store<1>(o + 2 * i + 1, p1);
-                } else {
-                    store<W>(o + 2 * i, p);
-                }
+                store<V>(o, x);
             }
         }
     }
@@ -131,7 +123,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 template <bool kInBf16, bool kOutBf16, bool kHalf>
 cudaError_t rope_go(const RopeArgs &a, bool wide, int64_t blocks, cudaStream_t st) {
     if (wide)
-        rope_kernel<kInBf16, kOutBf16, kHalf, 8><<<(unsigned)blocks, kRopeThreads, 0, st>>>(a);
+        rope_kernel<kInBf16, kOutBf16, kHalf, kInBf16 ? 8 : 4><<<(unsigned)blocks, kRopeThreads, 0, st>>>(a);
     else
         rope_kernel<kInBf16, kOutBf16, kHalf, 1><<<(unsigned)blocks, kRopeThreads, 0, st>>>(a);
     return cudaGetLastError();
@@ -161,18 +153,34 @@ __global__ void __launch_bounds__(kRowsThreads) norm_rope_rows_kernel(
     } else {
         turn[0] = turn_of(__ldg(inv_freq + lane));
     }
-    for (int64_t r = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5); r < n; r += warps) {
-        const int64_t row = __ldg(dst + r);
+    // a row's values, position and place, asked for while the row before it is worked on
+    Raw<kBf16, 8> raw[2];
+    Raw<kBf16, 2> raw_k;
+    int32_t next_pos;
+    int64_t next_row;
+    auto fetch = [&](int64_t r) {
+        if (r >= n) return;
+        const T *xr = x + r * x_stride;
+        raw[0].load(xr + 8 * lane);
+        raw[1].load(xr + 256 + 8 * lane);
+        raw_k.load(xr + kKL + 2 * lane);
+        next_pos = __ldg(position + r);
+        next_row = __ldg(dst + r);
+    };
+    int64_t r = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
+    fetch(r);
+    for (; r < n; r += warps) {
+        float y[2][8], k[2];
+        raw[0].get(y[0]);
+        raw[1].get(y[1]);
+        raw_k.get(k);
+        const int32_t pos = next_pos;
+        const int64_t row = next_row;
+        fetch(r + warps);
         if (row < 0 || row >= cache_rows) {
             if (lane == 0 && err_word) atomicOr(err_word, (int)KV8_ERR_INDEX);
             continue;
         }
-        const T *xr = x + r * x_stride;
-        float y[2][8], k[2];
-        load<8>(xr + 8 * lane, y[0]);
-        load<8>(xr + 256 + 8 * lane, y[1]);
-        load<2>(xr + kKL + 2 * lane, k);
-        const int32_t pos = __ldg(position + r);
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 16; ++j) ss = fmaf(y[j >> 3][j & 7], y[j >> 3][j & 7], ss);
@@ -236,13 +244,13 @@ cudaError_t launch_rope(const void *x, int x_bf16, int64_t n, int heads, int wid
     a.position = position, a.inv_freq = inv_freq, a.scale = scale;
     a.n = n, a.heads = heads, a.at = rope_at, a.dim = rope_dim;
     a.n_rest = rest ? width - rope_dim : 0;
-    // eight values at a time where every run of eight lies on 16 bytes
+    // 16 bytes of x at a time where every run of eight values lies on 16 bytes
     const int64_t odd = x_row | x_head | rot_row | rot_head | (rest ? rest_row | rest_head : 0) | rope_at | (width - rope_dim) |
                         (half_layout ? rope_dim / 2 : rope_dim);
     const uintptr_t at = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(rot) | reinterpret_cast<uintptr_t>(rest);
     const bool wide = odd % 8 == 0 && at % 16 == 0;
-    const int V = wide ? 8 : 1;
-    const int per_head = a.n_rest / V + (half_layout ? rope_dim / 2 / V : rope_dim / (wide ? 8 : 2));
+    const int V = wide ? (x_bf16 ? 8 : 4) : 1;
+    const int per_head = a.n_rest / V + (half_layout ? rope_dim / 2 / V : rope_dim / (wide ? V : 2));
     // a block's items: four a thread, or one where that many blocks would leave SMs without work
     const int64_t all = n * heads * (int64_t)per_head;
     const int target = all >= (int64_t)device_sm_count() * kRopeThreads * kRopeUnroll ? kRopeThreads * kRopeUnroll : kRopeThreads;
@@ -271,7 +279,7 @@ cudaError_t launch_norm_rope_rows(const void *x, int x_bf16, int64_t n, int64_t 
                                   const int64_t *dst, uint8_t *kv8, float *kv_scale, int64_t cache_rows, int *err_word,
                                   cudaStream_t st) {
     int64_t blocks = (n + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
-    const int64_t cap = (int64_t)device_sm_count() * 8;
+    const int64_t cap = (int64_t)device_sm_count() * 4;
     if (blocks > cap) blocks = cap;
     auto go = [&](auto kernel) {
         kernel<<<(unsigned)blocks, kRowsThreads, 0, st>>>(x, n, x_stride, norm_w, eps, position, inv_freq, rope_scale, dst,
