@@ -25,7 +25,9 @@ using namespace sm100;
 
 constexpr int kMmBlk = KV8_KVB_BLOCK;  // K per scale block: 128 e4m3 bytes, one 128-byte swizzled row
 constexpr int kMmRows = 128;           // MMA M
-constexpr int kFacBlocks = 32;         // K blocks whose column factors stand in shared memory at a time (kSwap)
+constexpr int kScaleBlocks = 4, kScaleSlots = 4;  // K blocks whose scales travel together, and slots of them
+constexpr int kFirst = 4;              // the first warp that adds; warps 0 to 2 bring operands, issue products, bring scales
+constexpr int kRegsLoad = 40, kRegsAdd = 232;  // registers a thread of a pair's twelve warps: 4 x 40 + 8 x 232 = 12 x 168
 constexpr int kGroupTiles = 16;        // row tiles that are walked together, for the L2's sake
 
 struct MmArgs {
@@ -41,19 +43,25 @@ struct MmArgs {
     int *err_word;
 };
 
+// kNT: rows of the columns' operand.  With kNT = 256 two blocks are a pair: MMAs of 256 rows, half of both operands in each
+// block.
 template <bool kSwap, int kNT, int kStages>
 struct MmShape {
+    static constexpr bool kPair = kNT == 256;
     static constexpr int kEpi = kSwap ? 4 : 8;                 // warps that scale and add
-    static constexpr int kThreads = 64 + 32 * kEpi;
-    static constexpr int kCols = kSwap ? kNT : kNT / 2;        // accumulator columns of a thread
-    static constexpr int kAcc = kNT >= 256 ? 2 : 4;            // TMEM accumulators in turn
-    static constexpr uint32_t kTmem = kNT * kAcc < 32 ? 32 : kNT * kAcc;
-    static constexpr uint32_t kStage = (kMmRows + kNT) * 128;
-    static constexpr uint32_t kStaging = kSwap ? 0 : kEpi * 4096;
-    static constexpr uint32_t kFac = kSwap ? kFacBlocks * kNT * 4 : 0;
+    static constexpr int kThreads = 32 * (kFirst + kEpi);
+    static constexpr int kCols = kNT / (kEpi / 4);             // accumulator columns of a thread
+    static constexpr int kLoad = kPair ? kNT / 2 : kNT;        // rows of the columns' operand that a block loads
+    static constexpr int kChunk = 16;                          // of which so many are loaded at a time
+    static constexpr int kAcc = kPair ? 2 : 4;                 // TMEM accumulators in turn
+    static constexpr uint32_t kTmem = kNT * kAcc;
+    static constexpr uint32_t kStage = (kMmRows + kLoad) * 128;
+    static constexpr uint32_t kStaging = kSwap ? 0 : kEpi * 2 * 4096;
+    static constexpr int kScales = (kSwap ? kNT : kMmRows) + 4;  // floats of a K block: those of a8's rows, then of w8's blocks
+    static constexpr uint32_t kFac = kScaleSlots * kScaleBlocks * kScales * 4;
     static constexpr uint32_t kBytes = 1024 + kStages * kStage + kStaging + kFac + 256;
     static_assert(kBytes <= 227 * 1024, "shared memory of a block");
-    static_assert(kNT * kMmRows * 4 <= kStages * kStage || kNT == 256, "a tile's sums fit the stages");
+    static_assert(kNT * kMmRows * 4 <= kStages * kStage, "a tile's sums fit the stages");
 };
 
 template <bool kSwap, int kNT, int kStages, int kBlocks, bool kBf16, bool kSplit>
@@ -62,22 +70,27 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                    const __grid_constant__ CUtensorMap map_out, const MmArgs a) {
     using S = MmShape<kSwap, kNT, kStages>;
     using Out = typename Elem<kBf16>::T;
+    constexpr bool kPair = S::kPair;
+    static_assert(!(kPair && kSplit), "a cluster is a pair or a split");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *staging = smem + kStages * S::kStage;
     float *fac = reinterpret_cast<float *>(staging + S::kStaging);
     uint64_t *bars = reinterpret_cast<uint64_t *>(staging + S::kStaging + S::kFac);
     uint64_t *full = bars, *empty = bars + kStages, *t_full = bars + 2 * kStages, *t_empty = t_full + S::kAcc, *drain = t_empty + S::kAcc;
-    static_assert((2 * kStages + 2 * S::kAcc + 1) * 8 + 8 <= 256, "barriers");
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *s_full = drain + 1, *s_empty = s_full + kScaleSlots;
+    static_assert((2 * kStages + 2 * S::kAcc + 1 + 2 * kScaleSlots) * 8 + 8 <= 256, "barriers");
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_empty + kScaleSlots);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = kSplit ? a.split : 1;
-    const int rank = kSplit ? (int)cluster_rank() : 0;
-    const int first = kSplit ? (int)blockIdx.x / split : (int)blockIdx.x, step = kSplit ? (int)gridDim.x / split : (int)gridDim.x;
+    const int rank = kSplit || kPair ? (int)cluster_rank() : 0;
+    const int cluster = kPair ? 2 : split, first = (int)blockIdx.x / cluster, step = (int)gridDim.x / cluster;
+    constexpr int kRows = kPair ? 2 * kMmRows : kMmRows;  // rows of a tile
+    const int row0 = kPair ? rank * kMmRows : 0;          // this block's among them
     const int tiles = a.p_tiles * a.q_tiles;
-    const int kb0 = (int)((int64_t)a.kb * rank / split), kb1 = (int)((int64_t)a.kb * (rank + 1) / split);
+    const int kb0 = kSplit ? (int)((int64_t)a.kb * rank / split) : 0, kb1 = kSplit ? (int)((int64_t)a.kb * (rank + 1) / split) : a.kb;
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -86,21 +99,29 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         }
         for (int i = 0; i < S::kAcc; ++i) {
             mbar_init(t_full + i, 1);
-            mbar_init(t_empty + i, S::kEpi);
+            mbar_init(t_empty + i, S::kEpi * (kPair ? 2 : 1));
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(s_full + i, 32);
+            mbar_init(s_empty + i, S::kEpi);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 0) {
-        tmem_alloc(tmem_slot, S::kTmem);
-        tmem_relinquish();
+        if constexpr (kPair) {
+            tmem_alloc_pair(tmem_slot, S::kTmem);
+        } else {
+            tmem_alloc(tmem_slot, S::kTmem);
+            tmem_relinquish();
+        }
     }
     tc_fence_before_sync();
     __syncthreads();
+    if constexpr (kPair) cluster_sync();  // the other block's barriers stand
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-
     // tile -> (tile of the MMA rows' operand, tile of the columns'): kGroupTiles row tiles at a time, the columns' outside
     auto place = [&](int tile, int &tp, int &tq) {
         const int per = kGroupTiles * a.q_tiles, g = tile / per, r = tile - g * per;
@@ -111,64 +132,124 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
 
     if (warp == 0) {
         // ---- loads
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int tile = first; tile < tiles && ok; tile += step) {
-                int tp, tq;
-                place(tile, tp, tq);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (it >= kStages && !bar_wait(empty + s, (it / kStages - 1) & 1, abort_flag, a.err_word)) {
-                        ok = false;
-                        break;
+        if constexpr (kPair) fewer_registers<kRegsLoad>();
+        int it = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+            int tp, tq;
+            place(tile, tp, tq);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % kStages;
+                if (it >= kStages) ok = __all_sync(0xffffffffu, bar_wait_inline(empty + s, (it / kStages - 1) & 1, abort_flag, a.err_word));
+                if (!ok) break;
+                uint8_t *p = smem + s * S::kStage;
+                if (elect_one()) {
+                    if constexpr (kPair) {  // both blocks' bytes count on block 0's barrier
+                        const uint32_t bar = of_rank(full + s, 0);
+                        if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * S::kStage);
+                        tma_load_2d_pair(p, &map_p, kb * kMmBlk, tp * kRows + row0, bar);
+                        tma_load_2d_pair(p + kMmRows * 128, &map_q, kb * kMmBlk, tq * kNT + rank * S::kLoad, bar);
+                    } else {
+                        mbar_arrive_expect_tx(full + s, S::kStage);
+                        tma_load_2d(p, &map_p, kb * kMmBlk, tp * kRows, full + s);
+                        tma_load_2d(p + kMmRows * 128, &map_q, kb * kMmBlk, tq * kNT, full + s);
                     }
-                    uint8_t *p = smem + s * S::kStage;
-                    mbar_arrive_expect_tx(full + s, S::kStage);
-                    tma_load_2d(p, &map_p, kb * kMmBlk, tp * kMmRows, full + s);
-                    tma_load_2d(p + kMmRows * 128, &map_q, kb * kMmBlk, tq * kNT, full + s);
                 }
+                __syncwarp();
             }
-            if (!ok)  // the copies in flight end before the block does
-                for (int i = it < kStages ? 0 : it - kStages; i < it; ++i)
-                    (void)bar_wait(full + i % kStages, (i / kStages) & 1, nullptr, nullptr, 1ll << 28);
         }
+        if (!ok && (!kPair || rank == 0))  // the copies in flight end before the block does
+            for (int i = it < kStages ? 0 : it - kStages; i < it; ++i)
+                (void)bar_wait_inline(full + i % kStages, (i / kStages) & 1, nullptr, nullptr, 1ll << 28);
         __syncwarp();
     } else if (warp == 1) {
         // ---- products
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(kMmRows, kNT, false, false);
+        if constexpr (kPair) fewer_registers<kRegsLoad>();
+        if (!kPair || rank == 0) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kNT, false, false);
+            const uint64_t desc0 = smem_desc(smem_u32(smem), 0, 1024, kSw128);
+            const uint32_t d0 = __shfl_sync(0xffffffffu, tmem, 0);
             int it = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % kStages, c = it % S::kAcc;
-                    if (it >= S::kAcc && !bar_wait(t_empty + c, (it / S::kAcc - 1) & 1, abort_flag, a.err_word)) ok = false;
-                    if (ok && !bar_wait(full + s, (it / kStages) & 1, abort_flag, a.err_word)) ok = false;
+                    ok = bar_wait_inline(full + s, (it / kStages) & 1, abort_flag, a.err_word);
+                    if (it >= S::kAcc && ok) ok = bar_wait_inline(t_empty + c, (it / S::kAcc - 1) & 1, abort_flag, a.err_word);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint32_t p = smem_u32(smem + s * S::kStage), d = tmem + (uint32_t)(c * kNT);
+                    // (a descriptor's address counts 16 bytes; 32 bytes of K a step)
+                    const uint64_t dp = desc0 + s * (S::kStage >> 4), dq = dp + (kMmRows * 128 >> 4);
+                    const uint32_t d = d0 + (uint32_t)(c * kNT);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f8f6f4(d, smem_desc(p + kk * 32, 0, 1024, kSw128), smem_desc(p + kMmRows * 128 + kk * 32, 0, 1024, kSw128),
-                                   idesc, kk > 0);
-                    mma_commit(empty + s);
-                    mma_commit(t_full + c);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if constexpr (kPair)
+                                mma_f8f6f4_pair(d, dp + 2 * kk, dq + 2 * kk, idesc, kk > 0);
+                            else
+                                mma_f8f6f4(d, dp + 2 * kk, dq + 2 * kk, idesc, kk > 0);
+                        }
+                        if constexpr (kPair) {
+                            mma_commit_pair(t_full + c);
+                            mma_commit_pair(empty + s);
+                        } else {
+                            mma_commit(t_full + c);
+                            mma_commit(empty + s);
+                        }
+                    }
+                    __syncwarp();
                 }
             }
             if (!ok) {
-                mma_commit(drain);
-                (void)bar_wait(drain, 0, nullptr, nullptr, 1ll << 28);
+                if (elect_one()) {
+                    if constexpr (kPair)
+                        mma_commit_pair(drain);
+                    else
+                        mma_commit(drain);
+                }
+                __syncwarp();
+                (void)bar_wait_inline(drain, 0, nullptr, nullptr, 1ll << 28);
             }
         }
         __syncwarp();
-    } else {
-        // ---- scales and sums
-        const int quad = warp & 3, half = (warp - 2) >> 2, epi_tid = tid - 64;  // (a warp reads TMEM lanes 32 (warp % 4) ..)
+    } else if (warp == 2) {
+        // ---- scales, kScaleBlocks K blocks at a time.  (Loaded by the warps that add, they would hold up each of their arrivals
+        // until they are there: 8192 x 4096 x 16384 took 449 us so, 356 without any scales.)
+        if constexpr (kPair) fewer_registers<kRegsLoad>();
+        // a8's rows (kSwap: the tile's columns) and w8's blocks of 128; past the ends the last one's are repeated, for sums that are not written
+        int g = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+            int tp, tq;
+            place(tile, tp, tq);
+            const int m0 = kSwap ? tq * kNT : tp * kRows + row0, n0 = kSwap ? tp * kMmRows : tq * kNT;
+            constexpr int kMs = kSwap ? kNT : kMmRows, kNs = kPair ? 2 : 1;
+            for (int k = kb0; k < kb1; k += kScaleBlocks, ++g) {
+                const int s = g % kScaleSlots;
+                if (g >= kScaleSlots) ok = __all_sync(0xffffffffu, bar_wait_inline(s_empty + s, (g / kScaleSlots - 1) & 1, abort_flag, a.err_word));
+                if (!ok) break;
+                for (int u = 0; u < kScaleBlocks && k + u < kb1; ++u) {
+                    float *to = fac + (s * kScaleBlocks + u) * S::kScales;
+                    const float *from = a.a_scale + (k + u) * a.a_scale_stride;
+#pragma unroll
+                    for (int i = 0; i < kMs; i += 32)
+                        if (i + lane < kMs) cp_async_4(to + i + lane, from + min(m0 + i + lane, a.M - 1));
+                    if (lane < kNs) cp_async_4(to + kMs + lane, a.w_scale + (int64_t)min(n0 / kMmBlk + lane, (a.N - 1) / kMmBlk) * a.kb + k + u);
+                }
+                cp_async_mbar_arrive(s_full + s);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");  // (none is in flight when the block ends)
+        __syncwarp();
+    } else if (warp >= kFirst) {
+        // ---- sums
+        if constexpr (kPair) more_registers<kRegsAdd>();
+        const int quad = warp & 3, half = (warp - kFirst) >> 2;  // (a warp reads TMEM lanes 32 (warp % 4) ..)
         const int row = quad * 32 + lane, col0 = half * S::kCols;
         const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
         Out *out = static_cast<Out *>(a.out);
-        int it = 0;
+        int it = 0, g = 0, parts = 0;  // K blocks, slots of scales, staging tiles
         bool ok = true;
         for (int tile = first; tile < tiles; tile += step) {
             int tp, tq;
@@ -176,65 +257,61 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
             uint64_t acc[S::kCols / 2];
 #pragma unroll
             for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0;
-            // adds one K block: acc += D * factor, the loads one ahead of the sums
+            // adds one K block: acc += D * factor
             auto add_block = [&](auto factor) {
                 const int c = it % S::kAcc;
-                if (ok) ok = bar_wait(t_full + c, (it / S::kAcc) & 1, abort_flag, a.err_word);
+                if (ok) ok = bar_wait_inline(t_full + c, (it / S::kAcc) & 1, abort_flag, a.err_word);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 tc_fence_after_sync();
                 const uint32_t d = tmem + lane_addr + (uint32_t)(c * kNT + col0);
-                uint32_t v[2][16];
-                tmem_ld_32x32b_x16(d, v[0]);
 #pragma unroll
-                for (int j = 0; j < S::kCols / 16; ++j) {
-                    tmem_wait_ld(v[j & 1]);
-                    if (j + 1 < S::kCols / 16) {
-                        tmem_ld_32x32b_x16(d + 16 * (j + 1), v[(j + 1) & 1]);
-                    } else {
+                for (int j = 0; j < S::kCols; j += S::kChunk) {
+                    uint32_t v[S::kChunk / 16][16];
+#pragma unroll
+                    for (int i = 0; i < S::kChunk / 16; ++i) tmem_ld_32x32b_x16(d + j + 16 * i, v[i]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < S::kChunk / 16; ++i) tmem_loaded(v[i]);
+                    if (j + S::kChunk == S::kCols) {
                         tc_fence_before_sync();
-                        if (lane == 0) mbar_arrive(t_empty + c);
+                        if (lane == 0) {
+                            if constexpr (kPair)
+                                mbar_arrive_cluster_relaxed(of_rank(t_empty + c, 0));
+                            else
+                                mbar_arrive(t_empty + c);
+                        }
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        acc[8 * j + i] = f2_fma(f2_pack(__uint_as_float(v[j & 1][2 * i]), __uint_as_float(v[j & 1][2 * i + 1])),
-                                                factor(8 * j + i), acc[8 * j + i]);
+                    for (int i = 0; i < S::kChunk / 2; ++i)
+                        acc[j / 2 + i] = f2_fma(f2_pack(__uint_as_float(v[i / 8][2 * (i % 8)]), __uint_as_float(v[i / 8][2 * (i % 8) + 1])),
+                                                factor(j / 2 + i), acc[j / 2 + i]);
                 }
                 ++it;
             };
-            if constexpr (kSwap) {
-                for (int k0 = kb0; k0 < kb1; k0 += kFacBlocks) {
-                    const int nk = min(kFacBlocks, kb1 - k0);
-                    named_sync(1, 32 * S::kEpi);
-                    for (int i = epi_tid; i < nk * kNT; i += 32 * S::kEpi) {
-                        const int k = i / kNT, m = tq * kNT + i - k * kNT;
-                        fac[i] = m < a.M ? __ldg(a.a_scale + (k0 + k) * a.a_scale_stride + m) * __ldg(a.w_scale + (int64_t)tp * a.kb + k0 + k) : 0.f;
+            for (int k = kb0; k < kb1; k += kScaleBlocks, ++g) {
+                const int s = g % kScaleSlots;
+                const float *sc = fac + s * kScaleBlocks * S::kScales;
+                if (ok) ok = bar_wait_inline(s_full + s, (g / kScaleSlots) & 1, abort_flag, a.err_word);
+                ok = __all_sync(0xffffffffu, ok);
+                if constexpr (kSwap) {
+                    for (int u = 0; u < kScaleBlocks && k + u < kb1; ++u) {
+                        const uint64_t *f = reinterpret_cast<const uint64_t *>(sc + u * S::kScales);
+                        const uint64_t w = f2_pack(sc[u * S::kScales + kNT], sc[u * S::kScales + kNT]);
+                        add_block([&](int i) { return f2_mul(f[i], w); });
                     }
-                    named_sync(1, 32 * S::kEpi);
-                    for (int k = 0; k < nk; ++k) {
-                        const uint64_t *f = reinterpret_cast<const uint64_t *>(fac + k * kNT);
-                        add_block([&](int i) { return f[i]; });
-                    }
-                }
-            } else {
-                const int m = tp * kMmRows + row, nb = (tq * kNT + col0) / kMmBlk;
-                const float *sa = a.a_scale + m, *sw = a.w_scale + (int64_t)nb * a.kb;
-                const bool have = m < a.M && nb * kMmBlk < a.N;
-                float fa[4], fw[4];  // the factors of the next four blocks, on their way
-                auto fetch = [&](int u, int kb) {
-                    const bool h = have && kb < kb1;
-                    fa[u] = h ? __ldg(sa + kb * a.a_scale_stride) : 0.f;
-                    fw[u] = h ? __ldg(sw + kb) : 0.f;
-                };
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty + s);
+                } else {
+                    float f[kScaleBlocks];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) fetch(u, kb0 + u);
-                for (int k = kb0; k < kb1; k += 4) {
+                    for (int u = 0; u < kScaleBlocks; ++u) f[u] = sc[u * S::kScales + row] * sc[u * S::kScales + kMmRows + col0 / kMmBlk];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty + s);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
+                    for (int u = 0; u < kScaleBlocks; ++u) {
                         if (k + u < kb1) {
-                            const float f = fa[u] * fw[u];
-                            const uint64_t ff = f2_pack(f, f);
-                            fetch(u, k + u + 4);
+                            const uint64_t ff = f2_pack(f[u], f[u]);
                             add_block([&](int) { return ff; });
                         }
                     }
@@ -262,14 +339,14 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                     if (m < a.M && n < a.N) store<1>(out + m * a.out_stride + n, r);
                 }
             } else {
-                // 32 rows x 128 bytes at a time through a swizzled staging tile of the warp's own
+                // 32 rows x 128 bytes at a time through two swizzled staging tiles of the warp's own, in turn
                 constexpr int kPart = kBf16 ? 64 : 32;
-                uint8_t *st = staging + (warp - 2) * 4096;
-                const int m0 = tp * kMmRows + quad * 32;
+                const int m0 = tp * kRows + row0 + quad * 32;
 #pragma unroll
                 for (int c = 0; c < S::kCols; c += kPart) {
                     const int n0 = tq * kNT + col0 + c;
-                    if (lane == 0) bulk_wait_read();
+                    uint8_t *st = staging + ((warp - kFirst) * 2 + (parts++ & 1)) * 4096;
+                    if (lane == 0) bulk_wait_read<1>();
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -290,9 +367,9 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                     if (a.tma_out) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0 && m0 < a.M && n0 < a.N) {
-                            tma_store_2d(&map_out, st, n0, m0);
-                            bulk_commit();
+                        if (lane == 0) {
+                            if (m0 < a.M && n0 < a.N) tma_store_2d(&map_out, st, n0, m0);
+                            bulk_commit();  // (an empty group where nothing is stored: the count of groups goes by the parts)
                         }
                     } else {
                         __syncwarp();
@@ -310,17 +387,20 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
             __syncwarp();
         }
     }
+    if constexpr (kPair) {
+        if (warp == 3) fewer_registers<kRegsLoad>();
+    }
     if constexpr (kSplit) {
         __syncthreads();
         cluster_sync();
-        if (warp >= 2 && *(volatile int *)abort_flag == 0) {
+        if (warp >= kFirst && *(volatile int *)abort_flag == 0) {
             int tp, tq;
             place(first, tp, tq);
             const uint32_t red = smem_u32(smem);
             Out *out = static_cast<Out *>(a.out);
             const int per = kNT / split, c0 = rank * per;  // this block's columns of the tile
             if constexpr (kSwap) {
-                for (int i = tid - 64; i < per * kMmRows; i += 32 * S::kEpi) {
+                for (int i = tid - 32 * kFirst; i < per * kMmRows; i += 32 * S::kEpi) {
                     const int c = c0 + i / kMmRows, r = i % kMmRows;
                     float v[1] = {0.f};
                     for (int b = 0; b < split; ++b) v[0] += cluster_load(red + (c * kMmRows + r) * 4, b);
@@ -328,7 +408,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                     if (m < a.M && n < a.N) store<1>(out + m * a.out_stride + n, v);
                 }
             } else {
-                for (int i = tid - 64; i < per / 8 * kMmRows; i += 32 * S::kEpi) {
+                for (int i = tid - 32 * kFirst; i < per / 8 * kMmRows; i += 32 * S::kEpi) {
                     const int c = c0 + i / kMmRows * 8, r = i % kMmRows;
                     float v[8];
 #pragma unroll
@@ -356,7 +436,13 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, S::kTmem);
+    if constexpr (kPair) cluster_sync();  // neither block leaves while the other's copies, products or arrivals may reach it
+    if (warp == 0) {
+        if constexpr (kPair)
+            tmem_dealloc_pair(tmem, S::kTmem);
+        else
+            tmem_dealloc(tmem, S::kTmem);
+    }
 }
 
 bool map_bytes(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const uint8_t *p, int K, int64_t rows, int64_t stride, int box) {
@@ -383,7 +469,7 @@ cudaError_t mm_launch(MmCall c, int blocks) {
     alignas(64) CUtensorMap map_a, map_w, map_out;
     const int w = kBf16 ? 2 : 4;
     if (!map_bytes(encode, &map_a, c.a8, c.K, c.a.M, c.a_stride, kSwap ? kNT : kMmRows) ||
-        !map_bytes(encode, &map_w, c.w8, c.K, c.a.N, c.K, kSwap ? kMmRows : kNT))
+        !map_bytes(encode, &map_w, c.w8, c.K, c.a.N, c.K, kSwap ? kMmRows : S::kLoad))
         return cudaErrorInvalidValue;
     map_out = map_a;  // (not read where out is not written by tensor stores)
     c.a.tma_out = reinterpret_cast<uintptr_t>(c.a.out) % 16 == 0 && c.a.out_stride * w % 16 == 0;
@@ -404,9 +490,9 @@ cudaError_t mm_launch(MmCall c, int blocks) {
     cfg.dynamicSmemBytes = S::kBytes;
     cfg.stream = c.st;
     cudaLaunchAttribute attr[1];
-    if (kSplit) {
+    if (kSplit || S::kPair) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)c.a.split;
+        attr[0].val.clusterDim.x = S::kPair ? 2u : (unsigned)c.a.split;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -444,22 +530,21 @@ cudaError_t launch_matmul8(const uint8_t *a8, int64_t a_stride, const float *a_s
         if (nt == 32) return mm_typed<true, 32, 5, 2, true>(c, blocks);
         return mm_typed<true, 64, 4, 2, true>(c, blocks);
     }
-    c.a.p_tiles = tiles_of(M, kMmRows);
-    const int wide = c.a.p_tiles * tiles_of(N, 256), narrow = c.a.p_tiles * tiles_of(N, 128);
+    const int rows = tiles_of(M, kMmRows), narrow = rows * tiles_of(N, 128), pairs = tiles_of(M, 256) * tiles_of(N, 256);
     if (narrow * 2 <= sms && c.a.kb >= 4) {
-        c.a.q_tiles = tiles_of(N, 128);
+        c.a.p_tiles = rows, c.a.q_tiles = tiles_of(N, 128);
         c.a.split = 1;
         while (c.a.split < 8 && narrow * c.a.split * 2 <= sms && c.a.kb >= c.a.split * 4) c.a.split *= 2;
-        return mm_typed<false, 128, 5, 1, true>(c, narrow * c.a.split);
+        return mm_typed<false, 128, 4, 1, true>(c, narrow * c.a.split);
     }
     c.a.split = 1;
     // in units of a 128 x 128 tile's time: rounds of the persistent blocks
-    if (2 * tiles_of(wide, sms) <= tiles_of(narrow, sms)) {
-        c.a.q_tiles = tiles_of(N, 256);
-        return mm_typed<false, 256, 4, 1, false>(c, wide < sms ? wide : sms);
+    if (2 * tiles_of(pairs, sms / 2) <= tiles_of(narrow, sms)) {
+        c.a.p_tiles = tiles_of(M, 256), c.a.q_tiles = tiles_of(N, 256);
+        return mm_typed<false, 256, 4, 1, false>(c, 2 * (pairs < sms / 2 ? pairs : sms / 2));
     }
-    c.a.q_tiles = tiles_of(N, 128);
-    return mm_typed<false, 128, 5, 1, false>(c, narrow < sms ? narrow : sms);
+    c.a.p_tiles = rows, c.a.q_tiles = tiles_of(N, 128);
+    return mm_typed<false, 128, 4, 1, false>(c, narrow < sms ? narrow : sms);
 }
 
 }  // namespace kv8
