@@ -11,9 +11,9 @@
 //     a warp.  Persistent blocks, one an SM.
 //   few rows (kSwap = true): MMA rows are 128 rows of w8, columns up to kNT = 16 / 32 / 64 rows of a8: the weight is read
 //     once, whatever the number of rows, and no MMA row is idle.  The columns' factors sa sw stand in shared memory.
-// Where the tiles are fewer than the SMs, a cluster of 2, 4 or 8 blocks shares a tile along K; each block adds the others'
-// sums for its part of the tile through distributed shared memory, in the order of their ranks (the result does not depend
-// on timing, and no workspace is needed).
+// Where the tiles are fewer than the SMs, a cluster of up to 8 blocks shares a tile along K: each block owns some columns of
+// the tile, the others store their sums for them into its shared memory, and it adds them in the order of their ranks (the
+// result does not depend on timing, and no workspace is needed).
 #include "elem.cuh"
 #include "internal.h"
 #include "sm100_more.cuh"
@@ -48,21 +48,42 @@ struct MmArgs {
 template <bool kSwap, int kNT, int kStages>
 struct MmShape {
     static constexpr bool kPair = kNT == 256;
-    static constexpr int kEpi = kSwap ? 4 : 8;                 // warps that scale and add
+    static constexpr int kEpi = kNT == 16 ? 4 : 8;             // warps that scale and add
     static constexpr int kThreads = 32 * (kFirst + kEpi);
     static constexpr int kCols = kNT / (kEpi / 4);             // accumulator columns of a thread
     static constexpr int kLoad = kPair ? kNT / 2 : kNT;        // rows of the columns' operand that a block loads
-    static constexpr int kChunk = 16;                          // of which so many are loaded at a time
+    static constexpr int kChunk = kPair ? 16 : kCols < 32 ? kCols : 32;  // of which so many are loaded at a time,
+    static constexpr int kBatch = kNT == 16 ? 4 : kNT == 32 ? 2 : 1;     // of so many K blocks together
     static constexpr int kAcc = kPair ? 2 : 4;                 // TMEM accumulators in turn
     static constexpr uint32_t kTmem = kNT * kAcc;
     static constexpr uint32_t kStage = (kMmRows + kLoad) * 128;
-    static constexpr uint32_t kStaging = kSwap ? 0 : kEpi * 2 * 4096;
+    static constexpr uint32_t kStaging = kEpi * 2 * 4096;
     static constexpr int kScales = (kSwap ? kNT : kMmRows) + 4;  // floats of a K block: those of a8's rows, then of w8's blocks
     static constexpr uint32_t kFac = kScaleSlots * kScaleBlocks * kScales * 4;
-    static constexpr uint32_t kBytes = 1024 + kStages * kStage + kStaging + kFac + 256;
-    static_assert(kBytes <= 227 * 1024, "shared memory of a block");
-    static_assert(kNT * kMmRows * 4 <= kStages * kStage, "a tile's sums fit the stages");
+    // split (1, 2, 4 or 8): columns that a block owns, whose sums come from every rank; at least 4, or 8 where they are written so
+    static constexpr __host__ __device__ int own(int split) {
+        const int least = kSwap ? 4 : 8;
+        return kNT / split < least ? least : kNT / split;
+    }
+    static constexpr int kRedCols = kNT == 16 ? 32 : kNT;  // the most of split * own(split)
+    static constexpr uint32_t bytes(bool split) {
+        return 1024 + kStages * kStage + (split ? kRedCols * kMmRows * 4 : kStaging) + kFac + 256;
+    }
 };
+
+// eight values of a row, of which `left` exist
+template <typename Out>
+__device__ __forceinline__ void store_row(Out *p, const float (&v)[8], int left, bool wide) {
+    if (wide && left >= 8) {
+        store<8>(p, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float one[1] = {v[j]};
+            if (j < left) store<1>(p + j, one);
+        }
+    }
+}
 
 template <bool kSwap, int kNT, int kStages, int kBlocks, bool kBf16, bool kSplit>
 __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlocks)
@@ -71,15 +92,17 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     using S = MmShape<kSwap, kNT, kStages>;
     using Out = typename Elem<kBf16>::T;
     constexpr bool kPair = S::kPair;
-    static_assert(!(kPair && kSplit), "a cluster is a pair or a split");
+    static_assert(!(kPair && kSplit) && (kSplit || !kSwap), "a cluster is a pair or a split");
+    static_assert((S::bytes(kSplit) + 1024) * kBlocks <= 228 * 1024, "shared memory of an SM");
+    constexpr uint32_t kOut = kSplit ? S::kRedCols * kMmRows * 4 : S::kStaging;  // staging of the output, or the sums of a split
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *staging = smem + kStages * S::kStage;
-    float *fac = reinterpret_cast<float *>(staging + S::kStaging);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + S::kStaging + S::kFac);
+    float *fac = reinterpret_cast<float *>(staging + kOut);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(staging + kOut + S::kFac);
     uint64_t *full = bars, *empty = bars + kStages, *t_full = bars + 2 * kStages, *t_empty = t_full + S::kAcc, *drain = t_empty + S::kAcc;
-    uint64_t *s_full = drain + 1, *s_empty = s_full + kScaleSlots;
-    static_assert((2 * kStages + 2 * S::kAcc + 1 + 2 * kScaleSlots) * 8 + 8 <= 256, "barriers");
+    uint64_t *red_full = drain + 1, *s_full = drain + 2, *s_empty = s_full + kScaleSlots;
+    static_assert((2 * kStages + 2 * S::kAcc + 2 + 2 * kScaleSlots) * 8 + 8 <= 256, "barriers");
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_empty + kScaleSlots);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
 
@@ -92,36 +115,46 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     const int tiles = a.p_tiles * a.q_tiles;
     const int kb0 = kSplit ? (int)((int64_t)a.kb * rank / split) : 0, kb1 = kSplit ? (int)((int64_t)a.kb * (rank + 1) / split) : a.kb;
 
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, 1);
-        }
-        for (int i = 0; i < S::kAcc; ++i) {
-            mbar_init(t_full + i, 1);
-            mbar_init(t_empty + i, S::kEpi * (kPair ? 2 : 1));
-        }
-        for (int i = 0; i < kScaleSlots; ++i) {
-            mbar_init(s_full + i, 32);
-            mbar_init(s_empty + i, S::kEpi);
-        }
-        mbar_init(drain, 1);
-        *abort_flag = 0;
-        fence_barrier_init();
-    }
+    // warp 0 makes the barriers and begins to load, warp 3 allocates the accumulators; the others wait for both
     if (warp == 0) {
-        if constexpr (kPair) {
-            tmem_alloc_pair(tmem_slot, S::kTmem);
-        } else {
-            tmem_alloc(tmem_slot, S::kTmem);
-            tmem_relinquish();
+        if (lane == 0) {
+            prefetch_tensormap(&map_p);
+            prefetch_tensormap(&map_q);
+            for (int i = 0; i < kStages; ++i) {
+                mbar_init(full + i, 1);
+                mbar_init(empty + i, 1);
+            }
+            for (int i = 0; i < S::kAcc; ++i) {
+                mbar_init(t_full + i, 1);
+                mbar_init(t_empty + i, S::kEpi * (kPair ? 2 : 1));
+            }
+            for (int i = 0; i < kScaleSlots; ++i) {
+                mbar_init(s_full + i, 32);
+                mbar_init(s_empty + i, S::kEpi);
+            }
+            mbar_init(drain, 1);
+            mbar_init(red_full, S::kEpi * split);
+            *abort_flag = 0;
+            fence_barrier_init();
         }
+        __syncwarp();
+        named_arrive(1, S::kThreads);
+    } else {
+        if (warp == 3) {
+            if constexpr (kPair) {
+                tmem_alloc_pair(tmem_slot, S::kTmem);
+            } else {
+                tmem_alloc(tmem_slot, S::kTmem);
+                tmem_relinquish();
+            }
+            tc_fence_before_sync();
+        }
+        named_sync(1, S::kThreads);
+        tc_fence_after_sync();
     }
-    tc_fence_before_sync();
-    __syncthreads();
-    if constexpr (kPair) cluster_sync();  // the other block's barriers stand
-    tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    if constexpr (kPair || kSplit) cluster_arrive_relaxed();
+    if constexpr (kPair) cluster_wait();  // the other block's barriers stand
+
     // tile -> (tile of the MMA rows' operand, tile of the columns'): kGroupTiles row tiles at a time, the columns' outside
     auto place = [&](int tile, int &tp, int &tq) {
         const int per = kGroupTiles * a.q_tiles, g = tile / per, r = tile - g * per;
@@ -168,7 +201,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         if (!kPair || rank == 0) {
             constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kNT, false, false);
             const uint64_t desc0 = smem_desc(smem_u32(smem), 0, 1024, kSw128);
-            const uint32_t d0 = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t d0 = __shfl_sync(0xffffffffu, *tmem_slot, 0);
             int it = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
@@ -229,6 +262,23 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                 const int s = g % kScaleSlots;
                 if (g >= kScaleSlots) ok = __all_sync(0xffffffffu, bar_wait_inline(s_empty + s, (g / kScaleSlots - 1) & 1, abort_flag, a.err_word));
                 if (!ok) break;
+                if constexpr (kSwap) {  // the columns' factors are multiplied here, once
+                    float x[kScaleBlocks][(kMs + 31) / 32], w[kScaleBlocks];
+#pragma unroll
+                    for (int u = 0; u < kScaleBlocks; ++u) {
+                        const int kb = min(k + u, kb1 - 1);
+                        w[u] = __ldg(a.w_scale + (int64_t)tp * a.kb + kb);
+#pragma unroll
+                        for (int i = 0; i < kMs; i += 32) x[u][i / 32] = __ldg(a.a_scale + kb * a.a_scale_stride + min(m0 + i + lane, a.M - 1));
+                    }
+#pragma unroll
+                    for (int u = 0; u < kScaleBlocks; ++u)
+#pragma unroll
+                        for (int i = 0; i < kMs; i += 32)
+                            if (i + lane < kMs) fac[(s * kScaleBlocks + u) * S::kScales + i + lane] = x[u][i / 32] * w[u];
+                    mbar_arrive(s_full + s);
+                    continue;
+                }
                 for (int u = 0; u < kScaleBlocks && k + u < kb1; ++u) {
                     float *to = fac + (s * kScaleBlocks + u) * S::kScales;
                     const float *from = a.a_scale + (k + u) * a.a_scale_stride;
@@ -247,7 +297,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         if constexpr (kPair) more_registers<kRegsAdd>();
         const int quad = warp & 3, half = (warp - kFirst) >> 2;  // (a warp reads TMEM lanes 32 (warp % 4) ..)
         const int row = quad * 32 + lane, col0 = half * S::kCols;
-        const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+        const uint32_t tmem = *tmem_slot, lane_addr = (uint32_t)(quad * 32) << 16;
         Out *out = static_cast<Out *>(a.out);
         int it = 0, g = 0, parts = 0;  // K blocks, slots of scales, staging tiles
         bool ok = true;
@@ -257,37 +307,55 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
             uint64_t acc[S::kCols / 2];
 #pragma unroll
             for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0;
-            // adds one K block: acc += D * factor
-            auto add_block = [&](auto factor) {
-                const int c = it % S::kAcc;
-                if (ok) ok = bar_wait_inline(t_full + c, (it / S::kAcc) & 1, abort_flag, a.err_word);
+            // adds n <= kBatch K blocks: acc += D * factor(block, pair of columns)
+            auto add_blocks = [&](int n, auto factor) {
+                const auto at = [&](int u) { return (it + u) % S::kAcc; };
+                if (ok) {
+#pragma unroll
+                    for (int u = 0; u < S::kBatch; ++u)
+                        if (u < n && ok) ok = bar_wait_inline(t_full + at(u), ((it + u) / S::kAcc) & 1, abort_flag, a.err_word);
+                }
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 tc_fence_after_sync();
-                const uint32_t d = tmem + lane_addr + (uint32_t)(c * kNT + col0);
 #pragma unroll
                 for (int j = 0; j < S::kCols; j += S::kChunk) {
-                    uint32_t v[S::kChunk / 16][16];
+                    uint32_t v[S::kBatch][S::kChunk / 16][16];
 #pragma unroll
-                    for (int i = 0; i < S::kChunk / 16; ++i) tmem_ld_32x32b_x16(d + j + 16 * i, v[i]);
+                    for (int u = 0; u < S::kBatch; ++u)
+#pragma unroll
+                        for (int i = 0; i < S::kChunk / 16; ++i)
+                            if (u < n) tmem_ld_32x32b_x16(tmem + lane_addr + (uint32_t)(at(u) * kNT + col0 + j + 16 * i), v[u][i]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < S::kChunk / 16; ++i) tmem_loaded(v[i]);
+                    for (int u = 0; u < S::kBatch; ++u)
+#pragma unroll
+                        for (int i = 0; i < S::kChunk / 16; ++i) tmem_loaded(v[u][i]);
                     if (j + S::kChunk == S::kCols) {
                         tc_fence_before_sync();
                         if (lane == 0) {
-                            if constexpr (kPair)
-                                mbar_arrive_cluster_relaxed(of_rank(t_empty + c, 0));
-                            else
-                                mbar_arrive(t_empty + c);
+#pragma unroll
+                            for (int u = 0; u < S::kBatch; ++u) {
+                                if (u < n) {
+                                    if constexpr (kPair)
+                                        mbar_arrive_cluster_relaxed(of_rank(t_empty + at(u), 0));
+                                    else
+                                        mbar_arrive(t_empty + at(u));
+                                }
+                            }
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < S::kChunk / 2; ++i)
-                        acc[j / 2 + i] = f2_fma(f2_pack(__uint_as_float(v[i / 8][2 * (i % 8)]), __uint_as_float(v[i / 8][2 * (i % 8) + 1])),
-                                                factor(j / 2 + i), acc[j / 2 + i]);
+                    for (int u = 0; u < S::kBatch; ++u) {
+                        if (u < n) {
+#pragma unroll
+                            for (int i = 0; i < S::kChunk / 2; ++i)
+                                acc[j / 2 + i] = f2_fma(f2_pack(__uint_as_float(v[u][i / 8][2 * (i % 8)]), __uint_as_float(v[u][i / 8][2 * (i % 8) + 1])),
+                                                        factor(u, j / 2 + i), acc[j / 2 + i]);
+                        }
+                    }
                 }
-                ++it;
+                it += n;
             };
             for (int k = kb0; k < kb1; k += kScaleBlocks, ++g) {
                 const int s = g % kScaleSlots;
@@ -295,10 +363,13 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                 if (ok) ok = bar_wait_inline(s_full + s, (g / kScaleSlots) & 1, abort_flag, a.err_word);
                 ok = __all_sync(0xffffffffu, ok);
                 if constexpr (kSwap) {
-                    for (int u = 0; u < kScaleBlocks && k + u < kb1; ++u) {
-                        const uint64_t *f = reinterpret_cast<const uint64_t *>(sc + u * S::kScales);
-                        const uint64_t w = f2_pack(sc[u * S::kScales + kNT], sc[u * S::kScales + kNT]);
-                        add_block([&](int i) { return f2_mul(f[i], w); });
+#pragma unroll
+                    for (int u = 0; u < kScaleBlocks; u += S::kBatch) {
+                        if (k + u < kb1)
+                            add_blocks(min(S::kBatch, kb1 - k - u), [&](int b, int i) {
+                                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + (u + b) * S::kScales + col0 + 4 * (i / 2));
+                                return i % 2 ? f.y : f.x;
+                            });
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_empty + s);
@@ -312,32 +383,91 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                     for (int u = 0; u < kScaleBlocks; ++u) {
                         if (k + u < kb1) {
                             const uint64_t ff = f2_pack(f[u], f[u]);
-                            add_block([&](int) { return ff; });
+                            add_blocks(1, [&](int, int) { return ff; });
                         }
                     }
                 }
             }
             if constexpr (kSplit) {
-                // the block's sums, [column][row], over the stages (which no copy or product uses any more)
-                float *red = reinterpret_cast<float *>(smem);
+                // (rows of out that do not exist have no sums to hand over)
+                const int own = S::own(split);
+                const int cols = kSwap ? min(kNT, a.M - tq * kNT) : min(kNT, a.N - tq * kNT);  // the tile's columns that exist
+                if (split == 1) {
+                    if (ok) {
+                        const int n = kSwap ? tp * kMmRows + row : tq * kNT + col0, m = kSwap ? tq * kNT + col0 : tp * kMmRows + row;
+                        if constexpr (kSwap) {
 #pragma unroll
-                for (int i = 0; i < S::kCols / 2; ++i) {
-                    float lo, hi;
-                    f2_unpack(acc[i], lo, hi);
-                    red[(col0 + 2 * i) * kMmRows + row] = lo;
-                    red[(col0 + 2 * i + 1) * kMmRows + row] = hi;
+                            for (int i = 0; i < S::kCols; ++i) {
+                                float v[2];
+                                f2_unpack(acc[i / 2], v[0], v[1]);
+                                const float r[1] = {v[i & 1]};
+                                if (m + i < a.M && n < a.N) store<1>(out + (m + i) * a.out_stride + n, r);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < S::kCols; i += 8) {
+                                float v[8];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) f2_unpack(acc[i / 2 + j], v[2 * j], v[2 * j + 1]);
+                                if (m < a.M) store_row(out + m * a.out_stride + n + i, v, a.N - n - i, a.tma_out);
+                            }
+                        }
+                    }
+                    cluster_wait();
+                } else {
+                    cluster_wait();  // every block's barriers stand
+                    // sums of a tile lie as [rank][column / 4][row][4 columns] in the block that owns the columns
+                    float4 *red = reinterpret_cast<float4 *>(staging);
+                    if (ok) {
+                        uint32_t to = 0;
+#pragma unroll
+                        for (int i = 0; i < S::kCols; i += 4) {
+                            const int c = col0 + i;
+                            if (i == 0 || c % own == 0) to = of_rank(red + (rank * own + c % own) / 4 * kMmRows + row, c / own);
+                            float v[4];
+                            f2_unpack(acc[i / 2], v[0], v[1]);
+                            f2_unpack(acc[i / 2 + 1], v[2], v[3]);
+                            if (c < cols) cluster_store(to, v[0], v[1], v[2], v[3]);
+                            to += kMmRows * 16;
+                        }
+                        fence_cluster();
+                        __syncwarp();
+                        if (lane < split && lane * own < cols) mbar_arrive_cluster(of_rank(red_full, lane));
+                    }
+                    const int c0 = rank * own, mine = min(own, cols - c0);
+                    if (mine > 0) {
+                        ok = bar_wait_cluster(red_full, 0, abort_flag, a.err_word);
+                        constexpr int kG = kSwap ? 4 : 8;  // columns of a step
+                        for (int i = tid - 32 * kFirst; ok && i < (mine + kG - 1) / kG * kMmRows; i += 32 * S::kEpi) {
+                            const int c = i / kMmRows * kG, r = i % kMmRows;
+                            float v[kG];
+#pragma unroll
+                            for (int j = 0; j < kG; ++j) v[j] = 0.f;
+#pragma unroll
+                            for (int b = 0; b < 8; ++b) {
+                                if (b < split) {
+#pragma unroll
+                                    for (int j = 0; j < kG; j += 4) {
+                                        const float4 x = red[(b * own + c + j) / 4 * kMmRows + r];
+                                        v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
+                                    }
+                                }
+                            }
+                            if constexpr (kSwap) {
+                                const int m = tq * kNT + c0 + c, n = tp * kMmRows + r;
+#pragma unroll
+                                for (int j = 0; j < kG; ++j) {
+                                    const float one[1] = {v[j]};
+                                    if (m + j < a.M && n < a.N) store<1>(out + (m + j) * a.out_stride + n, one);
+                                }
+                            } else {
+                                const int m = tp * kMmRows + r, n = tq * kNT + c0 + c;
+                                if (m < a.M) store_row(out + m * a.out_stride + n, v, a.N - n, a.tma_out);
+                            }
+                        }
+                    }
                 }
             } else if (!ok) {
-            } else if constexpr (kSwap) {
-                const int n = tp * kMmRows + row;
-#pragma unroll
-                for (int i = 0; i < S::kCols; ++i) {
-                    float v[2];
-                    f2_unpack(acc[i / 2], v[0], v[1]);
-                    const int m = tq * kNT + i;
-                    const float r[1] = {v[i & 1]};
-                    if (m < a.M && n < a.N) store<1>(out + m * a.out_stride + n, r);
-                }
             } else {
                 // 32 rows x 128 bytes at a time through two swizzled staging tiles of the warp's own, in turn
                 constexpr int kPart = kBf16 ? 64 : 32;
@@ -391,57 +521,20 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         if (warp == 3) fewer_registers<kRegsLoad>();
     }
     if constexpr (kSplit) {
-        __syncthreads();
-        cluster_sync();
-        if (warp >= kFirst && *(volatile int *)abort_flag == 0) {
-            int tp, tq;
-            place(first, tp, tq);
-            const uint32_t red = smem_u32(smem);
-            Out *out = static_cast<Out *>(a.out);
-            const int per = kNT / split, c0 = rank * per;  // this block's columns of the tile
-            if constexpr (kSwap) {
-                for (int i = tid - 32 * kFirst; i < per * kMmRows; i += 32 * S::kEpi) {
-                    const int c = c0 + i / kMmRows, r = i % kMmRows;
-                    float v[1] = {0.f};
-                    for (int b = 0; b < split; ++b) v[0] += cluster_load(red + (c * kMmRows + r) * 4, b);
-                    const int m = tq * kNT + c, n = tp * kMmRows + r;
-                    if (m < a.M && n < a.N) store<1>(out + m * a.out_stride + n, v);
-                }
-            } else {
-                for (int i = tid - 32 * kFirst; i < per / 8 * kMmRows; i += 32 * S::kEpi) {
-                    const int c = c0 + i / kMmRows * 8, r = i % kMmRows;
-                    float v[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-                    for (int b = 0; b < split; ++b)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] += cluster_load(red + ((c + j) * kMmRows + r) * 4, b);
-                    const int m = tp * kMmRows + r, n = tq * kNT + c;
-                    if (m >= a.M) continue;
-                    Out *o = out + m * a.out_stride + n;
-                    if (a.tma_out && n + 8 <= a.N) {
-                        store<8>(o, v);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float one[1] = {v[j]};
-                            if (n + j < a.N) store<1>(o + j, one);
-                        }
-                    }
-                }
-            }
-        }
         __syncwarp();
-        cluster_sync();  // nobody leaves while another block reads its sums
+        if (warp < kFirst) cluster_wait();
     }
     tc_fence_before_sync();
     __syncthreads();
-    if constexpr (kPair) cluster_sync();  // neither block leaves while the other's copies, products or arrivals may reach it
-    if (warp == 0) {
+    if constexpr (kPair || kSplit) {  // no block leaves while another's copies, products, sums or arrivals may reach it
+        cluster_arrive();
+        cluster_wait();
+    }
+    if (warp == 3) {
         if constexpr (kPair)
-            tmem_dealloc_pair(tmem, S::kTmem);
+            tmem_dealloc_pair(*tmem_slot, S::kTmem);
         else
-            tmem_dealloc(tmem, S::kTmem);
+            tmem_dealloc(*tmem_slot, S::kTmem);
     }
 }
 
@@ -482,12 +575,12 @@ cudaError_t mm_launch(MmCall c, int blocks) {
             return cudaErrorInvalidValue;
     }
     auto kernel = matmul8_kernel<kSwap, kNT, kStages, kBlocks, kBf16, kSplit>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes(kSplit));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kBytes;
+    cfg.dynamicSmemBytes = S::bytes(kSplit);
     cfg.stream = c.st;
     cudaLaunchAttribute attr[1];
     if (kSplit || S::kPair) {
@@ -527,8 +620,8 @@ cudaError_t launch_matmul8(const uint8_t *a8, int64_t a_stride, const float *a_s
         while (c.a.split < 8 && c.a.p_tiles * c.a.split * 2 <= slots && c.a.kb >= c.a.split * 4) c.a.split *= 2;
         const int blocks = c.a.p_tiles * c.a.split;
         if (nt == 16) return mm_typed<true, 16, 5, 2, true>(c, blocks);
-        if (nt == 32) return mm_typed<true, 32, 5, 2, true>(c, blocks);
-        return mm_typed<true, 64, 4, 2, true>(c, blocks);
+        if (nt == 32) return mm_typed<true, 32, 4, 2, true>(c, blocks);
+        return mm_typed<true, 64, 3, 2, true>(c, blocks);
     }
     const int rows = tiles_of(M, kMmRows), narrow = rows * tiles_of(N, 128), pairs = tiles_of(M, 256) * tiles_of(N, 256);
     if (narrow * 2 <= sms && c.a.kb >= 4) {
