@@ -52,7 +52,7 @@ struct MmShape {
     static constexpr int kThreads = 32 * (kFirst + kEpi);
     static constexpr int kCols = kNT / (kEpi / 4);             // accumulator columns of a thread
     static constexpr int kLoad = kPair ? kNT / 2 : kNT;        // rows of the columns' operand that a block loads
-    static constexpr int kChunk = kPair ? 16 : kCols < 32 ? kCols : 32;  // of which so many are loaded at a time,
+    static constexpr int kChunk = kNT >= 256 || kNT == 64 ? 16 : kCols < 32 ? kCols : 32;  // of which so many are loaded at a time,
     static constexpr int kBatch = kNT == 16 ? 4 : kNT == 32 ? 2 : 1;     // of so many K blocks together
     static constexpr int kAcc = kPair ? 2 : 4;                 // TMEM accumulators in turn
     static constexpr uint32_t kTmem = kNT * kAcc;
@@ -60,25 +60,26 @@ struct MmShape {
     static constexpr uint32_t kStaging = kEpi * 2 * 4096;
     static constexpr int kScales = (kSwap ? kNT : kMmRows) + 4;  // floats of a K block: those of a8's rows, then of w8's blocks
     static constexpr uint32_t kFac = kScaleSlots * kScaleBlocks * kScales * 4;
-    // split (1, 2, 4 or 8): columns that a block owns, whose sums come from every rank; at least 4, or 8 where they are written so
+    // split (1, 2, 4 or 8): columns that a block owns, whose sums come from every rank; at least 4
     static constexpr __host__ __device__ int own(int split) {
-        const int least = kSwap ? 4 : 8;
-        return kNT / split < least ? least : kNT / split;
+        return kNT / split < 4 ? 4 : kNT / split;
     }
     static constexpr int kRedCols = kNT == 16 ? 32 : kNT;  // the most of split * own(split)
+    static constexpr int kRedRow = kMmRows + 1;            // (rows of 16 bytes, so that neighbours in either direction lie in other banks)
+    static constexpr uint32_t kRed = kRedCols / 4 * kRedRow * 16;
     static constexpr uint32_t bytes(bool split) {
-        return 1024 + kStages * kStage + (split ? kRedCols * kMmRows * 4 : kStaging) + kFac + 256;
+        return 1024 + kStages * kStage + (split ? kRed : kStaging) + kFac + 256;
     }
 };
 
-// eight values of a row, of which `left` exist
-template <typename Out>
-__device__ __forceinline__ void store_row(Out *p, const float (&v)[8], int left, bool wide) {
-    if (wide && left >= 8) {
-        store<8>(p, v);
+// V values of a row, of which `left` exist
+template <int V, typename Out>
+__device__ __forceinline__ void store_row(Out *p, const float (&v)[V], int left, bool wide) {
+    if (wide && left >= V) {
+        store<V>(p, v);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < V; ++j) {
             const float one[1] = {v[j]};
             if (j < left) store<1>(p + j, one);
         }
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     constexpr bool kPair = S::kPair;
     static_assert(!(kPair && kSplit) && (kSplit || !kSwap), "a cluster is a pair or a split");
     static_assert((S::bytes(kSplit) + 1024) * kBlocks <= 228 * 1024, "shared memory of an SM");
-    constexpr uint32_t kOut = kSplit ? S::kRedCols * kMmRows * 4 : S::kStaging;  // staging of the output, or the sums of a split
+    constexpr uint32_t kOut = kSplit ? S::kRed : S::kStaging;  // staging of the output, or the sums of a split
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *staging = smem + kStages * S::kStage;
@@ -166,6 +167,8 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     if (warp == 0) {
         // ---- loads
         if constexpr (kPair) fewer_registers<kRegsLoad>();
+        grid_dependency_wait();  // (what comes before needs nothing of the kernel before this one)
+        grid_launch_dependents();
         int it = 0;
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
@@ -250,6 +253,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         // ---- scales, kScaleBlocks K blocks at a time.  (Loaded by the warps that add, they would hold up each of their arrivals
         // until they are there: 8192 x 4096 x 16384 took 449 us so, 356 without any scales.)
         if constexpr (kPair) fewer_registers<kRegsLoad>();
+        grid_dependency_wait();
         // a8's rows (kSwap: the tile's columns) and w8's blocks of 128; past the ends the last one's are repeated, for sums that are not written
         int g = 0;
         bool ok = true;
@@ -257,25 +261,35 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
             int tp, tq;
             place(tile, tp, tq);
             const int m0 = kSwap ? tq * kNT : tp * kRows + row0, n0 = kSwap ? tp * kMmRows : tq * kNT;
-            constexpr int kMs = kSwap ? kNT : kMmRows, kNs = kPair ? 2 : 1;
+            constexpr int kMs = kSwap ? kNT : kMmRows, kNs = kPair ? 2 : 1, kXs = (kMs + 31) / 32;
+            float x[kScaleBlocks][kXs], w[kScaleBlocks];
+            auto fetch = [&](int k) {
+#pragma unroll
+                for (int u = 0; u < kScaleBlocks; ++u) {
+                    const int kb = min(k + u, kb1 - 1);
+                    w[u] = load_now(a.w_scale + (int64_t)tp * a.kb + kb);
+#pragma unroll
+                    for (int i = 0; i < kXs; ++i) x[u][i] = load_now(a.a_scale + kb * a.a_scale_stride + min(m0 + 32 * i + lane, a.M - 1));
+                }
+            };
             for (int k = kb0; k < kb1; k += kScaleBlocks, ++g) {
                 const int s = g % kScaleSlots;
+                if constexpr (kSwap)
+                    if (k == kb0) fetch(k);
                 if (g >= kScaleSlots) ok = __all_sync(0xffffffffu, bar_wait_inline(s_empty + s, (g / kScaleSlots - 1) & 1, abort_flag, a.err_word));
                 if (!ok) break;
-                if constexpr (kSwap) {  // the columns' factors are multiplied here, once
-                    float x[kScaleBlocks][(kMs + 31) / 32], w[kScaleBlocks];
-#pragma unroll
-                    for (int u = 0; u < kScaleBlocks; ++u) {
-                        const int kb = min(k + u, kb1 - 1);
-                        w[u] = __ldg(a.w_scale + (int64_t)tp * a.kb + kb);
-#pragma unroll
-                        for (int i = 0; i < kMs; i += 32) x[u][i / 32] = __ldg(a.a_scale + kb * a.a_scale_stride + min(m0 + i + lane, a.M - 1));
-                    }
+                if constexpr (kSwap) {  // the columns' factors are multiplied here, once; the next group's are on their way meanwhile
+                    float y[kScaleBlocks][kXs];
 #pragma unroll
                     for (int u = 0; u < kScaleBlocks; ++u)
 #pragma unroll
-                        for (int i = 0; i < kMs; i += 32)
-                            if (i + lane < kMs) fac[(s * kScaleBlocks + u) * S::kScales + i + lane] = x[u][i / 32] * w[u];
+                        for (int i = 0; i < kXs; ++i) y[u][i] = x[u][i] * w[u];
+                    if (k + kScaleBlocks < kb1) fetch(k + kScaleBlocks);
+#pragma unroll
+                    for (int u = 0; u < kScaleBlocks; ++u)
+#pragma unroll
+                        for (int i = 0; i < kXs; ++i)
+                            if (32 * i + lane < kMs) fac[(s * kScaleBlocks + u) * S::kScales + 32 * i + lane] = y[u][i];
                     mbar_arrive(s_full + s);
                     continue;
                 }
@@ -295,6 +309,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     } else if (warp >= kFirst) {
         // ---- sums
         if constexpr (kPair) more_registers<kRegsAdd>();
+        grid_dependency_wait();  // (out may still be read by the kernel before)
         const int quad = warp & 3, half = (warp - kFirst) >> 2;  // (a warp reads TMEM lanes 32 (warp % 4) ..)
         const int row = quad * 32 + lane, col0 = half * S::kCols;
         const uint32_t tmem = *tmem_slot, lane_addr = (uint32_t)(quad * 32) << 16;
@@ -423,12 +438,12 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
 #pragma unroll
                         for (int i = 0; i < S::kCols; i += 4) {
                             const int c = col0 + i;
-                            if (i == 0 || c % own == 0) to = of_rank(red + (rank * own + c % own) / 4 * kMmRows + row, c / own);
+                            if (i == 0 || c % own == 0) to = of_rank(red + (rank * own + c % own) / 4 * S::kRedRow + row, c / own);
                             float v[4];
                             f2_unpack(acc[i / 2], v[0], v[1]);
                             f2_unpack(acc[i / 2 + 1], v[2], v[3]);
                             if (c < cols) cluster_store(to, v[0], v[1], v[2], v[3]);
-                            to += kMmRows * 16;
+                            to += S::kRedRow * 16;
                         }
                         fence_cluster();
                         __syncwarp();
@@ -437,26 +452,22 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                     const int c0 = rank * own, mine = min(own, cols - c0);
                     if (mine > 0) {
                         ok = bar_wait_cluster(red_full, 0, abort_flag, a.err_word);
-                        constexpr int kG = kSwap ? 4 : 8;  // columns of a step
-                        for (int i = tid - 32 * kFirst; ok && i < (mine + kG - 1) / kG * kMmRows; i += 32 * S::kEpi) {
-                            const int c = i / kMmRows * kG, r = i % kMmRows;
-                            float v[kG];
-#pragma unroll
-                            for (int j = 0; j < kG; ++j) v[j] = 0.f;
+                        // four columns of a row a step; neighbours in a warp are neighbours in out: rows of the tile (kSwap), or its columns
+                        const int quads = (mine + 3) / 4;
+                        for (int i = tid - 32 * kFirst; ok && i < quads * kMmRows; i += 32 * S::kEpi) {
+                            const int r = kSwap ? i % kMmRows : i / quads, c = 4 * (kSwap ? i / kMmRows : i - r * quads);
+                            float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                             for (int b = 0; b < 8; ++b) {
                                 if (b < split) {
-#pragma unroll
-                                    for (int j = 0; j < kG; j += 4) {
-                                        const float4 x = red[(b * own + c + j) / 4 * kMmRows + r];
-                                        v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
-                                    }
+                                    const float4 x = red[(b * own + c) / 4 * S::kRedRow + r];
+                                    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
                                 }
                             }
                             if constexpr (kSwap) {
                                 const int m = tq * kNT + c0 + c, n = tp * kMmRows + r;
 #pragma unroll
-                                for (int j = 0; j < kG; ++j) {
+                                for (int j = 0; j < 4; ++j) {
                                     const float one[1] = {v[j]};
                                     if (m + j < a.M && n < a.N) store<1>(out + (m + j) * a.out_stride + n, one);
                                 }
@@ -582,14 +593,14 @@ cudaError_t mm_launch(MmCall c, int blocks) {
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::bytes(kSplit);
     cfg.stream = c.st;
-    cudaLaunchAttribute attr[1];
-    if (kSplit || S::kPair) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = S::kPair ? 2u : (unsigned)c.a.split;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S::kPair ? 2u : (unsigned)c.a.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kSplit || S::kPair ? 2 : 1;
     e = kSwap ? cudaLaunchKernelEx(&cfg, kernel, map_w, map_a, map_out, c.a) : cudaLaunchKernelEx(&cfg, kernel, map_a, map_w, map_out, c.a);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();

@@ -72,6 +72,13 @@ __device__ __forceinline__ bool bar_wait_cluster(uint64_t *bar, uint32_t parity,
     }
 }
 
+// A load that goes out where it stands (the compiler moves a plain one down to its use).
+__device__ __forceinline__ float load_now(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 // Four bytes, global -> shared, asynchronously (cp_async_mbar_arrive() tells when).
 __device__ __forceinline__ void cp_async_4(void *smem_dst, const void *gsrc) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gsrc) : "memory");
