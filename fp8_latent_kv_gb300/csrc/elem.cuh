@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace kv8 {
 
@@ -52,6 +53,19 @@ struct Raw {
             }
         }
     }
+    __device__ __forceinline__ void store(typename Elem<kBf16>::T *p) const {  // as loaded
+        if constexpr (V == 1) {
+            if constexpr (kBf16)
+                *p = __ushort_as_bfloat16((uint16_t)w[0]);
+            else
+                *p = __uint_as_float(w[0]);
+        } else {
+            static_assert(kWords % 4 == 0, "whole 16 bytes");
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0;
@@ -66,6 +80,13 @@ struct Raw {
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i]);
         }
+    }
+    // values 2 i, 2 i + 1 as a pair of f32
+    __device__ __forceinline__ uint64_t pair(int i) const {
+        if constexpr (kBf16)
+            return sm100::f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+        else
+            return sm100::f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     }
 };
 

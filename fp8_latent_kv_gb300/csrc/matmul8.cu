@@ -291,17 +291,17 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                         for (int i = 0; i < kXs; ++i)
                             if (32 * i + lane < kMs) fac[(s * kScaleBlocks + u) * S::kScales + 32 * i + lane] = y[u][i];
                     mbar_arrive(s_full + s);
-                    continue;
-                }
-                for (int u = 0; u < kScaleBlocks && k + u < kb1; ++u) {
-                    float *to = fac + (s * kScaleBlocks + u) * S::kScales;
-                    const float *from = a.a_scale + (k + u) * a.a_scale_stride;
+                } else {
+                    for (int u = 0; u < kScaleBlocks && k + u < kb1; ++u) {
+                        float *to = fac + (s * kScaleBlocks + u) * S::kScales;
+                        const float *from = a.a_scale + (k + u) * a.a_scale_stride;
 #pragma unroll
-                    for (int i = 0; i < kMs; i += 32)
-                        if (i + lane < kMs) cp_async_4(to + i + lane, from + min(m0 + i + lane, a.M - 1));
-                    if (lane < kNs) cp_async_4(to + kMs + lane, a.w_scale + (int64_t)min(n0 / kMmBlk + lane, (a.N - 1) / kMmBlk) * a.kb + k + u);
+                        for (int i = 0; i < kMs; i += 32)
+                            if (i + lane < kMs) cp_async_4(to + i + lane, from + min(m0 + i + lane, a.M - 1));
+                        if (lane < kNs) cp_async_4(to + kMs + lane, a.w_scale + (int64_t)min(n0 / kMmBlk + lane, (a.N - 1) / kMmBlk) * a.kb + k + u);
+                    }
+                    cp_async_mbar_arrive(s_full + s);
                 }
-                cp_async_mbar_arrive(s_full + s);
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");  // (none is in flight when the block ends)

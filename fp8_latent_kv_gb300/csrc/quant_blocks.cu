@@ -10,7 +10,7 @@
 #include "elem.cuh"
 #include "internal.h"
 #include "norm.cuh"
-#include "quant_row.cuh"
+#include "quant_fast.cuh"
 
 #include <type_traits>
 
@@ -19,23 +19,79 @@ namespace {
 
 constexpr int kQThreads = 256, kQBlk = KV8_KVB_BLOCK;
 
+using sm100::f2_fma;
+using sm100::f2_mul;
+using sm100::f2_pack;
+using sm100::f2_unpack;
+
 __device__ __forceinline__ float half_warp_max(float v) {
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
-// Quantizes a lane's eight values of a block that its half warp holds; returns the block's scale.
-__device__ __forceinline__ float quant8(const float (&y)[8], uint2 &bytes) {
-    float amax = 0.f;
+// Quantizes J times eight values a lane, of which each sixteen lanes hold J blocks (z[j], as pairs, times `factor`): bytes, and
+// the scale of one block, number `mine`, which every lane (lane & 15) / (16 / J) == mine returns.
+// The maxima of the J blocks are taken together: with each exchange a lane keeps half of the blocks that it still
+// carries, so J = 4 takes 5 exchanges instead of 16 and the divisions are made once.
+template <int J>
+__device__ __forceinline__ float quant_blocks_of(const uint64_t (&z)[J][4], float factor, uint2 (&bytes)[J], int &mine) {
+    const int lane = threadIdx.x & 31;
+    float m[J];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = finite_abs_max(amax, y[i]);
-    amax = half_warp_max(amax);
-    float pre, mul, scale;
-    row_quant_factors(amax, pre, mul, scale);
-    bytes.x = enc4(scale4(make_float4(y[0], y[1], y[2], y[3]), pre, mul));
-    bytes.y = enc4(scale4(make_float4(y[4], y[5], y[6], y[7]), pre, mul));
-    return scale;
+    for (int j = 0; j < J; ++j) {
+        m[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2_unpack(z[j][i], a, b);
+            m[j] = abs_max_nan(m[j], a, b);
+        }
+    }
+    int left = 8;
+    mine = 0;
+#pragma unroll
+    for (int k = J; k > 1; k /= 2, left /= 2) {
+        const bool up = lane & left;
+#pragma unroll
+        for (int j = 0; j < k / 2; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, up ? m[j] : m[j + k / 2], left);
+            m[j] = max_nan(up ? m[j + k / 2] : m[j], other);
+        }
+        mine += up ? k / 2 : 0;
+    }
+#pragma unroll
+    for (; left > 0; left /= 2) m[0] = max_nan(m[0], __shfl_xor_sync(0xffffffffu, m[0], left));
+    float mul, scale;
+    bool plain = plain_factors(m[0] * factor, mul, scale);
+    const float whole = mul * factor;
+    plain = plain && whole <= 3.402823466e38f;
+    if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const float f = __shfl_sync(0xffffffffu, whole, (lane & 16) | j * (16 / J));
+            const uint64_t ff = f2_pack(f, f);
+            bytes[j] = make_uint2(enc2_scaled(z[j][0], ff) | enc2_scaled(z[j][1], ff) << 16, enc2_scaled(z[j][2], ff) | enc2_scaled(z[j][3], ff) << 16);
+        }
+        return scale;
+    }
+    float of_mine = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        float y[8], amax = 0.f, pre;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_unpack(z[j][i], y[2 * i], y[2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            y[i] *= factor;
+            amax = finite_abs_max(amax, y[i]);
+        }
+        row_quant_factors(half_warp_max(amax), pre, mul, scale);
+        bytes[j].x = enc4(scale4(make_float4(y[0], y[1], y[2], y[3]), pre, mul));
+        bytes[j].y = enc4(scale4(make_float4(y[4], y[5], y[6], y[7]), pre, mul));
+        if (j == mine) of_mine = scale;
+    }
+    return of_mine;
 }
 
 // No norm: a block of threads takes 8 rows (a warp each) x kQCols blocks of 128 columns, so that its scales, 8
@@ -63,16 +119,20 @@ __global__ void __launch_bounds__(kQThreads) quant_blocks_kernel(const void *__r
         else
             raw[j].zero();
     }
+    uint64_t z[kQCols / 2][4];
+#pragma unroll
+    for (int j = 0; j < kQCols / 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[j][i] = raw[j].pair(i);
+    uint2 b[kQCols / 2];
+    int mine;
+    const float s = quant_blocks_of<kQCols / 2>(z, 1.f, b, mine);
 #pragma unroll
     for (int j = 0; j < kQCols / 2; ++j) {
         const int col = (kb0 + 2 * j) * kQBlk + 8 * lane;
-        float y[8];
-        raw[j].get(y);
-        uint2 b;
-        const float s = quant8(y, b);
-        if (row < n && col < width) *reinterpret_cast<uint2 *>(q + row * width + col) = b;
-        if ((lane & 15) == 0) sc[2 * j + (lane >> 4)][warp] = s;
+        if (row < n && col < width) *reinterpret_cast<uint2 *>(q + row * width + col) = b[j];
     }
+    if (lane % (32 / kQCols) == 0) sc[2 * mine + (lane >> 4)][warp] = s;
     __syncthreads();
     if (threadIdx.x < kQCols * kQRows) {
         const int k = threadIdx.x / kQRows, r = threadIdx.x % kQRows;
@@ -80,76 +140,104 @@ __global__ void __launch_bounds__(kQThreads) quant_blocks_kernel(const void *__r
     }
 }
 
-// With a norm: kT threads a row (a warp, or the whole block), kJ vectors of eight values each.
-template <bool kBf16, int kT, int kJ>
-__global__ void __launch_bounds__(kQThreads) norm_quant_blocks_kernel(const void *__restrict__ xv, int64_t n, int width,
-                                                                      int64_t x_stride, const float *__restrict__ norm_w,
-                                                                      float eps, uint8_t *__restrict__ q,
-                                                                      float *__restrict__ scale, int64_t scale_stride) {
+// With a norm: kT threads a row (a warp, or the whole block), kJ vectors of eight values each, row after row; a row is loaded
+// while the one before is worked on.
+template <bool kBf16, int kT, int kJ, int kBlocks>
+__global__ void __launch_bounds__(kT < kQThreads ? kQThreads : kT, kBlocks)
+    norm_quant_blocks_kernel(const void *__restrict__ xv, int64_t n, int width, int64_t x_stride,
+                             const float *__restrict__ norm_w, float eps, uint8_t *__restrict__ q,
+                             float *__restrict__ scale, int64_t scale_stride) {
     using T = typename Elem<kBf16>::T;
-    __shared__ float part[kQThreads / 32];
-    __shared__ double part_d[kQThreads / 32];
+    constexpr int kRows = kT < kQThreads ? kQThreads / kT : 1;  // of a block at a time
+    __shared__ float part[2][kT / 32];
+    __shared__ double part_d[2][kT / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = kT == 32 ? lane : threadIdx.x;
-    const int64_t row = (int64_t)blockIdx.x * (kQThreads / kT) + (kT == 32 ? warp : 0);
-    if (row >= n) return;  // (whole warps; with kT == kQThreads no block)
-    const T *x = static_cast<const T *>(xv) + row * x_stride;
+    const T *x = static_cast<const T *>(xv);
     Raw<kBf16, 8> raw[kJ];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-        const int col = 8 * (t + kT * j);
-        if (col < width)
-            raw[j].load(x + col);
-        else
-            raw[j].zero();
-    }
-    float y[kJ][8], ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) raw[j].get(y[j]);
-#pragma unroll
-    for (int j = 0; j < kJ; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(y[j][i], y[j][i], ss);
-    ss = warp_sum(ss);
-    if constexpr (kT > 32) {
-        if (lane == 0) part[warp] = ss;
-        __syncthreads();
-        ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < kT / 32; ++i) ss += part[i];
-    }
-    const float ms = ss / (float)width + eps;
-    float pre = 1.f, inv = __frsqrt_rn(ms);
-    if (!(ms >= 1e-32f && ss <= 1e30f)) {  // squares that leave the f32 range, infinities, NaN: the same for the whole row
-        double sd = 0.0;
+        for (int j = 0; j < kJ; ++j) {
+            const int col = 8 * (t + kT * j);
+            if (row < n && col < width)
+                raw[j].load(x + row * x_stride + col);
+            else
+                raw[j].zero();
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * kRows + (kT == 32 ? warp : 0);
+    fetch(row);
+    for (int turn = 0; row < n; row += (int64_t)gridDim.x * kRows, turn ^= 1) {  // (one row a warp, or a block: no thread leaves others behind)
+        uint64_t z[kJ][4], s2 = 0;
 #pragma unroll
         for (int j = 0; j < kJ; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sd += (double)y[j][i] * (double)y[j][i];
-        sd = warp_sum_f64(sd);
+            for (int i = 0; i < 4; ++i) z[j][i] = raw[j].pair(i);
+        fetch(row + (int64_t)gridDim.x * kRows);
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s2 = f2_fma(z[j][i], z[j][i], s2);
+        float ss, s_hi;
+        f2_unpack(s2, ss, s_hi);
+        ss += s_hi;
+        ss = warp_sum(ss);
         if constexpr (kT > 32) {
-            if (lane == 0) part_d[warp] = sd;
+            if (lane == 0) part[turn][warp] = ss;
             __syncthreads();
-            sd = 0.0;
-            for (int i = 0; i < kT / 32; ++i) sd += part_d[i];
-        }
-        norm_factor_f64(sd / width + (double)eps, pre, inv);
-    }
+            ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-        const int col = 8 * (t + kT * j);
-        if (8 * ((t & ~31) + kT * j) >= width) break;  // (whole warps)
-        if (col < width) {
-            float w[8];
-            load<8>(norm_w + col, w);
+            for (int i = 0; i < kT / 32; ++i) ss += part[turn][i];
+        }
+        const float ms = ss / (float)width + eps;
+        float pre = 1.f, inv = __frsqrt_rn(ms);
+        if (!(ms >= 1e-32f && ss <= 1e30f)) {  // squares that leave the f32 range, infinities, NaN: the same for the whole row
+            double sd = 0.0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[j][i] = y[j][i] * pre * inv * w[i];
+            for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float lo, hi;
+                    f2_unpack(z[j][i], lo, hi);
+                    sd += (double)lo * (double)lo + (double)hi * (double)hi;
+                }
+            sd = warp_sum_f64(sd);
+            if constexpr (kT > 32) {
+                if (lane == 0) part_d[turn][warp] = sd;
+                __syncthreads();
+                sd = 0.0;
+                for (int i = 0; i < kT / 32; ++i) sd += part_d[turn][i];
+            }
+            norm_factor_f64(sd / width + (double)eps, pre, inv);
+        } else if (ss < 1e-30f) {  // (values so small that a product with the weight could lose bits)
+            pre = 18446744073709551616.f;  // 2^64
+            inv *= 5.421010862427522e-20f;
         }
-        uint2 b;
-        const float s = quant8(y[j], b);
-        if (col < width) {
-            *reinterpret_cast<uint2 *>(q + row * width + col) = b;
-            if ((lane & 15) == 0) scale[col / kQBlk * scale_stride + row] = s;
+        if (pre != 1.f) {
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[j][i] = f2_mul(z[j][i], f2_pack(pre, pre));
         }
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+            const int col = 8 * (t + kT * j);
+            if (col < width) {
+                Raw<false, 8> w;
+                w.load(norm_w + col);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[j][i] = f2_mul(z[j][i], w.pair(i));
+            }
+        }
+        uint2 b[kJ];
+        int mine;
+        const float sc = quant_blocks_of<kJ>(z, inv, b, mine);
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+            const int col = 8 * (t + kT * j);
+            if (col < width) *reinterpret_cast<uint2 *>(q + row * width + col) = b[j];
+        }
+        const int block = (8 * (t + kT * mine)) / kQBlk;
+        if (lane % (16 / kJ) == 0 && block * kQBlk < width) scale[block * scale_stride + row] = sc;
     }
 }
 
@@ -167,18 +255,18 @@ cudaError_t launch_quant_blocks(const void *x, int x_bf16, int64_t n, int width,
         return cudaGetLastError();
     }
     // a warp a row up to 1024 columns, from there a block
-    auto go = [&](auto kernel, int threads) {
-        const int per = kQThreads / threads;
-        kernel<<<(unsigned)((n + per - 1) / per), kQThreads, 0, st>>>(x, n, width, x_stride, norm_w, eps, q, scale, scale_stride);
+    auto go = [&](auto kernel, int threads, int rows, int blocks_per_sm) {
+        const int64_t need = (n + rows - 1) / rows, most = (int64_t)device_sm_count() * blocks_per_sm;
+        kernel<<<(unsigned)(need < most ? need : most), threads, 0, st>>>(x, n, width, x_stride, norm_w, eps, q, scale, scale_stride);
     };
     auto pick = [&](auto bf16) {
         constexpr bool b = decltype(bf16)::value;
-        if (width <= 512) go(norm_quant_blocks_kernel<b, 32, 2>, 32);
-        else if (width <= 1024) go(norm_quant_blocks_kernel<b, 32, 4>, 32);
-        else if (width <= 2048) go(norm_quant_blocks_kernel<b, 256, 1>, 256);
-        else if (width <= 4096) go(norm_quant_blocks_kernel<b, 256, 2>, 256);
-        else if (width <= 8192) go(norm_quant_blocks_kernel<b, 256, 4>, 256);
-        else go(norm_quant_blocks_kernel<b, 256, 8>, 256);
+        if (width <= 512) go(norm_quant_blocks_kernel<b, 32, 2, 4>, 256, 8, 4);
+        else if (width <= 1024) go(norm_quant_blocks_kernel<b, 32, 4, 2>, 256, 8, 2);
+        else if (width <= 2048) go(norm_quant_blocks_kernel<b, 256, 1, 5>, 256, 1, 5);
+        else if (width <= 4096) go(norm_quant_blocks_kernel<b, 256, 2, 4>, 256, 1, 4);
+        else if (width <= 8192) go(norm_quant_blocks_kernel<b, 256, 4, 2>, 256, 1, 2);
+        else go(norm_quant_blocks_kernel<b, 512, 4, 1>, 512, 1, 1);
     };
     if (x_bf16) pick(std::true_type{});
     else pick(std::false_type{});

@@ -9,17 +9,22 @@
 #include "elem.cuh"
 #include "internal.h"
 #include "norm.cuh"
-#include "quant_row.cuh"
+#include "quant_fast.cuh"
 #include "rope.cuh"
 #include "sm100.cuh"
 
 namespace kv8 {
 namespace {
 
+using sm100::f2_fma;
+using sm100::f2_mul;
+using sm100::f2_pack;
+using sm100::f2_unpack;
+
 // ---------------------------------------------------------------------------------------------------------
 // kv8_rope
 // ---------------------------------------------------------------------------------------------------------
-constexpr int kRopeThreads = 256, kRopeUnroll = 4, kRopeTable = 1024;  // cos / sin pairs of a block's tokens
+constexpr int kRopeThreads = 256, kRopeUnroll = 2, kRopeTable = 1024;  // items of a thread in flight; cos / sin pairs of a block's tokens
 
 struct RopeArgs {
     const void *x;
@@ -32,19 +37,22 @@ struct RopeArgs {
     int64_t n;
     int heads, at, dim, n_rest;      // n_rest: elements of a head that are not turned, 0 where `rest` is not asked for
     int tokens, head_part, n_parts;  // a block: `tokens` tokens of `head_part` heads, n_parts blocks for all heads
+    uint32_t per_head_inv;           // 2^32 / items of a head, rounded up: (it * that) >> 32 divides the few items of a block
 };
 
 // A block takes some tokens and heads; a thread's item is V values of the rest, V / 2 interleaved pairs, or V pairs
-// of the half layout (V: 16 bytes of x, or one value).  The loads of a thread's items go out together, the first ones
-// before the block's cosines and sines are computed.  An item reads all it needs before it writes, so the rotated part
-// may be written over x.
+// of the half layout (V: 16 bytes of x, or one value).  kRopeUnroll items of a thread are loaded while the ones before
+// are turned and written, the first ones while the block makes its cosines and sines.  An item reads all it needs before it
+// writes, so the rotated part may be written over x.
 template <bool kInBf16, bool kOutBf16, bool kHalf, int V>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a) {
     using In = typename Elem<kInBf16>::T;
     using Out = typename Elem<kOutBf16>::T;
     constexpr int P = kHalf ? V : (V == 1 ? 1 : V / 2);  // pairs of a rotated item
     constexpr bool kTwo = kHalf || V == 1;               // which lies in two places
+    constexpr int U = kRopeUnroll, kStep = kRopeThreads * U;
     __shared__ float2 table[kRopeTable];
+    __shared__ uint64_t turns[KV8_MAX_ROPE / 2];
     const int half_dim = a.dim / 2;
     const int64_t block = blockIdx.x / a.n_parts;
     const int part = (int)(blockIdx.x - block * a.n_parts);
@@ -52,53 +60,51 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     const int tokens = (int)(a.n - n0 < a.tokens ? a.n - n0 : a.tokens);
     const int h0 = part * a.head_part, heads = min(a.head_part, a.heads - h0);
     const int rest_items = a.n_rest / V, per_head = rest_items + half_dim / P, items = tokens * heads * per_head;
-    Raw<kInBf16, V> u[kRopeUnroll], v[kTwo ? kRopeUnroll : 1];
-    auto where = [&](int it, int &t, int &h, int &k) {
-        const int th = it / per_head;
-        k = it - th * per_head;
-        t = th / heads;
-        h = h0 + th - t * heads;
+    const In *xb = static_cast<const In *>(a.x) + n0 * a.x_row + h0 * a.x_head;
+    Out *rest_b = static_cast<Out *>(a.rest) + n0 * a.rest_row + h0 * a.rest_head, *rot_b = static_cast<Out *>(a.rot) + n0 * a.rot_row + h0 * a.rot_head;
+    struct Item {
+        Raw<kInBf16, V> u, v;  // (v: the second place)
+        int t, h, k;           // token and head of the block, number within the head
     };
-    auto fetch = [&](int base) {
+    auto fetch = [&](int base, Item(&w)[U]) {
 #pragma unroll
-        for (int j = 0; j < kRopeUnroll; ++j) {
+        for (int j = 0; j < U; ++j) {
             const int it = base + j * kRopeThreads;
-            if (it >= items) break;
-            int t, h, k;
-            where(it, t, h, k);
-            const In *x = static_cast<const In *>(a.x) + (n0 + t) * a.x_row + h * a.x_head;
-            const int i = (k - rest_items) * P;
-            const int e = k < rest_items ? (k * V < a.at ? k * V : k * V + a.dim) : a.at + (kHalf ? i : 2 * i);
-            u[j].load(x + e);
-            if constexpr (kTwo)
-                if (k >= rest_items) v[j].load(x + e + (kHalf ? half_dim : 1));
+            if (it < items) {
+                const int th = per_head == 1 ? it : (int)__umulhi((uint32_t)it, a.per_head_inv);
+                w[j].k = it - th * per_head;
+                w[j].t = tokens == 1 ? 0 : th / heads;
+                w[j].h = th - w[j].t * heads;
+                const In *x = xb + w[j].t * a.x_row + w[j].h * a.x_head;
+                const int i = (w[j].k - rest_items) * P;
+                const int e = w[j].k < rest_items ? (w[j].k * V < a.at ? w[j].k * V : w[j].k * V + a.dim) : a.at + (kHalf ? i : 2 * i);
+                w[j].u.load(x + e);
+                if constexpr (kTwo)
+                    if (w[j].k >= rest_items) w[j].v.load(x + e + (kHalf ? half_dim : 1));
+            }
         }
     };
-    fetch(threadIdx.x);
-    for (int i = threadIdx.x; i < tokens * half_dim; i += kRopeThreads) {
-        const int t = i / half_dim, k = i - t * half_dim;
-        table[i] = turn_cos_sin(__ldg(a.position + n0 + t), turn_of(__ldg(a.inv_freq + k)), a.scale);
-    }
-    __syncthreads();
-    for (int base = threadIdx.x; base < items; base += kRopeThreads * kRopeUnroll) {
-        if (base != threadIdx.x) fetch(base);
+    auto turn = [&](int base, const Item(&w)[U]) {
 #pragma unroll
-        for (int j = 0; j < kRopeUnroll; ++j) {
-            const int it = base + j * kRopeThreads;
-            if (it >= items) break;
-            int t, h, k;
-            where(it, t, h, k);
+        for (int j = 0; j < U; ++j) {
+            if (base + j * kRopeThreads >= items) continue;
             float x[V], y[V];
-            u[j].get(x);
-            if (k < rest_items) {
-                store<V>(static_cast<Out *>(a.rest) + (n0 + t) * a.rest_row + h * a.rest_head + k * V, x);
+            if (w[j].k < rest_items) {
+                Out *o = rest_b + w[j].t * a.rest_row + w[j].h * a.rest_head + w[j].k * V;
+                if constexpr (kInBf16 == kOutBf16) {
+                    w[j].u.store(o);
+                } else {
+                    w[j].u.get(x);
+                    store<V>(o, x);
+                }
                 continue;
             }
-            const int i = (k - rest_items) * P;
-            Out *o = static_cast<Out *>(a.rot) + (n0 + t) * a.rot_row + h * a.rot_head + (kHalf ? i : 2 * i);
-            const float2 *cs = table + t * half_dim + i;
+            w[j].u.get(x);
+            const int i = (w[j].k - rest_items) * P;
+            Out *o = rot_b + w[j].t * a.rot_row + w[j].h * a.rot_head + (kHalf ? i : 2 * i);
+            const float2 *cs = table + w[j].t * half_dim + i;
             if constexpr (kTwo) {
-                v[j].get(y);
+                w[j].v.get(y);
 #pragma unroll
                 for (int m = 0; m < V; ++m) {
                     const float p = x[m], q = y[m];
@@ -117,6 +123,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
                 store<V>(o, x);
             }
         }
+    };
+    Item w0[U], w1[U];
+    fetch(threadIdx.x, w0);
+    if (threadIdx.x < half_dim) turns[threadIdx.x] = turn_of(__ldg(a.inv_freq + threadIdx.x));
+    __syncthreads();
+    for (int i = threadIdx.x; i < tokens * half_dim; i += kRopeThreads) {
+        const int t = i / half_dim;
+        table[i] = turn_cos_sin(__ldg(a.position + n0 + t), turns[i - t * half_dim], a.scale);
+    }
+    __syncthreads();
+    for (int base = threadIdx.x; base < items; base += 2 * kStep) {
+        fetch(base + kStep, w1);
+        turn(base, w0);
+        fetch(base + 2 * kStep, w0);
+        turn(base + kStep, w1);
     }
 }
 
@@ -133,11 +154,12 @@ cudaError_t rope_go(const RopeArgs &a, bool wide, int64_t blocks, cudaStream_t s
 // kv8_norm_rope_rows
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kRowsThreads = 256;
+constexpr int rows_blocks(bool bf16) { return bf16 ? 3 : 2; }  // blocks an SM, by their registers
 
 // One warp a row, grid-stride: lane l holds latent elements 8 l .. and 256 + 8 l .., and rotary elements 2 l, 2 l + 1
 // (a pair of the interleaved layout; of the half layout the partners sit in lane l xor 16).
 template <bool kBf16, bool kHalf>
-__global__ void __launch_bounds__(kRowsThreads) norm_rope_rows_kernel(
+__global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_rows_kernel(
     const void *__restrict__ xv, int64_t n, int64_t x_stride, const float *__restrict__ norm_w, float eps,
     const int32_t *__restrict__ position, const float *__restrict__ inv_freq, float rope_scale,
     const int64_t *__restrict__ dst, uint8_t *__restrict__ kv8, float *__restrict__ kv_scale, int64_t cache_rows,
@@ -152,6 +174,14 @@ __global__ void __launch_bounds__(kRowsThreads) norm_rope_rows_kernel(
         turn[1] = turn_of(__ldg(inv_freq + 2 * (lane & 15) + 1));
     } else {
         turn[0] = turn_of(__ldg(inv_freq + lane));
+    }
+    uint64_t w[8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        Raw<false, 8> a;
+        a.load(norm_w + 256 * j + 8 * lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 * j + i] = a.pair(i);
     }
     // a row's values, position and place, asked for while the row before it is worked on
     Raw<kBf16, 8> raw[2];
@@ -170,9 +200,10 @@ __global__ void __launch_bounds__(kRowsThreads) norm_rope_rows_kernel(
     int64_t r = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
     fetch(r);
     for (; r < n; r += warps) {
-        float y[2][8], k[2];
-        raw[0].get(y[0]);
-        raw[1].get(y[1]);
+        uint64_t z[8];
+        float k[2];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = raw[j / 4].pair(j % 4);
         raw_k.get(k);
         const int32_t pos = next_pos;
         const int64_t row = next_row;
@@ -181,26 +212,12 @@ __global__ void __launch_bounds__(kRowsThreads) norm_rope_rows_kernel(
             if (lane == 0 && err_word) atomicOr(err_word, (int)KV8_ERR_INDEX);
             continue;
         }
-        float ss = 0.f;
+        uint64_t s2 = 0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) ss = fmaf(y[j >> 3][j & 7], y[j >> 3][j & 7], ss);
-        ss = warp_sum(ss);
-        const float ms = ss * (1.f / kKL) + eps;
-        float pre = 1.f, inv = __frsqrt_rn(ms);
-        if (!(ms >= 1e-32f && ss <= 1e30f)) {  // squares that leave the f32 range, infinities, NaN
-            double sd = 0.0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sd += (double)y[j >> 3][j & 7] * (double)y[j >> 3][j & 7];
-            norm_factor_f64(warp_sum_f64(sd) / kKL + (double)eps, pre, inv);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(norm_w + 256 * j + 8 * lane));
-            const float4 b = __ldg(reinterpret_cast<const float4 *>(norm_w + 256 * j + 8 * lane) + 1);
-            const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[j][q] = y[j][q] * pre * inv * w[q];
-        }
+        for (int j = 0; j < 8; ++j) s2 = f2_fma(z[j], z[j], s2);
+        float ss, s_hi;
+        f2_unpack(s2, ss, s_hi);
+        ss = warp_sum(ss + s_hi);
         const float2 c0 = turn_cos_sin(pos, turn[0], rope_scale);
         if constexpr (kHalf) {
             const float2 c1 = turn_cos_sin(pos, turn[1], rope_scale);
@@ -213,21 +230,68 @@ __global__ void __launch_bounds__(kRowsThreads) norm_rope_rows_kernel(
             k[0] = u * c0.x - v * c0.y;
             k[1] = u * c0.y + v * c0.x;
         }
-        float amax = finite_abs_max(finite_abs_max(0.f, k[0]), k[1]);
+        const float ms = ss * (1.f / kKL) + eps;
+        float pre = 1.f, inv = __frsqrt_rn(ms);
+        if (!(ms >= 1e-32f && ss <= 1e30f)) {  // squares that leave the f32 range, infinities, NaN
+            double sd = 0.0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) amax = finite_abs_max(amax, y[j >> 3][j & 7]);
-        amax = warp_max(amax);
-        float qpre, mul, sc;
-        row_quant_factors(amax, qpre, mul, sc);
+            for (int j = 0; j < 8; ++j) {
+                float lo, hi;
+                f2_unpack(z[j], lo, hi);
+                sd += (double)lo * (double)lo + (double)hi * (double)hi;
+            }
+            norm_factor_f64(warp_sum_f64(sd) / kKL + (double)eps, pre, inv);
+        } else if (ss < 1e-30f) {  // (values so small that a product with the weight could lose bits)
+            pre = 18446744073709551616.f;  // 2^64
+            inv *= 5.421010862427522e-20f;
+        }
+        if (pre != 1.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = f2_mul(z[j], f2_pack(pre, pre));
+        }
+        // the latent part's maximum before its factor, so that factor and quantizer are one product
+        float amax = 0.f, mul, sc;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            z[j] = f2_mul(z[j], w[j]);
+            float lo, hi;
+            f2_unpack(z[j], lo, hi);
+            amax = abs_max_nan(amax, lo, hi);
+        }
+        amax = warp_max_nan(abs_max_nan(amax * inv, k[0], k[1]));
+        uint2 b[2];
+        uint32_t bk;
+        const bool plain = plain_factors(amax, mul, sc);
+        const float whole = mul * inv;
+        if (plain && whole <= 3.402823466e38f) {
+            const uint64_t f = f2_pack(whole, whole);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                b[j] = make_uint2(enc2_scaled(z[4 * j], f) | enc2_scaled(z[4 * j + 1], f) << 16, enc2_scaled(z[4 * j + 2], f) | enc2_scaled(z[4 * j + 3], f) << 16);
+            bk = enc2_finite(k[0] * mul, k[1] * mul);
+        } else {
+            float y[16], qpre;
+            amax = finite_abs_max(finite_abs_max(0.f, k[0]), k[1]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f2_unpack(z[j], y[2 * j], y[2 * j + 1]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                y[j] *= inv;
+                amax = finite_abs_max(amax, y[j]);
+            }
+            amax = warp_max(amax);
+            row_quant_factors(amax, qpre, mul, sc);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                b[j] = make_uint2(enc4(scale4(make_float4(y[8 * j], y[8 * j + 1], y[8 * j + 2], y[8 * j + 3]), qpre, mul)),
+                                  enc4(scale4(make_float4(y[8 * j + 4], y[8 * j + 5], y[8 * j + 6], y[8 * j + 7]), qpre, mul)));
+            bk = enc2(__fmul_rn(__fmul_rn(k[0], qpre), mul), __fmul_rn(__fmul_rn(k[1], qpre), mul));
+        }
         if (lane == 0) kv_scale[row] = sc;
         uint8_t *q = kv8 + row * kRow;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<uint2 *>(q + 256 * j + 8 * lane) =
-                make_uint2(enc4(scale4(make_float4(y[j][0], y[j][1], y[j][2], y[j][3]), qpre, mul)),
-                           enc4(scale4(make_float4(y[j][4], y[j][5], y[j][6], y[j][7]), qpre, mul)));
-        *reinterpret_cast<uint16_t *>(q + kKL + 2 * lane) =
-            (uint16_t)enc2(__fmul_rn(__fmul_rn(k[0], qpre), mul), __fmul_rn(__fmul_rn(k[1], qpre), mul));
+        *reinterpret_cast<uint2 *>(q + 8 * lane) = b[0];
+        *reinterpret_cast<uint2 *>(q + 256 + 8 * lane) = b[1];
+        *reinterpret_cast<uint16_t *>(q + kKL + 2 * lane) = (uint16_t)bk;
     }
 }
 
@@ -251,9 +315,10 @@ cudaError_t launch_rope(const void *x, int x_bf16, int64_t n, int heads, int wid
     const bool wide = odd % 8 == 0 && at % 16 == 0;
     const int V = wide ? (x_bf16 ? 8 : 4) : 1;
     const int per_head = a.n_rest / V + (half_layout ? rope_dim / 2 / V : rope_dim / (wide ? V : 2));
-    // a block's items: four a thread, or one where that many blocks would leave SMs without work
-    const int64_t all = n * heads * (int64_t)per_head;
-    const int target = all >= (int64_t)device_sm_count() * kRopeThreads * kRopeUnroll ? kRopeThreads * kRopeUnroll : kRopeThreads;
+    a.per_head_inv = (uint32_t)(((1ull << 32) + per_head - 1) / per_head);
+    // a block's items: sixteen a thread, or fewer where that would leave fewer than two blocks an SM
+    const int64_t each = n * heads * (int64_t)per_head / ((int64_t)device_sm_count() * 2 * kRopeThreads);
+    const int target = kRopeThreads * (int)(each < 1 ? 1 : each < 16 ? each : 16);
     int hp = target / per_head;
     a.head_part = hp < 1 ? 1 : hp < heads ? hp : heads;
     a.n_parts = (heads + a.head_part - 1) / a.head_part;
@@ -279,7 +344,7 @@ cudaError_t launch_norm_rope_rows(const void *x, int x_bf16, int64_t n, int64_t 
                                   const int64_t *dst, uint8_t *kv8, float *kv_scale, int64_t cache_rows, int *err_word,
                                   cudaStream_t st) {
     int64_t blocks = (n + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
-    const int64_t cap = (int64_t)device_sm_count() * 4;
+    const int64_t cap = (int64_t)device_sm_count() * rows_blocks(x_bf16 != 0);
     if (blocks > cap) blocks = cap;
     auto go = [&](auto kernel) {
         kernel<<<(unsigned)blocks, kRowsThreads, 0, st>>>(x, n, x_stride, norm_w, eps, position, inv_freq, rope_scale, dst,
