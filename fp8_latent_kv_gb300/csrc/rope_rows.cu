@@ -179,9 +179,11 @@ cudaError_t rope_go(const RopeArgs &a, bool wide, int64_t blocks, cudaStream_t s
 // kv8_norm_rope_rows
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kRowsThreads = 256;
-constexpr int rows_blocks(bool bf16) { return bf16 ? 3 : 2; }  // blocks an SM, by their registers
+constexpr int kRowsAhead = 3;  // rows of a warp in shared memory or on their way
+constexpr int rows_blocks(bool) { return 3; }  // blocks an SM
+constexpr int row_bytes(bool bf16) { return kRow * (bf16 ? 2 : 4); }
 
-// One warp a row, grid-stride: lane l holds latent elements 8 l .. and 256 + 8 l .., and rotary elements 2 l, 2 l + 1
+// One warp a row, grid-stride, the next rows on their way to shared memory meanwhile (each warp for itself): lane l holds latent elements 8 l .. and 256 + 8 l .., and rotary elements 2 l, 2 l + 1
 // (a pair of the interleaved layout; of the half layout the partners sit in lane l xor 16).
 template <bool kBf16, bool kHalf>
 __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_rows_kernel(
@@ -208,31 +210,50 @@ __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_ro
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[4 * j + i] = a.pair(i);
     }
-    // a row's values, position and place, asked for while the row before it is worked on
-    Raw<kBf16, 8> raw[2];
-    Raw<kBf16, 2> raw_k;
+    extern __shared__ __align__(16) uint8_t rows_smem[];
+    uint8_t *ring = rows_smem + (threadIdx.x >> 5) * (kRowsAhead * row_bytes(kBf16));
     int32_t next_pos;
     int64_t next_row;
-    auto fetch = [&](int64_t r) {
-        if (r >= n) return;
-        const T *xr = x + r * x_stride;
-        raw[0].load(xr + 8 * lane);
-        raw[1].load(xr + 256 + 8 * lane);
-        raw_k.load(xr + kKL + 2 * lane);
-        next_pos = __ldg(position + r);
-        next_row = __ldg(dst + r);
+    auto ask = [&](int64_t r, int slot) {  // (a group for every row, empty past the last one)
+        if (r < n) {
+            const uint8_t *from = reinterpret_cast<const uint8_t *>(x + r * x_stride);
+#pragma unroll
+            for (int c = 0; c < row_bytes(kBf16); c += 512)
+                if (c + 16 * lane < row_bytes(kBf16)) sm100::cp_async_16(ring + slot * row_bytes(kBf16) + c + 16 * lane, from + c + 16 * lane);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto ask_place = [&](int64_t r) {
+        if (r < n) {
+            next_pos = __ldg(position + r);
+            next_row = __ldg(dst + r);
+        }
     };
     int64_t r = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
-    fetch(r);
-    for (; r < n; r += warps) {
+#pragma unroll
+    for (int i = 0; i < kRowsAhead - 1; ++i) ask(r + i * warps, i);
+    ask_place(r);
+    for (int slot = 0; r < n; r += warps, slot = (slot + 1) % kRowsAhead) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRowsAhead - 2) : "memory");
+        __syncwarp();
         uint64_t z[8];
         float k[2];
+        {
+            const T *xr = reinterpret_cast<const T *>(ring + slot * row_bytes(kBf16));
+            Raw<kBf16, 8> raw[2];
+            Raw<kBf16, 2> raw_k;
+            raw[0].load(xr + 8 * lane);
+            raw[1].load(xr + 256 + 8 * lane);
+            raw_k.load(xr + kKL + 2 * lane);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = raw[j / 4].pair(j % 4);
-        raw_k.get(k);
+            for (int j = 0; j < 8; ++j) z[j] = raw[j / 4].pair(j % 4);
+            raw_k.get(k);
+        }
+        __syncwarp();
+        ask(r + (kRowsAhead - 1) * warps, (slot + kRowsAhead - 1) % kRowsAhead);  // (the slot of the row before this one)
         const int32_t pos = next_pos;
         const int64_t row = next_row;
-        fetch(r + warps);
+        ask_place(r + warps);
         if (row < 0 || row >= cache_rows) {
             if (lane == 0 && err_word) atomicOr(err_word, (int)KV8_ERR_INDEX);
             continue;
@@ -373,15 +394,16 @@ cudaError_t launch_norm_rope_rows(const void *x, int x_bf16, int64_t n, int64_t 
     int64_t blocks = (n + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
     const int64_t cap = (int64_t)device_sm_count() * rows_blocks(x_bf16 != 0);
     if (blocks > cap) blocks = cap;
-    auto go = [&](auto kernel) {
-        kernel<<<(unsigned)blocks, kRowsThreads, 0, st>>>(x, n, x_stride, norm_w, eps, position, inv_freq, rope_scale, dst,
-                                                          kv8, kv_scale, cache_rows, err_word);
+    const int smem = kRowsThreads / 32 * kRowsAhead * row_bytes(x_bf16 != 0);
+    auto go = [&](auto kernel) -> cudaError_t {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kernel<<<(unsigned)blocks, kRowsThreads, smem, st>>>(x, n, x_stride, norm_w, eps, position, inv_freq, rope_scale, dst, kv8,
+                                                             kv_scale, cache_rows, err_word);
+        return cudaGetLastError();
     };
-    if (x_bf16)
-        half_layout ? go(norm_rope_rows_kernel<true, true>) : go(norm_rope_rows_kernel<true, false>);
-    else
-        half_layout ? go(norm_rope_rows_kernel<false, true>) : go(norm_rope_rows_kernel<false, false>);
-    return cudaGetLastError();
+    if (x_bf16) return half_layout ? go(norm_rope_rows_kernel<true, true>) : go(norm_rope_rows_kernel<true, false>);
+    return half_layout ? go(norm_rope_rows_kernel<false, true>) : go(norm_rope_rows_kernel<false, false>);
 }
 
 }  // namespace kv8
