@@ -364,9 +364,19 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                     for (int u = 0; u < S::kBatch; ++u) {
                         if (u < n) {
 #pragma unroll
-                            for (int i = 0; i < S::kChunk / 2; ++i)
-                                acc[j / 2 + i] = f2_fma(f2_pack(__uint_as_float(v[u][i / 8][2 * (i % 8)]), __uint_as_float(v[u][i / 8][2 * (i % 8) + 1])),
-                                                        factor(u, j / 2 + i), acc[j / 2 + i]);
+                            for (int i = 0; i < S::kChunk / 2; ++i) {
+                                const uint32_t x = v[u][i / 8][2 * (i % 8)], y = v[u][i / 8][2 * (i % 8) + 1];
+                                uint64_t &sum = acc[j / 2 + i];
+                                const uint64_t f = factor(u, j / 2 + i);
+                                if constexpr (kSwap) {
+                                    sum = f2_fma(f2_pack(__uint_as_float(x), __uint_as_float(y)), f, sum);
+                                } else {  // (one factor: plain FMAs keep the tensor cores busier; 8192 x 4096 x 16384: 385 us packed, 364 plain)
+                                    float lo, hi, f0, f1;
+                                    f2_unpack(sum, lo, hi);
+                                    f2_unpack(f, f0, f1);
+                                    sum = f2_pack(fmaf(__uint_as_float(x), f0, lo), fmaf(__uint_as_float(y), f1, hi));
+                                }
+                            }
                         }
                     }
                 }
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                 for (int c = 0; c < S::kCols; c += kPart) {
                     const int n0 = tq * kNT + col0 + c;
                     uint8_t *st = staging + ((warp - kFirst) * 2 + (parts++ & 1)) * 4096;
-                    if (lane == 0) bulk_wait_read<1>();
+                    if (elect_one()) bulk_wait_read<1>();
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -508,7 +518,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                     if (a.tma_out) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (elect_one()) {
                             if (m0 < a.M && n0 < a.N) tma_store_2d(&map_out, st, n0, m0);
                             bulk_commit();  // (an empty group where nothing is stored: the count of groups goes by the parts)
                         }
@@ -524,7 +534,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
             }
         }
         if constexpr (!kSplit && !kSwap) {
-            if (lane == 0) bulk_wait();
+            if (elect_one()) bulk_wait();
             __syncwarp();
         }
     }
