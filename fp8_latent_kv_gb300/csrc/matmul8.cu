@@ -624,6 +624,61 @@ cudaError_t mm_typed(const MmCall &c, int blocks) {
 
 int tiles_of(int n, int t) { return (n + t - 1) / t; }
 
+// The forms of the kernel, and what each takes: microseconds, fitted to its times over M from 1 to 2048, N from 576 to 24576 and
+// K from 512 to 8192 (rms 5 to 15 %).  A launch has a fixed part; each round of its tiles takes `kb` a K block (few rows: `shared`
+// times that where two blocks share an SM, or as long as DRAM takes for the blocks' 16 KB of weight each) and `round`.  A split
+// adds its exchange.  Both sides of the borders, in us: 64 x 24576 x 2048: tiles of 64 rows 14.4, of 32 19.2; 64 x 2048 x 2048:
+// 7.1 and 5.7.  128 x 8192 x 8192: 128-wide tiles whole 25.6, in halves of K 20.4; 128 x 8192 x 2048: 8.2 and 9.5.
+// 2048 x 8192 x 2048: pairs of 256 32.9, 128-wide 41.4; 128 x 24576 x 8192: 58.1 and 52.3.
+enum MmForm { kFew16, kFew32, kFew64, kSplit128, kWhole128, kPair256, kForms };
+struct MmTimes {
+    double fixed, kb, round, shared;
+};
+constexpr MmTimes kTimes[kForms] = {{-0.9, 0.264, 4.0, 1.67}, {-0.7, 0.266, 4.0, 1.6}, {0.6, 0.314, 4.0, 1.9},
+                                    {5.4, 0.355, 0.0, 1.0},   {2.6, 0.332, 0.54, 1.0}, {2.7, 0.395, 1.46, 1.0}};
+constexpr double kSplitTime[4] = {0.0, 1.0, 0.9, 1.4};  // by log2 of the split
+constexpr double kWeightTime = 0.0026;                  // 16 KB of weight from DRAM
+
+struct MmPlan {
+    MmForm form;
+    int p_tiles, q_tiles, split, blocks;
+    double us;
+};
+
+MmPlan mm_plan(int M, int N, int kb, int sms) {
+    MmPlan best{};
+    best.us = 1e30;
+    for (int f = 0; f < kForms; ++f) {
+        MmPlan p{};
+        p.form = (MmForm)f;
+        const bool few = f <= kFew64;
+        const int nt = f == kFew16 ? 16 : f == kFew32 ? 32 : 64;
+        if (few && M > 16 * nt) continue;
+        p.p_tiles = few ? tiles_of(N, kMmRows) : tiles_of(M, f == kPair256 ? 256 : kMmRows);
+        p.q_tiles = few ? tiles_of(M, nt) : tiles_of(N, f == kPair256 ? 256 : 128);
+        const int64_t tiles = (int64_t)p.p_tiles * p.q_tiles;
+        const int slots = few ? 2 * sms : f == kPair256 ? sms / 2 : sms;  // tiles at a time
+        for (int log = 0; log < (few || f == kSplit128 ? 4 : 1); ++log) {
+            p.split = 1 << log;
+            if (f == kSplit128 && log == 0) continue;
+            // (clusters of 8 find room for 256 blocks of few rows; of the 128-wide ones 16 no longer fitted at once)
+            if (log > 0 && (kb < 2 * p.split || tiles * p.split > (log < 3 ? slots : few ? 256 : 96))) break;
+            if (tiles * p.split > 0x3fffffff) break;
+            const int64_t rounds = (tiles * p.split + slots - 1) / slots;
+            const double at_once = (double)(tiles * p.split < slots ? tiles * p.split : slots) / p.q_tiles;
+            double each = kTimes[f].kb * (tiles * p.split > sms ? kTimes[f].shared : 1.0);
+            if (few && at_once * kWeightTime > each) each = at_once * kWeightTime;
+            p.us = kTimes[f].fixed + rounds * ((kb + p.split - 1) / p.split * each + kTimes[f].round) + kSplitTime[log];
+            if (p.us < best.us) {
+                best = p;
+                const int64_t launch = few || f == kSplit128 ? tiles * p.split : tiles < slots ? tiles : slots;
+                best.blocks = (int)(f == kPair256 ? 2 * launch : launch);
+            }
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 cudaError_t launch_matmul8(const uint8_t *a8, int64_t a_stride, const float *a_scale, int64_t a_scale_stride, int M, int N,
@@ -633,32 +688,16 @@ cudaError_t launch_matmul8(const uint8_t *a8, int64_t a_stride, const float *a_s
     c.a8 = a8, c.w8 = w8, c.a_stride = a_stride, c.K = K, c.bf16 = out_bf16 != 0, c.st = st;
     c.a.a_scale = a_scale, c.a.a_scale_stride = a_scale_stride, c.a.w_scale = w_scale;
     c.a.out = out, c.a.out_stride = out_stride, c.a.M = M, c.a.N = N, c.a.kb = tiles_of(K, kMmBlk), c.a.err_word = err_word;
-    const int sms = device_sm_count();
-    if (M <= 64) {
-        const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64, slots = 2 * sms;
-        c.a.p_tiles = tiles_of(N, kMmRows), c.a.q_tiles = 1;
-        c.a.split = 1;
-        while (c.a.split < 8 && c.a.p_tiles * c.a.split * 2 <= slots && c.a.kb >= c.a.split * 4) c.a.split *= 2;
-        const int blocks = c.a.p_tiles * c.a.split;
-        if (nt == 16) return mm_typed<true, 16, 5, 2, true>(c, blocks);
-        if (nt == 32) return mm_typed<true, 32, 4, 2, true>(c, blocks);
-        return mm_typed<true, 64, 3, 2, true>(c, blocks);
+    const MmPlan p = mm_plan(M, N, c.a.kb, device_sm_count());
+    c.a.p_tiles = p.p_tiles, c.a.q_tiles = p.q_tiles, c.a.split = p.split;
+    switch (p.form) {
+        case kFew16: return mm_typed<true, 16, 5, 2, true>(c, p.blocks);
+        case kFew32: return mm_typed<true, 32, 4, 2, true>(c, p.blocks);
+        case kFew64: return mm_typed<true, 64, 3, 2, true>(c, p.blocks);
+        case kSplit128: return mm_typed<false, 128, 4, 1, true>(c, p.blocks);
+        case kWhole128: return mm_typed<false, 128, 4, 1, false>(c, p.blocks);
+        default: return mm_typed<false, 256, 4, 1, false>(c, p.blocks);
     }
-    const int rows = tiles_of(M, kMmRows), narrow = rows * tiles_of(N, 128), pairs = tiles_of(M, 256) * tiles_of(N, 256);
-    if (narrow * 2 <= sms && c.a.kb >= 4) {
-        c.a.p_tiles = rows, c.a.q_tiles = tiles_of(N, 128);
-        c.a.split = 1;
-        while (c.a.split < 8 && narrow * c.a.split * 2 <= sms && c.a.kb >= c.a.split * 4) c.a.split *= 2;
-        return mm_typed<false, 128, 4, 1, true>(c, narrow * c.a.split);
-    }
-    c.a.split = 1;
-    // in units of a 128 x 128 tile's time: rounds of the persistent blocks
-    if (2 * tiles_of(pairs, sms / 2) <= tiles_of(narrow, sms)) {
-        c.a.p_tiles = tiles_of(M, 256), c.a.q_tiles = tiles_of(N, 256);
-        return mm_typed<false, 256, 4, 1, false>(c, 2 * (pairs < sms / 2 ? pairs : sms / 2));
-    }
-    c.a.p_tiles = rows, c.a.q_tiles = tiles_of(N, 128);
-    return mm_typed<false, 128, 4, 1, false>(c, narrow < sms ? narrow : sms);
 }
 
 }  // namespace kv8
