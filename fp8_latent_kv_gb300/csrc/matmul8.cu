@@ -28,7 +28,7 @@ constexpr int kMmRows = 128;           // MMA M
 constexpr int kScaleBlocks = 4, kScaleSlots = 4;  // K blocks whose scales travel together, and slots of them
 constexpr int kFirst = 4;              // the first warp that adds; warps 0 to 2 bring operands, issue products, bring scales
 constexpr int kRegsLoad = 40, kRegsAdd = 232;  // registers a thread of a pair's twelve warps: 4 x 40 + 8 x 232 = 12 x 168
-constexpr int kGroupTiles = 16;        // row tiles that are walked together, for the L2's sake
+constexpr int kGroupRows = 2048;       // rows of tiles that are walked together, for the L2's sake
 
 struct MmArgs {
     const float *a_scale;
@@ -156,12 +156,13 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     if constexpr (kPair || kSplit) cluster_arrive_relaxed();
     if constexpr (kPair) cluster_wait();  // the other block's barriers stand
 
-    // tile -> (tile of the MMA rows' operand, tile of the columns'): kGroupTiles row tiles at a time, the columns' outside
+    // tile -> (tile of the MMA rows' operand, tile of the columns'): kGroupRows rows at a time, the columns' outside
     auto place = [&](int tile, int &tp, int &tq) {
-        const int per = kGroupTiles * a.q_tiles, g = tile / per, r = tile - g * per;
-        const int rows = min(kGroupTiles, a.p_tiles - g * kGroupTiles);
+        constexpr int kGroup = kGroupRows / kRows;
+        const int per = kGroup * a.q_tiles, g = tile / per, r = tile - g * per;
+        const int rows = min(kGroup, a.p_tiles - g * kGroup);
         tq = r / rows;
-        tp = g * kGroupTiles + r - tq * rows;
+        tp = g * kGroup + r - tq * rows;
     };
 
     if (warp == 0) {
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     } else if (warp == 1) {
         // ---- products
         if constexpr (kPair) fewer_registers<kRegsLoad>();
+        grid_dependency_wait();  // (so that the time limits of its waits do not count the kernel before)
         if (!kPair || rank == 0) {
             constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kNT, false, false);
             const uint64_t desc0 = smem_desc(smem_u32(smem), 0, 1024, kSw128);

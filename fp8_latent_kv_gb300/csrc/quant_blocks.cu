@@ -9,6 +9,7 @@
 // its squares and its scaling.
 #include "elem.cuh"
 #include "internal.h"
+#include "launch.h"
 #include "norm.cuh"
 #include "quant_fast.cuh"
 
@@ -105,6 +106,8 @@ __global__ void __launch_bounds__(kQThreads) quant_blocks_kernel(const void *__r
                                                                  int col_parts) {
     using T = typename Elem<kBf16>::T;
     __shared__ float sc[kQCols][kQRows];
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t tile = blockIdx.x / col_parts;
     const int kb0 = (int)(blockIdx.x - tile * col_parts) * kQCols;
@@ -153,6 +156,8 @@ __global__ void __launch_bounds__(kT < kQThreads ? kQThreads : kT, kBlocks)
     __shared__ double part_d[2][kT / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = kT == 32 ? lane : threadIdx.x;
     const T *x = static_cast<const T *>(xv);
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
     Raw<kBf16, 8> raw[kJ];
     auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -248,29 +253,25 @@ cudaError_t launch_quant_blocks(const void *x, int x_bf16, int64_t n, int width,
     if (!norm_w) {
         const int parts = (width + kQCols * kQBlk - 1) / (kQCols * kQBlk);
         const int64_t blocks = (n + kQRows - 1) / kQRows * parts;
-        if (x_bf16)
-            quant_blocks_kernel<true><<<(unsigned)blocks, kQThreads, 0, st>>>(x, n, width, x_stride, q, scale, scale_stride, parts);
-        else
-            quant_blocks_kernel<false><<<(unsigned)blocks, kQThreads, 0, st>>>(x, n, width, x_stride, q, scale, scale_stride, parts);
-        return cudaGetLastError();
+        return launch_dependent(x_bf16 ? quant_blocks_kernel<true> : quant_blocks_kernel<false>, (unsigned)blocks, kQThreads, 0, st, x, n,
+                                width, x_stride, q, scale, scale_stride, parts);
     }
     // a warp a row up to 1024 columns, from there a block
     auto go = [&](auto kernel, int threads, int rows, int blocks_per_sm) {
         const int64_t need = (n + rows - 1) / rows, most = (int64_t)device_sm_count() * blocks_per_sm;
-        kernel<<<(unsigned)(need < most ? need : most), threads, 0, st>>>(x, n, width, x_stride, norm_w, eps, q, scale, scale_stride);
+        return launch_dependent(kernel, (unsigned)(need < most ? need : most), threads, 0, st, x, n, width, x_stride, norm_w, eps, q, scale,
+                                scale_stride);
     };
     auto pick = [&](auto bf16) {
         constexpr bool b = decltype(bf16)::value;
-        if (width <= 512) go(norm_quant_blocks_kernel<b, 32, 2, 4>, 256, 8, 4);
-        else if (width <= 1024) go(norm_quant_blocks_kernel<b, 32, 4, 2>, 256, 8, 2);
-        else if (width <= 2048) go(norm_quant_blocks_kernel<b, 256, 1, 5>, 256, 1, 5);
-        else if (width <= 4096) go(norm_quant_blocks_kernel<b, 256, 2, 4>, 256, 1, 4);
-        else if (width <= 8192) go(norm_quant_blocks_kernel<b, 256, 4, 2>, 256, 1, 2);
-        else go(norm_quant_blocks_kernel<b, 512, 4, 1>, 512, 1, 1);
+        if (width <= 512) return go(norm_quant_blocks_kernel<b, 32, 2, 4>, 256, 8, 4);
+        if (width <= 1024) return go(norm_quant_blocks_kernel<b, 32, 4, 2>, 256, 8, 2);
+        if (width <= 2048) return go(norm_quant_blocks_kernel<b, 256, 1, 5>, 256, 1, 5);
+        if (width <= 4096) return go(norm_quant_blocks_kernel<b, 256, 2, 4>, 256, 1, 4);
+        if (width <= 8192) return go(norm_quant_blocks_kernel<b, 256, 4, 2>, 256, 1, 2);
+        return go(norm_quant_blocks_kernel<b, 512, 4, 1>, 512, 1, 1);
     };
-    if (x_bf16) pick(std::true_type{});
-    else pick(std::false_type{});
-    return cudaGetLastError();
+    return x_bf16 ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace kv8

@@ -8,6 +8,7 @@
 // Both kernels read every value once and write every value once, so DRAM bounds them.
 #include "elem.cuh"
 #include "internal.h"
+#include "launch.h"
 #include "norm.cuh"
 #include "quant_fast.cuh"
 #include "rope.cuh"
@@ -87,6 +88,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
         }
     };
     Item w0[U], w1[U];
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
     fetch(threadIdx.x, w0);
     if (threadIdx.x < half_dim) turns[threadIdx.x] = turn_of(__ldg(a.inv_freq + threadIdx.x));
 
@@ -168,11 +171,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
 
 template <bool kInBf16, bool kOutBf16, bool kHalf>
 cudaError_t rope_go(const RopeArgs &a, bool wide, int64_t blocks, cudaStream_t st) {
-    if (wide)
-        rope_kernel<kInBf16, kOutBf16, kHalf, kInBf16 ? 8 : 4><<<(unsigned)blocks, kRopeThreads, 0, st>>>(a);
-    else
-        rope_kernel<kInBf16, kOutBf16, kHalf, 1><<<(unsigned)blocks, kRopeThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(wide ? rope_kernel<kInBf16, kOutBf16, kHalf, kInBf16 ? 8 : 4> : rope_kernel<kInBf16, kOutBf16, kHalf, 1>,
+                            (unsigned)blocks, kRopeThreads, 0, st, a);
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_ro
     const T *x = static_cast<const T *>(xv);
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kRowsThreads / 32);
+    sm100::grid_dependency_wait();
+    sm100::grid_launch_dependents();
     uint64_t turn[kHalf ? 2 : 1];
     if constexpr (kHalf) {
         turn[0] = turn_of(__ldg(inv_freq + 2 * (lane & 15)));
@@ -396,11 +398,12 @@ cudaError_t launch_norm_rope_rows(const void *x, int x_bf16, int64_t n, int64_t 
     if (blocks > cap) blocks = cap;
     const int smem = kRowsThreads / 32 * kRowsAhead * row_bytes(x_bf16 != 0);
     auto go = [&](auto kernel) -> cudaError_t {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)blocks, kRowsThreads, smem, st>>>(x, n, x_stride, norm_w, eps, position, inv_freq, rope_scale, dst, kv8,
-                                                             kv_scale, cache_rows, err_word);
-        return cudaGetLastError();
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_dependent(kernel, (unsigned)blocks, kRowsThreads, smem, st, x, n, x_stride, norm_w, eps, position, inv_freq, rope_scale,
+                                dst, kv8, kv_scale, cache_rows, err_word);
     };
     if (x_bf16) return half_layout ? go(norm_rope_rows_kernel<true, true>) : go(norm_rope_rows_kernel<true, false>);
     return half_layout ? go(norm_rope_rows_kernel<false, true>) : go(norm_rope_rows_kernel<false, false>);
