@@ -18,6 +18,8 @@
 #include "internal.h"
 #include "sm100_more.cuh"
 
+#include <math.h>
+
 namespace kv8 {
 namespace {
 
@@ -626,20 +628,24 @@ cudaError_t mm_typed(const MmCall &c, int blocks) {
 
 int tiles_of(int n, int t) { return (n + t - 1) / t; }
 
-// The forms of the kernel, and what each takes: microseconds, fitted to its times over M from 1 to 2048, N from 576 to 24576 and
-// K from 512 to 8192 (rms 5 to 15 %).  A launch has a fixed part; each round of its tiles takes `kb` a K block (few rows: `shared`
-// times that where two blocks share an SM, or as long as DRAM takes for the blocks' 16 KB of weight each) and `round`.  A split
-// adds its exchange.  Both sides of the borders, in us: 64 x 24576 x 2048: tiles of 64 rows 14.4, of 32 19.2; 64 x 2048 x 2048:
-// 7.1 and 5.7.  128 x 8192 x 8192: 128-wide tiles whole 25.6, in halves of K 20.4; 128 x 8192 x 2048: 8.2 and 9.5.
+// The forms of the kernel, and what each takes: microseconds, fitted to 1100 of its times over M from 1 to 8192, N from 512 to
+// 24576 and K from 512 to 16384 (each form within 5 % rms; the form of the least estimate took 0.6 % longer than the best one on
+// average, 17 % at most).  A launch has a fixed part, its first round of tiles in it; a further round takes `round`, a K block
+// `kb` (few rows: `shared` times that where two blocks share an SM), or `weight` for each block that streams weights beside it,
+// whichever is more, rounded off between the two by a fourth-power mean.  A split adds its exchange.
+// Both sides of the borders, in us: 64 x 24576 x 2048: tiles of 64 rows 14.4, of 32 19.2; 64 x 2048 x 2048: 7.1 and 5.7.
+// 128 x 8192 x 8192: 128-wide tiles whole 25.6, in halves of K 20.4; 128 x 8192 x 2048: 8.2 and 9.5.
 // 2048 x 8192 x 2048: pairs of 256 32.9, 128-wide 41.4; 128 x 24576 x 8192: 58.1 and 52.3.
 enum MmForm { kFew16, kFew32, kFew64, kSplit128, kWhole128, kPair256, kForms };
 struct MmTimes {
-    double fixed, kb, round, shared;
+    double fixed, kb, round, shared, weight, split[4];  // split: by its log2
 };
-constexpr MmTimes kTimes[kForms] = {{-0.9, 0.264, 4.0, 1.67}, {-0.7, 0.266, 4.0, 1.6}, {0.6, 0.314, 4.0, 1.9},
-                                    {5.4, 0.355, 0.0, 1.0},   {2.6, 0.332, 0.54, 1.0}, {2.7, 0.395, 1.46, 1.0}};
-constexpr double kSplitTime[4] = {0.0, 1.0, 0.9, 1.4};  // by log2 of the split
-constexpr double kWeightTime = 0.0026;                  // 16 KB of weight from DRAM
+constexpr MmTimes kTimes[kForms] = {{3.07, 0.268, 2.55, 1.26, 0.0025, {0.0, 0.99, 1.11, 1.40}},
+                                    {3.25, 0.287, 2.80, 1.34, 0.0026, {0.0, 1.18, 1.18, 1.58}},
+                                    {4.20, 0.365, 4.31, 1.41, 0.0026, {0.0, 1.33, 1.46, 1.44}},
+                                    {6.40, 0.308, 0.0, 1.0, 0.0031, {0.0, 0.0, 0.30, 0.80}},
+                                    {3.07, 0.320, 0.56, 1.0, 0.0, {}},
+                                    {4.19, 0.378, 1.62, 1.0, 0.0, {}}};
 
 struct MmPlan {
     MmForm form;
@@ -666,14 +672,15 @@ MmPlan mm_plan(int M, int N, int kb, int sms) {
             // (clusters of 8 find room for 256 blocks of few rows; of the 128-wide ones 16 no longer fitted at once)
             if (log > 0 && (kb < 2 * p.split || tiles * p.split > (log < 3 ? slots : few ? 256 : 96))) break;
             if (tiles * p.split > 0x3fffffff) break;
-            const int64_t rounds = (tiles * p.split + slots - 1) / slots;
-            const double at_once = (double)(tiles * p.split < slots ? tiles * p.split : slots) / p.q_tiles;
-            double each = kTimes[f].kb * (tiles * p.split > sms ? kTimes[f].shared : 1.0);
-            if (few && at_once * kWeightTime > each) each = at_once * kWeightTime;
-            p.us = kTimes[f].fixed + rounds * ((kb + p.split - 1) / p.split * each + kTimes[f].round) + kSplitTime[log];
+            const int64_t at_once = tiles * p.split < slots ? tiles * p.split : slots, rounds = (tiles * p.split + slots - 1) / slots;
+            const MmTimes &t = kTimes[f];
+            const double own = t.kb * (tiles * p.split > sms ? t.shared : 1.0);
+            const double stream = t.weight * (double)at_once / (few ? p.q_tiles : p.p_tiles);
+            const double each = sqrt(sqrt(own * own * own * own + stream * stream * stream * stream));
+            p.us = t.fixed + rounds * ((kb + p.split - 1) / p.split * each) + (rounds - 1) * t.round + t.split[log];
             if (p.us < best.us) {
                 best = p;
-                const int64_t launch = few || f == kSplit128 ? tiles * p.split : tiles < slots ? tiles : slots;
+                const int64_t launch = few || f == kSplit128 ? tiles * p.split : at_once;
                 best.blocks = (int)(f == kPair256 ? 2 * launch : launch);
             }
         }
