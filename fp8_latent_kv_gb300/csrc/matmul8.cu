@@ -74,14 +74,14 @@ struct MmShape {
     }
 };
 
-// V values of a row, of which `left` exist
-template <int V, typename Out>
-__device__ __forceinline__ void store_row(Out *p, const float (&v)[V], int left, bool wide) {
-    if (wide && left >= V) {
-        store<V>(p, v);
+// four values of a row, of which `left` exist
+template <typename Out>
+__device__ __forceinline__ void store_row(Out *p, const float (&v)[4], int left, bool wide) {
+    if (wide && left >= 4) {
+        store<4>(p, v);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
+        for (int j = 0; j < 4; ++j) {
             const float one[1] = {v[j]};
             if (j < left) store<1>(p + j, one);
         }
@@ -421,26 +421,14 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                 // (rows of out that do not exist have no sums to hand over)
                 const int own = S::own(split);
                 const int cols = kSwap ? min(kNT, a.M - tq * kNT) : min(kNT, a.N - tq * kNT);  // the tile's columns that exist
-                if (split == 1) {
-                    if (ok) {
-                        const int n = kSwap ? tp * kMmRows + row : tq * kNT + col0, m = kSwap ? tq * kNT + col0 : tp * kMmRows + row;
-                        if constexpr (kSwap) {
+                if (kSwap && split == 1) {
+                    const int n = tp * kMmRows + row, m = tq * kNT + col0;
 #pragma unroll
-                            for (int i = 0; i < S::kCols; ++i) {
-                                float v[2];
-                                f2_unpack(acc[i / 2], v[0], v[1]);
-                                const float r[1] = {v[i & 1]};
-                                if (m + i < a.M && n < a.N) store<1>(out + (m + i) * a.out_stride + n, r);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < S::kCols; i += 8) {
-                                float v[8];
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) f2_unpack(acc[i / 2 + j], v[2 * j], v[2 * j + 1]);
-                                if (m < a.M) store_row(out + m * a.out_stride + n + i, v, a.N - n - i, a.tma_out);
-                            }
-                        }
+                    for (int i = 0; i < S::kCols; ++i) {
+                        float v[2];
+                        f2_unpack(acc[i / 2], v[0], v[1]);
+                        const float r[1] = {v[i & 1]};
+                        if (ok && m + i < a.M && n < a.N) store<1>(out + (m + i) * a.out_stride + n, r);
                     }
                     cluster_wait();
                 } else {

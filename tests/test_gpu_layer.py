@@ -290,7 +290,10 @@ def test_one_block_is_the_row_quantizer(lib):
 # -------------------------------------------------------------------------------------------------------------
 SHAPES = [(1, 1, 16), (1, 64, 128), (1, 4096, 16384), (2, 127, 112), (15, 128, 144), (16, 129, 512), (17, 576, 4112), (31, 24576, 256), (33, 200, 2064),
           (48, 8192, 1024), (64, 1343, 1040), (65, 100, 128), (100, 576, 2048), (127, 300, 272), (128, 128, 16), (129, 130, 640), (256, 256, 4096),
-          (300, 1000, 1008), (1000, 576, 4112), (700, 8200, 384), (2048, 4096, 512), (1111, 2345, 1232), (3000, 40, 256), (66, 24576, 2048)]
+          (300, 1000, 1008), (1000, 576, 4112), (700, 8200, 384), (2048, 4096, 512), (1111, 2345, 1232), (3000, 40, 256), (66, 24576, 2048),
+          # every form of the kernel and split of K (on 152 SMs)
+          (3, 8200, 1600), (3, 100, 1024), (65, 4096, 1024), (65, 4096, 2064), (300, 100, 1024), (300, 100, 2064), (37, 24576, 2048), (129, 5000, 6400),
+          (1000, 100, 1600), (700, 100, 2064), (129, 4096, 3200), (300, 900, 3200), (700, 200, 8192), (129, 12200, 528)]
 
 
 def product(lib, a8, sa, w8, sw, ot, stride=0, off=0):
@@ -369,6 +372,69 @@ def test_matmul_is_the_same_every_time_and_row_by_row_alike(lib, M):
     first = product(lib, a8, sa, w8, sw, F32)
     for _ in range(5):
         assert torch.equal(product(lib, a8, sa, w8, sw, F32), first)
+
+
+def test_matmul_scales_with_room_between_blocks(lib):
+    """Scales of more rows than the call takes: the blocks' rows lie further apart."""
+    g = gen(8)
+    for M, N, K in ((5, 300, 1040), (200, 300, 1040), (1500, 2100, 400)):
+        w8, sw = weight(g, N, K, DEV)
+        a8, _ = weight(g, M, K, DEV)
+        room = torch.full((-(-K // BLK), M + 11), float("nan"), device=DEV)
+        room[:, :M] = torch.exp2(torch.randn((-(-K // BLK), M), generator=g)).to(DEV)
+        ref, tol = matmul(a8, room[:, :M], w8, sw, F32)
+        assert bool(((product(lib, a8, room[:, :M], w8, sw, F32).double() - ref).abs() <= tol).all())
+
+
+def test_calls_with_nothing_to_do(lib):
+    """No rows: nothing is read, nothing written."""
+    z = lambda *s, dtype=F32: torch.zeros(s, dtype=dtype, device=DEV)  # noqa: E731
+    u8, i32 = torch.uint8, torch.int32
+    lib.kv8_matmul8(z(0, 256, dtype=u8), z(2, 0), z(128, 256, dtype=u8), z(1, 2), z(0, 128))
+    lib.kv8_quant_blocks(z(0, 256), z(0, 256, dtype=u8), z(2, 0))
+    lib.kv8_rope(z(0, 4, 64), z(0, dtype=i32), z(32), 0, z(0, 4, 64))
+    lib.kv8_norm_rope_rows(z(0, 576), z(512), EPS, z(0, dtype=i32), z(32), z(0, dtype=torch.int64), z(5, 576, dtype=u8), z(5))
+    torch.cuda.synchronize()
+
+
+def codes_on_gpu(rows, cols, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c = torch.randint(0, 256, (rows, cols), dtype=torch.uint8, device=DEV, generator=g)
+    return c.masked_fill_((c & 0x7F) == 0x7F, 0x3A)
+
+
+@pytest.mark.parametrize("M,N,K", [(70000, 40, 32768), (3, 70000, 32768), (300, 70000, 32768)])
+def test_matmul_operands_past_32_bits(lib, M, N, K):
+    a8, w8 = codes_on_gpu(M, K, 1), codes_on_gpu(N, K, 2)
+    g = gen(M)
+    kb = K // BLK
+    sa, sw = (torch.exp2(torch.randn(s, generator=g) - 6).to(DEV) for s in ((kb, M), (-(-N // BLK), kb)))
+    out = torch.empty((M, N), device=DEV)
+    lib.kv8_matmul8(a8, sa, w8, sw, out)
+    rows = torch.arange(M, device=DEV)[-2:] if M > 1000 else torch.arange(2, device=DEV)
+    first = N - N % BLK - BLK  # the last whole block of columns and what follows it
+    first = max(first, 0)
+    ref, tol = matmul(a8[rows], sa[:, rows].contiguous(), w8[first:].contiguous(), sw[first // BLK:].contiguous(), F32)
+    assert bool(((out[rows][:, first:].double() - ref).abs() <= tol).all())
+    assert bool(torch.isfinite(out).all())
+
+
+def test_quant_and_rows_past_32_bits(lib):
+    n, width = 140000, 16384  # 2.3e9 values
+    x = torch.randn((n, width), device=DEV, generator=torch.Generator(device="cuda").manual_seed(1), dtype=BF)
+    q, s = torch.empty((n, width), dtype=torch.uint8, device=DEV), torch.empty((width // BLK, n), device=DEV)
+    rows = torch.tensor([0, 131071, 131072, n - 1], device=DEV)
+    w = torch.ones(width, device=DEV)
+    for norm_w in (None, w):
+        lib.kv8_quant_blocks(x, q, s, norm_w=norm_w)
+        blocks_check(x[rows], norm_w, 1e-6, q[rows], s[:, rows])
+    del x, q, s
+    g = gen(2)
+    xs, w, pos, f, dst, _, _, scale, layout, eps = rows_case(lib, g, 50, BF, 0, 0)
+    kv8, ks = torch.empty((4000000, 576), dtype=torch.uint8, device=DEV), torch.empty(4000000, device=DEV)
+    dst = (3999999 - dst).contiguous()
+    lib.kv8_norm_rope_rows(xs, w, eps, pos, f, dst, kv8, ks, rope_scale=scale)
+    check_codes(kv8[dst], ks[dst], *rows_ref(xs, w, pos, f, scale, layout, eps))
 
 
 def test_matmul_outputs_past_32_bits(lib):
