@@ -72,7 +72,7 @@ __device__ __forceinline__ float quant_blocks_of(const uint64_t (&z)[J][4], floa
         for (int j = 0; j < J; ++j) {
             const float f = __shfl_sync(0xffffffffu, whole, (lane & 16) | j * (16 / J));
             const uint64_t ff = f2_pack(f, f);
-            bytes[j] = make_uint2(enc2_scaled(z[j][0], ff) | enc2_scaled(z[j][1], ff) << 16, enc2_scaled(z[j][2], ff) | enc2_scaled(z[j][3], ff) << 16);
+            bytes[j] = make_uint2(enc4_scaled(z[j][0], z[j][1], ff), enc4_scaled(z[j][2], z[j][3], ff));
         }
         return scale;
     }

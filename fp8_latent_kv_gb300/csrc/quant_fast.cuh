@@ -35,11 +35,19 @@ __device__ __forceinline__ uint32_t enc2_finite(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
     return v;
 }
-// the two halves of a pair times `mul`, encoded
-__device__ __forceinline__ uint32_t enc2_scaled(uint64_t pair, uint64_t mul) {
-    float lo, hi;
-    sm100::f2_unpack(sm100::f2_mul(pair, mul), lo, hi);
-    return enc2_finite(lo, hi);
+// two pairs times `mul`, encoded
+__device__ __forceinline__ uint32_t enc4_scaled(uint64_t p, uint64_t q, uint64_t mul) {
+    float a, b, c, d;
+    sm100::f2_unpack(sm100::f2_mul(p, mul), a, b);
+    sm100::f2_unpack(sm100::f2_mul(q, mul), c, d);
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
 }
 
 }  // namespace kv8

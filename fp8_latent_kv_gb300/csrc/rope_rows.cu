@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_ro
             const uint64_t f = f2_pack(whole, whole);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                b[j] = make_uint2(enc2_scaled(z[4 * j], f) | enc2_scaled(z[4 * j + 1], f) << 16, enc2_scaled(z[4 * j + 2], f) | enc2_scaled(z[4 * j + 3], f) << 16);
+                b[j] = make_uint2(enc4_scaled(z[4 * j], z[4 * j + 1], f), enc4_scaled(z[4 * j + 2], z[4 * j + 3], f));
             bk = enc2_finite(k[0] * mul, k[1] * mul);
         } else {
             float y[16], qpre;
