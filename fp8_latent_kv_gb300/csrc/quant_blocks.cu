@@ -146,12 +146,12 @@ __global__ void __launch_bounds__(kQThreads) quant_blocks_kernel(const void *__r
 // With a norm: kT threads a row (a warp, or the whole block), kJ vectors of eight values each, row after row; a row is loaded
 // while the one before is worked on.
 template <bool kBf16, int kT, int kJ, int kBlocks>
-__global__ void __launch_bounds__(kT < kQThreads ? kQThreads : kT, kBlocks)
+__global__ void __launch_bounds__(kT == 32 ? kQThreads : kT, kBlocks)
     norm_quant_blocks_kernel(const void *__restrict__ xv, int64_t n, int width, int64_t x_stride,
                              const float *__restrict__ norm_w, float eps, uint8_t *__restrict__ q,
                              float *__restrict__ scale, int64_t scale_stride) {
     using T = typename Elem<kBf16>::T;
-    constexpr int kRows = kT < kQThreads ? kQThreads / kT : 1;  // of a block at a time
+    constexpr int kRows = kT == 32 ? kQThreads / kT : 1;  // of a block at a time
     __shared__ float part[2][kT / 32];
     __shared__ double part_d[2][kT / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = kT == 32 ? lane : threadIdx.x;
@@ -256,7 +256,9 @@ cudaError_t launch_quant_blocks(const void *x, int x_bf16, int64_t n, int width,
         return launch_dependent(x_bf16 ? quant_blocks_kernel<true> : quant_blocks_kernel<false>, (unsigned)blocks, kQThreads, 0, st, x, n,
                                 width, x_stride, q, scale, scale_stride, parts);
     }
-    // a warp a row up to 1024 columns, from there a block
+    // A warp a row up to 1024 columns, from there a block, of as few threads as hold a row: what a thread's blocks of columns
+    // share (their maxima, the divisions) is made once for them.  (8192 bf16 rows of 2048: 64 threads 12.8 us, 256 threads 18.0;
+    // of 4096: 128 threads 21.1, 256 threads 25.0; f32 rows of 4096, with twice the bytes on their way: 32.1 and 30.0.)
     auto go = [&](auto kernel, int threads, int rows, int blocks_per_sm) {
         const int64_t need = (n + rows - 1) / rows, most = (int64_t)device_sm_count() * blocks_per_sm;
         return launch_dependent(kernel, (unsigned)(need < most ? need : most), threads, 0, st, x, n, width, x_stride, norm_w, eps, q, scale,
@@ -266,9 +268,14 @@ cudaError_t launch_quant_blocks(const void *x, int x_bf16, int64_t n, int width,
         constexpr bool b = decltype(bf16)::value;
         if (width <= 512) return go(norm_quant_blocks_kernel<b, 32, 2, 4>, 256, 8, 4);
         if (width <= 1024) return go(norm_quant_blocks_kernel<b, 32, 4, 2>, 256, 8, 2);
-        if (width <= 2048) return go(norm_quant_blocks_kernel<b, 256, 1, 5>, 256, 1, 5);
-        if (width <= 4096) return go(norm_quant_blocks_kernel<b, 256, 2, 4>, 256, 1, 4);
-        if (width <= 8192) return go(norm_quant_blocks_kernel<b, 256, 4, 2>, 256, 1, 2);
+        if (width <= 2048) return go(norm_quant_blocks_kernel<b, 64, 4, b ? 12 : 8>, 64, 1, b ? 12 : 8);
+        if (width <= 4096) {
+            if constexpr (b)
+                return go(norm_quant_blocks_kernel<b, 128, 4, 6>, 128, 1, 6);
+            else
+                return go(norm_quant_blocks_kernel<b, 256, 2, 4>, 256, 1, 4);
+        }
+        if (width <= 8192) return go(norm_quant_blocks_kernel<b, 256, 4, b ? 3 : 2>, 256, 1, b ? 3 : 2);
         return go(norm_quant_blocks_kernel<b, 512, 4, 1>, 512, 1, 1);
     };
     return x_bf16 ? pick(std::true_type{}) : pick(std::false_type{});
