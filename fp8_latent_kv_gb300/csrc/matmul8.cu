@@ -14,6 +14,17 @@
 // Where the tiles are fewer than the SMs, a cluster of up to 8 blocks shares a tile along K: each block owns some columns of
 // the tile, the others store their sums for them into its shared memory, and it adds them in the order of their ranks (the
 // result does not depend on timing, and no workspace is needed).
+//
+// What bounds it.  Many rows: a K block's 128 x 256 sums a block leave TMEM while the next one's are made, and with two
+// accumulators of 256 columns filling TMEM the next but one waits for them: 512 cycles of products, about 550 until the end
+// of the products has come to the adding warps and their end back to the issuing one, about 480 of loads and FMAs, for two
+// blocks of K: 770 a block, tensor pipe 68 % active (8192 x 4096 x 16384: 357 us, 3.08 PFLOP/s; products alone 289 us).
+// Taken and left: one block's 128 x 256 tile, which needs 48 KB a stage for the same work where a pair's needs 32 (452 us);
+// sixteen adding warps (409), two MMAs of 128 columns a K block (398), loads of 32 columns at a time (403), or one ahead of the
+// sums (406): TMEM loads in larger bursts hold up the products.  An output as large as the product's work
+// is bound by its writes: 4096 x 32768 x 512 takes 80 us for 268 MB, which a plain fill writes in 70 us.
+// Few rows: the weight's bytes (37 x 24576 x 2048: 13.9 us, 3.8 TB/s; 1 x 4096 x 16384: 14.4 us, 4.7 TB/s), of which about
+// 3 us are a launch's way to its first bytes and 1 to 3 us the exchange of a split.
 #include "elem.cuh"
 #include "internal.h"
 #include "sm100_more.cuh"
@@ -254,8 +265,8 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         }
         __syncwarp();
     } else if (warp == 2) {
-        // ---- scales, kScaleBlocks K blocks at a time.  (Loaded by the warps that add, they would hold up each of their arrivals
-        // until they are there: 8192 x 4096 x 16384 took 449 us so, 356 without any scales.)
+        // ---- scales, kScaleBlocks K blocks at a time.  (Loaded by the warps that add, they held up each of their arrivals
+        // until they were there: 8192 x 4096 x 16384 took 449 us so, 387 from here.)
         if constexpr (kPair) fewer_registers<kRegsLoad>();
         grid_dependency_wait();
         // a8's rows (kSwap: the tile's columns) and w8's blocks of 128; past the ends the last one's are repeated, for sums that are not written

@@ -4,9 +4,10 @@
 //     y = x                                         or  y[i] = x[i] w[i] / sqrt(mean(x^2) + eps)
 //     scale[k] = amax over block k of |y| / 448;    q[i] = e4m3(y[i] * 448 / amax)     (the row quantizer's steps, per block)
 //
-// Every value is read once and every byte written once, so DRAM bounds both kernels: sixteen lanes hold a block (eight
-// values each) in registers between its maximum and its bytes, and a normed row stays in registers between the sum of
-// its squares and its scaling.
+// Every value is read once and every byte written once, so DRAM is the floor of both kernels: eight values a lane stay in
+// registers between their block's maximum and its bytes, and a normed row between the sum of its squares and its scaling.
+// Without a norm they reach it (8192 x 16384: f32 93 us, 7.2 TB/s, part of the bytes still in L2 at the end; bf16 61 us, 6.6 TB/s);
+// with one, a row's two passes over its registers take f32 rows of 16384 to 110 us (6.1 TB/s) and bf16 rows to 90 (4.5).
 #include "elem.cuh"
 #include "internal.h"
 #include "launch.h"

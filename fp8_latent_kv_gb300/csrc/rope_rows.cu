@@ -5,7 +5,10 @@
 //     a = p inv_freq[i];   u' = scale (u cos a - v sin a);   v' = scale (u sin a + v cos a)
 // All arithmetic is f32; an output in bf16 is rounded once.
 //
-// Both kernels read every value once and write every value once, so DRAM bounds them.
+// Both kernels read every value once and write every value once, so DRAM is their floor.  kv8_rope reaches it: 8192 tokens of
+// 128 bf16 heads of 192, 805 MB, in 121 us (6.65 TB/s, a plain copy's rate).  kv8_norm_rope_rows takes 25.3 us for 65536 bf16 rows
+// (114 MB, 4.5 TB/s; issue slots 66 % taken: about 300 instructions a row) and 32.4 us for f32 rows (5.9 TB/s); a half warp a
+// row halves what a row costs once, but holds twice the registers, and was no faster (24.5 us, and 1000 rows 2.6 -> 3.9 us).
 #include "elem.cuh"
 #include "internal.h"
 #include "launch.h"
