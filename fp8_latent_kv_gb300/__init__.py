@@ -362,23 +362,32 @@ def kv8_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0, c
     return torch.tensor(list(table), dtype=torch.float32), scale.value
 
 
+# The four calls below look at all their tensors in one expression, since on a small call the looks take as long as the launch;
+# where it is false, _args and _rows say which tensor it was.
 def kv8_rope(x, position, inv_freq, rope_at: int, rot, rest=None, rope_scale: float = 1.0, layout: int = KV8_ROPE_INTERLEAVED,
              stream=None) -> None:
     """x [n][heads][width] (f32 / bf16, strided) -> rot [n][heads][rope_dim], its elements rope_at.. rotated, and (optional) rest
     [n][heads][width - rope_dim] (both f32 / bf16, strided).  position [n] int32, inv_freq [rope_dim / 2] f32.  In place:
     rot = x[..., rope_at:rope_at + rope_dim]."""
     import torch
-    fn, f = "kv8_rope", (torch.float32, torch.bfloat16)
-    (n, heads, width), dim = x.shape, rot.shape[-1]
-    dev = _args(fn, ("position", position, torch.int32, (n,)), ("inv_freq", inv_freq, torch.float32, (dim // 2,)))
-    _rows(fn, "x", x, f, (n, heads, width), dev)
-    _rows(fn, "rot", rot, f, (n, heads, dim), dev)
-    if rest is not None:
-        _rows(fn, "rest", rest, (rot.dtype,), (n, heads, width - dim), dev)
+    fn, f32, bf16, dev = "kv8_rope", torch.float32, torch.bfloat16, torch.cuda.current_device()
+    (n, heads, width), dim, xt, ot = x.shape, rot.shape[-1], x.dtype, rot.dtype
+    xs, rs = x.stride(), rot.stride()
+    es = (0, 0, 1) if rest is None else rest.stride()
+    if not ((xt is bf16 or xt is f32) and (ot is bf16 or ot is f32) and xs[-1] == rs[-1] == es[-1] == 1 and position.dtype is torch.int32
+            and inv_freq.dtype is f32 and rot.shape == (n, heads, dim) and position.shape == (n,) and inv_freq.shape == (dim // 2,)
+            and position.is_contiguous() and inv_freq.is_contiguous() and x.get_device() == dev and rot.get_device() == dev
+            and position.get_device() == dev and inv_freq.get_device() == dev
+            and (rest is None or (rest.dtype is ot and rest.shape == (n, heads, width - dim) and rest.get_device() == dev))):
+        _args(fn, ("position", position, torch.int32, (n,)), ("inv_freq", inv_freq, f32, (dim // 2,)))
+        _rows(fn, "x", x, (f32, bf16), (n, heads, width), dev)
+        _rows(fn, "rot", rot, (f32, bf16), (n, heads, dim), dev)
+        if rest is not None:
+            _rows(fn, "rest", rest, (ot,), (n, heads, width - dim), dev)
     _check(fn, load().kv8_rope(
-        x.data_ptr(), _dtype_code(x.dtype), n, heads, width, rope_at, dim, x.stride(0), x.stride(1), position.data_ptr(),
-        inv_freq.data_ptr(), rope_scale, layout, rot.data_ptr(), rot.stride(0), rot.stride(1), _ptr(rest),
-        0 if rest is None else rest.stride(0), 0 if rest is None else rest.stride(1), _dtype_code(rot.dtype), _stream(stream, dev)))
+        x.data_ptr(), KV8_BF16 if xt is bf16 else KV8_F32, n, heads, width, rope_at, dim, xs[0], xs[1], position.data_ptr(),
+        inv_freq.data_ptr(), rope_scale, layout, rot.data_ptr(), rs[0], rs[1], None if rest is None else rest.data_ptr(), es[0], es[1],
+        KV8_BF16 if ot is bf16 else KV8_F32, _stream(stream, dev)))
 
 
 def kv8_norm_rope_rows(x, norm_w, eps: float, position, inv_freq, dst_rows, kv8, kv_scale, rope_scale: float = 1.0,
@@ -386,14 +395,21 @@ def kv8_norm_rope_rows(x, norm_w, eps: float, position, inv_freq, dst_rows, kv8,
     """x [n][576] (f32 / bf16, rows strided): norm of 0..511 with norm_w [512] f32, rotation of 512..575 by position [n] int32 and
     inv_freq [32] f32, quantized into cache rows dst_rows [n] int64 of kv8 [rows][576] uint8, kv_scale [rows] f32."""
     import torch
-    fn, f32 = "kv8_norm_rope_rows", torch.float32
-    n, rows = x.shape[0], kv8.shape[0]
-    dev = _args(fn, ("norm_w", norm_w, f32, (KV8_KL,)), ("position", position, torch.int32, (n,)), ("inv_freq", inv_freq, f32, (KV8_KR // 2,)),
-                ("dst_rows", dst_rows, torch.int64, (n,)), ("kv8", kv8, torch.uint8, (rows, KV8_ROW_BYTES)), ("kv_scale", kv_scale, f32, (rows,)),
-                ("err_word", err_word, torch.int32, (1,)))
-    _rows(fn, "x", x, (f32, torch.bfloat16), (n, KV8_ROW_BYTES), dev)
+    fn, f32, bf16, i32, dev = "kv8_norm_rope_rows", torch.float32, torch.bfloat16, torch.int32, torch.cuda.current_device()
+    n, rows, xt, xs = x.shape[0], kv8.shape[0], x.dtype, x.stride()
+    if not ((xt is bf16 or xt is f32) and xs[-1] == 1 and x.shape == (n, KV8_ROW_BYTES) and norm_w.dtype is f32 and inv_freq.dtype is f32
+            and kv_scale.dtype is f32 and position.dtype is i32 and dst_rows.dtype is torch.int64 and kv8.dtype is torch.uint8
+            and norm_w.shape == (KV8_KL,) and inv_freq.shape == (KV8_KR // 2,) and position.shape == (n,) and dst_rows.shape == (n,)
+            and kv8.shape == (rows, KV8_ROW_BYTES) and kv_scale.shape == (rows,) and norm_w.is_contiguous() and inv_freq.is_contiguous()
+            and position.is_contiguous() and dst_rows.is_contiguous() and kv8.is_contiguous() and kv_scale.is_contiguous()
+            and x.get_device() == dev and norm_w.get_device() == dev and position.get_device() == dev and inv_freq.get_device() == dev
+            and dst_rows.get_device() == dev and kv8.get_device() == dev and kv_scale.get_device() == dev and err_word is None):
+        _args(fn, ("norm_w", norm_w, f32, (KV8_KL,)), ("position", position, i32, (n,)), ("inv_freq", inv_freq, f32, (KV8_KR // 2,)),
+              ("dst_rows", dst_rows, torch.int64, (n,)), ("kv8", kv8, torch.uint8, (rows, KV8_ROW_BYTES)), ("kv_scale", kv_scale, f32, (rows,)),
+              ("err_word", err_word, i32, (1,)))
+        _rows(fn, "x", x, (f32, bf16), (n, KV8_ROW_BYTES), dev)
     _check(fn, load().kv8_norm_rope_rows(
-        x.data_ptr(), _dtype_code(x.dtype), n, x.stride(0) if n > 1 else KV8_ROW_BYTES, norm_w.data_ptr(), eps, position.data_ptr(),
+        x.data_ptr(), KV8_BF16 if xt is bf16 else KV8_F32, n, xs[0] if n > 1 else KV8_ROW_BYTES, norm_w.data_ptr(), eps, position.data_ptr(),
         inv_freq.data_ptr(), rope_scale, layout, dst_rows.data_ptr(), kv8.data_ptr(), kv_scale.data_ptr(), rows, _ptr(err_word),
         _stream(stream, dev)))
 
@@ -402,33 +418,43 @@ def kv8_quant_blocks(x, q, scale, norm_w=None, eps: float = 1e-6, stream=None) -
     """x [n][width] (f32 / bf16, rows strided), normed with norm_w [width] f32 where given -> q [n][width] uint8 e4m3, scale
     [ceil(width / 128)][n] f32 (rows strided)."""
     import torch
-    fn, f32 = "kv8_quant_blocks", torch.float32
-    n, width = x.shape
+    fn, f32, bf16, dev = "kv8_quant_blocks", torch.float32, torch.bfloat16, torch.cuda.current_device()
+    (n, width), xt, xs, ss = x.shape, x.dtype, x.stride(), scale.stride()
     blocks = -(-width // KV8_KVB_BLOCK)
-    dev = _args(fn, ("q", q, torch.uint8, (n, width)), ("norm_w", norm_w, f32, (width,)))
-    _rows(fn, "x", x, (f32, torch.bfloat16), (n, width), dev)
-    _rows(fn, "scale", scale, (f32,), (blocks, n), dev)
+    if not ((xt is bf16 or xt is f32) and xs[-1] == 1 and ss[-1] == 1 and q.dtype is torch.uint8 and scale.dtype is f32 and q.shape == (n, width)
+            and scale.shape == (blocks, n) and q.is_contiguous() and x.get_device() == dev and q.get_device() == dev
+            and scale.get_device() == dev and (norm_w is None or (norm_w.dtype is f32 and norm_w.shape == (width,)
+                                                                  and norm_w.is_contiguous() and norm_w.get_device() == dev))):
+        _args(fn, ("q", q, torch.uint8, (n, width)), ("norm_w", norm_w, f32, (width,)))
+        _rows(fn, "x", x, (f32, bf16), (n, width), dev)
+        _rows(fn, "scale", scale, (f32,), (blocks, n), dev)
     _check(fn, load().kv8_quant_blocks(
-        x.data_ptr(), _dtype_code(x.dtype), n, width, x.stride(0) if n > 1 else -(-width // 16) * 16, _ptr(norm_w), eps, q.data_ptr(),
-        scale.data_ptr(), scale.stride(0) if blocks > 1 else n, _stream(stream, dev)))
+        x.data_ptr(), KV8_BF16 if xt is bf16 else KV8_F32, n, width, xs[0] if n > 1 else -(-width // 16) * 16,
+        None if norm_w is None else norm_w.data_ptr(), eps, q.data_ptr(), scale.data_ptr(), ss[0] if blocks > 1 else n, _stream(stream, dev)))
 
 
 def kv8_matmul8(a8, a_scale, w8, w_scale, out, err_word=None, stream=None) -> None:
     """out [M][N] (f32 / bf16, rows strided) = a8 [M][K] uint8 e4m3 (rows strided), with a_scale [ceil(K / 128)][M] f32 (rows
     strided) or [M] f32, times the fmt=8 weight w8 [N][K] uint8, w_scale [ceil(N / 128)][ceil(K / 128)] f32."""
     import torch
-    fn, f32, u8 = "kv8_matmul8", torch.float32, torch.uint8
-    (M, K), N = a8.shape, w8.shape[0]
+    fn, f32, bf16, u8, dev = "kv8_matmul8", torch.float32, torch.bfloat16, torch.uint8, torch.cuda.current_device()
+    (M, K), N, ot = a8.shape, w8.shape[0], out.dtype
     kb = -(-K // KV8_KVB_BLOCK)
-    dev = _args(fn, ("w8", w8, u8, (N, K)), ("w_scale", w_scale, f32, (-(-N // KV8_KVB_BLOCK), kb)), ("err_word", err_word, torch.int32, (1,)))
-    _rows(fn, "a8", a8, (u8,), (M, K), dev)
-    per_row = a_scale.dim() == 1
-    _rows(fn, "a_scale", a_scale, (f32,), (M,) if per_row else (kb, M), dev)
-    _rows(fn, "out", out, (f32, torch.bfloat16), (M, N), dev)
+    a_s, ss, os_ = a8.stride(), a_scale.stride(), out.stride()
+    per_row = len(ss) == 1
+    if not ((ot is bf16 or ot is f32) and a8.dtype is u8 and w8.dtype is u8 and a_scale.dtype is f32 and w_scale.dtype is f32
+            and a_s[-1] == 1 and ss[-1] == 1 and os_[-1] == 1 and w8.shape == (N, K) and out.shape == (M, N)
+            and a_scale.shape == ((M,) if per_row else (kb, M)) and w_scale.shape == (-(-N // KV8_KVB_BLOCK), kb) and w8.is_contiguous()
+            and w_scale.is_contiguous() and a8.get_device() == dev and a_scale.get_device() == dev and w8.get_device() == dev
+            and w_scale.get_device() == dev and out.get_device() == dev and err_word is None):
+        _args(fn, ("w8", w8, u8, (N, K)), ("w_scale", w_scale, f32, (-(-N // KV8_KVB_BLOCK), kb)), ("err_word", err_word, torch.int32, (1,)))
+        _rows(fn, "a8", a8, (u8,), (M, K), dev)
+        _rows(fn, "a_scale", a_scale, (f32,), (M,) if per_row else (kb, M), dev)
+        _rows(fn, "out", out, (f32, bf16), (M, N), dev)
     _check(fn, load().kv8_matmul8(
-        a8.data_ptr(), a8.stride(0) if M > 1 else -(-K // 16) * 16, a_scale.data_ptr(), 0 if per_row else (a_scale.stride(0) if kb > 1 else M),
-        M, N, K, w8.data_ptr(), w_scale.data_ptr(), out.data_ptr(), _dtype_code(out.dtype), out.stride(0) if M > 1 else N, _ptr(err_word),
-        _stream(stream, dev)))
+        a8.data_ptr(), a_s[0] if M > 1 else -(-K // 16) * 16, a_scale.data_ptr(), 0 if per_row else (ss[0] if kb > 1 else M),
+        M, N, K, w8.data_ptr(), w_scale.data_ptr(), out.data_ptr(), KV8_BF16 if ot is bf16 else KV8_F32, os_[0] if M > 1 else N,
+        _ptr(err_word), _stream(stream, dev)))
 
 
 def kv8_wait_selftest(limit_ns: int, err_word, wait_status, stream=None) -> None:
