@@ -385,10 +385,10 @@ int kv8_rope_freqs(int rope_dim, double theta, double factor, double context, do
     auto pair_of = [&](double beta) {
         return rope_dim * log(context / (beta * 6.283185307179586)) / (2.0 * log(theta));
     };
-    const double low = fmax(floor(pair_of(beta_fast)), 0.0), high = fmin(ceil(pair_of(beta_slow)), rope_dim - 1.0);
+    const double low = fmax(floor(pair_of(beta_fast)), 0.0), high = fmax(fmin(ceil(pair_of(beta_slow)), rope_dim - 1.0), 0.0);
     for (int i = 0; i < rope_dim / 2; ++i) {
         const double f = pow(theta, -2.0 * i / rope_dim);
-        const double far = i <= low ? 0.0 : i >= high ? 1.0 : (i - low) / (high - low);
+        const double far = i >= high ? 1.0 : i <= low ? 0.0 : (i - low) / (high - low);
         inv_freq[i] = (float)(f * (1.0 - far) + f / factor * far);
     }
     *rope_scale = (float)(1.0 + 0.1 * log(factor));

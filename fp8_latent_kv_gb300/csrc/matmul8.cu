@@ -430,6 +430,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
             }
             if constexpr (kSplit) {
                 // (rows of out that do not exist have no sums to hand over)
+                __syncwarp();
                 const int own = S::own(split);
                 const int cols = kSwap ? min(kNT, a.M - tq * kNT) : min(kNT, a.N - tq * kNT);  // the tile's columns that exist
                 if (kSwap && split == 1) {

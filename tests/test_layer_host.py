@@ -89,8 +89,12 @@ def test_frequencies(lib):
     assert bool(((g.double() - want).abs() <= 2.0 ** -23 * want).all())
     assert bool((g[:low + 1] == f[:low + 1]).all()) and bool(((g[high:] * 40 - f[high:]).abs() <= 1e-6 * f[high:]).all())
     # the two borders at one pair: a step, no division by zero
-    h, _ = kv.kv8_rope_freqs(2, 10000.0, 8.0, 4096, 1.0, 1.0)
-    assert math.isfinite(h[0])
+    h, _ = kv.kv8_rope_freqs(64, 10000.0, 8.0, 4096, 7.0, 7.0)
+    at = 64 * math.log(4096 / (7 * 2 * math.pi)) / (2 * math.log(10000.0))
+    assert bool((h[:math.floor(at)] == f[:math.floor(at)]).all()) and bool((h[math.ceil(at):] * 8 == f[math.ceil(at):]).all())
+    # a context in which no pair makes a turn: all slowed down; one in which all make many: none
+    assert bool((kv.kv8_rope_freqs(64, 10000.0, 8.0, 2)[0] * 8 == f).all())
+    assert torch.equal(kv.kv8_rope_freqs(64, 10000.0, 8.0, 1e9)[0], f)
 
 
 @pytest.mark.parametrize("bad", [dict(rope_dim=0), dict(rope_dim=7), dict(rope_dim=258), dict(theta=1.0), dict(theta=math.nan), dict(factor=0.5),
