@@ -26,9 +26,10 @@ def values(codes):
 def rotate(x, position, inv_freq, scale, layout):
     """x [n][heads][dim] f64 -> (rotated, what an element of it may be off by before its output rounding).
 
-    The bound: an angle's fraction of a turn is held to 2^-32, then as an f32 in half turns (U at most): pi (2^-31 + U) in the
-    cosine and sine, whose own f32 functions are good to 2 steps (4 U), the scale and two products and a sum another 4 U:
-    under 12 U (|u| + |v|) |scale| in all."""
+    The bound: an angle's fraction of a turn is held to 2^-32; the rest after whole quarters, pi/4 at most, is off by that and
+    three roundings (conversion, constant, product): 2 pi 2^-32 + 3 U pi/4 < 2.4 U.  The series of its cosine and sine end 2^-29
+    (0.04 U) early and round twice at the end: below 5 U.  The scale, a product and the sum round once each: under 12 U
+    (|u| + |v|) |scale| in all, with room for the products of errors."""
     a = (position.double()[:, None] * inv_freq.double())[:, None]
     d = x.shape[-1]
     i, j = (slice(0, None, 2), slice(1, None, 2)) if layout == 0 else (slice(0, d // 2), slice(d // 2, d))

@@ -82,6 +82,10 @@ def test_rope_strides_and_in_place(lib, layout, xt):
             lib.kv8_rope(x, -pos, f, at, x[..., at:], layout=layout)
             d = (x[..., at:] - before.permute(1, 0, 2)[:n, :, off + at:off + width]).abs()[keep]
             size = before.permute(1, 0, 2)[:n, :, off + at:off + width].abs().max()
+            # A cosine or sine is off by 5 U at most: its angle, pi/4 at most, by pi 2^-32 2 + 3 U pi/4 (conversion, constant, product),
+            # its series by 2^-29 and 2 U of roundings.  An element is then off by 2 * 5 U of the largest one and, for its two products
+            # and their sum, 2 * 1.42 U: below 24 U.  There are two turns; the values between them, and the first turn's errors in the
+            # second, are up to sqrt(2) < 2 times as large.
             assert float(d.max()) <= 2 * 24 * U * 2 * float(size)
     one = randn((n, 1, width), g, xt)
     a, b = (torch.empty((n, heads, dim), dtype=xt, device=DEV) for _ in range(2))
