@@ -114,11 +114,13 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     uint8_t *staging = smem + kStages * S::kStage;
     float *fac = reinterpret_cast<float *>(staging + kOut);
     uint64_t *bars = reinterpret_cast<uint64_t *>(staging + kOut + S::kFac);
-    uint64_t *full = bars, *empty = bars + kStages, *t_full = bars + 2 * kStages, *t_empty = t_full + S::kAcc, *drain = t_empty + S::kAcc;
-    uint64_t *red_full = drain + 1, *s_full = drain + 2, *s_empty = s_full + kScaleSlots;
-    static_assert((2 * kStages + 2 * S::kAcc + 2 + 2 * kScaleSlots) * 8 + 8 <= 256, "barriers");
+    uint64_t *full = bars, *empty = bars + kStages, *t_full = bars + 2 * kStages, *t_empty = t_full + S::kAcc;
+    uint64_t *red_full = t_empty + S::kAcc, *s_full = red_full + 1, *s_empty = s_full + kScaleSlots;
+    static_assert((2 * kStages + 2 * S::kAcc + 1 + 2 * kScaleSlots) * 8 + 28 <= 256, "barriers");
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_empty + kScaleSlots);
     int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
+    int *issued = abort_flag + 1;  // (pair) K blocks loaded, K blocks multiplied
+    int *peer = issued + 2;        // what the other block stores here: whether it gave up, and its `issued`
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = kSplit ? a.split : 1;
@@ -146,9 +148,9 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                 mbar_init(s_full + i, 32);
                 mbar_init(s_empty + i, S::kEpi);
             }
-            mbar_init(drain, 1);
             mbar_init(red_full, S::kEpi * split);
             *abort_flag = 0;
+            issued[0] = issued[1] = peer[0] = peer[1] = peer[2] = 0;
             fence_barrier_init();
         }
         __syncwarp();
@@ -166,8 +168,26 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         named_sync(1, S::kThreads);
         tc_fence_after_sync();
     }
-    if constexpr (kPair || kSplit) cluster_arrive_relaxed();
-    if constexpr (kPair) cluster_wait();  // the other block's barriers stand
+    if constexpr (kSplit) cluster_arrive_relaxed();
+    if constexpr (kPair) {  // the other block's barriers stand, and its words are zero
+        cluster_arrive();
+        cluster_wait();
+    }
+
+    // What is in flight when a warp ends its work.  A block whose shared memory a copy or a commit's arrival may still reach must
+    // not leave, and a barrier of all threads does not wait for either: of n K blocks the last ones' barriers are waited for.  (The
+    // phases before them have passed: a K block is loaded, or multiplied, when the one before it in its stage or accumulator has
+    // been used.)
+    auto copies_landed = [&](int n) {
+        for (int i = n < kStages ? 0 : n - kStages; i < n; ++i)
+            (void)bar_wait_inline(full + i % kStages, (i / kStages) & 1, nullptr, nullptr, kDrainCycles);
+    };
+    auto commits_arrived = [&](int n) {
+        for (int i = n < kStages ? 0 : n - kStages; i < n; ++i)
+            (void)bar_wait_inline(empty + i % kStages, (i / kStages) & 1, nullptr, nullptr, kDrainCycles);
+        for (int i = n < S::kAcc ? 0 : n - S::kAcc; i < n; ++i)
+            (void)bar_wait_inline(t_full + i % S::kAcc, (i / S::kAcc) & 1, nullptr, nullptr, kDrainCycles);
+    };
 
     // tile -> (tile of the MMA rows' operand, tile of the columns'): kGroupRows rows at a time, the columns' outside
     auto place = [&](int tile, int &tp, int &tq) {
@@ -208,9 +228,13 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                 __syncwarp();
             }
         }
-        if (!ok && (!kPair || rank == 0))  // the copies in flight end before the block does
-            for (int i = it < kStages ? 0 : it - kStages; i < it; ++i)
-                (void)bar_wait_inline(full + i % kStages, (i / kStages) & 1, nullptr, nullptr, 1ll << 28);
+        if constexpr (kPair) {  // used, in both blocks, and said so here: block 0's products do not end before both blocks' copies
+            for (int i = it < kStages ? 0 : it - kStages; i < it && ok; ++i)
+                ok = __all_sync(0xffffffffu, bar_wait_inline(empty + i % kStages, (i / kStages) & 1, abort_flag, a.err_word));
+            if (lane == 0) issued[0] = it;
+        } else {
+            copies_landed(it);
+        }
         __syncwarp();
     } else if (warp == 1) {
         // ---- products
@@ -252,16 +276,8 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
                     __syncwarp();
                 }
             }
-            if (!ok) {
-                if (elect_one()) {
-                    if constexpr (kPair)
-                        mma_commit_pair(drain);
-                    else
-                        mma_commit(drain);
-                }
-                __syncwarp();
-                (void)bar_wait_inline(drain, 0, nullptr, nullptr, 1ll << 28);
-            }
+            commits_arrived(it);
+            if (kPair && lane == 0) issued[1] = it;
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -551,9 +567,44 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     }
     tc_fence_before_sync();
     __syncthreads();
-    if constexpr (kPair || kSplit) {  // no block leaves while another's copies, products, sums or arrivals may reach it
+    // no block leaves while another's products, sums or the arrivals of its threads may reach it
+    if constexpr (kPair) {
+        if (tid == 0 && *(volatile int *)abort_flag) cluster_store(of_rank(peer, rank ^ 1), 1);
+        __syncwarp();
+    }
+    if constexpr (kPair || kSplit) {
         cluster_arrive();
         cluster_wait();
+    }
+    if constexpr (kPair) {
+        // A wait gave up in one of the two blocks (both find it here): they may have loaded different numbers of K blocks, and
+        // block 0's barriers count both blocks' bytes.  The one that is behind loads as many (its stages are free: the other one
+        // saw them used), block 0 waits for the copies of both, block 1 for the commits that block 0 sent it.
+        if (*(volatile int *)abort_flag || *(volatile int *)peer) {
+            if (warp < 2 && lane == 0) cluster_store(of_rank(peer + 1 + warp, rank ^ 1), issued[warp]);
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            if (warp == 0) {
+                const int mine = issued[0], most = max(mine, *(volatile int *)(peer + 1));
+                for (int i = mine; i < most; ++i) {
+                    uint8_t *p = smem + i % kStages * S::kStage;
+                    if (elect_one()) {
+                        const uint32_t bar = of_rank(full + i % kStages, 0);
+                        if (rank == 0) mbar_arrive_expect_tx(full + i % kStages, 2 * S::kStage);
+                        tma_load_2d_pair(p, &map_p, 0, 0, bar);
+                        tma_load_2d_pair(p + kMmRows * 128, &map_q, 0, 0, bar);
+                    }
+                    __syncwarp();
+                }
+                if (rank == 0) copies_landed(most);
+            } else if (warp == 1 && rank == 1) {
+                commits_arrived(*(volatile int *)(peer + 2));
+            }
+            __syncthreads();
+            cluster_arrive();
+            cluster_wait();
+        }
     }
     if (warp == 3) {
         if constexpr (kPair)

@@ -30,6 +30,8 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+constexpr long long kDrainCycles = 1ll << 28;  // an eighth of a second: for what a block still has in flight at its end
+
 // bar_wait with its slow part in line: a call would cost a thread that holds many values its registers.
 __device__ __forceinline__ bool bar_wait_inline(uint64_t *bar, uint32_t parity, int *abort_flag, int *err, long long limit = kWaitCycles) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -158,6 +160,9 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_store(uint32_t cluster_addr, float a, float b, float c, float d) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+__device__ __forceinline__ void cluster_store(uint32_t cluster_addr, int v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
