@@ -85,6 +85,50 @@ struct MmShape {
     }
 };
 
+// What is in flight when a warp ends its work.  A block whose shared memory a copy or a commit's arrival may still reach must
+// not leave, and a barrier of all threads does not wait for either: of n K blocks the last ones' barriers are waited for.  (The
+// phases before them have passed: a K block is loaded, or multiplied, when the one before it in its stage or accumulator has
+// been used.)
+template <int kBars>
+__device__ __forceinline__ void phases_ended(uint64_t *bars, int n) {
+#pragma unroll 1
+    for (int i = n < kBars ? 0 : n - kBars; i < n; ++i) (void)bar_wait_inline(bars + i % kBars, (i / kBars) & 1, nullptr, nullptr, kDrainCycles);
+}
+
+// A wait gave up in one block of a pair.  The two may have loaded different numbers of K blocks, and block 0's barriers count both
+// blocks' bytes.  The one that is behind loads as many (its stages are free: the other one saw them used), block 0 waits for the
+// copies of both, block 1 for the commits that block 0 sent it.
+template <typename S, int kStages>
+__device__ __forceinline__ void even_out(const CUtensorMap &map_p, const CUtensorMap &map_q, uint8_t *smem, uint64_t *full, uint64_t *empty,
+                                         uint64_t *t_full, const int *issued, const int *peer, uint32_t rank, int warp) {
+    if (warp < 2 && elect_one()) cluster_store(of_rank(peer + 1 + warp, rank ^ 1), issued[warp]);
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 0) {
+        const int mine = issued[0], most = max(mine, *(const volatile int *)(peer + 1));
+#pragma unroll 1
+        for (int i = mine; i < most; ++i) {
+            uint8_t *p = smem + i % kStages * S::kStage;
+            if (elect_one()) {
+                const uint32_t bar = of_rank(full + i % kStages, 0);
+                if (rank == 0) mbar_arrive_expect_tx(full + i % kStages, 2 * S::kStage);
+                tma_load_2d_pair(p, &map_p, 0, 0, bar);
+                tma_load_2d_pair(p + kMmRows * 128, &map_q, 0, 0, bar);
+            }
+            __syncwarp();
+        }
+        if (rank == 0) phases_ended<kStages>(full, most);
+    } else if (warp == 1 && rank == 1) {
+        const int products = *(const volatile int *)(peer + 2);
+        phases_ended<kStages>(empty, products);
+        phases_ended<S::kAcc>(t_full, products);
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+}
+
 // four values of a row, of which `left` exist
 template <typename Out>
 __device__ __forceinline__ void store_row(Out *p, const float (&v)[4], int left, bool wide) {
@@ -122,7 +166,8 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     int *issued = abort_flag + 1;  // (pair) K blocks loaded, K blocks multiplied
     int *peer = issued + 2;        // what the other block stores here: whether it gave up, and its `issued`
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (told to be the same in the whole warp: one row of 16384 10.2 -> 9.6 us)
     const int split = kSplit ? a.split : 1;
     const int rank = kSplit || kPair ? (int)cluster_rank() : 0;
     const int cluster = kPair ? 2 : split, first = (int)blockIdx.x / cluster, step = (int)gridDim.x / cluster;
@@ -174,21 +219,6 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         cluster_wait();
     }
 
-    // What is in flight when a warp ends its work.  A block whose shared memory a copy or a commit's arrival may still reach must
-    // not leave, and a barrier of all threads does not wait for either: of n K blocks the last ones' barriers are waited for.  (The
-    // phases before them have passed: a K block is loaded, or multiplied, when the one before it in its stage or accumulator has
-    // been used.)
-    auto copies_landed = [&](int n) {
-        for (int i = n < kStages ? 0 : n - kStages; i < n; ++i)
-            (void)bar_wait_inline(full + i % kStages, (i / kStages) & 1, nullptr, nullptr, kDrainCycles);
-    };
-    auto commits_arrived = [&](int n) {
-        for (int i = n < kStages ? 0 : n - kStages; i < n; ++i)
-            (void)bar_wait_inline(empty + i % kStages, (i / kStages) & 1, nullptr, nullptr, kDrainCycles);
-        for (int i = n < S::kAcc ? 0 : n - S::kAcc; i < n; ++i)
-            (void)bar_wait_inline(t_full + i % S::kAcc, (i / S::kAcc) & 1, nullptr, nullptr, kDrainCycles);
-    };
-
     // tile -> (tile of the MMA rows' operand, tile of the columns'): kGroupRows rows at a time, the columns' outside
     auto place = [&](int tile, int &tp, int &tq) {
         constexpr int kGroup = kGroupRows / kRows;
@@ -198,146 +228,148 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         tp = g * kGroup + r - tq * rows;
     };
 
-    if (warp == 0) {
-        // ---- loads
-        if constexpr (kPair) fewer_registers<kRegsLoad>();
-        grid_dependency_wait();  // (what comes before needs nothing of the kernel before this one)
-        grid_launch_dependents();
-        int it = 0;
-        bool ok = true;
-        for (int tile = first; tile < tiles && ok; tile += step) {
-            int tp, tq;
-            place(tile, tp, tq);
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % kStages;
-                if (it >= kStages) ok = __all_sync(0xffffffffu, bar_wait_inline(empty + s, (it / kStages - 1) & 1, abort_flag, a.err_word));
-                if (!ok) break;
-                uint8_t *p = smem + s * S::kStage;
-                if (elect_one()) {
-                    if constexpr (kPair) {  // both blocks' bytes count on block 0's barrier
-                        const uint32_t bar = of_rank(full + s, 0);
-                        if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * S::kStage);
-                        tma_load_2d_pair(p, &map_p, kb * kMmBlk, tp * kRows + row0, bar);
-                        tma_load_2d_pair(p + kMmRows * 128, &map_q, kb * kMmBlk, tq * kNT + rank * S::kLoad, bar);
-                    } else {
-                        mbar_arrive_expect_tx(full + s, S::kStage);
-                        tma_load_2d(p, &map_p, kb * kMmBlk, tp * kRows, full + s);
-                        tma_load_2d(p + kMmRows * 128, &map_q, kb * kMmBlk, tq * kNT, full + s);
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        if constexpr (kPair) {  // used, in both blocks, and said so here: block 0's products do not end before both blocks' copies
-            for (int i = it < kStages ? 0 : it - kStages; i < it && ok; ++i)
-                ok = __all_sync(0xffffffffu, bar_wait_inline(empty + i % kStages, (i / kStages) & 1, abort_flag, a.err_word));
-            if (lane == 0) issued[0] = it;
-        } else {
-            copies_landed(it);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---- products
-        if constexpr (kPair) fewer_registers<kRegsLoad>();
-        grid_dependency_wait();  // (so that the time limits of its waits do not count the kernel before)
-        if (!kPair || rank == 0) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kNT, false, false);
-            const uint64_t desc0 = smem_desc(smem_u32(smem), 0, 1024, kSw128);
-            const uint32_t d0 = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    if (warp < kFirst) {
+        if constexpr (kPair) fewer_registers<kRegsLoad>();  // (one instruction for all four warps)
+        if (warp == 0) {
+            // ---- loads
+            grid_dependency_wait();  // (what comes before needs nothing of the kernel before this one)
+            grid_launch_dependents();
             int it = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
+                int tp, tq;
+                place(tile, tp, tq);
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % kStages, c = it % S::kAcc;
-                    ok = bar_wait_inline(full + s, (it / kStages) & 1, abort_flag, a.err_word);
-                    if (it >= S::kAcc && ok) ok = bar_wait_inline(t_empty + c, (it / S::kAcc - 1) & 1, abort_flag, a.err_word);
-                    ok = __all_sync(0xffffffffu, ok);
+                    const int s = it % kStages;
+                    if (it >= kStages) ok = __all_sync(0xffffffffu, bar_wait_inline(empty + s, (it / kStages - 1) & 1, abort_flag, a.err_word));
                     if (!ok) break;
-                    tc_fence_after_sync();
-                    // (a descriptor's address counts 16 bytes; 32 bytes of K a step)
-                    const uint64_t dp = desc0 + s * (S::kStage >> 4), dq = dp + (kMmRows * 128 >> 4);
-                    const uint32_t d = d0 + (uint32_t)(c * kNT);
+                    uint8_t *p = smem + s * S::kStage;
                     if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            if constexpr (kPair)
-                                mma_f8f6f4_pair(d, dp + 2 * kk, dq + 2 * kk, idesc, kk > 0);
-                            else
-                                mma_f8f6f4(d, dp + 2 * kk, dq + 2 * kk, idesc, kk > 0);
-                        }
-                        if constexpr (kPair) {
-                            mma_commit_pair(t_full + c);
-                            mma_commit_pair(empty + s);
+                        if constexpr (kPair) {  // both blocks' bytes count on block 0's barrier
+                            const uint32_t bar = of_rank(full + s, 0);
+                            if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * S::kStage);
+                            tma_load_2d_pair(p, &map_p, kb * kMmBlk, tp * kRows + row0, bar);
+                            tma_load_2d_pair(p + kMmRows * 128, &map_q, kb * kMmBlk, tq * kNT + rank * S::kLoad, bar);
                         } else {
-                            mma_commit(t_full + c);
-                            mma_commit(empty + s);
+                            mbar_arrive_expect_tx(full + s, S::kStage);
+                            tma_load_2d(p, &map_p, kb * kMmBlk, tp * kRows, full + s);
+                            tma_load_2d(p + kMmRows * 128, &map_q, kb * kMmBlk, tq * kNT, full + s);
                         }
                     }
                     __syncwarp();
                 }
             }
-            commits_arrived(it);
-            if (kPair && lane == 0) issued[1] = it;
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ---- scales, kScaleBlocks K blocks at a time.  (Loaded by the warps that add, they held up each of their arrivals
-        // until they were there: 8192 x 4096 x 16384 took 449 us so, 387 from here.)
-        if constexpr (kPair) fewer_registers<kRegsLoad>();
-        grid_dependency_wait();
-        // a8's rows (kSwap: the tile's columns) and w8's blocks of 128; past the ends the last one's are repeated, for sums that are not written
-        int g = 0;
-        bool ok = true;
-        for (int tile = first; tile < tiles && ok; tile += step) {
-            int tp, tq;
-            place(tile, tp, tq);
-            const int m0 = kSwap ? tq * kNT : tp * kRows + row0, n0 = kSwap ? tp * kMmRows : tq * kNT;
-            constexpr int kMs = kSwap ? kNT : kMmRows, kNs = kPair ? 2 : 1, kXs = (kMs + 31) / 32;
-            float x[kScaleBlocks][kXs], w[kScaleBlocks];
-            auto fetch = [&](int k) {
+            if constexpr (kPair) {  // used, in both blocks, and said so here: block 0's products do not end before both blocks' copies
+#pragma unroll 1
+                for (int i = it < kStages ? 0 : it - kStages; i < it && ok; ++i)
+                    ok = __all_sync(0xffffffffu, bar_wait_inline(empty + i % kStages, (i / kStages) & 1, abort_flag, a.err_word));
+                if (lane == 0) issued[0] = it;
+            } else {
+                phases_ended<kStages>(full, it);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---- products
+            grid_dependency_wait();  // (so that the time limits of its waits do not count the kernel before)
+            if (!kPair || rank == 0) {
+                constexpr uint32_t idesc = idesc_e4m3_f32(kRows, kNT, false, false);
+                const uint64_t desc0 = smem_desc(smem_u32(smem), 0, 1024, kSw128);
+                const uint32_t d0 = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+                int it = 0;
+                bool ok = true;
+                for (int tile = first; tile < tiles && ok; tile += step) {
+                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                        const int s = it % kStages, c = it % S::kAcc;
+                        ok = bar_wait_inline(full + s, (it / kStages) & 1, abort_flag, a.err_word);
+                        if (it >= S::kAcc && ok) ok = bar_wait_inline(t_empty + c, (it / S::kAcc - 1) & 1, abort_flag, a.err_word);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        // (a descriptor's address counts 16 bytes; 32 bytes of K a step)
+                        const uint64_t dp = desc0 + s * (S::kStage >> 4), dq = dp + (kMmRows * 128 >> 4);
+                        const uint32_t d = d0 + (uint32_t)(c * kNT);
+                        if (elect_one()) {
 #pragma unroll
-                for (int u = 0; u < kScaleBlocks; ++u) {
-                    const int kb = min(k + u, kb1 - 1);
-                    w[u] = load_now(a.w_scale + (int64_t)tp * a.kb + kb);
-#pragma unroll
-                    for (int i = 0; i < kXs; ++i) x[u][i] = load_now(a.a_scale + kb * a.a_scale_stride + min(m0 + 32 * i + lane, a.M - 1));
-                }
-            };
-            for (int k = kb0; k < kb1; k += kScaleBlocks, ++g) {
-                const int s = g % kScaleSlots;
-                if constexpr (kSwap)
-                    if (k == kb0) fetch(k);
-                if (g >= kScaleSlots) ok = __all_sync(0xffffffffu, bar_wait_inline(s_empty + s, (g / kScaleSlots - 1) & 1, abort_flag, a.err_word));
-                if (!ok) break;
-                if constexpr (kSwap) {  // the columns' factors are multiplied here, once; the next group's are on their way meanwhile
-                    float y[kScaleBlocks][kXs];
-#pragma unroll
-                    for (int u = 0; u < kScaleBlocks; ++u)
-#pragma unroll
-                        for (int i = 0; i < kXs; ++i) y[u][i] = x[u][i] * w[u];
-                    if (k + kScaleBlocks < kb1) fetch(k + kScaleBlocks);
-#pragma unroll
-                    for (int u = 0; u < kScaleBlocks; ++u)
-#pragma unroll
-                        for (int i = 0; i < kXs; ++i)
-                            if (32 * i + lane < kMs) fac[(s * kScaleBlocks + u) * S::kScales + 32 * i + lane] = y[u][i];
-                    mbar_arrive(s_full + s);
-                } else {
-                    for (int u = 0; u < kScaleBlocks && k + u < kb1; ++u) {
-                        float *to = fac + (s * kScaleBlocks + u) * S::kScales;
-                        const float *from = a.a_scale + (k + u) * a.a_scale_stride;
-#pragma unroll
-                        for (int i = 0; i < kMs; i += 32)
-                            if (i + lane < kMs) cp_async_4(to + i + lane, from + min(m0 + i + lane, a.M - 1));
-                        if (lane < kNs) cp_async_4(to + kMs + lane, a.w_scale + (int64_t)min(n0 / kMmBlk + lane, (a.N - 1) / kMmBlk) * a.kb + k + u);
+                            for (int kk = 0; kk < 4; ++kk) {
+                                if constexpr (kPair)
+                                    mma_f8f6f4_pair(d, dp + 2 * kk, dq + 2 * kk, idesc, kk > 0);
+                                else
+                                    mma_f8f6f4(d, dp + 2 * kk, dq + 2 * kk, idesc, kk > 0);
+                            }
+                            if constexpr (kPair) {
+                                mma_commit_pair(t_full + c);
+                                mma_commit_pair(empty + s);
+                            } else {
+                                mma_commit(t_full + c);
+                                mma_commit(empty + s);
+                            }
+                        }
+                        __syncwarp();
                     }
-                    cp_async_mbar_arrive(s_full + s);
+                }
+                phases_ended<kStages>(empty, it);
+                phases_ended<S::kAcc>(t_full, it);
+                if (kPair && lane == 0) issued[1] = it;
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ---- scales, kScaleBlocks K blocks at a time.  (Loaded by the warps that add, they held up each of their arrivals
+            // until they were there: 8192 x 4096 x 16384 took 449 us so, 387 from here.)
+            grid_dependency_wait();
+            // a8's rows (kSwap: the tile's columns) and w8's blocks of 128; past the ends the last one's are repeated, for sums that are not written
+            int g = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                int tp, tq;
+                place(tile, tp, tq);
+                const int m0 = kSwap ? tq * kNT : tp * kRows + row0, n0 = kSwap ? tp * kMmRows : tq * kNT;
+                constexpr int kMs = kSwap ? kNT : kMmRows, kNs = kPair ? 2 : 1, kXs = (kMs + 31) / 32;
+                float x[kScaleBlocks][kXs], w[kScaleBlocks];
+                auto fetch = [&](int k) {
+#pragma unroll
+                    for (int u = 0; u < kScaleBlocks; ++u) {
+                        const int kb = min(k + u, kb1 - 1);
+                        w[u] = load_now(a.w_scale + (int64_t)tp * a.kb + kb);
+#pragma unroll
+                        for (int i = 0; i < kXs; ++i) x[u][i] = load_now(a.a_scale + kb * a.a_scale_stride + min(m0 + 32 * i + lane, a.M - 1));
+                    }
+                };
+                for (int k = kb0; k < kb1; k += kScaleBlocks, ++g) {
+                    const int s = g % kScaleSlots;
+                    if constexpr (kSwap)
+                        if (k == kb0) fetch(k);
+                    if (g >= kScaleSlots) ok = __all_sync(0xffffffffu, bar_wait_inline(s_empty + s, (g / kScaleSlots - 1) & 1, abort_flag, a.err_word));
+                    if (!ok) break;
+                    if constexpr (kSwap) {  // the columns' factors are multiplied here, once; the next group's are on their way meanwhile
+                        float y[kScaleBlocks][kXs];
+#pragma unroll
+                        for (int u = 0; u < kScaleBlocks; ++u)
+#pragma unroll
+                            for (int i = 0; i < kXs; ++i) y[u][i] = x[u][i] * w[u];
+                        if (k + kScaleBlocks < kb1) fetch(k + kScaleBlocks);
+#pragma unroll
+                        for (int u = 0; u < kScaleBlocks; ++u)
+#pragma unroll
+                            for (int i = 0; i < kXs; ++i)
+                                if (32 * i + lane < kMs) fac[(s * kScaleBlocks + u) * S::kScales + 32 * i + lane] = y[u][i];
+                        mbar_arrive(s_full + s);
+                    } else {
+                        for (int u = 0; u < kScaleBlocks && k + u < kb1; ++u) {
+                            float *to = fac + (s * kScaleBlocks + u) * S::kScales;
+                            const float *from = a.a_scale + (k + u) * a.a_scale_stride;
+#pragma unroll
+                            for (int i = 0; i < kMs; i += 32)
+                                if (i + lane < kMs) cp_async_4(to + i + lane, from + min(m0 + i + lane, a.M - 1));
+                            if (lane < kNs) cp_async_4(to + kMs + lane, a.w_scale + (int64_t)min(n0 / kMmBlk + lane, (a.N - 1) / kMmBlk) * a.kb + k + u);
+                        }
+                        cp_async_mbar_arrive(s_full + s);
+                    }
                 }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");  // (none is in flight when the block ends)
+            __syncwarp();
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");  // (none is in flight when the block ends)
-        __syncwarp();
-    } else if (warp >= kFirst) {
+    } else {
         // ---- sums
         if constexpr (kPair) more_registers<kRegsAdd>();
         grid_dependency_wait();  // (out may still be read by the kernel before)
@@ -558,9 +590,6 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
             __syncwarp();
         }
     }
-    if constexpr (kPair) {
-        if (warp == 3) fewer_registers<kRegsLoad>();
-    }
     if constexpr (kSplit) {
         __syncwarp();
         if (warp < kFirst) cluster_wait();
@@ -569,7 +598,7 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
     __syncthreads();
     // no block leaves while another's products, sums or the arrivals of its threads may reach it
     if constexpr (kPair) {
-        if (tid == 0 && *(volatile int *)abort_flag) cluster_store(of_rank(peer, rank ^ 1), 1);
+        if (elect_one() && *(volatile int *)abort_flag) cluster_store(of_rank(peer, cluster_rank() ^ 1), 1);
         __syncwarp();
     }
     if constexpr (kPair || kSplit) {
@@ -577,33 +606,14 @@ __global__ void __launch_bounds__(MmShape<kSwap, kNT, kStages>::kThreads, kBlock
         cluster_wait();
     }
     if constexpr (kPair) {
-        // A wait gave up in one of the two blocks (both find it here): they may have loaded different numbers of K blocks, and
-        // block 0's barriers count both blocks' bytes.  The one that is behind loads as many (its stages are free: the other one
-        // saw them used), block 0 waits for the copies of both, block 1 for the commits that block 0 sent it.
-        if (*(volatile int *)abort_flag || *(volatile int *)peer) {
-            if (warp < 2 && lane == 0) cluster_store(of_rank(peer + 1 + warp, rank ^ 1), issued[warp]);
-            __syncwarp();
-            cluster_arrive();
-            cluster_wait();
-            if (warp == 0) {
-                const int mine = issued[0], most = max(mine, *(volatile int *)(peer + 1));
-                for (int i = mine; i < most; ++i) {
-                    uint8_t *p = smem + i % kStages * S::kStage;
-                    if (elect_one()) {
-                        const uint32_t bar = of_rank(full + i % kStages, 0);
-                        if (rank == 0) mbar_arrive_expect_tx(full + i % kStages, 2 * S::kStage);
-                        tma_load_2d_pair(p, &map_p, 0, 0, bar);
-                        tma_load_2d_pair(p + kMmRows * 128, &map_q, 0, 0, bar);
-                    }
-                    __syncwarp();
-                }
-                if (rank == 0) copies_landed(most);
-            } else if (warp == 1 && rank == 1) {
-                commits_arrived(*(volatile int *)(peer + 2));
-            }
-            __syncthreads();
-            cluster_arrive();
-            cluster_wait();
+        if (*(volatile int *)abort_flag | *(volatile int *)peer) {  // (the same in all threads of both blocks)
+            // all places anew: kept until here they would cost the warps of few registers some of theirs
+            uint32_t base = smem_u32(smem_raw), thread = threadIdx.x;
+            asm volatile("" : "+r"(base), "+r"(thread));
+            uint8_t *again = smem_raw + ((1024u - (base & 1023u)) & 1023u);
+            uint64_t *b = reinterpret_cast<uint64_t *>(again + (reinterpret_cast<uint8_t *>(bars) - smem));
+            int *words = reinterpret_cast<int *>(again + (reinterpret_cast<uint8_t *>(issued) - smem));
+            even_out<S, kStages>(map_p, map_q, again, b, b + kStages, b + 2 * kStages, words, words + 2, cluster_rank(), thread >> 5);
         }
     }
     if (warp == 3) {
