@@ -458,8 +458,8 @@ def kv8_matmul8(a8, a_scale, w8, w_scale, out, err_word=None, stream=None) -> No
 
 
 def kv8_wait_selftest(limit_ns: int, err_word, wait_status, stream=None) -> None:
-    """Diagnostic: both bounded waits on what nothing completes, limit_ns each; sets KV8_ERR_TIMEOUT in err_word and 2 in
-    wait_status (both int32 device tensors)."""
+    """Diagnostic: the bounded waits on what nothing completes, limit_ns each (the product's two a quarter of it); sets
+    KV8_ERR_TIMEOUT in err_word and 2 in wait_status (both int32 device tensors)."""
     _check("kv8_wait_selftest", load().kv8_wait_selftest(limit_ns, _ptr(err_word), _ptr(wait_status), _stream(stream)))
 
 

@@ -59,13 +59,13 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool bar_wait_cluster(uint64_t *bar, uint32_t parity, int *abort_flag, int *err) {
+__device__ __forceinline__ bool bar_wait_cluster(uint64_t *bar, uint32_t parity, int *abort_flag, int *err, long long limit = kWaitCycles) {
     const long long t0 = clock64();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait_cluster(bar, parity)) return true;
         if ((i & 31u) == 0) {
             if (*(volatile int *)abort_flag) return false;
-            if (clock64() - t0 > kWaitCycles) {
+            if (clock64() - t0 > limit) {
                 *(volatile int *)abort_flag = 1;
                 if (err) atomicOr(err, (int)KV8_ERR_TIMEOUT);
                 return false;

@@ -529,11 +529,11 @@ KV8_API int kv8_copy(void *dst, const void *src, size_t bytes, void *stream);
 
 /* -----------------------------------------------------------------------------------------------
  * kv8_wait_selftest -- diagnostic of the timeout path.  One CTA waits on an mbarrier that nothing
- * completes, through the bounded waits the library's tensor-core kernels use for their TMA, MMA and
- * softmax hand-offs, one after the other: one with its limit in nanoseconds, one in cycles of the SM's clock
- * (2 a nanosecond).  After limit_ns (in [1000, 1e9] ns) each gives up: KV8_ERR_TIMEOUT is OR-ed into
- * *err_word, *wait_status is set to 2 (1 would mean a wait completed) and the kernel returns normally,
- * leaving the context usable.  err_word and wait_status: device ints (required).
+ * completes, through the bounded waits the library's tensor-core kernels use for their TMA, MMA,
+ * softmax and cluster hand-offs, one after the other: one with its limit in nanoseconds, three in cycles of the SM's
+ * clock (2 a nanosecond).  After limit_ns (in [1000, 1e9] ns; the last two, those of kv8_matmul8, after a quarter of it)
+ * each gives up: KV8_ERR_TIMEOUT is OR-ed into *err_word, *wait_status is set to 2 (1 would mean that a wait completed,
+ * or did not report) and the kernel returns normally, leaving the context usable.  err_word and wait_status: device ints (required).
  * --------------------------------------------------------------------------------------------- */
 KV8_API int kv8_wait_selftest(uint64_t limit_ns, int *err_word, int *wait_status, void *stream);
 

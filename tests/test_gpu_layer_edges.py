@@ -60,3 +60,20 @@ def test_products_have_ended_when_the_next_call_takes_their_memory(lib):
         for (mm, quant), want in zip(calls, alone):
             assert mm[5].item() == 0
             assert all(torch.equal(a, b) for a, b in zip((mm[4], quant[1], quant[2]), want))
+
+
+def test_the_products_waits_run_to_their_limits(lib):
+    """50 ms by the global timer, 10^8 cycles of the SM's clock (48.3 ms at its highest, 2.07 GHz) and, for the product's two waits,
+    2.5 * 10^7 each: 122 ms at the least.  (A wait that did not set its abort flag or its error would leave another status.)"""
+    err, st = (torch.zeros(1, dtype=torch.int32, device=DEV) for _ in range(2))
+    lib.kv8_wait_selftest(1000, err, st)  # (the first launch loads the kernel)
+    torch.cuda.synchronize()
+    assert err.item() == lib.KV8_ERR_TIMEOUT and st.item() == 2
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    err.zero_(), st.zero_()
+    begin.record()
+    lib.kv8_wait_selftest(50_000_000, err, st)
+    end.record()
+    torch.cuda.synchronize()
+    assert err.item() == lib.KV8_ERR_TIMEOUT and st.item() == 2
+    assert 121 < begin.elapsed_time(end) < 240
