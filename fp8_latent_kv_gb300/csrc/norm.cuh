@@ -5,7 +5,7 @@
 
 namespace kv8 {
 
-// The factor of a root-mean-square norm, y = (x * pre) * inv, where the f32 sum of squares left its range: from the f64 mean square (eps
+// The factor of a root-mean-square norm, y = ((x * pre) * inv) * w, where the f32 sum of squares left its range: from the f64 mean square (eps
 // included).  pre, a power of two, keeps inv a normal f32.  A mean square that is not finite gives 0 (NaN for NaN).
 __device__ __forceinline__ double warp_sum_f64(double v) {
 #pragma unroll

@@ -32,12 +32,12 @@ __device__ __forceinline__ float half_warp_max(float v) {
     return v;
 }
 
-// Quantizes J times eight values a lane, of which each sixteen lanes hold J blocks (z[j], as pairs, times `factor`): bytes, and
-// the scale of one block, number `mine`, which every lane (lane & 15) / (16 / J) == mine returns.
+// Quantizes J times eight values a lane, of which each sixteen lanes hold J blocks (z[j], as pairs): bytes, and the scale of one
+// block, number `mine`, which every lane (lane & 15) / (16 / J) == mine returns.
 // The maxima of the J blocks are taken together: with each exchange a lane keeps half of the blocks that it still
 // carries, so J = 4 takes 5 exchanges instead of 16 and the divisions are made once.
 template <int J>
-__device__ __forceinline__ float quant_blocks_of(const uint64_t (&z)[J][4], float factor, uint2 (&bytes)[J], int &mine) {
+__device__ __forceinline__ float quant_blocks_of(const uint64_t (&z)[J][4], uint2 (&bytes)[J], int &mine) {
     const int lane = threadIdx.x & 31;
     float m[J];
 #pragma unroll
@@ -65,13 +65,11 @@ __device__ __forceinline__ float quant_blocks_of(const uint64_t (&z)[J][4], floa
 #pragma unroll
     for (; left > 0; left /= 2) m[0] = max_nan(m[0], __shfl_xor_sync(0xffffffffu, m[0], left));
     float mul, scale;
-    bool plain = plain_factors(m[0] * factor, mul, scale);
-    const float whole = mul * factor;
-    plain = plain && whole <= 3.402823466e38f;
+    const bool plain = plain_factors(m[0], mul, scale);
     if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const float f = __shfl_sync(0xffffffffu, whole, (lane & 16) | j * (16 / J));
+            const float f = __shfl_sync(0xffffffffu, mul, (lane & 16) | j * (16 / J));
             const uint64_t ff = f2_pack(f, f);
             bytes[j] = make_uint2(enc4_scaled(z[j][0], z[j][1], ff), enc4_scaled(z[j][2], z[j][3], ff));
         }
@@ -84,10 +82,7 @@ __device__ __forceinline__ float quant_blocks_of(const uint64_t (&z)[J][4], floa
 #pragma unroll
         for (int i = 0; i < 4; ++i) f2_unpack(z[j][i], y[2 * i], y[2 * i + 1]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            y[i] *= factor;
-            amax = finite_abs_max(amax, y[i]);
-        }
+        for (int i = 0; i < 8; ++i) amax = finite_abs_max(amax, y[i]);
         row_quant_factors(half_warp_max(amax), pre, mul, scale);
         bytes[j].x = enc4(scale4(make_float4(y[0], y[1], y[2], y[3]), pre, mul));
         bytes[j].y = enc4(scale4(make_float4(y[4], y[5], y[6], y[7]), pre, mul));
@@ -130,7 +125,7 @@ __global__ void __launch_bounds__(kQThreads) quant_blocks_kernel(const void *__r
         for (int i = 0; i < 4; ++i) z[j][i] = raw[j].pair(i);
     uint2 b[kQCols / 2];
     int mine;
-    const float s = quant_blocks_of<kQCols / 2>(z, 1.f, b, mine);
+    const float s = quant_blocks_of<kQCols / 2>(z, b, mine);
 #pragma unroll
     for (int j = 0; j < kQCols / 2; ++j) {
         const int col = (kb0 + 2 * j) * kQBlk + 8 * lane;
@@ -214,9 +209,6 @@ __global__ void __launch_bounds__(kT == 32 ? kQThreads : kT, kBlocks)
                 for (int i = 0; i < kT / 32; ++i) sd += part_d[turn][i];
             }
             norm_factor_f64(sd / width + (double)eps, pre, inv);
-        } else if (ss < 1e-30f) {  // (values so small that a product with the weight could lose bits)
-            pre = 18446744073709551616.f;  // 2^64
-            inv *= 5.421010862427522e-20f;
         }
         if (pre != 1.f) {
 #pragma unroll
@@ -224,6 +216,7 @@ __global__ void __launch_bounds__(kT == 32 ? kQThreads : kT, kBlocks)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) z[j][i] = f2_mul(z[j][i], f2_pack(pre, pre));
         }
+        // (the norm's factor first: then no row's size and no weight's can take the product out of range)
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
             const int col = 8 * (t + kT * j);
@@ -231,12 +224,12 @@ __global__ void __launch_bounds__(kT == 32 ? kQThreads : kT, kBlocks)
                 Raw<false, 8> w;
                 w.load(norm_w + col);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[j][i] = f2_mul(z[j][i], w.pair(i));
+                for (int i = 0; i < 4; ++i) z[j][i] = f2_mul(f2_mul(z[j][i], f2_pack(inv, inv)), w.pair(i));
             }
         }
         uint2 b[kJ];
         int mine;
-        const float sc = quant_blocks_of<kJ>(z, inv, b, mine);
+        const float sc = quant_blocks_of<kJ>(z, b, mine);
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
             const int col = 8 * (t + kT * j);

@@ -292,30 +292,25 @@ __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_ro
                 sd += (double)lo * (double)lo + (double)hi * (double)hi;
             }
             norm_factor_f64(warp_sum_f64(sd) / kKL + (double)eps, pre, inv);
-        } else if (ss < 1e-30f) {  // (values so small that a product with the weight could lose bits)
-            pre = 18446744073709551616.f;  // 2^64
-            inv *= 5.421010862427522e-20f;
         }
         if (pre != 1.f) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) z[j] = f2_mul(z[j], f2_pack(pre, pre));
         }
-        // the latent part's maximum before its factor, so that factor and quantizer are one product
+        // (the norm's factor first: then no row's size and no weight's can take the product out of range)
         float amax = 0.f, mul, sc;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            z[j] = f2_mul(z[j], w[j]);
+            z[j] = f2_mul(f2_mul(z[j], f2_pack(inv, inv)), w[j]);
             float lo, hi;
             f2_unpack(z[j], lo, hi);
             amax = abs_max_nan(amax, lo, hi);
         }
-        amax = warp_max_nan(abs_max_nan(amax * inv, k[0], k[1]));
+        amax = warp_max_nan(abs_max_nan(amax, k[0], k[1]));
         uint2 b[2];
         uint32_t bk;
-        const bool plain = plain_factors(amax, mul, sc);
-        const float whole = mul * inv;
-        if (plain && whole <= 3.402823466e38f) {
-            const uint64_t f = f2_pack(whole, whole);
+        if (plain_factors(amax, mul, sc)) {
+            const uint64_t f = f2_pack(mul, mul);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 b[j] = make_uint2(enc4_scaled(z[4 * j], z[4 * j + 1], f), enc4_scaled(z[4 * j + 2], z[4 * j + 3], f));
@@ -326,10 +321,7 @@ __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_ro
 #pragma unroll
             for (int j = 0; j < 8; ++j) f2_unpack(z[j], y[2 * j], y[2 * j + 1]);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                y[j] *= inv;
-                amax = finite_abs_max(amax, y[j]);
-            }
+            for (int j = 0; j < 16; ++j) amax = finite_abs_max(amax, y[j]);
             amax = warp_max(amax);
             row_quant_factors(amax, qpre, mul, sc);
 #pragma unroll

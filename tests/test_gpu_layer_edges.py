@@ -1,5 +1,8 @@
 """What the calls around the attention promise at their edges: products whose blocks hand their SMs to the next call, and what the
 header says of bytes, angles and rows."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -77,3 +80,74 @@ def test_the_products_waits_run_to_their_limits(lib):
     torch.cuda.synchronize()
     assert err.item() == lib.KV8_ERR_TIMEOUT and st.item() == 2
     assert 121 < begin.elapsed_time(end) < 240
+
+
+# -------------------------------------------------------------------------------------------------------------
+# bytes: a normed row is quantized as the row quantizer quantizes the f32 row
+# -------------------------------------------------------------------------------------------------------------
+def whole_rows(g, n, width, xt):
+    """Rows of whole numbers up to 15 (exact in bf16, and any order of the sum of their squares is exact in f32 and a power of two
+    below 2^24), their f32 normed values as the header has them: x times the correctly rounded 1 / sqrt(mean), times w."""
+    x = torch.randint(-15, 16, (n, width), generator=g).float()
+    x[:, 0] += (x == 0).all(1).float()
+    w = 1 + 0.3 * torch.randn(width, generator=g)
+    mean = (x.double() ** 2).sum(1) / width
+    inv = (1 / torch.sqrt(mean)).float()
+    return x.to(xt).to(DEV), w.to(DEV), (x * inv[:, None]).to(DEV)
+
+
+@pytest.mark.parametrize("xt", [BF, F32])
+@pytest.mark.parametrize("width,n", [(512, 30000), (1024, 16000), (2048, 8000), (4096, 4000), (8192, 2000), (16384, 1000)])
+def test_normed_blocks_are_the_row_quantizers_bytes(lib, width, n, xt):
+    g = gen(width)
+    x, w, xn = whole_rows(g, n, width, xt)
+    w[128:256] = 1e-40  # a block whose 448 / amax overflows, beside the others
+    w[384:512] = 0
+    q, s = torch.empty((n, width), dtype=torch.uint8, device=DEV), torch.empty((width // BLK, n), device=DEV)
+    lib.kv8_quant_blocks(x, q, s, norm_w=w, eps=0.0)
+    y = (xn * w).view(n * width // BLK, BLK)
+    q2, s2 = torch.empty((n * width // BLK, BLK), dtype=torch.uint8, device=DEV), torch.empty(n * width // BLK, device=DEV)
+    lib.kv8_quant_rows_w(y, q2, s2)
+    assert int((q.view(-1, BLK) != q2).sum()) == 0 and torch.equal(s.t().contiguous().view(-1), s2)
+
+
+@pytest.mark.parametrize("xt", [BF, F32])
+def test_fresh_rows_are_the_row_quantizers_bytes(lib, xt):
+    """Positions of 0 turn nothing: the row that kv8_quant_rows would take is known."""
+    g = gen(1)
+    n = 40000
+    x, w, xn = whole_rows(g, n, 512, xt)
+    rope = torch.randn((n, 64), generator=g).to(xt).to(DEV) * torch.exp2(torch.randint(-3, 4, (n, 1), generator=g).float()).to(DEV).to(xt)
+    pos, f, dst = torch.zeros(n, dtype=torch.int32, device=DEV), lib.kv8_rope_freqs(64)[0].to(DEV), torch.arange(n, device=DEV)
+    kv8, ks = torch.empty((n, 576), dtype=torch.uint8, device=DEV), torch.empty(n, device=DEV)
+    q2, s2 = torch.empty_like(kv8), torch.empty_like(ks)
+    for layout in (0, 1):
+        lib.kv8_norm_rope_rows(torch.cat([x, rope], 1), w, 0.0, pos, f, dst, kv8, ks, layout=layout)
+        lib.kv8_quant_rows(torch.cat([xn * w, rope.float()], 1), q2, s2)
+        assert int((kv8 != q2).sum()) == 0 and torch.equal(ks, s2)
+
+
+@pytest.mark.parametrize("size,weight", [(1e8, 1e32), (1e-12, 1e-30), (1e17, 1e28), (1e-20, 1e-36), (2.5e38, 1.0), (1e-41, 1e3)])
+def test_a_norm_before_its_weight(lib, size, weight):
+    """The normed value is near 1 whatever the row's size, so a weight of any size leaves the product in range: the result is the one
+    of a row of size 1, to the norm's own bound (512 values: the sum rounds 16 + 13 times, half of which enters the root, and 6
+    roundings come after it: 20.5 U, for each of the two rows; what the scaled row was rounded to, U in a value and in the root; the
+    scale's two quotients): below 48 U, and a code then lies at most one border further."""
+    g = gen(3)
+    x = torch.randn((6, 512), generator=g).clamp(-1, 1) + 0.25
+    w = (1 + 0.3 * torch.randn(512, generator=g)).to(DEV) * weight
+    got = []
+    for k in (size, 1.0):
+        xs = (x.double() * k).float().to(DEV)
+        if k < 1e-37:  # (subnormal values: what they stand for is taken back to size 1)
+            x = xs.double().cpu() / k
+        q, s = torch.empty((6, 512), dtype=torch.uint8, device=DEV), torch.empty((4, 6), device=DEV)
+        lib.kv8_quant_blocks(xs, q, s, norm_w=w, eps=0.0)
+        rows, ks = torch.empty((6, 576), dtype=torch.uint8, device=DEV), torch.empty(6, device=DEV)
+        lib.kv8_norm_rope_rows(torch.cat([xs, torch.zeros((6, 64), device=DEV)], 1), w, 0.0, torch.zeros(6, dtype=torch.int32, device=DEV),
+                               torch.ones(32, device=DEV), torch.arange(6, device=DEV), rows, ks)
+        got.append((q, s, rows[:, :512], ks))
+    for (a, b) in zip(got[0][1::2], got[1][1::2]):  # scales
+        assert bool(torch.isfinite(a).all()) and bool(((a.double() - b.double()).abs() <= 48 * U * b.double() + 2.0 ** -149).all())
+    for (a, b) in zip(got[0][0::2], got[1][0::2]):  # codes: next to one another (of the same sign)
+        assert bool(((a.int() - b.int()).abs() <= 1).all())
