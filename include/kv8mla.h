@@ -489,7 +489,7 @@ KV8_API int kv8_norm_rope_rows(const void *x, int x_dtype, int64_t n, int64_t x_
  * Every block is quantized as kv8_quant_rows quantizes a row (amax / 448 over its finite values, the same bytes).
  *   x [n][width] of type x_dtype, rows x_stride elements apart (>= width; x and the rows 16-byte aligned).
  *   norm_w [width] f32 (16-byte aligned) or NULL: with it, x_i is first replaced by x_i norm_w[i] / sqrt(mean(x^2) + eps),
- *   in f32, not rounded in between; a row with a NaN or an infinity becomes zeros.
+ *   in f32, not rounded in between; a row with a NaN or an infinity becomes bytes and scales of 0.
  *   q [n][width] u8; scale: block k of row r at scale[k * scale_stride + r] (f32, scale_stride >= n), so one block's
  *   scales of all rows lie together.  The last block is shorter where width is no multiple of 128.
  *   width a multiple of 16 in [16, KV8_MAX_WIDTH], with a norm up to KV8_MAX_NORM_WIDTH; n in [0, KV8_MAX_ROWS]. */

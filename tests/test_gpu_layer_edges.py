@@ -151,3 +151,16 @@ def test_a_norm_before_its_weight(lib, size, weight):
         assert bool(torch.isfinite(a).all()) and bool(((a.double() - b.double()).abs() <= 48 * U * b.double() + 2.0 ** -149).all())
     for (a, b) in zip(got[0][0::2], got[1][0::2]):  # codes: next to one another (of the same sign)
         assert bool(((a.int() - b.int()).abs() <= 1).all())
+
+
+def test_a_row_with_an_infinity_is_bytes_of_zero(lib):
+    x = torch.randn((3, 2048), generator=gen(4)).to(DEV)
+    x[0, 5], x[1, 2047], x[2, 77] = math.inf, -math.inf, math.nan
+    q, s = torch.empty((3, 2048), dtype=torch.uint8, device=DEV), torch.empty((16, 3), device=DEV)
+    lib.kv8_quant_blocks(x, q, s, norm_w=torch.ones(2048, device=DEV))
+    assert bool((q == 0).all()) and bool((s == 0).all())
+    rows, ks = torch.empty((3, 576), dtype=torch.uint8, device=DEV), torch.empty(3, device=DEV)
+    x[1, 511] = -math.inf
+    lib.kv8_norm_rope_rows(torch.cat([x[:, :512], x[:, 600:664]], 1), torch.ones(512, device=DEV), 1e-6, torch.zeros(3, dtype=torch.int32, device=DEV),
+                           torch.ones(32, device=DEV), torch.arange(3, device=DEV), rows, ks)
+    assert bool((rows[:, :512] == 0).all()) and bool((rows[:, 512:] != 0).any(1).all())
