@@ -200,13 +200,7 @@ __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_ro
     const int64_t warps = (int64_t)gridDim.x * (kRowsThreads / 32);
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
-    uint64_t turn[kHalf ? 2 : 1];
-    if constexpr (kHalf) {
-        turn[0] = turn_of(__ldg(inv_freq + 2 * (lane & 15)));
-        turn[1] = turn_of(__ldg(inv_freq + 2 * (lane & 15) + 1));
-    } else {
-        turn[0] = turn_of(__ldg(inv_freq + lane));
-    }
+    const uint64_t turn = turn_of(__ldg(inv_freq + lane));
     uint64_t w[8];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -269,9 +263,11 @@ __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_ro
         float ss, s_hi;
         f2_unpack(s2, ss, s_hi);
         ss = warp_sum(ss + s_hi);
-        const float2 c0 = turn_cos_sin(pos, turn[0], rope_scale);
-        if constexpr (kHalf) {
-            const float2 c1 = turn_cos_sin(pos, turn[1], rope_scale);
+        float2 c0 = turn_cos_sin(pos, turn, rope_scale);
+        if constexpr (kHalf) {  // (a lane's two pairs are numbers 2 (l mod 16) and the next: their angles are two other lanes')
+            const int from = 2 * (lane & 15);
+            const float2 c1 = make_float2(__shfl_sync(0xffffffffu, c0.x, from + 1), __shfl_sync(0xffffffffu, c0.y, from + 1));
+            c0 = make_float2(__shfl_sync(0xffffffffu, c0.x, from), __shfl_sync(0xffffffffu, c0.y, from));
             const float sign = lane < 16 ? -1.f : 1.f;
             const float o0 = __shfl_xor_sync(0xffffffffu, k[0], 16), o1 = __shfl_xor_sync(0xffffffffu, k[1], 16);
             k[0] = k[0] * c0.x + sign * o0 * c0.y;

@@ -439,8 +439,9 @@ KV8_API int kv8_tree_commit(int B, const int32_t *q_start, const int32_t *lens, 
  *
  * Rotary positions.  Pair i of a rotated part (u, v: KV8_ROPE_INTERLEAVED or KV8_ROPE_HALF) at position p becomes
  *     u' = rope_scale (u cos a - v sin a),   v' = rope_scale (u sin a + v cos a),   a = p inv_freq[i]
- * with inv_freq [rope_dim / 2] f32 (device, finite), position [n] int32 (any value; a negative one turns back, so
- * -p undoes p where rope_scale is 1).  The angle is reduced exactly: positions of a million lose nothing.
+ * with inv_freq [rope_dim / 2] f32 (device; from -2^40 to 2^40), position [n] int32 (any value; a negative one turns back,
+ * so -p undoes p where rope_scale is 1).  The frequency's part of a turn is held to 2^-65, the turn to |p| 2^-65, and its cosine
+ * and sine to 6 roundings of f32 relative to themselves: neither positions of a million nor the smallest angles lose anything.
  * Every scaling for long contexts is a choice of inv_freq and rope_scale.
  *
  * kv8_rope_freqs -- such a choice, on the host: inv_freq [rope_dim / 2] and *rope_scale are HOST memory.

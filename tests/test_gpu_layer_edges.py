@@ -164,3 +164,71 @@ def test_a_row_with_an_infinity_is_bytes_of_zero(lib):
     lib.kv8_norm_rope_rows(torch.cat([x[:, :512], x[:, 600:664]], 1), torch.ones(512, device=DEV), 1e-6, torch.zeros(3, dtype=torch.int32, device=DEV),
                            torch.ones(32, device=DEV), torch.arange(3, device=DEV), rows, ks)
     assert bool((rows[:, :512] == 0).all()) and bool((rows[:, 512:] != 0).any(1).all())
+
+
+# -------------------------------------------------------------------------------------------------------------
+# angles
+# -------------------------------------------------------------------------------------------------------------
+def exact_angle(p, f):
+    """p f reduced to [-pi, pi], rounded once to f64: whole-number arithmetic on 1 / (2 pi) to 320 bits (pi by Machin's formula)."""
+    bits = 320
+    one = 1 << (bits + 32)
+
+    def arctan_of_inverse(k):
+        term = total = one // k
+        n, sign = 3, -1
+        while term:
+            term //= k * k
+            total += sign * (term // n)
+            n, sign = n + 2, -sign
+        return total
+    pi = 4 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239))  # times 2^(bits + 32)
+    inverse = (one << bits) // (2 * pi)                          # 2^bits / (2 pi)
+    m, e = math.frexp(f)
+    whole, e = int(m * (1 << 24)), e - 24                          # f = whole 2^e
+    t = p * whole * inverse
+    t = t << e if e >= 0 else t >> -e
+    t &= (1 << bits) - 1
+    if t >> (bits - 1):
+        t -= 1 << bits
+    return 2 * math.pi * (t / (1 << bits))
+
+
+def turned(lib, pos, f, layout=0):
+    """cos and sin as kv8_rope makes them: pairs (1, 0) turned."""
+    n, pairs = len(pos), len(f)
+    x = torch.zeros((n, 1, pairs, 2), device=DEV)
+    x[..., 0] = 1
+    x = x if layout == 0 else x.transpose(2, 3)
+    rot = torch.empty((n, 1, 2 * pairs), device=DEV)
+    lib.kv8_rope(x.reshape(n, 1, 2 * pairs), torch.tensor(pos, dtype=torch.int32, device=DEV), torch.tensor(f, dtype=torch.float32, device=DEV), 0, rot, layout=layout)
+    out = rot.view(n, pairs, 2) if layout == 0 else rot.view(n, 2, pairs).transpose(1, 2)
+    return out.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_angles_of_every_size(lib, layout):
+    """A cosine or sine is held to 6 U of itself and what its angle is off by.  The frequency's fraction of a turn is rounded to 2^-64
+    (2^-65 off) and |f| 2^-128 off for the 128 bits of 1 / (2 pi) that make it; the position multiplies both.  The rest of the turn
+    after whole quarters then rounds three times (conversion, constant, product; 3 U of itself, which a sine below pi/4 takes over
+    at most, a cosine to 0.8 of it), the series rounds its last sum once (U), the terms before it, a tenth of a sine and 0.44 of a cosine at
+    most, two or three times (below U); they end at 0.05 U of the value."""
+    freqs, _ = lib.kv8_rope_freqs(64, 10000.0, 40.0, 4096)
+    f = [float(v) for v in freqs] + [float(np.float32(v)) for v in (0.9999, 3.14159274, 12345.678, 1e6, -0.37, -2.5e-5, 1e-9, 0.0)]
+    pos = [0, 1, 2, 3, 5, 8, -1, -7, 100, 1001, 4096, 65537, 999999, (1 << 20) - 1, 123456789, (1 << 31) - 1, -(1 << 31), -(1 << 30) + 1]
+    got = turned(lib, pos, f, layout)
+    worst = 0.0
+    for i, p in enumerate(pos):
+        for j, v in enumerate(f):
+            a = exact_angle(p, v)
+            off = 2 * math.pi * abs(p) * (2.0 ** -65 + abs(v) * 2.0 ** -128)
+            for k, want in enumerate((math.cos(a), math.sin(a))):
+                worst = max(worst, abs(got[i, j, k] - want) / (6 * U * abs(want) + off + 2.0 ** -149))
+    assert worst <= 1, f"{worst:.4g} times the bound"
+
+
+def test_exact_angle_against_f64():
+    for p, f in ((1, 1.0), (7, 0.25), (100, 1e-3), (-5, 0.5), (1000, 0.1)):
+        v = float(np.float32(f))
+        a = math.remainder(p * v, 2 * math.pi)
+        assert abs(exact_angle(p, v) - a) < 1e-12 * max(1, abs(p * v))
