@@ -1,5 +1,7 @@
 // launch.h -- a kernel launched as a programmatic dependent of the one before it on its stream: it may start while that one
-// ends, and calls sm100::grid_dependency_wait() before it touches memory.
+// ends, and calls sm100::grid_dependency_wait() before it touches memory.  What it reads may be written while it already runs, so none of
+// its loads is a read-only one (no __ldg, no const __restrict__ parameter): those ask for memory that stays as it is all the
+// kernel's life, and may be moved ahead of the wait.
 #pragma once
 
 #include <cuda_runtime.h>

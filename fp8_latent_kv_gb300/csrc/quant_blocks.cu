@@ -96,10 +96,8 @@ __device__ __forceinline__ float quant_blocks_of(const uint64_t (&z)[J][4], uint
 constexpr int kQCols = 8, kQRows = kQThreads / 32;
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kQThreads) quant_blocks_kernel(const void *__restrict__ xv, int64_t n, int width,
-                                                                 int64_t x_stride, uint8_t *__restrict__ q,
-                                                                 float *__restrict__ scale, int64_t scale_stride,
-                                                                 int col_parts) {
+__global__ void __launch_bounds__(kQThreads) quant_blocks_kernel(const void *xv, int64_t n, int width, int64_t x_stride, uint8_t *q,
+                                                                 float *scale, int64_t scale_stride, int col_parts) {
     using T = typename Elem<kBf16>::T;
     __shared__ float sc[kQCols][kQRows];
     sm100::grid_dependency_wait();
@@ -143,9 +141,8 @@ __global__ void __launch_bounds__(kQThreads) quant_blocks_kernel(const void *__r
 // while the one before is worked on.
 template <bool kBf16, int kT, int kJ, int kBlocks>
 __global__ void __launch_bounds__(kT == 32 ? kQThreads : kT, kBlocks)
-    norm_quant_blocks_kernel(const void *__restrict__ xv, int64_t n, int width, int64_t x_stride,
-                             const float *__restrict__ norm_w, float eps, uint8_t *__restrict__ q,
-                             float *__restrict__ scale, int64_t scale_stride) {
+    norm_quant_blocks_kernel(const void *xv, int64_t n, int width, int64_t x_stride, const float *norm_w, float eps, uint8_t *q,
+                             float *scale, int64_t scale_stride) {
     using T = typename Elem<kBf16>::T;
     constexpr int kRows = kT == 32 ? kQThreads / kT : 1;  // of a block at a time
     __shared__ float part[2][kT / 32];

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
     fetch(threadIdx.x, w0);
-    if (threadIdx.x < half_dim) turns[threadIdx.x] = turn_of(__ldg(a.inv_freq + threadIdx.x));
+    if (threadIdx.x < half_dim) turns[threadIdx.x] = turn_of(a.inv_freq[threadIdx.x]);
 
     if (a.n_rest > 0) {
         Out *rest = static_cast<Out *>(a.rest) + n0 * a.rest_row + h0 * a.rest_head;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * half_dim; i += kRopeThreads) {
         const int t = i / half_dim;
-        table[i] = turn_cos_sin(__ldg(a.position + n0 + t), turns[i - t * half_dim], a.scale);
+        table[i] = turn_cos_sin(a.position[n0 + t], turns[i - t * half_dim], a.scale);
     }
     __syncthreads();
     Out *rot = static_cast<Out *>(a.rot) + n0 * a.rot_row + h0 * a.rot_head;
@@ -190,17 +190,15 @@ constexpr int row_bytes(bool bf16) { return kRow * (bf16 ? 2 : 4); }
 // (a pair of the interleaved layout; of the half layout the partners sit in lane l xor 16).
 template <bool kBf16, bool kHalf>
 __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_rows_kernel(
-    const void *__restrict__ xv, int64_t n, int64_t x_stride, const float *__restrict__ norm_w, float eps,
-    const int32_t *__restrict__ position, const float *__restrict__ inv_freq, float rope_scale,
-    const int64_t *__restrict__ dst, uint8_t *__restrict__ kv8, float *__restrict__ kv_scale, int64_t cache_rows,
-    int *err_word) {
+    const void *xv, int64_t n, int64_t x_stride, const float *norm_w, float eps, const int32_t *position, const float *inv_freq,
+    float rope_scale, const int64_t *dst, uint8_t *kv8, float *kv_scale, int64_t cache_rows, int *err_word) {
     using T = typename Elem<kBf16>::T;
     const T *x = static_cast<const T *>(xv);
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kRowsThreads / 32);
     sm100::grid_dependency_wait();
     sm100::grid_launch_dependents();
-    const uint64_t turn = turn_of(__ldg(inv_freq + lane));
+    const uint64_t turn = turn_of(inv_freq[lane]);
     uint64_t w[8];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -224,8 +222,8 @@ __global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_ro
     };
     auto ask_place = [&](int64_t r) {
         if (r < n) {
-            next_pos = __ldg(position + r);
-            next_row = __ldg(dst + r);
+            next_pos = position[r];
+            next_row = dst[r];
         }
     };
     int64_t r = (int64_t)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);

@@ -77,7 +77,7 @@ __device__ __forceinline__ bool bar_wait_cluster(uint64_t *bar, uint32_t parity,
 // A load that goes out where it stands (the compiler moves a plain one down to its use).
 __device__ __forceinline__ float load_now(const float *p) {
     float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
     return v;
 }
 

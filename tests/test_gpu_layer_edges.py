@@ -232,3 +232,68 @@ def test_exact_angle_against_f64():
         v = float(np.float32(f))
         a = math.remainder(p * v, 2 * math.pi)
         assert abs(exact_angle(p, v) - a) < 1e-12 * max(1, abs(p * v))
+
+
+# -------------------------------------------------------------------------------------------------------------
+# calls one after the other
+# -------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("n", [1, 40, 700])
+def test_a_call_sees_what_the_call_before_it_has_just_written(lib, n):
+    """Every call's input is the output of the call before, written again and again into the same memory while the next kernel may
+    already run: quantized rows and their scales, products, slots, positions and rotated heads."""
+    g = gen(n)
+    hid, H, page = 1024, 8, 16
+    xs = [torch.randn((n, hid), generator=g).to(BF).to(DEV) for _ in range(3)]
+    w, w8, sw = torch.ones(hid, device=DEV), *weight(g, H * 192, hid, DEV)
+    v8, sv = weight(g, 576, hid, DEV)
+    q, s = torch.empty((n, hid), dtype=torch.uint8, device=DEV), torch.empty((hid // BLK, n), device=DEV)
+    heads, fresh, f, lw = torch.empty((n, H * 192), device=DEV), torch.empty((n, 576), device=DEV), lib.kv8_rope_freqs(64)[0].to(DEV), torch.ones(512, device=DEV)
+    rot, rest = torch.empty((n, H, 64), device=DEV), torch.empty((n, H, 128), device=DEV)
+    rows = -(-n // page) * page
+    kv8, ks = torch.zeros((rows, 576), dtype=torch.uint8, device=DEV), torch.zeros(rows, device=DEV)
+    per = 256
+    B = -(-n // per)  # sequences of up to 256 rows
+    counts = [min(per, n - per * b) for b in range(B)]
+    start = torch.tensor([0] + np.cumsum(counts).tolist(), dtype=torch.int32, device=DEV)
+    lens, parent = torch.zeros(B, dtype=torch.int32, device=DEV), torch.cat([torch.arange(-1, c - 1) for c in counts]).to(torch.int32).to(DEV)
+    n_pages, table = torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros((B, per // page), dtype=torch.int32, device=DEV)
+    free, n_free = torch.arange(rows // page, dtype=torch.int32, device=DEV), torch.tensor([rows // page], dtype=torch.int32, device=DEV)
+    slots, mask = torch.zeros(n, dtype=torch.int64, device=DEV), torch.zeros((n, per // 32), dtype=torch.int32, device=DEV)
+    pos, err = torch.zeros(n, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def go(x, each=lambda: None):
+        for call in (lambda: lib.kv8_page_plan(lens, start, page, n_pages, table, free, n_free, slots, err_word=err),
+                     lambda: lib.kv8_quant_blocks(x, q, s, norm_w=w),
+                     lambda: lib.kv8_matmul8(q, s, w8, sw, heads, err_word=err),
+                     lambda: lib.kv8_matmul8(q, s, v8, sv, fresh, err_word=err),
+                     lambda: lib.kv8_tree_mask(parent, start, lens, mask, position=pos, err_word=err),
+                     lambda: lib.kv8_norm_rope_rows(fresh, lw, 1e-6, pos, f, slots, kv8, ks, err_word=err),
+                     lambda: lib.kv8_rope(heads.view(n, H, 192), pos, f, 128, rot, rest),
+                     lambda: lib.kv8_rope(rot, pos, f, 0, rot),
+                     lambda: lib.kv8_quant_blocks(rest.view(n, H * 128), q, s),
+                     lambda: lib.kv8_matmul8(q, s, w8, sw, heads, err_word=err)):
+            call()
+            each()
+    outs = (q, s, heads, fresh, rot, rest, kv8, ks, slots, pos)
+    want = []
+    for x in xs:
+        go(x, torch.cuda.synchronize)
+        want.append([o.clone() for o in outs])
+    assert err.item() == 0 and not torch.equal(want[0][2], want[1][2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for x in xs:
+            go(x)
+    for turn in range(6):
+        for _ in range(4):
+            if turn % 2:
+                graph.replay()
+            else:
+                for x in xs:
+                    go(x)
+        got = [o.clone() for o in outs]
+        assert all(torch.equal(a, b) for a, b in zip(got, want[-1]))
+        go(xs[turn % 2])
+        got = [o.clone() for o in outs]
+        assert all(torch.equal(a, b) for a, b in zip(got, want[turn % 2]))
+    assert err.item() == 0
