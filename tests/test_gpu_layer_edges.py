@@ -297,3 +297,49 @@ def test_a_call_sees_what_the_call_before_it_has_just_written(lib, n):
         got = [o.clone() for o in outs]
         assert all(torch.equal(a, b) for a, b in zip(got, want[turn % 2]))
     assert err.item() == 0
+
+
+# -------------------------------------------------------------------------------------------------------------
+# products: a row's place does not matter
+# -------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 4096), (16, 1000, 4096), (37, 24576, 256), (64, 1000, 4096), (64, 24576, 256), (200, 1000, 4096), (48, 8200, 1024),
+                                   (300, 900, 3200), (1024, 1000, 4096), (129, 12200, 528), (700, 8200, 384), (1500, 2100, 400), (2048, 4096, 512)])
+@pytest.mark.parametrize("ot", [BF, F32])
+def test_products_do_not_depend_on_a_rows_or_columns_place(lib, M, N, K, ot):
+    """Three kinds of rows (codes and scales), each at many places of the left operand, tiles' first and last rows among them: bit-equal rows of
+    the output.  Likewise three kinds of columns: weight blocks of equal codes and scales."""
+    g = gen(M + N)
+    kb, nb = -(-K // BLK), -(-N // BLK)
+    a3, _ = weight(g, 3, K, DEV)
+    s3 = torch.exp2(torch.randn((kb, 3), generator=g) - 6).to(DEV)
+    kind = torch.randint(0, 3, (M,), generator=g)
+    kind[[0, M - 1]] = 0
+    for at in (15, 16, 31, 32, 63, 64, 127, 128, 255, 256):
+        if at < M:
+            kind[at] = 0
+    kind = kind.to(DEV)
+    w3, _ = weight(g, 3 * BLK, K, DEV)
+    v3 = torch.exp2(torch.randn((3, kb), generator=g) - 6).to(DEV)
+    block = torch.randint(0, 3, (nb,), generator=g).to(DEV)
+    block[[0, nb - 1]] = 1
+    w8 = w3.view(3, BLK, K)[block].reshape(nb * BLK, K)[:N].contiguous()
+    out = torch.empty((M, N), dtype=ot, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lib.kv8_matmul8(a3[kind].contiguous(), s3[:, kind].contiguous(), w8, v3[block].contiguous(), out, err_word=err)
+    assert err.item() == 0
+    ref, tol = matmul(a3, s3, w3, v3, ot)
+    for k in range(3):
+        rows = out[kind == k]
+        assert bool((rows == rows[:1]).all()), f"rows of kind {k}"
+        first = torch.full((3 * BLK,), -1, device=DEV, dtype=torch.long)
+        for b in range(nb):  # every block of a kind against the kind's reference, and bit for bit against the first of it
+            if len(rows) == 0:
+                continue
+            c, t = slice(b * BLK, min(N, (b + 1) * BLK)), int(block[b])
+            got = rows[0, c]
+            want = ref[k, t * BLK:t * BLK + len(got)]
+            assert bool(((got.double() - want).abs() <= tol[k, t * BLK:t * BLK + len(got)]).all())
+            if first[t] < 0:
+                first[t] = b
+            else:
+                assert torch.equal(got, rows[0, int(first[t]) * BLK:int(first[t]) * BLK + len(got)]), f"columns of kind {t}"
