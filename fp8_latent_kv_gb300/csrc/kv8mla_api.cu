@@ -400,7 +400,7 @@ int kv8_rope(const void *x, int x_dtype, int64_t n, int heads, int width, int ro
              int64_t rot_row_stride, int64_t rot_head_stride, void *rest, int64_t rest_row_stride, int64_t rest_head_stride,
              int out_dtype, void *stream) {
     if (n < 0 || n > KV8_MAX_ROWS || heads < 1 || heads > KV8_MAX_HEADS || rope_dim < 2 || rope_dim > KV8_MAX_ROPE ||
-        rope_dim % 2 != 0 || width > KV8_MAX_WIDTH || rope_at < 0 || rope_at > width - rope_dim || !valid_dtype(x_dtype) ||
+        rope_dim % 2 != 0 || width < rope_dim || width > KV8_MAX_WIDTH || rope_at < 0 || rope_at > width - rope_dim || !valid_dtype(x_dtype) ||
         !valid_dtype(out_dtype) || !valid_layout(layout) || !isfinite(rope_scale))
         return KV8_EINVAL;
     if (n == 0) return KV8_OK;
