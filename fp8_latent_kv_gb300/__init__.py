@@ -353,8 +353,9 @@ def _rows(fn: str, name: str, t, dtypes, shape, dev: int) -> None:
 
 def kv8_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0, context: float = 4096, beta_fast: float = 32.0,
                    beta_slow: float = 1.0):
-    """(inv_freq [rope_dim / 2] f32 CPU tensor, rope_scale): plain frequencies, or interpolated by parts for a context `factor`
-    times as long."""
+    """(inv_freq [rope_dim / 2] f32 CPU tensor, scale): plain frequencies, or interpolated by parts for a context `factor` times as
+    long.  The scale is one of whole queries and keys: the calls' rope_scale where whole heads are rotated; where a part of them is,
+    rope_scale stays 1 and the attention call's sm_scale is multiplied by scale * scale."""
     import torch
     table, scale = (ctypes.c_float * max(1, rope_dim // 2))(), ctypes.c_float()
     _check("kv8_rope_freqs", load().kv8_rope_freqs(rope_dim, theta, factor, context, beta_fast, beta_slow, ctypes.addressof(table),

@@ -442,14 +442,18 @@ KV8_API int kv8_tree_commit(int B, const int32_t *q_start, const int32_t *lens, 
  * with inv_freq [rope_dim / 2] f32 (device; from -2^40 to 2^40), position [n] int32 (any value; a negative one turns back,
  * so -p undoes p where rope_scale is 1).  The frequency's part of a turn is held to 2^-65, the turn to |p| 2^-65, and its cosine
  * and sine to 6 roundings of f32 relative to themselves: neither positions of a million nor the smallest angles lose anything.
- * Every scaling for long contexts is a choice of inv_freq and rope_scale.
+ * A scaling for long contexts is a choice of inv_freq, and of a factor on the scores.  rope_scale is a factor on the rotated
+ * elements alone: on a head of which only a part is rotated (this library's: 64 elements of a key beside 512 or 128 others) it scales
+ * that part's share of the scores and nothing else.  A factor on whole queries and keys belongs, squared, in sm_scale.
  *
  * kv8_rope_freqs -- such a choice, on the host: inv_freq [rope_dim / 2] and *rope_scale are HOST memory.
  *   f_i = theta^(-2i / rope_dim); with factor = 1 the table is f and the scale 1.  With factor > 1 the frequencies are
  *   interpolated by parts ("YaRN: Efficient Context Window Extension of Large Language Models", NTK-by-parts): a pair that
  *   makes more than beta_fast turns in `context` positions keeps f_i, one that makes fewer than beta_slow gets
  *   f_i / factor, and between the two pairs (their numbers rounded outward, limited to [0, rope_dim - 1]) the share of
- *   f_i / factor grows linearly with i; the scale is 0.1 ln(factor) + 1.
+ *   f_i / factor grows linearly with i; the scale is 0.1 ln(factor) + 1.  The method multiplies whole queries and whole keys with that
+ *   scale.  Where a head is rotated as a whole, it is the rope_scale of both; for this library's heads rope_scale stays 1 and the
+ *   attention call's sm_scale is multiplied by its square.
  *   rope_dim even in [2, KV8_MAX_ROPE]; theta > 1; factor >= 1; context >= 1; 0 < beta_slow <= beta_fast.
  * --------------------------------------------------------------------------------------------- */
 KV8_API int kv8_rope_freqs(int rope_dim, double theta, double factor, double context, double beta_fast, double beta_slow,

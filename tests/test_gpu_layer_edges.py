@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from layer_ref import BLK, U, matmul, weight
+from helpers import parity
+from layer_ref import BLK, U, matmul, rotate, values, weight
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda")
@@ -343,3 +344,29 @@ def test_products_do_not_depend_on_a_rows_or_columns_place(lib, M, N, K, ot):
                 first[t] = b
             else:
                 assert torch.equal(got, rows[0, int(first[t]) * BLK:int(first[t]) * BLK + len(got)]), f"columns of kind {t}"
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_scores_of_a_long_context(lib, layout):
+    """Frequencies for forty times the context, as the header has them used with heads that are rotated in part: rope_scale 1, and
+    the scale's square in sm_scale.  Held to the method's definition, whole queries and whole keys times the scale, in 64 bits (the
+    rows as quantized), within the library's bound for attention outputs."""
+    g = gen(8)
+    T, H, at = 700, 16, 100000
+    f, scale = lib.kv8_rope_freqs(64, 10000.0, 40.0, 4096)
+    f, sm = f.to(DEV), 192.0 ** -0.5
+    pos = (at + torch.arange(T)).to(torch.int32).to(DEV)
+    kv8, ks = torch.empty((T, 576), dtype=torch.uint8, device=DEV), torch.empty(T, device=DEV)
+    lib.kv8_norm_rope_rows(torch.randn((T, 576), generator=g).to(DEV), torch.ones(512, device=DEV), 1e-6, pos, f, torch.arange(T, device=DEV), kv8, ks, layout=layout)
+    q_lat, heads = torch.randn((H, 512), generator=g).to(DEV), torch.randn((1, H, 192), generator=g).to(DEV)
+    q_rope, last = torch.empty((1, H, 64), device=DEV), pos[-1:].contiguous()
+    lib.kv8_rope(heads, last, f, 128, q_rope, layout=layout)
+    ws = torch.empty(lib.mla_decode8_workspace_bytes(H, T, 0) // 4, device=DEV)
+    out, err = torch.empty((H, 512), device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    lib.mla_absorb_decode8(q_lat, q_rope[0], kv8, ks, T, sm * scale * scale, ws, out, err_word=err)
+    assert err.item() == 0
+    c = values(kv8) * ks.double()[:, None]
+    turned_q, _ = rotate(heads[..., 128:].double(), last, f, 1.0, layout)
+    q = scale * torch.cat([q_lat.double(), turned_q[0]], 1)
+    want = torch.softmax(sm * (q @ (scale * c).t()), 1) @ c[:, :512]
+    parity(out.cpu().numpy(), want.cpu().numpy(), "scores of a long context")
