@@ -91,13 +91,6 @@ struct Raw {
 };
 
 template <int V>
-__device__ __forceinline__ void load(const float *p, float (&v)[V]) {
-    Raw<false, V> r;
-    r.load(p);
-    r.get(v);
-}
-
-template <int V>
 __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[V]) {
     if constexpr (V == 8)
         *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));

@@ -183,13 +183,13 @@ cudaError_t rope_go(const RopeArgs &a, bool wide, int64_t blocks, cudaStream_t s
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kRowsThreads = 256;
 constexpr int kRowsAhead = 3;  // rows of a warp in shared memory or on their way
-constexpr int rows_blocks(bool) { return 3; }  // blocks an SM
+constexpr int kRowsBlocks = 3;  // an SM
 constexpr int row_bytes(bool bf16) { return kRow * (bf16 ? 2 : 4); }
 
 // One warp a row, grid-stride, the next rows on their way to shared memory meanwhile (each warp for itself): lane l holds latent elements 8 l .. and 256 + 8 l .., and rotary elements 2 l, 2 l + 1
 // (a pair of the interleaved layout; of the half layout the partners sit in lane l xor 16).
 template <bool kBf16, bool kHalf>
-__global__ void __launch_bounds__(kRowsThreads, rows_blocks(kBf16)) norm_rope_rows_kernel(
+__global__ void __launch_bounds__(kRowsThreads, kRowsBlocks) norm_rope_rows_kernel(
     const void *xv, int64_t n, int64_t x_stride, const float *norm_w, float eps, const int32_t *position, const float *inv_freq,
     float rope_scale, const int64_t *dst, uint8_t *kv8, float *kv_scale, int64_t cache_rows, int *err_word) {
     using T = typename Elem<kBf16>::T;
@@ -383,7 +383,7 @@ cudaError_t launch_norm_rope_rows(const void *x, int x_bf16, int64_t n, int64_t 
                                   const int64_t *dst, uint8_t *kv8, float *kv_scale, int64_t cache_rows, int *err_word,
                                   cudaStream_t st) {
     int64_t blocks = (n + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
-    const int64_t cap = (int64_t)device_sm_count() * rows_blocks(x_bf16 != 0);
+    const int64_t cap = (int64_t)device_sm_count() * kRowsBlocks;
     if (blocks > cap) blocks = cap;
     const int smem = kRowsThreads / 32 * kRowsAhead * row_bytes(x_bf16 != 0);
     auto go = [&](auto kernel) -> cudaError_t {
