@@ -6,11 +6,13 @@
 // 128 to the next, so each block's sums leave TMEM, are multiplied by sa sw and added in f32 registers while the tensor
 // cores work on the next block in other columns.
 //
-// Two layouts of one kernel:
-//   many rows (kSwap = false): MMA rows are 128 rows of a8, columns kNT rows of w8.  sa is one number a thread, sw one
-//     a warp.  Persistent blocks, one an SM.
-//   few rows (kSwap = true): MMA rows are 128 rows of w8, columns up to kNT = 16 / 32 / 64 rows of a8: the weight is read
-//     once, whatever the number of rows, and no MMA row is idle.  The columns' factors sa sw stand in shared memory.
+// Three arrangements of one kernel:
+//   many rows, whole tiles (kSwap = kSplit = false): MMA rows are 128 rows of a8 (256 of a pair of blocks), columns kNT rows of
+//     w8.  sa is one number a thread, sw one a warp.  Persistent blocks, one an SM, that take tile after tile.
+//   many rows, shared tiles (kSwap = false, kSplit): tiles of 128 x 128, one for each cluster.
+//   few rows (kSwap, kSplit): MMA rows are 128 rows of w8, columns kNT = 16 / 32 / 64 rows of a8, so that no MMA row is idle.  One
+//     tile for each cluster, or block.  A tile reads its rows of the weight once; up to 16 tiles of kNT rows lie side by side,
+//     and each of them reads the weight again (from the L2, where it holds them).  The columns' factors sa sw stand in shared memory.
 // Where the tiles are fewer than the SMs, a cluster of up to 8 blocks shares a tile along K: each block owns some columns of
 // the tile, the others store their sums for them into its shared memory, and it adds them in the order of their ranks (the
 // result does not depend on timing, and no workspace is needed).
@@ -18,13 +20,14 @@
 // What bounds it.  Many rows: a K block's 128 x 256 sums a block leave TMEM while the next one's are made, and with two
 // accumulators of 256 columns filling TMEM the next but one waits for them: 512 cycles of products, about 550 until the end
 // of the products has come to the adding warps and their end back to the issuing one, about 480 of loads and FMAs, for two
-// blocks of K: 770 a block, tensor pipe 68 % active (8192 x 4096 x 16384: 357 us, 3.08 PFLOP/s; products alone 289 us).
-// Taken and left: one block's 128 x 256 tile, which needs 48 KB a stage for the same work where a pair's needs 32 (452 us);
+// blocks of K: 770 a block, tensor pipe 68 % active (8192 x 4096 x 16384: 363 us in bursts, 3.03 PFLOP/s; products alone 289 us).
+// Taken and left, beside 357 us then: one block's 128 x 256 tile, which needs 48 KB a stage for the same work where a pair's needs 32 (452 us);
 // sixteen adding warps (409), two MMAs of 128 columns a K block (398), loads of 32 columns at a time (403), or one ahead of the
 // sums (406): TMEM loads in larger bursts hold up the products.  An output as large as the product's work
-// is bound by its writes: 4096 x 32768 x 512 takes 80 us for 268 MB, which a plain fill writes in 70 us.
-// Few rows: the weight's bytes (37 x 24576 x 2048: 13.9 us, 3.8 TB/s; 1 x 4096 x 16384: 14.4 us, 4.7 TB/s), of which about
-// 3 us are a launch's way to its first bytes and 1 to 3 us the exchange of a split.
+// is bound by its writes: 4096 x 32768 x 512 takes 78 us for 268 MB, which a plain fill writes in 71 us.
+// Few rows: the weight's bytes (37 x 24576 x 2048: 14.8 us, 3.5 TB/s; 1 x 4096 x 16384: 14.3 us, 4.7 TB/s), of which about
+// 3 us are a launch's way to its first bytes and 1 to 3 us the exchange of a split; where the tiles are not a multiple of the SMs,
+// the SMs that hold two.
 #include "elem.cuh"
 #include "internal.h"
 #include "sm100_more.cuh"
@@ -40,7 +43,10 @@ constexpr int kMmBlk = KV8_KVB_BLOCK;  // K per scale block: 128 e4m3 bytes, one
 constexpr int kMmRows = 128;           // MMA M
 constexpr int kScaleBlocks = 4, kScaleSlots = 4;  // K blocks whose scales travel together, and slots of them
 constexpr int kFirst = 4;              // the first warp that adds; warps 0 to 2 bring operands, issue products, bring scales
-constexpr int kRegsLoad = 40, kRegsAdd = 232;  // registers a thread of a pair's twelve warps: 4 x 40 + 8 x 232 = 12 x 168
+// Registers a thread of a pair's twelve warps: 4 x 40 + 8 x 232 = 12 x 168.  (One setmaxnreg for all four warps that hand some on, as
+// the ISA has it: lowered in each warp's own part instead, 8192 x 4096 x 16384 took 2 % less in bursts and 4 % less at the power limit,
+// 4096 x 32768 x 512 1 % more.  48 and 224: 2 % slower; no hand-over, 168 for all: 10 to 50 %, for sums that spill.)
+constexpr int kRegsLoad = 40, kRegsAdd = 232;
 constexpr int kGroupRows = 2048;       // rows of tiles that are walked together, for the L2's sake
 
 struct MmArgs {

@@ -6,8 +6,10 @@
 //
 // Every value is read once and every byte written once, so DRAM is the floor of both kernels: eight values a lane stay in
 // registers between their block's maximum and its bytes, and a normed row between the sum of its squares and its scaling.
-// Without a norm they reach it (8192 x 16384: f32 93 us, 7.2 TB/s, part of the bytes still in L2 at the end; bf16 61 us, 6.6 TB/s);
-// with one, a row's two passes over its registers take f32 rows of 16384 to 110 us (6.1 TB/s) and bf16 rows to 90 (4.5).
+// Without a norm they reach it (8192 x 16384: f32 93 us, 7.3 TB/s, part of the bytes still in L2 at the end; bf16 61 us, 6.6 TB/s).
+// With one f32 rows of 16384 take 111 us (6.1 TB/s), bf16 rows 93 (4.4), of 8192 47, of 4096 25, of 2048 15 (3.4): the row, the next
+// row and the products lie in 80 to 120 registers, so that few warps an SM (36 % of the most at 8192 columns) have a row's chain of sum, barrier,
+// root, maxima and divisions to cover; neither DRAM (51 %) nor issue slots (57 %) are full.
 #include "elem.cuh"
 #include "internal.h"
 #include "launch.h"
@@ -248,8 +250,8 @@ cudaError_t launch_quant_blocks(const void *x, int x_bf16, int64_t n, int width,
                                 width, x_stride, q, scale, scale_stride, parts);
     }
     // A warp a row up to 1024 columns, from there a block, of as few threads as hold a row: what a thread's blocks of columns
-    // share (their maxima, the divisions) is made once for them.  (8192 bf16 rows of 2048: 64 threads 12.8 us, 256 threads 18.0;
-    // of 4096: 128 threads 21.1, 256 threads 25.0; f32 rows of 4096, with twice the bytes on their way: 32.1 and 30.0.)
+    // share (their maxima, the divisions) is made once for them.  (8192 bf16 rows of 2048, partly in the L2: 64 threads 12.8 us, 256
+    // threads 18.0; of 4096: 128 threads 21.1, 256 threads 25.0; f32 rows of 4096, with twice the bytes on their way: 32.1 and 30.0.)
     auto go = [&](auto kernel, int threads, int rows, int blocks_per_sm) {
         const int64_t need = (n + rows - 1) / rows, most = (int64_t)device_sm_count() * blocks_per_sm;
         return launch_dependent(kernel, (unsigned)(need < most ? need : most), threads, 0, st, x, n, width, x_stride, norm_w, eps, q, scale,

@@ -6,9 +6,11 @@
 // All arithmetic is f32; an output in bf16 is rounded once.
 //
 // Both kernels read every value once and write every value once, so DRAM is their floor.  kv8_rope reaches it: 8192 tokens of
-// 128 bf16 heads of 192, 805 MB, in 121 us (6.65 TB/s, a plain copy's rate).  kv8_norm_rope_rows takes 25.3 us for 65536 bf16 rows
-// (114 MB, 4.5 TB/s; issue slots 66 % taken: about 300 instructions a row) and 32.4 us for f32 rows (5.9 TB/s); a half warp a
-// row halves what a row costs once, but holds twice the registers, and was no faster (24.5 us, and 1000 rows 2.6 -> 3.9 us).
+// 128 bf16 heads of 192, 805 MB, in 121 us (6.65 TB/s, a plain copy's rate).  kv8_norm_rope_rows does not: 26.1 us for 65536 bf16 rows
+// (114 MB, 4.4 TB/s; half layout 26.5) and 31.5 us for f32 rows (6.0 TB/s).  With bf16 rows neither DRAM (37 %) nor the issue slots
+// (67 %) are full: a row is about 300 instructions in a chain of sum, root, products, maximum, division and bytes, and 24 warps an SM
+// do not cover it all.  A half warp a row halves what a row costs once, but holds twice the registers, and was no faster (24.5 us where
+// a warp a row took 25.3, and 1000 rows 2.6 -> 3.9 us).
 #include "elem.cuh"
 #include "internal.h"
 #include "launch.h"
@@ -186,8 +188,9 @@ constexpr int kRowsAhead = 3;  // rows of a warp in shared memory or on their wa
 constexpr int kRowsBlocks = 3;  // an SM
 constexpr int row_bytes(bool bf16) { return kRow * (bf16 ? 2 : 4); }
 
-// One warp a row, grid-stride, the next rows on their way to shared memory meanwhile (each warp for itself): lane l holds latent elements 8 l .. and 256 + 8 l .., and rotary elements 2 l, 2 l + 1
-// (a pair of the interleaved layout; of the half layout the partners sit in lane l xor 16).
+// One warp a row, grid-stride, the next rows on their way to shared memory meanwhile (each warp for itself): lane l holds latent
+// elements 8 l .. and 256 + 8 l .., rotary elements 2 l, 2 l + 1 (a pair of the interleaved layout; of the half layout the partners sit in
+// lane l xor 16), and the angle of pair l.
 template <bool kBf16, bool kHalf>
 __global__ void __launch_bounds__(kRowsThreads, kRowsBlocks) norm_rope_rows_kernel(
     const void *xv, int64_t n, int64_t x_stride, const float *norm_w, float eps, const int32_t *position, const float *inv_freq,

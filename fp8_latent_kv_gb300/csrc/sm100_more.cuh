@@ -1,5 +1,5 @@
 // sm100_more.cuh -- inline-PTX wrappers of the block-scaled product's kernel that sm100.cuh has no use for: tensor stores,
-// a TMEM load wait that its results depend on, thread-block clusters.  Written from the PTX ISA's descriptions.
+// a TMEM load wait that its results depend on, bounded waits in line and across a cluster, pairs of blocks, thread-block clusters.  Written from the PTX ISA's descriptions.
 #pragma once
 
 #include "sm100.cuh"
