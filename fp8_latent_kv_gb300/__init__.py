@@ -357,7 +357,7 @@ def kv8_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0, c
     long.  The scale is one of whole queries and keys: the calls' rope_scale where whole heads are rotated; where a part of them is,
     rope_scale stays 1 and the attention call's sm_scale is multiplied by scale * scale."""
     import torch
-    table, scale = (ctypes.c_float * max(1, rope_dim // 2))(), ctypes.c_float()
+    table, scale = (ctypes.c_float * max(1, min(rope_dim, KV8_MAX_ROPE) // 2))(), ctypes.c_float()
     _check("kv8_rope_freqs", load().kv8_rope_freqs(rope_dim, theta, factor, context, beta_fast, beta_slow, ctypes.addressof(table),
                                                    ctypes.addressof(scale)))
     return torch.tensor(list(table), dtype=torch.float32), scale.value

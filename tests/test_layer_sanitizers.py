@@ -37,3 +37,21 @@ def test_layer_calls_host_side_under_asan_ubsan(tmp_path):
     _run(["g++", *SAN, *objs, "-L" + cudart, "-lcudart_static", "-ldl", "-lpthread", "-lrt", "-o", exe])
     r = _run([exe], env=dict(ENV, CUDA_VISIBLE_DEVICES=""))
     assert "layer driver ok" in r.stdout
+
+
+@pytest.mark.parametrize("rope_dim", [-2, 0, 1, 257, 258, 1 << 20, (1 << 31) - 2])
+def test_frequencies_of_a_size_out_of_range_allocate_nothing(rope_dim):
+    """The binding makes no table for a size that the call refuses."""
+    import tracemalloc
+
+    import torch  # noqa: F401  (its import is not the call's)
+    import fp8_latent_kv_gb300 as kv
+    from fp8_latent_kv_gb300 import build as kvbuild
+    kvbuild.build()
+    kv.load()
+    tracemalloc.start()
+    with pytest.raises(kv.Kv8Error):
+        kv.kv8_rope_freqs(rope_dim)
+    most = tracemalloc.get_traced_memory()[1]
+    tracemalloc.stop()
+    assert most < 1 << 20
